@@ -227,6 +227,94 @@ PKV_API pkv_status pkv_paged_attn_mixed(pkv_cache cache, const void *q, int num_
                                 int num_splits, void *workspace, size_t workspace_bytes,
                                 void *out, pkv_dtype out_dtype, float *lse, void *stream);
 
+/* How pkv_rope_append treats query and key heads.
+ *   rotary_dim   leading elements of each head that are rotated: a multiple of 16, 0 (none) to
+ *                head_dim; the others pass unrotated.
+ *   interleaved  0: pair i is elements i and i + rotary_dim / 2; else elements 2i and 2i + 1.
+ *   inv_freq     device FP32 [rotary_dim / 2]: pair i of a token at position p is turned by the angle
+ *                p * inv_freq[i] (exact to FP32's precision for every int32 position). Scaling for
+ *                long contexts is a choice of these values. NULL allowed when rotary_dim is 0.
+ *   mscale       factor on the cosines and sines (1 for none); finite.
+ *   q_weight, k_weight  RMS norm weights [head_dim] in the cache dtype, applied to each query / key head
+ *                before the rotation: x * rsqrt(mean(x^2) + eps) * weight; NULL: no norm.
+ *   eps          >= 0 and finite. */
+typedef struct {
+    int rotary_dim;
+    int interleaved;
+    const float *inv_freq;
+    float mscale;
+    const void *q_weight;
+    const void *k_weight;
+    float eps;
+} pkv_rope;
+
+/* rope_append -- the rows between a layer's projections and its attention, in one pass: norm of each
+ * query and key head, rotary positions, queries written to q_out, keys and values into their pages
+ * (the addressing of pkv_kv_cache_append). All arithmetic in FP32, one rounding at the end; an FP8 cache
+ * receives keys quantised from the FP32 values (scale and codes as pkv_kv_format), values as
+ * pkv_kv_cache_append writes them. The pages name neither step; they are the usual ones of the models they serve.
+ *   q             token t's heads [Hq, D] at q + t * q_stride elements, in the cache dtype;
+ *   k, v          likewise [Hkv, D] with k_stride, v_stride. Strides are multiples of 8 elements and at
+ *                 least a token's row: the three may be views of one fused projection's output.
+ *   positions     int32 [num_new_tokens]: the rotary position of each token (any int32; a drafted
+ *                 token's is its depth in the tree, not its slot in the cache).
+ *   cu_new_lens, ctx_before, block_tables, batch, max_blocks_per_seq, num_new_tokens
+ *                 as pkv_kv_cache_append; tokens at or behind cu_new_lens[batch] are left alone (neither
+ *                 q_out nor the cache is written for them).
+ *   q_out         token t's rotated heads [Hq, D] at q_out + t * q_out_stride; may be q itself with the
+ *                 same stride (in place), else must not overlap q, k or v.
+ * Keys and values whose position or page is out of range are skipped and flagged (their queries are still
+ * written). */
+PKV_API pkv_status pkv_rope_append(pkv_cache cache, pkv_rope rope, const void *q, long long q_stride, int num_q_heads,
+                           const void *k, long long k_stride, const void *v, long long v_stride,
+                           const int *positions, const int *cu_new_lens, const int *ctx_before,
+                           const int *block_tables, int batch, int max_blocks_per_seq, int num_new_tokens,
+                           void *q_out, long long q_out_stride, void *stream);
+
+/* Bytes of workspace pkv_paged_attn_tree needs for these sizes (independent of batch and lengths);
+ * 0 for sizes that it refuses. */
+PKV_API size_t pkv_tree_workspace_size(int num_q_heads, int num_kv_heads, int head_dim, int max_q_len);
+
+/* paged_attn_tree -- attention of drafted tokens: sequence b's n_b = cu_q_lens[b+1] - cu_q_lens[b] nodes, whose
+ * K and V are already in the cache at its last n_b positions (append first, then attend), each see the whole context
+ * before them, positions below context_lens[b] - n_b, and the nodes that their mask row gives.
+ *   q             [total_q, Hq, D] in the cache dtype, packed by sequence (row cu_q_lens[b] + i is node i).
+ *   tree_mask     int32 [total_q, mask_words]: bit j % 32 of word j / 32 of row cu_q_lens[b] + i set when node i
+ *                 sees node j (a tree: its ancestors and itself; any other set is as good). Bits at or
+ *                 beyond n_b are ignored. mask_words >= ceil(max_q_len / 32).
+ *   cu_q_lens     int32 [batch+1], non-decreasing from 0, at most total_q; rows of q at or behind
+ *                 cu_q_lens[batch] are left alone.
+ *   context_lens  int32 [batch]: cached tokens including the drafted ones (>= n_b).
+ *   max_q_len     an upper bound of n_b over the batch.
+ *   scale         > 0 and finite.
+ *   workspace     pkv_tree_workspace_size() bytes of device scratch; contents need no init. Calls that may
+ *                 overlap on the GPU need one each.
+ *   out           [total_q, Hq, D] in out_dtype; lse FP32 [total_q, Hq] or NULL.
+ * A node that sees nothing (no context, empty mask row) gets output 0 and lse -inf. What a masked key or value
+ * holds, infinities and NaN included, does not reach the nodes that do not see it. A sequence with a length out of
+ * range (n_b > max_q_len, context_lens[b] < n_b or beyond the table) is skipped and flagged, its rows
+ * left as they were; a page id outside the pool is flagged and page 0 read.
+ * 16-bit caches (an FP8 cache: PKV_ERR_UNSUPPORTED), head_dim 64, 128 or 256, any grouping, any number of nodes. */
+PKV_API pkv_status pkv_paged_attn_tree(pkv_cache cache, const void *q, int num_q_heads, const int *tree_mask, int mask_words,
+                               const int *cu_q_lens, const int *context_lens, const int *block_tables, int batch,
+                               int max_blocks_per_seq, int total_q, int max_q_len, float scale, void *workspace,
+                               size_t workspace_bytes, void *out, pkv_dtype out_dtype, float *lse, void *stream);
+
+/* kv_cache_compact -- cached rows that are kept move to consecutive positions, in place, for every KV head's
+ * K and V (and an FP8 cache's scales): the accepted path of a drafted tree, the tokens that a window or an
+ * eviction rule leaves. Row k of sequence b, k < cu_keep[b+1] - cu_keep[b], goes from position
+ * keep_pos[cu_keep[b] + k] to dst_start[b] + k, bit for bit.
+ *   keep_pos      int32 [num_keep]: every source at or behind its destination, keep_pos[cu_keep[b] + k] >=
+ *                 dst_start[b] + k (ascending lists that start at or behind dst_start are). A source may be listed twice.
+ *   cu_keep       int32 [batch+1], non-decreasing from 0, at most num_keep.
+ *   dst_start     int32 [batch].
+ * Rows whose source lies before their destination or beyond the table, or whose page is out of the pool, are skipped and
+ * flagged (PKV_ERR_DEVICE_RANGE). The destinations' pages must be the sequence's own: a page that another
+ * table shares would change for both (and is undefined when the other moves rows of it in the same call). */
+PKV_API pkv_status pkv_kv_cache_compact(pkv_cache cache, const int *keep_pos, const int *cu_keep, const int *dst_start,
+                                const int *block_tables, int batch, int max_blocks_per_seq, int num_keep,
+                                void *stream);
+
 /* attn_combine -- log-sum-exp merge of split-KV partial results ([FAPA] s2: the
  * same rescale-by-exp(m_old - m_new) identity applied to whole splits).
  *   partial_o     FP32 [n_rows, num_splits, head_dim]: each split's output,

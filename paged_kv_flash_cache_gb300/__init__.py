@@ -27,6 +27,7 @@ __all__ = [
     "PkvError", "library_path", "load_library", "kv_cache_append", "paged_attn_decode", "paged_attn_prefill",
     "attn_combine", "decode_workspace_size", "decode_split_tokens", "get_device_error", "STATUS",
     "paged_attn_decode_noalloc", "paged_attn_mixed", "selftest_wait_timeout", "paged_attn_decode_step",
+    "rope_append", "paged_attn_tree", "tree_workspace_size", "kv_cache_compact",
 ]
 
 _HERE = os.path.dirname(os.path.abspath(__file__))
@@ -42,6 +43,7 @@ KV_NATIVE, KV_FP8_E4M3 = 0, 1
 # Every symbol include/pkv.h declares.
 EXPORTS = ("pkv_kv_cache_append", "pkv_decode_workspace_size", "pkv_decode_split_tokens", "pkv_paged_attn_decode",
            "pkv_paged_attn_decode_step", "pkv_paged_attn_decode_noalloc", "pkv_paged_attn_prefill", "pkv_paged_attn_mixed", "pkv_attn_combine",
+           "pkv_rope_append", "pkv_paged_attn_tree", "pkv_tree_workspace_size", "pkv_kv_cache_compact",
            "pkv_get_device_error", "pkv_selftest_wait_timeout", "pkv_status_string", "pkv_version")
 DECODE_NOALLOC_SCRATCH_BYTES = 32 * 1024 * 1024   # PKV_DECODE_NOALLOC_SCRATCH_BYTES in include/pkv.h
 
@@ -50,6 +52,12 @@ class PkvError(RuntimeError):
     def __init__(self, status: int, where: str):
         self.status = status
         super().__init__("%s failed: %s (%d)" % (where, STATUS.get(status, "unknown"), status))
+
+
+class _Rope(ctypes.Structure):
+    _fields_ = [("rotary_dim", ctypes.c_int), ("interleaved", ctypes.c_int), ("inv_freq", ctypes.c_void_p),
+                ("mscale", ctypes.c_float), ("q_weight", ctypes.c_void_p), ("k_weight", ctypes.c_void_p),
+                ("eps", ctypes.c_float)]
 
 
 class _Cache(ctypes.Structure):
@@ -89,6 +97,15 @@ def load_library():
         lib.pkv_paged_attn_prefill.restype = I
         lib.pkv_paged_attn_mixed.argtypes = [_Cache, P, I, P, P, P, I, I, I, I, F, I, I, P, Z, P, I, P, P]
         lib.pkv_paged_attn_mixed.restype = I
+        L = ctypes.c_longlong
+        lib.pkv_rope_append.argtypes = [_Cache, _Rope, P, L, I, P, L, P, L, P, P, P, P, I, I, I, P, L, P]
+        lib.pkv_rope_append.restype = I
+        lib.pkv_tree_workspace_size.argtypes = [I, I, I, I]
+        lib.pkv_tree_workspace_size.restype = Z
+        lib.pkv_paged_attn_tree.argtypes = [_Cache, P, I, P, I, P, P, P, I, I, I, I, F, P, Z, P, I, P, P]
+        lib.pkv_paged_attn_tree.restype = I
+        lib.pkv_kv_cache_compact.argtypes = [_Cache, P, P, P, P, I, I, I, P]
+        lib.pkv_kv_cache_compact.restype = I
         lib.pkv_attn_combine.argtypes = [P, P, I, I, I, P, I, P, P]
         lib.pkv_attn_combine.restype = I
         lib.pkv_selftest_wait_timeout.argtypes = [ctypes.c_uint, P]
@@ -324,6 +341,131 @@ def paged_attn_mixed(cache, q, cu_q_lens, context_lens, block_tables, max_q_len:
                                     _dev(out, "out"), _dtype_code(out.dtype), _dev(lse, "lse"), _stream(stream)),
            "pkv_paged_attn_mixed")
     return out
+
+
+def _rows(t, heads, head_dim, name):
+    """Pointer and token stride (elements) of [T, heads, head_dim] rows whose tokens may be strided."""
+    if not t.is_cuda:
+        raise ValueError("%s must be a CUDA tensor (there is no CPU path)" % name)
+    if t.dim() != 3 or tuple(t.shape[1:]) != (heads, head_dim):
+        raise ValueError("%s must be [tokens, %d, %d]" % (name, heads, head_dim))
+    if t.stride(2) != 1 or (heads > 1 and t.stride(1) != head_dim):
+        raise ValueError("%s: the heads of a token must be contiguous" % name)
+    stride = t.stride(0) if t.shape[0] > 1 else heads * head_dim
+    return ctypes.c_void_p(t.data_ptr()), stride
+
+
+def _same_device(device, tensors):
+    for name, t in tensors.items():
+        if t is not None and t.device != device:
+            raise ValueError("%s is on %s, the cache on %s" % (name, t.device, device))
+
+
+def rope_append(cache, q, k, v, inv_freq, cu_new_lens, ctx_before, block_tables, positions, interleaved: bool = False,
+                mscale: float = 1.0, q_weight=None, k_weight=None, eps: float = 1e-6, q_out=None, stream=None,
+                scales=None):
+    """Norm (with q_weight / k_weight) and rotate the query and key heads of new tokens, write keys and values into
+    their pages as kv_cache_append does, and return the rotated queries [T, Hq, D].
+
+    q [T, Hq, D], k and v [T, Hkv, D]: the heads of a token contiguous, tokens at any stride of whole 16 bytes (views
+    of one fused projection). inv_freq: float32 [rotary_dim / 2], see `rope.rope_frequencies`; the first
+    2 * len(inv_freq) elements of each head are rotated, in pairs (i, i + rotary_dim / 2) or, interleaved,
+    (2i, 2i + 1). positions: int32 [T]. q_out: where the queries go (q itself: in place); a new tensor if None."""
+    torch = _torch()
+    lib = load_library()
+    if k.dtype != q.dtype or v.dtype != q.dtype or k.shape != v.shape or k.shape[0] != q.shape[0]:
+        raise TypeError("q / k / v must match each other")
+    c = _cache_struct(cache, q.dtype, scales)
+    hkv, d = cache.shape[2], cache.shape[4]
+    total, hq = q.shape[:2]
+    batch, mb = block_tables.shape
+    if inv_freq.dtype != torch.float32 or inv_freq.dim() != 1 or 2 * inv_freq.shape[0] > d:
+        raise ValueError("inv_freq must be float32 [rotary_dim / 2], rotary_dim <= head_dim")
+    if positions.shape != (total,):
+        raise ValueError("positions must be [tokens]")
+    if cu_new_lens.shape != (batch + 1,) or ctx_before.shape != (batch,):
+        raise ValueError("cu_new_lens must be [batch + 1], ctx_before [batch]")
+    for name, w in (("q_weight", q_weight), ("k_weight", k_weight)):
+        if w is not None and (w.dtype != q.dtype or tuple(w.shape) != (d,)):
+            raise ValueError("%s must be [head_dim] in the dtype of q" % name)
+    if q_out is None:
+        q_out = torch.empty((total, hq, d), dtype=q.dtype, device=q.device)
+    elif q_out.dtype != q.dtype or q_out.shape != q.shape:
+        raise ValueError("q_out must match q")
+    _same_device(cache.device, dict(q=q, k=k, v=v, inv_freq=inv_freq, positions=positions, cu_new_lens=cu_new_lens,
+                                    ctx_before=ctx_before, block_tables=block_tables, q_weight=q_weight,
+                                    k_weight=k_weight, q_out=q_out, scales=scales))
+    rope = _Rope(2 * inv_freq.shape[0], 1 if interleaved else 0, _dev(inv_freq, "inv_freq"), float(mscale),
+                 _dev(q_weight, "q_weight"), _dev(k_weight, "k_weight"), float(eps))
+    (qp, qs), (kp, ks), (vp, vs) = _rows(q, hq, d, "q"), _rows(k, hkv, d, "k"), _rows(v, hkv, d, "v")
+    op, os_ = _rows(q_out, hq, d, "q_out")
+    with torch.cuda.device(cache.device):
+        _check(lib.pkv_rope_append(c, rope, qp, qs, hq, kp, ks, vp, vs, _i32(positions, "positions"),
+                                   _i32(cu_new_lens, "cu_new_lens"), _i32(ctx_before, "ctx_before"),
+                                   _i32(block_tables, "block_tables"), batch, mb, total, op, os_, _stream(stream)),
+               "pkv_rope_append")
+    return q_out
+
+
+def tree_workspace_size(num_q_heads, num_kv_heads, head_dim, max_q_len) -> int:
+    return int(load_library().pkv_tree_workspace_size(num_q_heads, num_kv_heads, head_dim, max_q_len))
+
+
+def paged_attn_tree(cache, q, tree_mask, cu_q_lens, context_lens, block_tables, max_q_len: int,
+                    scale: Optional[float] = None, workspace=None, out=None, out_dtype=None, lse=None, stream=None):
+    """Drafted tokens ([sum n_b, Hq, D], their K/V already appended as each sequence's last n_b cached tokens) against
+    the paged context and, by tree_mask (int32 [sum n_b, words], bit j % 32 of word j / 32: node i sees node j; see
+    `workloads.tree_mask`), one another. Returns `out`."""
+    torch = _torch()
+    lib = load_library()
+    c = _cache_struct(cache, q.dtype)
+    total_q, hq, d = q.shape
+    batch, mb = block_tables.shape
+    if d != cache.shape[4]:
+        raise ValueError("q must have the cache's head_dim")
+    if tree_mask.dim() != 2 or tree_mask.shape[0] != total_q:
+        raise ValueError("tree_mask must be [rows of q, words]")
+    if cu_q_lens.shape != (batch + 1,) or context_lens.shape != (batch,):
+        raise ValueError("cu_q_lens must be [batch + 1], context_lens [batch]")
+    if out is None:
+        out = torch.empty((total_q, hq, d), dtype=out_dtype or q.dtype, device=q.device)
+    elif out.shape != q.shape:
+        raise ValueError("out must have the shape of q")
+    if lse is not None and (lse.dtype != torch.float32 or tuple(lse.shape) != (total_q, hq)):
+        raise ValueError("lse must be float32 [rows of q, Hq]")
+    if workspace is None:
+        workspace = torch.empty(tree_workspace_size(hq, cache.shape[2], d, max_q_len), dtype=torch.uint8,
+                                device=q.device)
+    _same_device(cache.device, dict(q=q, tree_mask=tree_mask, cu_q_lens=cu_q_lens, context_lens=context_lens,
+                                    block_tables=block_tables, workspace=workspace, out=out, lse=lse))
+    ws_bytes = workspace.numel() * workspace.element_size()
+    scale = (1.0 / math.sqrt(d)) if scale is None else float(scale)
+    with torch.cuda.device(cache.device):
+        _check(lib.pkv_paged_attn_tree(c, _dev(q, "q"), hq, _i32(tree_mask, "tree_mask"), int(tree_mask.shape[1]),
+                                       _i32(cu_q_lens, "cu_q_lens"), _i32(context_lens, "context_lens"),
+                                       _i32(block_tables, "block_tables"), batch, mb, total_q, int(max_q_len), scale,
+                                       _dev(workspace, "workspace"), ws_bytes, _dev(out, "out"),
+                                       _dtype_code(out.dtype), _dev(lse, "lse"), _stream(stream)),
+               "pkv_paged_attn_tree")
+    return out
+
+
+def kv_cache_compact(cache, keep_pos, cu_keep, dst_start, block_tables, stream=None, scales=None) -> None:
+    """Move the cached rows that are kept, in place: row k of sequence b from position keep_pos[cu_keep[b] + k] to
+    dst_start[b] + k (every source at or behind its destination). int32: keep_pos [num_keep], cu_keep [batch + 1],
+    dst_start [batch]."""
+    torch = _torch()
+    lib = load_library()
+    c = _cache_struct(cache, torch.float16 if is_fp8_cache(cache) else cache.dtype, scales)
+    batch, mb = block_tables.shape
+    if keep_pos.dim() != 1 or cu_keep.shape != (batch + 1,) or dst_start.shape != (batch,):
+        raise ValueError("keep_pos must be [num_keep], cu_keep [batch + 1], dst_start [batch]")
+    _same_device(cache.device, dict(keep_pos=keep_pos, cu_keep=cu_keep, dst_start=dst_start, block_tables=block_tables,
+                                    scales=scales))
+    with torch.cuda.device(cache.device):
+        _check(lib.pkv_kv_cache_compact(c, _i32(keep_pos, "keep_pos"), _i32(cu_keep, "cu_keep"),
+                                        _i32(dst_start, "dst_start"), _i32(block_tables, "block_tables"), batch, mb,
+                                        int(keep_pos.shape[0]), _stream(stream)), "pkv_kv_cache_compact")
 
 
 def attn_combine(partial_o, partial_lse, out=None, out_dtype=None, lse=None, stream=None):

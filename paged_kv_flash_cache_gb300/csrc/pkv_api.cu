@@ -5,6 +5,7 @@
 #include <stdint.h>
 
 #include <atomic>
+#include <cmath>
 #include <mutex>
 
 #include "pkv_internal.h"
@@ -527,6 +528,193 @@ pkv_status pkv_paged_attn_mixed(pkv_cache cache, const void *q, int num_q_heads,
     if (st != PKV_OK) return st;
     return prefill_impl(cache, q, num_q_heads, cu_q_lens, context_lens, block_tables, batch, max_blocks_per_seq,
                         total_q, max_q_len, scale, causal, out, out_dtype, lse, stream, 1);
+}
+
+pkv_status pkv_rope_append(pkv_cache cache, pkv_rope rope, const void *q, long long q_stride, int num_q_heads,
+                           const void *k, long long k_stride, const void *v, long long v_stride,
+                           const int *positions, const int *cu_new_lens, const int *ctx_before,
+                           const int *block_tables, int batch, int max_blocks_per_seq, int num_new_tokens,
+                           void *q_out, long long q_out_stride, void *stream) {
+    pkv_status st = check_cache(cache);
+    if (st != PKV_OK) return st;
+    if (batch < 0 || num_new_tokens < 0 || max_blocks_per_seq <= 0 || num_q_heads <= 0) return PKV_ERR_INVALID_ARG;
+    // whole 16-byte vectors hold whole pairs in both layouts
+    if (rope.rotary_dim < 0 || rope.rotary_dim > cache.head_dim) return PKV_ERR_INVALID_ARG;
+    if (rope.rotary_dim % 16 != 0) return PKV_ERR_UNSUPPORTED;
+    if (!(rope.eps >= 0.f) || !(rope.eps < INFINITY) || !(rope.mscale > -INFINITY) || !(rope.mscale < INFINITY))
+        return PKV_ERR_INVALID_ARG;
+    const long long q_row = (long long)num_q_heads * cache.head_dim, kv_row = (long long)cache.num_kv_heads * cache.head_dim;
+    if (q_stride < q_row || q_out_stride < q_row || k_stride < kv_row || v_stride < kv_row) return PKV_ERR_INVALID_ARG;
+    if (q_stride % 8 || q_out_stride % 8 || k_stride % 8 || v_stride % 8) return PKV_ERR_INVALID_ARG;
+    if (batch == 0 || num_new_tokens == 0) return PKV_OK;
+    if (!q || !k || !v || !positions || !cu_new_lens || !ctx_before || !block_tables || !q_out) return PKV_ERR_INVALID_ARG;
+    if (rope.rotary_dim > 0 && !rope.inv_freq) return PKV_ERR_INVALID_ARG;
+    if (!aligned16(q) || !aligned16(k) || !aligned16(v) || !aligned16(q_out) || !aligned16(rope.q_weight) ||
+        !aligned16(rope.k_weight))
+        return PKV_ERR_INVALID_ARG;
+    DeviceSlot *s = slot();
+    if (!s) return PKV_ERR_CUDA;
+    RopeArgs a;
+    a.cache = cache.ptr;
+    a.num_blocks = cache.num_blocks;
+    a.num_kv_heads = cache.num_kv_heads;
+    a.block_size = cache.block_size;
+    a.log2_block_size = ilog2(cache.block_size);
+    a.head_dim = cache.head_dim;
+    a.dtype = (int)cache.dtype;
+    a.fp8 = cache.format == PKV_KV_FP8_E4M3 ? 1 : 0;
+    a.scales = a.fp8 ? cache.scales : nullptr;
+    a.q = q;
+    a.k = k;
+    a.v = v;
+    a.q_stride = q_stride;
+    a.k_stride = k_stride;
+    a.v_stride = v_stride;
+    a.num_q_heads = num_q_heads;
+    a.positions = positions;
+    a.cu_new_lens = cu_new_lens;
+    a.ctx_before = ctx_before;
+    a.block_tables = block_tables;
+    a.batch = batch;
+    a.max_blocks_per_seq = max_blocks_per_seq;
+    a.num_new_tokens = num_new_tokens;
+    a.inv_freq = rope.inv_freq;
+    a.rotary_dim = rope.rotary_dim;
+    a.interleaved = rope.interleaved ? 1 : 0;
+    a.mscale = rope.mscale;
+    a.q_weight = rope.q_weight;
+    a.k_weight = rope.k_weight;
+    a.eps = rope.eps;
+    a.q_out = q_out;
+    a.q_out_stride = q_out_stride;
+    a.chunks = a.chunk_rows = 0;  // set by the launcher
+    a.err = s->err_ptr;
+    return launch_rope_append(a, static_cast<cudaStream_t>(stream)) == cudaSuccess ? PKV_OK : PKV_ERR_CUDA;
+}
+
+pkv_status pkv_kv_cache_compact(pkv_cache cache, const int *keep_pos, const int *cu_keep, const int *dst_start,
+                                const int *block_tables, int batch, int max_blocks_per_seq, int num_keep,
+                                void *stream) {
+    pkv_status st = check_cache(cache);
+    if (st != PKV_OK) return st;
+    if (batch < 0 || num_keep < 0 || max_blocks_per_seq <= 0) return PKV_ERR_INVALID_ARG;
+    if (batch == 0 || num_keep == 0) return PKV_OK;
+    if (!keep_pos || !cu_keep || !dst_start || !block_tables) return PKV_ERR_INVALID_ARG;
+    DeviceSlot *s = slot();
+    if (!s) return PKV_ERR_CUDA;
+    CompactArgs a;
+    a.cache = cache.ptr;
+    a.scales = cache.format == PKV_KV_FP8_E4M3 ? cache.scales : nullptr;
+    a.num_blocks = cache.num_blocks;
+    a.num_kv_heads = cache.num_kv_heads;
+    a.block_size = cache.block_size;
+    a.log2_block_size = ilog2(cache.block_size);
+    a.head_dim = cache.head_dim;
+    a.keep_pos = keep_pos;
+    a.cu_keep = cu_keep;
+    a.dst_start = dst_start;
+    a.block_tables = block_tables;
+    a.batch = batch;
+    a.max_blocks_per_seq = max_blocks_per_seq;
+    a.num_keep = num_keep;
+    a.parts = 1;  // set by the launcher, with slices
+    a.slices = 0;
+    a.err = s->err_ptr;
+    return launch_compact(a, static_cast<cudaStream_t>(stream)) == cudaSuccess ? PKV_OK : PKV_ERR_CUDA;
+}
+
+}  // extern "C"
+
+namespace pkv {
+namespace {
+
+// Rows of the tree kernel for a group of query heads: heads of a unit, nodes of a 128-row tile and of
+// a row block, rows of a partial.
+struct TreeRows {
+    int unit_heads, tile_nodes, block_nodes, part_rows;
+};
+
+TreeRows tree_rows(int group, int head_dim, int max_q_len) {
+    TreeRows t;
+    t.unit_heads = group;
+    for (int d = 128; t.unit_heads > 128; --d)
+        if (group % d == 0) t.unit_heads = d;
+    const int most = 128 / t.unit_heads;  // whole nodes a tile
+    t.tile_nodes = max_q_len < most ? max_q_len : most;
+    const int lanes = head_dim <= 128 ? 2 : 1;
+    t.block_nodes = t.tile_nodes * lanes;
+    t.part_rows = max_q_len > t.tile_nodes ? 128 * lanes : 128;
+    return t;
+}
+
+}  // namespace
+}  // namespace pkv
+
+extern "C" {
+
+size_t pkv_tree_workspace_size(int num_q_heads, int num_kv_heads, int head_dim, int max_q_len) {
+    if (num_q_heads <= 0 || num_kv_heads <= 0 || head_dim <= 0 || max_q_len <= 0 || num_q_heads % num_kv_heads != 0)
+        return 0;
+    const TreeRows t = tree_rows(num_q_heads / num_kv_heads, head_dim, max_q_len);
+    // a run's merge item, and its two partials: rows of head_dim outputs and an lse
+    return (size_t)kTreeMaxRuns * (sizeof(MergeItem) + 2 * (size_t)t.part_rows * ((size_t)head_dim + 1) * sizeof(float));
+}
+
+pkv_status pkv_paged_attn_tree(pkv_cache cache, const void *q, int num_q_heads, const int *tree_mask, int mask_words,
+                               const int *cu_q_lens, const int *context_lens, const int *block_tables, int batch,
+                               int max_blocks_per_seq, int total_q, int max_q_len, float scale, void *workspace,
+                               size_t workspace_bytes, void *out, pkv_dtype out_dtype, float *lse, void *stream) {
+    pkv_status st = check_cache(cache);
+    if (st != PKV_OK) return st;
+    if (cache.format != PKV_KV_NATIVE) return PKV_ERR_UNSUPPORTED;
+    if ((st = check_out_dtype(out_dtype, cache.dtype)) != PKV_OK) return st;
+    if (batch < 0 || max_blocks_per_seq <= 0 || num_q_heads <= 0 || total_q < 0 || max_q_len < 0 || mask_words < 0)
+        return PKV_ERR_INVALID_ARG;
+    if (num_q_heads % cache.num_kv_heads != 0) return PKV_ERR_INVALID_ARG;
+    if (!(scale > 0.f) || !(scale < INFINITY)) return PKV_ERR_INVALID_ARG;
+    if (batch == 0 || total_q == 0 || max_q_len == 0) return PKV_OK;
+    if (mask_words < max_q_len / 32 + (max_q_len % 32 != 0)) return PKV_ERR_INVALID_ARG;
+    if (!q || !tree_mask || !cu_q_lens || !context_lens || !block_tables || !out) return PKV_ERR_INVALID_ARG;
+    if (!aligned16(q) || !aligned16(out) || (lse && !aligned16(lse))) return PKV_ERR_INVALID_ARG;
+    const long long cap = (long long)max_blocks_per_seq * cache.block_size;
+    if (cap > (1ll << 30)) return PKV_ERR_UNSUPPORTED;
+    const size_t need = pkv_tree_workspace_size(num_q_heads, cache.num_kv_heads, cache.head_dim, max_q_len);
+    if (!workspace || workspace_bytes < need || !aligned16(workspace)) return PKV_ERR_WORKSPACE;
+    DeviceSlot *s = slot();
+    if (!s) return PKV_ERR_CUDA;
+    const int group = num_q_heads / cache.num_kv_heads;
+    const TreeRows t = tree_rows(group, cache.head_dim, max_q_len);
+    TreeArgs a;
+    a.cache = view_of(cache);
+    a.q = q;
+    a.num_q_heads = num_q_heads;
+    a.tree_mask = reinterpret_cast<const uint32_t *>(tree_mask);
+    a.mask_words = mask_words;
+    a.cu_q_lens = cu_q_lens;
+    a.context_lens = context_lens;
+    a.block_tables = block_tables;
+    a.batch = batch;
+    a.max_blocks_per_seq = max_blocks_per_seq;
+    a.total_q = total_q;
+    a.max_q_len = max_q_len;
+    a.scale = scale;
+    a.unit_heads = t.unit_heads;
+    a.head_groups = group / t.unit_heads;
+    a.units = cache.num_kv_heads * a.head_groups;
+    a.tile_nodes = t.tile_nodes;
+    a.block_nodes = t.block_nodes;
+    a.part_rows = t.part_rows;
+    a.part_o = reinterpret_cast<float *>(static_cast<uint8_t *>(workspace) + kTreeMaxRuns * sizeof(MergeItem));
+    a.part_lse = a.part_o + (size_t)kTreeMaxRuns * 2 * t.part_rows * cache.head_dim;
+    a.merge = static_cast<MergeItem *>(workspace);
+    a.out = out;
+    a.out_dtype = (int)out_dtype;
+    a.lse = lse;
+    a.err = s->err_ptr;
+    const int grid = s->info.num_sms < kTreeMaxRuns ? s->info.num_sms : kTreeMaxRuns;
+    const cudaError_t e = launch_tree(a, grid, static_cast<cudaStream_t>(stream));
+    if (e == cudaErrorNotSupported) return PKV_ERR_UNSUPPORTED;
+    return e == cudaSuccess ? PKV_OK : PKV_ERR_CUDA;
 }
 
 pkv_status pkv_get_device_error(void *stream, int *code) {

@@ -67,6 +67,68 @@ struct DecodeArgs {
     const void *k_new, *v_new;
 };
 
+struct RopeArgs {
+    void *cache;
+    int num_blocks, num_kv_heads, block_size, log2_block_size;
+    int head_dim, dtype, fp8;
+    float *scales;
+    const void *q, *k, *v;
+    long long q_stride, k_stride, v_stride;  // elements from token to token
+    int num_q_heads;
+    const int *positions, *cu_new_lens, *ctx_before, *block_tables;
+    int batch, max_blocks_per_seq, num_new_tokens;
+    const float *inv_freq;
+    int rotary_dim, interleaved;
+    float mscale;
+    const void *q_weight, *k_weight;
+    float eps;
+    void *q_out;
+    long long q_out_stride;
+    int chunks, chunk_rows;  // warps per token and head rows per warp (set by the launcher)
+    int *err;
+};
+
+struct CompactArgs {
+    void *cache;
+    float *scales;  // FP8 cache: row scales; nullptr: a native cache
+    int num_blocks, num_kv_heads, block_size, log2_block_size, head_dim;
+    const int *keep_pos, *cu_keep, *dst_start, *block_tables;
+    int batch, max_blocks_per_seq, num_keep;
+    int parts;         // column parts of a row (set by the launcher)
+    long long slices;  // (sequence, K or V, head, part) slices (set by the launcher)
+    int *err;
+};
+
+// An item that several runs of the tree kernel share (written by the run it begins in; nodes = 0: none).
+struct MergeItem {
+    int q0, node0, nodes, unit, parts;
+    int pad[3];
+};
+
+struct TreeArgs {
+    CacheView cache;
+    const void *q;
+    int num_q_heads;
+    const uint32_t *tree_mask;
+    int mask_words;  // 32-bit words of a mask row
+    const int *cu_q_lens, *context_lens, *block_tables;
+    int batch, max_blocks_per_seq, total_q, max_q_len;
+    float scale;
+    int unit_heads;   // query heads of a unit: a KV head's group, or its largest divisor up to 128
+    int head_groups;  // units per KV head
+    int units;        // num_kv_heads * head_groups
+    int tile_nodes;   // nodes of a 128-row tile
+    int block_nodes;  // nodes of a row block (one or two tiles)
+    int part_rows;    // rows of a partial
+    MergeItem *merge;  // [grid]
+    float *part_o;     // [grid][2][part_rows][D]
+    float *part_lse;   // [grid][2][part_rows], log2 units
+    void *out;
+    int out_dtype;
+    float *lse;
+    int *err;
+};
+
 struct CombineArgs {
     const float *part_o, *part_lse;
     int n_rows, num_splits, head_dim;
@@ -178,6 +240,14 @@ cudaError_t launch_prefill_wide(const PrefillArgs &a, cudaStream_t s);
 // tokens, 128-byte swizzle
 cudaError_t encode_q_heads_map(const void *q, int bf16, int total_q, int num_q_heads, int head_dim, int box_rows,
                                CUtensorMap *map);
+// q [total_q, Hq, D] as encode_q_heads_map, boxes of 64 columns x box_heads heads x box_rows tokens
+cudaError_t encode_q_group_map(const void *q, int bf16, int total_q, int num_q_heads, int head_dim, int box_heads,
+                               int box_rows, CUtensorMap *map);
+cudaError_t launch_rope_append(const RopeArgs &a, cudaStream_t s);
+cudaError_t launch_compact(const CompactArgs &a, cudaStream_t s);
+// Runs of the tree kernel at most (one CTA an SM): sizes its workspace without asking the device.
+constexpr int kTreeMaxRuns = 160;
+cudaError_t launch_tree(const TreeArgs &a, int grid, cudaStream_t s);
 int decode_ctas_per_sm(int head_dim, int group, int dtype);
 int decode_max_batch();
 

@@ -833,21 +833,26 @@ cudaError_t encode_cache_map(const CacheView &c, int box_rows, CUtensorMap *map)
     return cudaSuccess;
 }
 
-cudaError_t encode_q_heads_map(const void *q, int bf16, int total_q, int num_q_heads, int head_dim, int box_rows,
-                               CUtensorMap *map) {
+cudaError_t encode_q_group_map(const void *q, int bf16, int total_q, int num_q_heads, int head_dim, int box_heads,
+                               int box_rows, CUtensorMap *map) {
     EncodeTiledFn enc = encode_fn();
     if (!enc) return cudaErrorNotSupported;
-    if (total_q <= 0 || box_rows <= 0 || box_rows > 256) return cudaErrorNotSupported;
-    // q [total_q, Hq, D]: x = d, y = head, z = token; box 64 x 1 x box_rows
+    if (total_q <= 0 || box_rows <= 0 || box_rows > 256 || box_heads <= 0 || box_heads > 256) return cudaErrorNotSupported;
+    // q [total_q, Hq, D]: x = d, y = head, z = token; box 64 x box_heads x box_rows
     cuuint64_t dims[3] = {(cuuint64_t)head_dim, (cuuint64_t)num_q_heads, (cuuint64_t)total_q};
     cuuint64_t strides[2] = {(cuuint64_t)head_dim * 2, (cuuint64_t)num_q_heads * head_dim * 2};
-    cuuint32_t box[3] = {64, 1, (cuuint32_t)box_rows};
+    cuuint32_t box[3] = {64, (cuuint32_t)box_heads, (cuuint32_t)box_rows};
     cuuint32_t es[3] = {1, 1, 1};
     if (enc(map, bf16 ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16 : CU_TENSOR_MAP_DATA_TYPE_FLOAT16, 3, const_cast<void *>(q),
             dims, strides, box, es, CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
             CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) != CUDA_SUCCESS)
         return cudaErrorInvalidValue;
     return cudaSuccess;
+}
+
+cudaError_t encode_q_heads_map(const void *q, int bf16, int total_q, int num_q_heads, int head_dim, int box_rows,
+                               CUtensorMap *map) {
+    return encode_q_group_map(q, bf16, total_q, num_q_heads, head_dim, 1, box_rows, map);
 }
 
 cudaError_t encode_rows_map(const void *ptr, int bf16, long long rows, int cols, int box_cols, int box_rows,

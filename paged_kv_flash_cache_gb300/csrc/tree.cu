@@ -1,0 +1,794 @@
+// tree.cu -- paged_attn_tree: the drafted tokens of each sequence, a tree (or any set) of n_b nodes whose
+// keys and values are the sequence's last n_b cached tokens, attend to the paged context before them and,
+// among themselves, to the nodes that a bit mask gives each (its ancestors and itself).
+//
+// Mathematics: node i of sequence b sees position p when p < L_b - n_b, or when bit p - (L_b - n_b) of its
+// mask row is set; out = softmax over what it sees of (q . k * scale), times V ("为什么Attention是O(n²)",
+// mathematics section), keys read through the block table ("企业官网建设流程全解析", section 2.1; layout of
+// "Flash Attention与Paged Attention如何共同优化大模型推理？", section 3) in one pass with that page's
+// section 2 running max and sum.
+//
+// Rows: the query heads of a KV head read the same keys, so the rows of a product are (node, head of the
+// group): 128 of them a tile, whole nodes. S = Q K^T and O += P V are tcgen05.mma with M = 128.
+//
+// Two lanes. TMEM holds two score tiles and two outputs (head_dim up to 128), each with a warpgroup that
+// does its softmax, so that one lane's softmax overlaps the other's products:
+//   wide    a block of more than 128 rows: lane A its first 128 rows, lane B the others, both over every
+//           key tile (K and V come from memory once for both);
+//   narrow  up to 128 rows: both lanes the same rows, lane A the even key tiles, lane B the odd ones,
+//           their (max, sum, output) joined at the end.
+// At head_dim 256 the output takes half of TMEM: one lane, 64-key tiles.
+//
+// Work: the (sequence, KV head, row block) items, laid end to end in key tiles, are cut into equal runs,
+// one a CTA (one CTA an SM): any mix of lengths fills the GPU evenly, an item is split only where a run
+// ends, and a CTA leaves at most two partial items, so the workspace does not grow with the batch. A merge
+// kernel joins the partials of each split item in the order of the keys (no atomics: the same result every time).
+//
+// Warps: 0 loads Q and the K / V tiles by TMA into a ring (a lane per page), 1 issues the MMAs and owns
+// TMEM, 2 walks the run and hands its segments to the others, the warpgroups of lanes A and B do softmax and
+// output. P goes to the tensor cores as its 16-bit rounding plus the rounding's remainder (two products), so it
+// is not a rounding to 16 bits.
+//
+// Rows that see nothing (a padded node): 0 and -inf. Masked keys: their scores are replaced, never
+// multiplied, so that K may hold anything; V rows beyond the context are zeroed in shared memory, and a
+// drafted token's V is swept for infinities and NaN, since 0 * inf would reach rows that do not see it:
+// they are zeroed for the product and, for the rows that do see them, put back in the output.
+#include <cuda.h>
+
+#include "pkv_device.cuh"
+#include "pkv_internal.h"
+#include "tcgen05.cuh"
+#include "warp_mma.cuh"
+
+namespace pkv {
+namespace {
+
+constexpr int kBM = 128;              // rows of a tile
+constexpr float kRescaleLog2 = 8.0f;  // O is rescaled when the running max grows by more than 2^8
+constexpr int kSegs = 4;              // segments handed out ahead
+constexpr int kMinTiles = 2;          // key tiles of a run at least: both lanes have one
+
+// One run's part of an item: key tiles [t0, t1) of nodes [node0, node0 + nodes) of one sequence and KV
+// head (or share of its group). nodes = 0 ends the run.
+struct Segment {
+    int b, q0, n, len;       // sequence, its first row of q, nodes, cached tokens (drafted ones included)
+    int unit, node0, nodes;  // unit head, first node, nodes of this row block
+    int t0, t1;
+    int slot;  // -1: the whole item (the output is final); else the CTA's partial 0 or 1
+    int pad[2];
+};
+
+template <int D>
+struct TreeLayout {
+    static constexpr int kLanes = D <= 128 ? 2 : 1;
+    static constexpr int kBN = D <= 128 ? 128 : 64;  // keys a tile
+    static constexpr int kHalves = D / 64;           // 128-byte swizzle atoms along D
+    static constexpr uint32_t kQHalf = kBM * 128;
+    static constexpr uint32_t kQBytes = kHalves * kQHalf;
+    static constexpr uint32_t kTileHalf = kBN * 128;
+    static constexpr uint32_t kTileBytes = kHalves * kTileHalf;  // a K or a V tile
+    static constexpr int kRing = D == 64 ? 8 : 5;
+    static constexpr uint32_t kRingOff = kLanes * kQBytes;
+    static constexpr uint32_t kMlOff = kRingOff + kRing * kTileBytes;  // [128] (max, sum) between the lanes
+    static constexpr uint32_t kBarOff = kMlOff + kBM * 8;
+    static constexpr uint32_t kSegOff = kBarOff + 512;
+    static constexpr uint32_t kSmem = kSegOff + kSegs * sizeof(Segment) + 1024;  // + alignment slack
+    static constexpr int kThreads = 128 * (1 + kLanes);
+    // TMEM: S of lane x at kBN x (P in its place), O of lane x at 256 + 128 x
+    static constexpr uint32_t kColO = 256;
+};
+
+// What a run works on, from the lengths on the device; false (flagged) if they are out of range.
+struct SeqWork {
+    int q0, n, len;
+    long long tiles, blocks;  // key tiles, row blocks
+};
+
+__device__ __forceinline__ SeqWork seq_work(const TreeArgs &a, int b, int bn, bool flag) {
+    SeqWork w;
+    const int q1 = __ldg(a.cu_q_lens + b + 1);
+    w.q0 = __ldg(a.cu_q_lens + b);
+    w.len = __ldg(a.context_lens + b);
+    w.n = q1 - w.q0;
+    w.tiles = w.blocks = 0;
+    const bool ok = w.q0 >= 0 && q1 >= w.q0 && q1 <= a.total_q && w.n <= a.max_q_len && w.len >= w.n &&
+                    w.len <= (a.max_blocks_per_seq << a.cache.log2_block_size);
+    if (!ok) {
+        if (flag) set_error(a.err, kErrDeviceRange);
+        w.n = 0;
+    }
+    if (w.n > 0) {
+        w.tiles = (w.len + bn - 1) / bn;
+        w.blocks = (w.n + a.block_nodes - 1) / a.block_nodes;
+    }
+    return w;
+}
+
+// 32 mask bits of a row for keys j .. j + 31 of the tree (j may be negative: context, seen by all; bits at
+// or behind n are not set).
+__device__ __forceinline__ uint32_t mask_word(const uint32_t *row, int w, int n) {
+    if (w < 0) return 0xffffffffu;
+    const int left = n - 32 * w;
+    if (left <= 0) return 0u;
+    const uint32_t x = __ldg(row + w);
+    return left < 32 ? x & ((1u << left) - 1u) : x;
+}
+
+template <bool BF16>
+__device__ __forceinline__ bool nonfinite_pair(uint32_t w) {
+    constexpr uint32_t m = BF16 ? 0x7f80u : 0x7c00u;
+    return (w & m) == m || ((w >> 16) & m) == m;
+}
+
+template <bool BF16>
+__device__ __forceinline__ uint32_t drop_nonfinite(uint32_t w) {
+    constexpr uint32_t m = BF16 ? 0x7f80u : 0x7c00u;
+    if ((w & m) == m) w &= 0xffff0000u;
+    if (((w >> 16) & m) == m) w &= 0x0000ffffu;
+    return w;
+}
+
+template <int D, bool BF16>
+__global__ void __launch_bounds__(TreeLayout<D>::kThreads, 1)
+    tree_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CUtensorMap tm_kv, TreeArgs a) {
+    using L = TreeLayout<D>;
+    constexpr int kBN = L::kBN, kLanes = L::kLanes, kRing = L::kRing;
+    extern __shared__ uint8_t smem_raw[];
+    // 1024-byte alignment: the 128-byte swizzle pattern is a function of address bits 4-9.
+    uint8_t *smem = smem_raw + ((1024u - (smem_addr(smem_raw) & 1023u)) & 1023u);
+    uint8_t *sQ = smem;
+    uint8_t *sRing = smem + L::kRingOff;
+    float2 *sMl = reinterpret_cast<float2 *>(smem + L::kMlOff);
+    uint64_t *bars = reinterpret_cast<uint64_t *>(smem + L::kBarOff);
+    uint64_t *kv_full = bars;              // [kRing]
+    uint64_t *kv_empty = kv_full + kRing;  // [kRing]
+    uint64_t *q_full = kv_empty + kRing;   // a segment's Q tiles have landed
+    uint64_t *q_empty = q_full + 1;        // its QK products are done
+    uint64_t *s_full = q_empty + 1;        // [2] S of a lane computed (and its last P V done)
+    uint64_t *p_full = s_full + 2;         // [2] P written over it
+    uint64_t *o_done = p_full + 2;         // every P V of the segment is done
+    uint64_t *o_empty = o_done + 1;        // its outputs are read
+    uint64_t *ml_full = o_empty + 1;       // narrow: (max, sum) handed over
+    uint64_t *seg_full = ml_full + 1;      // [kSegs]
+    uint64_t *seg_empty = seg_full + kSegs;
+    uint64_t *drain = seg_empty + kSegs;   // every MMA issued has completed
+    unsigned long long *s_total = reinterpret_cast<unsigned long long *>(drain + 1);
+    uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(s_total + 1);
+    volatile int *abort_flag = reinterpret_cast<volatile int *>(tmem_slot + 1);
+    volatile int *s_poison = abort_flag + 1;  // [4] by segment: V of a drafted token was not finite
+    Segment *segs = reinterpret_cast<Segment *>(smem + L::kSegOff);
+
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const int gu = a.unit_heads;  // query heads of a unit
+    constexpr int kSoftmaxWarps = 4 * kLanes;
+
+    if (threadIdx.x == 0) {
+        for (int i = 0; i < kRing; ++i) {
+            mbar_init(&kv_full[i], 1);
+            mbar_init(&kv_empty[i], 1);
+        }
+        mbar_init(q_full, 1);
+        mbar_init(q_empty, 1);
+        for (int i = 0; i < 2; ++i) {
+            mbar_init(&s_full[i], 1);
+            mbar_init(&p_full[i], 4);
+        }
+        mbar_init(o_done, 1);
+        mbar_init(o_empty, kSoftmaxWarps);
+        mbar_init(ml_full, kSoftmaxWarps);
+        for (int i = 0; i < kSegs; ++i) {
+            mbar_init(&seg_full[i], 1);
+            mbar_init(&seg_empty[i], 2 + kSoftmaxWarps);  // producer, MMA, softmax warps
+        }
+        mbar_init(drain, 1);
+        *s_total = 0;
+        *abort_flag = 0;
+        s_poison[0] = s_poison[1] = s_poison[2] = s_poison[3] = 0;
+        fence_barrier_init();
+    }
+    if (warp == 1) {
+        tc::tmem_alloc(tmem_slot, 512);
+        tc::tmem_relinquish();
+    }
+    tc::fence_before_sync();
+    __syncthreads();
+    tc::fence_after_sync();
+    const uint32_t tmem = *tmem_slot;
+    pdl_wait();  // lengths, tables, masks, q and the drafted K / V may come from the previous kernel
+
+    // the whole batch's key tiles, and this CTA's run of them
+    {
+        long long mine = 0;
+        for (int b = threadIdx.x; b < a.batch; b += L::kThreads) {
+            const SeqWork w = seq_work(a, b, kBN, blockIdx.x == 0);
+            mine += w.tiles * w.blocks;
+        }
+#pragma unroll
+        for (int o = 16; o > 0; o >>= 1) mine += __shfl_xor_sync(0xffffffffu, mine, o);
+        if (lane == 0 && mine) atomicAdd(s_total, (unsigned long long)mine);
+    }
+    __syncthreads();
+    const long long total = (long long)*s_total * a.units;
+    long long run = (total + gridDim.x - 1) / gridDim.x;
+    if (run < kMinTiles) run = kMinTiles;
+
+    // segment i of the run: wait for it and copy it out
+    uint32_t seg_i = 0;
+    auto next_segment = [&](Segment &s) -> bool {
+        if (!mbar_wait(&seg_full[seg_i % kSegs], (seg_i / kSegs) & 1u, abort_flag, a.err)) return false;
+        s = segs[seg_i % kSegs];
+        return s.nodes > 0;
+    };
+    // the nodes of lane A's tile, whether the block is wide, and the rows of lane x
+    auto lane_nodes = [&](const Segment &s, int x) -> int {
+        if (s.nodes <= a.tile_nodes) return s.nodes;  // narrow
+        return x == 0 ? a.tile_nodes : s.nodes - a.tile_nodes;
+    };
+
+    if (warp < 4) {
+        if constexpr (kLanes == 2) tc::regs_dec<72>();
+        if (warp == 0) {
+            // ==================================== TMA producer ====================================
+            const int bs = a.cache.block_size, lbs = a.cache.log2_block_size;
+            const int box_rows = bs < kBN ? bs : kBN;
+            const uint64_t pol = l2_policy_evict_first();
+            if (lane == 0) {
+                tc::prefetch_tensormap(&tm_q);
+                tc::prefetch_tensormap(&tm_kv);
+            }
+            uint32_t item = 0, qn = 0;
+            bool ok = true;
+            Segment s;
+            for (; (ok = next_segment(s)); ++seg_i) {
+                const bool wide = s.nodes > a.tile_nodes;
+                const int T = s.t1 - s.t0, ahead = kLanes == 1 || wide ? 1 : 2;
+                const int kvh = s.unit / a.head_groups;
+                const int *bt = a.block_tables + (size_t)s.b * a.max_blocks_per_seq;
+                // tile j's K (kv 0) or V (kv 1), a lane per page; ids of tile j in each lane
+                auto pages = [&](int j) -> int {
+                    const int start = (s.t0 + j) * kBN, n = min(kBN, s.len - start);
+                    const int npages = bs < kBN ? (n + bs - 1) >> lbs : 1;
+                    int pb = 0;
+                    if (lane < npages) {
+                        pb = __ldg(bt + (start >> lbs) + lane);
+                        if (pb < 0 || pb >= a.cache.num_blocks) {
+                            set_error(a.err, kErrDeviceRange);
+                            pb = 0;
+                        }
+                    }
+                    return pb;
+                };
+                auto issue = [&](int j, int kv, int pb) -> bool {
+                    const int start = (s.t0 + j) * kBN, n = min(kBN, s.len - start);
+                    const int npages = bs < kBN ? (n + bs - 1) >> lbs : 1;
+                    const int off = bs < kBN ? 0 : (start & (bs - 1));
+                    const uint32_t slot = item % kRing;
+                    if (!mbar_wait(&kv_empty[slot], ((item / kRing) & 1u) ^ 1u, abort_flag, a.err)) return false;
+                    if (lane == 0) mbar_arrive_expect_tx(&kv_full[slot], (uint32_t)npages * box_rows * 128u * L::kHalves);
+                    __syncwarp();
+                    if (lane < npages) {
+                        const int row = ((pb * 2 + kv) * a.cache.num_kv_heads + kvh) * bs + off;
+                        uint8_t *dst = sRing + slot * L::kTileBytes + (uint32_t)lane * box_rows * 128u;
+#pragma unroll
+                        for (int hf = 0; hf < L::kHalves; ++hf)
+                            tc::tma_load_2d_hint(dst + hf * L::kTileHalf, &tm_kv, hf * 64, row, &kv_full[slot], pol);
+                    }
+                    ++item;
+                    return true;
+                };
+                // Q: the block's nodes, gu heads each, one box per tile and 64 columns
+                if (!(ok = mbar_wait(q_empty, (qn & 1u) ^ 1u, abort_flag, a.err))) break;
+                if (lane == 0) {
+                    const int tiles = wide ? 2 : 1;
+                    mbar_arrive_expect_tx(q_full, (uint32_t)tiles * a.tile_nodes * gu * 128u * L::kHalves);
+                    for (int x = 0; x < tiles; ++x)
+#pragma unroll
+                        for (int hf = 0; hf < L::kHalves; ++hf)
+                            tc::tma_load_3d(sQ + x * L::kQBytes + hf * L::kQHalf, &tm_q, hf * 64, s.unit * gu,
+                                            s.q0 + s.node0 + x * a.tile_nodes, q_full);
+                }
+                ++qn;
+                // ring order = the order of use: K of the first tiles, then V_j, K_{j + ahead}
+                int pb[3];
+                pb[0] = pages(0);
+                ok = issue(0, 0, pb[0]);
+                if (ok && ahead == 2 && T > 1) {
+                    pb[1] = pages(1);
+                    ok = issue(1, 0, pb[1]);
+                }
+                for (int j = 0; ok && j < T; ++j) {
+                    if (j + ahead < T) pb[ahead] = pages(j + ahead);
+                    ok = issue(j, 1, pb[0]);
+                    if (ok && j + ahead < T) ok = issue(j + ahead, 0, pb[ahead]);
+                    pb[0] = pb[1];
+                    pb[1] = pb[2];
+                }
+                __syncwarp();
+                if (lane == 0) mbar_arrive(&seg_empty[seg_i % kSegs]);
+                if (!ok) break;
+            }
+            // every copy has landed before the CTA exits (bounded), also when another role gave up
+            volatile int no_abort = 0;
+            for (uint32_t i = item > (uint32_t)kRing ? item - kRing : 0u; i < item; ++i)
+                mbar_wait(&kv_full[i % kRing], (i / kRing) & 1u, &no_abort, nullptr);
+            if (qn > 0) mbar_wait(q_full, (qn - 1) & 1u, &no_abort, nullptr);
+        } else if (warp == 1) {
+            // ====================================== MMA issuer ======================================
+            if (lane == 0) {
+                const uint32_t id_qk = tc::idesc_f16(BF16, kBM, kBN, false);
+                const uint32_t id_pv = tc::idesc_f16(BF16, kBM, D, true);
+                const uint32_t aQ = smem_addr(sQ), aRing = smem_addr(sRing);
+                uint32_t item = 0;       // ring items taken before this segment
+                uint32_t np[2] = {0, 0};  // P tiles taken, by lane
+                bool ok = true;
+                Segment s;
+                for (; (ok = next_segment(s)); ++seg_i) {
+                    const bool wide = s.nodes > a.tile_nodes;
+                    const int T = s.t1 - s.t0, ahead = kLanes == 1 || wide ? 1 : 2;
+                    // ring items of tile j (see the producer's order)
+                    auto k_item = [&](int j) { return item + (j < ahead ? j : 2 * j - ahead + 1); };
+                    auto v_item = [&](int j) { return item + j + min(T, ahead + j); };
+                    auto full = [&](uint32_t i) {
+                        return mbar_wait(&kv_full[i % kRing], (i / kRing) & 1u, abort_flag, a.err);
+                    };
+                    auto qk = [&](int x, int j, bool last_use) -> bool {
+                        const uint32_t i = k_item(j);
+                        if (!full(i)) return false;
+                        tc::fence_after_sync();
+                        const uint32_t aK = aRing + (i % kRing) * L::kTileBytes;
+                        const uint32_t aQx = aQ + (wide ? x : 0) * L::kQBytes;
+#pragma unroll
+                        for (int kk = 0; kk < D / 16; ++kk)
+                            tc::mma_f16_ss(tmem + kBN * x,
+                                           tc::smem_desc(aQx + (kk >> 2) * L::kQHalf + (kk & 3) * 32u, 16, 1024),
+                                           tc::smem_desc(aK + (kk >> 2) * L::kTileHalf + (kk & 3) * 32u, 16, 1024), id_qk,
+                                           kk > 0 ? 1u : 0u);
+                        tc::mma_commit(&s_full[x]);
+                        if (last_use) tc::mma_commit(&kv_empty[i % kRing]);
+                        return true;
+                    };
+                    auto pv = [&](int x, int j, bool first, bool last_use) -> bool {
+                        if (!mbar_wait(&p_full[x], np[x] & 1u, abort_flag, a.err)) return false;
+                        ++np[x];
+                        const uint32_t i = v_item(j);
+                        if (!full(i)) return false;
+                        // the segment's first P V overwrites an output: the last segment's must be read
+                        if (first && !mbar_wait(o_empty, (seg_i & 1u) ^ 1u, abort_flag, a.err)) return false;
+                        tc::fence_after_sync();
+                        const uint32_t aV = aRing + (i % kRing) * L::kTileBytes;
+                        const uint32_t tO = tmem + L::kColO + 128u * x, tP = tmem + kBN * x;
+#pragma unroll
+                        for (int part = 0; part < 2; ++part)
+#pragma unroll
+                            for (int kk = 0; kk < kBN / 16; ++kk)
+                                tc::mma_f16_ts(tO, tP + (uint32_t)(kBN / 2) * part + 8u * kk,
+                                               tc::smem_desc(aV + (uint32_t)kk * 2048u, L::kTileHalf, 1024), id_pv,
+                                               (first && part == 0 && kk == 0) ? 0u : 1u);
+                        if (last_use) tc::mma_commit(&kv_empty[i % kRing]);
+                        return true;
+                    };
+                    if (!(ok = mbar_wait(q_full, seg_i & 1u, abort_flag, a.err))) break;
+                    tc::fence_after_sync();
+                    if (kLanes == 1 || wide) {
+                        ok = qk(0, 0, kLanes == 1) && (kLanes == 1 || qk(1, 0, true));
+                        for (int j = 0; ok && j < T; ++j) {
+                            const bool more = j + 1 < T;
+                            if (!more) tc::mma_commit(q_empty);  // every QK of the segment is issued
+                            ok = pv(0, j, j == 0, kLanes == 1) && (!more || qk(0, j + 1, kLanes == 1));
+                            if (kLanes == 2) ok = ok && pv(1, j, j == 0, true) && (!more || qk(1, j + 1, true));
+                        }
+                    } else {
+                        ok = qk(0, 0, true) && (T < 2 || qk(1, 1, true));
+                        for (int j = 0; ok && j < T; ++j) {
+                            const bool more = j + 2 < T;
+                            if (j + 2 == T || T == 1) tc::mma_commit(q_empty);
+                            ok = pv(j & 1, j, j < 2, true) && (!more || qk(j & 1, j + 2, true));
+                        }
+                    }
+                    if (!ok) break;
+                    tc::mma_commit(o_done);
+                    item += 2 * T;
+                    mbar_arrive(&seg_empty[seg_i % kSegs]);
+                }
+                tc::mma_commit(drain);
+                volatile int no_abort = 0;
+                mbar_wait(drain, 0, &no_abort, a.err);
+            }
+            __syncwarp();
+        } else if (warp == 2) {
+            // ================================== walk of the run ==================================
+            const long long begin = run * blockIdx.x, end = min(total, begin + run);
+            uint32_t n = 0;
+            bool ok = true;
+            MergeItem left = {};  // the item that begins in this run and goes on in the next ones
+            auto publish = [&](const Segment &s) -> bool {
+                if (!mbar_wait(&seg_empty[n % kSegs], ((n / kSegs) & 1u) ^ 1u, abort_flag, a.err)) return false;
+                if (lane == 0) {
+                    segs[n % kSegs] = s;
+                    mbar_arrive(&seg_full[n % kSegs]);
+                }
+                ++n;
+                return true;
+            };
+            long long before = 0;  // key tiles of the sequences passed
+            for (int b0 = 0; ok && b0 < a.batch && before < end; b0 += 32) {
+                SeqWork w = {0, 0, 0, 0, 0};
+                if (b0 + lane < a.batch) w = seq_work(a, b0 + lane, kBN, false);
+                const long long mine = w.tiles * w.blocks * a.units;
+                long long scan = mine;
+#pragma unroll
+                for (int o = 1; o < 32; o <<= 1) {
+                    const long long y = __shfl_up_sync(0xffffffffu, scan, o);
+                    if (lane >= o) scan += y;
+                }
+                const long long first = before + scan - mine, last = before + scan;
+                unsigned hit = __ballot_sync(0xffffffffu, mine > 0 && first < end && last > begin);
+                before += __shfl_sync(0xffffffffu, scan, 31);
+                while (ok && hit) {
+                    const int src = __ffs(hit) - 1;
+                    hit &= hit - 1;
+                    Segment s = {};
+                    s.b = b0 + src;
+                    s.q0 = __shfl_sync(0xffffffffu, w.q0, src);
+                    s.n = __shfl_sync(0xffffffffu, w.n, src);
+                    s.len = __shfl_sync(0xffffffffu, w.len, src);
+                    const long long s0 = __shfl_sync(0xffffffffu, first, src), s1 = __shfl_sync(0xffffffffu, last, src);
+                    const int tiles = (int)__shfl_sync(0xffffffffu, w.tiles, src);
+                    const int blocks = (int)__shfl_sync(0xffffffffu, w.blocks, src);
+                    for (long long at = max(begin, s0); ok && at < min(end, s1); at += s.t1 - s.t0) {
+                        // the row blocks of a KV head follow one another: the second finds the keys in L2
+                        const long long it = (at - s0) / tiles;
+                        s.unit = (int)(it / blocks);
+                        s.node0 = (int)(it % blocks) * a.block_nodes;
+                        s.nodes = min(a.block_nodes, s.n - s.node0);
+                        s.t0 = (int)((at - s0) % tiles);
+                        s.t1 = (int)min((long long)tiles, s.t0 + (end - at));
+                        s.slot = s.t0 > 0 ? 0 : (s.t1 < tiles ? 1 : -1);
+                        if (s.slot == 1) {
+                            const long long item_end = s0 + it * tiles + tiles - 1;  // its last key tile
+                            left.q0 = s.q0;
+                            left.node0 = s.node0;
+                            left.nodes = s.nodes;
+                            left.unit = s.unit;
+                            left.parts = (int)(item_end / run - blockIdx.x) + 1;
+                        }
+                        ok = publish(s);
+                    }
+                }
+            }
+            if (lane == 0) a.merge[blockIdx.x] = left;
+            if (ok) publish(Segment{});
+        }
+    } else {
+        // ================================ softmax + output: lane x ================================
+        if constexpr (kLanes == 2) tc::regs_inc<208>();
+        const int x = (warp - 4) >> 2, w4 = warp & 3;
+        const int r = w4 * 32 + lane;  // row of the tile = TMEM lane
+        const uint32_t lane_base = (uint32_t)(w4 * 32) << 16;
+        const float c2 = a.scale * kLog2e;
+        const int node_r = r / gu, head_r = r - node_r * gu;
+        const uint32_t tS = tmem + kBN * x + lane_base;
+        const uint32_t tO = tmem + L::kColO + 128u * x + lane_base;
+        uint32_t ns = 0;    // score tiles of this lane so far
+        uint32_t item = 0;  // ring items before this segment
+        uint32_t nml = 0;   // narrow segments so far
+        Segment s;
+        for (; next_segment(s); ++seg_i) {
+            const bool wide = s.nodes > a.tile_nodes;
+            const bool split = kLanes == 2 && !wide;  // the lanes share the rows
+            const int T = s.t1 - s.t0, ahead = kLanes == 1 || wide ? 1 : 2;
+            const int rows = lane_nodes(s, x) * gu;
+            const bool row_ok = r < rows, warp_ok = w4 * 32 < rows;  // warp_ok: uniform
+            const int tree0 = s.len - s.n;  // position of node 0
+            const int node = s.node0 + (wide ? x * a.tile_nodes : 0) + node_r;
+            const uint32_t *mrow = a.tree_mask + (size_t)(s.q0 + node) * a.mask_words;
+            float m = -INFINITY, l = 0.f;
+            bool ok = true;
+            for (int j = split ? x : 0; j < T; j += split ? 2 : 1, ++ns) {
+                const int start = (s.t0 + j) * kBN;
+                const int j0 = start - tree0;          // tree index of the tile's first key (negative: context)
+                const bool tail = j0 + kBN > 0;        // drafted tokens (or the end) in this tile
+                uint32_t vis[kBN / 32];
+                if (tail) {
+#pragma unroll
+                    for (int i = 0; i < kBN / 32; ++i) vis[i] = 0u;
+                    if (row_ok) {
+                        const int w0 = j0 >> 5;
+                        uint32_t lo = mask_word(mrow, w0, s.n);
+#pragma unroll
+                        for (int i = 0; i < kBN / 32; ++i) {
+                            const uint32_t hi = mask_word(mrow, w0 + i + 1, s.n);
+                            vis[i] = __funnelshift_r(lo, hi, j0 & 31);
+                            lo = hi;
+                        }
+                    }
+                }
+                if (!(ok = mbar_wait(&s_full[x], ns & 1u, abort_flag, a.err))) break;
+                tc::fence_after_sync();
+                if (warp_ok) {
+                    float v[kBN];
+#pragma unroll
+                    for (int cc = 0; cc < kBN / 32; ++cc)
+                        tc::tmem_ld32(tS + cc * 32, *reinterpret_cast<float(*)[32]>(&v[cc * 32]));
+                    tc::tmem_wait_ld();
+                    if (tail) {
+#pragma unroll
+                        for (int i = 0; i < kBN; ++i) v[i] = (vis[i / 32] >> (i % 32)) & 1u ? v[i] : -INFINITY;
+                    }
+                    float m8[8];
+#pragma unroll
+                    for (int q = 0; q < 8; ++q) m8[q] = fmax3(v[q], v[q + 8], v[q + 16]);
+#pragma unroll
+                    for (int i = 24; i < kBN; i += 16)
+#pragma unroll
+                        for (int q = 0; q < 8; ++q)
+                            m8[q] = fmax3(m8[q], v[i + q], (i + 8 + q < kBN) ? v[i + 8 + q] : -INFINITY);
+                    const float mx = fmaxf(fmax3(m8[0], m8[1], m8[2]), fmax3(fmax3(m8[3], m8[4], m8[5]), m8[6], m8[7]));
+                    const float m_new = fmaxf(m, mx * c2);
+                    const bool grow = m_new > m + kRescaleLog2;  // false while the row has seen nothing
+                    const float alpha = grow ? ex2f(m - m_new) : 1.f;  // 0 when m = -inf
+                    if (grow) {
+                        m = m_new;
+                        l *= alpha;
+                    }
+                    // O of the lane's earlier tiles (its last P V was issued before this S: done)
+                    if (j >= (split ? 2 : 1) && __any_sync(0xffffffffu, grow)) {
+#pragma unroll
+                        for (int cc = 0; cc < D / 32; ++cc) {
+                            float o[32];
+                            tc::tmem_ld32(tO + cc * 32, o);
+                            tc::tmem_wait_ld();
+#pragma unroll
+                            for (int i = 0; i < 32; ++i) o[i] *= alpha;
+                            tc::tmem_st32(tO + cc * 32, o);
+                        }
+                    }
+                    const float base = m == -INFINITY ? 0.f : m;  // a row that has seen nothing: ex2(-inf - 0) = 0
+                    const float2 cc2 = make_float2(c2, c2), nm2 = make_float2(-base, -base);
+                    float2 l4[4] = {make_float2(0.f, 0.f), make_float2(0.f, 0.f), make_float2(0.f, 0.f),
+                                    make_float2(0.f, 0.f)};
+#pragma unroll
+                    for (int cc = 0; cc < kBN / 32; ++cc) {
+                        uint32_t ph[16], pl[16];
+#pragma unroll
+                        for (int q = 0; q < 16; ++q) {
+                            const float2 xq = ffma2(make_float2(v[cc * 32 + 2 * q], v[cc * 32 + 2 * q + 1]), cc2, nm2);
+                            const float2 e = make_float2(ex2f(xq.x), ex2f(xq.y));
+                            l4[q & 3] = fadd2(l4[q & 3], e);
+                            split_pair<BF16>(e.x, e.y, ph[q], pl[q]);
+                        }
+                        tc::tmem_st16(tS + cc * 16, ph);
+                        tc::tmem_st16(tS + kBN / 2 + cc * 16, pl);
+                    }
+                    const float2 ls = fadd2(fadd2(l4[0], l4[1]), fadd2(l4[2], l4[3]));
+                    l += ls.x + ls.y;
+                }
+                // V of drafted tokens and beyond the end: zero what is past the end, sweep the drafted rows
+                if (tail && (split || x == 0)) {
+                    const uint32_t vi = item + j + min(T, ahead + j);
+                    if (!(ok = mbar_wait(&kv_full[vi % kRing], (vi / kRing) & 1u, abort_flag, a.err))) break;
+                    uint8_t *sV = sRing + (vi % kRing) * L::kTileBytes;
+                    const int n_valid = min(kBN, s.len - start);
+                    bool bad = false;
+                    // 8 lanes a row (128 bytes of a 64-column half), 4 rows a warp and step
+                    for (int row = max(0, -j0) / 16 * 16 + w4 * 4 + (lane >> 3); row < kBN; row += 16)
+#pragma unroll
+                        for (int hf = 0; hf < L::kHalves; ++hf) {
+                            uint4 *p = reinterpret_cast<uint4 *>(sV + hf * L::kTileHalf + (uint32_t)row * 128u + (lane & 7) * 16);
+                            if (row >= n_valid) {
+                                *p = make_uint4(0, 0, 0, 0);
+                            } else if (row >= -j0) {
+                                uint4 q = *p;
+                                if (nonfinite_pair<BF16>(q.x) || nonfinite_pair<BF16>(q.y) || nonfinite_pair<BF16>(q.z) ||
+                                    nonfinite_pair<BF16>(q.w)) {
+                                    q = make_uint4(drop_nonfinite<BF16>(q.x), drop_nonfinite<BF16>(q.y),
+                                                   drop_nonfinite<BF16>(q.z), drop_nonfinite<BF16>(q.w));
+                                    *p = q;
+                                    bad = true;
+                                }
+                            }
+                        }
+                    if (bad) s_poison[seg_i & 3u] = 1;
+                    tc::fence_proxy_async_smem();
+                }
+                tc::tmem_wait_st();
+                tc::fence_before_sync();
+                __syncwarp();
+                if (lane == 0) mbar_arrive(&p_full[x]);
+            }
+            if (!ok) break;
+            // ---- output of the segment ----
+            // rows shared by the lanes: rows 0-63 are finished by lane A, 64-127 by lane B
+            const bool mine = !split || (w4 >> 1) == x;
+            float fa = 1.f, fb = 0.f, lse2 = m, lt = l;  // out = fa O_A + fb O_B (or f O of this lane)
+            if (split) {
+                if (!mine) sMl[r] = make_float2(m, l);
+                __syncwarp();
+                if (lane == 0) mbar_arrive(ml_full);
+                if (!mbar_wait(ml_full, nml & 1u, abort_flag, a.err)) break;
+                ++nml;
+                if (mine) {
+                    const float2 o = sMl[r];
+                    const float M = fmaxf(m, o.x);
+                    const float w_me = m == -INFINITY ? 0.f : ex2f(m - M), w_o = o.x == -INFINITY ? 0.f : ex2f(o.x - M);
+                    lt = w_me * l + w_o * o.y;
+                    lse2 = M;
+                    fa = x == 0 ? w_me : w_o;
+                    fb = x == 0 ? w_o : w_me;
+                }
+            }
+            const float inv = lt > 0.f ? 1.f / lt : (lt == 0.f ? 0.f : lt);  // (a NaN sum stays NaN)
+            lse2 = lt == 0.f ? -INFINITY : lse2 + __log2f(lt);
+            fa *= inv;
+            fb *= inv;
+            if (!mbar_wait(o_done, seg_i & 1u, abort_flag, a.err)) break;
+            tc::fence_after_sync();
+            if (mine && warp_ok) {
+                const bool poison = s_poison[seg_i & 3u] != 0;
+                const size_t orow = (size_t)(s.q0 + node) * a.num_q_heads + (size_t)s.unit * gu + head_r;
+                const size_t prow = ((size_t)blockIdx.x * 2 + (s.slot > 0)) * a.part_rows + (wide ? x * kBM : 0) + r;
+                const uint32_t tOa = tmem + L::kColO + lane_base + (wide ? 128u * x : 0u);
+#pragma unroll
+                for (int cc = 0; cc < D / 32; ++cc) {
+                    float o[32];
+                    tc::tmem_ld32(tOa + cc * 32, o);
+                    if (split) {
+                        float p[32];
+                        tc::tmem_ld32(tOa + 128u + cc * 32, p);
+                        tc::tmem_wait_ld();
+                        // a lane without a tile left its output as it was: not read
+#pragma unroll
+                        for (int i = 0; i < 32; ++i) o[i] = (fa == 0.f ? 0.f : o[i] * fa) + (fb == 0.f ? 0.f : p[i] * fb);
+                    } else {
+                        tc::tmem_wait_ld();
+#pragma unroll
+                        for (int i = 0; i < 32; ++i) o[i] = fa == 0.f ? 0.f : o[i] * fa;
+                    }
+                    if (poison && row_ok) {
+                        // infinities and NaN of the drafted V rows that this row sees
+                        const int k0 = max(0, s.t0 * kBN - tree0), k1 = min(s.n, s.t1 * kBN - tree0);
+                        for (int k = k0; k < k1; ++k) {
+                            if (!((mask_word(mrow, k >> 5, s.n) >> (k & 31)) & 1u)) continue;
+                            const int pos = tree0 + k;
+                            int pb = __ldg(a.block_tables + (size_t)s.b * a.max_blocks_per_seq +
+                                           (pos >> a.cache.log2_block_size));
+                            if (pb < 0 || pb >= a.cache.num_blocks) pb = 0;
+                            const size_t row = (((size_t)pb * 2 + 1) * a.cache.num_kv_heads + s.unit / a.head_groups) *
+                                                   a.cache.block_size + (pos & (a.cache.block_size - 1));
+                            const uint16_t *vp = static_cast<const uint16_t *>(a.cache.ptr) + row * D + cc * 32;
+#pragma unroll 1
+                            for (int i = 0; i < 4; ++i) {
+                                const uint4 raw = __ldg(reinterpret_cast<const uint4 *>(vp) + i);
+                                if (!(nonfinite_pair<BF16>(raw.x) || nonfinite_pair<BF16>(raw.y) ||
+                                      nonfinite_pair<BF16>(raw.z) || nonfinite_pair<BF16>(raw.w)))
+                                    continue;
+                                float f[8];
+                                if constexpr (BF16) unpack8(raw, f, BF16Tag());
+                                else unpack8(raw, f, F16Tag());
+#pragma unroll
+                                for (int c = 0; c < 4; ++c)
+                                    if (c == i)
+#pragma unroll
+                                        for (int q = 0; q < 8; ++q)
+                                            if (!isfinite(f[q])) o[8 * c + q] += f[q];
+                            }
+                        }
+                    }
+                    if (row_ok) {
+#pragma unroll
+                        for (int q = 0; q < 4; ++q) {
+                            const float y[8] = {o[8 * q], o[8 * q + 1], o[8 * q + 2], o[8 * q + 3],
+                                                o[8 * q + 4], o[8 * q + 5], o[8 * q + 6], o[8 * q + 7]};
+                            if (s.slot < 0) store_out_vec<8>(a.out, orow * D + cc * 32 + 8 * q, y, a.out_dtype);
+                            else store_out_vec<8>(a.part_o, prow * D + cc * 32 + 8 * q, y, 2);
+                        }
+                    }
+                }
+                if (row_ok) {
+                    if (s.slot >= 0) a.part_lse[prow] = lse2;
+                    else if (a.lse) a.lse[orow] = lse2 * kLn2;
+                }
+            }
+            tc::fence_before_sync();
+            __syncwarp();
+            if (lane == 0) {
+                // the flag of the segment after next: its last readers, two segments back, arrived on
+                // o_empty before the last segment's products; its next setters follow products that
+                // wait for the arrival below
+                if (warp == 4) s_poison[(seg_i + 2u) & 3u] = 0;
+                mbar_arrive(o_empty);
+                mbar_arrive(&seg_empty[seg_i % kSegs]);
+            }
+            item += 2 * T;
+        }
+    }
+    tc::fence_before_sync();
+    __syncthreads();
+    pdl_launch_dependents();
+    if (warp == 1) {
+        tc::fence_after_sync();
+        tc::tmem_dealloc(tmem, 512);
+    }
+}
+
+// The partials of the item that begins in run blockIdx.x and is split: run c0's partial 1, then partial 0
+// of the runs behind it. A warp per row: weights 2^(lse_i - max), out = sum w o / sum w.
+template <int D>
+__global__ void __launch_bounds__(256) tree_merge_kernel(TreeArgs a) {
+    constexpr int V = D / 32;
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    pdl_wait();
+    const MergeItem it = a.merge[blockIdx.x];
+    const int rows = it.nodes * a.unit_heads;
+    for (int r = blockIdx.y * 8 + warp; r < rows; r += gridDim.y * 8) {
+        // rows of a wide block: lane B's start at row 128 of the partial
+        const int node = r / a.unit_heads, head = r - node * a.unit_heads;
+        const int pr = node < a.tile_nodes ? r : kBM + r - a.tile_nodes * a.unit_heads;
+        auto prow = [&](int i) { return ((size_t)(blockIdx.x + i) * 2 + (i == 0 ? 1 : 0)) * a.part_rows + pr; };
+        float M = -INFINITY;
+        bool nan = false;
+        for (int i = lane; i < it.parts; i += 32) {
+            const float x = __ldcg(a.part_lse + prow(i));
+            nan |= x != x;
+            M = fmaxf(M, x);
+        }
+#pragma unroll
+        for (int o = 16; o > 0; o >>= 1) M = fmaxf(M, __shfl_xor_sync(0xffffffffu, M, o));
+        if (__any_sync(0xffffffffu, nan)) M = NAN;
+        float acc[V], sum = 0.f;
+#pragma unroll
+        for (int v = 0; v < V; ++v) acc[v] = 0.f;
+        for (int i = 0; i < it.parts; ++i) {
+            const float x = __ldcg(a.part_lse + prow(i));
+            if (x == -INFINITY) continue;  // saw nothing
+            const float w = ex2f(x - M);
+            sum += w;
+            const float *p = a.part_o + prow(i) * D + V * lane;
+#pragma unroll
+            for (int v = 0; v < V; ++v) acc[v] = fmaf(w, __ldcg(p + v), acc[v]);
+        }
+        const float inv = sum == 0.f ? 0.f : 1.f / sum;
+#pragma unroll
+        for (int v = 0; v < V; ++v) acc[v] *= inv;
+        const size_t orow = (size_t)(it.q0 + it.node0 + node) * a.num_q_heads + (size_t)it.unit * a.unit_heads + head;
+        store_out_vec<V>(a.out, orow * D + V * lane, acc, a.out_dtype);
+        if (lane == 0 && a.lse) a.lse[orow] = sum == 0.f ? -INFINITY : (M + __log2f(sum)) * kLn2;
+    }
+    pdl_launch_dependents();
+}
+
+template <int D, bool BF16>
+cudaError_t launch_tree_t(const TreeArgs &a, int grid, cudaStream_t s) {
+    using L = TreeLayout<D>;
+    CUtensorMap tm_q, tm_kv;
+    cudaError_t e = encode_q_group_map(a.q, BF16 ? 1 : 0, a.total_q, a.num_q_heads, D, a.unit_heads, a.tile_nodes, &tm_q);
+    if (e != cudaSuccess) return e;
+    e = encode_cache_map(a.cache, a.cache.block_size < L::kBN ? a.cache.block_size : L::kBN, &tm_kv);
+    if (e != cudaSuccess) return e;
+    const DeviceInfo &info = device_info();
+    if ((int)L::kSmem > info.max_smem) return cudaErrorNotSupported;
+    auto kern = tree_kernel<D, BF16>;
+    static DeviceFlags configured;
+    if (!configured.test(info.device)) {
+        e = set_smem_attributes(kern, info.max_smem);
+        if (e != cudaSuccess) return e;
+        configured.set(info.device);
+    }
+    e = launch_pdl(kern, dim3(grid), dim3(L::kThreads), L::kSmem, s, tm_q, tm_kv, a);
+    if (e != cudaSuccess) return e;
+    return launch_pdl(tree_merge_kernel<D>, dim3(grid, 8), dim3(256), 0, s, a);
+}
+
+}  // namespace
+
+cudaError_t launch_tree(const TreeArgs &a, int grid, cudaStream_t s) {
+    const bool bf16 = a.cache.dtype == 1;
+    switch (a.cache.head_dim) {
+        case 256: return bf16 ? launch_tree_t<256, true>(a, grid, s) : launch_tree_t<256, false>(a, grid, s);
+        case 128: return bf16 ? launch_tree_t<128, true>(a, grid, s) : launch_tree_t<128, false>(a, grid, s);
+        case 64: return bf16 ? launch_tree_t<64, true>(a, grid, s) : launch_tree_t<64, false>(a, grid, s);
+        default: return cudaErrorNotSupported;
+    }
+}
+
+}  // namespace pkv

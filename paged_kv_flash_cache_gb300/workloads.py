@@ -125,6 +125,38 @@ def cu_lens(lens: Sequence[int]) -> torch.Tensor:
     return out
 
 
+def tree_mask(parents: Sequence[Sequence[int]], max_q_len: Optional[int] = None) -> torch.Tensor:
+    """Mask rows for `paged_attn_tree`, packed by sequence (int32 [sum n_b, words]): node i sees itself and
+    its ancestors. parents[b][i] is the index of node i's parent in sequence b, below i, or -1 for a node
+    whose parent is the context."""
+    most = max([max_q_len or 0] + [len(p) for p in parents])
+    words = max(1, (most + 31) // 32)
+    rows = []
+    for b, seq in enumerate(parents):
+        seen: List[int] = []
+        for i, p in enumerate(seq):
+            p = int(p)
+            if not -1 <= p < i:
+                raise ValueError("sequence %d: the parent of node %d must be -1 or an earlier node" % (b, i))
+            seen.append((1 << i) | (seen[p] if p >= 0 else 0))
+        for m in seen:
+            w = [(m >> (32 * k)) & 0xFFFFFFFF for k in range(words)]
+            rows.append([x - (1 << 32) if x >= 1 << 31 else x for x in w])
+    return torch.tensor(rows, dtype=torch.int32).reshape(len(rows), words)
+
+
+def tree_depths(parents: Sequence[Sequence[int]]) -> torch.Tensor:
+    """Depth of every node, packed by sequence (int32): 0 for a node whose parent is the context. The rotary
+    position of a drafted token is its sequence's context length plus its depth."""
+    out: List[int] = []
+    for seq in parents:
+        d: List[int] = []
+        for p in seq:
+            d.append(0 if int(p) < 0 else d[int(p)] + 1)
+        out += d
+    return torch.tensor(out, dtype=torch.int32)
+
+
 def randn_t(gen: torch.Generator, shape, dtype: str) -> torch.Tensor:
     """N(0, 1) draws in fp32 on the generator's device, rounded to fp16 / bf16."""
     return torch.randn(shape, generator=gen, dtype=torch.float32, device=gen.device).to(TORCH_DTYPE[dtype])
