@@ -212,17 +212,11 @@ __global__ void __launch_bounds__(TreeLayout<D>::kThreads, 1)
     long long run = (total + gridDim.x - 1) / gridDim.x;
     if (run < kMinTiles) run = kMinTiles;
 
-    // segment i of the run: wait for it and copy it out
+    // segment seg_i of the run; it stays in shared memory until every role has arrived on seg_empty
     uint32_t seg_i = 0;
-    auto next_segment = [&](Segment &s) -> bool {
-        if (!mbar_wait(&seg_full[seg_i % kSegs], (seg_i / kSegs) & 1u, abort_flag, a.err)) return false;
-        s = segs[seg_i % kSegs];
-        return s.nodes > 0;
-    };
-    // the nodes of lane A's tile, whether the block is wide, and the rows of lane x
-    auto lane_nodes = [&](const Segment &s, int x) -> int {
-        if (s.nodes <= a.tile_nodes) return s.nodes;  // narrow
-        return x == 0 ? a.tile_nodes : s.nodes - a.tile_nodes;
+    auto next_segment = [&]() -> bool {
+        return mbar_wait(&seg_full[seg_i % kSegs], (seg_i / kSegs) & 1u, abort_flag, a.err) &&
+               segs[seg_i % kSegs].nodes > 0;
     };
 
     if (warp < 4) {
@@ -238,44 +232,12 @@ __global__ void __launch_bounds__(TreeLayout<D>::kThreads, 1)
             }
             uint32_t item = 0, qn = 0;
             bool ok = true;
-            Segment s;
-            for (; (ok = next_segment(s)); ++seg_i) {
+            for (; (ok = next_segment()); ++seg_i) {
+                const Segment s = segs[seg_i % kSegs];
                 const bool wide = s.nodes > a.tile_nodes;
-                const int T = s.t1 - s.t0, ahead = kLanes == 1 || wide ? 1 : 2;
+                const int T = s.t1 - s.t0, ahead = kLanes == 1 || wide ? 1 : min(2, T);
                 const int kvh = s.unit / a.head_groups;
                 const int *bt = a.block_tables + (size_t)s.b * a.max_blocks_per_seq;
-                // tile j's K (kv 0) or V (kv 1), a lane per page; ids of tile j in each lane
-                auto pages = [&](int j) -> int {
-                    const int start = (s.t0 + j) * kBN, n = min(kBN, s.len - start);
-                    const int npages = bs < kBN ? (n + bs - 1) >> lbs : 1;
-                    int pb = 0;
-                    if (lane < npages) {
-                        pb = __ldg(bt + (start >> lbs) + lane);
-                        if (pb < 0 || pb >= a.cache.num_blocks) {
-                            set_error(a.err, kErrDeviceRange);
-                            pb = 0;
-                        }
-                    }
-                    return pb;
-                };
-                auto issue = [&](int j, int kv, int pb) -> bool {
-                    const int start = (s.t0 + j) * kBN, n = min(kBN, s.len - start);
-                    const int npages = bs < kBN ? (n + bs - 1) >> lbs : 1;
-                    const int off = bs < kBN ? 0 : (start & (bs - 1));
-                    const uint32_t slot = item % kRing;
-                    if (!mbar_wait(&kv_empty[slot], ((item / kRing) & 1u) ^ 1u, abort_flag, a.err)) return false;
-                    if (lane == 0) mbar_arrive_expect_tx(&kv_full[slot], (uint32_t)npages * box_rows * 128u * L::kHalves);
-                    __syncwarp();
-                    if (lane < npages) {
-                        const int row = ((pb * 2 + kv) * a.cache.num_kv_heads + kvh) * bs + off;
-                        uint8_t *dst = sRing + slot * L::kTileBytes + (uint32_t)lane * box_rows * 128u;
-#pragma unroll
-                        for (int hf = 0; hf < L::kHalves; ++hf)
-                            tc::tma_load_2d_hint(dst + hf * L::kTileHalf, &tm_kv, hf * 64, row, &kv_full[slot], pol);
-                    }
-                    ++item;
-                    return true;
-                };
                 // Q: the block's nodes, gu heads each, one box per tile and 64 columns
                 if (!(ok = mbar_wait(q_empty, (qn & 1u) ^ 1u, abort_flag, a.err))) break;
                 if (lane == 0) {
@@ -288,20 +250,55 @@ __global__ void __launch_bounds__(TreeLayout<D>::kThreads, 1)
                                             s.q0 + s.node0 + x * a.tile_nodes, q_full);
                 }
                 ++qn;
-                // ring order = the order of use: K of the first tiles, then V_j, K_{j + ahead}
-                int pb[3];
-                pb[0] = pages(0);
-                ok = issue(0, 0, pb[0]);
-                if (ok && ahead == 2 && T > 1) {
-                    pb[1] = pages(1);
-                    ok = issue(1, 0, pb[1]);
-                }
-                for (int j = 0; ok && j < T; ++j) {
-                    if (j + ahead < T) pb[ahead] = pages(j + ahead);
-                    ok = issue(j, 1, pb[0]);
-                    if (ok && j + ahead < T) ok = issue(j + ahead, 0, pb[ahead]);
-                    pb[0] = pb[1];
-                    pb[1] = pb[2];
+                // ring order = the order of use: K of the first `ahead` tiles, then V_j, K_{j + ahead}, and the
+                // last V: item n is tile j's K (kv 0) or V (kv 1)
+                auto tile_of = [&](int n, int &kv) -> int {
+                    if (n < ahead) {
+                        kv = 0;
+                        return n;
+                    }
+                    if (n >= 2 * T - ahead) {
+                        kv = 1;
+                        return n - T;
+                    }
+                    kv = (n - ahead) & 1 ? 0 : 1;
+                    return ((n - ahead) >> 1) + (kv ? 0 : ahead);
+                };
+                // pages of tile j: tile rows of the page, lane by lane
+                auto page_count = [&](int j) -> int {
+                    const int n = min(kBN, s.len - (s.t0 + j) * kBN);
+                    return bs < kBN ? (n + bs - 1) >> lbs : 1;
+                };
+                auto page_id = [&](int j) -> int {
+                    return lane < page_count(j) ? __ldg(bt + (((s.t0 + j) * kBN) >> lbs) + lane) : 0;
+                };
+                int kv = 0;
+                int pb_next = page_id(0);
+                for (int n = 0; n < 2 * T; ++n) {
+                    const int j = tile_of(n, kv);
+                    int pb = pb_next;  // loaded while the last item went out
+                    if (n + 1 < 2 * T) {
+                        int kv1;
+                        pb_next = page_id(tile_of(n + 1, kv1));
+                    }
+                    const int start = (s.t0 + j) * kBN, npages = page_count(j);
+                    const int off = bs < kBN ? 0 : (start & (bs - 1));
+                    const uint32_t slot = item % kRing;
+                    if (!(ok = mbar_wait(&kv_empty[slot], ((item / kRing) & 1u) ^ 1u, abort_flag, a.err))) break;
+                    if (lane == 0) mbar_arrive_expect_tx(&kv_full[slot], (uint32_t)npages * box_rows * 128u * L::kHalves);
+                    __syncwarp();
+                    if (lane < npages) {
+                        if (pb < 0 || pb >= a.cache.num_blocks) {
+                            set_error(a.err, kErrDeviceRange);
+                            pb = 0;
+                        }
+                        const int row = ((pb * 2 + kv) * a.cache.num_kv_heads + kvh) * bs + off;
+                        uint8_t *dst = sRing + slot * L::kTileBytes + (uint32_t)lane * box_rows * 128u;
+#pragma unroll
+                        for (int hf = 0; hf < L::kHalves; ++hf)
+                            tc::tma_load_2d_hint(dst + hf * L::kTileHalf, &tm_kv, hf * 64, row, &kv_full[slot], pol);
+                    }
+                    ++item;
                 }
                 __syncwarp();
                 if (lane == 0) mbar_arrive(&seg_empty[seg_i % kSegs]);
@@ -321,68 +318,58 @@ __global__ void __launch_bounds__(TreeLayout<D>::kThreads, 1)
                 uint32_t item = 0;       // ring items taken before this segment
                 uint32_t np[2] = {0, 0};  // P tiles taken, by lane
                 bool ok = true;
-                Segment s;
-                for (; (ok = next_segment(s)); ++seg_i) {
+                for (; (ok = next_segment()); ++seg_i) {
+                    const Segment &s = segs[seg_i % kSegs];
                     const bool wide = s.nodes > a.tile_nodes;
-                    const int T = s.t1 - s.t0, ahead = kLanes == 1 || wide ? 1 : 2;
-                    // ring items of tile j (see the producer's order)
-                    auto k_item = [&](int j) { return item + (j < ahead ? j : 2 * j - ahead + 1); };
-                    auto v_item = [&](int j) { return item + j + min(T, ahead + j); };
-                    auto full = [&](uint32_t i) {
-                        return mbar_wait(&kv_full[i % kRing], (i / kRing) & 1u, abort_flag, a.err);
-                    };
-                    auto qk = [&](int x, int j, bool last_use) -> bool {
-                        const uint32_t i = k_item(j);
-                        if (!full(i)) return false;
-                        tc::fence_after_sync();
-                        const uint32_t aK = aRing + (i % kRing) * L::kTileBytes;
-                        const uint32_t aQx = aQ + (wide ? x : 0) * L::kQBytes;
-#pragma unroll
-                        for (int kk = 0; kk < D / 16; ++kk)
-                            tc::mma_f16_ss(tmem + kBN * x,
-                                           tc::smem_desc(aQx + (kk >> 2) * L::kQHalf + (kk & 3) * 32u, 16, 1024),
-                                           tc::smem_desc(aK + (kk >> 2) * L::kTileHalf + (kk & 3) * 32u, 16, 1024), id_qk,
-                                           kk > 0 ? 1u : 0u);
-                        tc::mma_commit(&s_full[x]);
-                        if (last_use) tc::mma_commit(&kv_empty[i % kRing]);
-                        return true;
-                    };
-                    auto pv = [&](int x, int j, bool first, bool last_use) -> bool {
-                        if (!mbar_wait(&p_full[x], np[x] & 1u, abort_flag, a.err)) return false;
-                        ++np[x];
-                        const uint32_t i = v_item(j);
-                        if (!full(i)) return false;
-                        // the segment's first P V overwrites an output: the last segment's must be read
-                        if (first && !mbar_wait(o_empty, (seg_i & 1u) ^ 1u, abort_flag, a.err)) return false;
-                        tc::fence_after_sync();
-                        const uint32_t aV = aRing + (i % kRing) * L::kTileBytes;
-                        const uint32_t tO = tmem + L::kColO + 128u * x, tP = tmem + kBN * x;
-#pragma unroll
-                        for (int part = 0; part < 2; ++part)
+                    const int T = s.t1 - s.t0, ahead = kLanes == 1 || wide ? 1 : min(2, T);
+                    if (!(ok = mbar_wait(q_full, seg_i & 1u, abort_flag, a.err))) break;
+                    // Steps: lane x = t % kLanes takes tile j: P V of tile j, then Q K of the lane's next
+                    // tile. (t < 0: the first Q K of each lane.) Wide lanes share tile t / 2 and B, the second,
+                    // frees its ring slots; narrow lanes take turns on tiles t.
+                    const bool shared_tile = kLanes == 2 && wide;
+                    const int steps = shared_tile ? 2 * T : T, stride = shared_tile || kLanes == 1 ? 1 : 2;
+                    for (int t = -kLanes; ok && t < steps; ++t) {
+                        const int x = kLanes == 2 ? t & 1 : 0;
+                        const int j = shared_tile ? t >> 1 : t;
+                        const bool frees = !shared_tile || x == 1;
+                        if (t >= 0) {
+                            if (!(ok = mbar_wait(&p_full[x], np[x] & 1u, abort_flag, a.err))) break;
+                            ++np[x];
+                            const uint32_t i = item + j + min(T, ahead + j);  // V_j in the ring
+                            if (!(ok = mbar_wait(&kv_full[i % kRing], (i / kRing) & 1u, abort_flag, a.err))) break;
+                            // a segment's first P V overwrites an output: the last segment's must be read
+                            const bool first = j < stride;
+                            if (first && !(ok = mbar_wait(o_empty, (seg_i & 1u) ^ 1u, abort_flag, a.err))) break;
+                            tc::fence_after_sync();
+                            const uint64_t dV = tc::smem_desc(aRing + (i % kRing) * L::kTileBytes, L::kTileHalf, 1024);
+                            const uint32_t tO = tmem + L::kColO + 128u * x, tP = tmem + kBN * x;
+                            // 16 keys a step: 8 columns of P in their 32-column chunk, the remainders 16 behind
 #pragma unroll
                             for (int kk = 0; kk < kBN / 16; ++kk)
-                                tc::mma_f16_ts(tO, tP + (uint32_t)(kBN / 2) * part + 8u * kk,
-                                               tc::smem_desc(aV + (uint32_t)kk * 2048u, L::kTileHalf, 1024), id_pv,
-                                               (first && part == 0 && kk == 0) ? 0u : 1u);
-                        if (last_use) tc::mma_commit(&kv_empty[i % kRing]);
-                        return true;
-                    };
-                    if (!(ok = mbar_wait(q_full, seg_i & 1u, abort_flag, a.err))) break;
-                    tc::fence_after_sync();
-                    if (kLanes == 1 || wide) {
-                        ok = qk(0, 0, kLanes == 1) && (kLanes == 1 || qk(1, 0, true));
-                        for (int j = 0; ok && j < T; ++j) {
-                            const bool more = j + 1 < T;
-                            if (!more) tc::mma_commit(q_empty);  // every QK of the segment is issued
-                            ok = pv(0, j, j == 0, kLanes == 1) && (!more || qk(0, j + 1, kLanes == 1));
-                            if (kLanes == 2) ok = ok && pv(1, j, j == 0, true) && (!more || qk(1, j + 1, true));
+#pragma unroll
+                                for (int part = 0; part < 2; ++part)
+                                    tc::mma_f16_ts(tO, tP + 32u * (kk >> 1) + 8u * (kk & 1) + 16u * part,
+                                                   dV + (uint32_t)(kk * 2048 >> 4), id_pv,
+                                                   (first && part == 0 && kk == 0) ? 0u : 1u);
+                            if (frees) tc::mma_commit(&kv_empty[i % kRing]);
                         }
-                    } else {
-                        ok = qk(0, 0, true) && (T < 2 || qk(1, 1, true));
-                        for (int j = 0; ok && j < T; ++j) {
-                            const bool more = j + 2 < T;
-                            if (j + 2 == T || T == 1) tc::mma_commit(q_empty);
-                            ok = pv(j & 1, j, j < 2, true) && (!more || qk(j & 1, j + 2, true));
+                        const int jn = j + stride;
+                        if (jn >= 0 && jn < T) {
+                            const uint32_t i = item + (jn < ahead ? jn : 2 * jn - ahead + 1);  // K_jn in the ring
+                            if (!(ok = mbar_wait(&kv_full[i % kRing], (i / kRing) & 1u, abort_flag, a.err))) break;
+                            tc::fence_after_sync();
+                            // (a descriptor's address field counts 16 bytes and has room for all of shared
+                            // memory: the steps along it are additions)
+                            const uint64_t dK = tc::smem_desc(aRing + (i % kRing) * L::kTileBytes, 16, 1024);
+                            const uint64_t dQ = tc::smem_desc(aQ + (wide ? x : 0) * L::kQBytes, 16, 1024);
+#pragma unroll
+                            for (int kk = 0; kk < D / 16; ++kk)
+                                tc::mma_f16_ss(tmem + kBN * x, dQ + (((kk >> 2) * L::kQHalf + (kk & 3) * 32u) >> 4),
+                                               dK + (((kk >> 2) * L::kTileHalf + (kk & 3) * 32u) >> 4), id_qk,
+                                               kk > 0 ? 1u : 0u);
+                            tc::mma_commit(&s_full[x]);
+                            if (frees) tc::mma_commit(&kv_empty[i % kRing]);
+                            if (jn == T - 1 && frees) tc::mma_commit(q_empty);  // the segment's last Q K
                         }
                     }
                     if (!ok) break;
@@ -466,33 +453,36 @@ __global__ void __launch_bounds__(TreeLayout<D>::kThreads, 1)
         const int r = w4 * 32 + lane;  // row of the tile = TMEM lane
         const uint32_t lane_base = (uint32_t)(w4 * 32) << 16;
         const float c2 = a.scale * kLog2e;
-        const int node_r = r / gu, head_r = r - node_r * gu;
         const uint32_t tS = tmem + kBN * x + lane_base;
         const uint32_t tO = tmem + L::kColO + 128u * x + lane_base;
         uint32_t ns = 0;    // score tiles of this lane so far
         uint32_t item = 0;  // ring items before this segment
         uint32_t nml = 0;   // narrow segments so far
-        Segment s;
-        for (; next_segment(s); ++seg_i) {
+        for (; next_segment(); ++seg_i) {
+            const Segment &s = segs[seg_i % kSegs];
             const bool wide = s.nodes > a.tile_nodes;
             const bool split = kLanes == 2 && !wide;  // the lanes share the rows
-            const int T = s.t1 - s.t0, ahead = kLanes == 1 || wide ? 1 : 2;
-            const int rows = lane_nodes(s, x) * gu;
+            const int T = s.t1 - s.t0, ahead = kLanes == 1 || wide ? 1 : min(2, T);
+            // wide: lane A's tile is full, lane B has the rest
+            const int rows = (!wide ? s.nodes : x == 0 ? a.tile_nodes : s.nodes - a.tile_nodes) * gu;
             const bool row_ok = r < rows, warp_ok = w4 * 32 < rows;  // warp_ok: uniform
-            const int tree0 = s.len - s.n;  // position of node 0
-            const int node = s.node0 + (wide ? x * a.tile_nodes : 0) + node_r;
-            const uint32_t *mrow = a.tree_mask + (size_t)(s.q0 + node) * a.mask_words;
+            // (recomputed from the segment where they are needed: the key loop's registers hold a row of scores)
+            auto row_node = [&]() -> int { return s.node0 + (s.nodes > a.tile_nodes ? x * a.tile_nodes : 0) + r / gu; };
+            auto mask_row = [&]() -> const uint32_t * {
+                return a.tree_mask + (size_t)(s.q0 + row_node()) * a.mask_words;
+            };
             float m = -INFINITY, l = 0.f;
             bool ok = true;
             for (int j = split ? x : 0; j < T; j += split ? 2 : 1, ++ns) {
                 const int start = (s.t0 + j) * kBN;
-                const int j0 = start - tree0;          // tree index of the tile's first key (negative: context)
+                const int j0 = start - (s.len - s.n);  // tree index of the tile's first key (negative: context)
                 const bool tail = j0 + kBN > 0;        // drafted tokens (or the end) in this tile
                 uint32_t vis[kBN / 32];
                 if (tail) {
 #pragma unroll
                     for (int i = 0; i < kBN / 32; ++i) vis[i] = 0u;
                     if (row_ok) {
+                        const uint32_t *mrow = mask_row();
                         const int w0 = j0 >> 5;
                         uint32_t lo = mask_word(mrow, w0, s.n);
 #pragma unroll
@@ -549,6 +539,7 @@ __global__ void __launch_bounds__(TreeLayout<D>::kThreads, 1)
                                     make_float2(0.f, 0.f)};
 #pragma unroll
                     for (int cc = 0; cc < kBN / 32; ++cc) {
+                        // P over the chunk's own scores: 16 columns of roundings, 16 of remainders
                         uint32_t ph[16], pl[16];
 #pragma unroll
                         for (int q = 0; q < 16; ++q) {
@@ -557,8 +548,8 @@ __global__ void __launch_bounds__(TreeLayout<D>::kThreads, 1)
                             l4[q & 3] = fadd2(l4[q & 3], e);
                             split_pair<BF16>(e.x, e.y, ph[q], pl[q]);
                         }
-                        tc::tmem_st16(tS + cc * 16, ph);
-                        tc::tmem_st16(tS + kBN / 2 + cc * 16, pl);
+                        tc::tmem_st16(tS + cc * 32, ph);
+                        tc::tmem_st16(tS + cc * 32 + 16, pl);
                     }
                     const float2 ls = fadd2(fadd2(l4[0], l4[1]), fadd2(l4[2], l4[3]));
                     l += ls.x + ls.y;
@@ -567,7 +558,7 @@ __global__ void __launch_bounds__(TreeLayout<D>::kThreads, 1)
                 if (tail && (split || x == 0)) {
                     const uint32_t vi = item + j + min(T, ahead + j);
                     if (!(ok = mbar_wait(&kv_full[vi % kRing], (vi / kRing) & 1u, abort_flag, a.err))) break;
-                    uint8_t *sV = sRing + (vi % kRing) * L::kTileBytes;
+                    uint8_t *const sV = sRing + (vi % kRing) * L::kTileBytes;
                     const int n_valid = min(kBN, s.len - start);
                     bool bad = false;
                     // 8 lanes a row (128 bytes of a 64-column half), 4 rows a warp and step
@@ -625,7 +616,9 @@ __global__ void __launch_bounds__(TreeLayout<D>::kThreads, 1)
             tc::fence_after_sync();
             if (mine && warp_ok) {
                 const bool poison = s_poison[seg_i & 3u] != 0;
-                const size_t orow = (size_t)(s.q0 + node) * a.num_q_heads + (size_t)s.unit * gu + head_r;
+                const int node = row_node(), tree0 = s.len - s.n;  // position of node 0
+                const uint32_t *mrow = mask_row();
+                const size_t orow = (size_t)(s.q0 + node) * a.num_q_heads + (size_t)s.unit * gu + r % gu;
                 const size_t prow = ((size_t)blockIdx.x * 2 + (s.slot > 0)) * a.part_rows + (wide ? x * kBM : 0) + r;
                 const uint32_t tOa = tmem + L::kColO + lane_base + (wide ? 128u * x : 0u);
 #pragma unroll
