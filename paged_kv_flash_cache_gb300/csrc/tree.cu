@@ -46,7 +46,8 @@ namespace {
 constexpr int kBM = 128;              // rows of a tile
 constexpr float kRescaleLog2 = 8.0f;  // O is rescaled when the running max grows by more than 2^8
 constexpr int kSegs = 4;              // segments handed out ahead
-constexpr int kMinTiles = 2;          // key tiles of a run at least: both lanes have one
+constexpr int kItemCost = 2;          // an item's set-up and output, in key tiles
+constexpr int kMinTiles = 2;          // work of a run at least, in key tiles
 
 // One run's part of an item: key tiles [t0, t1) of nodes [node0, node0 + nodes) of one sequence and KV
 // head (or share of its group). nodes = 0 ends the run.
@@ -67,9 +68,10 @@ struct TreeLayout {
     static constexpr uint32_t kQBytes = kHalves * kQHalf;
     static constexpr uint32_t kTileHalf = kBN * 128;
     static constexpr uint32_t kTileBytes = kHalves * kTileHalf;  // a K or a V tile
-    static constexpr int kRing = D == 64 ? 8 : 5;
+    static constexpr int kRing = D == 64 ? 8 : 4;
     static constexpr uint32_t kRingOff = kLanes * kQBytes;
-    static constexpr uint32_t kMlOff = kRingOff + kRing * kTileBytes;  // [128] (max, sum) between the lanes
+    static constexpr uint32_t kStageOff = kRingOff + kRing * kTileBytes;  // output rows, 4 KB a softmax warp
+    static constexpr uint32_t kMlOff = kStageOff + 4 * kLanes * 4096u;    // [128] (max, sum) between the lanes
     static constexpr uint32_t kBarOff = kMlOff + kBM * 8;
     static constexpr uint32_t kSegOff = kBarOff + 512;
     static constexpr uint32_t kSmem = kSegOff + kSegs * sizeof(Segment) + 1024;  // + alignment slack
@@ -81,8 +83,14 @@ struct TreeLayout {
 // What a run works on, from the lengths on the device; false (flagged) if they are out of range.
 struct SeqWork {
     int q0, n, len;
-    long long tiles, blocks;  // key tiles, row blocks
+    int tiles, blocks;  // key tiles, row blocks
 };
+
+// Work of one unit (KV head) of a sequence, in key tiles: an item costs its tiles and kItemCost for its set-up,
+// refill of the pipeline and output.
+__device__ __forceinline__ long long seq_cost(const SeqWork &w) {
+    return w.blocks > 0 ? (long long)(w.tiles + kItemCost) * w.blocks : 0;
+}
 
 __device__ __forceinline__ SeqWork seq_work(const TreeArgs &a, int b, int bn, bool flag) {
     SeqWork w;
@@ -201,7 +209,7 @@ __global__ void __launch_bounds__(TreeLayout<D>::kThreads, 1)
         long long mine = 0;
         for (int b = threadIdx.x; b < a.batch; b += L::kThreads) {
             const SeqWork w = seq_work(a, b, kBN, blockIdx.x == 0);
-            mine += w.tiles * w.blocks;
+            mine += seq_cost(w);
         }
 #pragma unroll
         for (int o = 16; o > 0; o >>= 1) mine += __shfl_xor_sync(0xffffffffu, mine, o);
@@ -315,33 +323,44 @@ __global__ void __launch_bounds__(TreeLayout<D>::kThreads, 1)
                 const uint32_t id_qk = tc::idesc_f16(BF16, kBM, kBN, false);
                 const uint32_t id_pv = tc::idesc_f16(BF16, kBM, D, true);
                 const uint32_t aQ = smem_addr(sQ), aRing = smem_addr(sRing);
-                uint32_t item = 0;       // ring items taken before this segment
-                uint32_t np[2] = {0, 0};  // P tiles taken, by lane
+                uint32_t slot = 0, ph = 0;  // ring position: the next item to use
+                auto advance = [&](uint32_t &sl, uint32_t &p) {
+                    if (++sl == (uint32_t)kRing) {
+                        sl = 0;
+                        p ^= 1u;
+                    }
+                };
+                uint32_t np = 0;  // parities of the lanes' next P tiles
+                const uint64_t dK0 = tc::smem_desc(aRing, 16, 1024), dQ0 = tc::smem_desc(aQ, 16, 1024);
+                const uint64_t dV0 = tc::smem_desc(aRing, L::kTileHalf, 1024);
                 bool ok = true;
                 for (; (ok = next_segment()); ++seg_i) {
                     const Segment &s = segs[seg_i % kSegs];
-                    const bool wide = s.nodes > a.tile_nodes;
-                    const int T = s.t1 - s.t0, ahead = kLanes == 1 || wide ? 1 : min(2, T);
+                    const int T = s.t1 - s.t0;
+                    // Steps: lane x = t % kLanes takes tile j: P V of tile j, then Q K of the lane's next tile.
+                    // (t < 0: the first Q K of each lane.) Wide lanes share tile t / 2 and B, the second, frees its
+                    // ring slots; narrow lanes take turns on tiles t. The ring holds the tiles in this order (see
+                    // the producer): a step's V, then its K.
+                    const bool wide = kLanes == 2 && s.nodes > a.tile_nodes;
+                    const int steps = wide ? 2 * T : T, stride = wide || kLanes == 1 ? 1 : 2;
                     if (!(ok = mbar_wait(q_full, seg_i & 1u, abort_flag, a.err))) break;
-                    // Steps: lane x = t % kLanes takes tile j: P V of tile j, then Q K of the lane's next
-                    // tile. (t < 0: the first Q K of each lane.) Wide lanes share tile t / 2 and B, the second,
-                    // frees its ring slots; narrow lanes take turns on tiles t.
-                    const bool shared_tile = kLanes == 2 && wide;
-                    const int steps = shared_tile ? 2 * T : T, stride = shared_tile || kLanes == 1 ? 1 : 2;
+                    tc::fence_after_sync();
                     for (int t = -kLanes; ok && t < steps; ++t) {
                         const int x = kLanes == 2 ? t & 1 : 0;
-                        const int j = shared_tile ? t >> 1 : t;
-                        const bool frees = !shared_tile || x == 1;
+                        const int j = wide ? t >> 1 : t, jn = j + stride;
+                        const bool frees = !wide || x == 1;
+                        uint32_t sl = slot, sp = ph;  // the step's K
                         if (t >= 0) {
-                            if (!(ok = mbar_wait(&p_full[x], np[x] & 1u, abort_flag, a.err))) break;
-                            ++np[x];
-                            const uint32_t i = item + j + min(T, ahead + j);  // V_j in the ring
-                            if (!(ok = mbar_wait(&kv_full[i % kRing], (i / kRing) & 1u, abort_flag, a.err))) break;
+                            if (!(ok = mbar_wait(&p_full[x], (np >> x) & 1u, abort_flag, a.err))) break;
+                            np ^= 1u << x;
+                            if (!(ok = mbar_wait(&kv_full[slot], ph, abort_flag, a.err))) break;
                             // a segment's first P V overwrites an output: the last segment's must be read
                             const bool first = j < stride;
                             if (first && !(ok = mbar_wait(o_empty, (seg_i & 1u) ^ 1u, abort_flag, a.err))) break;
                             tc::fence_after_sync();
-                            const uint64_t dV = tc::smem_desc(aRing + (i % kRing) * L::kTileBytes, L::kTileHalf, 1024);
+                            // (a descriptor's address field counts 16 bytes and has room for all of shared memory:
+                            // the steps along it are additions)
+                            const uint64_t dV = dV0 + slot * (L::kTileBytes >> 4);
                             const uint32_t tO = tmem + L::kColO + 128u * x, tP = tmem + kBN * x;
                             // 16 keys a step: 8 columns of P in their 32-column chunk, the remainders 16 behind
 #pragma unroll
@@ -351,30 +370,31 @@ __global__ void __launch_bounds__(TreeLayout<D>::kThreads, 1)
                                     tc::mma_f16_ts(tO, tP + 32u * (kk >> 1) + 8u * (kk & 1) + 16u * part,
                                                    dV + (uint32_t)(kk * 2048 >> 4), id_pv,
                                                    (first && part == 0 && kk == 0) ? 0u : 1u);
-                            if (frees) tc::mma_commit(&kv_empty[i % kRing]);
+                            if (frees) tc::mma_commit(&kv_empty[slot]);
+                            advance(sl, sp);
                         }
-                        const int jn = j + stride;
-                        if (jn >= 0 && jn < T) {
-                            const uint32_t i = item + (jn < ahead ? jn : 2 * jn - ahead + 1);  // K_jn in the ring
-                            if (!(ok = mbar_wait(&kv_full[i % kRing], (i / kRing) & 1u, abort_flag, a.err))) break;
+                        if (jn < T) {
+                            if (!(ok = mbar_wait(&kv_full[sl], sp, abort_flag, a.err))) break;
                             tc::fence_after_sync();
-                            // (a descriptor's address field counts 16 bytes and has room for all of shared
-                            // memory: the steps along it are additions)
-                            const uint64_t dK = tc::smem_desc(aRing + (i % kRing) * L::kTileBytes, 16, 1024);
-                            const uint64_t dQ = tc::smem_desc(aQ + (wide ? x : 0) * L::kQBytes, 16, 1024);
+                            const uint64_t dK = dK0 + sl * (L::kTileBytes >> 4);
+                            const uint64_t dQ = dQ0 + (wide ? x : 0) * (L::kQBytes >> 4);
 #pragma unroll
                             for (int kk = 0; kk < D / 16; ++kk)
                                 tc::mma_f16_ss(tmem + kBN * x, dQ + (((kk >> 2) * L::kQHalf + (kk & 3) * 32u) >> 4),
                                                dK + (((kk >> 2) * L::kTileHalf + (kk & 3) * 32u) >> 4), id_qk,
                                                kk > 0 ? 1u : 0u);
                             tc::mma_commit(&s_full[x]);
-                            if (frees) tc::mma_commit(&kv_empty[i % kRing]);
+                            if (frees) tc::mma_commit(&kv_empty[sl]);
                             if (jn == T - 1 && frees) tc::mma_commit(q_empty);  // the segment's last Q K
+                            advance(sl, sp);
+                        }
+                        if (frees) {
+                            slot = sl;
+                            ph = sp;
                         }
                     }
                     if (!ok) break;
                     tc::mma_commit(o_done);
-                    item += 2 * T;
                     mbar_arrive(&seg_empty[seg_i % kSegs]);
                 }
                 tc::mma_commit(drain);
@@ -397,11 +417,11 @@ __global__ void __launch_bounds__(TreeLayout<D>::kThreads, 1)
                 ++n;
                 return true;
             };
-            long long before = 0;  // key tiles of the sequences passed
+            long long before = 0;  // work of the sequences passed
             for (int b0 = 0; ok && b0 < a.batch && before < end; b0 += 32) {
                 SeqWork w = {0, 0, 0, 0, 0};
                 if (b0 + lane < a.batch) w = seq_work(a, b0 + lane, kBN, false);
-                const long long mine = w.tiles * w.blocks * a.units;
+                const long long mine = seq_cost(w) * a.units;
                 long long scan = mine;
 #pragma unroll
                 for (int o = 1; o < 32; o <<= 1) {
@@ -420,26 +440,35 @@ __global__ void __launch_bounds__(TreeLayout<D>::kThreads, 1)
                     s.n = __shfl_sync(0xffffffffu, w.n, src);
                     s.len = __shfl_sync(0xffffffffu, w.len, src);
                     const long long s0 = __shfl_sync(0xffffffffu, first, src), s1 = __shfl_sync(0xffffffffu, last, src);
-                    const int tiles = (int)__shfl_sync(0xffffffffu, w.tiles, src);
-                    const int blocks = (int)__shfl_sync(0xffffffffu, w.blocks, src);
-                    for (long long at = max(begin, s0); ok && at < min(end, s1); at += s.t1 - s.t0) {
-                        // the row blocks of a KV head follow one another: the second finds the keys in L2
-                        const long long it = (at - s0) / tiles;
-                        s.unit = (int)(it / blocks);
-                        s.node0 = (int)(it % blocks) * a.block_nodes;
-                        s.nodes = min(a.block_nodes, s.n - s.node0);
-                        s.t0 = (int)((at - s0) % tiles);
-                        s.t1 = (int)min((long long)tiles, s.t0 + (end - at));
-                        s.slot = s.t0 > 0 ? 0 : (s.t1 < tiles ? 1 : -1);
-                        if (s.slot == 1) {
-                            const long long item_end = s0 + it * tiles + tiles - 1;  // its last key tile
-                            left.q0 = s.q0;
-                            left.node0 = s.node0;
-                            left.nodes = s.nodes;
-                            left.unit = s.unit;
-                            left.parts = (int)(item_end / run - blockIdx.x) + 1;
+                    const int tiles = __shfl_sync(0xffffffffu, w.tiles, src);
+                    const int blocks = __shfl_sync(0xffffffffu, w.blocks, src);
+                    const int cost = tiles + kItemCost;
+                    // the sequence's items (a unit's row blocks one after the other: the second finds the keys in
+                    // L2) that this run meets, from the one that `begin` falls into
+                    const int it0 = begin > s0 ? (int)((begin - s0) / cost) : 0;
+                    s.unit = it0 / blocks;
+                    int blk = it0 - s.unit * blocks;
+                    for (long long at = s0 + (long long)it0 * cost; ok && at < min(end, s1); at += cost) {
+                        // an item's first kItemCost units of work stand for its set-up and output
+                        s.t0 = (int)max(0ll, begin - at - kItemCost);
+                        s.t1 = (int)min((long long)tiles, end - at - kItemCost);
+                        if (s.t1 > s.t0) {
+                            s.node0 = blk * a.block_nodes;
+                            s.nodes = min(a.block_nodes, s.n - s.node0);
+                            s.slot = s.t0 > 0 ? 0 : (s.t1 < tiles ? 1 : -1);
+                            if (s.slot == 1) {
+                                left.q0 = s.q0;
+                                left.node0 = s.node0;
+                                left.nodes = s.nodes;
+                                left.unit = s.unit;
+                                left.parts = (int)((at + cost - 1) / run - blockIdx.x) + 1;  // to its last tile's run
+                            }
+                            ok = publish(s);
                         }
-                        ok = publish(s);
+                        if (++blk == blocks) {
+                            blk = 0;
+                            ++s.unit;
+                        }
                     }
                 }
             }
@@ -456,7 +485,7 @@ __global__ void __launch_bounds__(TreeLayout<D>::kThreads, 1)
         const uint32_t tS = tmem + kBN * x + lane_base;
         const uint32_t tO = tmem + L::kColO + 128u * x + lane_base;
         uint32_t ns = 0;    // score tiles of this lane so far
-        uint32_t item = 0;  // ring items before this segment
+        uint32_t item = 0;  // ring items before this segment (the V of its tile j: see the sweep)
         uint32_t nml = 0;   // narrow segments so far
         for (; next_segment(); ++seg_i) {
             const Segment &s = segs[seg_i % kSegs];
@@ -618,10 +647,36 @@ __global__ void __launch_bounds__(TreeLayout<D>::kThreads, 1)
                 const bool poison = s_poison[seg_i & 3u] != 0;
                 const int node = row_node(), tree0 = s.len - s.n;  // position of node 0
                 const uint32_t *mrow = mask_row();
-                const size_t orow = (size_t)(s.q0 + node) * a.num_q_heads + (size_t)s.unit * gu + r % gu;
+                const bool part = s.slot >= 0;
                 const size_t prow = ((size_t)blockIdx.x * 2 + (s.slot > 0)) * a.part_rows + (wide ? x * kBM : 0) + r;
+                const size_t orow = part ? prow : (size_t)(s.q0 + node) * a.num_q_heads + (size_t)s.unit * gu + r % gu;
+                if (row_ok) {
+                    if (part) a.part_lse[prow] = lse2;
+                    else if (a.lse) a.lse[orow] = lse2 * kLn2;
+                }
                 const uint32_t tOa = tmem + L::kColO + lane_base + (wide ? 128u * x : 0u);
+                // rows go out through shared memory, 128 bytes of each at a time: 8 lanes a row instead of
+                // 32 rows a store
+                const bool f32 = part || a.out_dtype == 2;
+                uint8_t *out = static_cast<uint8_t *>(part ? static_cast<void *>(a.part_o) : a.out);
+                const long long row_bytes = D * (f32 ? 4 : 2);
+                const long long dst_row = row_ok ? (long long)orow * row_bytes : -1;
+                uint8_t *stage = smem + L::kStageOff + (warp - 4) * 4096;
+                auto stage16 = [&](int c, const uint4 &v) {  // 16-byte piece c of this lane's row
+                    *reinterpret_cast<uint4 *>(stage + lane * 128 + ((c ^ (lane & 7)) << 4)) = v;
+                };
+                auto flush = [&](int col_bytes) {
+                    __syncwarp();
 #pragma unroll
+                    for (int i = 0; i < 8; ++i) {
+                        const int rr = i * 4 + (lane >> 3);
+                        const long long d = __shfl_sync(0xffffffffu, dst_row, rr);
+                        const uint4 v = *reinterpret_cast<const uint4 *>(stage + rr * 128 + (((lane & 7) ^ (rr & 7)) << 4));
+                        if (d >= 0) *reinterpret_cast<uint4 *>(out + d + col_bytes + (lane & 7) * 16) = v;
+                    }
+                    __syncwarp();
+                };
+#pragma unroll 1
                 for (int cc = 0; cc < D / 32; ++cc) {
                     float o[32];
                     tc::tmem_ld32(tOa + cc * 32, o);
@@ -667,19 +722,21 @@ __global__ void __launch_bounds__(TreeLayout<D>::kThreads, 1)
                             }
                         }
                     }
-                    if (row_ok) {
+                    if (f32) {
 #pragma unroll
-                        for (int q = 0; q < 4; ++q) {
-                            const float y[8] = {o[8 * q], o[8 * q + 1], o[8 * q + 2], o[8 * q + 3],
-                                                o[8 * q + 4], o[8 * q + 5], o[8 * q + 6], o[8 * q + 7]};
-                            if (s.slot < 0) store_out_vec<8>(a.out, orow * D + cc * 32 + 8 * q, y, a.out_dtype);
-                            else store_out_vec<8>(a.part_o, prow * D + cc * 32 + 8 * q, y, 2);
-                        }
+                        for (int q = 0; q < 8; ++q)
+                            stage16(q, make_uint4(__float_as_uint(o[4 * q]), __float_as_uint(o[4 * q + 1]),
+                                                  __float_as_uint(o[4 * q + 2]), __float_as_uint(o[4 * q + 3])));
+                        flush(cc * 128);
+                    } else {
+#pragma unroll
+                        for (int q = 0; q < 4; ++q)
+                            stage16((cc & 1) * 4 + q,
+                                    make_uint4(pack_pair<BF16>(o[8 * q], o[8 * q + 1]), pack_pair<BF16>(o[8 * q + 2], o[8 * q + 3]),
+                                               pack_pair<BF16>(o[8 * q + 4], o[8 * q + 5]),
+                                               pack_pair<BF16>(o[8 * q + 6], o[8 * q + 7])));
+                        if (cc & 1) flush((cc >> 1) * 128);
                     }
-                }
-                if (row_ok) {
-                    if (s.slot >= 0) a.part_lse[prow] = lse2;
-                    else if (a.lse) a.lse[orow] = lse2 * kLn2;
                 }
             }
             tc::fence_before_sync();
@@ -731,15 +788,42 @@ __global__ void __launch_bounds__(256) tree_merge_kernel(TreeArgs a) {
         float acc[V], sum = 0.f;
 #pragma unroll
         for (int v = 0; v < V; ++v) acc[v] = 0.f;
-        for (int i = 0; i < it.parts; ++i) {
-            const float x = __ldcg(a.part_lse + prow(i));
-            if (x == -INFINITY) continue;  // saw nothing
-            const float w = ex2f(x - M);
-            sum += w;
-            const float *p = a.part_o + prow(i) * D + V * lane;
+        // 32 partials at a time: lane i holds the weight of partial i; kFlight rows in flight
+        constexpr int kFlight = D == 256 ? 4 : 8;
+        for (int i0 = 0; i0 < it.parts; i0 += 32) {
+            const int n = min(32, it.parts - i0);
+            const float x = lane < n ? __ldcg(a.part_lse + prow(i0 + lane)) : -INFINITY;
+            const float w_l = x == -INFINITY ? 0.f : ex2f(x - M);
+            sum += w_l;
+            for (int k = 0; k < n; k += kFlight) {
+                float y[kFlight][V];
 #pragma unroll
-            for (int v = 0; v < V; ++v) acc[v] = fmaf(w, __ldcg(p + v), acc[v]);
+                for (int f = 0; f < kFlight; ++f)
+                    if (k + f < n) {
+                        const float *p = a.part_o + prow(i0 + k + f) * D + V * lane;
+                        if constexpr (V == 2) {
+                            const float2 q = __ldcg(reinterpret_cast<const float2 *>(p));
+                            y[f][0] = q.x, y[f][1] = q.y;
+                        } else {
+#pragma unroll
+                            for (int g = 0; g < V / 4; ++g) {
+                                const float4 q = __ldcg(reinterpret_cast<const float4 *>(p) + g);
+                                y[f][4 * g] = q.x, y[f][4 * g + 1] = q.y, y[f][4 * g + 2] = q.z, y[f][4 * g + 3] = q.w;
+                            }
+                        }
+                    }
+#pragma unroll
+                for (int f = 0; f < kFlight; ++f) {
+                    if (k + f >= n) break;
+                    const float w = __shfl_sync(0xffffffffu, w_l, k + f);
+                    if (w == 0.f) continue;  // saw nothing
+#pragma unroll
+                    for (int v = 0; v < V; ++v) acc[v] = fmaf(w, y[f][v], acc[v]);
+                }
+            }
         }
+#pragma unroll
+        for (int o = 16; o > 0; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
         const float inv = sum == 0.f ? 0.f : 1.f / sum;
 #pragma unroll
         for (int v = 0; v < V; ++v) acc[v] *= inv;
