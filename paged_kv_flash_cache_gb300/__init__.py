@@ -73,6 +73,8 @@ def library_path() -> str:
 def load_library():
     """Load libpkv.so (built in-tree by paged_kv_flash_cache_gb300.build). Raises if absent."""
     global _lib
+    if _lib is not None:
+        return _lib
     with _lock:
         if _lib is not None:
             return _lib
@@ -124,20 +126,31 @@ def load_library():
 # marshalling helpers
 # ---------------------------------------------------------------------------------------------
 
+# A call of a few microseconds on the GPU waits for its marshalling: the helpers take plain ints (ctypes makes the
+# pointers), look names up once and enter a device context only when another device is current.
+
+_torch_module = None
+_DTYPES = {}
+_current_raw_stream = None
+
+
 def _torch():
-    import torch
-    return torch
+    global _torch_module, _current_raw_stream
+    if _torch_module is None:
+        import torch
+        _DTYPES.update({torch.float16: F16, torch.bfloat16: BF16, torch.float32: F32})
+        # the current stream's handle without a Stream object around it, where this PyTorch offers it
+        _current_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)
+        _torch_module = torch
+    return _torch_module
 
 
 def _dtype_code(dt) -> int:
-    torch = _torch()
-    if dt == torch.float16:
-        return F16
-    if dt == torch.bfloat16:
-        return BF16
-    if dt == torch.float32:
-        return F32
-    raise TypeError("unsupported dtype %s" % dt)
+    _torch()
+    code = _DTYPES.get(dt)
+    if code is None:
+        raise TypeError("unsupported dtype %s" % dt)
+    return code
 
 
 def _dev(t, name):
@@ -147,26 +160,38 @@ def _dev(t, name):
         raise ValueError("%s must be a CUDA tensor (there is no CPU path)" % name)
     if not t.is_contiguous():
         raise ValueError("%s must be contiguous" % name)
-    return ctypes.c_void_p(t.data_ptr())
+    return t.data_ptr()
 
 
 def _i32(t, name):
-    torch = _torch()
-    if t.dtype != torch.int32:
+    if t.dtype != _torch().int32:
         raise TypeError("%s must be int32" % name)
     return _dev(t, name)
 
 
-def _stream(stream):
-    torch = _torch()
+def _stream(stream, device=None):
+    """The stream's handle; None: the current stream (of device index `device`, or of the current device)."""
     if stream is None:
-        stream = torch.cuda.current_stream()
-    return ctypes.c_void_p(stream.cuda_stream if hasattr(stream, "cuda_stream") else int(stream))
+        torch = _torch()
+        if _current_raw_stream is not None:
+            return _current_raw_stream(torch.cuda.current_device() if device is None else device)
+        return torch.cuda.current_stream(device).cuda_stream
+    return stream.cuda_stream if hasattr(stream, "cuda_stream") else int(stream)
+
+
+def _on_device(index, fn, *args):
+    """fn(*args) with device `index` current: the library launches on the current device."""
+    torch = _torch()
+    if torch.cuda.current_device() == index:
+        return fn(*args)
+    with torch.cuda.device(index):
+        return fn(*args)
 
 
 def is_fp8_cache(cache) -> bool:
     torch = _torch()
-    return cache.dtype == torch.uint8 or cache.dtype == getattr(torch, "float8_e4m3fn", None)
+    dt = cache.dtype
+    return dt is torch.uint8 or dt is torch.float8_e4m3fn
 
 
 def _cache_struct(cache, act_dtype, scales=None) -> _Cache:
@@ -345,20 +370,19 @@ def paged_attn_mixed(cache, q, cu_q_lens, context_lens, block_tables, max_q_len:
 
 def _rows(t, heads, head_dim, name):
     """Pointer and token stride (elements) of [T, heads, head_dim] rows whose tokens may be strided."""
-    if not t.is_cuda:
-        raise ValueError("%s must be a CUDA tensor (there is no CPU path)" % name)
-    if t.dim() != 3 or tuple(t.shape[1:]) != (heads, head_dim):
+    shape = t.shape
+    if len(shape) != 3 or shape[1] != heads or shape[2] != head_dim:
         raise ValueError("%s must be [tokens, %d, %d]" % (name, heads, head_dim))
-    if t.stride(2) != 1 or (heads > 1 and t.stride(1) != head_dim):
+    s0, s1, s2 = t.stride()
+    if s2 != 1 or (heads > 1 and s1 != head_dim):
         raise ValueError("%s: the heads of a token must be contiguous" % name)
-    stride = t.stride(0) if t.shape[0] > 1 else heads * head_dim
-    return ctypes.c_void_p(t.data_ptr()), stride
+    return t.data_ptr(), s0 if shape[0] > 1 else heads * head_dim
 
 
-def _same_device(device, tensors):
-    for name, t in tensors.items():
-        if t is not None and t.device != device:
-            raise ValueError("%s is on %s, the cache on %s" % (name, t.device, device))
+def _same_device(index, *tensors):
+    for t in tensors:
+        if t is not None and t.get_device() != index:
+            raise ValueError("a tensor on %s with a cache on cuda:%d" % (t.device, index))
 
 
 def rope_append(cache, q, k, v, inv_freq, cu_new_lens, ctx_before, block_tables, positions, interleaved: bool = False,
@@ -375,35 +399,35 @@ def rope_append(cache, q, k, v, inv_freq, cu_new_lens, ctx_before, block_tables,
     lib = load_library()
     if k.dtype != q.dtype or v.dtype != q.dtype or k.shape != v.shape or k.shape[0] != q.shape[0]:
         raise TypeError("q / k / v must match each other")
+    index = cache.get_device()
+    _same_device(index, q, k, v, inv_freq, positions, cu_new_lens, ctx_before, block_tables, q_weight, k_weight, q_out,
+                 scales)
     c = _cache_struct(cache, q.dtype, scales)
-    hkv, d = cache.shape[2], cache.shape[4]
-    total, hq = q.shape[:2]
+    hkv, d = c.num_kv_heads, c.head_dim
+    total, hq = q.shape[0], q.shape[1]
     batch, mb = block_tables.shape
-    if inv_freq.dtype != torch.float32 or inv_freq.dim() != 1 or 2 * inv_freq.shape[0] > d:
+    half = inv_freq.shape[0]
+    if inv_freq.dtype != torch.float32 or inv_freq.dim() != 1 or 2 * half > d:
         raise ValueError("inv_freq must be float32 [rotary_dim / 2], rotary_dim <= head_dim")
     if positions.shape != (total,):
         raise ValueError("positions must be [tokens]")
     if cu_new_lens.shape != (batch + 1,) or ctx_before.shape != (batch,):
         raise ValueError("cu_new_lens must be [batch + 1], ctx_before [batch]")
     for name, w in (("q_weight", q_weight), ("k_weight", k_weight)):
-        if w is not None and (w.dtype != q.dtype or tuple(w.shape) != (d,)):
+        if w is not None and (w.dtype != q.dtype or w.shape != (d,)):
             raise ValueError("%s must be [head_dim] in the dtype of q" % name)
     if q_out is None:
         q_out = torch.empty((total, hq, d), dtype=q.dtype, device=q.device)
     elif q_out.dtype != q.dtype or q_out.shape != q.shape:
         raise ValueError("q_out must match q")
-    _same_device(cache.device, dict(q=q, k=k, v=v, inv_freq=inv_freq, positions=positions, cu_new_lens=cu_new_lens,
-                                    ctx_before=ctx_before, block_tables=block_tables, q_weight=q_weight,
-                                    k_weight=k_weight, q_out=q_out, scales=scales))
-    rope = _Rope(2 * inv_freq.shape[0], 1 if interleaved else 0, _dev(inv_freq, "inv_freq"), float(mscale),
-                 _dev(q_weight, "q_weight"), _dev(k_weight, "k_weight"), float(eps))
+    rope = _Rope(2 * half, 1 if interleaved else 0, _dev(inv_freq, "inv_freq"), mscale, _dev(q_weight, "q_weight"),
+                 _dev(k_weight, "k_weight"), eps)
     (qp, qs), (kp, ks), (vp, vs) = _rows(q, hq, d, "q"), _rows(k, hkv, d, "k"), _rows(v, hkv, d, "v")
     op, os_ = _rows(q_out, hq, d, "q_out")
-    with torch.cuda.device(cache.device):
-        _check(lib.pkv_rope_append(c, rope, qp, qs, hq, kp, ks, vp, vs, _i32(positions, "positions"),
-                                   _i32(cu_new_lens, "cu_new_lens"), _i32(ctx_before, "ctx_before"),
-                                   _i32(block_tables, "block_tables"), batch, mb, total, op, os_, _stream(stream)),
-               "pkv_rope_append")
+    _check(_on_device(index, lib.pkv_rope_append, c, rope, qp, qs, hq, kp, ks, vp, vs, _i32(positions, "positions"),
+                      _i32(cu_new_lens, "cu_new_lens"), _i32(ctx_before, "ctx_before"),
+                      _i32(block_tables, "block_tables"), batch, mb, total, op, os_, _stream(stream, index)),
+           "pkv_rope_append")
     return q_out
 
 
@@ -418,10 +442,12 @@ def paged_attn_tree(cache, q, tree_mask, cu_q_lens, context_lens, block_tables, 
     `workloads.tree_mask`), one another. Returns `out`."""
     torch = _torch()
     lib = load_library()
+    index = cache.get_device()
+    _same_device(index, q, tree_mask, cu_q_lens, context_lens, block_tables, workspace, out, lse)
     c = _cache_struct(cache, q.dtype)
     total_q, hq, d = q.shape
     batch, mb = block_tables.shape
-    if d != cache.shape[4]:
+    if d != c.head_dim:
         raise ValueError("q must have the cache's head_dim")
     if tree_mask.dim() != 2 or tree_mask.shape[0] != total_q:
         raise ValueError("tree_mask must be [rows of q, words]")
@@ -431,22 +457,18 @@ def paged_attn_tree(cache, q, tree_mask, cu_q_lens, context_lens, block_tables, 
         out = torch.empty((total_q, hq, d), dtype=out_dtype or q.dtype, device=q.device)
     elif out.shape != q.shape:
         raise ValueError("out must have the shape of q")
-    if lse is not None and (lse.dtype != torch.float32 or tuple(lse.shape) != (total_q, hq)):
+    if lse is not None and (lse.dtype != torch.float32 or lse.shape != (total_q, hq)):
         raise ValueError("lse must be float32 [rows of q, Hq]")
     if workspace is None:
-        workspace = torch.empty(tree_workspace_size(hq, cache.shape[2], d, max_q_len), dtype=torch.uint8,
+        workspace = torch.empty(lib.pkv_tree_workspace_size(hq, c.num_kv_heads, d, max_q_len), dtype=torch.uint8,
                                 device=q.device)
-    _same_device(cache.device, dict(q=q, tree_mask=tree_mask, cu_q_lens=cu_q_lens, context_lens=context_lens,
-                                    block_tables=block_tables, workspace=workspace, out=out, lse=lse))
     ws_bytes = workspace.numel() * workspace.element_size()
     scale = (1.0 / math.sqrt(d)) if scale is None else float(scale)
-    with torch.cuda.device(cache.device):
-        _check(lib.pkv_paged_attn_tree(c, _dev(q, "q"), hq, _i32(tree_mask, "tree_mask"), int(tree_mask.shape[1]),
-                                       _i32(cu_q_lens, "cu_q_lens"), _i32(context_lens, "context_lens"),
-                                       _i32(block_tables, "block_tables"), batch, mb, total_q, int(max_q_len), scale,
-                                       _dev(workspace, "workspace"), ws_bytes, _dev(out, "out"),
-                                       _dtype_code(out.dtype), _dev(lse, "lse"), _stream(stream)),
-               "pkv_paged_attn_tree")
+    _check(_on_device(index, lib.pkv_paged_attn_tree, c, _dev(q, "q"), hq, _i32(tree_mask, "tree_mask"),
+                      tree_mask.shape[1], _i32(cu_q_lens, "cu_q_lens"), _i32(context_lens, "context_lens"),
+                      _i32(block_tables, "block_tables"), batch, mb, total_q, int(max_q_len), scale,
+                      _dev(workspace, "workspace"), ws_bytes, _dev(out, "out"), _dtype_code(out.dtype), _dev(lse, "lse"),
+                      _stream(stream, index)), "pkv_paged_attn_tree")
     return out
 
 
@@ -456,16 +478,15 @@ def kv_cache_compact(cache, keep_pos, cu_keep, dst_start, block_tables, stream=N
     dst_start [batch]."""
     torch = _torch()
     lib = load_library()
+    index = cache.get_device()
+    _same_device(index, keep_pos, cu_keep, dst_start, block_tables, scales)
     c = _cache_struct(cache, torch.float16 if is_fp8_cache(cache) else cache.dtype, scales)
     batch, mb = block_tables.shape
     if keep_pos.dim() != 1 or cu_keep.shape != (batch + 1,) or dst_start.shape != (batch,):
         raise ValueError("keep_pos must be [num_keep], cu_keep [batch + 1], dst_start [batch]")
-    _same_device(cache.device, dict(keep_pos=keep_pos, cu_keep=cu_keep, dst_start=dst_start, block_tables=block_tables,
-                                    scales=scales))
-    with torch.cuda.device(cache.device):
-        _check(lib.pkv_kv_cache_compact(c, _i32(keep_pos, "keep_pos"), _i32(cu_keep, "cu_keep"),
-                                        _i32(dst_start, "dst_start"), _i32(block_tables, "block_tables"), batch, mb,
-                                        int(keep_pos.shape[0]), _stream(stream)), "pkv_kv_cache_compact")
+    _check(_on_device(index, lib.pkv_kv_cache_compact, c, _i32(keep_pos, "keep_pos"), _i32(cu_keep, "cu_keep"),
+                      _i32(dst_start, "dst_start"), _i32(block_tables, "block_tables"), batch, mb, keep_pos.shape[0],
+                      _stream(stream, index)), "pkv_kv_cache_compact")
 
 
 def attn_combine(partial_o, partial_lse, out=None, out_dtype=None, lse=None, stream=None):
