@@ -26,8 +26,9 @@
 //
 // Warps: 0 loads Q and the K / V tiles by TMA into a ring (a lane per page), 1 issues the MMAs and owns
 // TMEM, 2 walks the run and hands its segments to the others, the warpgroups of lanes A and B do softmax and
-// output. P goes to the tensor cores as its 16-bit rounding plus the rounding's remainder (two products), so it
-// is not a rounding to 16 bits.
+// output. P goes to the tensor cores as its 16-bit rounding plus the rounding's remainder (two products), so that it
+// is not a rounding to 16 bits -- but for wide blocks with a 16-bit output, which the tensor cores bound: there P is
+// rounded once, half a step of the output's own type (the prefill's choice too).
 //
 // Rows that see nothing (a padded node): 0 and -inf. Masked keys: their scores are replaced, never
 // multiplied, so that K may hold anything; V rows beyond the context are zeroed in shared memory, and a
@@ -68,9 +69,11 @@ struct TreeLayout {
     static constexpr uint32_t kQBytes = kHalves * kQHalf;
     static constexpr uint32_t kTileHalf = kBN * 128;
     static constexpr uint32_t kTileBytes = kHalves * kTileHalf;  // a K or a V tile
+    // ring slots; a launch whose blocks are all narrow has one more in the place of lane B's Q tile
     static constexpr int kRing = D == 64 ? 8 : 4;
-    static constexpr uint32_t kRingOff = kLanes * kQBytes;
-    static constexpr uint32_t kStageOff = kRingOff + kRing * kTileBytes;  // output rows, 4 KB a softmax warp
+    static constexpr int kRingMax = kRing + (kLanes == 2 ? 1 : 0);
+    static_assert(kLanes == 1 || kQBytes == kTileBytes, "a Q tile's place is a ring slot's");
+    static constexpr uint32_t kStageOff = kLanes * kQBytes + kRing * kTileBytes;  // output rows, 4 KB a softmax warp
     static constexpr uint32_t kMlOff = kStageOff + 4 * kLanes * 4096u;    // [128] (max, sum) between the lanes
     static constexpr uint32_t kBarOff = kMlOff + kBM * 8;
     static constexpr uint32_t kSegOff = kBarOff + 512;
@@ -136,21 +139,31 @@ __device__ __forceinline__ uint32_t drop_nonfinite(uint32_t w) {
     return w;
 }
 
+// What rounding to 16 bits left of a pair (hi: the rounded pair), itself rounded to 16 bits.
+template <bool BF16>
+__device__ __forceinline__ uint32_t remainder_pair(float a, float b, uint32_t hi) {
+    if constexpr (BF16) return pack_pair<true>(a - __uint_as_float(hi << 16), b - __uint_as_float(hi & 0xffff0000u));
+    const float2 f = __half22float2(*reinterpret_cast<const __half2 *>(&hi));
+    return pack_pair<false>(a - f.x, b - f.y);
+}
+
 template <int D, bool BF16>
 __global__ void __launch_bounds__(TreeLayout<D>::kThreads, 1)
     tree_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CUtensorMap tm_kv, TreeArgs a) {
     using L = TreeLayout<D>;
-    constexpr int kBN = L::kBN, kLanes = L::kLanes, kRing = L::kRing;
+    constexpr int kBN = L::kBN, kLanes = L::kLanes, kRingMax = L::kRingMax;
+    const bool all_narrow = kLanes == 2 && a.max_q_len <= a.tile_nodes;
+    const uint32_t ring = all_narrow ? kRingMax : L::kRing;
     extern __shared__ uint8_t smem_raw[];
     // 1024-byte alignment: the 128-byte swizzle pattern is a function of address bits 4-9.
     uint8_t *smem = smem_raw + ((1024u - (smem_addr(smem_raw) & 1023u)) & 1023u);
     uint8_t *sQ = smem;
-    uint8_t *sRing = smem + L::kRingOff;
+    uint8_t *sRing = smem + (all_narrow ? 1 : kLanes) * L::kQBytes;
     float2 *sMl = reinterpret_cast<float2 *>(smem + L::kMlOff);
     uint64_t *bars = reinterpret_cast<uint64_t *>(smem + L::kBarOff);
-    uint64_t *kv_full = bars;              // [kRing]
-    uint64_t *kv_empty = kv_full + kRing;  // [kRing]
-    uint64_t *q_full = kv_empty + kRing;   // a segment's Q tiles have landed
+    uint64_t *kv_full = bars;                 // [kRingMax]
+    uint64_t *kv_empty = kv_full + kRingMax;  // [kRingMax]
+    uint64_t *q_full = kv_empty + kRingMax;   // a segment's Q tiles have landed
     uint64_t *q_empty = q_full + 1;        // its QK products are done
     uint64_t *s_full = q_empty + 1;        // [2] S of a lane computed (and its last P V done)
     uint64_t *p_full = s_full + 2;         // [2] P written over it
@@ -171,7 +184,7 @@ __global__ void __launch_bounds__(TreeLayout<D>::kThreads, 1)
     constexpr int kSoftmaxWarps = 4 * kLanes;
 
     if (threadIdx.x == 0) {
-        for (int i = 0; i < kRing; ++i) {
+        for (int i = 0; i < kRingMax; ++i) {
             mbar_init(&kv_full[i], 1);
             mbar_init(&kv_empty[i], 1);
         }
@@ -238,7 +251,8 @@ __global__ void __launch_bounds__(TreeLayout<D>::kThreads, 1)
                 tc::prefetch_tensormap(&tm_q);
                 tc::prefetch_tensormap(&tm_kv);
             }
-            uint32_t item = 0, qn = 0;
+            uint32_t qn = 0;
+            uint32_t slot = 0, ph = 1, landing = 0;  // ring position and what to find on kv_empty; items issued (at most ring)
             bool ok = true;
             for (; (ok = next_segment()); ++seg_i) {
                 const Segment s = segs[seg_i % kSegs];
@@ -291,8 +305,7 @@ __global__ void __launch_bounds__(TreeLayout<D>::kThreads, 1)
                     }
                     const int start = (s.t0 + j) * kBN, npages = page_count(j);
                     const int off = bs < kBN ? 0 : (start & (bs - 1));
-                    const uint32_t slot = item % kRing;
-                    if (!(ok = mbar_wait(&kv_empty[slot], ((item / kRing) & 1u) ^ 1u, abort_flag, a.err))) break;
+                    if (!(ok = mbar_wait(&kv_empty[slot], ph, abort_flag, a.err))) break;
                     if (lane == 0) mbar_arrive_expect_tx(&kv_full[slot], (uint32_t)npages * box_rows * 128u * L::kHalves);
                     __syncwarp();
                     if (lane < npages) {
@@ -306,7 +319,11 @@ __global__ void __launch_bounds__(TreeLayout<D>::kThreads, 1)
                         for (int hf = 0; hf < L::kHalves; ++hf)
                             tc::tma_load_2d_hint(dst + hf * L::kTileHalf, &tm_kv, hf * 64, row, &kv_full[slot], pol);
                     }
-                    ++item;
+                    if (landing < ring) ++landing;
+                    if (++slot == ring) {
+                        slot = 0;
+                        ph ^= 1u;
+                    }
                 }
                 __syncwarp();
                 if (lane == 0) mbar_arrive(&seg_empty[seg_i % kSegs]);
@@ -314,8 +331,14 @@ __global__ void __launch_bounds__(TreeLayout<D>::kThreads, 1)
             }
             // every copy has landed before the CTA exits (bounded), also when another role gave up
             volatile int no_abort = 0;
-            for (uint32_t i = item > (uint32_t)kRing ? item - kRing : 0u; i < item; ++i)
-                mbar_wait(&kv_full[i % kRing], (i / kRing) & 1u, &no_abort, nullptr);
+            for (uint32_t i = 0; i < landing; ++i) {  // backwards: a slot's last load has the parity that ph had then
+                if (slot == 0) {
+                    slot = ring;
+                    ph ^= 1u;
+                }
+                --slot;
+                mbar_wait(&kv_full[slot], ph ^ 1u, &no_abort, nullptr);
+            }
             if (qn > 0) mbar_wait(q_full, (qn - 1) & 1u, &no_abort, nullptr);
         } else if (warp == 1) {
             // ====================================== MMA issuer ======================================
@@ -325,7 +348,7 @@ __global__ void __launch_bounds__(TreeLayout<D>::kThreads, 1)
                 const uint32_t aQ = smem_addr(sQ), aRing = smem_addr(sRing);
                 uint32_t slot = 0, ph = 0;  // ring position: the next item to use
                 auto advance = [&](uint32_t &sl, uint32_t &p) {
-                    if (++sl == (uint32_t)kRing) {
+                    if (++sl == ring) {
                         sl = 0;
                         p ^= 1u;
                     }
@@ -343,6 +366,7 @@ __global__ void __launch_bounds__(TreeLayout<D>::kThreads, 1)
                     // the producer): a step's V, then its K.
                     const bool wide = kLanes == 2 && s.nodes > a.tile_nodes;
                     const int steps = wide ? 2 * T : T, stride = wide || kLanes == 1 ? 1 : 2;
+                    const bool two_parts = !wide || a.out_dtype == 2;
                     if (!(ok = mbar_wait(q_full, seg_i & 1u, abort_flag, a.err))) break;
                     tc::fence_after_sync();
                     for (int t = -kLanes; ok && t < steps; ++t) {
@@ -350,6 +374,7 @@ __global__ void __launch_bounds__(TreeLayout<D>::kThreads, 1)
                         const int j = wide ? t >> 1 : t, jn = j + stride;
                         const bool frees = !wide || x == 1;
                         uint32_t sl = slot, sp = ph;  // the step's K
+                        bool k_here = false;
                         if (t >= 0) {
                             if (!(ok = mbar_wait(&p_full[x], (np >> x) & 1u, abort_flag, a.err))) break;
                             np ^= 1u << x;
@@ -358,24 +383,25 @@ __global__ void __launch_bounds__(TreeLayout<D>::kThreads, 1)
                             const bool first = j < stride;
                             if (first && !(ok = mbar_wait(o_empty, (seg_i & 1u) ^ 1u, abort_flag, a.err))) break;
                             tc::fence_after_sync();
+                            advance(sl, sp);
+                            k_here = jn < T && mbar_test_wait(&kv_full[sl], sp);  // (asked before the products' issue)
                             // (a descriptor's address field counts 16 bytes and has room for all of shared memory:
                             // the steps along it are additions)
                             const uint64_t dV = dV0 + slot * (L::kTileBytes >> 4);
                             const uint32_t tO = tmem + L::kColO + 128u * x, tP = tmem + kBN * x;
                             // 16 keys a step: 8 columns of P in their 32-column chunk, the remainders 16 behind
 #pragma unroll
-                            for (int kk = 0; kk < kBN / 16; ++kk)
-#pragma unroll
-                                for (int part = 0; part < 2; ++part)
-                                    tc::mma_f16_ts(tO, tP + 32u * (kk >> 1) + 8u * (kk & 1) + 16u * part,
-                                                   dV + (uint32_t)(kk * 2048 >> 4), id_pv,
-                                                   (first && part == 0 && kk == 0) ? 0u : 1u);
+                            for (int kk = 0; kk < kBN / 16; ++kk) {
+                                const uint32_t tPk = tP + 32u * (kk >> 1) + 8u * (kk & 1);
+                                const uint64_t dVk = dV + (uint32_t)(kk * 2048 >> 4);
+                                tc::mma_f16_ts(tO, tPk, dVk, id_pv, (first && kk == 0) ? 0u : 1u);
+                                if (two_parts) tc::mma_f16_ts(tO, tPk + 16u, dVk, id_pv, 1u);
+                            }
                             if (frees) tc::mma_commit(&kv_empty[slot]);
-                            advance(sl, sp);
                         }
                         if (jn < T) {
-                            if (!(ok = mbar_wait(&kv_full[sl], sp, abort_flag, a.err))) break;
-                            tc::fence_after_sync();
+                            // (S of the lane: its softmax was done with it before P, waited for above)
+                            if (!k_here && !(ok = mbar_wait(&kv_full[sl], sp, abort_flag, a.err))) break;
                             const uint64_t dK = dK0 + sl * (L::kTileBytes >> 4);
                             const uint64_t dQ = dQ0 + (wide ? x : 0) * (L::kQBytes >> 4);
 #pragma unroll
@@ -491,6 +517,7 @@ __global__ void __launch_bounds__(TreeLayout<D>::kThreads, 1)
             const Segment &s = segs[seg_i % kSegs];
             const bool wide = s.nodes > a.tile_nodes;
             const bool split = kLanes == 2 && !wide;  // the lanes share the rows
+            const bool two_parts = !(kLanes == 2 && wide) || a.out_dtype == 2;
             const int T = s.t1 - s.t0, ahead = kLanes == 1 || wide ? 1 : min(2, T);
             // wide: lane A's tile is full, lane B has the rest
             const int rows = (!wide ? s.nodes : x == 0 ? a.tile_nodes : s.nodes - a.tile_nodes) * gu;
@@ -569,16 +596,23 @@ __global__ void __launch_bounds__(TreeLayout<D>::kThreads, 1)
 #pragma unroll
                     for (int cc = 0; cc < kBN / 32; ++cc) {
                         // P over the chunk's own scores: 16 columns of roundings, 16 of remainders
-                        uint32_t ph[16], pl[16];
+                        uint32_t ph[16];
 #pragma unroll
                         for (int q = 0; q < 16; ++q) {
                             const float2 xq = ffma2(make_float2(v[cc * 32 + 2 * q], v[cc * 32 + 2 * q + 1]), cc2, nm2);
                             const float2 e = make_float2(ex2f(xq.x), ex2f(xq.y));
                             l4[q & 3] = fadd2(l4[q & 3], e);
-                            split_pair<BF16>(e.x, e.y, ph[q], pl[q]);
+                            ph[q] = pack_pair<BF16>(e.x, e.y);
+                            v[cc * 32 + 2 * q] = e.x;
+                            v[cc * 32 + 2 * q + 1] = e.y;
                         }
                         tc::tmem_st16(tS + cc * 32, ph);
-                        tc::tmem_st16(tS + cc * 32 + 16, pl);
+                        if (two_parts) {
+#pragma unroll
+                            for (int q = 0; q < 16; ++q)
+                                ph[q] = remainder_pair<BF16>(v[cc * 32 + 2 * q], v[cc * 32 + 2 * q + 1], ph[q]);
+                            tc::tmem_st16(tS + cc * 32 + 16, ph);
+                        }
                     }
                     const float2 ls = fadd2(fadd2(l4[0], l4[1]), fadd2(l4[2], l4[3]));
                     l += ls.x + ls.y;
@@ -586,8 +620,8 @@ __global__ void __launch_bounds__(TreeLayout<D>::kThreads, 1)
                 // V of drafted tokens and beyond the end: zero what is past the end, sweep the drafted rows
                 if (tail && (split || x == 0)) {
                     const uint32_t vi = item + j + min(T, ahead + j);
-                    if (!(ok = mbar_wait(&kv_full[vi % kRing], (vi / kRing) & 1u, abort_flag, a.err))) break;
-                    uint8_t *const sV = sRing + (vi % kRing) * L::kTileBytes;
+                    if (!(ok = mbar_wait(&kv_full[vi % ring], (vi / ring) & 1u, abort_flag, a.err))) break;
+                    uint8_t *const sV = sRing + (vi % ring) * L::kTileBytes;
                     const int n_valid = min(kBN, s.len - start);
                     bool bad = false;
                     // 8 lanes a row (128 bytes of a 64-column half), 4 rows a warp and step
