@@ -66,6 +66,18 @@ __device__ __forceinline__ void fence_proxy_async_smem() {
     asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
 }
 
+// One thread of a converged warp. (The compiler knows that a branch on elect.sync has one thread in it, and
+// hands an instruction that takes warp-uniform operands its descriptors directly; on `lane == 0` it does not.)
+__device__ __forceinline__ bool elect_one() {
+    uint32_t is;
+    asm volatile(
+        "{\n\t.reg .pred p;\n\t"
+        "elect.sync _|p, 0xffffffff;\n\t"
+        "selp.u32 %0, 1, 0, p;\n\t}"
+        : "=r"(is));
+    return is != 0;
+}
+
 // ---- MMA: D[tmem] (+)= A[smem] * B[smem], issued by one thread ----------------------------------
 __device__ __forceinline__ void mma_f16_ss(uint32_t d_tmem, uint64_t a_desc, uint64_t b_desc, uint32_t idesc,
                                            uint32_t accumulate) {

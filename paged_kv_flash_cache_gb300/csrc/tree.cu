@@ -11,13 +11,14 @@
 // Rows: the query heads of a KV head read the same keys, so the rows of a product are (node, head of the
 // group): 128 of them a tile, whole nodes. S = Q K^T and O += P V are tcgen05.mma with M = 128.
 //
-// Two lanes. TMEM holds two score tiles and two outputs (head_dim up to 128), each with a warpgroup that
-// does its softmax, so that one lane's softmax overlaps the other's products:
-//   wide    a block of more than 128 rows: lane A its first 128 rows, lane B the others, both over every
-//           key tile (K and V come from memory once for both);
-//   narrow  up to 128 rows: both lanes the same rows, lane A the even key tiles, lane B the odd ones,
-//           their (max, sum, output) joined at the end.
-// At head_dim 256 the output takes half of TMEM: one lane, 64-key tiles.
+// Two lanes, each with an output and two score buffers of 64 keys in TMEM (head_dim up to 128) and a warpgroup
+// for its softmax; K and V come in tiles of 128 keys, once for both:
+//   wide    a block of more than 128 rows: lane A its first 128 rows, lane B the others, both over every key;
+//   narrow  up to 128 rows: both lanes the same rows, lane A the first 64 keys of each tile, lane B the other
+//           64, their (max, sum, output) joined at the end.
+// At head_dim 256 the output takes half of TMEM: one lane, 64-key tiles. While a lane's softmax works on one
+// score buffer its next 64 keys' Q K^T fills the other: Q K(u + 1) is issued before P V(u). (With one buffer of
+// 128 keys a lane the chain softmax - P V - Q K - softmax, 5100 cycles a tile of a wide block, bounded the kernel.)
 //
 // Work: the (sequence, KV head, row block) items, laid end to end in key tiles, are cut into equal runs,
 // one a CTA (one CTA an SM): any mix of lengths fills the GPU evenly, an item is split only where a run
@@ -64,6 +65,7 @@ template <int D>
 struct TreeLayout {
     static constexpr int kLanes = D <= 128 ? 2 : 1;
     static constexpr int kBN = D <= 128 ? 128 : 64;  // keys a tile
+    static constexpr int kSub = 64;                  // keys of a score buffer
     static constexpr int kHalves = D / 64;           // 128-byte swizzle atoms along D
     static constexpr uint32_t kQHalf = kBM * 128;
     static constexpr uint32_t kQBytes = kHalves * kQHalf;
@@ -79,7 +81,7 @@ struct TreeLayout {
     static constexpr uint32_t kSegOff = kBarOff + 512;
     static constexpr uint32_t kSmem = kSegOff + kSegs * sizeof(Segment) + 1024;  // + alignment slack
     static constexpr int kThreads = 128 * (1 + kLanes);
-    // TMEM: S of lane x at kBN x (P in its place), O of lane x at 256 + 128 x
+    // TMEM: score buffer i of lane x at 128 i + 64 x (P in its place), O of lane x at 256 + 128 x
     static constexpr uint32_t kColO = 256;
 };
 
@@ -151,7 +153,7 @@ template <int D, bool BF16>
 __global__ void __launch_bounds__(TreeLayout<D>::kThreads, 1)
     tree_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CUtensorMap tm_kv, TreeArgs a) {
     using L = TreeLayout<D>;
-    constexpr int kBN = L::kBN, kLanes = L::kLanes, kRingMax = L::kRingMax;
+    constexpr int kBN = L::kBN, kSub = L::kSub, kLanes = L::kLanes, kRingMax = L::kRingMax;
     const bool all_narrow = kLanes == 2 && a.max_q_len <= a.tile_nodes;
     const uint32_t ring = all_narrow ? kRingMax : L::kRing;
     extern __shared__ uint8_t smem_raw[];
@@ -165,9 +167,10 @@ __global__ void __launch_bounds__(TreeLayout<D>::kThreads, 1)
     uint64_t *kv_empty = kv_full + kRingMax;  // [kRingMax]
     uint64_t *q_full = kv_empty + kRingMax;   // a segment's Q tiles have landed
     uint64_t *q_empty = q_full + 1;        // its QK products are done
-    uint64_t *s_full = q_empty + 1;        // [2] S of a lane computed (and its last P V done)
+    uint64_t *s_full = q_empty + 1;        // [2] score buffer i of the lanes computed
     uint64_t *p_full = s_full + 2;         // [2] P written over it
-    uint64_t *o_done = p_full + 2;         // every P V of the segment is done
+    uint64_t *pv_late = p_full + 2;        // the segment's last P V but one is done
+    uint64_t *o_done = pv_late + 1;        // every P V of the segment is done
     uint64_t *o_empty = o_done + 1;        // its outputs are read
     uint64_t *ml_full = o_empty + 1;       // narrow: (max, sum) handed over
     uint64_t *seg_full = ml_full + 1;      // [kSegs]
@@ -192,8 +195,9 @@ __global__ void __launch_bounds__(TreeLayout<D>::kThreads, 1)
         mbar_init(q_empty, 1);
         for (int i = 0; i < 2; ++i) {
             mbar_init(&s_full[i], 1);
-            mbar_init(&p_full[i], 4);
+            mbar_init(&p_full[i], kSoftmaxWarps);
         }
+        mbar_init(pv_late, 1);
         mbar_init(o_done, 1);
         mbar_init(o_empty, kSoftmaxWarps);
         mbar_init(ml_full, kSoftmaxWarps);
@@ -256,8 +260,8 @@ __global__ void __launch_bounds__(TreeLayout<D>::kThreads, 1)
             bool ok = true;
             for (; (ok = next_segment()); ++seg_i) {
                 const Segment s = segs[seg_i % kSegs];
-                const bool wide = s.nodes > a.tile_nodes;
-                const int T = s.t1 - s.t0, ahead = kLanes == 1 || wide ? 1 : min(2, T);
+                const bool wide = kLanes == 2 && s.nodes > a.tile_nodes;
+                const int T = s.t1 - s.t0, ahead = wide ? 1 : min(2, T);
                 const int kvh = s.unit / a.head_groups;
                 const int *bt = a.block_tables + (size_t)s.b * a.max_blocks_per_seq;
                 // Q: the block's nodes, gu heads each, one box per tile and 64 columns
@@ -342,83 +346,97 @@ __global__ void __launch_bounds__(TreeLayout<D>::kThreads, 1)
             if (qn > 0) mbar_wait(q_full, (qn - 1) & 1u, &no_abort, nullptr);
         } else if (warp == 1) {
             // ====================================== MMA issuer ======================================
-            if (lane == 0) {
-                const uint32_t id_qk = tc::idesc_f16(BF16, kBM, kBN, false);
+            if (tc::elect_one()) {
+                const uint32_t id_sub = tc::idesc_f16(BF16, kBM, kSub, false), id_tile = tc::idesc_f16(BF16, kBM, kBN, false);
                 const uint32_t id_pv = tc::idesc_f16(BF16, kBM, D, true);
                 const uint32_t aQ = smem_addr(sQ), aRing = smem_addr(sRing);
-                uint32_t slot = 0, ph = 0;  // ring position: the next item to use
-                auto advance = [&](uint32_t &sl, uint32_t &p) {
-                    if (++sl == ring) {
-                        sl = 0;
-                        p ^= 1u;
-                    }
-                };
-                uint32_t np = 0;  // parities of the lanes' next P tiles
+                // (a descriptor's address field counts 16 bytes and has room for all of shared memory: the steps
+                // along it are additions)
                 const uint64_t dK0 = tc::smem_desc(aRing, 16, 1024), dQ0 = tc::smem_desc(aQ, 16, 1024);
                 const uint64_t dV0 = tc::smem_desc(aRing, L::kTileHalf, 1024);
+                uint32_t slot = 0, ph = 0;  // ring position
+                uint32_t g0 = 0;            // score buffers that each lane used before this segment
+                // the ring item `ahead` items on: its slot, and the parity that says it has landed
+                auto at = [&](uint32_t n, uint32_t &sl, uint32_t &par) {
+                    sl = slot + n;
+                    par = ph;
+                    if (sl >= ring) {
+                        sl -= ring;
+                        par ^= 1u;
+                    }
+                };
+                auto advance = [&](uint32_t n) { at(n, slot, ph); };
                 bool ok = true;
                 for (; (ok = next_segment()); ++seg_i) {
                     const Segment &s = segs[seg_i % kSegs];
                     const int T = s.t1 - s.t0;
-                    // Steps: lane x = t % kLanes takes tile j: P V of tile j, then Q K of the lane's next tile.
-                    // (t < 0: the first Q K of each lane.) Wide lanes share tile t / 2 and B, the second, frees its
-                    // ring slots; narrow lanes take turns on tiles t. The ring holds the tiles in this order (see
-                    // the producer): a step's V, then its K.
+                    // A lane's work is U score buffers: wide, both halves of every tile (buffer u: half u % 2 of tile
+                    // u / 2); narrow, its half of every tile (the one lane of head_dim 256: the tile). Step u: each
+                    // lane's Q K of buffer u + 1, then its P V of buffer u; u = -1: the first Q K. The ring holds the
+                    // tiles in this order of use: wide K_0, V_0, K_1, V_1 ..., else K_0, K_1, V_0, K_2, V_1 ...
                     const bool wide = kLanes == 2 && s.nodes > a.tile_nodes;
-                    const int steps = wide ? 2 * T : T, stride = wide || kLanes == 1 ? 1 : 2;
                     const bool two_parts = !wide || a.out_dtype == 2;
+                    const int U = wide ? 2 * T : T;
                     if (!(ok = mbar_wait(q_full, seg_i & 1u, abort_flag, a.err))) break;
                     tc::fence_after_sync();
-                    for (int t = -kLanes; ok && t < steps; ++t) {
-                        const int x = kLanes == 2 ? t & 1 : 0;
-                        const int j = wide ? t >> 1 : t, jn = j + stride;
-                        const bool frees = !wide || x == 1;
-                        uint32_t sl = slot, sp = ph;  // the step's K
-                        bool k_here = false;
-                        if (t >= 0) {
-                            if (!(ok = mbar_wait(&p_full[x], (np >> x) & 1u, abort_flag, a.err))) break;
-                            np ^= 1u << x;
-                            if (!(ok = mbar_wait(&kv_full[slot], ph, abort_flag, a.err))) break;
+                    for (int u = -1; ok && u < U; ++u) {
+                        const bool more = u + 1 < U, odd = u & 1;
+                        // ring items from the position on: this step's K and V, and how many the step uses up
+                        const uint32_t k_at = wide && odd && u > 0 ? 2 : 0;
+                        const uint32_t v_at = wide ? 1 : more ? 1 : 0;
+                        const uint32_t used = wide ? (odd && u > 0 ? 2 : 0) : (more ? 1 : 0) + (u >= 0 ? 1 : 0);
+                        uint32_t k_slot, k_par, v_slot, v_par;
+                        at(k_at, k_slot, k_par);
+                        at(v_at, v_slot, v_par);
+                        const uint32_t g = g0 + (uint32_t)u;  // buffer u of the lanes: score buffer g % 2
+                        if (more) {
+                            // (the buffer's last P V was issued a step ago: in order)
+                            if (!(ok = mbar_wait(&kv_full[k_slot], k_par, abort_flag, a.err))) break;
+                            const uint32_t i = (g + 1u) & 1u;
+                            // wide: a product of 64 keys for each lane's rows; narrow: one of the tile's 128 keys, whose
+                            // two halves land in the lanes' (neighbouring) buffers
+                            const uint32_t idesc = wide ? id_sub : id_tile;
+                            uint64_t dK = dK0 + k_slot * (L::kTileBytes >> 4), dQ = dQ0;
+                            if (wide) dK += (uint32_t)((u + 1) & 1) * (kSub * 128 >> 4);
+#pragma unroll 1
+                            for (int x = 0; x < (wide ? 2 : 1); ++x, dQ += L::kQBytes >> 4)
+#pragma unroll
+                                for (int kk = 0; kk < D / 16; ++kk)
+                                    tc::mma_f16_ss(tmem + 128u * i + 64u * x, dQ + (((kk >> 2) * L::kQHalf + (kk & 3) * 32u) >> 4),
+                                                   dK + (((kk >> 2) * L::kTileHalf + (kk & 3) * 32u) >> 4), idesc,
+                                                   kk > 0 ? 1u : 0u);
+                            tc::mma_commit(&s_full[i]);
+                            if (!wide || !odd) tc::mma_commit(&kv_empty[k_slot]);
+                            if (u + 2 == U) tc::mma_commit(q_empty);  // the segment's last Q K
+                        }
+                        if (u >= 0) {
+                            const uint32_t i = g & 1u;
+                            if (!(ok = mbar_wait(&kv_full[v_slot], v_par, abort_flag, a.err))) break;
                             // a segment's first P V overwrites an output: the last segment's must be read
-                            const bool first = j < stride;
-                            if (first && !(ok = mbar_wait(o_empty, (seg_i & 1u) ^ 1u, abort_flag, a.err))) break;
+                            if (u == 0 && !(ok = mbar_wait(o_empty, (seg_i & 1u) ^ 1u, abort_flag, a.err))) break;
+                            if (!(ok = mbar_wait(&p_full[i], (g >> 1) & 1u, abort_flag, a.err))) break;
                             tc::fence_after_sync();
-                            advance(sl, sp);
-                            k_here = jn < T && mbar_test_wait(&kv_full[sl], sp);  // (asked before the products' issue)
-                            // (a descriptor's address field counts 16 bytes and has room for all of shared memory:
-                            // the steps along it are additions)
-                            const uint64_t dV = dV0 + slot * (L::kTileBytes >> 4);
-                            const uint32_t tO = tmem + L::kColO + 128u * x, tP = tmem + kBN * x;
-                            // 16 keys a step: 8 columns of P in their 32-column chunk, the remainders 16 behind
+                            uint64_t dV = dV0 + v_slot * (L::kTileBytes >> 4);
+                            if (wide) dV += (uint32_t)odd * (kSub * 128 >> 4);
+#pragma unroll 1
+                            for (int x = 0; x < kLanes; ++x) {
+                                const uint32_t tO = tmem + L::kColO + 128u * x, tP = tmem + 128u * i + 64u * x;
+                                // 16 keys a step: 8 columns of P in their 32-column chunk, the remainders 16 behind
 #pragma unroll
-                            for (int kk = 0; kk < kBN / 16; ++kk) {
-                                const uint32_t tPk = tP + 32u * (kk >> 1) + 8u * (kk & 1);
-                                const uint64_t dVk = dV + (uint32_t)(kk * 2048 >> 4);
-                                tc::mma_f16_ts(tO, tPk, dVk, id_pv, (first && kk == 0) ? 0u : 1u);
-                                if (two_parts) tc::mma_f16_ts(tO, tPk + 16u, dVk, id_pv, 1u);
+                                for (int kk = 0; kk < kSub / 16; ++kk) {
+                                    const uint32_t tPk = tP + 32u * (kk >> 1) + 8u * (kk & 1);
+                                    const uint64_t dVk = dV + (uint32_t)(kk * 2048 >> 4);
+                                    tc::mma_f16_ts(tO, tPk, dVk, id_pv, (u == 0 && kk == 0) ? 0u : 1u);
+                                    if (two_parts) tc::mma_f16_ts(tO, tPk + 16u, dVk, id_pv, 1u);
+                                }
+                                if (!wide) dV += kSub * 128 >> 4;
                             }
-                            if (frees) tc::mma_commit(&kv_empty[slot]);
+                            if (u == U - 2) tc::mma_commit(pv_late);
+                            if (!wide || odd) tc::mma_commit(&kv_empty[v_slot]);
                         }
-                        if (jn < T) {
-                            // (S of the lane: its softmax was done with it before P, waited for above)
-                            if (!k_here && !(ok = mbar_wait(&kv_full[sl], sp, abort_flag, a.err))) break;
-                            const uint64_t dK = dK0 + sl * (L::kTileBytes >> 4);
-                            const uint64_t dQ = dQ0 + (wide ? x : 0) * (L::kQBytes >> 4);
-#pragma unroll
-                            for (int kk = 0; kk < D / 16; ++kk)
-                                tc::mma_f16_ss(tmem + kBN * x, dQ + (((kk >> 2) * L::kQHalf + (kk & 3) * 32u) >> 4),
-                                               dK + (((kk >> 2) * L::kTileHalf + (kk & 3) * 32u) >> 4), id_qk,
-                                               kk > 0 ? 1u : 0u);
-                            tc::mma_commit(&s_full[x]);
-                            if (frees) tc::mma_commit(&kv_empty[sl]);
-                            if (jn == T - 1 && frees) tc::mma_commit(q_empty);  // the segment's last Q K
-                            advance(sl, sp);
-                        }
-                        if (frees) {
-                            slot = sl;
-                            ph = sp;
-                        }
+                        advance(used);
                     }
+                    g0 += (uint32_t)U;
                     if (!ok) break;
                     tc::mma_commit(o_done);
                     mbar_arrive(&seg_empty[seg_i % kSegs]);
@@ -508,67 +526,63 @@ __global__ void __launch_bounds__(TreeLayout<D>::kThreads, 1)
         const int r = w4 * 32 + lane;  // row of the tile = TMEM lane
         const uint32_t lane_base = (uint32_t)(w4 * 32) << 16;
         const float c2 = a.scale * kLog2e;
-        const uint32_t tS = tmem + kBN * x + lane_base;
         const uint32_t tO = tmem + L::kColO + 128u * x + lane_base;
-        uint32_t ns = 0;    // score tiles of this lane so far
+        uint32_t g0 = 0;    // score buffers of this lane before this segment
         uint32_t item = 0;  // ring items before this segment (the V of its tile j: see the sweep)
-        uint32_t nml = 0;   // narrow segments so far
+        uint32_t nml = 0;     // narrow segments so far
+        uint32_t n_late = 0;  // segments of two buffers or more so far
         for (; next_segment(); ++seg_i) {
             const Segment &s = segs[seg_i % kSegs];
-            const bool wide = s.nodes > a.tile_nodes;
+            const bool wide = kLanes == 2 && s.nodes > a.tile_nodes;
             const bool split = kLanes == 2 && !wide;  // the lanes share the rows
-            const bool two_parts = !(kLanes == 2 && wide) || a.out_dtype == 2;
-            const int T = s.t1 - s.t0, ahead = kLanes == 1 || wide ? 1 : min(2, T);
+            const bool two_parts = !wide || a.out_dtype == 2;
+            const int T = s.t1 - s.t0, ahead = wide ? 1 : min(2, T);
+            const int U = wide ? 2 * T : T;  // score buffers
             // wide: lane A's tile is full, lane B has the rest
             const int rows = (!wide ? s.nodes : x == 0 ? a.tile_nodes : s.nodes - a.tile_nodes) * gu;
             const bool row_ok = r < rows, warp_ok = w4 * 32 < rows;  // warp_ok: uniform
-            // (recomputed from the segment where they are needed: the key loop's registers hold a row of scores)
+            // (recomputed from the segment where they are needed)
             auto row_node = [&]() -> int { return s.node0 + (s.nodes > a.tile_nodes ? x * a.tile_nodes : 0) + r / gu; };
             auto mask_row = [&]() -> const uint32_t * {
                 return a.tree_mask + (size_t)(s.q0 + row_node()) * a.mask_words;
             };
             float m = -INFINITY, l = 0.f;
             bool ok = true;
-            for (int j = split ? x : 0; j < T; j += split ? 2 : 1, ++ns) {
-                const int start = (s.t0 + j) * kBN;
-                const int j0 = start - (s.len - s.n);  // tree index of the tile's first key (negative: context)
-                const bool tail = j0 + kBN > 0;        // drafted tokens (or the end) in this tile
-                uint32_t vis[kBN / 32];
-                if (tail) {
-#pragma unroll
-                    for (int i = 0; i < kBN / 32; ++i) vis[i] = 0u;
-                    if (row_ok) {
-                        const uint32_t *mrow = mask_row();
-                        const int w0 = j0 >> 5;
-                        uint32_t lo = mask_word(mrow, w0, s.n);
-#pragma unroll
-                        for (int i = 0; i < kBN / 32; ++i) {
-                            const uint32_t hi = mask_word(mrow, w0 + i + 1, s.n);
-                            vis[i] = __funnelshift_r(lo, hi, j0 & 31);
-                            lo = hi;
-                        }
-                    }
+            for (int u = 0; u < U; ++u) {
+                const uint32_t g = g0 + (uint32_t)u, i = g & 1u;
+                const int half = kLanes == 1 ? 0 : wide ? u & 1 : x, j = wide ? u >> 1 : u;
+                const int start = (s.t0 + j) * kBN + half * kSub;
+                const int j0 = start - (s.len - s.n);  // tree index of the buffer's first key (negative: context)
+                const bool tail = j0 + kSub > 0;       // drafted tokens (or the end) among its keys
+                const uint32_t tS = tmem + 128u * i + 64u * x + lane_base;
+                uint32_t vis[2] = {0u, 0u};
+                if (tail && row_ok) {
+                    const uint32_t *mrow = mask_row();
+                    const int w0 = j0 >> 5;
+                    const uint32_t a0 = mask_word(mrow, w0, s.n), a1 = mask_word(mrow, w0 + 1, s.n),
+                                   a2 = mask_word(mrow, w0 + 2, s.n);
+                    vis[0] = __funnelshift_r(a0, a1, j0 & 31);
+                    vis[1] = __funnelshift_r(a1, a2, j0 & 31);
                 }
-                if (!(ok = mbar_wait(&s_full[x], ns & 1u, abort_flag, a.err))) break;
+                if (!(ok = mbar_wait(&s_full[i], (g >> 1) & 1u, abort_flag, a.err))) break;
                 tc::fence_after_sync();
                 if (warp_ok) {
-                    float v[kBN];
-#pragma unroll
-                    for (int cc = 0; cc < kBN / 32; ++cc)
-                        tc::tmem_ld32(tS + cc * 32, *reinterpret_cast<float(*)[32]>(&v[cc * 32]));
+                    float v[kSub];
+                    tc::tmem_ld32(tS, *reinterpret_cast<float(*)[32]>(&v[0]));
+                    tc::tmem_ld32(tS + 32, *reinterpret_cast<float(*)[32]>(&v[32]));
                     tc::tmem_wait_ld();
                     if (tail) {
 #pragma unroll
-                        for (int i = 0; i < kBN; ++i) v[i] = (vis[i / 32] >> (i % 32)) & 1u ? v[i] : -INFINITY;
+                        for (int k = 0; k < kSub; ++k) v[k] = (vis[k / 32] >> (k % 32)) & 1u ? v[k] : -INFINITY;
                     }
                     float m8[8];
 #pragma unroll
                     for (int q = 0; q < 8; ++q) m8[q] = fmax3(v[q], v[q + 8], v[q + 16]);
 #pragma unroll
-                    for (int i = 24; i < kBN; i += 16)
+                    for (int k = 24; k < kSub; k += 16)
 #pragma unroll
                         for (int q = 0; q < 8; ++q)
-                            m8[q] = fmax3(m8[q], v[i + q], (i + 8 + q < kBN) ? v[i + 8 + q] : -INFINITY);
+                            m8[q] = fmax3(m8[q], v[k + q], (k + 8 + q < kSub) ? v[k + 8 + q] : -INFINITY);
                     const float mx = fmaxf(fmax3(m8[0], m8[1], m8[2]), fmax3(fmax3(m8[3], m8[4], m8[5]), m8[6], m8[7]));
                     const float m_new = fmaxf(m, mx * c2);
                     const bool grow = m_new > m + kRescaleLog2;  // false while the row has seen nothing
@@ -577,24 +591,12 @@ __global__ void __launch_bounds__(TreeLayout<D>::kThreads, 1)
                         m = m_new;
                         l *= alpha;
                     }
-                    // O of the lane's earlier tiles (its last P V was issued before this S: done)
-                    if (j >= (split ? 2 : 1) && __any_sync(0xffffffffu, grow)) {
-#pragma unroll
-                        for (int cc = 0; cc < D / 32; ++cc) {
-                            float o[32];
-                            tc::tmem_ld32(tO + cc * 32, o);
-                            tc::tmem_wait_ld();
-#pragma unroll
-                            for (int i = 0; i < 32; ++i) o[i] *= alpha;
-                            tc::tmem_st32(tO + cc * 32, o);
-                        }
-                    }
                     const float base = m == -INFINITY ? 0.f : m;  // a row that has seen nothing: ex2(-inf - 0) = 0
                     const float2 cc2 = make_float2(c2, c2), nm2 = make_float2(-base, -base);
                     float2 l4[4] = {make_float2(0.f, 0.f), make_float2(0.f, 0.f), make_float2(0.f, 0.f),
                                     make_float2(0.f, 0.f)};
 #pragma unroll
-                    for (int cc = 0; cc < kBN / 32; ++cc) {
+                    for (int cc = 0; cc < kSub / 32; ++cc) {
                         // P over the chunk's own scores: 16 columns of roundings, 16 of remainders
                         uint32_t ph[16];
 #pragma unroll
@@ -616,22 +618,42 @@ __global__ void __launch_bounds__(TreeLayout<D>::kThreads, 1)
                     }
                     const float2 ls = fadd2(fadd2(l4[0], l4[1]), fadd2(l4[2], l4[3]));
                     l += ls.x + ls.y;
+                    // O of the lane's earlier keys, once their last P V is done: it was issued before the next
+                    // buffer's Q K, so that buffer's barrier says so (it waits for no P of this one)
+                    if (u > 0 && __any_sync(0xffffffffu, grow)) {
+                        uint64_t *bar = u + 1 < U ? &s_full[i ^ 1u] : pv_late;
+                        if (!(ok = mbar_wait(bar, u + 1 < U ? ((g + 1u) >> 1) & 1u : n_late & 1u, abort_flag, a.err))) break;
+                        tc::fence_after_sync();
+#pragma unroll 1
+                        for (int cc = 0; cc < D / 32; ++cc) {
+                            float o[32];
+                            tc::tmem_ld32(tO + cc * 32, o);
+                            tc::tmem_wait_ld();
+#pragma unroll
+                            for (int k = 0; k < 32; ++k) o[k] *= alpha;
+                            tc::tmem_st32(tO + cc * 32, o);
+                        }
+                    }
                 }
-                // V of drafted tokens and beyond the end: zero what is past the end, sweep the drafted rows
-                if (tail && (split || x == 0)) {
+                // V of drafted tokens and beyond the end: zero what is past the end, sweep the drafted rows. A
+                // narrow lane does its half of the tile, lane A of a wide block all of it with the first half
+                // (its products come before lane B's).
+                const int tile_j0 = j0 - half * kSub;  // tree index of the tile's first key
+                if (wide ? x == 0 && half == 0 && tile_j0 + kBN > 0 : tail) {
                     const uint32_t vi = item + j + min(T, ahead + j);
                     if (!(ok = mbar_wait(&kv_full[vi % ring], (vi / ring) & 1u, abort_flag, a.err))) break;
                     uint8_t *const sV = sRing + (vi % ring) * L::kTileBytes;
-                    const int n_valid = min(kBN, s.len - start);
+                    const int n_valid = min(kBN, s.len - (s.t0 + j) * kBN);
+                    const int row0 = wide ? 0 : half * kSub, row1 = wide ? kBN : row0 + kSub;
                     bool bad = false;
                     // 8 lanes a row (128 bytes of a 64-column half), 4 rows a warp and step
-                    for (int row = max(0, -j0) / 16 * 16 + w4 * 4 + (lane >> 3); row < kBN; row += 16)
+                    for (int row = max(row0, -tile_j0 / 16 * 16) + w4 * 4 + (lane >> 3); row < row1; row += 16)
 #pragma unroll
                         for (int hf = 0; hf < L::kHalves; ++hf) {
                             uint4 *p = reinterpret_cast<uint4 *>(sV + hf * L::kTileHalf + (uint32_t)row * 128u + (lane & 7) * 16);
                             if (row >= n_valid) {
                                 *p = make_uint4(0, 0, 0, 0);
-                            } else if (row >= -j0) {
+                            } else if (row >= -tile_j0) {
                                 uint4 q = *p;
                                 if (nonfinite_pair<BF16>(q.x) || nonfinite_pair<BF16>(q.y) || nonfinite_pair<BF16>(q.z) ||
                                     nonfinite_pair<BF16>(q.w)) {
@@ -648,9 +670,11 @@ __global__ void __launch_bounds__(TreeLayout<D>::kThreads, 1)
                 tc::tmem_wait_st();
                 tc::fence_before_sync();
                 __syncwarp();
-                if (lane == 0) mbar_arrive(&p_full[x]);
+                if (lane == 0) mbar_arrive(&p_full[i]);
             }
             if (!ok) break;
+            g0 += (uint32_t)U;
+            if (U > 1) ++n_late;
             // ---- output of the segment ----
             // rows shared by the lanes: rows 0-63 are finished by lane A, 64-127 by lane B
             const bool mine = !split || (w4 >> 1) == x;
@@ -718,7 +742,6 @@ __global__ void __launch_bounds__(TreeLayout<D>::kThreads, 1)
                         float p[32];
                         tc::tmem_ld32(tOa + 128u + cc * 32, p);
                         tc::tmem_wait_ld();
-                        // a lane without a tile left its output as it was: not read
 #pragma unroll
                         for (int i = 0; i < 32; ++i) o[i] = (fa == 0.f ? 0.f : o[i] * fa) + (fb == 0.f ? 0.f : p[i] * fb);
                     } else {
