@@ -25,8 +25,7 @@
 // ends, and a CTA leaves at most two partial items, so the workspace does not grow with the batch. A merge
 // kernel joins the partials of each split item in the order of the keys (no atomics: the same result every time).
 //
-// Warps: 0 loads Q and the K / V tiles by TMA into a ring (a lane per page), 1 issues the MMAs and owns
-// TMEM, 2 walks the run and hands its segments to the others, the warpgroups of lanes A and B do softmax and
+// Warps: 0 loads Q and the K tiles, 3 the V tiles by TMA into a ring, 1 issues the MMAs and owns TMEM, 2 walks the run and hands its segments to the others, the warpgroups of lanes A and B do softmax and
 // output. P goes to the tensor cores as its 16-bit rounding plus the rounding's remainder (two products), so that it
 // is not a rounding to 16 bits -- but for wide blocks with a 16-bit output, which the tensor cores bound: there P is
 // rounded once, half a step of the output's own type (the prefill's choice too).
@@ -203,7 +202,7 @@ __global__ void __launch_bounds__(TreeLayout<D>::kThreads, 1)
         mbar_init(ml_full, kSoftmaxWarps);
         for (int i = 0; i < kSegs; ++i) {
             mbar_init(&seg_full[i], 1);
-            mbar_init(&seg_empty[i], 2 + kSoftmaxWarps);  // producer, MMA, softmax warps
+            mbar_init(&seg_empty[i], 3 + kSoftmaxWarps);  // producers, MMA, softmax warps
         }
         mbar_init(drain, 1);
         *s_total = 0;
@@ -246,17 +245,23 @@ __global__ void __launch_bounds__(TreeLayout<D>::kThreads, 1)
 
     if (warp < 4) {
         if constexpr (kLanes == 2) tc::regs_dec<72>();
-        if (warp == 0) {
-            // ==================================== TMA producer ====================================
+        if (warp == 0 || warp == 3) {
+            // ======================= TMA producers: Q and the K tiles (warp 0), the V tiles (warp 3) =======================
+            // Two warps, since issuing the boxes of a tile's pages takes about 50 cycles a box: at 16 tokens a page one
+            // warp spent 1300 cycles an item, which bounded the kernel. Page ids are read 32 at a time, one window ahead.
+            const int kv = warp == 0 ? 0 : 1;
             const int bs = a.cache.block_size, lbs = a.cache.log2_block_size;
             const int box_rows = bs < kBN ? bs : kBN;
             const uint64_t pol = l2_policy_evict_first();
-            if (lane == 0) {
-                tc::prefetch_tensormap(&tm_q);
+            if (tc::elect_one()) {
+                if (kv == 0) tc::prefetch_tensormap(&tm_q);
                 tc::prefetch_tensormap(&tm_kv);
             }
             uint32_t qn = 0;
-            uint32_t slot = 0, ph = 1, landing = 0;  // ring position and what to find on kv_empty; items issued (at most ring)
+            uint32_t base = 0, base_ph = 1;  // ring slot of the segment's first item, and the parity to find on kv_empty
+            uint32_t slot = 0, ph = 1;
+            uint32_t used = 0, par = 0;  // slots this warp has loaded into, and the parity of each one's last load
+            uint32_t items = 0;          // items of the run, up to ring
             bool ok = true;
             for (; (ok = next_segment()); ++seg_i) {
                 const Segment s = segs[seg_i % kSegs];
@@ -264,84 +269,96 @@ __global__ void __launch_bounds__(TreeLayout<D>::kThreads, 1)
                 const int T = s.t1 - s.t0, ahead = wide ? 1 : min(2, T);
                 const int kvh = s.unit / a.head_groups;
                 const int *bt = a.block_tables + (size_t)s.b * a.max_blocks_per_seq;
-                // Q: the block's nodes, gu heads each, one box per tile and 64 columns
-                if (!(ok = mbar_wait(q_empty, (qn & 1u) ^ 1u, abort_flag, a.err))) break;
-                if (lane == 0) {
-                    const int tiles = wide ? 2 : 1;
-                    mbar_arrive_expect_tx(q_full, (uint32_t)tiles * a.tile_nodes * gu * 128u * L::kHalves);
-                    for (int x = 0; x < tiles; ++x)
-#pragma unroll
-                        for (int hf = 0; hf < L::kHalves; ++hf)
-                            tc::tma_load_3d(sQ + x * L::kQBytes + hf * L::kQHalf, &tm_q, hf * 64, s.unit * gu,
-                                            s.q0 + s.node0 + x * a.tile_nodes, q_full);
-                }
-                ++qn;
-                // ring order = the order of use: K of the first `ahead` tiles, then V_j, K_{j + ahead}, and the
-                // last V: item n is tile j's K (kv 0) or V (kv 1)
-                auto tile_of = [&](int n, int &kv) -> int {
-                    if (n < ahead) {
-                        kv = 0;
-                        return n;
-                    }
-                    if (n >= 2 * T - ahead) {
-                        kv = 1;
-                        return n - T;
-                    }
-                    kv = (n - ahead) & 1 ? 0 : 1;
-                    return ((n - ahead) >> 1) + (kv ? 0 : ahead);
-                };
-                // pages of tile j: tile rows of the page, lane by lane
-                auto page_count = [&](int j) -> int {
-                    const int n = min(kBN, s.len - (s.t0 + j) * kBN);
-                    return bs < kBN ? (n + bs - 1) >> lbs : 1;
-                };
-                auto page_id = [&](int j) -> int {
-                    return lane < page_count(j) ? __ldg(bt + (((s.t0 + j) * kBN) >> lbs) + lane) : 0;
-                };
-                int kv = 0;
-                int pb_next = page_id(0);
-                for (int n = 0; n < 2 * T; ++n) {
-                    const int j = tile_of(n, kv);
-                    int pb = pb_next;  // loaded while the last item went out
-                    if (n + 1 < 2 * T) {
-                        int kv1;
-                        pb_next = page_id(tile_of(n + 1, kv1));
-                    }
-                    const int start = (s.t0 + j) * kBN, npages = page_count(j);
-                    const int off = bs < kBN ? 0 : (start & (bs - 1));
-                    if (!(ok = mbar_wait(&kv_empty[slot], ph, abort_flag, a.err))) break;
-                    if (lane == 0) mbar_arrive_expect_tx(&kv_full[slot], (uint32_t)npages * box_rows * 128u * L::kHalves);
-                    __syncwarp();
-                    if (lane < npages) {
+                const int last_page = (min(s.t1 * kBN, s.len) - 1) >> lbs;
+                // ids of pages first + lane (a tile's pages never straddle two windows)
+                auto window = [&](int first) -> int {
+                    int pb = 0;
+                    if (first + lane <= last_page) {
+                        pb = __ldg(bt + first + lane);
                         if (pb < 0 || pb >= a.cache.num_blocks) {
                             set_error(a.err, kErrDeviceRange);
                             pb = 0;
                         }
-                        const int row = ((pb * 2 + kv) * a.cache.num_kv_heads + kvh) * bs + off;
-                        uint8_t *dst = sRing + slot * L::kTileBytes + (uint32_t)lane * box_rows * 128u;
-#pragma unroll
-                        for (int hf = 0; hf < L::kHalves; ++hf)
-                            tc::tma_load_2d_hint(dst + hf * L::kTileHalf, &tm_kv, hf * 64, row, &kv_full[slot], pol);
                     }
-                    if (landing < ring) ++landing;
-                    if (++slot == ring) {
-                        slot = 0;
+                    return pb;
+                };
+                int first = (s.t0 * kBN) >> lbs;
+                int w0 = window(first), w1 = first + 32 <= last_page ? window(first + 32) : 0;
+                if (kv == 0) {
+                    // Q: the block's nodes, gu heads each, one box per tile and 64 columns
+                    if (!(ok = mbar_wait(q_empty, (qn & 1u) ^ 1u, abort_flag, a.err))) break;
+                    if (tc::elect_one()) {
+                        const int tiles = wide ? 2 : 1;
+                        mbar_arrive_expect_tx(q_full, (uint32_t)tiles * a.tile_nodes * gu * 128u * L::kHalves);
+                        for (int x = 0; x < tiles; ++x)
+#pragma unroll
+                            for (int hf = 0; hf < L::kHalves; ++hf)
+                                tc::tma_load_3d(sQ + x * L::kQBytes + hf * L::kQHalf, &tm_q, hf * 64, s.unit * gu,
+                                                s.q0 + s.node0 + x * a.tile_nodes, q_full);
+                    }
+                    ++qn;
+                }
+                // ring order = the order of use: K of the first `ahead` tiles, then V_j, K_{j + ahead}, and the last V
+                slot = base;
+                ph = base_ph;
+                auto step = [&](uint32_t n) {
+                    slot += n;
+                    if (slot >= ring) {
+                        slot -= ring;
                         ph ^= 1u;
                     }
+                };
+                if (kv) step((uint32_t)ahead);
+                for (int j = 0; j < T; ++j) {
+                    if (j > 0) step(kv ? (ahead + j <= T ? 2u : 1u) : (j < ahead ? 1u : 2u));
+                    const int start = (s.t0 + j) * kBN, page0 = start >> lbs;
+                    const int npages = bs < kBN ? (min(kBN, s.len - start) + bs - 1) >> lbs : 1;
+                    const int off = bs < kBN ? 0 : (start & (bs - 1));
+                    if (page0 >= first + 32) {
+                        first += 32;
+                        w0 = w1;
+                        if (first + 32 <= last_page) w1 = window(first + 32);
+                    }
+                    if (!(ok = mbar_wait(&kv_empty[slot], ph, abort_flag, a.err))) break;
+                    uint8_t *dst = sRing + slot * L::kTileBytes;
+                    if (tc::elect_one())
+                        mbar_arrive_expect_tx(&kv_full[slot], (uint32_t)npages * box_rows * 128u * L::kHalves);
+                    for (int pg = 0; pg < npages; ++pg, dst += (uint32_t)box_rows * 128u) {
+                        const int pb = __shfl_sync(0xffffffffu, w0, page0 - first + pg);
+                        const int row = ((pb * 2 + kv) * a.cache.num_kv_heads + kvh) * bs + off;
+                        if (tc::elect_one()) {
+#pragma unroll
+                            for (int hf = 0; hf < L::kHalves; ++hf)
+                                tc::tma_load_2d_hint(dst + hf * L::kTileHalf, &tm_kv, hf * 64, row, &kv_full[slot], pol);
+                        }
+                    }
+                    used |= 1u << slot;
+                    par = (par & ~(1u << slot)) | ((ph ^ 1u) << slot);
                 }
+                if (!ok) break;
+                items = min(ring, items + 2u * (uint32_t)T);
+                base += 2u * (uint32_t)T;
+                if ((base / ring) & 1u) base_ph ^= 1u;
+                base %= ring;
                 __syncwarp();
                 if (lane == 0) mbar_arrive(&seg_empty[seg_i % kSegs]);
-                if (!ok) break;
             }
-            // every copy has landed before the CTA exits (bounded), also when another role gave up
+            // Every copy lands before the CTA exits. At the end of the run warp 3, whose item is the last, waits for
+            // the last item of every slot; a warp that gave up in between waits for its own (a slot that the other
+            // one has loaded since shows another parity: a short limit).
             volatile int no_abort = 0;
-            for (uint32_t i = 0; i < landing; ++i) {  // backwards: a slot's last load has the parity that ph had then
-                if (slot == 0) {
-                    slot = ring;
-                    ph ^= 1u;
+            if (*abort_flag) {
+                for (uint32_t i = 0; i < ring; ++i)
+                    if ((used >> i) & 1u) mbar_wait(&kv_full[i], (par >> i) & 1u, &no_abort, nullptr, 10000000ull);
+            } else if (kv == 1) {
+                for (; items > 0; --items) {
+                    if (base == 0) {
+                        base = ring;
+                        base_ph ^= 1u;
+                    }
+                    --base;
+                    mbar_wait(&kv_full[base], base_ph ^ 1u, &no_abort, nullptr);
                 }
-                --slot;
-                mbar_wait(&kv_full[slot], ph ^ 1u, &no_abort, nullptr);
             }
             if (qn > 0) mbar_wait(q_full, (qn - 1) & 1u, &no_abort, nullptr);
         } else if (warp == 1) {
