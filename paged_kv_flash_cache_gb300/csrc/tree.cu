@@ -372,88 +372,116 @@ __global__ void __launch_bounds__(TreeLayout<D>::kThreads, 1)
                 const uint64_t dK0 = tc::smem_desc(aRing, 16, 1024), dQ0 = tc::smem_desc(aQ, 16, 1024);
                 const uint64_t dV0 = tc::smem_desc(aRing, L::kTileHalf, 1024);
                 uint32_t slot = 0, ph = 0;  // ring position
-                uint32_t g0 = 0;            // score buffers that each lane used before this segment
-                // the ring item `ahead` items on: its slot, and the parity that says it has landed
-                auto at = [&](uint32_t n, uint32_t &sl, uint32_t &par) {
-                    sl = slot + n;
-                    par = ph;
-                    if (sl >= ring) {
-                        sl -= ring;
-                        par ^= 1u;
+                uint32_t g = 0;             // score buffers that each lane has used
+                auto advance = [&]() {
+                    if (++slot == ring) {
+                        slot = 0;
+                        ph ^= 1u;
                     }
                 };
-                auto advance = [&](uint32_t n) { at(n, slot, ph); };
+                // score buffer i: the lanes' Q K of the K tile in ring slot sl. Wide: 64 of its keys (`half`) for each
+                // lane's rows; else the tile's keys for the one set of rows, the halves of 128 landing in the lanes'
+                // (neighbouring) buffers.
+                auto qk = [&](bool wide, uint32_t sl, uint32_t half, uint32_t i) {
+                    uint64_t dK = dK0 + sl * (L::kTileBytes >> 4) + half * (kSub * 128 >> 4), dQ = dQ0;
+                    const uint32_t idesc = wide ? id_sub : id_tile;
+                    uint32_t tS = tmem + 128u * i;
+#pragma unroll 1
+                    for (int x = 0; x < (wide ? 2 : 1); ++x, dQ += L::kQBytes >> 4, tS += 64u)
+#pragma unroll
+                        for (int kk = 0; kk < D / 16; ++kk)
+                            tc::mma_f16_ss(tS, dQ + (((kk >> 2) * L::kQHalf + (kk & 3) * 32u) >> 4),
+                                           dK + (((kk >> 2) * L::kTileHalf + (kk & 3) * 32u) >> 4), idesc, kk > 0 ? 1u : 0u);
+                    tc::mma_commit(&s_full[i]);
+                };
+                // O (+)= P V of score buffer i: the V tile in ring slot sl, wide: its 64 keys `half` for both lanes, else
+                // a half for each lane. 16 keys a step: 8 columns of P in their 32-column chunk, the remainders 16 behind.
+                auto pv = [&](bool wide, bool two_parts, uint32_t sl, uint32_t half, uint32_t i, bool first) {
+                    uint64_t dV = dV0 + sl * (L::kTileBytes >> 4) + half * (kSub * 128 >> 4);
+                    uint32_t tO = tmem + L::kColO, tP = tmem + 128u * i;
+#pragma unroll 1
+                    for (int x = 0; x < kLanes; ++x, tO += 128u, tP += 64u) {
+                        if (two_parts) {
+#pragma unroll
+                            for (int kk = 0; kk < kSub / 16; ++kk) {
+                                const uint32_t tPk = tP + 32u * (kk >> 1) + 8u * (kk & 1);
+                                const uint64_t dVk = dV + (uint32_t)(kk * 2048 >> 4);
+                                tc::mma_f16_ts(tO, tPk, dVk, id_pv, (first && kk == 0) ? 0u : 1u);
+                                tc::mma_f16_ts(tO, tPk + 16u, dVk, id_pv, 1u);
+                            }
+                        } else {
+#pragma unroll
+                            for (int kk = 0; kk < kSub / 16; ++kk)
+                                tc::mma_f16_ts(tO, tP + 32u * (kk >> 1) + 8u * (kk & 1), dV + (uint32_t)(kk * 2048 >> 4), id_pv,
+                                               (first && kk == 0) ? 0u : 1u);
+                        }
+                        if (!wide) dV += kSub * 128 >> 4;
+                    }
+                };
+                auto wait = [&](uint64_t *bar, uint32_t par) { return mbar_wait(bar, par, abort_flag, a.err); };
                 bool ok = true;
                 for (; (ok = next_segment()); ++seg_i) {
                     const Segment &s = segs[seg_i % kSegs];
                     const int T = s.t1 - s.t0;
-                    // A lane's work is U score buffers: wide, both halves of every tile (buffer u: half u % 2 of tile
-                    // u / 2); narrow, its half of every tile (the one lane of head_dim 256: the tile). Step u: each
-                    // lane's Q K of buffer u + 1, then its P V of buffer u; u = -1: the first Q K. The ring holds the
-                    // tiles in this order of use: wide K_0, V_0, K_1, V_1 ..., else K_0, K_1, V_0, K_2, V_1 ...
+                    // A lane's work is U score buffers: wide, both halves of every tile; else a tile each. Step u: Q K of
+                    // buffer u + 1, then P V of buffer u. (A buffer's Q K follows its last P V in issue order.) The ring
+                    // holds the tiles in this order of use: wide K_0, V_0, K_1, V_1 ..., else K_0, K_1, V_0, K_2, V_1 ...
                     const bool wide = kLanes == 2 && s.nodes > a.tile_nodes;
-                    const bool two_parts = !wide || a.out_dtype == 2;
-                    const int U = wide ? 2 * T : T;
-                    if (!(ok = mbar_wait(q_full, seg_i & 1u, abort_flag, a.err))) break;
+                    if (!(ok = wait(q_full, seg_i & 1u))) break;
                     tc::fence_after_sync();
-                    for (int u = -1; ok && u < U; ++u) {
-                        const bool more = u + 1 < U, odd = u & 1;
-                        // ring items from the position on: this step's K and V, and how many the step uses up
-                        const uint32_t k_at = wide && odd && u > 0 ? 2 : 0;
-                        const uint32_t v_at = wide ? 1 : more ? 1 : 0;
-                        const uint32_t used = wide ? (odd && u > 0 ? 2 : 0) : (more ? 1 : 0) + (u >= 0 ? 1 : 0);
-                        uint32_t k_slot, k_par, v_slot, v_par;
-                        at(k_at, k_slot, k_par);
-                        at(v_at, v_slot, v_par);
-                        const uint32_t g = g0 + (uint32_t)u;  // buffer u of the lanes: score buffer g % 2
-                        if (more) {
-                            // (the buffer's last P V was issued a step ago: in order)
-                            if (!(ok = mbar_wait(&kv_full[k_slot], k_par, abort_flag, a.err))) break;
-                            const uint32_t i = (g + 1u) & 1u;
-                            // wide: a product of 64 keys for each lane's rows; narrow: one of the tile's 128 keys, whose
-                            // two halves land in the lanes' (neighbouring) buffers
-                            const uint32_t idesc = wide ? id_sub : id_tile;
-                            uint64_t dK = dK0 + k_slot * (L::kTileBytes >> 4), dQ = dQ0;
-                            if (wide) dK += (uint32_t)((u + 1) & 1) * (kSub * 128 >> 4);
-#pragma unroll 1
-                            for (int x = 0; x < (wide ? 2 : 1); ++x, dQ += L::kQBytes >> 4)
-#pragma unroll
-                                for (int kk = 0; kk < D / 16; ++kk)
-                                    tc::mma_f16_ss(tmem + 128u * i + 64u * x, dQ + (((kk >> 2) * L::kQHalf + (kk & 3) * 32u) >> 4),
-                                                   dK + (((kk >> 2) * L::kTileHalf + (kk & 3) * 32u) >> 4), idesc,
-                                                   kk > 0 ? 1u : 0u);
-                            tc::mma_commit(&s_full[i]);
-                            if (!wide || !odd) tc::mma_commit(&kv_empty[k_slot]);
-                            if (u + 2 == U) tc::mma_commit(q_empty);  // the segment's last Q K
-                        }
-                        if (u >= 0) {
-                            const uint32_t i = g & 1u;
-                            if (!(ok = mbar_wait(&kv_full[v_slot], v_par, abort_flag, a.err))) break;
+                    if (wide) {
+                        const bool two_parts = a.out_dtype == 2;
+                        if (!(ok = wait(&kv_full[slot], ph))) break;
+                        qk(true, slot, 0, g & 1u);
+                        for (int j = 0; j < T; ++j) {
+                            // buffers 2 j (the tile's first half), 2 j + 1
+                            qk(true, slot, 1, (g + 1u) & 1u);
+                            tc::mma_commit(&kv_empty[slot]);
+                            if (j == T - 1) tc::mma_commit(q_empty);  // the segment's last Q K
+                            advance();
+                            if (!(ok = wait(&kv_full[slot], ph) && wait(&p_full[g & 1u], (g >> 1) & 1u))) break;
                             // a segment's first P V overwrites an output: the last segment's must be read
-                            if (u == 0 && !(ok = mbar_wait(o_empty, (seg_i & 1u) ^ 1u, abort_flag, a.err))) break;
-                            if (!(ok = mbar_wait(&p_full[i], (g >> 1) & 1u, abort_flag, a.err))) break;
+                            if (j == 0 && !(ok = wait(o_empty, (seg_i & 1u) ^ 1u))) break;
                             tc::fence_after_sync();
-                            uint64_t dV = dV0 + v_slot * (L::kTileBytes >> 4);
-                            if (wide) dV += (uint32_t)odd * (kSub * 128 >> 4);
-#pragma unroll 1
-                            for (int x = 0; x < kLanes; ++x) {
-                                const uint32_t tO = tmem + L::kColO + 128u * x, tP = tmem + 128u * i + 64u * x;
-                                // 16 keys a step: 8 columns of P in their 32-column chunk, the remainders 16 behind
-#pragma unroll
-                                for (int kk = 0; kk < kSub / 16; ++kk) {
-                                    const uint32_t tPk = tP + 32u * (kk >> 1) + 8u * (kk & 1);
-                                    const uint64_t dVk = dV + (uint32_t)(kk * 2048 >> 4);
-                                    tc::mma_f16_ts(tO, tPk, dVk, id_pv, (u == 0 && kk == 0) ? 0u : 1u);
-                                    if (two_parts) tc::mma_f16_ts(tO, tPk + 16u, dVk, id_pv, 1u);
-                                }
-                                if (!wide) dV += kSub * 128 >> 4;
+                            pv(true, two_parts, slot, 0, g & 1u, j == 0);
+                            const uint32_t v_slot = slot;
+                            advance();
+                            if (j + 1 < T) {
+                                if (!(ok = wait(&kv_full[slot], ph))) break;
+                                qk(true, slot, 0, g & 1u);
+                            } else {
+                                tc::mma_commit(pv_late);
                             }
-                            if (u == U - 2) tc::mma_commit(pv_late);
-                            if (!wide || odd) tc::mma_commit(&kv_empty[v_slot]);
+                            ++g;
+                            if (!(ok = wait(&p_full[g & 1u], (g >> 1) & 1u))) break;
+                            tc::fence_after_sync();
+                            pv(true, two_parts, v_slot, 1, g & 1u, false);
+                            tc::mma_commit(&kv_empty[v_slot]);
+                            ++g;
                         }
-                        advance(used);
+                    } else {
+                        if (!(ok = wait(&kv_full[slot], ph))) break;
+                        qk(false, slot, 0, g & 1u);
+                        tc::mma_commit(&kv_empty[slot]);
+                        if (T == 1) tc::mma_commit(q_empty);
+                        advance();
+                        for (int j = 0; j < T; ++j, ++g) {
+                            if (j + 1 < T) {
+                                if (!(ok = wait(&kv_full[slot], ph))) break;
+                                qk(false, slot, 0, (g + 1u) & 1u);
+                                tc::mma_commit(&kv_empty[slot]);
+                                if (j + 2 == T) tc::mma_commit(q_empty);
+                                advance();
+                            }
+                            if (!(ok = wait(&kv_full[slot], ph) && wait(&p_full[g & 1u], (g >> 1) & 1u))) break;
+                            if (j == 0 && !(ok = wait(o_empty, (seg_i & 1u) ^ 1u))) break;
+                            tc::fence_after_sync();
+                            pv(false, true, slot, 0, g & 1u, j == 0);
+                            tc::mma_commit(&kv_empty[slot]);
+                            if (j + 2 == T) tc::mma_commit(pv_late);
+                            advance();
+                        }
                     }
-                    g0 += (uint32_t)U;
                     if (!ok) break;
                     tc::mma_commit(o_done);
                     mbar_arrive(&seg_empty[seg_i % kSegs]);
@@ -836,25 +864,48 @@ __global__ void __launch_bounds__(TreeLayout<D>::kThreads, 1)
 }
 
 // The partials of the item that begins in run blockIdx.x and is split: run c0's partial 1, then partial 0
-// of the runs behind it. A warp per row: weights 2^(lse_i - max), out = sum w o / sum w.
+// of the runs behind it. A warp per row: weights 2^(lse_i - max), out = sum w o / sum w, in the order of the keys. Bound:
+// latency (three dependent reads), so that a row's first partials are read along with their lse.
 template <int D>
 __global__ void __launch_bounds__(256) tree_merge_kernel(TreeArgs a) {
     constexpr int V = D / 32;
+    constexpr int kFlight = D == 256 ? 4 : 8;  // rows in flight
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     pdl_wait();
     const MergeItem it = a.merge[blockIdx.x];
     const int rows = it.nodes * a.unit_heads;
-    for (int r = blockIdx.y * 8 + warp; r < rows; r += gridDim.y * 8) {
+    const int r = blockIdx.y * 8 + warp;
+    if (r < rows) {
         // rows of a wide block: lane B's start at row 128 of the partial
         const int node = r / a.unit_heads, head = r - node * a.unit_heads;
         const int pr = node < a.tile_nodes ? r : kBM + r - a.tile_nodes * a.unit_heads;
         auto prow = [&](int i) { return ((size_t)(blockIdx.x + i) * 2 + (i == 0 ? 1 : 0)) * a.part_rows + pr; };
-        float M = -INFINITY;
-        bool nan = false;
-        for (int i = lane; i < it.parts; i += 32) {
-            const float x = __ldcg(a.part_lse + prow(i));
-            nan |= x != x;
-            M = fmaxf(M, x);
+        float y[kFlight][V];
+        auto read = [&](int k0, int n) {
+#pragma unroll
+            for (int f = 0; f < kFlight; ++f)
+                if (f < n) {
+                    const float *p = a.part_o + prow(k0 + f) * D + V * lane;
+                    if constexpr (V == 2) {
+                        const float2 q = __ldcg(reinterpret_cast<const float2 *>(p));
+                        y[f][0] = q.x, y[f][1] = q.y;
+                    } else {
+#pragma unroll
+                        for (int c = 0; c < V / 4; ++c) {
+                            const float4 q = __ldcg(reinterpret_cast<const float4 *>(p) + c);
+                            y[f][4 * c] = q.x, y[f][4 * c + 1] = q.y, y[f][4 * c + 2] = q.z, y[f][4 * c + 3] = q.w;
+                        }
+                    }
+                }
+        };
+        read(0, it.parts);
+        float x = lane < it.parts ? __ldcg(a.part_lse + prow(lane)) : -INFINITY;
+        float M = x;
+        bool nan = x != x;
+        for (int i = lane + 32; i < it.parts; i += 32) {
+            const float z = __ldcg(a.part_lse + prow(i));
+            nan |= z != z;
+            M = fmaxf(M, z);
         }
 #pragma unroll
         for (int o = 16; o > 0; o >>= 1) M = fmaxf(M, __shfl_xor_sync(0xffffffffu, M, o));
@@ -862,30 +913,14 @@ __global__ void __launch_bounds__(256) tree_merge_kernel(TreeArgs a) {
         float acc[V], sum = 0.f;
 #pragma unroll
         for (int v = 0; v < V; ++v) acc[v] = 0.f;
-        // 32 partials at a time: lane i holds the weight of partial i; kFlight rows in flight
-        constexpr int kFlight = D == 256 ? 4 : 8;
+        // 32 partials at a time: lane i holds the weight of partial i
         for (int i0 = 0; i0 < it.parts; i0 += 32) {
             const int n = min(32, it.parts - i0);
-            const float x = lane < n ? __ldcg(a.part_lse + prow(i0 + lane)) : -INFINITY;
+            if (i0 > 0) x = lane < n ? __ldcg(a.part_lse + prow(i0 + lane)) : -INFINITY;
             const float w_l = x == -INFINITY ? 0.f : ex2f(x - M);
             sum += w_l;
             for (int k = 0; k < n; k += kFlight) {
-                float y[kFlight][V];
-#pragma unroll
-                for (int f = 0; f < kFlight; ++f)
-                    if (k + f < n) {
-                        const float *p = a.part_o + prow(i0 + k + f) * D + V * lane;
-                        if constexpr (V == 2) {
-                            const float2 q = __ldcg(reinterpret_cast<const float2 *>(p));
-                            y[f][0] = q.x, y[f][1] = q.y;
-                        } else {
-#pragma unroll
-                            for (int g = 0; g < V / 4; ++g) {
-                                const float4 q = __ldcg(reinterpret_cast<const float4 *>(p) + g);
-                                y[f][4 * g] = q.x, y[f][4 * g + 1] = q.y, y[f][4 * g + 2] = q.z, y[f][4 * g + 3] = q.w;
-                            }
-                        }
-                    }
+                if (i0 + k > 0) read(i0 + k, n - k);
 #pragma unroll
                 for (int f = 0; f < kFlight; ++f) {
                     if (k + f >= n) break;
@@ -927,7 +962,7 @@ cudaError_t launch_tree_t(const TreeArgs &a, int grid, cudaStream_t s) {
     }
     e = launch_pdl(kern, dim3(grid), dim3(L::kThreads), L::kSmem, s, tm_q, tm_kv, a);
     if (e != cudaSuccess) return e;
-    return launch_pdl(tree_merge_kernel<D>, dim3(grid, 8), dim3(256), 0, s, a);
+    return launch_pdl(tree_merge_kernel<D>, dim3(grid, (a.block_nodes * a.unit_heads + 7) / 8), dim3(256), 0, s, a);
 }
 
 }  // namespace
