@@ -9,10 +9,16 @@
 // if src_j = dst_k >= dst_j, so j <= k -- a row written is never one that a later row still reads.
 //
 // Pure bandwidth: each moved row is read once and written once. A slice is one (sequence, K or V,
-// head) and a column part of its rows; slices touch disjoint bytes, so they run as independent CTAs.
-// Inside a slice the CTA moves chunks of kUnroll x (256 / VP) rows in order: the loads of chunk c + 1
-// are issued before the stores of chunk c, with one barrier between a chunk's loads and its stores
-// (a store of chunk c can only meet a source of chunk c or earlier, whose loads precede the barrier).
+// head); slices touch disjoint rows. A group of threads moves a slice's rows chunk by chunk, kUnroll 16-byte
+// vectors a thread: the rows' places are looked up a chunk ahead, a thread a row, into shared memory, so that the
+// moves themselves wait for one read only; a barrier stands between a chunk's loads and its stores (a
+// store of chunk c can only meet a source of chunk c or earlier, whose loads precede the barrier).
+//   few rows   a warp a slice;
+//   more       `shares` CTAs a slice, each moving an equal piece of its rows. Pieces are independent
+//              when no row's source lies in a later piece's destinations (a window moved up behind a prompt); every CTA of the slice looks the list over and finds the same answer. Otherwise the rows go in
+//              order and the CTAs take a share of each row's columns instead, as far as 64 bytes a share.
+// 8 x 8192 rows of 8 heads x 128 (537 MB read and written): 242 us with column shares only (64 bytes of a row at
+// different times), 147 us with pieces and each vector's thread looking its row up, 97 us (82% of the copy rate) as it is.
 #include "pkv_device.cuh"
 #include "pkv_internal.h"
 
@@ -20,15 +26,10 @@ namespace pkv {
 namespace {
 
 constexpr int kCompactThreads = 256;
-constexpr int kUnroll = 4;
-
-// The rows of one chunk held by a thread: a 16-byte vector and, from the first thread of a row's
-// part 0 over an FP8 cache, the row's scale; dst < 0: nothing to store.
-struct Chunk {
-    uint4 v[kUnroll];
-    float sc[kUnroll];
-    long long dst[kUnroll];
-};
+constexpr int kUnroll = 8;
+constexpr int kResident = 3;  // CTAs an SM (registers)
+// Rows are counted in 32 bits: 2^32 rows of the shortest, 64 bytes, are more than the memory holds.
+constexpr uint32_t kNoRow = 0xffffffffu;  // nothing to move
 
 __device__ __forceinline__ uint4 ld_once(const uint4 *p) {
     uint4 v;
@@ -39,78 +40,135 @@ __device__ __forceinline__ uint4 ld_once(const uint4 *p) {
     return v;
 }
 
-// VP: 16-byte vectors of a row that the CTA moves (a power of two; the row's vectors / VP parts).
-template <int VP>
-__global__ void __launch_bounds__(kCompactThreads) compact_kernel(CompactArgs a) {
-    constexpr int kRows = kCompactThreads / VP;
-    const int e = threadIdx.x % VP, tr = threadIdx.x / VP;
+// kGroup threads (a warp, or the CTA) a slice.
+template <int kGroup>
+__global__ void __launch_bounds__(kCompactThreads, kResident) compact_kernel(CompactArgs a) {
+    constexpr int kGroups = kCompactThreads / kGroup;
+    // a chunk's source and destination rows, three chunks in turn: kUnroll * kGroup vectors are at most 2 * kGroup rows
+    __shared__ uint32_t s_src[3][2 * kCompactThreads], s_dst[3][2 * kCompactThreads];
+    const int tid = threadIdx.x % kGroup, s0 = threadIdx.x / kGroup * 2 * kGroup;
     uint4 *cache = static_cast<uint4 *>(a.cache);
-    const int row_vecs = VP * a.parts;
     const long long cap = (long long)a.max_blocks_per_seq << a.log2_block_size;
+    auto sync = [] {
+        if constexpr (kGroup == 32) __syncwarp();
+        else __syncthreads();
+    };
 
     pdl_wait();  // the previous kernel may still read or write the pages
-    for (long long s = blockIdx.x; s < a.slices; s += gridDim.x) {
-        const int part = (int)(s % a.parts);
-        long long rest = s / a.parts;
-        const int h = (int)(rest % a.num_kv_heads);
-        rest /= a.num_kv_heads;
+    const long long total = a.slices * a.shares;
+    for (long long s = (long long)blockIdx.x * kGroups + threadIdx.x / kGroup; s < total; s += (long long)gridDim.x * kGroups) {
+        // heads first: the CTAs that run together move the same tokens' rows, which are neighbours in their pages
+        const int h = (int)(s % a.num_kv_heads);
+        long long rest = s / a.num_kv_heads;
         const int kv = (int)(rest & 1);
-        const int b = (int)(rest >> 1);
+        rest >>= 1;
+        const int share = (int)(rest % a.shares), b = (int)(rest / a.shares);
         const int r0 = __ldg(a.cu_keep + b), r1 = __ldg(a.cu_keep + b + 1);
         const int start = __ldg(a.dst_start + b);
         if (r0 < 0 || r1 < r0 || r1 > a.num_keep || start < 0) {
-            if (threadIdx.x == 0) set_error(a.err, kErrDeviceRange);
+            if (tid == 0) set_error(a.err, kErrDeviceRange);
             continue;
         }
         const int n = r1 - r0;
+        const int *keep = a.keep_pos + r0;
         const int *bt = a.block_tables + (size_t)b * a.max_blocks_per_seq;
-        const bool first_lane = e == 0 && part == 0;  // carries the row's scale
 
-        // row index of position pos in this slice's (K or V, head), or -1 (flagged)
-        auto row_of = [&](long long pos) -> long long {
+        // this group's rows [k0, k_end), 2^log2_v vectors of each from vector col on
+        int k0 = 0, k_end = n, log2_v = a.log2_row_vecs, col = 0;
+        if constexpr (kGroup > 32) {
+            if (a.shares > 1) {
+                const int piece = (n + a.shares - 1) / a.shares;
+                // does a row read what a later piece writes?
+                bool meets = false;
+                int piece_end = piece;  // of k's piece
+                for (int k8 = tid; k8 < n; k8 += 8 * kGroup) {
+                    int src[8];
+#pragma unroll
+                    for (int u = 0; u < 8; ++u) src[u] = k8 + u * kGroup < n ? __ldg(keep + k8 + u * kGroup) : start;
+#pragma unroll
+                    for (int u = 0; u < 8; ++u) {
+                        const long long at = (long long)src[u] - start;  // the row that goes to the source of k
+                        while (k8 + u * kGroup >= piece_end) piece_end += piece;
+                        meets |= at >= piece_end && at < n;
+                    }
+                }
+                if (!__syncthreads_or(meets)) {
+                    k0 = share * piece;
+                    k_end = min(n, k0 + piece);
+                } else {
+                    if (share >= 1 << a.log2_col_shares) continue;
+                    log2_v -= a.log2_col_shares;
+                    col = share << log2_v;
+                }
+            }
+        }
+        const int rows = (kUnroll * kGroup) >> a.log2_row_vecs;  // rows of a chunk (with fewer columns: fewer vectors a thread)
+        // row index of position pos in this slice's (K or V, head), or kNoRow (flagged)
+        auto row_of = [&](long long pos) -> uint32_t {
             const int pb = __ldg(bt + (pos >> a.log2_block_size));
             if (pb < 0 || pb >= a.num_blocks) {
                 set_error(a.err, kErrDeviceRange);
-                return -1;
+                return kNoRow;
             }
-            return (((long long)pb * 2 + kv) * a.num_kv_heads + h) * a.block_size + (pos & (a.block_size - 1));
+            return (((uint32_t)pb * 2 + kv) * a.num_kv_heads + h) * a.block_size + (uint32_t)(pos & (a.block_size - 1));
         };
-        auto load = [&](int base, Chunk &c) {
+        auto look_up = [&](int buf, int base) {
 #pragma unroll
-            for (int u = 0; u < kUnroll; ++u) {
-                const int k = base + u * kRows + tr;
-                c.dst[u] = -1;
-                if (k >= n) continue;
-                const long long src = __ldg(a.keep_pos + r0 + k), dst = (long long)start + k;
-                if (src == dst && src < cap) continue;
-                if (src < dst || src >= cap) {
-                    set_error(a.err, kErrDeviceRange);
-                    continue;
+            for (int r = tid; r < rows; r += kGroup) {
+                uint32_t rs = kNoRow, rd = kNoRow;
+                const int k = base + r;
+                if (k < k_end) {
+                    const long long src = __ldg(keep + k), dst = (long long)start + k;
+                    if (src < dst || src >= cap) {
+                        set_error(a.err, kErrDeviceRange);
+                    } else if (src != dst) {
+                        rs = row_of(src);
+                        rd = row_of(dst);
+                        if (rs == kNoRow) rd = kNoRow;
+                    }
                 }
-                const long long rs = row_of(src), rd = row_of(dst);
-                if (rs < 0 || rd < 0) continue;
-                c.dst[u] = rd;
-                c.v[u] = ld_once(cache + rs * row_vecs + part * VP + e);
-                if (a.scales && first_lane) c.sc[u] = __ldcg(a.scales + rs);
+                s_src[buf][s0 + r] = rs;
+                s_dst[buf][s0 + r] = rd;
             }
         };
-        auto store = [&](const Chunk &c) {
+        // vector u of this thread: row ra + u * rb of the chunk (the same vector of each)
+        const int ra = tid >> log2_v, rb = kGroup >> log2_v;
+        uint4 *const base_v = cache + col + (tid & ((1 << log2_v) - 1));
+        const bool scales = a.scales && col == 0;
+        int buf = 0;
+        look_up(0, k0);
+        sync();
+        for (int base = k0; base < k_end; base += rows) {
+            uint4 v[kUnroll];
+            float sc[2];
 #pragma unroll
             for (int u = 0; u < kUnroll; ++u) {
-                if (c.dst[u] < 0) continue;
-                cache[c.dst[u] * row_vecs + part * VP + e] = c.v[u];
-                if (a.scales && first_lane) a.scales[c.dst[u]] = c.sc[u];
+                const int r = ra + u * rb;
+                if (r < rows && s_dst[buf][s0 + r] != kNoRow) v[u] = ld_once(base_v + ((size_t)s_src[buf][s0 + r] << a.log2_row_vecs));
             }
-        };
-        Chunk cur, nxt;
-        load(0, cur);
-        for (int base = 0; base < n; base += kUnroll * kRows) {
-            load(base + kUnroll * kRows, nxt);
-            __syncthreads();  // every load of this chunk (and of the next) precedes this chunk's stores
-            store(cur);
-            cur = nxt;
+            if (scales)
+#pragma unroll
+                for (int u = 0; u < 2; ++u) {
+                    const int r = tid + u * kGroup;
+                    if (r < rows && s_dst[buf][s0 + r] != kNoRow) sc[u] = __ldcg(a.scales + s_src[buf][s0 + r]);
+                }
+            const int next = buf == 2 ? 0 : buf + 1;
+            if (base + rows < k_end) look_up(next, base + rows);
+            sync();  // every load of this chunk precedes its stores
+#pragma unroll
+            for (int u = 0; u < kUnroll; ++u) {
+                const int r = ra + u * rb;
+                if (r < rows && s_dst[buf][s0 + r] != kNoRow) base_v[(size_t)s_dst[buf][s0 + r] << a.log2_row_vecs] = v[u];
+            }
+            if (scales)
+#pragma unroll
+                for (int u = 0; u < 2; ++u) {
+                    const int r = tid + u * kGroup;
+                    if (r < rows && s_dst[buf][s0 + r] != kNoRow) a.scales[s_dst[buf][s0 + r]] = sc[u];
+                }
+            buf = next;
         }
-        __syncthreads();  // slices of one CTA may share nothing, but its next loads follow these stores
+        sync();  // the next slice's look-ups overwrite these
     }
     pdl_launch_dependents();
 }
@@ -118,23 +176,28 @@ __global__ void __launch_bounds__(kCompactThreads) compact_kernel(CompactArgs a)
 }  // namespace
 
 cudaError_t launch_compact(const CompactArgs &a, cudaStream_t s) {
-    const int row_vecs = a.head_dim * (a.scales ? 1 : 2) / 16;  // 4 .. 32
-    // Column parts of 64 bytes or more until there are two CTAs an SM (a single sequence has only
-    // 2 Hkv rows of slices); whole rows otherwise.
     CompactArgs c = a;
-    const long long rows = (long long)a.batch * 2 * a.num_kv_heads;
-    int vp = row_vecs;
-    while (vp > 4 && rows * (row_vecs / vp) < 2ll * device_info().num_sms) vp /= 2;
-    c.parts = row_vecs / vp;
-    c.slices = rows * c.parts;
-    const long long cap = 32ll * device_info().num_sms;
-    const dim3 grid((unsigned)(c.slices < cap ? c.slices : cap)), block(kCompactThreads);
-    switch (vp) {
-        case 4: return launch_pdl(compact_kernel<4>, grid, block, 0, s, c);
-        case 8: return launch_pdl(compact_kernel<8>, grid, block, 0, s, c);
-        case 16: return launch_pdl(compact_kernel<16>, grid, block, 0, s, c);
-        default: return launch_pdl(compact_kernel<32>, grid, block, 0, s, c);
+    const int row_vecs = a.head_dim * (a.scales ? 1 : 2) / 16;  // 4, 8, 16 or 32
+    c.log2_row_vecs = row_vecs == 4 ? 2 : row_vecs == 8 ? 3 : row_vecs == 16 ? 4 : 5;
+    c.slices = (long long)a.batch * 2 * a.num_kv_heads;
+    c.shares = 1;
+    c.log2_col_shares = 0;
+    const int sms = device_info().num_sms;
+    // the rows of a sequence on average: what a warp moves in one chunk is a warp's (accepted paths)
+    if ((long long)a.num_keep * row_vecs <= (long long)a.batch * 32 * kUnroll) {
+        const long long ctas = (c.slices + kCompactThreads / 32 - 1) / (kCompactThreads / 32), cap = 32ll * sms;
+        return launch_pdl(compact_kernel<32>, dim3((unsigned)(ctas < cap ? ctas : cap)), dim3(kCompactThreads), 0, s, c);
     }
+    // CTAs a slice: four rounds of the SMs' (8 x 8192 rows of 8 heads: 97 us; two rounds 112, eight 105), and for each
+    // two chunks of an average sequence's rows at least
+    const long long round = (long long)kResident * sms, chunk = kUnroll * kCompactThreads / row_vecs;
+    const long long avg = (a.num_keep + a.batch - 1) / a.batch;
+    long long shares = 4 * round / c.slices;
+    if (shares > avg / (2 * chunk)) shares = avg / (2 * chunk);
+    c.shares = shares < 1 ? 1 : shares > 64 ? 64 : (int)shares;
+    while ((2 << c.log2_col_shares) <= c.shares && c.log2_row_vecs - c.log2_col_shares > 2) ++c.log2_col_shares;
+    const long long ctas = c.slices * c.shares, cap = 32ll * sms;
+    return launch_pdl(compact_kernel<kCompactThreads>, dim3((unsigned)(ctas < cap ? ctas : cap)), dim3(kCompactThreads), 0, s, c);
 }
 
 }  // namespace pkv

@@ -617,8 +617,9 @@ pkv_status pkv_kv_cache_compact(pkv_cache cache, const int *keep_pos, const int 
     a.batch = batch;
     a.max_blocks_per_seq = max_blocks_per_seq;
     a.num_keep = num_keep;
-    a.parts = 1;  // set by the launcher, with slices
-    a.slices = 0;
+    a.slices = 0;  // this and the next three are the launcher's
+    a.shares = 1;
+    a.log2_col_shares = a.log2_row_vecs = 0;
     a.err = s->err_ptr;
     return launch_compact(a, static_cast<cudaStream_t>(stream)) == cudaSuccess ? PKV_OK : PKV_ERR_CUDA;
 }

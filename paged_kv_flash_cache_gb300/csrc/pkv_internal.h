@@ -94,8 +94,11 @@ struct CompactArgs {
     int num_blocks, num_kv_heads, block_size, log2_block_size, head_dim;
     const int *keep_pos, *cu_keep, *dst_start, *block_tables;
     int batch, max_blocks_per_seq, num_keep;
-    int parts;         // column parts of a row (set by the launcher)
-    long long slices;  // (sequence, K or V, head, part) slices (set by the launcher)
+    // set by the launcher:
+    long long slices;     // (sequence, K or V, head)
+    int shares;           // CTAs a slice
+    int log2_col_shares;  // of them with a share of the columns where the rows have to go in order
+    int log2_row_vecs;    // 16-byte vectors of a row
     int *err;
 };
 
