@@ -587,7 +587,7 @@ pkv_status pkv_rope_append(pkv_cache cache, pkv_rope rope, const void *q, long l
     a.eps = rope.eps;
     a.q_out = q_out;
     a.q_out_stride = q_out_stride;
-    a.chunks = a.chunk_rows = 0;  // set by the launcher
+    a.share_groups = 0;  // set by the launcher
     a.err = s->err_ptr;
     return launch_rope_append(a, static_cast<cudaStream_t>(stream)) == cudaSuccess ? PKV_OK : PKV_ERR_CUDA;
 }

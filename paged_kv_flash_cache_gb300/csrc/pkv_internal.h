@@ -84,7 +84,7 @@ struct RopeArgs {
     float eps;
     void *q_out;
     long long q_out_stride;
-    int chunks, chunk_rows;  // warps per token and head rows per warp (set by the launcher)
+    int share_groups;  // row groups of a token per warp (set by the launcher)
     int *err;
 };
 
