@@ -132,15 +132,18 @@ def load_library():
 _torch_module = None
 _DTYPES = {}
 _current_raw_stream = None
+_current_device = None
 
 
 def _torch():
-    global _torch_module, _current_raw_stream
+    global _torch_module, _current_raw_stream, _current_device
     if _torch_module is None:
         import torch
         _DTYPES.update({torch.float16: F16, torch.bfloat16: BF16, torch.float32: F32})
         # the current stream's handle without a Stream object around it, where this PyTorch offers it
         _current_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)
+        # (torch.cuda.current_device without its initialisation check, which a CUDA tensor has passed)
+        _current_device = getattr(torch._C, "_cuda_getDevice", torch.cuda.current_device)
         _torch_module = torch
     return _torch_module
 
@@ -181,10 +184,9 @@ def _stream(stream, device=None):
 
 def _on_device(index, fn, *args):
     """fn(*args) with device `index` current: the library launches on the current device."""
-    torch = _torch()
-    if torch.cuda.current_device() == index:
+    if _current_device() == index:
         return fn(*args)
-    with torch.cuda.device(index):
+    with _torch().cuda.device(index):
         return fn(*args)
 
 
@@ -368,21 +370,31 @@ def paged_attn_mixed(cache, q, cu_q_lens, context_lens, block_tables, max_q_len:
     return out
 
 
-def _rows(t, heads, head_dim, name):
-    """Pointer and token stride (elements) of [T, heads, head_dim] rows whose tokens may be strided."""
-    shape = t.shape
-    if len(shape) != 3 or shape[1] != heads or shape[2] != head_dim:
-        raise ValueError("%s must be [tokens, %d, %d]" % (name, heads, head_dim))
+def _at(t, dtype, index, name):
+    """Pointer of a contiguous tensor of `dtype` on the cache's device (None: NULL)."""
+    if t is None:
+        return None
+    if t.get_device() != index:
+        raise ValueError("%s is on %s, the cache on another device" % (name, t.device))
+    if t.dtype is not dtype:
+        raise TypeError("%s must be %s" % (name, dtype))
+    if not t.is_contiguous():
+        raise ValueError("%s must be contiguous" % name)
+    return t.data_ptr()
+
+
+def _rows(t, total, heads, head_dim, dtype, index, name):
+    """Pointer and token stride (elements) of [total, heads, head_dim] rows whose tokens may be strided."""
+    if t.get_device() != index:
+        raise ValueError("%s is on %s, the cache on another device" % (name, t.device))
+    if t.dtype is not dtype:
+        raise TypeError("%s must be %s" % (name, dtype))
+    if t.shape != (total, heads, head_dim):
+        raise ValueError("%s must be [%d, %d, %d]" % (name, total, heads, head_dim))
     s0, s1, s2 = t.stride()
-    if s2 != 1 or (heads > 1 and s1 != head_dim):
+    if s2 != 1 or (s1 != head_dim and heads > 1):
         raise ValueError("%s: the heads of a token must be contiguous" % name)
-    return t.data_ptr(), s0 if shape[0] > 1 else heads * head_dim
-
-
-def _same_device(index, *tensors):
-    for t in tensors:
-        if t is not None and t.get_device() != index:
-            raise ValueError("a tensor on %s with a cache on cuda:%d" % (t.device, index))
+    return t.data_ptr(), s0 if total > 1 else heads * head_dim
 
 
 def rope_append(cache, q, k, v, inv_freq, cu_new_lens, ctx_before, block_tables, positions, interleaved: bool = False,
@@ -397,36 +409,33 @@ def rope_append(cache, q, k, v, inv_freq, cu_new_lens, ctx_before, block_tables,
     (2i, 2i + 1). positions: int32 [T]. q_out: where the queries go (q itself: in place); a new tensor if None."""
     torch = _torch()
     lib = load_library()
-    if k.dtype != q.dtype or v.dtype != q.dtype or k.shape != v.shape or k.shape[0] != q.shape[0]:
-        raise TypeError("q / k / v must match each other")
-    index = cache.get_device()
-    _same_device(index, q, k, v, inv_freq, positions, cu_new_lens, ctx_before, block_tables, q_weight, k_weight, q_out,
-                 scales)
-    c = _cache_struct(cache, q.dtype, scales)
+    index, dtype, i32 = cache.get_device(), q.dtype, torch.int32
+    c = _cache_struct(cache, dtype, scales)
     hkv, d = c.num_kv_heads, c.head_dim
     total, hq = q.shape[0], q.shape[1]
     batch, mb = block_tables.shape
-    half = inv_freq.shape[0]
-    if inv_freq.dtype != torch.float32 or inv_freq.dim() != 1 or 2 * half > d:
+    half = inv_freq.numel()
+    if 2 * half > d:
         raise ValueError("inv_freq must be float32 [rotary_dim / 2], rotary_dim <= head_dim")
     if positions.shape != (total,):
         raise ValueError("positions must be [tokens]")
     if cu_new_lens.shape != (batch + 1,) or ctx_before.shape != (batch,):
         raise ValueError("cu_new_lens must be [batch + 1], ctx_before [batch]")
-    for name, w in (("q_weight", q_weight), ("k_weight", k_weight)):
-        if w is not None and (w.dtype != q.dtype or w.shape != (d,)):
-            raise ValueError("%s must be [head_dim] in the dtype of q" % name)
+    if (q_weight is not None and q_weight.shape != (d,)) or (k_weight is not None and k_weight.shape != (d,)):
+        raise ValueError("q_weight and k_weight must be [head_dim]")
+    if scales is not None and scales.get_device() != index:
+        raise ValueError("scales on %s, the cache on another device" % scales.device)
+    qp, qs = _rows(q, total, hq, d, dtype, index, "q")
+    kp, ks = _rows(k, total, hkv, d, dtype, index, "k")
+    vp, vs = _rows(v, total, hkv, d, dtype, index, "v")
     if q_out is None:
-        q_out = torch.empty((total, hq, d), dtype=q.dtype, device=q.device)
-    elif q_out.dtype != q.dtype or q_out.shape != q.shape:
-        raise ValueError("q_out must match q")
-    rope = _Rope(2 * half, 1 if interleaved else 0, _dev(inv_freq, "inv_freq"), mscale, _dev(q_weight, "q_weight"),
-                 _dev(k_weight, "k_weight"), eps)
-    (qp, qs), (kp, ks), (vp, vs) = _rows(q, hq, d, "q"), _rows(k, hkv, d, "k"), _rows(v, hkv, d, "v")
-    op, os_ = _rows(q_out, hq, d, "q_out")
-    _check(_on_device(index, lib.pkv_rope_append, c, rope, qp, qs, hq, kp, ks, vp, vs, _i32(positions, "positions"),
-                      _i32(cu_new_lens, "cu_new_lens"), _i32(ctx_before, "ctx_before"),
-                      _i32(block_tables, "block_tables"), batch, mb, total, op, os_, _stream(stream, index)),
+        q_out = torch.empty((total, hq, d), dtype=dtype, device=q.device)
+    op, os_ = _rows(q_out, total, hq, d, dtype, index, "q_out")
+    rope = _Rope(2 * half, 1 if interleaved else 0, _at(inv_freq, torch.float32, index, "inv_freq"), mscale,
+                 _at(q_weight, dtype, index, "q_weight"), _at(k_weight, dtype, index, "k_weight"), eps)
+    _check(_on_device(index, lib.pkv_rope_append, c, rope, qp, qs, hq, kp, ks, vp, vs, _at(positions, i32, index, "positions"),
+                      _at(cu_new_lens, i32, index, "cu_new_lens"), _at(ctx_before, i32, index, "ctx_before"),
+                      _at(block_tables, i32, index, "block_tables"), batch, mb, total, op, os_, _stream(stream, index)),
            "pkv_rope_append")
     return q_out
 
@@ -442,9 +451,8 @@ def paged_attn_tree(cache, q, tree_mask, cu_q_lens, context_lens, block_tables, 
     `workloads.tree_mask`), one another. Returns `out`."""
     torch = _torch()
     lib = load_library()
-    index = cache.get_device()
-    _same_device(index, q, tree_mask, cu_q_lens, context_lens, block_tables, workspace, out, lse)
-    c = _cache_struct(cache, q.dtype)
+    index, dtype, i32 = cache.get_device(), q.dtype, torch.int32
+    c = _cache_struct(cache, dtype)
     total_q, hq, d = q.shape
     batch, mb = block_tables.shape
     if d != c.head_dim:
@@ -454,20 +462,21 @@ def paged_attn_tree(cache, q, tree_mask, cu_q_lens, context_lens, block_tables, 
     if cu_q_lens.shape != (batch + 1,) or context_lens.shape != (batch,):
         raise ValueError("cu_q_lens must be [batch + 1], context_lens [batch]")
     if out is None:
-        out = torch.empty((total_q, hq, d), dtype=out_dtype or q.dtype, device=q.device)
+        out = torch.empty((total_q, hq, d), dtype=out_dtype or dtype, device=q.device)
     elif out.shape != q.shape:
         raise ValueError("out must have the shape of q")
-    if lse is not None and (lse.dtype != torch.float32 or lse.shape != (total_q, hq)):
+    if lse is not None and lse.shape != (total_q, hq):
         raise ValueError("lse must be float32 [rows of q, Hq]")
     if workspace is None:
         workspace = torch.empty(lib.pkv_tree_workspace_size(hq, c.num_kv_heads, d, max_q_len), dtype=torch.uint8,
                                 device=q.device)
-    ws_bytes = workspace.numel() * workspace.element_size()
     scale = (1.0 / math.sqrt(d)) if scale is None else float(scale)
-    _check(_on_device(index, lib.pkv_paged_attn_tree, c, _dev(q, "q"), hq, _i32(tree_mask, "tree_mask"),
-                      tree_mask.shape[1], _i32(cu_q_lens, "cu_q_lens"), _i32(context_lens, "context_lens"),
-                      _i32(block_tables, "block_tables"), batch, mb, total_q, int(max_q_len), scale,
-                      _dev(workspace, "workspace"), ws_bytes, _dev(out, "out"), _dtype_code(out.dtype), _dev(lse, "lse"),
+    out_code = _dtype_code(out.dtype)
+    _check(_on_device(index, lib.pkv_paged_attn_tree, c, _at(q, dtype, index, "q"), hq, _at(tree_mask, i32, index, "tree_mask"),
+                      tree_mask.shape[1], _at(cu_q_lens, i32, index, "cu_q_lens"),
+                      _at(context_lens, i32, index, "context_lens"), _at(block_tables, i32, index, "block_tables"), batch, mb,
+                      total_q, int(max_q_len), scale, _at(workspace, workspace.dtype, index, "workspace"), workspace.nbytes,
+                      _at(out, out.dtype, index, "out"), out_code, _at(lse, torch.float32, index, "lse"),
                       _stream(stream, index)), "pkv_paged_attn_tree")
     return out
 
@@ -478,14 +487,16 @@ def kv_cache_compact(cache, keep_pos, cu_keep, dst_start, block_tables, stream=N
     dst_start [batch]."""
     torch = _torch()
     lib = load_library()
-    index = cache.get_device()
-    _same_device(index, keep_pos, cu_keep, dst_start, block_tables, scales)
-    c = _cache_struct(cache, torch.float16 if is_fp8_cache(cache) else cache.dtype, scales)
+    index, i32 = cache.get_device(), torch.int32
+    c = _cache_struct(cache, torch.float16 if scales is not None else cache.dtype, scales)
     batch, mb = block_tables.shape
     if keep_pos.dim() != 1 or cu_keep.shape != (batch + 1,) or dst_start.shape != (batch,):
         raise ValueError("keep_pos must be [num_keep], cu_keep [batch + 1], dst_start [batch]")
-    _check(_on_device(index, lib.pkv_kv_cache_compact, c, _i32(keep_pos, "keep_pos"), _i32(cu_keep, "cu_keep"),
-                      _i32(dst_start, "dst_start"), _i32(block_tables, "block_tables"), batch, mb, keep_pos.shape[0],
+    if scales is not None and scales.get_device() != index:
+        raise ValueError("scales on %s, the cache on another device" % scales.device)
+    _check(_on_device(index, lib.pkv_kv_cache_compact, c, _at(keep_pos, i32, index, "keep_pos"),
+                      _at(cu_keep, i32, index, "cu_keep"), _at(dst_start, i32, index, "dst_start"),
+                      _at(block_tables, i32, index, "block_tables"), batch, mb, keep_pos.shape[0],
                       _stream(stream, index)), "pkv_kv_cache_compact")
 
 
