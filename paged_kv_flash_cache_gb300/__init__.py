@@ -198,10 +198,14 @@ def is_fp8_cache(cache) -> bool:
 
 def _cache_struct(cache, act_dtype, scales=None) -> _Cache:
     """The C view of `cache`; act_dtype is the type of q / k_new / v_new."""
-    torch = _torch()
-    if cache.dim() != 5 or cache.shape[1] != 2:
+    torch = _torch_module or _torch()
+    shape = cache.shape
+    if len(shape) != 5 or shape[1] != 2:
         raise ValueError("cache must be [num_blocks, 2, num_kv_heads, block_size, head_dim]")
-    nb, _, hkv, bs, d = cache.shape
+    nb, _, hkv, bs, d = shape
+    code = _DTYPES.get(cache.dtype)
+    if code is not None and scales is None and act_dtype is cache.dtype:
+        return _Cache(_dev(cache, "cache"), nb, hkv, bs, d, code, KV_NATIVE, None)
     if is_fp8_cache(cache):
         if scales is None or scales.dtype != torch.float32 or tuple(scales.shape) != (nb, 2, hkv, bs):
             raise ValueError("an FP8 cache needs float32 scales [num_blocks, 2, num_kv_heads, block_size]")
@@ -429,8 +433,10 @@ def rope_append(cache, q, k, v, inv_freq, cu_new_lens, ctx_before, block_tables,
     kp, ks = _rows(k, total, hkv, d, dtype, index, "k")
     vp, vs = _rows(v, total, hkv, d, dtype, index, "v")
     if q_out is None:
-        q_out = torch.empty((total, hq, d), dtype=dtype, device=q.device)
-    op, os_ = _rows(q_out, total, hq, d, dtype, index, "q_out")
+        q_out = q.new_empty((total, hq, d))
+        op, os_ = q_out.data_ptr(), hq * d
+    else:
+        op, os_ = _rows(q_out, total, hq, d, dtype, index, "q_out")
     rope = _Rope(2 * half, 1 if interleaved else 0, _at(inv_freq, torch.float32, index, "inv_freq"), mscale,
                  _at(q_weight, dtype, index, "q_weight"), _at(k_weight, dtype, index, "k_weight"), eps)
     _check(_on_device(index, lib.pkv_rope_append, c, rope, qp, qs, hq, kp, ks, vp, vs, _at(positions, i32, index, "positions"),
@@ -462,14 +468,13 @@ def paged_attn_tree(cache, q, tree_mask, cu_q_lens, context_lens, block_tables, 
     if cu_q_lens.shape != (batch + 1,) or context_lens.shape != (batch,):
         raise ValueError("cu_q_lens must be [batch + 1], context_lens [batch]")
     if out is None:
-        out = torch.empty((total_q, hq, d), dtype=out_dtype or dtype, device=q.device)
+        out = q.new_empty((total_q, hq, d), dtype=out_dtype or dtype)
     elif out.shape != q.shape:
         raise ValueError("out must have the shape of q")
     if lse is not None and lse.shape != (total_q, hq):
         raise ValueError("lse must be float32 [rows of q, Hq]")
     if workspace is None:
-        workspace = torch.empty(lib.pkv_tree_workspace_size(hq, c.num_kv_heads, d, max_q_len), dtype=torch.uint8,
-                                device=q.device)
+        workspace = q.new_empty(lib.pkv_tree_workspace_size(hq, c.num_kv_heads, d, max_q_len), dtype=torch.uint8)
     scale = (1.0 / math.sqrt(d)) if scale is None else float(scale)
     out_code = _dtype_code(out.dtype)
     _check(_on_device(index, lib.pkv_paged_attn_tree, c, _at(q, dtype, index, "q"), hq, _at(tree_mask, i32, index, "tree_mask"),
