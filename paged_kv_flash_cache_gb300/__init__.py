@@ -8,7 +8,11 @@ stream. There is no CPU fallback: if the library is missing every call raises.
 
 Entry points (same names as the C ABI without the ``pkv_`` prefix):
   kv_cache_append, paged_attn_decode, paged_attn_decode_step, paged_attn_prefill, paged_attn_mixed,
-  attn_combine, decode_workspace_size, decode_split_tokens, get_device_error.
+  attn_combine, decode_workspace_size, decode_split_tokens, get_device_error;
+  around the attention of a step, and of a step with drafted tokens: rope_append (norm, rotary positions,
+  append), paged_attn_tree and tree_workspace_size (a tree of drafted tokens over the cache), kv_cache_compact
+  (the rows that are kept move to the front). `rope.rope_frequencies`, `workloads.tree_mask` and
+  `workloads.tree_depths` make their arguments on the host.
 Cache tensors have shape [num_blocks, 2, num_kv_heads, block_size, head_dim]
 (K at index 0, V at index 1) in float16 or bfloat16, or hold FP8 E4M3 codes
 (torch.float8_e4m3fn or uint8) with a float32 `scales` tensor
@@ -451,14 +455,17 @@ def tree_workspace_size(num_q_heads, num_kv_heads, head_dim, max_q_len) -> int:
 
 
 def paged_attn_tree(cache, q, tree_mask, cu_q_lens, context_lens, block_tables, max_q_len: int,
-                    scale: Optional[float] = None, workspace=None, out=None, out_dtype=None, lse=None, stream=None):
+                    scale: Optional[float] = None, workspace=None, out=None, out_dtype=None, lse=None, stream=None,
+                    scales=None):
     """Drafted tokens ([sum n_b, Hq, D], their K/V already appended as each sequence's last n_b cached tokens) against
     the paged context and, by tree_mask (int32 [sum n_b, words], bit j % 32 of word j / 32: node i sees node j; see
     `workloads.tree_mask`), one another. Returns `out`."""
     torch = _torch()
     lib = load_library()
     index, dtype, i32 = cache.get_device(), q.dtype, torch.int32
-    c = _cache_struct(cache, dtype)
+    c = _cache_struct(cache, dtype, scales)
+    if scales is not None and scales.get_device() != index:
+        raise ValueError("scales on %s, the cache on another device" % scales.device)
     total_q, hq, d = q.shape
     batch, mb = block_tables.shape
     if d != c.head_dim:

@@ -20,15 +20,23 @@
 // score buffer its next 64 keys' Q K^T fills the other: Q K(u + 1) is issued before P V(u). (With one buffer of
 // 128 keys a lane the chain softmax - P V - Q K - softmax, 5100 cycles a tile of a wide block, bounded the kernel.)
 //
-// Work: the (sequence, KV head, row block) items, laid end to end in key tiles, are cut into equal runs,
-// one a CTA (one CTA an SM): any mix of lengths fills the GPU evenly, an item is split only where a run
-// ends, and a CTA leaves at most two partial items, so the workspace does not grow with the batch. A merge
-// kernel joins the partials of each split item in the order of the keys (no atomics: the same result every time).
+// Work: the (sequence, KV head, row block) items, laid end to end in key tiles (an item weighs kItemCost tiles more for
+// its set-up and output), are cut into equal runs, one a CTA (one CTA an SM): any mix of lengths fills the GPU
+// evenly, an item is split only where a run ends, and a CTA leaves at most two partial items, so the workspace does not grow
+// with the batch. A merge kernel joins the partials of each split item in the order of the keys (no atomics: the same
+// result every time).
 //
-// Warps: 0 loads Q and the K tiles, 3 the V tiles by TMA into a ring, 1 issues the MMAs and owns TMEM, 2 walks the run and hands its segments to the others, the warpgroups of lanes A and B do softmax and
-// output. P goes to the tensor cores as its 16-bit rounding plus the rounding's remainder (two products), so that it
-// is not a rounding to 16 bits -- but for wide blocks with a 16-bit output, which the tensor cores bound: there P is
-// rounded once, half a step of the output's own type (the prefill's choice too).
+// Warps: 0 loads Q and the K tiles, 3 the V tiles by TMA into a ring, 1 issues the MMAs and owns TMEM, 2 walks the run
+// and hands its segments to the others, the warpgroups of lanes A and B do softmax and output. P goes to the tensor cores
+// as its 16-bit rounding plus the rounding's remainder (two products), so that it is not a rounding to 16 bits -- but for
+// wide blocks with a 16-bit output, which the chain of products and softmax bounds (a 63-node batch: 96 us with
+// two parts, 88 with one): there P is rounded once, half a step of the output's own type (the prefill's choice too).
+//
+// Measured, main kernel and merge, back to back: 16 sequences x 64 nodes, 32 KV heads x 128, contexts 1k-8k in pages of 16
+// (1.02 GB): 167 us, 90% of the copy rate, bound by HBM; 25 nodes of 32 / 8 heads over 131k tokens in pages of 64 (0.54 GB): 98 us,
+// 81%, the merge 8 us of it; 32 sequences x 63 nodes of 32 / 8 heads, contexts to 8k (0.27 GB, 252 rows a KV head): 77 us, 52%, bound by
+// the wide chain (about 3800 cycles a tile, of them 2560 in the tensor cores) and the merge, 13 us; 8 sequences x 31 nodes at head_dim 256
+// (0.16 GB): 39 us, 61%, four ring slots beside the 64 KB of Q.
 //
 // Rows that see nothing (a padded node): 0 and -inf. Masked keys: their scores are replaced, never
 // multiplied, so that K may hold anything; V rows beyond the context are zeroed in shared memory, and a
@@ -60,7 +68,7 @@ struct Segment {
     int pad[2];
 };
 
-template <int D>
+template <int D, bool FP8>
 struct TreeLayout {
     static constexpr int kLanes = D <= 128 ? 2 : 1;
     static constexpr int kBN = D <= 128 ? 128 : 64;  // keys a tile
@@ -71,13 +79,20 @@ struct TreeLayout {
     static constexpr uint32_t kTileHalf = kBN * 128;
     static constexpr uint32_t kTileBytes = kHalves * kTileHalf;  // a K or a V tile
     // ring slots; a launch whose blocks are all narrow has one more in the place of lane B's Q tile
-    static constexpr int kRing = D == 64 ? 8 : 4;
+    static constexpr int kRing = D == 64 && !FP8 ? 8 : 4;
     static constexpr int kRingMax = kRing + (kLanes == 2 ? 1 : 0);
     static_assert(kLanes == 1 || kQBytes == kTileBytes, "a Q tile's place is a ring slot's");
-    static constexpr uint32_t kStageOff = kLanes * kQBytes + kRing * kTileBytes;  // output rows, 4 KB a softmax warp
-    static constexpr uint32_t kMlOff = kStageOff + 4 * kLanes * 4096u;    // [128] (max, sum) between the lanes
-    static constexpr uint32_t kBarOff = kMlOff + kBM * 8;
-    static constexpr uint32_t kSegOff = kBarOff + 512;
+    // output rows on their way out, kStageRow bytes of each: 4 (FP8: 2) KB a softmax warp
+    static constexpr uint32_t kStageRow = FP8 ? 64 : 128;
+    static constexpr uint32_t kStageOff = kLanes * kQBytes + kRing * kTileBytes;
+    static constexpr uint32_t kMlOff = kStageOff + 4 * kLanes * 32 * kStageRow;  // [128] (max, sum) between the lanes
+    // FP8: the row scales of the ring's tiles, and of the last four K tiles (a ring slot may be refilled while its scores
+    // are still in the softmax); head_dim 64: the codes of the ring's tiles (head_dim 128: in the tile's second half)
+    static constexpr uint32_t kScaleOff = kMlOff + kBM * 8;
+    static constexpr uint32_t kKScaleOff = kScaleOff + (FP8 ? kRingMax * 512u : 0u);
+    static constexpr uint32_t kCodeOff = kKScaleOff + (FP8 ? 4 * 512u : 0u);
+    static constexpr uint32_t kBarOff = kCodeOff + (FP8 && D == 64 ? kRingMax * kBN * 64u : 0u);
+    static constexpr uint32_t kSegOff = kBarOff + 640;
     static constexpr uint32_t kSmem = kSegOff + kSegs * sizeof(Segment) + 1024;  // + alignment slack
     static constexpr int kThreads = 128 * (1 + kLanes);
     // TMEM: score buffer i of lane x at 128 i + 64 x (P in its place), O of lane x at 256 + 128 x
@@ -148,10 +163,29 @@ __device__ __forceinline__ uint32_t remainder_pair(float a, float b, uint32_t hi
     return pack_pair<false>(a - f.x, b - f.y);
 }
 
-template <int D, bool BF16>
-__global__ void __launch_bounds__(TreeLayout<D>::kThreads, 1)
+// Eight E4M3 codes (8 bytes) times `scale` as 16-bit values; `drop`: values that are not finite become 0 (told in `bad`).
+template <bool BF16>
+__device__ __forceinline__ uint4 values_of(const uint2 &codes, float scale, bool drop, bool &bad) {
+    float2 f[4];
+    unpack_e4m3x8(codes, f);
+    uint32_t w[4];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        f[i] = fmul2(f[i], make_float2(scale, scale));
+        w[i] = pack_pair<BF16>(f[i].x, f[i].y);
+        if (drop && nonfinite_pair<BF16>(w[i])) {
+            bad = true;
+            w[i] = drop_nonfinite<BF16>(w[i]);
+        }
+    }
+    return make_uint4(w[0], w[1], w[2], w[3]);
+}
+
+template <int D, bool BF16, bool FP8>
+__global__ void __launch_bounds__(TreeLayout<D, FP8>::kThreads, 1)
     tree_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CUtensorMap tm_kv, TreeArgs a) {
-    using L = TreeLayout<D>;
+    using L = TreeLayout<D, FP8>;
+    static_assert(!FP8 || D <= 128, "an FP8 cache has head_dim 64 or 128");
     constexpr int kBN = L::kBN, kSub = L::kSub, kLanes = L::kLanes, kRingMax = L::kRingMax;
     const bool all_narrow = kLanes == 2 && a.max_q_len <= a.tile_nodes;
     const uint32_t ring = all_narrow ? kRingMax : L::kRing;
@@ -175,7 +209,8 @@ __global__ void __launch_bounds__(TreeLayout<D>::kThreads, 1)
     uint64_t *seg_full = ml_full + 1;      // [kSegs]
     uint64_t *seg_empty = seg_full + kSegs;
     uint64_t *drain = seg_empty + kSegs;   // every MMA issued has completed
-    unsigned long long *s_total = reinterpret_cast<unsigned long long *>(drain + 1);
+    uint64_t *conv_full = drain + 1;       // FP8: [kRingMax] a tile's codes are 16-bit values
+    unsigned long long *s_total = reinterpret_cast<unsigned long long *>(conv_full + kRingMax);
     uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(s_total + 1);
     volatile int *abort_flag = reinterpret_cast<volatile int *>(tmem_slot + 1);
     volatile int *s_poison = abort_flag + 1;  // [4] by segment: V of a drafted token was not finite
@@ -189,6 +224,7 @@ __global__ void __launch_bounds__(TreeLayout<D>::kThreads, 1)
         for (int i = 0; i < kRingMax; ++i) {
             mbar_init(&kv_full[i], 1);
             mbar_init(&kv_empty[i], 1);
+            mbar_init(&conv_full[i], kSoftmaxWarps);
         }
         mbar_init(q_full, 1);
         mbar_init(q_empty, 1);
@@ -321,6 +357,20 @@ __global__ void __launch_bounds__(TreeLayout<D>::kThreads, 1)
                     }
                     if (!(ok = mbar_wait(&kv_empty[slot], ph, abort_flag, a.err))) break;
                     uint8_t *dst = sRing + slot * L::kTileBytes;
+                    if constexpr (FP8) {
+                        // one box row of codes and a scale a token
+                        dst = D == 128 ? dst + L::kTileHalf : smem + L::kCodeOff + slot * (kBN * 64u);
+                        float *dst_sc = reinterpret_cast<float *>(smem + L::kScaleOff) + slot * 128u;
+                        if (tc::elect_one()) mbar_arrive_expect_tx(&kv_full[slot], (uint32_t)npages * box_rows * (D + 4u));
+                        for (int pg = 0; pg < npages; ++pg, dst += (uint32_t)box_rows * D, dst_sc += box_rows) {
+                            const int pb = __shfl_sync(0xffffffffu, w0, page0 - first + pg);
+                            const int row = ((pb * 2 + kv) * a.cache.num_kv_heads + kvh) * bs + off;
+                            if (tc::elect_one()) {
+                                tc::tma_load_2d_hint(dst, &tm_kv, 0, row, &kv_full[slot], pol);
+                                bulk_g2s(dst_sc, a.cache.scales + row, (uint32_t)box_rows * 4u, &kv_full[slot], pol);
+                            }
+                        }
+                    } else {
                     if (tc::elect_one())
                         mbar_arrive_expect_tx(&kv_full[slot], (uint32_t)npages * box_rows * 128u * L::kHalves);
                     for (int pg = 0; pg < npages; ++pg, dst += (uint32_t)box_rows * 128u) {
@@ -331,6 +381,7 @@ __global__ void __launch_bounds__(TreeLayout<D>::kThreads, 1)
                             for (int hf = 0; hf < L::kHalves; ++hf)
                                 tc::tma_load_2d_hint(dst + hf * L::kTileHalf, &tm_kv, hf * 64, row, &kv_full[slot], pol);
                         }
+                    }
                     }
                     used |= 1u << slot;
                     par = (par & ~(1u << slot)) | ((ph ^ 1u) << slot);
@@ -373,6 +424,7 @@ __global__ void __launch_bounds__(TreeLayout<D>::kThreads, 1)
                 const uint64_t dV0 = tc::smem_desc(aRing, L::kTileHalf, 1024);
                 uint32_t slot = 0, ph = 0;  // ring position
                 uint32_t g = 0;             // score buffers that each lane has used
+                uint64_t *const tile_full = FP8 ? conv_full : kv_full;  // the ring's tiles as the products read them
                 auto advance = [&]() {
                     if (++slot == ring) {
                         slot = 0;
@@ -431,7 +483,7 @@ __global__ void __launch_bounds__(TreeLayout<D>::kThreads, 1)
                     tc::fence_after_sync();
                     if (wide) {
                         const bool two_parts = a.out_dtype == 2;
-                        if (!(ok = wait(&kv_full[slot], ph))) break;
+                        if (!(ok = wait(&tile_full[slot], ph))) break;
                         qk(true, slot, 0, g & 1u);
                         for (int j = 0; j < T; ++j) {
                             // buffers 2 j (the tile's first half), 2 j + 1
@@ -439,7 +491,7 @@ __global__ void __launch_bounds__(TreeLayout<D>::kThreads, 1)
                             tc::mma_commit(&kv_empty[slot]);
                             if (j == T - 1) tc::mma_commit(q_empty);  // the segment's last Q K
                             advance();
-                            if (!(ok = wait(&kv_full[slot], ph) && wait(&p_full[g & 1u], (g >> 1) & 1u))) break;
+                            if (!(ok = wait(&tile_full[slot], ph) && wait(&p_full[g & 1u], (g >> 1) & 1u))) break;
                             // a segment's first P V overwrites an output: the last segment's must be read
                             if (j == 0 && !(ok = wait(o_empty, (seg_i & 1u) ^ 1u))) break;
                             tc::fence_after_sync();
@@ -447,7 +499,7 @@ __global__ void __launch_bounds__(TreeLayout<D>::kThreads, 1)
                             const uint32_t v_slot = slot;
                             advance();
                             if (j + 1 < T) {
-                                if (!(ok = wait(&kv_full[slot], ph))) break;
+                                if (!(ok = wait(&tile_full[slot], ph))) break;
                                 qk(true, slot, 0, g & 1u);
                             } else {
                                 tc::mma_commit(pv_late);
@@ -460,20 +512,20 @@ __global__ void __launch_bounds__(TreeLayout<D>::kThreads, 1)
                             ++g;
                         }
                     } else {
-                        if (!(ok = wait(&kv_full[slot], ph))) break;
+                        if (!(ok = wait(&tile_full[slot], ph))) break;
                         qk(false, slot, 0, g & 1u);
                         tc::mma_commit(&kv_empty[slot]);
                         if (T == 1) tc::mma_commit(q_empty);
                         advance();
                         for (int j = 0; j < T; ++j, ++g) {
                             if (j + 1 < T) {
-                                if (!(ok = wait(&kv_full[slot], ph))) break;
+                                if (!(ok = wait(&tile_full[slot], ph))) break;
                                 qk(false, slot, 0, (g + 1u) & 1u);
                                 tc::mma_commit(&kv_empty[slot]);
                                 if (j + 2 == T) tc::mma_commit(q_empty);
                                 advance();
                             }
-                            if (!(ok = wait(&kv_full[slot], ph) && wait(&p_full[g & 1u], (g >> 1) & 1u))) break;
+                            if (!(ok = wait(&tile_full[slot], ph) && wait(&p_full[g & 1u], (g >> 1) & 1u))) break;
                             if (j == 0 && !(ok = wait(o_empty, (seg_i & 1u) ^ 1u))) break;
                             tc::fence_after_sync();
                             pv(false, true, slot, 0, g & 1u, j == 0);
@@ -574,6 +626,7 @@ __global__ void __launch_bounds__(TreeLayout<D>::kThreads, 1)
         const uint32_t tO = tmem + L::kColO + 128u * x + lane_base;
         uint32_t g0 = 0;    // score buffers of this lane before this segment
         uint32_t item = 0;  // ring items before this segment (the V of its tile j: see the sweep)
+        uint32_t tiles0 = 0;  // FP8: key tiles before this segment
         uint32_t nml = 0;     // narrow segments so far
         uint32_t n_late = 0;  // segments of two buffers or more so far
         for (; next_segment(); ++seg_i) {
@@ -593,6 +646,69 @@ __global__ void __launch_bounds__(TreeLayout<D>::kThreads, 1)
             };
             float m = -INFINITY, l = 0.f;
             bool ok = true;
+            // FP8: this warp's 16 rows of tile j's K (kv 0) or V (kv 1), codes to 16-bit values in the layout that TMA
+            // writes for a 16-bit cache. K: the codes' own values (exact; the row scales multiply the scores); V: times the
+            // row's scale, rounded to 16 bits. Rows beyond the context become 0; what is not finite in a drafted token's V
+            // becomes 0 and is told.
+            auto ring_item = [&](int kv, int j) -> uint32_t {
+                return item + (kv ? (uint32_t)(j + min(T, ahead + j)) : (uint32_t)(j < ahead ? j : 2 * j - ahead + 1));
+            };
+            auto convert = [&](int kv, int j) -> bool {
+                const uint32_t it = ring_item(kv, j), sl = it % ring, par = (it / ring) & 1u;
+                if (!mbar_wait(&kv_full[sl], par, abort_flag, a.err)) return false;
+                uint8_t *const tile = sRing + sl * L::kTileBytes;
+                const float *const sc = reinterpret_cast<const float *>(smem + L::kScaleOff) + sl * 128u;
+                const int first = (warp - 4) * 16, start = (s.t0 + j) * kBN;
+                const int n_valid = s.len - start, drafted = s.len - s.n - start;  // rows from here on
+                bool bad = false;
+                if constexpr (D == 128) {
+                    // a row's codes lie where the second half of its values goes: 8 lanes read it whole, then write
+#pragma unroll
+                    for (int i = 0; i < 4; ++i) {
+                        const int row = first + 4 * i + (lane >> 3), c = lane & 7, hf = c >> 2, k0 = 2 * (c & 3);
+                        const uint4 raw = *reinterpret_cast<const uint4 *>(tile + L::kTileHalf + row * 128 + ((c ^ (row & 7)) << 4));
+                        __syncwarp();
+                        const float scale = kv ? sc[row] : 1.f;
+                        const bool drop = kv && row >= drafted;
+                        uint4 v0 = values_of<BF16>(make_uint2(raw.x, raw.y), scale, drop, bad);
+                        uint4 v1 = values_of<BF16>(make_uint2(raw.z, raw.w), scale, drop, bad);
+                        if (row >= n_valid) v0 = v1 = make_uint4(0, 0, 0, 0);
+                        uint8_t *dst = tile + hf * L::kTileHalf + row * 128;
+                        *reinterpret_cast<uint4 *>(dst + ((k0 ^ (row & 7)) << 4)) = v0;
+                        *reinterpret_cast<uint4 *>(dst + (((k0 + 1) ^ (row & 7)) << 4)) = v1;
+                    }
+                } else if constexpr (D == 64) {
+                    const uint8_t *const codes = smem + L::kCodeOff + sl * (kBN * 64u);
+#pragma unroll
+                    for (int i = 0; i < 2; ++i) {
+                        const int row = first + 8 * i + (lane >> 2), c = lane & 3;
+                        const uint4 raw = *reinterpret_cast<const uint4 *>(codes + row * 64 + c * 16);
+                        const float scale = kv ? sc[row] : 1.f;
+                        const bool drop = kv && row >= drafted;
+                        uint4 v0 = values_of<BF16>(make_uint2(raw.x, raw.y), scale, drop, bad);
+                        uint4 v1 = values_of<BF16>(make_uint2(raw.z, raw.w), scale, drop, bad);
+                        if (row >= n_valid) v0 = v1 = make_uint4(0, 0, 0, 0);
+                        uint8_t *dst = tile + row * 128;
+                        *reinterpret_cast<uint4 *>(dst + (((2 * c) ^ (row & 7)) << 4)) = v0;
+                        *reinterpret_cast<uint4 *>(dst + (((2 * c + 1) ^ (row & 7)) << 4)) = v1;
+                    }
+                }
+                if (kv == 0 && lane < 16)
+                    reinterpret_cast<float *>(smem + L::kKScaleOff)[((tiles0 + (uint32_t)j) & 3u) * 128u + first + lane] = sc[first + lane];
+                // (rows beyond the context may have told: no one sees them, and the look at V below finds nothing)
+                if (bad) s_poison[seg_i & 3u] = 1;
+                tc::fence_proxy_async_smem();
+                __syncwarp();
+                if (lane == 0) mbar_arrive(&conv_full[sl]);
+                return true;
+            };
+            if constexpr (FP8) {
+                // the tiles that come first; the others as the loop goes, each after a P is handed over and before the
+                // MMA thread needs it: wide K_{j + 1} after P(2 j), V_{j + 1} after P(2 j + 1), else V_{u + 1} and K_{u + 2}
+#pragma unroll 1
+                for (int i = 0; ok && i <= ahead; ++i) ok = convert(i == ahead, i == ahead ? 0 : i);
+                if (!ok) break;
+            }
             for (int u = 0; u < U; ++u) {
                 const uint32_t g = g0 + (uint32_t)u, i = g & 1u;
                 const int half = kLanes == 1 ? 0 : wide ? u & 1 : x, j = wide ? u >> 1 : u;
@@ -616,6 +732,19 @@ __global__ void __launch_bounds__(TreeLayout<D>::kThreads, 1)
                     tc::tmem_ld32(tS, *reinterpret_cast<float(*)[32]>(&v[0]));
                     tc::tmem_ld32(tS + 32, *reinterpret_cast<float(*)[32]>(&v[32]));
                     tc::tmem_wait_ld();
+                    if constexpr (FP8) {
+                        // the K row scales (written by all the warps: this barrier says so again, to this one)
+                        const uint32_t it = ring_item(0, j);
+                        if (!(ok = mbar_wait(&conv_full[it % ring], (it / ring) & 1u, abort_flag, a.err))) break;
+                        const float4 *ks = reinterpret_cast<const float4 *>(smem + L::kKScaleOff) + ((tiles0 + (uint32_t)j) & 3u) * 32u + half * (kSub / 4);
+#pragma unroll
+                        for (int k = 0; k < kSub / 4; ++k) {
+                            const float4 f = ks[k];
+                            const float2 p = fmul2(make_float2(v[4 * k], v[4 * k + 1]), make_float2(f.x, f.y));
+                            const float2 q = fmul2(make_float2(v[4 * k + 2], v[4 * k + 3]), make_float2(f.z, f.w));
+                            v[4 * k] = p.x, v[4 * k + 1] = p.y, v[4 * k + 2] = q.x, v[4 * k + 3] = q.y;
+                        }
+                    }
                     if (tail) {
 #pragma unroll
                         for (int k = 0; k < kSub; ++k) v[k] = (vis[k / 32] >> (k % 32)) & 1u ? v[k] : -INFINITY;
@@ -684,7 +813,7 @@ __global__ void __launch_bounds__(TreeLayout<D>::kThreads, 1)
                 // narrow lane does its half of the tile, lane A of a wide block all of it with the first half
                 // (its products come before lane B's).
                 const int tile_j0 = j0 - half * kSub;  // tree index of the tile's first key
-                if (wide ? x == 0 && half == 0 && tile_j0 + kBN > 0 : tail) {
+                if (!FP8 && (wide ? x == 0 && half == 0 && tile_j0 + kBN > 0 : tail)) {
                     const uint32_t vi = item + j + min(T, ahead + j);
                     if (!(ok = mbar_wait(&kv_full[vi % ring], (vi / ring) & 1u, abort_flag, a.err))) break;
                     uint8_t *const sV = sRing + (vi % ring) * L::kTileBytes;
@@ -716,6 +845,14 @@ __global__ void __launch_bounds__(TreeLayout<D>::kThreads, 1)
                 tc::fence_before_sync();
                 __syncwarp();
                 if (lane == 0) mbar_arrive(&p_full[i]);
+                if constexpr (FP8) {
+#pragma unroll 1
+                    for (int i2 = 0; ok && i2 < 2; ++i2) {
+                        const int kv = wide ? u & 1 : 1 - i2, jn = wide ? j + 1 : kv ? u + 1 : u + 2;
+                        if (jn < T && !(wide && i2)) ok = convert(kv, jn);
+                    }
+                    if (!ok) break;
+                }
             }
             if (!ok) break;
             g0 += (uint32_t)U;
@@ -764,20 +901,23 @@ __global__ void __launch_bounds__(TreeLayout<D>::kThreads, 1)
                 uint8_t *out = static_cast<uint8_t *>(part ? static_cast<void *>(a.part_o) : a.out);
                 const long long row_bytes = D * (f32 ? 4 : 2);
                 const long long dst_row = row_ok ? (long long)orow * row_bytes : -1;
-                uint8_t *stage = smem + L::kStageOff + (warp - 4) * 4096;
-                auto stage16 = [&](int c, const uint4 &v) {  // 16-byte piece c of this lane's row
-                    *reinterpret_cast<uint4 *>(stage + lane * 128 + ((c ^ (lane & 7)) << 4)) = v;
-                };
+                constexpr int kStageRow = L::kStageRow, kPieces = kStageRow / 16;  // 16-byte pieces of a row at a time
+                uint8_t *stage = smem + L::kStageOff + (warp - 4) * 32 * kStageRow;
+                auto place = [&](int rr, int c) { return stage + rr * kStageRow + ((c ^ (rr & (kPieces - 1))) << 4); };
                 auto flush = [&](int col_bytes) {
                     __syncwarp();
 #pragma unroll
-                    for (int i = 0; i < 8; ++i) {
-                        const int rr = i * 4 + (lane >> 3);
+                    for (int i = 0; i < kPieces; ++i) {
+                        const int rr = i * (32 / kPieces) + lane / kPieces, c = lane % kPieces;
                         const long long d = __shfl_sync(0xffffffffu, dst_row, rr);
-                        const uint4 v = *reinterpret_cast<const uint4 *>(stage + rr * 128 + (((lane & 7) ^ (rr & 7)) << 4));
-                        if (d >= 0) *reinterpret_cast<uint4 *>(out + d + col_bytes + (lane & 7) * 16) = v;
+                        const uint4 v = *reinterpret_cast<const uint4 *>(place(rr, c));
+                        if (d >= 0) *reinterpret_cast<uint4 *>(out + d + col_bytes + c * 16) = v;
                     }
                     __syncwarp();
+                };
+                auto stage16 = [&](int piece, const uint4 &v) {  // 16-byte piece of this lane's output row
+                    *reinterpret_cast<uint4 *>(place(lane, piece % kPieces)) = v;
+                    if (piece % kPieces == kPieces - 1) flush((piece + 1 - kPieces) * 16);
                 };
                 // a weight of 0 (a lane that saw nothing) takes nothing, whatever the output holds
                 const bool use_a = fa != 0.f, use_b = split && fb != 0.f;
@@ -809,10 +949,16 @@ __global__ void __launch_bounds__(TreeLayout<D>::kThreads, 1)
                             if (pb < 0 || pb >= a.cache.num_blocks) pb = 0;
                             const size_t row = (((size_t)pb * 2 + 1) * a.cache.num_kv_heads + s.unit / a.head_groups) *
                                                    a.cache.block_size + (pos & (a.cache.block_size - 1));
-                            const uint16_t *vp = static_cast<const uint16_t *>(a.cache.ptr) + row * D + cc * 32;
 #pragma unroll 1
                             for (int i = 0; i < 4; ++i) {
-                                const uint4 raw = __ldg(reinterpret_cast<const uint4 *>(vp) + i);
+                                uint4 raw;  // 8 values as the products would read them
+                                if constexpr (FP8) {
+                                    bool none = false;
+                                    raw = values_of<BF16>(__ldg(static_cast<const uint2 *>(a.cache.ptr) + row * (D / 8) + cc * 4 + i),
+                                                          __ldg(a.cache.scales + row), false, none);
+                                } else {
+                                    raw = __ldg(static_cast<const uint4 *>(a.cache.ptr) + row * (D / 8) + cc * 4 + i);
+                                }
                                 if (!(nonfinite_pair<BF16>(raw.x) || nonfinite_pair<BF16>(raw.y) ||
                                       nonfinite_pair<BF16>(raw.z) || nonfinite_pair<BF16>(raw.w)))
                                     continue;
@@ -831,17 +977,15 @@ __global__ void __launch_bounds__(TreeLayout<D>::kThreads, 1)
                     if (f32) {
 #pragma unroll
                         for (int q = 0; q < 8; ++q)
-                            stage16(q, make_uint4(__float_as_uint(o[4 * q]), __float_as_uint(o[4 * q + 1]),
-                                                  __float_as_uint(o[4 * q + 2]), __float_as_uint(o[4 * q + 3])));
-                        flush(cc * 128);
+                            stage16(cc * 8 + q, make_uint4(__float_as_uint(o[4 * q]), __float_as_uint(o[4 * q + 1]),
+                                                           __float_as_uint(o[4 * q + 2]), __float_as_uint(o[4 * q + 3])));
                     } else {
 #pragma unroll
                         for (int q = 0; q < 4; ++q)
-                            stage16((cc & 1) * 4 + q,
+                            stage16(cc * 4 + q,
                                     make_uint4(pack_pair<BF16>(o[8 * q], o[8 * q + 1]), pack_pair<BF16>(o[8 * q + 2], o[8 * q + 3]),
                                                pack_pair<BF16>(o[8 * q + 4], o[8 * q + 5]),
                                                pack_pair<BF16>(o[8 * q + 6], o[8 * q + 7])));
-                        if (cc & 1) flush((cc >> 1) * 128);
                     }
                 }
             }
@@ -856,6 +1000,7 @@ __global__ void __launch_bounds__(TreeLayout<D>::kThreads, 1)
                 mbar_arrive(&seg_empty[seg_i % kSegs]);
             }
             item += 2 * T;
+            tiles0 += (uint32_t)T;
         }
     }
     tc::fence_before_sync();
@@ -947,9 +1092,9 @@ __global__ void __launch_bounds__(256) tree_merge_kernel(TreeArgs a) {
     pdl_launch_dependents();
 }
 
-template <int D, bool BF16>
+template <int D, bool BF16, bool FP8 = false>
 cudaError_t launch_tree_t(const TreeArgs &a, int grid, cudaStream_t s) {
-    using L = TreeLayout<D>;
+    using L = TreeLayout<D, FP8>;
     CUtensorMap tm_q, tm_kv;
     cudaError_t e = encode_q_group_map(a.q, BF16 ? 1 : 0, a.total_q, a.num_q_heads, D, a.unit_heads, a.tile_nodes, &tm_q);
     if (e != cudaSuccess) return e;
@@ -957,7 +1102,7 @@ cudaError_t launch_tree_t(const TreeArgs &a, int grid, cudaStream_t s) {
     if (e != cudaSuccess) return e;
     const DeviceInfo &info = device_info();
     if ((int)L::kSmem > info.max_smem) return cudaErrorNotSupported;
-    auto kern = tree_kernel<D, BF16>;
+    auto kern = tree_kernel<D, BF16, FP8>;
     static DeviceFlags configured;
     if (!configured.test(info.device)) {
         e = set_smem_attributes(kern, info.max_smem);
@@ -973,6 +1118,10 @@ cudaError_t launch_tree_t(const TreeArgs &a, int grid, cudaStream_t s) {
 
 cudaError_t launch_tree(const TreeArgs &a, int grid, cudaStream_t s) {
     const bool bf16 = a.cache.dtype == 1;
+    if (a.cache.fp8) {
+        if (a.cache.head_dim == 128) return bf16 ? launch_tree_t<128, true, true>(a, grid, s) : launch_tree_t<128, false, true>(a, grid, s);
+        return bf16 ? launch_tree_t<64, true, true>(a, grid, s) : launch_tree_t<64, false, true>(a, grid, s);
+    }
     switch (a.cache.head_dim) {
         case 256: return bf16 ? launch_tree_t<256, true>(a, grid, s) : launch_tree_t<256, false>(a, grid, s);
         case 128: return bf16 ? launch_tree_t<128, true>(a, grid, s) : launch_tree_t<128, false>(a, grid, s);

@@ -66,7 +66,8 @@ def test_tree_refusals(lib):
         assert call_tree(lib, **kw) == INVALID, kw
     assert call_tree(lib, dt=1) == UNSUPPORTED          # bf16 out of an fp16 cache
     assert call_tree(lib, mb=1 << 27) == UNSUPPORTED    # 2^31 tokens
-    assert call_tree(lib, cache(fmt=1, scales=4096)) == UNSUPPORTED
+    assert call_tree(lib, cache(d=256, fmt=1, scales=4096)) == UNSUPPORTED
+    assert call_tree(lib, cache(fmt=1)) == INVALID      # an FP8 cache without its scales
     assert call_tree(lib, cache(d=96)) == UNSUPPORTED
     need = pkv.tree_workspace_size(4, 2, 128, 8)
     assert call_tree(lib, bytes=need - 1) == WORKSPACE

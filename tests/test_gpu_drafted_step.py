@@ -72,10 +72,9 @@ def test_accepted_path_leaves_the_sequential_cache(hq, hkv, d, bs, fp8):
 
     paths = [path_to(p, a) for p, a in zip(parents, accepted)]
     start = [sum(n[:b]) for b in range(batch)]
-    if not fp8:
-        mask = W.tree_mask(parents).cuda()
-        out = pkv.paged_attn_tree(cache, q, mask, W.cu_lens(n).cuda(), i32([c + k for c, k in zip(ctx, n)]), table,
-                                  max_q_len=max(n), out_dtype=torch.float32)
+    mask = W.tree_mask(parents).cuda()
+    out = pkv.paged_attn_tree(cache, q, mask, W.cu_lens(n).cuda(), i32([c + k for c, k in zip(ctx, n)]), table,
+                              max_q_len=max(n), out_dtype=torch.float32, scales=scales)
 
     # the accepted path moves to the front of the drafted rows, whose pages' other rows stay the draft's
     keep = [ctx[b] + i for b in range(batch) for i in paths[b]]
@@ -90,14 +89,15 @@ def test_accepted_path_leaves_the_sequential_cache(hq, hkv, d, bs, fp8):
         new = [1 if b in live else 0 for b in range(batch)]
         x = torch.stack([draft[start[b] + paths[b][step]] for b in live])
         qs = append(seq, seq_scales, x, new, [ctx[b] + step for b in range(batch)], i32([ctx[b] + step for b in live]))
-        if not fp8:
-            # each step's query attends to what is cached by then: the tree's row of that node
-            lens = i32([ctx[b] + step + 1 for b in live])
-            ref = pkv.paged_attn_decode(seq, qs, table[live].contiguous(), lens, out_dtype=torch.float32)
-            for i, b in enumerate(live):
-                got = out[start[b] + paths[b][step]]
-                # both sides sum in FP32: the score's 0.9 D^1.5 2^-24 and P's 2^-17, twice each, of max|v| < 6
-                assert (got - ref[i]).abs().max() <= 4 * (0.9 * d ** 1.5 * 2.0 ** -24 + 2.0 ** -17) * 6
+        # each step's query attends to what is cached by then: the tree's row of that node
+        lens = i32([ctx[b] + step + 1 for b in live])
+        ref = pkv.paged_attn_decode(seq, qs, table[live].contiguous(), lens, out_dtype=torch.float32, scales=seq_scales)
+        for i, b in enumerate(live):
+            got = out[start[b] + paths[b][step]]
+            # both sides sum in FP32: the score's 0.9 D^1.5 2^-24 and P's 2^-17, twice each, of max|v| < 6; over an FP8 cache
+            # the tree's values are rounded to bf16 (half a step, 2^-8) and the decode's weights to f16 (2^-11)
+            tol = 4 * (0.9 * d ** 1.5 * 2.0 ** -24 + 2.0 ** -17) + (2.0 ** -8 + 2.0 ** -10 if fp8 else 0.0)
+            assert (got - ref[i]).abs().max() <= tol * 6
     for b in range(batch):
         for p in range(ctx[b] + len(paths[b])):
             pg, off = int(table[b, p // bs]), p % bs
