@@ -44,6 +44,8 @@
 // they are zeroed for the product and, for the rows that do see them, put back in the output.
 #include <cuda.h>
 
+#include <type_traits>
+
 #include "pkv_device.cuh"
 #include "pkv_internal.h"
 #include "tcgen05.cuh"
@@ -163,22 +165,58 @@ __device__ __forceinline__ uint32_t remainder_pair(float a, float b, uint32_t hi
     return pack_pair<false>(a - f.x, b - f.y);
 }
 
-// Eight E4M3 codes (8 bytes) times `scale` as 16-bit values; `drop`: values that are not finite become 0 (told in `bad`).
-template <bool BF16>
-__device__ __forceinline__ uint4 values_of(const uint2 &codes, float scale, bool drop, bool &bad) {
-    float2 f[4];
-    unpack_e4m3x8(codes, f);
+// E4M3 codes as 16-bit values, on the integer pipe as far as it goes: s.eeee.mmm (bias 7) in the place of an f16's
+// s.0eeee.mmm0000000 (bias 15) is the code's value times 2^-8, exactly, subnormal codes included; 0x7f (NaN) would read as
+// 480 and is told apart where it matters.
+constexpr float kCodeFactorInv = 256.f;
+
+// Two of the four codes of w, by the byte permutation `sel` (0x4140: the first two, 0x4342: the others), as an f16 pair.
+__device__ __forceinline__ uint32_t code_pair(uint32_t w, uint32_t sel) {
+    const uint32_t t = __byte_perm(w, 0u, sel);
+    return (t + (t & 0x00800080u)) << 7;
+}
+
+// Whether one of the four codes of w is a NaN.
+__device__ __forceinline__ bool has_nan_code(uint32_t w) {
+    // a byte x with x & 0x7f = 0x7f: adding 1 to its seven bits carries into the eighth
+    return (((w & 0x7f7f7f7fu) + 0x01010101u) & 0x80808080u) != 0u;
+}
+
+// Eight codes (8 bytes) as 16-bit values: K, the codes' values times 2^-8 (exact); V, times 256 `scale` in FP32, so the
+// values themselves, rounded once. NaN codes are NaN.
+template <bool BF16, bool V>
+__device__ __forceinline__ uint4 values_of(const uint2 &codes, float scale) {
     uint32_t w[4];
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
-        f[i] = fmul2(f[i], make_float2(scale, scale));
-        w[i] = pack_pair<BF16>(f[i].x, f[i].y);
-        if (drop && nonfinite_pair<BF16>(w[i])) {
-            bad = true;
-            w[i] = drop_nonfinite<BF16>(w[i]);
+        const uint32_t h = code_pair(i < 2 ? codes.x : codes.y, i & 1 ? 0x4342u : 0x4140u);
+        if constexpr (!BF16 && !V) {
+            w[i] = h;
+        } else {
+            float2 f = __half22float2(*reinterpret_cast<const __half2 *>(&h));
+            if constexpr (V) f = fmul2(f, make_float2(scale, scale));
+            w[i] = pack_pair<BF16>(f.x, f.y);
+        }
+    }
+    if (has_nan_code(codes.x) || has_nan_code(codes.y)) {
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            const uint32_t c = (i < 2 ? codes.x : codes.y) >> (i & 1 ? 16 : 0);
+            if ((c & 0x7fu) == 0x7fu) w[i] |= 0x7fffu;
+            if ((c & 0x7f00u) == 0x7f00u) w[i] |= 0x7fff0000u;
         }
     }
     return make_uint4(w[0], w[1], w[2], w[3]);
+}
+
+template <bool BF16>
+__device__ __forceinline__ bool nonfinite8(const uint4 &v) {
+    return nonfinite_pair<BF16>(v.x) || nonfinite_pair<BF16>(v.y) || nonfinite_pair<BF16>(v.z) || nonfinite_pair<BF16>(v.w);
+}
+
+template <bool BF16>
+__device__ __forceinline__ uint4 drop_nonfinite8(const uint4 &v) {
+    return make_uint4(drop_nonfinite<BF16>(v.x), drop_nonfinite<BF16>(v.y), drop_nonfinite<BF16>(v.z), drop_nonfinite<BF16>(v.w));
 }
 
 template <int D, bool BF16, bool FP8>
@@ -660,43 +698,45 @@ __global__ void __launch_bounds__(TreeLayout<D, FP8>::kThreads, 1)
                 const float *const sc = reinterpret_cast<const float *>(smem + L::kScaleOff) + sl * 128u;
                 const int first = (warp - 4) * 16, start = (s.t0 + j) * kBN;
                 const int n_valid = s.len - start, drafted = s.len - s.n - start;  // rows from here on
-                bool bad = false;
-                if constexpr (D == 128) {
-                    // a row's codes lie where the second half of its values goes: 8 lanes read it whole, then write
+                // head_dim 128: 8 lanes a row of codes, which lie where the second half of the row's values goes (the warp
+                // reads its rows before it writes any); head_dim 64: 4 lanes a row, the codes in a place of their own
+                constexpr int kLanesRow = D / 16, kRowsStep = 32 / kLanesRow, kSteps = 16 / kRowsStep;
+                const int c = lane % kLanesRow, hf = c >> 2, k0 = 2 * (c & 3);
+                uint4 raw[kSteps];
 #pragma unroll
-                    for (int i = 0; i < 4; ++i) {
-                        const int row = first + 4 * i + (lane >> 3), c = lane & 7, hf = c >> 2, k0 = 2 * (c & 3);
-                        const uint4 raw = *reinterpret_cast<const uint4 *>(tile + L::kTileHalf + row * 128 + ((c ^ (row & 7)) << 4));
-                        __syncwarp();
-                        const float scale = kv ? sc[row] : 1.f;
-                        const bool drop = kv && row >= drafted;
-                        uint4 v0 = values_of<BF16>(make_uint2(raw.x, raw.y), scale, drop, bad);
-                        uint4 v1 = values_of<BF16>(make_uint2(raw.z, raw.w), scale, drop, bad);
-                        if (row >= n_valid) v0 = v1 = make_uint4(0, 0, 0, 0);
+                for (int i = 0; i < kSteps; ++i) {
+                    const int row = first + kRowsStep * i + lane / kLanesRow;
+                    raw[i] = D == 128 ? *reinterpret_cast<const uint4 *>(tile + L::kTileHalf + row * 128 + ((c ^ (row & 7)) << 4))
+                                      : *reinterpret_cast<const uint4 *>(smem + L::kCodeOff + sl * (kBN * 64u) + row * 64 + c * 16);
+                }
+                __syncwarp();
+                auto values = [&](auto is_v) {
+                    constexpr bool V = decltype(is_v)::value;
+                    const bool tail = n_valid < kBN || drafted < kBN;
+#pragma unroll
+                    for (int i = 0; i < kSteps; ++i) {
+                        const int row = first + kRowsStep * i + lane / kLanesRow;
+                        const float scale = V ? sc[row] * kCodeFactorInv : 1.f;
+                        uint4 v0 = values_of<BF16, V>(make_uint2(raw[i].x, raw[i].y), scale);
+                        uint4 v1 = values_of<BF16, V>(make_uint2(raw[i].z, raw[i].w), scale);
+                        if (tail) {
+                            if (row >= n_valid) {
+                                v0 = v1 = make_uint4(0, 0, 0, 0);
+                            } else if (V && row >= drafted && (nonfinite8<BF16>(v0) || nonfinite8<BF16>(v1))) {
+                                v0 = drop_nonfinite8<BF16>(v0);
+                                v1 = drop_nonfinite8<BF16>(v1);
+                                s_poison[seg_i & 3u] = 1;
+                            }
+                        }
                         uint8_t *dst = tile + hf * L::kTileHalf + row * 128;
                         *reinterpret_cast<uint4 *>(dst + ((k0 ^ (row & 7)) << 4)) = v0;
                         *reinterpret_cast<uint4 *>(dst + (((k0 + 1) ^ (row & 7)) << 4)) = v1;
                     }
-                } else if constexpr (D == 64) {
-                    const uint8_t *const codes = smem + L::kCodeOff + sl * (kBN * 64u);
-#pragma unroll
-                    for (int i = 0; i < 2; ++i) {
-                        const int row = first + 8 * i + (lane >> 2), c = lane & 3;
-                        const uint4 raw = *reinterpret_cast<const uint4 *>(codes + row * 64 + c * 16);
-                        const float scale = kv ? sc[row] : 1.f;
-                        const bool drop = kv && row >= drafted;
-                        uint4 v0 = values_of<BF16>(make_uint2(raw.x, raw.y), scale, drop, bad);
-                        uint4 v1 = values_of<BF16>(make_uint2(raw.z, raw.w), scale, drop, bad);
-                        if (row >= n_valid) v0 = v1 = make_uint4(0, 0, 0, 0);
-                        uint8_t *dst = tile + row * 128;
-                        *reinterpret_cast<uint4 *>(dst + (((2 * c) ^ (row & 7)) << 4)) = v0;
-                        *reinterpret_cast<uint4 *>(dst + (((2 * c + 1) ^ (row & 7)) << 4)) = v1;
-                    }
-                }
+                };
+                if (kv) values(std::true_type{});
+                else values(std::false_type{});
                 if (kv == 0 && lane < 16)
-                    reinterpret_cast<float *>(smem + L::kKScaleOff)[((tiles0 + (uint32_t)j) & 3u) * 128u + first + lane] = sc[first + lane];
-                // (rows beyond the context may have told: no one sees them, and the look at V below finds nothing)
-                if (bad) s_poison[seg_i & 3u] = 1;
+                    reinterpret_cast<float *>(smem + L::kKScaleOff)[((tiles0 + (uint32_t)j) & 3u) * 128u + first + lane] = sc[first + lane] * kCodeFactorInv;
                 tc::fence_proxy_async_smem();
                 __syncwarp();
                 if (lane == 0) mbar_arrive(&conv_full[sl]);
@@ -953,15 +993,12 @@ __global__ void __launch_bounds__(TreeLayout<D, FP8>::kThreads, 1)
                             for (int i = 0; i < 4; ++i) {
                                 uint4 raw;  // 8 values as the products would read them
                                 if constexpr (FP8) {
-                                    bool none = false;
-                                    raw = values_of<BF16>(__ldg(static_cast<const uint2 *>(a.cache.ptr) + row * (D / 8) + cc * 4 + i),
-                                                          __ldg(a.cache.scales + row), false, none);
+                                    raw = values_of<BF16, true>(__ldg(static_cast<const uint2 *>(a.cache.ptr) + row * (D / 8) + cc * 4 + i),
+                                                                __ldg(a.cache.scales + row) * kCodeFactorInv);
                                 } else {
                                     raw = __ldg(static_cast<const uint4 *>(a.cache.ptr) + row * (D / 8) + cc * 4 + i);
                                 }
-                                if (!(nonfinite_pair<BF16>(raw.x) || nonfinite_pair<BF16>(raw.y) ||
-                                      nonfinite_pair<BF16>(raw.z) || nonfinite_pair<BF16>(raw.w)))
-                                    continue;
+                                if (!nonfinite8<BF16>(raw)) continue;
                                 float f[8];
                                 if constexpr (BF16) unpack8(raw, f, BF16Tag());
                                 else unpack8(raw, f, F16Tag());
