@@ -165,45 +165,39 @@ __device__ __forceinline__ uint32_t remainder_pair(float a, float b, uint32_t hi
     return pack_pair<false>(a - f.x, b - f.y);
 }
 
-// E4M3 codes as 16-bit values, on the integer pipe as far as it goes: s.eeee.mmm (bias 7) in the place of an f16's
-// s.0eeee.mmm0000000 (bias 15) is the code's value times 2^-8, exactly, subnormal codes included; 0x7f (NaN) would read as
-// 480 and is told apart where it matters.
+// E4M3 codes as 16-bit values, on the integer pipe as far as it goes. A code s.eeee.mmm (bias 7) in the place of an f16's
+// s.0eeee.mmm0000000 (bias 15) is its value times 2^-8, exactly, subnormal codes included; in the place of a bf16's
+// s.0000eeee.mmm0000 (bias 127) its value times 2^-120, which one exact product brings to 2^-8. A NaN code (which only a NaN
+// input leaves) reads as 480, as in the prefill.
 constexpr float kCodeFactorInv = 256.f;
 
-// Two of the four codes of w, by the byte permutation `sel` (0x4140: the first two, 0x4342: the others), as an f16 pair.
-__device__ __forceinline__ uint32_t code_pair(uint32_t w, uint32_t sel) {
+__device__ __forceinline__ uint32_t code_pair_f16(uint32_t w, uint32_t sel) {
     const uint32_t t = __byte_perm(w, 0u, sel);
     return (t + (t & 0x00800080u)) << 7;
 }
 
-// Whether one of the four codes of w is a NaN.
-__device__ __forceinline__ bool has_nan_code(uint32_t w) {
-    // a byte x with x & 0x7f = 0x7f: adding 1 to its seven bits carries into the eighth
-    return (((w & 0x7f7f7f7fu) + 0x01010101u) & 0x80808080u) != 0u;
+__device__ __forceinline__ uint32_t code_pair_bf16(uint32_t w, uint32_t sel) {
+    const uint32_t t = __byte_perm(w, 0u, sel) << 4;
+    const uint32_t tiny = t + (t & 0x08000800u) * 15u;  // the sign from bit 11 to bit 15
+    uint32_t r;
+    asm("mul.rn.bf16x2 %0, %1, %2;" : "=r"(r) : "r"(tiny), "r"(0x77807780u));  // 2^112
+    return r;
 }
 
-// Eight codes (8 bytes) as 16-bit values: K, the codes' values times 2^-8 (exact); V, times 256 `scale` in FP32, so the
-// values themselves, rounded once. NaN codes are NaN.
+// Eight codes (8 bytes) as 16-bit values. K: the codes' values times 2^-8 (exact); V: times 256 `scale` in FP32, so the
+// values themselves, rounded once.
 template <bool BF16, bool V>
 __device__ __forceinline__ uint4 values_of(const uint2 &codes, float scale) {
     uint32_t w[4];
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
-        const uint32_t h = code_pair(i < 2 ? codes.x : codes.y, i & 1 ? 0x4342u : 0x4140u);
-        if constexpr (!BF16 && !V) {
-            w[i] = h;
-        } else {
-            float2 f = __half22float2(*reinterpret_cast<const __half2 *>(&h));
-            if constexpr (V) f = fmul2(f, make_float2(scale, scale));
+        const uint32_t four = i < 2 ? codes.x : codes.y, sel = i & 1 ? 0x4342u : 0x4140u;
+        if constexpr (V) {
+            const uint32_t h = code_pair_f16(four, sel);
+            const float2 f = fmul2(__half22float2(*reinterpret_cast<const __half2 *>(&h)), make_float2(scale, scale));
             w[i] = pack_pair<BF16>(f.x, f.y);
-        }
-    }
-    if (has_nan_code(codes.x) || has_nan_code(codes.y)) {
-#pragma unroll
-        for (int i = 0; i < 4; ++i) {
-            const uint32_t c = (i < 2 ? codes.x : codes.y) >> (i & 1 ? 16 : 0);
-            if ((c & 0x7fu) == 0x7fu) w[i] |= 0x7fffu;
-            if ((c & 0x7f00u) == 0x7f00u) w[i] |= 0x7fff0000u;
+        } else {
+            w[i] = BF16 ? code_pair_bf16(four, sel) : code_pair_f16(four, sel);
         }
     }
     return make_uint4(w[0], w[1], w[2], w[3]);
@@ -664,7 +658,8 @@ __global__ void __launch_bounds__(TreeLayout<D, FP8>::kThreads, 1)
         const uint32_t tO = tmem + L::kColO + 128u * x + lane_base;
         uint32_t g0 = 0;    // score buffers of this lane before this segment
         uint32_t item = 0;  // ring items before this segment (the V of its tile j: see the sweep)
-        uint32_t tiles0 = 0;  // FP8: key tiles before this segment
+        uint32_t tiles0 = 0;  // FP8: key tiles before this segment; the next tile to convert: ring slot, parity
+        uint32_t c_slot = 0, c_par = 0;
         uint32_t nml = 0;     // narrow segments so far
         uint32_t n_late = 0;  // segments of two buffers or more so far
         for (; next_segment(); ++seg_i) {
@@ -688,16 +683,14 @@ __global__ void __launch_bounds__(TreeLayout<D, FP8>::kThreads, 1)
             // writes for a 16-bit cache. K: the codes' own values (exact; the row scales multiply the scores); V: times the
             // row's scale, rounded to 16 bits. Rows beyond the context become 0; what is not finite in a drafted token's V
             // becomes 0 and is told.
-            auto ring_item = [&](int kv, int j) -> uint32_t {
-                return item + (kv ? (uint32_t)(j + min(T, ahead + j)) : (uint32_t)(j < ahead ? j : 2 * j - ahead + 1));
-            };
+            // The tiles go in ring order, so that a running slot and parity name them.
+            const int seg_len = s.len, seg_t0 = s.t0, seg_n = s.n;
             auto convert = [&](int kv, int j) -> bool {
-                const uint32_t it = ring_item(kv, j), sl = it % ring, par = (it / ring) & 1u;
-                if (!mbar_wait(&kv_full[sl], par, abort_flag, a.err)) return false;
-                uint8_t *const tile = sRing + sl * L::kTileBytes;
-                const float *const sc = reinterpret_cast<const float *>(smem + L::kScaleOff) + sl * 128u;
-                const int first = (warp - 4) * 16, start = (s.t0 + j) * kBN;
-                const int n_valid = s.len - start, drafted = s.len - s.n - start;  // rows from here on
+                if (!mbar_wait(&kv_full[c_slot], c_par, abort_flag, a.err)) return false;
+                uint8_t *const tile = sRing + c_slot * L::kTileBytes;
+                const float *const sc = reinterpret_cast<const float *>(smem + L::kScaleOff) + c_slot * 128u;
+                const int first = (warp - 4) * 16, start = (seg_t0 + j) * kBN;
+                const int n_valid = seg_len - start, drafted = n_valid - seg_n;  // rows from here on
                 // head_dim 128: 8 lanes a row of codes, which lie where the second half of the row's values goes (the warp
                 // reads its rows before it writes any); head_dim 64: 4 lanes a row, the codes in a place of their own
                 constexpr int kLanesRow = D / 16, kRowsStep = 32 / kLanesRow, kSteps = 16 / kRowsStep;
@@ -707,7 +700,7 @@ __global__ void __launch_bounds__(TreeLayout<D, FP8>::kThreads, 1)
                 for (int i = 0; i < kSteps; ++i) {
                     const int row = first + kRowsStep * i + lane / kLanesRow;
                     raw[i] = D == 128 ? *reinterpret_cast<const uint4 *>(tile + L::kTileHalf + row * 128 + ((c ^ (row & 7)) << 4))
-                                      : *reinterpret_cast<const uint4 *>(smem + L::kCodeOff + sl * (kBN * 64u) + row * 64 + c * 16);
+                                      : *reinterpret_cast<const uint4 *>(smem + L::kCodeOff + c_slot * (kBN * 64u) + row * 64 + c * 16);
                 }
                 __syncwarp();
                 auto values = [&](auto is_v) {
@@ -739,12 +732,16 @@ __global__ void __launch_bounds__(TreeLayout<D, FP8>::kThreads, 1)
                     reinterpret_cast<float *>(smem + L::kKScaleOff)[((tiles0 + (uint32_t)j) & 3u) * 128u + first + lane] = sc[first + lane] * kCodeFactorInv;
                 tc::fence_proxy_async_smem();
                 __syncwarp();
-                if (lane == 0) mbar_arrive(&conv_full[sl]);
+                if (lane == 0) mbar_arrive(&conv_full[c_slot]);
+                if (++c_slot == ring) {
+                    c_slot = 0;
+                    c_par ^= 1u;
+                }
                 return true;
             };
             if constexpr (FP8) {
                 // the tiles that come first; the others as the loop goes, each after a P is handed over and before the
-                // MMA thread needs it: wide K_{j + 1} after P(2 j), V_{j + 1} after P(2 j + 1), else V_{u + 1} and K_{u + 2}
+                // MMA thread needs it: wide K_{j + 1} after P(2 j), V_{j + 1} after P(2 j + 1), else K_{u + 2} and V_{u + 1}
 #pragma unroll 1
                 for (int i = 0; ok && i <= ahead; ++i) ok = convert(i == ahead, i == ahead ? 0 : i);
                 if (!ok) break;
@@ -773,9 +770,7 @@ __global__ void __launch_bounds__(TreeLayout<D, FP8>::kThreads, 1)
                     tc::tmem_ld32(tS + 32, *reinterpret_cast<float(*)[32]>(&v[32]));
                     tc::tmem_wait_ld();
                     if constexpr (FP8) {
-                        // the K row scales (written by all the warps: this barrier says so again, to this one)
-                        const uint32_t it = ring_item(0, j);
-                        if (!(ok = mbar_wait(&conv_full[it % ring], (it / ring) & 1u, abort_flag, a.err))) break;
+                        // the K row scales (the warps wrote them before conv_full, which the scores' products waited for)
                         const float4 *ks = reinterpret_cast<const float4 *>(smem + L::kKScaleOff) + ((tiles0 + (uint32_t)j) & 3u) * 32u + half * (kSub / 4);
 #pragma unroll
                         for (int k = 0; k < kSub / 4; ++k) {
@@ -888,7 +883,7 @@ __global__ void __launch_bounds__(TreeLayout<D, FP8>::kThreads, 1)
                 if constexpr (FP8) {
 #pragma unroll 1
                     for (int i2 = 0; ok && i2 < 2; ++i2) {
-                        const int kv = wide ? u & 1 : 1 - i2, jn = wide ? j + 1 : kv ? u + 1 : u + 2;
+                        const int kv = wide ? u & 1 : i2, jn = wide ? j + 1 : kv ? u + 1 : u + 2;
                         if (jn < T && !(wide && i2)) ok = convert(kv, jn);
                     }
                     if (!ok) break;
