@@ -194,6 +194,18 @@ def _on_device(index, fn, *args):
         return fn(*args)
 
 
+def _new(like, shape, dtype, stream):
+    """An empty tensor on the device of `like`, from the memory of the stream that the call runs on: work that is still
+    pending on another stream never meets it."""
+    if stream is None:
+        return like.new_empty(shape, dtype=dtype)
+    torch = _torch()
+    if not hasattr(stream, "cuda_stream"):
+        stream = torch.cuda.ExternalStream(int(stream), device=like.device)
+    with torch.cuda.stream(stream):
+        return like.new_empty(shape, dtype=dtype)
+
+
 def is_fp8_cache(cache) -> bool:
     torch = _torch()
     dt = cache.dtype
@@ -437,7 +449,7 @@ def rope_append(cache, q, k, v, inv_freq, cu_new_lens, ctx_before, block_tables,
     kp, ks = _rows(k, total, hkv, d, dtype, index, "k")
     vp, vs = _rows(v, total, hkv, d, dtype, index, "v")
     if q_out is None:
-        q_out = q.new_empty((total, hq, d))
+        q_out = _new(q, (total, hq, d), dtype, stream)
         op, os_ = q_out.data_ptr(), hq * d
     else:
         op, os_ = _rows(q_out, total, hq, d, dtype, index, "q_out")
@@ -475,13 +487,13 @@ def paged_attn_tree(cache, q, tree_mask, cu_q_lens, context_lens, block_tables, 
     if cu_q_lens.shape != (batch + 1,) or context_lens.shape != (batch,):
         raise ValueError("cu_q_lens must be [batch + 1], context_lens [batch]")
     if out is None:
-        out = q.new_empty((total_q, hq, d), dtype=out_dtype or dtype)
+        out = _new(q, (total_q, hq, d), out_dtype or dtype, stream)
     elif out.shape != q.shape:
         raise ValueError("out must have the shape of q")
     if lse is not None and lse.shape != (total_q, hq):
         raise ValueError("lse must be float32 [rows of q, Hq]")
     if workspace is None:
-        workspace = q.new_empty(lib.pkv_tree_workspace_size(hq, c.num_kv_heads, d, max_q_len), dtype=torch.uint8)
+        workspace = _new(q, (lib.pkv_tree_workspace_size(hq, c.num_kv_heads, d, max_q_len),), torch.uint8, stream)
     scale = (1.0 / math.sqrt(d)) if scale is None else float(scale)
     out_code = _dtype_code(out.dtype)
     _check(_on_device(index, lib.pkv_paged_attn_tree, c, _at(q, dtype, index, "q"), hq, _at(tree_mask, i32, index, "tree_mask"),

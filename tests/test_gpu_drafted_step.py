@@ -155,3 +155,41 @@ def test_whole_step_in_one_graph():
         torch.cuda.synchronize()
         assert torch.equal(out, got) and torch.equal(cache, kept)
     assert pkv.get_device_error() == 0
+
+
+@pytest.mark.parametrize("as_handle", [False, True])
+def test_new_tensors_belong_to_the_calls_stream(as_handle):
+    """With a `stream` of the caller's, what the call allocates is that stream's memory: work still pending on the
+    current stream, on memory freed there since, does not reach the results."""
+    g = torch.Generator().manual_seed(9)
+    hq, hkv, d, bs, n, ctx = 8, 2, 128, 16, 40, 1000
+    dt = torch.float16
+    nb = -(-(ctx + n) // bs)
+    table = torch.arange(nb, dtype=torch.int32, device="cuda")[None]
+    cache = torch.randn((nb, 2, hkv, bs, d), generator=g).to(dt).cuda()
+    q, k, v = (torch.randn((n, h, d), generator=g).to(dt).cuda() for h in (hq, hkv, hkv))
+    inv, _ = rope.rope_frequencies(d, device="cuda")
+    mask = W.tree_mask([list(range(-1, n - 1))]).cuda()
+    pos, cu, before, lens = torch.arange(n, dtype=torch.int32, device="cuda") + ctx, i32([0, n]), i32([ctx]), i32([ctx + n])
+
+    def step(stream):
+        turned = pkv.rope_append(cache, q, k, v, inv, cu, before, table, positions=pos, stream=stream)
+        return turned, pkv.paged_attn_tree(cache, turned, mask, cu, lens, table, max_q_len=n, stream=stream)
+
+    expect = [t.clone() for t in step(None)]
+    side = torch.cuda.Stream()
+    torch.cuda.synchronize()
+    torch.cuda.empty_cache()
+    # two tensors of the results' size and one of the workspace's, freed with writes to them pending
+    held = [torch.empty_like(q) for _ in range(2)]
+    held.append(torch.empty(pkv.tree_workspace_size(hq, hkv, d, n), dtype=torch.uint8, device="cuda"))
+    torch.cuda._sleep(400_000_000)
+    for t in held:
+        t.fill_(77)
+    places = {t.data_ptr() for t in held}
+    del held, t
+    got = step(side.cuda_stream if as_handle else side)
+    assert not places & {t.data_ptr() for t in got}
+    torch.cuda.synchronize()
+    assert all(torch.equal(a, b) for a, b in zip(expect, got))
+    assert pkv.get_device_error() == 0
