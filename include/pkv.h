@@ -311,7 +311,8 @@ PKV_API pkv_status pkv_paged_attn_tree(pkv_cache cache, const void *q, int num_q
  *   cu_keep       int32 [batch+1], non-decreasing from 0, at most num_keep.
  *   dst_start     int32 [batch].
  * Rows whose source lies before their destination or beyond the table, or whose page is out of the pool, are skipped and
- * flagged (PKV_ERR_DEVICE_RANGE). The destinations' pages must be the sequence's own: a page that another
+ * flagged (PKV_ERR_DEVICE_RANGE). Pools of 2^32 rows (num_blocks * 2 * num_kv_heads * block_size) and more are not
+ * supported. The destinations' pages must be the sequence's own: a page that another
  * table shares would change for both (and is undefined when the other moves rows of it in the same call). */
 PKV_API pkv_status pkv_kv_cache_compact(pkv_cache cache, const int *keep_pos, const int *cu_keep, const int *dst_start,
                                 const int *block_tables, int batch, int max_blocks_per_seq, int num_keep,

@@ -28,7 +28,7 @@ namespace {
 constexpr int kCompactThreads = 256;
 constexpr int kUnroll = 8;
 constexpr int kResident = 3;  // CTAs an SM (registers)
-// Rows are counted in 32 bits: 2^32 rows of the shortest, 64 bytes, are more than the memory holds.
+// Rows of the pool are counted in 32 bits (the entry point refuses a pool of more).
 constexpr uint32_t kNoRow = 0xffffffffu;  // nothing to move
 
 __device__ __forceinline__ uint4 ld_once(const uint4 *p) {

@@ -96,6 +96,8 @@ def test_compact_refusals(lib):
         assert call(**kw) == INVALID, kw
     assert call(cache(bs=24)) == UNSUPPORTED
     assert call(cache(fmt=1)) == INVALID
+    assert call(cache(nb=1 << 26, hkv=2, bs=16)) == UNSUPPORTED    # 2^32 rows
+    assert call(cache(nb=1 << 30, hkv=1 << 30, bs=512)) == UNSUPPORTED
     assert call(batch=0) == 0 and call(n=0) == 0
 
 
