@@ -231,7 +231,7 @@ PKV_API pkv_status pkv_paged_attn_mixed(pkv_cache cache, const void *q, int num_
  *   rotary_dim   leading elements of each head that are rotated: a multiple of 16, 0 (none) to
  *                head_dim; the others pass unrotated.
  *   interleaved  0: pair i is elements i and i + rotary_dim / 2; else elements 2i and 2i + 1.
- *   inv_freq     device FP32 [rotary_dim / 2]: pair i of a token at position p is turned by the angle
+ *   inv_freq     device FP32 [rotary_dim / 2], finite: pair i of a token at position p is turned by the angle
  *                p * inv_freq[i] (exact to FP32's precision for every int32 position). Scaling for
  *                long contexts is a choice of these values. NULL allowed when rotary_dim is 0.
  *   mscale       factor on the cosines and sines (1 for none); finite.

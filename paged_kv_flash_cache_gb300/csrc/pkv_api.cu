@@ -549,6 +549,7 @@ pkv_status pkv_rope_append(pkv_cache cache, pkv_rope rope, const void *q, long l
     if (batch == 0 || num_new_tokens == 0) return PKV_OK;
     if (!q || !k || !v || !positions || !cu_new_lens || !ctx_before || !block_tables || !q_out) return PKV_ERR_INVALID_ARG;
     if (rope.rotary_dim > 0 && !rope.inv_freq) return PKV_ERR_INVALID_ARG;
+    if (q_out == q && q_out_stride != q_stride) return PKV_ERR_INVALID_ARG;  // (a token's rows would meet another's)
     if (!aligned16(q) || !aligned16(k) || !aligned16(v) || !aligned16(q_out) || !aligned16(rope.q_weight) ||
         !aligned16(rope.k_weight))
         return PKV_ERR_INVALID_ARG;

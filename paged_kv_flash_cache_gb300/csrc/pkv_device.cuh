@@ -62,19 +62,6 @@ __device__ __forceinline__ bool mbar_try_wait(uint64_t *bar, uint32_t parity) {
     return done != 0;
 }
 
-// As mbar_try_wait, returning at once.
-__device__ __forceinline__ bool mbar_test_wait(uint64_t *bar, uint32_t parity) {
-    uint32_t done;
-    asm volatile(
-        "{\n\t.reg .pred p;\n\t"
-        "mbarrier.test_wait.parity.shared::cta.b64 p, [%1], %2;\n\t"
-        "selp.u32 %0, 1, 0, p;\n\t}"
-        : "=r"(done)
-        : "r"(smem_addr(bar)), "r"(parity)
-        : "memory");
-    return done != 0;
-}
-
 // Wait for phase `parity` of `bar` to complete.  Gives up (returns false) when
 // *abort becomes non-zero or after timeout_ns (default kWaitTimeoutNs), in which case it
 // records kErrTimeout and raises *abort so the CTA's other roles stop too.

@@ -30,8 +30,6 @@
 // instruction for it (fma.rn.f32x2), and rows of one kind in a straight line. 8192 tokens of 32 + 8 + 8 heads x 128, normed
 // (201 MB): 37 us, 81% of the copy rate; 47 us with scalar arithmetic and the kind of row decided row by row, 66 us so with one
 // vector a lane and the other element by shuffle (41 against 25 million warp instructions).
-#include <climits>
-
 #include "pkv_device.cuh"
 #include "pkv_internal.h"
 #include "tcgen05.cuh"

@@ -403,17 +403,17 @@ __global__ void __launch_bounds__(TreeLayout<D, FP8>::kThreads, 1)
                             }
                         }
                     } else {
-                    if (tc::elect_one())
-                        mbar_arrive_expect_tx(&kv_full[slot], (uint32_t)npages * box_rows * 128u * L::kHalves);
-                    for (int pg = 0; pg < npages; ++pg, dst += (uint32_t)box_rows * 128u) {
-                        const int pb = __shfl_sync(0xffffffffu, w0, page0 - first + pg);
-                        const int row = ((pb * 2 + kv) * a.cache.num_kv_heads + kvh) * bs + off;
-                        if (tc::elect_one()) {
+                        if (tc::elect_one())
+                            mbar_arrive_expect_tx(&kv_full[slot], (uint32_t)npages * box_rows * 128u * L::kHalves);
+                        for (int pg = 0; pg < npages; ++pg, dst += (uint32_t)box_rows * 128u) {
+                            const int pb = __shfl_sync(0xffffffffu, w0, page0 - first + pg);
+                            const int row = ((pb * 2 + kv) * a.cache.num_kv_heads + kvh) * bs + off;
+                            if (tc::elect_one()) {
 #pragma unroll
-                            for (int hf = 0; hf < L::kHalves; ++hf)
-                                tc::tma_load_2d_hint(dst + hf * L::kTileHalf, &tm_kv, hf * 64, row, &kv_full[slot], pol);
+                                for (int hf = 0; hf < L::kHalves; ++hf)
+                                    tc::tma_load_2d_hint(dst + hf * L::kTileHalf, &tm_kv, hf * 64, row, &kv_full[slot], pol);
+                            }
                         }
-                    }
                     }
                     used |= 1u << slot;
                     par = (par & ~(1u << slot)) | ((ph ^ 1u) << slot);

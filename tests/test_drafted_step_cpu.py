@@ -42,6 +42,7 @@ def test_rope_append_refusals(lib):
                dict(pos=None), dict(cu=None), dict(before=None), dict(bt=None), dict(out=None), dict(q=P(4100)),
                dict(k=P(4104)), dict(v=P(4098)), dict(out=P(4100)), dict(qw=P(4100)), dict(kw=P(4104))):
         assert call_rope(lib, **kw) == INVALID, kw
+    assert call_rope(lib, out=P(8192), q=P(8192), os=520) == INVALID   # in place: q's own stride
     assert call_rope(lib, rot=24) == UNSUPPORTED
     assert call_rope(lib, cache(d=96)) == UNSUPPORTED
     assert call_rope(lib, cache(ptr=0)) == INVALID
