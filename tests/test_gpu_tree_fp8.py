@@ -121,7 +121,7 @@ def test_what_is_masked_may_hold_anything(bad, d, hq):
 
 
 def test_after_append_it_agrees_with_the_prefill():
-    """A chain over the codes that kv_cache_append wrote: paged_attn_prefill's causal chunk over the same cache."""
+    """A chain is the causal chunk that paged_attn_prefill attends over the same cache."""
     from paged_kv_flash_cache_gb300 import workloads as W
     n = 24
     c = Fp8Case([500, n + 7], [n, n], 8, 2, seed=18)
