@@ -96,7 +96,7 @@ struct TreeLayout {
     static constexpr uint32_t kBarOff = kCodeOff + (FP8 && D == 64 ? kRingMax * kBN * 64u : 0u);
     static constexpr uint32_t kSegOff = kBarOff + 640;
     static constexpr uint32_t kSmem = kSegOff + kSegs * sizeof(Segment) + 1024;  // + alignment slack
-    static constexpr int kThreads = 128 * (1 + kLanes);
+    static constexpr int kThreads = 128 * (1 + kLanes + (FP8 ? 1 : 0));  // FP8: a warpgroup for the keys' codes
     // TMEM: score buffer i of lane x at 128 i + 64 x (P in its place), O of lane x at 256 + 128 x
     static constexpr uint32_t kColO = 256;
 };
@@ -213,6 +213,56 @@ __device__ __forceinline__ uint4 drop_nonfinite8(const uint4 &v) {
     return make_uint4(drop_nonfinite<BF16>(v.x), drop_nonfinite<BF16>(v.y), drop_nonfinite<BF16>(v.z), drop_nonfinite<BF16>(v.w));
 }
 
+// FP8: a warp's kRows rows of a ring tile, rows `first` on, codes to 16-bit values in the layout that TMA writes for a 16-bit
+// cache. K: the codes' own values (exact; the row scales multiply the scores); V: times the row's scale, rounded to 16 bits.
+// Rows from n_valid on (beyond the context) become 0; what is not finite in a V row from `drafted` on becomes 0. Returns
+// whether there was any of that.
+template <int D, bool BF16, bool V, int kRows>
+__device__ __forceinline__ bool convert_rows(uint8_t *tile, const uint8_t *codes64, const float *sc, int first, int n_valid, int drafted, int lane) {
+    using L = TreeLayout<D, true>;
+    // head_dim 128: 8 lanes a row of codes, which lie where the second half of the row's values goes (the warp reads its
+    // rows before it writes any); of 8 lanes, lanes 4-7 take row r ^ 5 of the chunks that lanes 0-3 take of row r: neither
+    // their reads nor their writes meet in a bank then. head_dim 64: 4 lanes a row, the codes in a place of their own.
+    constexpr int kSteps = kRows * D / 512;
+    const int c = D == 128 ? (lane & 3) + ((lane >> 1) & 4) : lane & 3, hf = c >> 2, k0 = 2 * (c & 3);
+    const int r8 = D == 128 ? (lane >> 4) ^ (lane & 4 ? 5 : 0) : lane >> 2;
+    auto row_of = [&](int i) { return first + (D == 128 ? 8 * (i >> 1) + (r8 ^ (2 * (i & 1))) : 8 * i + r8); };
+    uint4 raw[kSteps];
+#pragma unroll
+    for (int i = 0; i < kSteps; ++i) {
+        const int row = row_of(i);
+        raw[i] = *reinterpret_cast<const uint4 *>(D == 128 ? tile + L::kTileHalf + row * 128 + ((c ^ (row & 7)) << 4) : codes64 + row * 64 + c * 16);
+    }
+    __syncwarp();
+    float scale[kSteps];
+#pragma unroll
+    for (int i = 0; i < kSteps; ++i) scale[i] = V ? sc[row_of(i)] * kCodeFactorInv : 1.f;
+    bool bad = false;
+    auto run = [&](auto has_tail) {
+#pragma unroll
+        for (int i = 0; i < kSteps; ++i) {
+            const int row = row_of(i);
+            uint4 v0 = values_of<BF16, V>(make_uint2(raw[i].x, raw[i].y), scale[i]);
+            uint4 v1 = values_of<BF16, V>(make_uint2(raw[i].z, raw[i].w), scale[i]);
+            if constexpr (decltype(has_tail)::value) {
+                if (row >= n_valid) {
+                    v0 = v1 = make_uint4(0, 0, 0, 0);
+                } else if (V && row >= drafted && (nonfinite8<BF16>(v0) || nonfinite8<BF16>(v1))) {
+                    v0 = drop_nonfinite8<BF16>(v0);
+                    v1 = drop_nonfinite8<BF16>(v1);
+                    bad = true;
+                }
+            }
+            uint8_t *dst = tile + hf * L::kTileHalf + row * 128;
+            *reinterpret_cast<uint4 *>(dst + ((k0 ^ (row & 7)) << 4)) = v0;
+            *reinterpret_cast<uint4 *>(dst + (((k0 + 1) ^ (row & 7)) << 4)) = v1;
+        }
+    };
+    if (n_valid < L::kBN || (V && drafted < L::kBN)) run(std::true_type{});
+    else run(std::false_type{});
+    return bad;
+}
+
 template <int D, bool BF16, bool FP8>
 __global__ void __launch_bounds__(TreeLayout<D, FP8>::kThreads, 1)
     tree_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CUtensorMap tm_kv, TreeArgs a) {
@@ -270,7 +320,7 @@ __global__ void __launch_bounds__(TreeLayout<D, FP8>::kThreads, 1)
         mbar_init(ml_full, kSoftmaxWarps);
         for (int i = 0; i < kSegs; ++i) {
             mbar_init(&seg_full[i], 1);
-            mbar_init(&seg_empty[i], 3 + kSoftmaxWarps);  // producers, MMA, softmax warps
+            mbar_init(&seg_empty[i], 3 + kSoftmaxWarps + (FP8 ? 4 : 0));  // producers, MMA, softmax, conversion
         }
         mbar_init(drain, 1);
         *s_total = 0;
@@ -648,9 +698,44 @@ __global__ void __launch_bounds__(TreeLayout<D, FP8>::kThreads, 1)
             if (lane == 0) a.merge[blockIdx.x] = left;
             if (ok) publish(Segment{});
         }
+    } else if (FP8 && warp >= 12) {
+        // ============================ FP8: the K tiles' codes to 16-bit values ============================
+        if constexpr (FP8) {
+            tc::regs_dec<96>();
+            uint32_t slot = 0, par = 0;  // ring slot and parity of the K tile in work
+            uint32_t tiles = 0;          // key tiles so far
+            auto step = [&](uint32_t n) {
+                slot += n;
+                if (slot >= ring) {
+                    slot -= ring;
+                    par ^= 1u;
+                }
+            };
+            for (; next_segment(); ++seg_i) {
+                const Segment &s = segs[seg_i % kSegs];
+                const bool wide = s.nodes > a.tile_nodes;
+                const int T = s.t1 - s.t0, ahead = wide ? 1 : min(2, T), first = (warp - 12) * 32;
+                bool ok = true;
+                for (int j = 0; j < T; ++j, ++tiles) {
+                    if (j > 0) step(j < ahead ? 1u : 2u);
+                    if (!(ok = mbar_wait(&kv_full[slot], par, abort_flag, a.err))) break;
+                    const float *const sc = reinterpret_cast<const float *>(smem + L::kScaleOff) + slot * 128u;
+                    convert_rows<D, BF16, false, 32>(sRing + slot * L::kTileBytes, smem + L::kCodeOff + slot * (kBN * 64u), sc, first,
+                                                     s.len - (s.t0 + j) * kBN, 0, lane);
+                    reinterpret_cast<float *>(smem + L::kKScaleOff)[(tiles & 3u) * 128u + first + lane] = sc[first + lane] * kCodeFactorInv;
+                    tc::fence_proxy_async_smem();
+                    __syncwarp();
+                    if (lane == 0) mbar_arrive_n(&conv_full[slot], 2);  // (a V tile has 8 warps' arrivals)
+                }
+                if (!ok) break;
+                step((uint32_t)ahead + 1u);  // (behind the segment's last V)
+                __syncwarp();
+                if (lane == 0) mbar_arrive(&seg_empty[seg_i % kSegs]);
+            }
+        }
     } else {
         // ================================ softmax + output: lane x ================================
-        if constexpr (kLanes == 2) tc::regs_inc<208>();
+        if constexpr (kLanes == 2) tc::regs_inc<FP8 ? 168 : 208>();
         const int x = (warp - 4) >> 2, w4 = warp & 3;
         const int r = w4 * 32 + lane;  // row of the tile = TMEM lane
         const uint32_t lane_base = (uint32_t)(w4 * 32) << 16;
@@ -658,8 +743,15 @@ __global__ void __launch_bounds__(TreeLayout<D, FP8>::kThreads, 1)
         const uint32_t tO = tmem + L::kColO + 128u * x + lane_base;
         uint32_t g0 = 0;    // score buffers of this lane before this segment
         uint32_t item = 0;  // ring items before this segment (the V of its tile j: see the sweep)
-        uint32_t tiles0 = 0;  // FP8: key tiles before this segment; the next tile to convert: ring slot, parity
-        uint32_t c_slot = 0, c_par = 0;
+        uint32_t tiles0 = 0;  // FP8: key tiles before this segment
+        uint32_t c_slot = 0, c_par = 0;  // FP8: ring slot and parity of the V tile in work
+        auto c_step = [&](uint32_t n) {
+            c_slot += n;
+            if (c_slot >= ring) {
+                c_slot -= ring;
+                c_par ^= 1u;
+            }
+        };
         uint32_t nml = 0;     // narrow segments so far
         uint32_t n_late = 0;  // segments of two buffers or more so far
         for (; next_segment(); ++seg_i) {
@@ -679,72 +771,25 @@ __global__ void __launch_bounds__(TreeLayout<D, FP8>::kThreads, 1)
             };
             float m = -INFINITY, l = 0.f;
             bool ok = true;
-            // FP8: this warp's 16 rows of tile j's K (kv 0) or V (kv 1), codes to 16-bit values in the layout that TMA
-            // writes for a 16-bit cache. K: the codes' own values (exact; the row scales multiply the scores); V: times the
-            // row's scale, rounded to 16 bits. Rows beyond the context become 0; what is not finite in a drafted token's V
-            // becomes 0 and is told.
-            // The tiles go in ring order, so that a running slot and parity name them.
+            // FP8: this warp's 16 rows of V_j, in the order of the tiles, V_0 now and V_{j + 1} after the last P over V_j is
+            // handed over. The keys' codes are the conversion warps', a tile and more ahead: 319 us for 16 x 64 nodes, 138
+            // for the long context (all conversions here: 336 and 169; all of them there: 345 and 151).
             const int seg_len = s.len, seg_t0 = s.t0, seg_n = s.n;
-            auto convert = [&](int kv, int j) -> bool {
+            auto convert_v = [&](int j) -> bool {
+                c_step(j == 0 ? (uint32_t)ahead : ahead + j <= T ? 2u : 1u);
                 if (!mbar_wait(&kv_full[c_slot], c_par, abort_flag, a.err)) return false;
-                uint8_t *const tile = sRing + c_slot * L::kTileBytes;
-                const float *const sc = reinterpret_cast<const float *>(smem + L::kScaleOff) + c_slot * 128u;
-                const int first = (warp - 4) * 16, start = (seg_t0 + j) * kBN;
-                const int n_valid = seg_len - start, drafted = n_valid - seg_n;  // rows from here on
-                // head_dim 128: 8 lanes a row of codes, which lie where the second half of the row's values goes (the warp
-                // reads its rows before it writes any); head_dim 64: 4 lanes a row, the codes in a place of their own
-                constexpr int kLanesRow = D / 16, kRowsStep = 32 / kLanesRow, kSteps = 16 / kRowsStep;
-                const int c = lane % kLanesRow, hf = c >> 2, k0 = 2 * (c & 3);
-                uint4 raw[kSteps];
-#pragma unroll
-                for (int i = 0; i < kSteps; ++i) {
-                    const int row = first + kRowsStep * i + lane / kLanesRow;
-                    raw[i] = D == 128 ? *reinterpret_cast<const uint4 *>(tile + L::kTileHalf + row * 128 + ((c ^ (row & 7)) << 4))
-                                      : *reinterpret_cast<const uint4 *>(smem + L::kCodeOff + c_slot * (kBN * 64u) + row * 64 + c * 16);
-                }
-                __syncwarp();
-                auto values = [&](auto is_v) {
-                    constexpr bool V = decltype(is_v)::value;
-                    const bool tail = n_valid < kBN || drafted < kBN;
-#pragma unroll
-                    for (int i = 0; i < kSteps; ++i) {
-                        const int row = first + kRowsStep * i + lane / kLanesRow;
-                        const float scale = V ? sc[row] * kCodeFactorInv : 1.f;
-                        uint4 v0 = values_of<BF16, V>(make_uint2(raw[i].x, raw[i].y), scale);
-                        uint4 v1 = values_of<BF16, V>(make_uint2(raw[i].z, raw[i].w), scale);
-                        if (tail) {
-                            if (row >= n_valid) {
-                                v0 = v1 = make_uint4(0, 0, 0, 0);
-                            } else if (V && row >= drafted && (nonfinite8<BF16>(v0) || nonfinite8<BF16>(v1))) {
-                                v0 = drop_nonfinite8<BF16>(v0);
-                                v1 = drop_nonfinite8<BF16>(v1);
-                                s_poison[seg_i & 3u] = 1;
-                            }
-                        }
-                        uint8_t *dst = tile + hf * L::kTileHalf + row * 128;
-                        *reinterpret_cast<uint4 *>(dst + ((k0 ^ (row & 7)) << 4)) = v0;
-                        *reinterpret_cast<uint4 *>(dst + (((k0 + 1) ^ (row & 7)) << 4)) = v1;
-                    }
-                };
-                if (kv) values(std::true_type{});
-                else values(std::false_type{});
-                if (kv == 0 && lane < 16)
-                    reinterpret_cast<float *>(smem + L::kKScaleOff)[((tiles0 + (uint32_t)j) & 3u) * 128u + first + lane] = sc[first + lane] * kCodeFactorInv;
+                const int n_valid = seg_len - (seg_t0 + j) * kBN;
+                if (convert_rows<D, BF16, true, 16>(sRing + c_slot * L::kTileBytes, smem + L::kCodeOff + c_slot * (kBN * 64u),
+                                                    reinterpret_cast<const float *>(smem + L::kScaleOff) + c_slot * 128u,
+                                                    (warp - 4) * 16, n_valid, n_valid - seg_n, lane))
+                    s_poison[seg_i & 3u] = 1;
                 tc::fence_proxy_async_smem();
                 __syncwarp();
                 if (lane == 0) mbar_arrive(&conv_full[c_slot]);
-                if (++c_slot == ring) {
-                    c_slot = 0;
-                    c_par ^= 1u;
-                }
                 return true;
             };
             if constexpr (FP8) {
-                // the tiles that come first; the others as the loop goes, each after a P is handed over and before the
-                // MMA thread needs it: wide K_{j + 1} after P(2 j), V_{j + 1} after P(2 j + 1), else K_{u + 2} and V_{u + 1}
-#pragma unroll 1
-                for (int i = 0; ok && i <= ahead; ++i) ok = convert(i == ahead, i == ahead ? 0 : i);
-                if (!ok) break;
+                if (!convert_v(0)) break;
             }
             for (int u = 0; u < U; ++u) {
                 const uint32_t g = g0 + (uint32_t)u, i = g & 1u;
@@ -881,12 +926,7 @@ __global__ void __launch_bounds__(TreeLayout<D, FP8>::kThreads, 1)
                 __syncwarp();
                 if (lane == 0) mbar_arrive(&p_full[i]);
                 if constexpr (FP8) {
-#pragma unroll 1
-                    for (int i2 = 0; ok && i2 < 2; ++i2) {
-                        const int kv = wide ? u & 1 : i2, jn = wide ? j + 1 : kv ? u + 1 : u + 2;
-                        if (jn < T && !(wide && i2)) ok = convert(kv, jn);
-                    }
-                    if (!ok) break;
+                    if ((!wide || (u & 1)) && j + 1 < T && !(ok = convert_v(j + 1))) break;
                 }
             }
             if (!ok) break;
@@ -1033,6 +1073,7 @@ __global__ void __launch_bounds__(TreeLayout<D, FP8>::kThreads, 1)
             }
             item += 2 * T;
             tiles0 += (uint32_t)T;
+            if constexpr (FP8) c_step(1u);  // (the last V was the segment's last item)
         }
     }
     tc::fence_before_sync();
