@@ -167,40 +167,48 @@ __device__ __forceinline__ uint32_t remainder_pair(float a, float b, uint32_t hi
 
 // E4M3 codes as 16-bit values, on the integer pipe as far as it goes. A code s.eeee.mmm (bias 7) in the place of an f16's
 // s.0eeee.mmm0000000 (bias 15) is its value times 2^-8, exactly, subnormal codes included; in the place of a bf16's
-// s.0000eeee.mmm0000 (bias 127) its value times 2^-120, which one exact product brings to 2^-8. A NaN code (which only a NaN
-// input leaves) reads as 480, as in the prefill.
+// s.0000eeee.mmm0000 (bias 127) its value times 2^-120. One exact 16-bit product with a power of two (a pair in `factor`)
+// brings it to where it is wanted: the keys to 2^-8, the values to their row scale's power of two. A NaN code (which only
+// a NaN input leaves) reads as 480, as in the prefill.
 constexpr float kCodeFactorInv = 256.f;
 
-__device__ __forceinline__ uint32_t code_pair_f16(uint32_t w, uint32_t sel) {
+template <bool BF16, bool V>
+__device__ __forceinline__ uint32_t code_pair(uint32_t w, uint32_t sel, uint32_t factor) {
     const uint32_t t = __byte_perm(w, 0u, sel);
-    return (t + (t & 0x00800080u)) << 7;
-}
-
-__device__ __forceinline__ uint32_t code_pair_bf16(uint32_t w, uint32_t sel) {
-    const uint32_t t = __byte_perm(w, 0u, sel) << 4;
-    const uint32_t tiny = t + (t & 0x08000800u) * 15u;  // the sign from bit 11 to bit 15
     uint32_t r;
-    asm("mul.rn.bf16x2 %0, %1, %2;" : "=r"(r) : "r"(tiny), "r"(0x77807780u));  // 2^112
+    if constexpr (BF16) {
+        const uint32_t u = t << 4, tiny = u + (u & 0x08000800u) * 15u;  // the sign from bit 11 to bit 15
+        asm("mul.rn.bf16x2 %0, %1, %2;" : "=r"(r) : "r"(tiny), "r"(factor));
+    } else {
+        r = (t + (t & 0x00800080u)) << 7;
+        if constexpr (V) asm("mul.rn.f16x2 %0, %0, %1;" : "+r"(r) : "r"(factor));
+    }
     return r;
 }
 
-// Eight codes (8 bytes) as 16-bit values. K: the codes' values times 2^-8 (exact); V: times 256 `scale` in FP32, so the
-// values themselves, rounded once.
+// Eight codes (8 bytes) as 16-bit values: K times 2^-8, V as `factor` says.
 template <bool BF16, bool V>
-__device__ __forceinline__ uint4 values_of(const uint2 &codes, float scale) {
-    uint32_t w[4];
-#pragma unroll
-    for (int i = 0; i < 4; ++i) {
-        const uint32_t four = i < 2 ? codes.x : codes.y, sel = i & 1 ? 0x4342u : 0x4140u;
-        if constexpr (V) {
-            const uint32_t h = code_pair_f16(four, sel);
-            const float2 f = fmul2(__half22float2(*reinterpret_cast<const __half2 *>(&h)), make_float2(scale, scale));
-            w[i] = pack_pair<BF16>(f.x, f.y);
-        } else {
-            w[i] = BF16 ? code_pair_bf16(four, sel) : code_pair_f16(four, sel);
-        }
+__device__ __forceinline__ uint4 values_of(const uint2 &codes, uint32_t factor) {
+    if (!V) factor = 0x77807780u;  // bf16: 2^112
+    return make_uint4(code_pair<BF16, V>(codes.x, 0x4140u, factor), code_pair<BF16, V>(codes.x, 0x4342u, factor),
+                      code_pair<BF16, V>(codes.y, 0x4140u, factor), code_pair<BF16, V>(codes.y, 0x4342u, factor));
+}
+
+// A V row's scale as 2^e times the rest: the power of two goes to the values (`factor` for code_pair, exact), the rest, in
+// [1, 2) for every scale that the append writes, to the weights. e is held to where factor and values are numbers
+// of the 16-bit type (f16 below 2^-22: values round as f16 subnormals do). A scale that is not finite: values that are not.
+template <bool BF16>
+__device__ __forceinline__ uint32_t split_scale(float scale, float &rest) {
+    const uint32_t bits = __float_as_uint(scale);
+    const int biased = (int)(bits >> 23) & 255;
+    if (biased == 255) {
+        rest = 1.f;
+        const uint32_t f = (bits & 0x007fffffu) ? 0x7fffu : ((BF16 ? 0x7f80u : 0x7c00u) | (bits >> 31 << 15));
+        return f * 0x10001u;
     }
-    return make_uint4(w[0], w[1], w[2], w[3]);
+    const int e = min(max(biased - 127, BF16 ? -100 : -22), 7);
+    rest = scale * __uint_as_float((uint32_t)(127 - e) << 23);
+    return (BF16 ? (uint32_t)(247 + e) << 7 : (uint32_t)(23 + e) << 10) * 0x10001u;
 }
 
 template <bool BF16>
@@ -214,11 +222,11 @@ __device__ __forceinline__ uint4 drop_nonfinite8(const uint4 &v) {
 }
 
 // FP8: a warp's kRows rows of a ring tile, rows `first` on, codes to 16-bit values in the layout that TMA writes for a 16-bit
-// cache. K: the codes' own values (exact; the row scales multiply the scores); V: times the row's scale, rounded to 16 bits.
-// Rows from n_valid on (beyond the context) become 0; what is not finite in a V row from `drafted` on becomes 0. Returns
+// cache. Both exactly: K the codes' own values (the row scales multiply the scores), V times their scales' powers of two
+// (the scales' rests, left in the scales' place, multiply the weights). Rows from n_valid on (beyond the context) become 0; what is not finite in a V row from `drafted` on becomes 0. Returns
 // whether there was any of that.
 template <int D, bool BF16, bool V, int kRows>
-__device__ __forceinline__ bool convert_rows(uint8_t *tile, const uint8_t *codes64, const float *sc, int first, int n_valid, int drafted, int lane) {
+__device__ __forceinline__ bool convert_rows(uint8_t *tile, const uint8_t *codes64, float *sc, int first, int n_valid, int drafted, int lane) {
     using L = TreeLayout<D, true>;
     // head_dim 128: 8 lanes a row of codes, which lie where the second half of the row's values goes (the warp reads its
     // rows before it writes any); of 8 lanes, lanes 4-7 take row r ^ 5 of the chunks that lanes 0-3 take of row r: neither
@@ -233,17 +241,20 @@ __device__ __forceinline__ bool convert_rows(uint8_t *tile, const uint8_t *codes
         const int row = row_of(i);
         raw[i] = *reinterpret_cast<const uint4 *>(D == 128 ? tile + L::kTileHalf + row * 128 + ((c ^ (row & 7)) << 4) : codes64 + row * 64 + c * 16);
     }
-    __syncwarp();
-    float scale[kSteps];
+    uint32_t factor[kSteps];
+    float rest = 0.f;
 #pragma unroll
-    for (int i = 0; i < kSteps; ++i) scale[i] = V ? sc[row_of(i)] * kCodeFactorInv : 1.f;
+    for (int i = 0; i < kSteps; ++i) factor[i] = V ? split_scale<BF16>(sc[row_of(i)], rest) : 0u;
+    if (V && lane < kRows) split_scale<BF16>(sc[first + lane], rest);
+    __syncwarp();
+    if (V && lane < kRows) sc[first + lane] = rest;
     bool bad = false;
     auto run = [&](auto has_tail) {
 #pragma unroll
         for (int i = 0; i < kSteps; ++i) {
             const int row = row_of(i);
-            uint4 v0 = values_of<BF16, V>(make_uint2(raw[i].x, raw[i].y), scale[i]);
-            uint4 v1 = values_of<BF16, V>(make_uint2(raw[i].z, raw[i].w), scale[i]);
+            uint4 v0 = values_of<BF16, V>(make_uint2(raw[i].x, raw[i].y), factor[i]);
+            uint4 v1 = values_of<BF16, V>(make_uint2(raw[i].z, raw[i].w), factor[i]);
             if constexpr (decltype(has_tail)::value) {
                 if (row >= n_valid) {
                     v0 = v1 = make_uint4(0, 0, 0, 0);
@@ -564,7 +575,7 @@ __global__ void __launch_bounds__(TreeLayout<D, FP8>::kThreads, 1)
                     if (!(ok = wait(q_full, seg_i & 1u))) break;
                     tc::fence_after_sync();
                     if (wide) {
-                        const bool two_parts = a.out_dtype == 2;
+                        const bool two_parts = !FP8 && a.out_dtype == 2;
                         if (!(ok = wait(&tile_full[slot], ph))) break;
                         qk(true, slot, 0, g & 1u);
                         for (int j = 0; j < T; ++j) {
@@ -610,7 +621,7 @@ __global__ void __launch_bounds__(TreeLayout<D, FP8>::kThreads, 1)
                             if (!(ok = wait(&tile_full[slot], ph) && wait(&p_full[g & 1u], (g >> 1) & 1u))) break;
                             if (j == 0 && !(ok = wait(o_empty, (seg_i & 1u) ^ 1u))) break;
                             tc::fence_after_sync();
-                            pv(false, true, slot, 0, g & 1u, j == 0);
+                            pv(false, !FP8, slot, 0, g & 1u, j == 0);
                             tc::mma_commit(&kv_empty[slot]);
                             if (j + 2 == T) tc::mma_commit(pv_late);
                             advance();
@@ -719,7 +730,7 @@ __global__ void __launch_bounds__(TreeLayout<D, FP8>::kThreads, 1)
                 for (int j = 0; j < T; ++j, ++tiles) {
                     if (j > 0) step(j < ahead ? 1u : 2u);
                     if (!(ok = mbar_wait(&kv_full[slot], par, abort_flag, a.err))) break;
-                    const float *const sc = reinterpret_cast<const float *>(smem + L::kScaleOff) + slot * 128u;
+                    float *const sc = reinterpret_cast<float *>(smem + L::kScaleOff) + slot * 128u;
                     convert_rows<D, BF16, false, 32>(sRing + slot * L::kTileBytes, smem + L::kCodeOff + slot * (kBN * 64u), sc, first,
                                                      s.len - (s.t0 + j) * kBN, 0, lane);
                     reinterpret_cast<float *>(smem + L::kKScaleOff)[(tiles & 3u) * 128u + first + lane] = sc[first + lane] * kCodeFactorInv;
@@ -758,7 +769,7 @@ __global__ void __launch_bounds__(TreeLayout<D, FP8>::kThreads, 1)
             const Segment &s = segs[seg_i % kSegs];
             const bool wide = kLanes == 2 && s.nodes > a.tile_nodes;
             const bool split = kLanes == 2 && !wide;  // the lanes share the rows
-            const bool two_parts = !wide || a.out_dtype == 2;
+            const bool two_parts = !FP8 && (!wide || a.out_dtype == 2);
             const int T = s.t1 - s.t0, ahead = wide ? 1 : min(2, T);
             const int U = wide ? 2 * T : T;  // score buffers
             // wide: lane A's tile is full, lane B has the rest
@@ -780,7 +791,7 @@ __global__ void __launch_bounds__(TreeLayout<D, FP8>::kThreads, 1)
                 if (!mbar_wait(&kv_full[c_slot], c_par, abort_flag, a.err)) return false;
                 const int n_valid = seg_len - (seg_t0 + j) * kBN;
                 if (convert_rows<D, BF16, true, 16>(sRing + c_slot * L::kTileBytes, smem + L::kCodeOff + c_slot * (kBN * 64u),
-                                                    reinterpret_cast<const float *>(smem + L::kScaleOff) + c_slot * 128u,
+                                                    reinterpret_cast<float *>(smem + L::kScaleOff) + c_slot * 128u,
                                                     (warp - 4) * 16, n_valid, n_valid - seg_n, lane))
                     s_poison[seg_i & 3u] = 1;
                 tc::fence_proxy_async_smem();
@@ -849,6 +860,9 @@ __global__ void __launch_bounds__(TreeLayout<D, FP8>::kThreads, 1)
                     const float2 cc2 = make_float2(c2, c2), nm2 = make_float2(-base, -base);
                     float2 l4[4] = {make_float2(0.f, 0.f), make_float2(0.f, 0.f), make_float2(0.f, 0.f),
                                     make_float2(0.f, 0.f)};
+                    // FP8: the V scales' rests, once every warp has converted its rows of the tile
+                    const float4 *vs = reinterpret_cast<const float4 *>(smem + L::kScaleOff) + c_slot * 32u + half * (kSub / 4);
+                    if (FP8 && !(ok = mbar_wait(&conv_full[c_slot], c_par, abort_flag, a.err))) break;
 #pragma unroll
                     for (int cc = 0; cc < kSub / 32; ++cc) {
                         // P over the chunk's own scores: 16 columns of roundings, 16 of remainders
@@ -858,6 +872,12 @@ __global__ void __launch_bounds__(TreeLayout<D, FP8>::kThreads, 1)
                             const float2 xq = ffma2(make_float2(v[cc * 32 + 2 * q], v[cc * 32 + 2 * q + 1]), cc2, nm2);
                             const float2 e = make_float2(ex2f(xq.x), ex2f(xq.y));
                             l4[q & 3] = fadd2(l4[q & 3], e);
+                            if constexpr (FP8) {
+                                const float4 r4 = vs[cc * 8 + q / 2];
+                                const float2 f = fmul2(e, q & 1 ? make_float2(r4.z, r4.w) : make_float2(r4.x, r4.y));
+                                ph[q] = pack_pair<BF16>(f.x, f.y);
+                                continue;
+                            }
                             ph[q] = pack_pair<BF16>(e.x, e.y);
                             v[cc * 32 + 2 * q] = e.x;
                             v[cc * 32 + 2 * q + 1] = e.y;
@@ -1028,8 +1048,9 @@ __global__ void __launch_bounds__(TreeLayout<D, FP8>::kThreads, 1)
                             for (int i = 0; i < 4; ++i) {
                                 uint4 raw;  // 8 values as the products would read them
                                 if constexpr (FP8) {
+                                    float rest;
                                     raw = values_of<BF16, true>(__ldg(static_cast<const uint2 *>(a.cache.ptr) + row * (D / 8) + cc * 4 + i),
-                                                                __ldg(a.cache.scales + row) * kCodeFactorInv);
+                                                                split_scale<BF16>(__ldg(a.cache.scales + row), rest));
                                 } else {
                                     raw = __ldg(static_cast<const uint4 *>(a.cache.ptr) + row * (D / 8) + cc * 4 + i);
                                 }

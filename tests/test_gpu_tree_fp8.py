@@ -40,8 +40,9 @@ class Fp8Case(Case):
         return out.cpu(), lse.cpu()
 
     def p_half(self, dtype):
-        """Besides P's rounding, each value is rounded once to the cache's 16-bit type: half a step of it."""
-        return super().p_half(dtype) + torch.finfo(self.dt).eps / 2
+        """Each weight, times what its value's row scale is above a power of two, is rounded once to the cache's 16-bit
+        type: half a step of it. The values' codes times those powers are exact."""
+        return torch.finfo(self.dt).eps / 2
 
 
 @pytest.mark.parametrize("dtype", ["f16", "bf16"])
@@ -133,3 +134,23 @@ def test_after_append_it_agrees_with_the_prefill():
                                  c.table.cuda(), max_q_len=n, out_dtype=torch.float32, scales=c.scales.cuda())
     # values rounded to bf16 here (half a step, 2^-8), P to f16 there (2^-11)
     assert (out - ref.cpu()).abs().max() <= (2.0 ** -8 + 2.0 ** -10) * float(c.cache.abs().max())
+
+
+@pytest.mark.parametrize("dtype,factor", [("bf16", 2.0 ** -90), ("bf16", 1e-20), ("bf16", 1e30), ("bf16", 0.3), ("f16", 2.0 ** -12),
+                                          ("f16", 3e-3), ("f16", 4000.0)])
+@pytest.mark.parametrize("d,n", [(64, 20), (128, 20), (128, 70)])
+def test_value_scales_of_any_size(d, n, dtype, factor):
+    """The value rows' scales, each row's its own, far from 1; some rows of zeros with a scale of 0."""
+    c = Fp8Case([300, n + 1], [n, n], 4, 2, d=d, seed=19, dtype=dtype)
+    g = torch.Generator().manual_seed(20)
+    c.scales[:, 1] *= factor * torch.rand(c.scales[:, 1].shape, generator=g)
+    zero = torch.rand(c.scales[:, 1].shape, generator=g) < 0.1
+    c.scales[:, 1][zero] = 0.0
+    c.codes[:, 1][zero] = 0
+    c.refresh()
+    out, _ = c.run(out_dtype=torch.float32)
+    ro, _, vmax = c.exact()
+    # as check(): FP32 sums of both products and ex2, and half a step of the cache's type on each weight
+    tol = (2 * (0.9 * d ** 1.5 * 2.0 ** -24 + 2.0 ** -17) + c.p_half(out.dtype)) * vmax
+    assert vmax > 0 and (out.double() - ro).abs().max() <= tol
+    assert pkv.get_device_error() == 0
