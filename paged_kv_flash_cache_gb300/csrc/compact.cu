@@ -15,8 +15,9 @@
 // store of chunk c can only meet a source of chunk c or earlier, whose loads precede the barrier).
 //   few rows   a warp a slice;
 //   more       `shares` CTAs a slice, each moving an equal piece of its rows. Pieces are independent
-//              when no row's source lies in a later piece's destinations (a window moved up behind a prompt); every CTA of the slice looks the list over and finds the same answer. Otherwise the rows go in
-//              order and the CTAs take a share of each row's columns instead, as far as 64 bytes a share.
+//              when no row's source lies in a later piece's destinations (a window moved up behind a prompt);
+//              every CTA of the slice looks the list over and finds the same answer. Otherwise the rows go in order
+//              and the CTAs take a share of each row's columns instead, as far as 64 bytes a share.
 // 8 x 8192 rows of 8 heads x 128 (537 MB read and written): 242 us with column shares only (64 bytes of a row at
 // different times), 147 us with pieces and each vector's thread looking its row up, 97 us (82% of the copy rate) as it is.
 #include "pkv_device.cuh"
@@ -102,7 +103,8 @@ __global__ void __launch_bounds__(kCompactThreads, kResident) compact_kernel(Com
                 }
             }
         }
-        const int rows = (kUnroll * kGroup) >> a.log2_row_vecs;  // rows of a chunk (with fewer columns: fewer vectors a thread)
+        // rows of a chunk (with fewer columns: fewer vectors a thread)
+        const int rows = (kUnroll * kGroup) >> a.log2_row_vecs;
         // row index of position pos in this slice's (K or V, head), or kNoRow (flagged)
         auto row_of = [&](long long pos) -> uint32_t {
             const int pb = __ldg(bt + (pos >> a.log2_block_size));
@@ -144,7 +146,8 @@ __global__ void __launch_bounds__(kCompactThreads, kResident) compact_kernel(Com
 #pragma unroll
             for (int u = 0; u < kUnroll; ++u) {
                 const int r = ra + u * rb;
-                if (r < rows && s_dst[buf][s0 + r] != kNoRow) v[u] = ld_once(base_v + ((size_t)s_src[buf][s0 + r] << a.log2_row_vecs));
+                if (r < rows && s_dst[buf][s0 + r] != kNoRow)
+                    v[u] = ld_once(base_v + ((size_t)s_src[buf][s0 + r] << a.log2_row_vecs));
             }
             if (scales)
 #pragma unroll

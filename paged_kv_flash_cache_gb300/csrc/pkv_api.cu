@@ -602,7 +602,8 @@ pkv_status pkv_kv_cache_compact(pkv_cache cache, const int *keep_pos, const int 
     if (batch == 0 || num_keep == 0) return PKV_OK;
     if (!keep_pos || !cu_keep || !dst_start || !block_tables) return PKV_ERR_INVALID_ARG;
     // rows are counted in 32 bits, the last count standing for none
-    if ((unsigned long long)cache.num_blocks * 2 * cache.num_kv_heads > 0xffffffffull / cache.block_size) return PKV_ERR_UNSUPPORTED;
+    if ((unsigned long long)cache.num_blocks * 2 * cache.num_kv_heads > 0xffffffffull / cache.block_size)
+        return PKV_ERR_UNSUPPORTED;
     DeviceSlot *s = slot();
     if (!s) return PKV_ERR_CUDA;
     CompactArgs a;

@@ -104,7 +104,8 @@ struct Coefficients {
 };
 
 template <bool BF16, bool INTER, bool NORM>
-__device__ __forceinline__ void fill(Coefficients &k, const void *w, const float *cosines, const float *sines, int va, int vb, bool rotates) {
+__device__ __forceinline__ void fill(Coefficients &k, const void *w, const float *cosines, const float *sines, int va,
+                                     int vb, bool rotates) {
     float2 wa[4], wb[4];
     if (NORM && w) {
         unpack_row<BF16>(__ldg(static_cast<const uint4 *>(w) + va), wa);
@@ -147,7 +148,8 @@ __device__ __forceinline__ void fill(Coefficients &k, const void *w, const float
 
 // Norm (if `normed`) and rotation of a lane's two vectors of a row.
 template <int D, bool INTER, bool NORM>
-__device__ __forceinline__ void turn_row(float2 (&fa)[4], float2 (&fb)[4], const Coefficients &k, bool normed, float eps, bool rotates) {
+__device__ __forceinline__ void turn_row(float2 (&fa)[4], float2 (&fb)[4], const Coefficients &k, bool normed, float eps,
+                                         bool rotates) {
     float2 rs2 = make_float2(1.f, 1.f);
     if (NORM) {
         float2 q = fmul2(fa[0], fa[0]), r = fmul2(fb[0], fb[0]);
@@ -175,7 +177,8 @@ __device__ __forceinline__ void turn_row(float2 (&fa)[4], float2 (&fb)[4], const
 
 // An FP8 row: the codes of a lane's two vectors and the row's scale.
 template <int D>
-__device__ __forceinline__ void store_codes(const RopeArgs &a, size_t row, const float2 (&fa)[4], const float2 (&fb)[4], int va, int vb, bool first, bool live) {
+__device__ __forceinline__ void store_codes(const RopeArgs &a, size_t row, const float2 (&fa)[4], const float2 (&fb)[4],
+                                            int va, int vb, bool first, bool live) {
     float amax = 0.f;
 #pragma unroll
     for (int i = 0; i < 4; ++i)
@@ -312,7 +315,8 @@ __global__ void __launch_bounds__(kRopeThreads, RopeShape<NORM>::kCtas) rope_app
             const int end = min(g_end, gq);
             for (int g = g_begin; ok && g < end; ++g) {
                 const int h0 = g * kGroup;
-                uint4 *dst = reinterpret_cast<uint4 *>(static_cast<uint16_t *>(a.q_out) + (size_t)t * a.q_out_stride) + (size_t)(h0 + sub) * (D / 8);
+                uint4 *dst = reinterpret_cast<uint4 *>(static_cast<uint16_t *>(a.q_out) + (size_t)t * a.q_out_stride) +
+                             (size_t)(h0 + sub) * (D / 8);
                 if (!(ok = next_group())) break;
 #pragma unroll
                 for (int u = 0; u < kUnroll; ++u) {
@@ -381,7 +385,8 @@ cudaError_t launch_rope_n(const RopeArgs &a, dim3 grid, cudaStream_t s) {
 
 template <int D, bool BF16, bool FP8, bool INTER>
 cudaError_t launch_rope_i(const RopeArgs &a, dim3 grid, cudaStream_t s) {
-    return a.q_weight || a.k_weight ? launch_rope_n<D, BF16, FP8, INTER, true>(a, grid, s) : launch_rope_n<D, BF16, FP8, INTER, false>(a, grid, s);
+    return a.q_weight || a.k_weight ? launch_rope_n<D, BF16, FP8, INTER, true>(a, grid, s)
+                                    : launch_rope_n<D, BF16, FP8, INTER, false>(a, grid, s);
 }
 
 template <int D, bool BF16, bool FP8>
@@ -392,7 +397,8 @@ cudaError_t launch_rope_t(const RopeArgs &a, dim3 grid, cudaStream_t s) {
 template <int D>
 cudaError_t launch_rope_d(const RopeArgs &a, dim3 grid, cudaStream_t s) {
     if constexpr (D <= 128) {
-        if (a.fp8) return a.dtype == 1 ? launch_rope_t<D, true, true>(a, grid, s) : launch_rope_t<D, false, true>(a, grid, s);
+        if (a.fp8)
+            return a.dtype == 1 ? launch_rope_t<D, true, true>(a, grid, s) : launch_rope_t<D, false, true>(a, grid, s);
     }
     return a.dtype == 1 ? launch_rope_t<D, true, false>(a, grid, s) : launch_rope_t<D, false, false>(a, grid, s);
 }

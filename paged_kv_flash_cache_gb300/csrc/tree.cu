@@ -22,21 +22,32 @@
 //
 // Work: the (sequence, KV head, row block) items, laid end to end in key tiles (an item weighs kItemCost tiles more for
 // its set-up and output), are cut into equal runs, one a CTA (one CTA an SM): any mix of lengths fills the GPU
-// evenly, an item is split only where a run ends, and a CTA leaves at most two partial items, so the workspace does not grow
-// with the batch. A merge kernel joins the partials of each split item in the order of the keys (no atomics: the same
-// result every time).
+// evenly, an item is split only where a run ends, and a CTA leaves at most two partial items, so the workspace does
+// not grow with the batch. A merge kernel joins the partials of each split item in the order of the keys (no atomics:
+// the same result every time).
 //
 // Warps: 0 loads Q and the K tiles, 3 the V tiles by TMA into a ring, 1 issues the MMAs and owns TMEM, 2 walks the run
-// and hands its segments to the others, the warpgroups of lanes A and B do softmax and output. P goes to the tensor cores
-// as its 16-bit rounding plus the rounding's remainder (two products), so that it is not a rounding to 16 bits -- but for
-// wide blocks with a 16-bit output, which the chain of products and softmax bounds (a 63-node batch: 96 us with
-// two parts, 88 with one): there P is rounded once, half a step of the output's own type (the prefill's choice too).
+// and hands its segments to the others, the warpgroups of lanes A and B do softmax and output.
 //
-// Measured, main kernel and merge, back to back: 16 sequences x 64 nodes, 32 KV heads x 128, contexts 1k-8k in pages of 16
-// (1.02 GB): 167 us, 90% of the copy rate, bound by HBM; 25 nodes of 32 / 8 heads over 131k tokens in pages of 64 (0.54 GB): 98 us,
-// 81%, the merge 8 us of it; 32 sequences x 63 nodes of 32 / 8 heads, contexts to 8k (0.27 GB, 252 rows a KV head): 77 us, 52%, bound by
-// the wide chain (about 3800 cycles a tile, of them 2560 in the tensor cores) and the merge, 13 us; 8 sequences x 31 nodes at head_dim 256
-// (0.16 GB): 39 us, 61%, four ring slots beside the 64 KB of Q.
+// P goes to the tensor cores as its 16-bit rounding plus the rounding's remainder (two products), so that it is not a
+// rounding to 16 bits. Two exceptions round it once, by half a step of the 16-bit type: wide blocks with a 16-bit output,
+// which the chain of products and softmax bounds (a 63-node batch: 96 us with two parts, 88 with one; the prefill's choice
+// too), and FP8 caches, whose codes are far coarser.
+//
+// An FP8 cache: the codes land where the tile's second half goes (head_dim 64: apart) and become 16-bit values in place,
+// exactly: the keys' by a warpgroup of their own, with their row scales on the scores in FP32; the values' by the softmax
+// warps, times their scales' powers of two, what the scales are above those going to the weights before P's one rounding.
+// Bound by the chain of conversion and softmax in the same warps, whose dependent instructions leave the schedulers idle
+// more than half of the time.
+//
+// Measured, main kernel and merge, back to back (of the copy rate):
+//   16 sequences x 64 nodes, 32 KV heads x 128, contexts 1k-8k in pages of 16 (1.02 GB): 167 us, 90%, bound by HBM;
+//     over an FP8 cache (0.54 GB) 279 us
+//   25 nodes of 32 / 8 heads over 131k tokens in pages of 64 (0.54 GB): 98 us, 81%, the merge 8 us of it; FP8 122 us
+//   32 sequences x 63 nodes of 32 / 8 heads, contexts to 8k (0.27 GB, 252 rows a KV head): 77 us, 52%, bound by the wide
+//     chain (about 3800 cycles a tile, of them 2560 in the tensor cores) and the merge, 13 us; FP8 123 us
+//   8 sequences x 31 nodes at head_dim 256 (0.16 GB): 39 us, 61%, four ring slots beside the 64 KB of Q
+// A partial's rows go out at 29 to 53 bytes a cycle and SM, all SMs at once (L2's write rate): 5000 to 10000 cycles a run.
 //
 // Rows that see nothing (a padded node): 0 and -inf. Masked keys: their scores are replaced, never
 // multiplied, so that K may hold anything; V rows beyond the context are zeroed in shared memory, and a
@@ -57,8 +68,8 @@ namespace {
 constexpr int kBM = 128;              // rows of a tile
 constexpr float kRescaleLog2 = 8.0f;  // O is rescaled when the running max grows by more than 2^8
 constexpr int kSegs = 4;              // segments handed out ahead
-constexpr int kItemCost = 3;          // an item's set-up and output, in key tiles (measured: about 11000 cycles against 3800)
-constexpr int kMinTiles = 2;          // work of a run at least, in key tiles
+constexpr int kItemCost = 3;          // an item's set-up and output, in key tiles (about 11000 cycles against 3800)
+constexpr int kMinTiles = 2;          // work of a run at least, in key tiles (4: 16.2 us for 15.6, 16 nodes over 4k tokens)
 
 // One run's part of an item: key tiles [t0, t1) of nodes [node0, node0 + nodes) of one sequence and KV
 // head (or share of its group). nodes = 0 ends the run.
@@ -221,12 +232,13 @@ __device__ __forceinline__ uint4 drop_nonfinite8(const uint4 &v) {
     return make_uint4(drop_nonfinite<BF16>(v.x), drop_nonfinite<BF16>(v.y), drop_nonfinite<BF16>(v.z), drop_nonfinite<BF16>(v.w));
 }
 
-// FP8: a warp's kRows rows of a ring tile, rows `first` on, codes to 16-bit values in the layout that TMA writes for a 16-bit
-// cache. Both exactly: K the codes' own values (the row scales multiply the scores), V times their scales' powers of two
-// (the scales' rests, left in the scales' place, multiply the weights). Rows from n_valid on (beyond the context) become 0; what is not finite in a V row from `drafted` on becomes 0. Returns
-// whether there was any of that.
+// FP8: a warp's kRows rows of a ring tile, rows `first` on, codes to 16-bit values in the layout that TMA writes for a
+// 16-bit cache. Both exactly: K the codes' own values (the row scales multiply the scores), V times their scales' powers
+// of two (the scales' rests, left in the scales' place, multiply the weights). Rows from n_valid on (beyond the context)
+// become 0; what is not finite in a V row from `drafted` on becomes 0. Returns whether there was any of that.
 template <int D, bool BF16, bool V, int kRows>
-__device__ __forceinline__ bool convert_rows(uint8_t *tile, const uint8_t *codes64, float *sc, int first, int n_valid, int drafted, int lane) {
+__device__ __forceinline__ bool convert_rows(uint8_t *tile, const uint8_t *codes64, float *sc, int first, int n_valid,
+                                             int drafted, int lane) {
     using L = TreeLayout<D, true>;
     // head_dim 128: 8 lanes a row of codes, which lie where the second half of the row's values goes (the warp reads its
     // rows before it writes any); of 8 lanes, lanes 4-7 take row r ^ 5 of the chunks that lanes 0-3 take of row r: neither
@@ -239,7 +251,8 @@ __device__ __forceinline__ bool convert_rows(uint8_t *tile, const uint8_t *codes
 #pragma unroll
     for (int i = 0; i < kSteps; ++i) {
         const int row = row_of(i);
-        raw[i] = *reinterpret_cast<const uint4 *>(D == 128 ? tile + L::kTileHalf + row * 128 + ((c ^ (row & 7)) << 4) : codes64 + row * 64 + c * 16);
+        raw[i] = *reinterpret_cast<const uint4 *>(D == 128 ? tile + L::kTileHalf + row * 128 + ((c ^ (row & 7)) << 4)
+                                                           : codes64 + row * 64 + c * 16);
     }
     uint32_t factor[kSteps];
     float rest = 0.f;
@@ -731,9 +744,10 @@ __global__ void __launch_bounds__(TreeLayout<D, FP8>::kThreads, 1)
                     if (j > 0) step(j < ahead ? 1u : 2u);
                     if (!(ok = mbar_wait(&kv_full[slot], par, abort_flag, a.err))) break;
                     float *const sc = reinterpret_cast<float *>(smem + L::kScaleOff) + slot * 128u;
-                    convert_rows<D, BF16, false, 32>(sRing + slot * L::kTileBytes, smem + L::kCodeOff + slot * (kBN * 64u), sc, first,
-                                                     s.len - (s.t0 + j) * kBN, 0, lane);
-                    reinterpret_cast<float *>(smem + L::kKScaleOff)[(tiles & 3u) * 128u + first + lane] = sc[first + lane] * kCodeFactorInv;
+                    convert_rows<D, BF16, false, 32>(sRing + slot * L::kTileBytes, smem + L::kCodeOff + slot * (kBN * 64u),
+                                                     sc, first, s.len - (s.t0 + j) * kBN, 0, lane);
+                    float *const ks = reinterpret_cast<float *>(smem + L::kKScaleOff) + (tiles & 3u) * 128u;
+                    ks[first + lane] = sc[first + lane] * kCodeFactorInv;
                     tc::fence_proxy_async_smem();
                     __syncwarp();
                     if (lane == 0) mbar_arrive_n(&conv_full[slot], 2);  // (a V tile has 8 warps' arrivals)
@@ -782,9 +796,10 @@ __global__ void __launch_bounds__(TreeLayout<D, FP8>::kThreads, 1)
             };
             float m = -INFINITY, l = 0.f;
             bool ok = true;
-            // FP8: this warp's 16 rows of V_j, in the order of the tiles, V_0 now and V_{j + 1} after the last P over V_j is
-            // handed over. The keys' codes are the conversion warps', a tile and more ahead: 319 us for 16 x 64 nodes, 138
-            // for the long context (all conversions here: 336 and 169; all of them there: 345 and 151).
+            // FP8: this warp's 16 rows of V_j, in the order of the tiles, V_0 now and V_{j + 1} after the last P over V_j
+            // is handed over. The keys' codes are the conversion warps', a tile and more ahead: 279 us for 16 x 64 nodes,
+            // 122 for the long context (all conversions there: 288 and 138; all of them here, before the values were
+            // exact: 336 and 169, against 319 and 138 then).
             const int seg_len = s.len, seg_t0 = s.t0, seg_n = s.n;
             auto convert_v = [&](int j) -> bool {
                 c_step(j == 0 ? (uint32_t)ahead : ahead + j <= T ? 2u : 1u);
@@ -827,7 +842,8 @@ __global__ void __launch_bounds__(TreeLayout<D, FP8>::kThreads, 1)
                     tc::tmem_wait_ld();
                     if constexpr (FP8) {
                         // the K row scales (the warps wrote them before conv_full, which the scores' products waited for)
-                        const float4 *ks = reinterpret_cast<const float4 *>(smem + L::kKScaleOff) + ((tiles0 + (uint32_t)j) & 3u) * 32u + half * (kSub / 4);
+                        const float4 *ks = reinterpret_cast<const float4 *>(smem + L::kKScaleOff) +
+                                           ((tiles0 + (uint32_t)j) & 3u) * 32u + half * (kSub / 4);
 #pragma unroll
                         for (int k = 0; k < kSub / 4; ++k) {
                             const float4 f = ks[k];
@@ -861,7 +877,8 @@ __global__ void __launch_bounds__(TreeLayout<D, FP8>::kThreads, 1)
                     float2 l4[4] = {make_float2(0.f, 0.f), make_float2(0.f, 0.f), make_float2(0.f, 0.f),
                                     make_float2(0.f, 0.f)};
                     // FP8: the V scales' rests, once every warp has converted its rows of the tile
-                    const float4 *vs = reinterpret_cast<const float4 *>(smem + L::kScaleOff) + c_slot * 32u + half * (kSub / 4);
+                    const float4 *vs = reinterpret_cast<const float4 *>(smem + L::kScaleOff) + c_slot * 32u +
+                                       half * (kSub / 4);
                     if (FP8 && !(ok = mbar_wait(&conv_full[c_slot], c_par, abort_flag, a.err))) break;
 #pragma unroll
                     for (int cc = 0; cc < kSub / 32; ++cc) {
@@ -999,15 +1016,18 @@ __global__ void __launch_bounds__(TreeLayout<D, FP8>::kThreads, 1)
                 constexpr int kStageRow = L::kStageRow, kPieces = kStageRow / 16;  // 16-byte pieces of a row at a time
                 uint8_t *stage = smem + L::kStageOff + (warp - 4) * 32 * kStageRow;
                 auto place = [&](int rr, int c) { return stage + rr * kStageRow + ((c ^ (rr & (kPieces - 1))) << 4); };
+                long long dst[kPieces];  // where this lane's pieces go
+#pragma unroll
+                for (int i = 0; i < kPieces; ++i) dst[i] = __shfl_sync(0xffffffffu, dst_row, i * (32 / kPieces) + lane / kPieces);
                 auto flush = [&](int col_bytes) {
                     __syncwarp();
+                    uint4 v[kPieces];
 #pragma unroll
-                    for (int i = 0; i < kPieces; ++i) {
-                        const int rr = i * (32 / kPieces) + lane / kPieces, c = lane % kPieces;
-                        const long long d = __shfl_sync(0xffffffffu, dst_row, rr);
-                        const uint4 v = *reinterpret_cast<const uint4 *>(place(rr, c));
-                        if (d >= 0) *reinterpret_cast<uint4 *>(out + d + col_bytes + c * 16) = v;
-                    }
+                    for (int i = 0; i < kPieces; ++i)
+                        v[i] = *reinterpret_cast<const uint4 *>(place(i * (32 / kPieces) + lane / kPieces, lane % kPieces));
+#pragma unroll
+                    for (int i = 0; i < kPieces; ++i)
+                        if (dst[i] >= 0) *reinterpret_cast<uint4 *>(out + dst[i] + col_bytes + lane % kPieces * 16) = v[i];
                     __syncwarp();
                 };
                 auto stage16 = [&](int piece, const uint4 &v) {  // 16-byte piece of this lane's output row
@@ -1049,7 +1069,8 @@ __global__ void __launch_bounds__(TreeLayout<D, FP8>::kThreads, 1)
                                 uint4 raw;  // 8 values as the products would read them
                                 if constexpr (FP8) {
                                     float rest;
-                                    raw = values_of<BF16, true>(__ldg(static_cast<const uint2 *>(a.cache.ptr) + row * (D / 8) + cc * 4 + i),
+                                    const uint2 *codes = static_cast<const uint2 *>(a.cache.ptr) + row * (D / 8);
+                                    raw = values_of<BF16, true>(__ldg(codes + cc * 4 + i),
                                                                 split_scale<BF16>(__ldg(a.cache.scales + row), rest));
                                 } else {
                                     raw = __ldg(static_cast<const uint4 *>(a.cache.ptr) + row * (D / 8) + cc * 4 + i);
@@ -1213,7 +1234,8 @@ cudaError_t launch_tree_t(const TreeArgs &a, int grid, cudaStream_t s) {
 cudaError_t launch_tree(const TreeArgs &a, int grid, cudaStream_t s) {
     const bool bf16 = a.cache.dtype == 1;
     if (a.cache.fp8) {
-        if (a.cache.head_dim == 128) return bf16 ? launch_tree_t<128, true, true>(a, grid, s) : launch_tree_t<128, false, true>(a, grid, s);
+        if (a.cache.head_dim == 128)
+            return bf16 ? launch_tree_t<128, true, true>(a, grid, s) : launch_tree_t<128, false, true>(a, grid, s);
         return bf16 ? launch_tree_t<64, true, true>(a, grid, s) : launch_tree_t<64, false, true>(a, grid, s);
     }
     switch (a.cache.head_dim) {
