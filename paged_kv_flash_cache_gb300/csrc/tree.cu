@@ -31,7 +31,7 @@
 //
 // P goes to the tensor cores as its 16-bit rounding plus the rounding's remainder (two products), so that it is not a
 // rounding to 16 bits. Two exceptions round it once, by half a step of the 16-bit type: wide blocks with a 16-bit output,
-// which the chain of products and softmax bounds (a 63-node batch: 96 us with two parts, 88 with one; the prefill's choice
+// which the chain of products and softmax bounds (a 63-node batch: 90 us with two parts, 75 with one; the prefill's choice
 // too), and FP8 caches, whose codes are far coarser.
 //
 // An FP8 cache: the codes land where the tile's second half goes (head_dim 64: apart) and become 16-bit values in place,
@@ -41,12 +41,13 @@
 // more than half of the time.
 //
 // Measured, main kernel and merge, back to back (of the copy rate):
-//   16 sequences x 64 nodes, 32 KV heads x 128, contexts 1k-8k in pages of 16 (1.02 GB): 167 us, 90%, bound by HBM;
+//   16 sequences x 64 nodes, 32 KV heads x 128, contexts 1k-8k in pages of 16 (1.02 GB): 165 us, 91%, bound by HBM;
 //     over an FP8 cache (0.54 GB) 279 us
 //   25 nodes of 32 / 8 heads over 131k tokens in pages of 64 (0.54 GB): 98 us, 81%, the merge 8 us of it; FP8 122 us
-//   32 sequences x 63 nodes of 32 / 8 heads, contexts to 8k (0.27 GB, 252 rows a KV head): 77 us, 52%, bound by the wide
+//   32 sequences x 63 nodes of 32 / 8 heads, contexts to 8k (0.27 GB, 252 rows a KV head): 75 us, 53%, bound by the wide
 //     chain (about 3800 cycles a tile, of them 2560 in the tensor cores) and the merge, 13 us; FP8 123 us
-//   8 sequences x 31 nodes at head_dim 256 (0.16 GB): 39 us, 61%, four ring slots beside the 64 KB of Q
+//   8 sequences x 31 nodes at head_dim 256 (0.16 GB): 38 us, 62%: its 64-key tiles at the copy rate (2400 cycles each), the
+//     rest set-up, output and merge of short runs
 // A partial's rows go out at 29 to 53 bytes a cycle and SM, all SMs at once (L2's write rate): 5000 to 10000 cycles a run.
 //
 // Rows that see nothing (a padded node): 0 and -inf. Masked keys: their scores are replaced, never
