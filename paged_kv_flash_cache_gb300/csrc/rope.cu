@@ -44,7 +44,7 @@ constexpr int kUnroll = 4;  // passes (of 512 / D rows) of a group
 constexpr int kGroupBytes = kUnroll * 1024;
 // CTAs an SM, and groups of a warp on their way or in work: with a norm the coefficients of two kinds of weights take
 // registers for 4 CTAs (3 slots each: 37 us for the prompts above; 6 of 2 spill, 48 us), without one there are enough for 6
-// (4099 tokens into an FP8 cache: 34 us against 38).
+// (4099 tokens into an FP8 cache: 33 us against 38).
 template <bool NORM>
 struct RopeShape {
     static constexpr int kCtas = NORM ? 4 : 6;
@@ -66,8 +66,11 @@ __device__ __forceinline__ uint4 pack_row(const float2 (&f)[4]) {
 
 // Eight E4M3 codes of f * inv.
 __device__ __forceinline__ uint2 codes_of(const float2 (&f)[4], float inv) {
-    return make_uint2(pack_e4m3x2(f[0].x * inv, f[0].y * inv) | (pack_e4m3x2(f[1].x * inv, f[1].y * inv) << 16),
-                      pack_e4m3x2(f[2].x * inv, f[2].y * inv) | (pack_e4m3x2(f[3].x * inv, f[3].y * inv) << 16));
+    float2 g[4];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) g[i] = fmul2(f[i], make_float2(inv, inv));
+    return make_uint2(pack_e4m3x2(g[0].x, g[0].y) | (pack_e4m3x2(g[1].x, g[1].y) << 16),
+                      pack_e4m3x2(g[2].x, g[2].y) | (pack_e4m3x2(g[3].x, g[3].y) << 16));
 }
 
 // Sequence of new token t: the last b with cu[b] <= t (t < cu[batch]).
@@ -182,7 +185,7 @@ __device__ __forceinline__ void store_codes(const RopeArgs &a, size_t row, const
     float amax = 0.f;
 #pragma unroll
     for (int i = 0; i < 4; ++i)
-        amax = fmaxf(amax, fmaxf(fmaxf(fabsf(fa[i].x), fabsf(fa[i].y)), fmaxf(fabsf(fb[i].x), fabsf(fb[i].y))));
+        amax = fmax3(fmax3(amax, fabsf(fa[i].x), fabsf(fa[i].y)), fabsf(fb[i].x), fabsf(fb[i].y));
 #pragma unroll
     for (int o = D / 32; o > 0; o >>= 1) amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, o));
     if (!live) return;
