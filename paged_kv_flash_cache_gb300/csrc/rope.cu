@@ -188,12 +188,14 @@ __device__ __forceinline__ void store_codes(const RopeArgs &a, size_t row, const
         amax = fmax3(fmax3(amax, fabsf(fa[i].x), fabsf(fa[i].y)), fabsf(fb[i].x), fabsf(fb[i].y));
 #pragma unroll
     for (int o = D / 32; o > 0; o >>= 1) amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, o));
+    // one division: the row's first lane makes the scale, the others 448 / amax, which the first takes from its neighbour
+    const float quotient = (first ? amax : 448.0f) / (first ? 448.0f : amax);
+    const float inv = __shfl_down_sync(0xffffffffu, quotient, first ? 1 : 0);
     if (!live) return;
     uint2 ca = make_uint2(0u, 0u), cb = ca;
     float scale = 0.f;
     if (amax > 0.f) {
-        scale = amax / 448.0f;
-        const float inv = 448.0f / amax;
+        scale = quotient;
         ca = codes_of(fa, inv);
         cb = codes_of(fb, inv);
     }
