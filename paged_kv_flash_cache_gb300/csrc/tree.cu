@@ -99,10 +99,11 @@ struct TreeLayout {
     // output rows on their way out, kStageRow bytes of each: 4 (FP8: 2) KB a softmax warp
     static constexpr uint32_t kStageRow = FP8 ? 64 : 128;
     static constexpr uint32_t kStageOff = kLanes * kQBytes + kRing * kTileBytes;
-    static constexpr uint32_t kMlOff = kStageOff + 4 * kLanes * 32 * kStageRow;  // [128] (max, sum) between the lanes
+    static constexpr uint32_t kStageEnd = kStageOff + 4 * kLanes * 32 * kStageRow;
+    static_assert(32 * kStageRow >= 2 * 32 * 8, "two (max, sum) of a warp's rows fit in its stage");
     // FP8: the row scales of the ring's tiles, and of the last four K tiles (a ring slot may be refilled while its scores
     // are still in the softmax); head_dim 64: the codes of the ring's tiles (head_dim 128: in the tile's second half)
-    static constexpr uint32_t kScaleOff = kMlOff + kBM * 8;
+    static constexpr uint32_t kScaleOff = kStageEnd;
     static constexpr uint32_t kKScaleOff = kScaleOff + (FP8 ? kRingMax * 512u : 0u);
     static constexpr uint32_t kCodeOff = kKScaleOff + (FP8 ? 4 * 512u : 0u);
     static constexpr uint32_t kBarOff = kCodeOff + (FP8 && D == 64 ? kRingMax * kBN * 64u : 0u);
@@ -301,7 +302,6 @@ __global__ void __launch_bounds__(TreeLayout<D, FP8>::kThreads, 1)
     uint8_t *smem = smem_raw + ((1024u - (smem_addr(smem_raw) & 1023u)) & 1023u);
     uint8_t *sQ = smem;
     uint8_t *sRing = smem + (all_narrow ? 1 : kLanes) * L::kQBytes;
-    float2 *sMl = reinterpret_cast<float2 *>(smem + L::kMlOff);
     uint64_t *bars = reinterpret_cast<uint64_t *>(smem + L::kBarOff);
     uint64_t *kv_full = bars;                 // [kRingMax]
     uint64_t *kv_empty = kv_full + kRingMax;  // [kRingMax]
@@ -975,13 +975,18 @@ __global__ void __launch_bounds__(TreeLayout<D, FP8>::kThreads, 1)
             const bool mine = !split || (w4 >> 1) == x;
             float fa = 1.f, fb = 0.f, lse2 = m, lt = l;  // out = fa O_A + fb O_B (or f O of this lane)
             if (split) {
-                if (!mine) sMl[r] = make_float2(m, l);
+                // (max, sum) through the stage of the warp that hands them over, which puts out no rows of a split segment:
+                // two places in turn. A place is written again two split segments later, behind a phase of ml_full that
+                // takes its reader's arrival; or by a wide segment's rows, behind an o_done that takes its reader's P.
+                float2 *const ml = reinterpret_cast<float2 *>(smem + L::kStageOff + ((warp - 4) ^ (mine ? 4 : 0)) * 32 *
+                                                              L::kStageRow) + (nml & 1u) * 32u + lane;
+                if (!mine) *ml = make_float2(m, l);
                 __syncwarp();
                 if (lane == 0) mbar_arrive(ml_full);
                 if (!mbar_wait(ml_full, nml & 1u, abort_flag, a.err)) break;
                 ++nml;
                 if (mine) {
-                    const float2 o = sMl[r];
+                    const float2 o = *ml;
                     const float M = fmaxf(m, o.x);
                     const float w_me = m == -INFINITY ? 0.f : ex2f(m - M), w_o = o.x == -INFINITY ? 0.f : ex2f(o.x - M);
                     lt = w_me * l + w_o * o.y;
