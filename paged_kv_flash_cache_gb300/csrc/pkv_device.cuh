@@ -245,6 +245,19 @@ __device__ __forceinline__ float fmax3(float a, float b, float c) {
     return d;
 }
 
+// The same, NaN if one of them is (max.f32 passes over NaN).
+__device__ __forceinline__ float fmax3_nan(float a, float b, float c) {
+    float d;
+    asm("max.NaN.f32 %0, %1, %2, %3;" : "=f"(d) : "f"(a), "f"(b), "f"(c));
+    return d;
+}
+
+__device__ __forceinline__ float fmax_nan(float a, float b) {
+    float d;
+    asm("max.NaN.f32 %0, %1, %2;" : "=f"(d) : "f"(a), "f"(b));
+    return d;
+}
+
 // Output element store with a single round-to-nearest-even conversion.
 // out_dtype: 0 = fp16, 1 = bf16, 2 = fp32.
 __device__ __forceinline__ void store_out(void *out, size_t idx, float v, int out_dtype) {

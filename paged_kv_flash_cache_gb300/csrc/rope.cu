@@ -178,26 +178,28 @@ __device__ __forceinline__ void turn_row(float2 (&fa)[4], float2 (&fb)[4], const
     }
 }
 
-// An FP8 row: the codes of a lane's two vectors and the row's scale.
+// An FP8 row: the codes of a lane's two vectors and the row's scale. A row with a NaN gets the scale NaN (and codes of 0
+// where its elements are finite), one with an infinity an infinite scale and NaN codes: none of its elements reads as a number.
 template <int D>
 __device__ __forceinline__ void store_codes(const RopeArgs &a, size_t row, const float2 (&fa)[4], const float2 (&fb)[4],
                                             int va, int vb, bool first, bool live) {
     float amax = 0.f;
 #pragma unroll
     for (int i = 0; i < 4; ++i)
-        amax = fmax3(fmax3(amax, fabsf(fa[i].x), fabsf(fa[i].y)), fabsf(fb[i].x), fabsf(fb[i].y));
+        amax = fmax3_nan(fmax3_nan(amax, fabsf(fa[i].x), fabsf(fa[i].y)), fabsf(fb[i].x), fabsf(fb[i].y));
 #pragma unroll
-    for (int o = D / 32; o > 0; o >>= 1) amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, o));
+    for (int o = D / 32; o > 0; o >>= 1) amax = fmax_nan(amax, __shfl_xor_sync(0xffffffffu, amax, o));
     // one division: the row's first lane makes the scale, the others 448 / amax, which the first takes from its neighbour
     const float quotient = (first ? amax : 448.0f) / (first ? 448.0f : amax);
     const float inv = __shfl_down_sync(0xffffffffu, quotient, first ? 1 : 0);
     if (!live) return;
     uint2 ca = make_uint2(0u, 0u), cb = ca;
     float scale = 0.f;
-    if (amax > 0.f) {
+    if (amax != 0.f) {
         scale = quotient;
-        ca = codes_of(fa, inv);
-        cb = codes_of(fb, inv);
+        const float times = amax > 0.f ? inv : 0.f;  // (not of a NaN)
+        ca = codes_of(fa, times);
+        cb = codes_of(fb, times);
     }
     uint2 *dst = static_cast<uint2 *>(a.cache) + row * (D / 8);
     dst[va] = ca;
