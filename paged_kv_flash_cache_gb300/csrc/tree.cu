@@ -37,15 +37,14 @@
 // An FP8 cache: the codes land where the tile's second half goes (head_dim 64: apart) and become 16-bit values in place,
 // exactly: the keys' by a warpgroup of their own, with their row scales on the scores in FP32; the values' by the softmax
 // warps, times their scales' powers of two, what the scales are above those going to the weights before P's one rounding.
-// Bound by the chain of conversion and softmax in the same warps, whose dependent instructions leave the schedulers idle
-// more than half of the time.
+// Bound by the chain of conversion and softmax in the same warps.
 //
 // Measured, main kernel and merge, back to back (of the copy rate):
 //   16 sequences x 64 nodes, 32 KV heads x 128, contexts 1k-8k in pages of 16 (1.02 GB): 165 us, 91%, bound by HBM;
-//     over an FP8 cache (0.54 GB) 279 us
-//   25 nodes of 32 / 8 heads over 131k tokens in pages of 64 (0.54 GB): 98 us, 81%, the merge 8 us of it; FP8 122 us
+//     over an FP8 cache (0.54 GB) 209 us
+//   25 nodes of 32 / 8 heads over 131k tokens in pages of 64 (0.54 GB): 98 us, 81%, the merge 8 us of it; FP8 117 us
 //   32 sequences x 63 nodes of 32 / 8 heads, contexts to 8k (0.27 GB, 252 rows a KV head): 75 us, 53%, bound by the wide
-//     chain (about 3800 cycles a tile, of them 2560 in the tensor cores) and the merge, 13 us; FP8 123 us
+//     chain (about 3800 cycles a tile, of them 2560 in the tensor cores) and the merge, 13 us; FP8 117 us
 //   8 sequences x 31 nodes at head_dim 256 (0.16 GB): 38 us, 62%: its 64-key tiles at the copy rate (2400 cycles each), the
 //     rest set-up, output and merge of short runs
 // A partial's rows go out at 29 to 53 bytes a cycle and SM, all SMs at once (L2's write rate): 5000 to 10000 cycles a run.
@@ -178,33 +177,28 @@ __device__ __forceinline__ uint32_t remainder_pair(float a, float b, uint32_t hi
     return pack_pair<false>(a - f.x, b - f.y);
 }
 
-// E4M3 codes as 16-bit values, on the integer pipe as far as it goes. A code s.eeee.mmm (bias 7) in the place of an f16's
-// s.0eeee.mmm0000000 (bias 15) is its value times 2^-8, exactly, subnormal codes included; in the place of a bf16's
-// s.0000eeee.mmm0000 (bias 127) its value times 2^-120. One exact 16-bit product with a power of two (a pair in `factor`)
-// brings it to where it is wanted: the keys to 2^-8, the values to their row scale's power of two. A NaN code (which only
-// a NaN input leaves) reads as 480, as in the prefill.
-constexpr float kCodeFactorInv = 256.f;
-
+// E4M3 codes as 16-bit values, exactly: cvt to f16 (16 x 64 nodes: 209 us; 279 with the codes' bits moved into place by
+// integer instructions, which read a NaN as 480), for bf16 on through FP32. A NaN code (0x7f, 0xff) is a NaN. V: times a power of two (a pair in
+// `factor`), exact too.
 template <bool BF16, bool V>
-__device__ __forceinline__ uint32_t code_pair(uint32_t w, uint32_t sel, uint32_t factor) {
-    const uint32_t t = __byte_perm(w, 0u, sel);
+__device__ __forceinline__ uint32_t code_pair(uint32_t codes, uint32_t factor) {
     uint32_t r;
+    asm("cvt.rn.f16x2.e4m3x2 %0, %1;" : "=r"(r) : "h"((unsigned short)codes));
     if constexpr (BF16) {
-        const uint32_t u = t << 4, tiny = u + (u & 0x08000800u) * 15u;  // the sign from bit 11 to bit 15
-        asm("mul.rn.bf16x2 %0, %1, %2;" : "=r"(r) : "r"(tiny), "r"(factor));
+        const float2 f = __half22float2(*reinterpret_cast<const __half2 *>(&r));
+        r = pack_pair<true>(f.x, f.y);
+        if constexpr (V) asm("mul.rn.bf16x2 %0, %0, %1;" : "+r"(r) : "r"(factor));
     } else {
-        r = (t + (t & 0x00800080u)) << 7;
         if constexpr (V) asm("mul.rn.f16x2 %0, %0, %1;" : "+r"(r) : "r"(factor));
     }
     return r;
 }
 
-// Eight codes (8 bytes) as 16-bit values: K times 2^-8, V as `factor` says.
+// Eight codes (8 bytes) as 16-bit values: K as they are, V times `factor`.
 template <bool BF16, bool V>
 __device__ __forceinline__ uint4 values_of(const uint2 &codes, uint32_t factor) {
-    if (!V) factor = 0x77807780u;  // bf16: 2^112
-    return make_uint4(code_pair<BF16, V>(codes.x, 0x4140u, factor), code_pair<BF16, V>(codes.x, 0x4342u, factor),
-                      code_pair<BF16, V>(codes.y, 0x4140u, factor), code_pair<BF16, V>(codes.y, 0x4342u, factor));
+    return make_uint4(code_pair<BF16, V>(codes.x & 0xffffu, factor), code_pair<BF16, V>(codes.x >> 16, factor),
+                      code_pair<BF16, V>(codes.y & 0xffffu, factor), code_pair<BF16, V>(codes.y >> 16, factor));
 }
 
 // A V row's scale as 2^e times the rest: the power of two goes to the values (`factor` for code_pair, exact), the rest, in
@@ -216,12 +210,12 @@ __device__ __forceinline__ uint32_t split_scale(float scale, float &rest) {
     const int biased = (int)(bits >> 23) & 255;
     if (biased == 255) {
         rest = 1.f;
-        const uint32_t f = (bits & 0x007fffffu) ? 0x7fffu : ((BF16 ? 0x7f80u : 0x7c00u) | (bits >> 31 << 15));
-        return f * 0x10001u;
+        return pack_pair<BF16>(scale, scale);
     }
     const int e = min(max(biased - 127, BF16 ? -100 : -22), 7);
     rest = scale * __uint_as_float((uint32_t)(127 - e) << 23);
-    return (BF16 ? (uint32_t)(247 + e) << 7 : (uint32_t)(23 + e) << 10) * 0x10001u;
+    const float power = __uint_as_float((uint32_t)(127 + e) << 23);
+    return pack_pair<BF16>(power, power);
 }
 
 template <bool BF16>
@@ -748,7 +742,7 @@ __global__ void __launch_bounds__(TreeLayout<D, FP8>::kThreads, 1)
                     convert_rows<D, BF16, false, 32>(sRing + slot * L::kTileBytes, smem + L::kCodeOff + slot * (kBN * 64u),
                                                      sc, first, s.len - (s.t0 + j) * kBN, 0, lane);
                     float *const ks = reinterpret_cast<float *>(smem + L::kKScaleOff) + (tiles & 3u) * 128u;
-                    ks[first + lane] = sc[first + lane] * kCodeFactorInv;
+                    ks[first + lane] = sc[first + lane];
                     tc::fence_proxy_async_smem();
                     __syncwarp();
                     if (lane == 0) mbar_arrive_n(&conv_full[slot], 2);  // (a V tile has 8 warps' arrivals)
@@ -798,9 +792,9 @@ __global__ void __launch_bounds__(TreeLayout<D, FP8>::kThreads, 1)
             float m = -INFINITY, l = 0.f;
             bool ok = true;
             // FP8: this warp's 16 rows of V_j, in the order of the tiles, V_0 now and V_{j + 1} after the last P over V_j
-            // is handed over. The keys' codes are the conversion warps', a tile and more ahead: 279 us for 16 x 64 nodes,
-            // 122 for the long context (all conversions there: 288 and 138; all of them here, before the values were
-            // exact: 336 and 169, against 319 and 138 then).
+            // is handed over. The keys' codes are the conversion warps', a tile and more ahead. (With conversions by
+            // integer instructions, 16 x 64 nodes and the long context: 279 and 122 us; all conversions there 288 and 138;
+            // all of them here, before the values were exact, 336 and 169 against 319 and 138 then.)
             const int seg_len = s.len, seg_t0 = s.t0, seg_n = s.n;
             auto convert_v = [&](int j) -> bool {
                 c_step(j == 0 ? (uint32_t)ahead : ahead + j <= T ? 2u : 1u);
