@@ -253,8 +253,9 @@ typedef struct {
  * (the addressing of pkv_kv_cache_append). All arithmetic in FP32, one rounding at the end; an FP8 cache
  * receives keys quantised from the FP32 values (scale and codes as pkv_kv_format), values as
  * pkv_kv_cache_append writes them, but that no element of a row with a NaN or an infinity reads as a number: its
- * scale is not finite (pkv_kv_cache_append passes over a NaN as it looks for the largest magnitude). The
- * pages name neither step; they are the usual ones of the models they serve.
+ * scale is not finite (pkv_kv_cache_append passes over a NaN as it looks for the largest magnitude), and that rows
+ * of magnitudes up to 2^-119 are stored as zeros. The pages name neither step; they are the usual ones of the
+ * models they serve.
  *   q             token t's heads [Hq, D] at q + t * q_stride elements, in the cache dtype;
  *   k, v          likewise [Hkv, D] with k_stride, v_stride. Strides are multiples of 8 elements and at
  *                 least a token's row: the three may be views of one fused projection's output.

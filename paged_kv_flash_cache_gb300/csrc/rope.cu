@@ -180,10 +180,13 @@ __device__ __forceinline__ void turn_row(float2 (&fa)[4], float2 (&fb)[4], const
 
 // An FP8 row: the codes of a lane's two vectors and the row's scale. A row with a NaN gets the scale NaN (and codes of 0
 // where its elements are finite), one with an infinity an infinite scale and NaN codes: none of its elements reads as a number.
+// A row of magnitudes up to kZeroRow, whose 448 / amax may be beyond FP32, is stored as one of zeros.
+constexpr float kZeroRow = 0x1p-119f;
+
 template <int D>
 __device__ __forceinline__ void store_codes(const RopeArgs &a, size_t row, const float2 (&fa)[4], const float2 (&fb)[4],
                                             int va, int vb, bool first, bool live) {
-    float amax = 0.f;
+    float amax = kZeroRow;
 #pragma unroll
     for (int i = 0; i < 4; ++i)
         amax = fmax3_nan(fmax3_nan(amax, fabsf(fa[i].x), fabsf(fa[i].y)), fabsf(fb[i].x), fabsf(fb[i].y));
@@ -195,7 +198,7 @@ __device__ __forceinline__ void store_codes(const RopeArgs &a, size_t row, const
     if (!live) return;
     uint2 ca = make_uint2(0u, 0u), cb = ca;
     float scale = 0.f;
-    if (amax != 0.f) {
+    if (amax != kZeroRow) {
         scale = quotient;
         const float times = amax > 0.f ? inv : 0.f;  // (not of a NaN)
         ca = codes_of(fa, times);
