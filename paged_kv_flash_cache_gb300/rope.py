@@ -8,8 +8,9 @@ The ladder: pair i of rotary_dim / 2 turns by base^(-2 i / rotary_dim) radians a
            divided by factor, the highest is left alone
   parts    each frequency by the turns it makes over the trained context (`original_length`): those
            with at least `fast` turns are kept, those with at most `slow` are divided by factor, the
-           ones between are blended linearly in the pair's index (between the indices at which the ladder
-           makes fast and slow turns); cosines and sines then carry 0.1 ln(factor) + 1
+           ones between are blended linearly in the pair's index (between the indices at which the ladder, or
+           its continuation, makes fast and slow turns, the second one rotary_dim - 1 at most); cosines and
+           sines then carry 0.1 ln(factor) + 1
   smooth   the same two ends, blended linearly in the turns themselves; no factor on the cosines
 """
 from __future__ import annotations
@@ -48,7 +49,7 @@ def rope_frequencies(rotary_dim: int, base: float = 10000.0, scaling: str = "non
             # the index at which the ladder makes t turns over the trained context
             def index(t):
                 return half * math.log(original_length / (2 * math.pi * t)) / math.log(base)
-            low, high = max(math.floor(index(fast)), 0), min(math.ceil(index(slow)), half - 1)
+            low, high = max(math.floor(index(fast)), 0), min(math.ceil(index(slow)), rotary_dim - 1)
             width = max(high - low, 1e-3)
             keep = [1.0 - min(max((i - low) / width, 0.0), 1.0) for i in range(half)]
             mscale = 0.1 * math.log(factor) + 1.0
