@@ -232,7 +232,7 @@ PKV_API pkv_status pkv_paged_attn_mixed(pkv_cache cache, const void *q, int num_
  *                head_dim; the others pass unrotated.
  *   interleaved  0: pair i is elements i and i + rotary_dim / 2; else elements 2i and 2i + 1.
  *   inv_freq     device FP32 [rotary_dim / 2], finite: pair i of a token at position p is turned by the angle
- *                p * inv_freq[i] (exact to FP32's precision for every int32 position). Scaling for
+ *                p * inv_freq[i] (exact to FP32's precision for every int32 position, |inv_freq[i]| up to 2^40). Scaling for
  *                long contexts is a choice of these values. NULL allowed when rotary_dim is 0.
  *   mscale       factor on the cosines and sines (1 for none); finite.
  *   q_weight, k_weight  RMS norm weights [head_dim] in the cache dtype, applied to each query / key head
