@@ -658,8 +658,8 @@ TreeRows tree_rows(int group, int head_dim, int max_q_len) {
 extern "C" {
 
 size_t pkv_tree_workspace_size(int num_q_heads, int num_kv_heads, int head_dim, int max_q_len) {
-    if (num_q_heads <= 0 || num_kv_heads <= 0 || head_dim <= 0 || max_q_len <= 0 || num_q_heads % num_kv_heads != 0)
-        return 0;
+    if (num_q_heads <= 0 || num_kv_heads <= 0 || max_q_len <= 0 || num_q_heads % num_kv_heads != 0) return 0;
+    if (head_dim != 64 && head_dim != 128 && head_dim != 256) return 0;
     const TreeRows t = tree_rows(num_q_heads / num_kv_heads, head_dim, max_q_len);
     // a run's merge item, and its two partials: rows of head_dim outputs and an lse
     return (size_t)kTreeMaxRuns * (sizeof(MergeItem) + 2 * (size_t)t.part_rows * ((size_t)head_dim + 1) * sizeof(float));

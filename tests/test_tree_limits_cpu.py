@@ -1,0 +1,16 @@
+"""Sizes that paged_attn_tree does not take, on the host: no GPU needed."""
+import pytest
+
+import paged_kv_flash_cache_gb300 as pkv
+from tests.test_drafted_step_cpu import UNSUPPORTED, cache, call_tree, lib  # noqa: F401
+
+
+@pytest.mark.parametrize("head_dim", [8, 32, 80, 96, 192, 512, 1 << 30])
+def test_no_workspace_for_head_dims_that_are_refused(lib, head_dim):  # noqa: F811
+    assert pkv.tree_workspace_size(4, 2, head_dim, 8) == 0
+    assert call_tree(lib, cache(d=head_dim)) == UNSUPPORTED
+
+
+@pytest.mark.parametrize("head_dim", [64, 128, 256])
+def test_workspace_for_those_that_are_not(lib, head_dim):  # noqa: F811
+    assert pkv.tree_workspace_size(4, 2, head_dim, 8) == 160 * (32 + 2 * 128 * (head_dim + 1) * 4)
