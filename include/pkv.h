@@ -293,9 +293,11 @@ PKV_API size_t pkv_tree_workspace_size(int num_q_heads, int num_kv_heads, int he
  *   workspace     pkv_tree_workspace_size() bytes of device scratch; contents need no init. Calls that may
  *                 overlap on the GPU need one each.
  *   out           [total_q, Hq, D] in out_dtype; lse FP32 [total_q, Hq] or NULL.
+ * Pools of 2^31 rows (num_blocks * 2 * num_kv_heads * block_size) and more and tables of more than 2^30 tokens a
+ * sequence are not supported (PKV_ERR_UNSUPPORTED).
  * A node that sees nothing (no context, empty mask row) gets output 0 and lse -inf. What a masked key or value
  * holds, infinities and NaN included, does not reach the nodes that do not see it; a NaN that a node sees (a NaN code
- * of an FP8 cache too) makes its outputs NaN, an infinity makes them infinite or NaN. A sequence with a length out of
+ * of an FP8 cache too) makes its outputs NaN, an infinite value makes them infinite or NaN. A sequence with a length out of
  * range (n_b > max_q_len, context_lens[b] < n_b or beyond the table) is skipped and flagged, its rows
  * left as they were; a page id outside the pool is flagged and page 0 read.
  * head_dim 64, 128 or 256 (an FP8 cache: 64 or 128), any grouping, any number of nodes. Sums and softmax statistics are FP32.

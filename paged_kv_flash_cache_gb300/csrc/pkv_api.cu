@@ -682,6 +682,9 @@ pkv_status pkv_paged_attn_tree(pkv_cache cache, const void *q, int num_q_heads, 
     if (!aligned16(q) || !aligned16(out) || (lse && !aligned16(lse))) return PKV_ERR_INVALID_ARG;
     const long long cap = (long long)max_blocks_per_seq * cache.block_size;
     if (cap > (1ll << 30)) return PKV_ERR_UNSUPPORTED;
+    // the pool's rows are int32 TMA coordinates
+    if ((unsigned long long)cache.num_blocks * 2 * cache.num_kv_heads > 0x7fffffffull / cache.block_size)
+        return PKV_ERR_UNSUPPORTED;
     const size_t need = pkv_tree_workspace_size(num_q_heads, cache.num_kv_heads, cache.head_dim, max_q_len);
     if (!workspace || workspace_bytes < need || !aligned16(workspace)) return PKV_ERR_WORKSPACE;
     DeviceSlot *s = slot();

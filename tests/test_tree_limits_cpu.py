@@ -14,3 +14,13 @@ def test_no_workspace_for_head_dims_that_are_refused(lib, head_dim):  # noqa: F8
 @pytest.mark.parametrize("head_dim", [64, 128, 256])
 def test_workspace_for_those_that_are_not(lib, head_dim):  # noqa: F811
     assert pkv.tree_workspace_size(4, 2, head_dim, 8) == 160 * (32 + 2 * 128 * (head_dim + 1) * 4)
+
+
+def test_pools_of_2_31_rows_are_refused(lib):  # noqa: F811
+    """The rows of the pool are TMA coordinates of 32 bits with a sign. (An FP8 pool of so many rows of 64 bytes has 137 GB.)"""
+    for c in (cache(nb=1 << 22, hkv=32, bs=8), cache(nb=1 << 21, hkv=8, bs=64, d=64, fmt=1, scales=4096),
+              cache(nb=(1 << 31) - 1, hkv=1 << 30, bs=512)):
+        assert call_tree(lib, c, hq=c.num_kv_heads) == UNSUPPORTED
+    # one page less: refused for something else (a workspace of one byte), or not at all
+    for c in (cache(nb=(1 << 22) - 1, hkv=32, bs=8), cache(nb=(1 << 21) - 1, hkv=8, bs=64, d=64, fmt=1, scales=4096)):
+        assert call_tree(lib, c, hq=c.num_kv_heads, bytes=1) == 3
