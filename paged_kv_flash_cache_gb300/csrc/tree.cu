@@ -67,6 +67,11 @@ namespace {
 
 constexpr int kBM = 128;              // rows of a tile
 constexpr float kRescaleLog2 = 8.0f;  // O is rescaled when the running max grows by more than 2^8
+// f16 weights (and with them the sum and the output, which the quotient takes out again) are 2^kUp times themselves: f16 has no
+// step below 2^-24, and of a long context keys that far below the largest weight can be as much as the rest together. Up to
+// 2^8 (kRescaleLog2) times that they stay below 2^15; over FP8 there is room for the V scales' rests, below 2^4 for scales below 2^11.
+template <bool BF16, bool FP8>
+constexpr float kUp = BF16 ? 0.f : FP8 ? 4.f : 7.f;
 constexpr int kSegs = 4;              // segments handed out ahead
 constexpr int kItemCost = 3;          // an item's set-up and output, in key tiles (about 11000 cycles against 3800)
 constexpr int kMinTiles = 2;          // work of a run at least, in key tiles (4: 16.2 us for 15.6, 16 nodes over 4k tokens)
@@ -867,7 +872,7 @@ __global__ void __launch_bounds__(TreeLayout<D, FP8>::kThreads, 1)
                         m = m_new;
                         l *= alpha;
                     }
-                    const float base = m == -INFINITY ? 0.f : m;  // a row that has seen nothing: ex2(-inf - 0) = 0
+                    const float base = m == -INFINITY ? 0.f : m - kUp<BF16, FP8>;  // a row that has seen nothing: ex2(-inf - 0) = 0
                     const float2 cc2 = make_float2(c2, c2), nm2 = make_float2(-base, -base);
                     float2 l4[4] = {make_float2(0.f, 0.f), make_float2(0.f, 0.f), make_float2(0.f, 0.f),
                                     make_float2(0.f, 0.f)};
@@ -990,7 +995,7 @@ __global__ void __launch_bounds__(TreeLayout<D, FP8>::kThreads, 1)
                 }
             }
             const float inv = lt > 0.f ? 1.f / lt : (lt == 0.f ? 0.f : lt);  // (a NaN sum stays NaN)
-            lse2 = lt == 0.f ? -INFINITY : lse2 + __log2f(lt);
+            lse2 = lt == 0.f ? -INFINITY : lse2 + __log2f(lt) - kUp<BF16, FP8>;
             fa *= inv;
             fb *= inv;
             if (!mbar_wait(o_done, seg_i & 1u, abort_flag, a.err)) break;
