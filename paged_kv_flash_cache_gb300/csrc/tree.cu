@@ -206,9 +206,11 @@ __device__ __forceinline__ uint4 values_of(const uint2 &codes, uint32_t factor) 
                       code_pair<BF16, V>(codes.y & 0xffffu, factor), code_pair<BF16, V>(codes.y >> 16, factor));
 }
 
-// A V row's scale as 2^e times the rest: the power of two goes to the values (`factor` for code_pair, exact), the rest, in
-// [1, 2) for every scale that the append writes, to the weights. e is held to where factor and values are numbers
-// of the 16-bit type (f16 below 2^-22: values round as f16 subnormals do). A scale that is not finite: values that are not.
+// A V row's scale as 2^e times the rest: the power of two goes to the values (`factor` for code_pair), the rest to the
+// weights. e is held to where factor and values are numbers of the 16-bit type: [-22, 7] (f16), [-100, 7] (bf16). The rest is
+// in [1, 2) for scales there, above 2 for scales from 2^8 on: bf16's exponents have room for it, f16's up to scales of 2^10
+// (f16 values have scales up to 147). Values are exact but for f16 and e < -15, where they round as subnormals do, by 2^-25 at
+// most: 2^-11.8 of the row's largest, 448 x 2^e. A scale that is not finite: values that are not.
 template <bool BF16>
 __device__ __forceinline__ uint32_t split_scale(float scale, float &rest) {
     const uint32_t bits = __float_as_uint(scale);
