@@ -14,8 +14,8 @@
 //
 // The angle: position * inv_freq reaches 10^5 radians and more in a long context, where an FP32 product
 // is off by hundredths. Only the angle's fraction of a turn matters, and integers wrap for free: with
-// F = frac(inv_freq / 2 pi) as a 64-bit fraction (one FP64 product per frequency and warp, two more above one radian a
-// position), F * position modulo 2^64 is the fraction of a turn, to 2^-24 of a turn or better for every int32 position and
+// F = frac(inv_freq / 2 pi) as a 64-bit fraction (a few FP64 operations per frequency and warp, 1 / 2 pi in two FP64
+// words), F * position modulo 2^64 is the fraction of a turn, to 2^-24 of a turn or better for every int32 position and
 // |inv_freq| up to 2^40; its top 32 bits, as a signed number of half turns, go to sincospif.
 //
 // One warp per (token, share of its rows). A row is held by D / 16 lanes, each with two 16-byte vectors that hold whole
@@ -52,16 +52,8 @@ struct RopeShape {
     static constexpr int kSmem = kWarps * kSlots * kGroupBytes;
 };
 
-// 1 / 2 pi in two FP64 numbers
+// 1 / 2 pi in two FP64 words
 constexpr double kInvTwoPi = 0.15915494309189533577, kInvTwoPiLow = -9.839338337591243e-18;
-
-// What inv_freq times the first of them rounds off and the second one adds, in 2^-64 turns: above one radian a position, turns
-// that far positions count. (Not inline: FP64 is slow, the usual frequencies are at most 1, and the code in place cost the FP8
-// rows 1 us of 33.)
-__device__ __noinline__ unsigned long long low_turns(float inv_freq) {
-    const double w = inv_freq, p = __dmul_rn(w, kInvTwoPi);
-    return (unsigned long long)(long long)(fma(w, kInvTwoPiLow, fma(w, kInvTwoPi, -p)) * 18446744073709551616.0);
-}
 
 template <bool BF16>
 __device__ __forceinline__ void unpack_row(const uint4 &raw, float2 (&f)[4]) {
@@ -254,6 +246,20 @@ __global__ void __launch_bounds__(kRopeThreads, RopeShape<NORM>::kCtas) rope_app
     }
     __syncthreads();
     pdl_wait();  // the projections come from the previous kernel, which may also still read the pages
+    // F = frac(inv_freq / 2 pi) in 64 bits, signed: what the product is from the nearest whole turn, rounded once, and the
+    // second word's part, which counts for frequencies above one radian a position
+    unsigned long long turn[kPer];
+#pragma unroll
+    for (int i = 0; i < kPer; ++i) {
+        const int f = lane + 32 * i;
+        turn[i] = 0;
+        if (f < a.rotary_dim / 2) {
+            const double w = (double)__ldg(a.inv_freq + f);
+            const double x = __fma_rn(w, kInvTwoPi, -rint(__dmul_rn(w, kInvTwoPi)));
+            turn[i] = (unsigned long long)(long long)(x * 0x1p64) +
+                      (unsigned long long)(long long)(w * (kInvTwoPiLow * 0x1p64));
+        }
+    }
     const int total = min(a.num_new_tokens, __ldg(a.cu_new_lens + a.batch));  // tokens behind the last sequence: left alone
     const int stride = gridDim.x * kWarps;
     // the groups of this warp's tokens in order: the next one to fetch, and the fetched and used ones so far
@@ -290,25 +296,6 @@ __global__ void __launch_bounds__(kRopeThreads, RopeShape<NORM>::kCtas) rope_app
         __syncwarp();  // every lane has read it
         fetch();
     };
-    // F = frac(inv_freq / 2 pi) in 64 bits, as a signed fraction: inv_freq / 2 pi to the nearest whole turn
-    unsigned long long turn[kPer];
-    bool more = false;
-#pragma unroll
-    for (int i = 0; i < kPer; ++i) {
-        const int f = lane + 32 * i;
-        turn[i] = 0;
-        if (f < a.rotary_dim / 2) {
-            const float w = __ldg(a.inv_freq + f);
-            const double p = __dmul_rn(w, kInvTwoPi);  // (rounded, whatever is made of it: see low_turns)
-            turn[i] = (unsigned long long)(long long)((p - rint(p)) * 18446744073709551616.0);
-            more |= fabsf(w) > 1.f;
-        }
-    }
-    if (more) {
-#pragma unroll
-        for (int i = 0; i < kPer; ++i)
-            if (lane + 32 * i < a.rotary_dim / 2) turn[i] += low_turns(__ldg(a.inv_freq + lane + 32 * i));
-    }
 #pragma unroll
     for (int i = 0; i < kSlots; ++i) fetch();
     bool ok = true;
