@@ -149,10 +149,13 @@ def tree_depths(parents: Sequence[Sequence[int]]) -> torch.Tensor:
     """Depth of every node, packed by sequence (int32): 0 for a node whose parent is the context. The rotary
     position of a drafted token is its sequence's context length plus its depth."""
     out: List[int] = []
-    for seq in parents:
+    for b, seq in enumerate(parents):
         d: List[int] = []
-        for p in seq:
-            d.append(0 if int(p) < 0 else d[int(p)] + 1)
+        for i, p in enumerate(seq):
+            p = int(p)
+            if not -1 <= p < i:
+                raise ValueError("sequence %d: the parent of node %d must be -1 or an earlier node" % (b, i))
+            d.append(0 if p < 0 else d[p] + 1)
         out += d
     return torch.tensor(out, dtype=torch.int32)
 

@@ -2,6 +2,7 @@
 import pytest
 
 import paged_kv_flash_cache_gb300 as pkv
+from paged_kv_flash_cache_gb300 import workloads as W
 from tests.test_drafted_step_cpu import UNSUPPORTED, cache, call_tree, lib  # noqa: F401
 
 
@@ -24,3 +25,10 @@ def test_pools_of_2_31_rows_are_refused(lib):  # noqa: F811
     # one page less: refused for something else (a workspace of one byte), or not at all
     for c in (cache(nb=(1 << 22) - 1, hkv=32, bs=8), cache(nb=(1 << 21) - 1, hkv=8, bs=64, d=64, fmt=1, scales=4096)):
         assert call_tree(lib, c, hq=c.num_kv_heads, bytes=1) == 3
+
+
+@pytest.mark.parametrize("parents", [[[0]], [[-1, 2, 0]], [[-2]], [[-1], [-1, 0, -3]]])
+def test_depths_refuse_the_parents_that_masks_refuse(parents):
+    for make in (W.tree_mask, W.tree_depths):
+        with pytest.raises(ValueError):
+            make(parents)
