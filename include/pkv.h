@@ -306,7 +306,7 @@ PKV_API size_t pkv_tree_workspace_size(int num_q_heads, int num_kv_heads, int he
  * than 128, and over an FP8 cache. There the products run in the 16-bit type of q: the key codes exactly, their row
  * scales in FP32 on the scores; the value codes times their row scales' powers of two, the weights times what the scales
  * are above those before their rounding. That is exact in bf16; f16 takes value scales below 2^10 (what f16 inputs leave is
- * at most 147), and below 2^-15 rounds values by 2^-11.8 of their row's largest at most. */
+ * at most 147), and below 2^-15 rounds values by 2^-11.8 of 448 times their scale at most. */
 PKV_API pkv_status pkv_paged_attn_tree(pkv_cache cache, const void *q, int num_q_heads, const int *tree_mask, int mask_words,
                                const int *cu_q_lens, const int *context_lens, const int *block_tables, int batch,
                                int max_blocks_per_seq, int total_q, int max_q_len, float scale, void *workspace,

@@ -13,6 +13,8 @@
 // vectors a thread: the rows' places are looked up a chunk ahead, a thread a row, into shared memory, so that the
 // moves themselves wait for one read only; a barrier stands between a chunk's loads and its stores (a
 // store of chunk c can only meet a source of chunk c or earlier, whose loads precede the barrier).
+// The batch's average number of rows chooses (counts on the device do not reach the launch), so a batch in which one list is much
+// longer than the others takes as long as that list does with what the average gives it:
 //   few rows   a warp a slice;
 //   more       `shares` CTAs a slice, each moving an equal piece of its rows. Pieces are independent
 //              when no row's source lies in a later piece's destinations (a window moved up behind a prompt);

@@ -43,8 +43,9 @@ constexpr int kWarps = kRopeThreads / 32;
 constexpr int kUnroll = 4;  // passes (of 512 / D rows) of a group
 constexpr int kGroupBytes = kUnroll * 1024;
 // CTAs an SM, and groups of a warp on their way or in work: with a norm the coefficients of two kinds of weights take
-// registers for 4 CTAs (3 slots each: 37 us for the prompts above; 6 of 2 spill, 48 us), without one there are enough for 6
-// (4099 tokens into an FP8 cache: 33 us against 38).
+// registers for 4 CTAs (3 slots each: 37 us for the prompts above; 6 of 2 spill, 48 us). Without one 6 are better (4099 tokens
+// into an FP8 cache: 33 us against 38), though their 80 registers make most of those kernels spill a little, 8 to 52 bytes
+// (the prompts above without norms: 37.5 us; 5 CTAs have not been tried there).
 template <bool NORM>
 struct RopeShape {
     static constexpr int kCtas = NORM ? 4 : 6;
@@ -87,11 +88,10 @@ __device__ __forceinline__ int sequence_of(const int *cu, int batch, int t) {
 }
 
 // Row of new token t's K in head 0 of its page (rows of the cache counted [page][K, V][head][offset]), or -1 (error
-// word set) for a position outside the table or a page outside the pool. cu / before: the sequences' lists, in global
-// or shared memory.
-__device__ __forceinline__ long long token_row(const RopeArgs &a, const int *cu, const int *before, int t) {
-    const int b = sequence_of(cu, a.batch, t);
-    const long long pos = (long long)before[b] + (t - cu[b]);
+// word set) for a position outside the table or a page outside the pool.
+__device__ __forceinline__ long long token_row(const RopeArgs &a, int t) {
+    const int b = sequence_of(a.cu_new_lens, a.batch, t);
+    const long long pos = (long long)a.ctx_before[b] + (t - a.cu_new_lens[b]);
     const long long logical = pos >> a.log2_block_size;
     int pb = -1;
     if (pos >= 0 && logical < a.max_blocks_per_seq) pb = __ldg(a.block_tables + (size_t)b * a.max_blocks_per_seq + logical);
@@ -307,7 +307,7 @@ __global__ void __launch_bounds__(kRopeThreads, RopeShape<NORM>::kCtas) rope_app
             const long long mine = t + (long long)lane * stride;
             if (mine < total) {
                 s_pos[warp][lane] = __ldg(a.positions + mine);
-                if (g_end > gq) s_row[warp][lane] = token_row(a, a.cu_new_lens, a.ctx_before, (int)mine);
+                if (g_end > gq) s_row[warp][lane] = token_row(a, (int)mine);
             }
         }
         __syncwarp();  // (and the last token's cosines are read)

@@ -73,7 +73,10 @@ constexpr float kRescaleLog2 = 8.0f;  // O is rescaled when the running max grow
 template <bool BF16, bool FP8>
 constexpr float kUp = BF16 ? 0.f : FP8 ? 4.f : 7.f;
 constexpr int kSegs = 4;              // segments handed out ahead
-constexpr int kItemCost = 3;          // an item's set-up and output, in key tiles (about 11000 cycles against 3800)
+// An item's set-up and output, in key tiles: about 11000 cycles against the 3800 of a wide block's tile at head_dim 128, where it
+// was measured. The other kernels use it too, though it fits them less well (head_dim 256: 64-key tiles of 2400 cycles), so
+// that their runs are less evenly cut.
+constexpr int kItemCost = 3;
 constexpr int kMinTiles = 2;          // work of a run at least, in key tiles (4: 16.2 us for 15.6, 16 nodes over 4k tokens)
 
 // One run's part of an item: key tiles [t0, t1) of nodes [node0, node0 + nodes) of one sequence and KV
