@@ -69,7 +69,7 @@ constexpr int kBM = 128;              // rows of a tile
 constexpr float kRescaleLog2 = 8.0f;  // O is rescaled when the running max grows by more than 2^8
 // f16 weights (and with them the sum and the output, which the quotient takes out again) are 2^kUp times themselves: f16 has no
 // step below 2^-24, and of a long context keys that far below the largest weight can be as much as the rest together. Up to
-// 2^8 (kRescaleLog2) times that they stay below 2^15; over FP8 there is room for the V scales' rests, below 2^4 for scales below 2^11.
+// 2^8 (kRescaleLog2) times that they stay within 2^15; over FP8 the V scales' rests, below 2^3 for scales below 2^10, do too.
 template <bool BF16, bool FP8>
 constexpr float kUp = BF16 ? 0.f : FP8 ? 4.f : 7.f;
 constexpr int kSegs = 4;              // segments handed out ahead
@@ -185,9 +185,9 @@ __device__ __forceinline__ uint32_t remainder_pair(float a, float b, uint32_t hi
     return pack_pair<false>(a - f.x, b - f.y);
 }
 
-// E4M3 codes as 16-bit values, exactly: cvt to f16 (16 x 64 nodes: 209 us; 279 with the codes' bits moved into place by
-// integer instructions, which read a NaN as 480), for bf16 on through FP32. A NaN code (0x7f, 0xff) is a NaN. V: times a power of two (a pair in
-// `factor`), exact too.
+// E4M3 codes as 16-bit values, exactly: cvt to f16, for bf16 on through FP32 (16 x 64 nodes: 209 us; 279 with the codes' bits
+// moved into place by integer instructions, which read a NaN as 480). A NaN code (0x7f, 0xff) is a NaN. V: times a power of
+// two, a pair of it in `factor` (see split_scale).
 template <bool BF16, bool V>
 __device__ __forceinline__ uint32_t code_pair(uint32_t codes, uint32_t factor) {
     uint32_t r;
@@ -877,7 +877,8 @@ __global__ void __launch_bounds__(TreeLayout<D, FP8>::kThreads, 1)
                         m = m_new;
                         l *= alpha;
                     }
-                    const float base = m == -INFINITY ? 0.f : m - kUp<BF16, FP8>;  // a row that has seen nothing: ex2(-inf - 0) = 0
+                    // (a row that has seen nothing: ex2(-inf - 0) = 0)
+                    const float base = m == -INFINITY ? 0.f : m - kUp<BF16, FP8>;
                     const float2 cc2 = make_float2(c2, c2), nm2 = make_float2(-base, -base);
                     float2 l4[4] = {make_float2(0.f, 0.f), make_float2(0.f, 0.f), make_float2(0.f, 0.f),
                                     make_float2(0.f, 0.f)};
