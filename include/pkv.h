@@ -81,16 +81,32 @@ typedef enum { PKV_F16 = 0, PKV_BF16 = 1, PKV_F32 = 2 } pkv_dtype;
  *                   in FP32 (amax = largest |x| of the row; an all-zero row stores
  *                   scale 0 and zero codes).  The pages name KV-cache compression
  *                   ([ON2]) without a scheme; this per-row scaling is the library's
- *                   reading of it. */
-typedef enum { PKV_KV_NATIVE = 0, PKV_KV_FP8_E4M3 = 1 } pkv_kv_format;
+ *                   reading of it.
+ *  PKV_KV_INT8_BLOCK  ptr holds one-byte integers in [-127, 127] and `scales` one FP32
+ *                   scale per block of tokens (a page), K or V, and KV head: element =
+ *                   code * scale. pkv_kv_cache_append writes powers of two. For the rows that a
+ *                   call adds to a page, a the largest magnitude in them (of one head's K or V):
+ *                   the scale becomes the least power of two s >= 2^-126 with a <= 127 s where the
+ *                   page has no older rows (0 for a = 0); stays where it has some and a <= 127 times
+ *                   the scale; else becomes that power of two, and the older codes c are rounded again,
+ *                   c * old / s to nearest even. The new codes are x / s to nearest even. A value is off
+ *                   by at most half a step of the scale it was written with, and by less than one step
+ *                   of the page's last scale in all, however often that grew. Rows with a NaN or an
+ *                   infinity make the scale NaN: the page reads as NaN until it starts again with its first row.
+ *                   Attention takes any finite scale >= 0 (caches quantised elsewhere): exactly in FP32
+ *                   in the decode, rounded to 11 bits relative to the context's largest in the prefill
+ *                   (powers of two are exact in both). */
+typedef enum { PKV_KV_NATIVE = 0, PKV_KV_FP8_E4M3 = 1, PKV_KV_INT8_BLOCK = 2 } pkv_kv_format;
 
 /* The paged KV cache [num_blocks, 2, num_kv_heads, block_size, head_dim] ([FAPA] s3).
  * dtype (PKV_F16 or PKV_BF16) is the type of q, k_new and v_new, of the default
  * output, and of the elements of a native cache.  Supported: head_dim 64, 128 or
- * 256 (256: a native cache only; an FP8 cache with head_dim 256 returns
+ * 256 (256: a native cache only; an FP8 or INT8 cache with head_dim 256 returns
  * PKV_ERR_UNSUPPORTED); block_size a power of two in [8, 512].  format and scales
- * are as above (scales [num_blocks, 2, num_kv_heads, block_size], 16-byte aligned;
- * NULL for a native cache).  Every call accepts an FP8 cache.  Over an FP8 cache
+ * are as above (scales [num_blocks, 2, num_kv_heads, block_size] for FP8, [num_blocks, 2,
+ * num_kv_heads] for INT8, 16-byte aligned; NULL for a native cache).  Every call accepts an FP8
+ * cache; pkv_rope_append, pkv_paged_attn_tree and pkv_kv_cache_compact refuse an INT8 cache
+ * (PKV_ERR_UNSUPPORTED).  Over an FP8 or INT8 cache
  * the tensor-core products run in f16 on the exact codes (the row scales are
  * applied in FP32): q must lie within f16's range (|q| < 65504; magnitudes below
  * 2^-24 count as 0). */
@@ -116,7 +132,9 @@ typedef struct {
  *                     sequence b goes to position ctx_before[b] + j.
  *   block_tables      int32 [batch, max_blocks_per_seq]; pages for every written
  *                     position must already be assigned.
- * A native cache receives a bit-exact copy.  Positions whose table slot is beyond max_blocks_per_seq,
+ * A native cache receives a bit-exact copy; an INT8 cache codes and scales as described at
+ * pkv_kv_format (the written pages must be the sequence's own: a page that another table shares would
+ * change for both, and two sequences of a call that write one page leave it undefined).  Positions whose table slot is beyond max_blocks_per_seq,
  * or whose page id is outside [0, num_blocks), are skipped and flag
  * PKV_ERR_DEVICE_RANGE.  Nothing else in the cache is modified. */
 PKV_API pkv_status pkv_kv_cache_append(pkv_cache cache, const void *k_new, const void *v_new,
@@ -327,6 +345,35 @@ PKV_API pkv_status pkv_paged_attn_tree(pkv_cache cache, const void *q, int num_q
 PKV_API pkv_status pkv_kv_cache_compact(pkv_cache cache, const int *keep_pos, const int *cu_keep, const int *dst_start,
                                 const int *block_tables, int batch, int max_blocks_per_seq, int num_keep,
                                 void *stream);
+
+/* kv_cache_copy -- pages copied bit for bit, from one pool to another or inside one (dst and src the same): copy on
+ * write of shared pages, moving a sequence's pages, compacting a pool. Page src_pages[i] goes to page dst_pages[i]:
+ * K, V and (FP8, INT8) scales of every head.
+ *   src, dst      the same format, type, heads, block_size and head_dim.
+ *   src_pages, dst_pages  int32 [num_pages]. No page is a destination twice, or a source and a destination, in one
+ *                 call (such a page's contents are undefined afterwards).
+ *   num_rows      int32 [num_pages]: the leading rows that are copied (0 to block_size; an INT8 page's scales go along
+ *                 where it is above 0), the others are left alone; NULL: whole pages.
+ * Page ids outside their pool and row counts out of range are skipped and flagged (PKV_ERR_DEVICE_RANGE). */
+PKV_API pkv_status pkv_kv_cache_copy(pkv_cache dst, pkv_cache src, const int *src_pages, const int *dst_pages,
+                             const int *num_rows, int num_pages, void *stream);
+
+/* kv_cache_fork -- sequences that continue others (parallel samples of a prompt, the beams of a search): child c
+ * continues parent p = parents[c], whose first context_lens[p] tokens it shares.
+ *   block_tables  int32 [num_parents, max_blocks_per_seq], context_lens int32 [num_parents]: the parents.
+ *   parents       int32 [num_children]. A parent may have any number of children.
+ *   new_pages     int32 [num_children]: a page for the child's next token, which no sequence holds; or -1.
+ *   out_tables    int32 [num_children, max_blocks_per_seq], out_lens int32 [num_children]: the children. They must not
+ *                 overlap an input (else PKV_ERR_INVALID_ARG).
+ * A child's table names its parent's full pages, which both then share. Where the parent's last page is partly
+ * filled, its rows are copied to new_pages[c], which takes its place; with -1 the child's table names the parent's
+ * page itself (right for one child of a parent that ends). Where it is full, new_pages[c] (if not -1) becomes the
+ * page of the child's next token. The entries behind are -1; out_lens[c] = context_lens[p].
+ * A parent outside [0, num_parents) or with a length out of range is flagged, and its child is empty; a new page
+ * outside the pool is flagged, and the child's entry is -1. Reference counts are the host's. */
+PKV_API pkv_status pkv_kv_cache_fork(pkv_cache cache, const int *block_tables, const int *context_lens, const int *parents,
+                             const int *new_pages, int num_parents, int num_children, int max_blocks_per_seq,
+                             int *out_tables, int *out_lens, void *stream);
 
 /* attn_combine -- log-sum-exp merge of split-KV partial results ([FAPA] s2: the
  * same rescale-by-exp(m_old - m_new) identity applied to whole splits).

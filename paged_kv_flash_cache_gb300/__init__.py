@@ -11,12 +11,14 @@ Entry points (same names as the C ABI without the ``pkv_`` prefix):
   attn_combine, decode_workspace_size, decode_split_tokens, get_device_error;
   around the attention of a step, and of a step with drafted tokens: rope_append (norm, rotary positions,
   append), paged_attn_tree and tree_workspace_size (a tree of drafted tokens over the cache), kv_cache_compact
-  (the rows that are kept move to the front). `rope.rope_frequencies`, `workloads.tree_mask` and
+  (the rows that are kept move to the front); kv_cache_copy and kv_cache_fork (pages copied; sequences that
+  continue others). `rope.rope_frequencies`, `workloads.tree_mask` and
   `workloads.tree_depths` make their arguments on the host.
 Cache tensors have shape [num_blocks, 2, num_kv_heads, block_size, head_dim]
 (K at index 0, V at index 1) in float16 or bfloat16, or hold FP8 E4M3 codes
 (torch.float8_e4m3fn or uint8) with a float32 `scales` tensor
-[num_blocks, 2, num_kv_heads, block_size], one scale per cached row; q, k_new and
+[num_blocks, 2, num_kv_heads, block_size], one scale per cached row, or INT8 codes
+(torch.int8) with `scales` [num_blocks, 2, num_kv_heads], one per page and head; q, k_new and
 v_new then stay float16 / bfloat16 (see pkv_kv_format in include/pkv.h).
 """
 from __future__ import annotations
@@ -31,7 +33,7 @@ __all__ = [
     "PkvError", "library_path", "load_library", "kv_cache_append", "paged_attn_decode", "paged_attn_prefill",
     "attn_combine", "decode_workspace_size", "decode_split_tokens", "get_device_error", "STATUS",
     "paged_attn_decode_noalloc", "paged_attn_mixed", "selftest_wait_timeout", "paged_attn_decode_step",
-    "rope_append", "paged_attn_tree", "tree_workspace_size", "kv_cache_compact",
+    "rope_append", "paged_attn_tree", "tree_workspace_size", "kv_cache_compact", "kv_cache_copy", "kv_cache_fork",
 ]
 
 _HERE = os.path.dirname(os.path.abspath(__file__))
@@ -42,12 +44,13 @@ _lib = None
 STATUS = {0: "PKV_OK", 1: "PKV_ERR_INVALID_ARG", 2: "PKV_ERR_UNSUPPORTED", 3: "PKV_ERR_WORKSPACE",
           4: "PKV_ERR_CUDA", 5: "PKV_ERR_DEVICE_RANGE", 6: "PKV_ERR_TIMEOUT"}
 F16, BF16, F32 = 0, 1, 2
-KV_NATIVE, KV_FP8_E4M3 = 0, 1
+KV_NATIVE, KV_FP8_E4M3, KV_INT8_BLOCK = 0, 1, 2
 
 # Every symbol include/pkv.h declares.
 EXPORTS = ("pkv_kv_cache_append", "pkv_decode_workspace_size", "pkv_decode_split_tokens", "pkv_paged_attn_decode",
            "pkv_paged_attn_decode_step", "pkv_paged_attn_decode_noalloc", "pkv_paged_attn_prefill", "pkv_paged_attn_mixed", "pkv_attn_combine",
            "pkv_rope_append", "pkv_paged_attn_tree", "pkv_tree_workspace_size", "pkv_kv_cache_compact",
+           "pkv_kv_cache_copy", "pkv_kv_cache_fork",
            "pkv_get_device_error", "pkv_selftest_wait_timeout", "pkv_status_string", "pkv_version")
 DECODE_NOALLOC_SCRATCH_BYTES = 32 * 1024 * 1024   # PKV_DECODE_NOALLOC_SCRATCH_BYTES in include/pkv.h
 
@@ -112,6 +115,10 @@ def load_library():
         lib.pkv_paged_attn_tree.restype = I
         lib.pkv_kv_cache_compact.argtypes = [_Cache, P, P, P, P, I, I, I, P]
         lib.pkv_kv_cache_compact.restype = I
+        lib.pkv_kv_cache_copy.argtypes = [_Cache, _Cache, P, P, P, I, P]
+        lib.pkv_kv_cache_copy.restype = I
+        lib.pkv_kv_cache_fork.argtypes = [_Cache, P, P, P, P, I, I, I, P, P, P]
+        lib.pkv_kv_cache_fork.restype = I
         lib.pkv_attn_combine.argtypes = [P, P, I, I, I, P, I, P, P]
         lib.pkv_attn_combine.restype = I
         lib.pkv_selftest_wait_timeout.argtypes = [ctypes.c_uint, P]
@@ -227,8 +234,15 @@ def _cache_struct(cache, act_dtype, scales=None) -> _Cache:
             raise ValueError("an FP8 cache needs float32 scales [num_blocks, 2, num_kv_heads, block_size]")
         return _Cache(_dev(cache, "cache"), nb, hkv, bs, d, _dtype_code(act_dtype), KV_FP8_E4M3,
                       _dev(scales, "scales"))
+    if cache.dtype is torch.int8:
+        if scales is None or scales.dtype != torch.float32 or tuple(scales.shape) != (nb, 2, hkv):
+            raise ValueError("an INT8 cache needs float32 scales [num_blocks, 2, num_kv_heads]")
+        if scales.get_device() != cache.get_device():
+            raise ValueError("scales on %s, the cache on another device" % scales.device)
+        return _Cache(_dev(cache, "cache"), nb, hkv, bs, d, _dtype_code(act_dtype), KV_INT8_BLOCK,
+                      _dev(scales, "scales"))
     if scales is not None:
-        raise ValueError("scales are only for an FP8 cache")
+        raise ValueError("scales are only for an FP8 or INT8 cache")
     if act_dtype != cache.dtype:
         raise TypeError("q / k_new / v_new must have the cache dtype")
     return _Cache(_dev(cache, "cache"), nb, hkv, bs, d, _dtype_code(cache.dtype), KV_NATIVE, None)
@@ -243,17 +257,52 @@ def _check(status: int, where: str):
 # entry points
 # ---------------------------------------------------------------------------------------------
 
+def _int8_args(cache, rows, rows_shape, batch, tables, lists):
+    """Checks of a call over an INT8 cache: the device of every tensor, the shape of the rows (name -> tensor) and of the
+    int32 lists (name -> (tensor, length))."""
+    index = cache.get_device()
+    for name, t in rows.items():
+        if t.shape != rows_shape:
+            raise ValueError("%s must be %s" % (name, list(rows_shape)))
+    for name, (t, n) in lists.items():
+        if t.shape != (n,):
+            raise ValueError("%s must be [%d]" % (name, n))
+        rows = dict(rows, **{name: t})
+    for name, t in dict(rows, block_tables=tables).items():
+        if t.get_device() != index:
+            raise ValueError("%s is on %s, the cache on another device" % (name, t.device))
+
+
+def _int8_out(cache, out, lse, shape, workspace=None):
+    """Checks of the tensors that an attention call over an INT8 cache writes."""
+    index = cache.get_device()
+    for name, t, want in (("out", out, shape), ("lse", lse, shape[:2]), ("workspace", workspace, None)):
+        if t is None:
+            continue
+        if t.get_device() != index:
+            raise ValueError("%s is on %s, the cache on another device" % (name, t.device))
+        if want is not None and tuple(t.shape) != tuple(want):
+            raise ValueError("%s must be %s" % (name, list(want)))
+    if lse is not None and lse.dtype != _torch().float32:
+        raise TypeError("lse must be float32")
+
+
 def kv_cache_append(cache, k_new, v_new, cu_new_lens, ctx_before, block_tables, stream=None, scales=None) -> None:
     """Scatter new tokens' K/V ([T_new, Hkv, D], packed by sequence) into their pages (an FP8
-    cache: quantised, with their row scales written to `scales`)."""
+    cache: quantised, with their row scales written to `scales`; an INT8 cache: quantised with its pages'
+    scales, which grow where a new row needs it)."""
     lib = load_library()
     if k_new.dtype != v_new.dtype or k_new.shape != v_new.shape:
         raise TypeError("k_new / v_new must match each other")
     c = _cache_struct(cache, k_new.dtype, scales)
     batch, mb = block_tables.shape
-    _check(lib.pkv_kv_cache_append(c, _dev(k_new, "k_new"), _dev(v_new, "v_new"), _i32(cu_new_lens, "cu_new_lens"),
-                                   _i32(ctx_before, "ctx_before"), _i32(block_tables, "block_tables"), batch, mb,
-                                   int(k_new.shape[0]), _stream(stream)), "pkv_kv_cache_append")
+    if c.format == KV_INT8_BLOCK:
+        _int8_args(cache, {"k_new": k_new, "v_new": v_new}, (k_new.shape[0], c.num_kv_heads, c.head_dim), batch, block_tables,
+                   {"cu_new_lens": (cu_new_lens, batch + 1), "ctx_before": (ctx_before, batch)})
+    index = cache.get_device()
+    _check(_on_device(index, lib.pkv_kv_cache_append, c, _dev(k_new, "k_new"), _dev(v_new, "v_new"),
+                      _i32(cu_new_lens, "cu_new_lens"), _i32(ctx_before, "ctx_before"), _i32(block_tables, "block_tables"),
+                      batch, mb, int(k_new.shape[0]), _stream(stream, index)), "pkv_kv_cache_append")
 
 
 def decode_workspace_size(batch, num_q_heads, num_kv_heads, head_dim, block_size, max_blocks_per_seq,
@@ -276,17 +325,22 @@ def paged_attn_decode(cache, q, block_tables, context_lens, scale: Optional[floa
     c = _cache_struct(cache, q.dtype, scales)
     batch, hq, d = q.shape
     mb = block_tables.shape[1]
+    if c.format == KV_INT8_BLOCK:
+        _int8_args(cache, {"q": q}, (block_tables.shape[0], hq, c.head_dim), batch, block_tables,
+                   {"context_lens": (context_lens, batch)})
+        _int8_out(cache, out, lse, q.shape, workspace)
+    index = cache.get_device()
     if out is None:
-        out = torch.empty((batch, hq, d), dtype=out_dtype or q.dtype, device=q.device)
+        out = _new(q, (batch, hq, d), out_dtype or q.dtype, stream)
     need = decode_workspace_size(batch, hq, cache.shape[2], d, cache.shape[3], mb, num_splits)
     if workspace is None and need > 0:
-        workspace = torch.empty(need, dtype=torch.uint8, device=q.device)
+        workspace = _new(q, (need,), torch.uint8, stream)
     ws_bytes = 0 if workspace is None else workspace.numel() * workspace.element_size()
     scale = (1.0 / math.sqrt(d)) if scale is None else float(scale)
-    _check(lib.pkv_paged_attn_decode(c, _dev(q, "q"), hq, _i32(block_tables, "block_tables"),
-                                     _i32(context_lens, "context_lens"), batch, mb, scale, int(num_splits),
-                                     _dev(workspace, "workspace"), ws_bytes, _dev(out, "out"),
-                                     _dtype_code(out.dtype), _dev(lse, "lse"), _stream(stream)),
+    _check(_on_device(index, lib.pkv_paged_attn_decode, c, _dev(q, "q"), hq, _i32(block_tables, "block_tables"),
+                      _i32(context_lens, "context_lens"), batch, mb, scale, int(num_splits),
+                      _dev(workspace, "workspace"), ws_bytes, _dev(out, "out"),
+                      _dtype_code(out.dtype), _dev(lse, "lse"), _stream(stream, index)),
            "pkv_paged_attn_decode")
     return out
 
@@ -305,18 +359,24 @@ def paged_attn_decode_step(cache, q, block_tables, context_lens, k_new, v_new, s
     if tuple(k_new.shape) != (batch, cache.shape[2], d):
         raise ValueError("k_new / v_new must be [batch, num_kv_heads, head_dim]")
     mb = block_tables.shape[1]
+    if c.format == KV_INT8_BLOCK:
+        _int8_args(cache, {"q": q}, (block_tables.shape[0], hq, c.head_dim), batch, block_tables,
+                   {"context_lens": (context_lens, batch)})
+        _int8_args(cache, {"k_new": k_new, "v_new": v_new}, k_new.shape, batch, block_tables, {})
+        _int8_out(cache, out, lse, q.shape, workspace)
+    index = cache.get_device()
     if out is None:
-        out = torch.empty((batch, hq, d), dtype=out_dtype or q.dtype, device=q.device)
+        out = _new(q, (batch, hq, d), out_dtype or q.dtype, stream)
     need = decode_workspace_size(batch, hq, cache.shape[2], d, cache.shape[3], mb, num_splits)
     if workspace is None and need > 0:
-        workspace = torch.empty(need, dtype=torch.uint8, device=q.device)
+        workspace = _new(q, (need,), torch.uint8, stream)
     ws_bytes = 0 if workspace is None else workspace.numel() * workspace.element_size()
     scale = (1.0 / math.sqrt(d)) if scale is None else float(scale)
-    _check(lib.pkv_paged_attn_decode_step(c, _dev(q, "q"), hq, _i32(block_tables, "block_tables"),
-                                          _i32(context_lens, "context_lens"), batch, mb, scale, int(num_splits),
-                                          _dev(workspace, "workspace"), ws_bytes, _dev(out, "out"),
-                                          _dtype_code(out.dtype), _dev(lse, "lse"), _dev(k_new, "k_new"),
-                                          _dev(v_new, "v_new"), _stream(stream)),
+    _check(_on_device(index, lib.pkv_paged_attn_decode_step, c, _dev(q, "q"), hq, _i32(block_tables, "block_tables"),
+                      _i32(context_lens, "context_lens"), batch, mb, scale, int(num_splits),
+                      _dev(workspace, "workspace"), ws_bytes, _dev(out, "out"),
+                      _dtype_code(out.dtype), _dev(lse, "lse"), _dev(k_new, "k_new"),
+                      _dev(v_new, "v_new"), _stream(stream, index)),
            "pkv_paged_attn_decode_step")
     return out
 
@@ -333,13 +393,18 @@ def paged_attn_decode_noalloc(cache, q, block_tables, context_lens, scale: Optio
     c = _cache_struct(cache, q.dtype, scales)
     batch, hq, d = q.shape
     mb = block_tables.shape[1]
+    if c.format == KV_INT8_BLOCK:
+        _int8_args(cache, {"q": q}, (block_tables.shape[0], hq, c.head_dim), batch, block_tables,
+                   {"context_lens": (context_lens, batch)})
+        _int8_out(cache, out, lse, q.shape)
+    index = cache.get_device()
     if out is None:
-        out = torch.empty((batch, hq, d), dtype=out_dtype or q.dtype, device=q.device)
+        out = _new(q, (batch, hq, d), out_dtype or q.dtype, stream)
     scale = (1.0 / math.sqrt(d)) if scale is None else float(scale)
-    _check(lib.pkv_paged_attn_decode_noalloc(c, _dev(q, "q"), hq, _i32(block_tables, "block_tables"),
-                                             _i32(context_lens, "context_lens"), batch, mb, scale, int(num_splits),
-                                             _dev(out, "out"), _dtype_code(out.dtype), _dev(lse, "lse"),
-                                             _stream(stream)), "pkv_paged_attn_decode_noalloc")
+    _check(_on_device(index, lib.pkv_paged_attn_decode_noalloc, c, _dev(q, "q"), hq, _i32(block_tables, "block_tables"),
+                      _i32(context_lens, "context_lens"), batch, mb, scale, int(num_splits),
+                      _dev(out, "out"), _dtype_code(out.dtype), _dev(lse, "lse"),
+                      _stream(stream, index)), "pkv_paged_attn_decode_noalloc")
     return out
 
 
@@ -354,13 +419,18 @@ def paged_attn_prefill(cache, q, cu_q_lens, context_lens, block_tables, max_q_le
     c = _cache_struct(cache, q.dtype, scales)
     total_q, hq, d = q.shape
     batch, mb = block_tables.shape
+    if c.format == KV_INT8_BLOCK:
+        _int8_args(cache, {"q": q}, (total_q, hq, c.head_dim), batch, block_tables,
+                   {"cu_q_lens": (cu_q_lens, batch + 1), "context_lens": (context_lens, batch)})
+        _int8_out(cache, out, lse, q.shape)
+    index = cache.get_device()
     if out is None:
-        out = torch.empty((total_q, hq, d), dtype=out_dtype or q.dtype, device=q.device)
+        out = _new(q, (total_q, hq, d), out_dtype or q.dtype, stream)
     scale = (1.0 / math.sqrt(d)) if scale is None else float(scale)
-    _check(lib.pkv_paged_attn_prefill(c, _dev(q, "q"), hq, _i32(cu_q_lens, "cu_q_lens"),
-                                      _i32(context_lens, "context_lens"), _i32(block_tables, "block_tables"), batch,
-                                      mb, total_q, int(max_q_len), scale, 1 if causal else 0, _dev(out, "out"),
-                                      _dtype_code(out.dtype), _dev(lse, "lse"), _stream(stream)),
+    _check(_on_device(index, lib.pkv_paged_attn_prefill, c, _dev(q, "q"), hq, _i32(cu_q_lens, "cu_q_lens"),
+                      _i32(context_lens, "context_lens"), _i32(block_tables, "block_tables"), batch,
+                      mb, total_q, int(max_q_len), scale, 1 if causal else 0, _dev(out, "out"),
+                      _dtype_code(out.dtype), _dev(lse, "lse"), _stream(stream, index)),
            "pkv_paged_attn_prefill")
     return out
 
@@ -375,17 +445,22 @@ def paged_attn_mixed(cache, q, cu_q_lens, context_lens, block_tables, max_q_len:
     c = _cache_struct(cache, q.dtype, scales)
     total_q, hq, d = q.shape
     batch, mb = block_tables.shape
+    if c.format == KV_INT8_BLOCK:
+        _int8_args(cache, {"q": q}, (total_q, hq, c.head_dim), batch, block_tables,
+                   {"cu_q_lens": (cu_q_lens, batch + 1), "context_lens": (context_lens, batch)})
+        _int8_out(cache, out, lse, q.shape, workspace)
+    index = cache.get_device()
     if out is None:
-        out = torch.empty((total_q, hq, d), dtype=out_dtype or q.dtype, device=q.device)
+        out = _new(q, (total_q, hq, d), out_dtype or q.dtype, stream)
     need = decode_workspace_size(batch, hq, cache.shape[2], d, cache.shape[3], mb, num_splits)
     if workspace is None and need > 0:
-        workspace = torch.empty(need, dtype=torch.uint8, device=q.device)
+        workspace = _new(q, (need,), torch.uint8, stream)
     ws_bytes = 0 if workspace is None else workspace.numel() * workspace.element_size()
     scale = (1.0 / math.sqrt(d)) if scale is None else float(scale)
-    _check(lib.pkv_paged_attn_mixed(c, _dev(q, "q"), hq, _i32(cu_q_lens, "cu_q_lens"), _i32(context_lens, "context_lens"),
-                                    _i32(block_tables, "block_tables"), batch, mb, total_q, int(max_q_len), scale,
-                                    1 if causal else 0, int(num_splits), _dev(workspace, "workspace"), ws_bytes,
-                                    _dev(out, "out"), _dtype_code(out.dtype), _dev(lse, "lse"), _stream(stream)),
+    _check(_on_device(index, lib.pkv_paged_attn_mixed, c, _dev(q, "q"), hq, _i32(cu_q_lens, "cu_q_lens"),
+                      _i32(context_lens, "context_lens"), _i32(block_tables, "block_tables"), batch, mb, total_q,
+                      int(max_q_len), scale, 1 if causal else 0, int(num_splits), _dev(workspace, "workspace"), ws_bytes,
+                      _dev(out, "out"), _dtype_code(out.dtype), _dev(lse, "lse"), _stream(stream, index)),
            "pkv_paged_attn_mixed")
     return out
 
@@ -522,6 +597,62 @@ def kv_cache_compact(cache, keep_pos, cu_keep, dst_start, block_tables, stream=N
                       _at(cu_keep, i32, index, "cu_keep"), _at(dst_start, i32, index, "dst_start"),
                       _at(block_tables, i32, index, "block_tables"), batch, mb, keep_pos.shape[0],
                       _stream(stream, index)), "pkv_kv_cache_compact")
+
+
+def kv_cache_copy(cache, src_pages, dst_pages, num_rows=None, src_cache=None, src_scales=None, stream=None,
+                  scales=None) -> None:
+    """Copy page src_pages[i] (of src_cache, or of `cache` itself) to page dst_pages[i] of `cache`, with its scales: whole,
+    or its leading num_rows[i] rows. int32 lists of one length. No page may be a destination twice, or a source and a
+    destination, in one call."""
+    torch = _torch()
+    lib = load_library()
+    index, i32 = cache.get_device(), torch.int32
+    act = torch.float16 if scales is not None else cache.dtype
+    c = _cache_struct(cache, act, scales)
+    if src_cache is None:
+        if src_scales is not None:
+            raise ValueError("src_scales without src_cache")
+        s = c
+    else:
+        if src_cache.get_device() != index or src_cache.dtype is not cache.dtype or src_cache.shape[1:] != cache.shape[1:]:
+            raise ValueError("src_cache must have the device, type, heads, block_size and head_dim of cache")
+        s = _cache_struct(src_cache, act, src_scales)
+    for t in (scales, src_scales):
+        if t is not None and t.get_device() != index:
+            raise ValueError("scales on %s, the cache on another device" % t.device)
+    if src_pages.dim() != 1 or dst_pages.shape != src_pages.shape or (num_rows is not None and num_rows.shape != src_pages.shape):
+        raise ValueError("src_pages, dst_pages and num_rows must be lists of one length")
+    _check(_on_device(index, lib.pkv_kv_cache_copy, c, s, _at(src_pages, i32, index, "src_pages"),
+                      _at(dst_pages, i32, index, "dst_pages"), _at(num_rows, i32, index, "num_rows"), src_pages.shape[0],
+                      _stream(stream, index)), "pkv_kv_cache_copy")
+
+
+def kv_cache_fork(cache, block_tables, context_lens, parents, new_pages, out_tables=None, out_lens=None, stream=None,
+                  scales=None):
+    """Children of sequences: child c shares the full pages of parent parents[c] and gets a copy of its partly filled
+    last page in new_pages[c] (-1: it goes on in the parent's). int32: block_tables [parents, MB], context_lens [parents],
+    parents and new_pages [children]. Returns (block tables [children, MB], context lengths [children])."""
+    torch = _torch()
+    lib = load_library()
+    index, i32 = cache.get_device(), torch.int32
+    c = _cache_struct(cache, torch.float16 if scales is not None else cache.dtype, scales)
+    if scales is not None and scales.get_device() != index:
+        raise ValueError("scales on %s, the cache on another device" % scales.device)
+    n, mb = block_tables.shape
+    m = parents.shape[0]
+    if context_lens.shape != (n,) or parents.shape != (m,) or new_pages.shape != (m,):
+        raise ValueError("context_lens must be [parents], parents and new_pages [children]")
+    if out_tables is None:
+        out_tables = _new(cache, (m, mb), i32, stream)
+    if out_lens is None:
+        out_lens = _new(cache, (m,), i32, stream)
+    if out_tables.shape != (m, mb) or out_lens.shape != (m,):
+        raise ValueError("out_tables must be [children, MB], out_lens [children]")
+    _check(_on_device(index, lib.pkv_kv_cache_fork, c, _at(block_tables, i32, index, "block_tables"),
+                      _at(context_lens, i32, index, "context_lens"), _at(parents, i32, index, "parents"),
+                      _at(new_pages, i32, index, "new_pages"), n, m, mb, _at(out_tables, i32, index, "out_tables"),
+                      _at(out_lens, i32, index, "out_lens"), _stream(stream, index)), "pkv_kv_cache_fork")
+    return out_tables, out_lens
 
 
 def attn_combine(partial_o, partial_lse, out=None, out_dtype=None, lse=None, stream=None):

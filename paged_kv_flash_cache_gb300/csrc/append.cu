@@ -201,6 +201,7 @@ __global__ void __launch_bounds__(kAppendThreads) append_fp8_kernel(AppendArgs a
 }  // namespace
 
 cudaError_t launch_append(const AppendArgs &a, cudaStream_t s) {
+    if (a.int8) return launch_append_int8(a, s);
     if (a.num_new_tokens == 0 || a.batch == 0) return cudaSuccess;
     const int warps_per_cta = kAppendThreads / 32;
     const long long items = (long long)a.num_new_tokens * ((a.num_kv_heads + kHeadsPerItem - 1) / kHeadsPerItem);

@@ -77,11 +77,12 @@ const DeviceInfo kNoDevice = {-1, 1, 1, 48 * 1024};
 pkv_status check_cache(const pkv_cache &c) {
     if (!c.ptr || !aligned16(c.ptr)) return PKV_ERR_INVALID_ARG;
     if (c.num_blocks < 0 || c.num_kv_heads <= 0 || c.block_size <= 0 || c.head_dim <= 0) return PKV_ERR_INVALID_ARG;
-    if (c.format != PKV_KV_NATIVE && c.format != PKV_KV_FP8_E4M3) return PKV_ERR_UNSUPPORTED;
-    if (c.format == PKV_KV_FP8_E4M3 && (!c.scales || !aligned16(c.scales))) return PKV_ERR_INVALID_ARG;
+    if (c.format != PKV_KV_NATIVE && c.format != PKV_KV_FP8_E4M3 && c.format != PKV_KV_INT8_BLOCK)
+        return PKV_ERR_UNSUPPORTED;
+    if (c.format != PKV_KV_NATIVE && (!c.scales || !aligned16(c.scales))) return PKV_ERR_INVALID_ARG;
     if (c.dtype != PKV_F16 && c.dtype != PKV_BF16) return PKV_ERR_UNSUPPORTED;
     if (c.head_dim != 64 && c.head_dim != 128 && c.head_dim != 256) return PKV_ERR_UNSUPPORTED;
-    if (c.format == PKV_KV_FP8_E4M3 && c.head_dim == 256) return PKV_ERR_UNSUPPORTED;
+    if (c.format != PKV_KV_NATIVE && c.head_dim == 256) return PKV_ERR_UNSUPPORTED;
     if (!is_pow2(c.block_size) || c.block_size < 8 || c.block_size > 512) return PKV_ERR_UNSUPPORTED;
     return PKV_OK;
 }
@@ -101,7 +102,8 @@ CacheView view_of(const pkv_cache &c) {
     v.head_dim = c.head_dim;
     v.dtype = (int)c.dtype;
     v.fp8 = c.format == PKV_KV_FP8_E4M3 ? 1 : 0;
-    v.scales = v.fp8 ? c.scales : nullptr;
+    v.int8 = c.format == PKV_KV_INT8_BLOCK ? 1 : 0;
+    v.scales = v.fp8 || v.int8 ? c.scales : nullptr;
     return v;
 }
 
@@ -186,7 +188,8 @@ pkv_status pkv_kv_cache_append(pkv_cache cache, const void *k_new, const void *v
     a.head_dim = cache.head_dim;
     a.dtype = (int)cache.dtype;
     a.fp8 = cache.format == PKV_KV_FP8_E4M3 ? 1 : 0;
-    a.scales = a.fp8 ? cache.scales : nullptr;
+    a.int8 = cache.format == PKV_KV_INT8_BLOCK ? 1 : 0;
+    a.scales = a.fp8 || a.int8 ? cache.scales : nullptr;
     a.k_new = k_new;
     a.v_new = v_new;
     a.cu_new_lens = cu_new_lens;
@@ -244,11 +247,12 @@ pkv_status decode_impl(const pkv_cache &cache, const void *q, int num_q_heads, c
     if (batch < 0 || max_blocks_per_seq <= 0 || num_q_heads <= 0 || num_splits < 0) return PKV_ERR_INVALID_ARG;
     if (num_q_heads % cache.num_kv_heads != 0) return PKV_ERR_INVALID_ARG;
     const int group = num_q_heads / cache.num_kv_heads;
-    const bool fp8 = cache.format == PKV_KV_FP8_E4M3;
+    const bool fp8 = cache.format == PKV_KV_FP8_E4M3, int8 = cache.format == PKV_KV_INT8_BLOCK;
     // an FP8 cache: 1, 2, 4, or any multiple of 8 query heads per KV head (8 per unit; head_dim 64:
     // at most 8); a native cache: any group
     if (fp8 && group != 1 && group != 2 && group != 4 && group % 8 != 0) return PKV_ERR_UNSUPPORTED;
     if (fp8 && group > 8 && cache.head_dim != 128) return PKV_ERR_UNSUPPORTED;
+    if (int8) return PKV_ERR_UNSUPPORTED;
     if (batch == 0) return PKV_OK;
     if (!q || !block_tables || !context_lens || !out) return PKV_ERR_INVALID_ARG;
     if (!aligned16(q) || !aligned16(out) || (lse && !aligned16(lse))) return PKV_ERR_INVALID_ARG;
@@ -315,7 +319,7 @@ pkv_status decode_impl(const pkv_cache &cache, const void *q, int num_q_heads, c
     a.err = s->err_ptr;
     // a decode step's append goes with the kernels that have a merge warp (16-bit cache, CUDA-core
     // and mma.sync paths); the others get the append kernel after the decode
-    const bool fused_append = k_new && !fp8 && path != kTcgen05;
+    const bool fused_append = k_new && !fp8 && !int8 && path != kTcgen05;
     a.k_new = fused_append ? k_new : nullptr;
     a.v_new = fused_append ? v_new : nullptr;
     cudaStream_t cs = static_cast<cudaStream_t>(stream);
@@ -387,7 +391,8 @@ pkv_status decode_impl(const pkv_cache &cache, const void *q, int num_q_heads, c
         ap.head_dim = cache.head_dim;
         ap.dtype = (int)cache.dtype;
         ap.fp8 = fp8 ? 1 : 0;
-        ap.scales = fp8 ? cache.scales : nullptr;
+        ap.int8 = int8 ? 1 : 0;
+        ap.scales = fp8 || int8 ? cache.scales : nullptr;
         ap.k_new = k_new;
         ap.v_new = v_new;
         ap.cu_new_lens = nullptr;  // one token per sequence, at position context_lens[b]
@@ -467,6 +472,7 @@ pkv_status prefill_impl(const pkv_cache &cache, const void *q, int num_q_heads, 
     if (batch < 0 || max_blocks_per_seq <= 0 || num_q_heads <= 0 || total_q < 0 || max_q_len < 0)
         return PKV_ERR_INVALID_ARG;
     if (num_q_heads % cache.num_kv_heads != 0) return PKV_ERR_INVALID_ARG;
+    if (cache.format == PKV_KV_INT8_BLOCK) return PKV_ERR_UNSUPPORTED;
     if (batch == 0 || total_q == 0) return PKV_OK;
     if (!q || !cu_q_lens || !context_lens || !block_tables || !out) return PKV_ERR_INVALID_ARG;
     if (!aligned16(q) || !aligned16(out) || (lse && !aligned16(lse))) return PKV_ERR_INVALID_ARG;
@@ -537,6 +543,7 @@ pkv_status pkv_rope_append(pkv_cache cache, pkv_rope rope, const void *q, long l
                            void *q_out, long long q_out_stride, void *stream) {
     pkv_status st = check_cache(cache);
     if (st != PKV_OK) return st;
+    if (cache.format == PKV_KV_INT8_BLOCK) return PKV_ERR_UNSUPPORTED;  // (a page's rows share a scale: rows do not go in one by one)
     if (batch < 0 || num_new_tokens < 0 || max_blocks_per_seq <= 0 || num_q_heads <= 0) return PKV_ERR_INVALID_ARG;
     // whole 16-byte vectors hold whole pairs in both layouts
     if (rope.rotary_dim < 0 || rope.rotary_dim > cache.head_dim) return PKV_ERR_INVALID_ARG;
@@ -598,6 +605,7 @@ pkv_status pkv_kv_cache_compact(pkv_cache cache, const int *keep_pos, const int 
                                 void *stream) {
     pkv_status st = check_cache(cache);
     if (st != PKV_OK) return st;
+    if (cache.format == PKV_KV_INT8_BLOCK) return PKV_ERR_UNSUPPORTED;  // (rows would change pages, and with them scales)
     if (batch < 0 || num_keep < 0 || max_blocks_per_seq <= 0) return PKV_ERR_INVALID_ARG;
     if (batch == 0 || num_keep == 0) return PKV_OK;
     if (!keep_pos || !cu_keep || !dst_start || !block_tables) return PKV_ERR_INVALID_ARG;
@@ -626,6 +634,104 @@ pkv_status pkv_kv_cache_compact(pkv_cache cache, const int *keep_pos, const int 
     a.log2_col_shares = a.log2_row_vecs = 0;
     a.err = s->err_ptr;
     return launch_compact(a, static_cast<cudaStream_t>(stream)) == cudaSuccess ? PKV_OK : PKV_ERR_CUDA;
+}
+
+}  // extern "C"
+
+namespace pkv {
+namespace {
+
+PagesArgs pages_of(const pkv_cache &dst, const pkv_cache &src, int *err) {
+    PagesArgs a = {};
+    a.src = src.ptr;
+    a.dst = dst.ptr;
+    a.src_blocks = src.num_blocks;
+    a.dst_blocks = dst.num_blocks;
+    a.block_size = dst.block_size;
+    a.log2_block_size = ilog2(dst.block_size);
+    a.slices = 2 * dst.num_kv_heads;
+    a.row_vecs = dst.head_dim * (dst.format == PKV_KV_NATIVE ? 2 : 1) / 16;
+    a.page_vecs = (long long)a.slices * dst.block_size * a.row_vecs;
+    if (dst.format != PKV_KV_NATIVE) {
+        a.scales_per_page = dst.format == PKV_KV_FP8_E4M3 ? a.slices * dst.block_size : a.slices;
+        a.src_scales = src.scales;
+        a.dst_scales = dst.scales;
+    }
+    a.err = err;
+    return a;
+}
+
+// A page's rows (and an FP8 cache's scales of a page) are counted in 32 bits.
+bool page_too_large(const pkv_cache &c) { return (long long)c.num_kv_heads * c.block_size > 0x3fffffffll; }
+
+bool overlap(const void *a, size_t na, const void *b, size_t nb) {
+    const uintptr_t x = reinterpret_cast<uintptr_t>(a), y = reinterpret_cast<uintptr_t>(b);
+    return x < y + nb && y < x + na;
+}
+
+}  // namespace
+}  // namespace pkv
+
+extern "C" {
+
+pkv_status pkv_kv_cache_copy(pkv_cache dst, pkv_cache src, const int *src_pages, const int *dst_pages,
+                             const int *num_rows, int num_pages, void *stream) {
+    pkv_status st = check_cache(dst);
+    if (st != PKV_OK) return st;
+    if ((st = check_cache(src)) != PKV_OK) return st;
+    if (dst.format != src.format || dst.num_kv_heads != src.num_kv_heads || dst.block_size != src.block_size ||
+        dst.head_dim != src.head_dim || dst.dtype != src.dtype)
+        return PKV_ERR_INVALID_ARG;
+    if (num_pages < 0) return PKV_ERR_INVALID_ARG;
+    if (page_too_large(dst)) return PKV_ERR_UNSUPPORTED;
+    if (num_pages == 0) return PKV_OK;
+    if (!src_pages || !dst_pages) return PKV_ERR_INVALID_ARG;
+    DeviceSlot *s = slot();
+    if (!s) return PKV_ERR_CUDA;
+    PagesArgs a = pages_of(dst, src, s->err_ptr);
+    a.src_pages = src_pages;
+    a.dst_pages = dst_pages;
+    a.num_rows = num_rows;
+    a.num_pages = num_pages;
+    const cudaError_t e = launch_copy_pages(a, static_cast<cudaStream_t>(stream));
+    if (e == cudaErrorNotSupported) return PKV_ERR_UNSUPPORTED;
+    return e == cudaSuccess ? PKV_OK : PKV_ERR_CUDA;
+}
+
+pkv_status pkv_kv_cache_fork(pkv_cache cache, const int *block_tables, const int *context_lens, const int *parents,
+                             const int *new_pages, int num_parents, int num_children, int max_blocks_per_seq,
+                             int *out_tables, int *out_lens, void *stream) {
+    pkv_status st = check_cache(cache);
+    if (st != PKV_OK) return st;
+    if (num_parents < 0 || num_children < 0 || max_blocks_per_seq <= 0) return PKV_ERR_INVALID_ARG;
+    if (page_too_large(cache)) return PKV_ERR_UNSUPPORTED;
+    if (num_children == 0) return PKV_OK;
+    if (!block_tables || !context_lens || !parents || !new_pages || !out_tables || !out_lens) return PKV_ERR_INVALID_ARG;
+    const size_t table_in = (size_t)num_parents * max_blocks_per_seq * 4, lens_in = (size_t)num_parents * 4;
+    const size_t table_out = (size_t)num_children * max_blocks_per_seq * 4, lens_out = (size_t)num_children * 4;
+    // a parent's row must not change while its children read it
+    if (overlap(out_tables, table_out, block_tables, table_in) || overlap(out_tables, table_out, context_lens, lens_in) ||
+        overlap(out_lens, lens_out, block_tables, table_in) || overlap(out_lens, lens_out, context_lens, lens_in) ||
+        overlap(out_tables, table_out, out_lens, lens_out) || overlap(out_tables, table_out, parents, lens_out) ||
+        overlap(out_tables, table_out, new_pages, lens_out) || overlap(out_lens, lens_out, parents, lens_out) ||
+        overlap(out_lens, lens_out, new_pages, lens_out))
+        return PKV_ERR_INVALID_ARG;
+    DeviceSlot *s = slot();
+    if (!s) return PKV_ERR_CUDA;
+    PagesArgs a = pages_of(cache, cache, s->err_ptr);
+    ForkArgs f = {};
+    f.block_tables = block_tables;
+    f.context_lens = context_lens;
+    f.parents = parents;
+    f.new_pages = new_pages;
+    f.num_parents = num_parents;
+    f.num_children = num_children;
+    f.max_blocks_per_seq = max_blocks_per_seq;
+    f.out_tables = out_tables;
+    f.out_lens = out_lens;
+    const cudaError_t e = launch_fork(a, f, static_cast<cudaStream_t>(stream));
+    if (e == cudaErrorNotSupported) return PKV_ERR_UNSUPPORTED;
+    return e == cudaSuccess ? PKV_OK : PKV_ERR_CUDA;
 }
 
 }  // extern "C"
@@ -671,6 +777,7 @@ pkv_status pkv_paged_attn_tree(pkv_cache cache, const void *q, int num_q_heads, 
                                size_t workspace_bytes, void *out, pkv_dtype out_dtype, float *lse, void *stream) {
     pkv_status st = check_cache(cache);
     if (st != PKV_OK) return st;
+    if (cache.format == PKV_KV_INT8_BLOCK) return PKV_ERR_UNSUPPORTED;
     if ((st = check_out_dtype(out_dtype, cache.dtype)) != PKV_OK) return st;
     if (batch < 0 || max_blocks_per_seq <= 0 || num_q_heads <= 0 || total_q < 0 || max_q_len < 0 || mask_words < 0)
         return PKV_ERR_INVALID_ARG;

@@ -17,6 +17,7 @@ struct CacheView {
     int num_blocks, num_kv_heads, block_size, log2_block_size, head_dim;
     int dtype;  // 0 fp16, 1 bf16: q / k_new / v_new, and the elements of a native cache
     int fp8;    // 1: ptr holds E4M3 codes and `scales` one FP32 scale per row
+    int int8;   // 1: ptr holds INT8 codes and `scales` one FP32 scale per (page, K or V, KV head)
     const float *scales;
 };
 
@@ -25,6 +26,7 @@ struct AppendArgs {
     int num_blocks, num_kv_heads, block_size, log2_block_size, head_dim;
     int dtype;      // type of k_new / v_new
     int fp8;        // 1: quantise into E4M3 codes + per-row scales
+    int int8;       // 1: quantise into INT8 codes + per-page scales
     float *scales;
     const void *k_new, *v_new;
     // cu_new_lens nullptr: one new token per sequence (a decode step), token t being sequence t's
@@ -100,6 +102,30 @@ struct CompactArgs {
     int log2_col_shares;  // of them with a share of the columns where the rows have to go in order
     int log2_row_vecs;    // 16-byte vectors of a row
     int *err;
+};
+
+struct PagesArgs {
+    const void *src;
+    void *dst;
+    const float *src_scales;
+    float *dst_scales;
+    int src_blocks, dst_blocks, block_size, log2_block_size;
+    int slices;           // (K or V, head) of a page
+    int row_vecs;         // 16-byte vectors of a row
+    long long page_vecs;  // and of a page
+    int scales_per_page;  // 0: a native cache
+    const int *src_pages, *dst_pages, *num_rows;  // kv_cache_copy; num_rows nullptr: whole pages
+    int num_pages;
+    // set by the launchers:
+    int whole, shares;  // pages as one run each; shares of a run
+    int *err;
+};
+
+struct ForkArgs {
+    const int *block_tables, *context_lens, *parents, *new_pages;
+    int num_parents, num_children, max_blocks_per_seq;
+    int *out_tables, *out_lens;
+    int table_ctas, table_parts;  // set by the launcher
 };
 
 // An item that several runs of the tree kernel share (written by the run it begins in; nodes = 0: none).
@@ -220,6 +246,9 @@ constexpr int kDecodeMaxSplits = 2048;  // splits of one context (bounds the spl
 constexpr int kUnitMisc = 8;           // ints of a decode CTA's unit table beyond its per-sequence and per-split parts
 
 cudaError_t launch_append(const AppendArgs &a, cudaStream_t s);
+cudaError_t launch_append_int8(const AppendArgs &a, cudaStream_t s);
+cudaError_t launch_copy_pages(PagesArgs a, cudaStream_t s);
+cudaError_t launch_fork(PagesArgs a, ForkArgs f, cudaStream_t s);
 cudaError_t encode_cache_map(const CacheView &c, int box_rows, CUtensorMap *map);
 // As encode_kv5_map with whole rows of D elements per box row and no swizzle (the CUDA-core
 // decode reads plain rows).
