@@ -252,7 +252,6 @@ pkv_status decode_impl(const pkv_cache &cache, const void *q, int num_q_heads, c
     // at most 8); a native cache: any group
     if (fp8 && group != 1 && group != 2 && group != 4 && group % 8 != 0) return PKV_ERR_UNSUPPORTED;
     if (fp8 && group > 8 && cache.head_dim != 128) return PKV_ERR_UNSUPPORTED;
-    if (int8) return PKV_ERR_UNSUPPORTED;
     if (batch == 0) return PKV_OK;
     if (!q || !block_tables || !context_lens || !out) return PKV_ERR_INVALID_ARG;
     if (!aligned16(q) || !aligned16(out) || (lse && !aligned16(lse))) return PKV_ERR_INVALID_ARG;
@@ -283,13 +282,19 @@ pkv_status decode_impl(const pkv_cache &cache, const void *q, int num_q_heads, c
     a.stages = 0;  // set by the group kernel's launcher
     // The kernel and the query heads of a unit (a KV head's group, or an equal share of it):
     //   FP8 cache: the FP8 kernels, at most 8 per unit;
+    //   INT8 cache: mma.sync units of the group or, above 8 heads, of its largest divisor up to 8;
     //   native cache, 1 or 2 heads per KV head: CUDA cores (decode.cu), the group as one unit;
     //   4 or 8: mma.sync units of the whole group (decode_gqa.cu);
     //   any other group: tcgen05 units (decode_tc.cu) of the group, or, above 128 heads, of its
     //   largest divisor up to 128.
-    enum { kCudaCores, kMmaSync, kTcgen05, kFp8Tensor } path;
+    enum { kCudaCores, kMmaSync, kTcgen05, kFp8Tensor, kInt8Tensor } path;
     int per_unit;
-    if (fp8) {
+    if (int8) {
+        path = kInt8Tensor;
+        per_unit = group;
+        for (int d = 8; per_unit > 8; --d)
+            if (group % d == 0) per_unit = d;
+    } else if (fp8) {
         path = cache.head_dim == 128 ? kFp8Tensor : kCudaCores;
         per_unit = group < 8 ? group : 8;
     } else if (group <= 2 && cache.head_dim <= 128) {
@@ -358,6 +363,7 @@ pkv_status decode_impl(const pkv_cache &cache, const void *q, int num_q_heads, c
         }
         cudaError_t le;
         switch (path) {
+            case kInt8Tensor: le = launch_decode_int8(d, grid, cs); break;
             case kFp8Tensor: le = launch_decode_fp8(d, grid, cs); break;
             case kMmaSync: le = launch_decode_gqa(d, grid, cs); break;
             case kTcgen05: le = launch_decode_tc(d, grid, cs); break;
@@ -370,6 +376,7 @@ pkv_status decode_impl(const pkv_cache &cache, const void *q, int num_q_heads, c
         c.part_lse = d.part_lse;
         c.n_rows = nb * num_q_heads;
         c.num_splits = s_max;
+        c.nan_lse = int8 ? 1 : 0;
         c.head_dim = cache.head_dim;
         c.context_lens = d.context_lens;
         c.rows_per_seq = num_q_heads;
@@ -444,6 +451,7 @@ pkv_status pkv_attn_combine(const float *partial_o, const float *partial_lse, in
     c.part_lse = partial_lse;
     c.n_rows = n_rows;
     c.num_splits = num_splits;
+    c.nan_lse = 0;
     c.head_dim = head_dim;
     c.context_lens = nullptr;
     c.cu_q_lens = nullptr;

@@ -161,6 +161,7 @@ struct TreeArgs {
 struct CombineArgs {
     const float *part_o, *part_lse;
     int n_rows, num_splits, head_dim;
+    int nan_lse;  // 1: a split's lse may be NaN, and then the row's is
     // When context_lens is set, row r = b * rows_per_seq + h uses ceil(len_b / chunk)
     // splits; rows with exactly one split were finished by the decode kernel.
     const int *context_lens;
@@ -254,6 +255,9 @@ cudaError_t encode_cache_map(const CacheView &c, int box_rows, CUtensorMap *map)
 // decode reads plain rows).
 cudaError_t encode_kv5_rows_map(const CacheView &c, int box_rows, CUtensorMap *map);
 cudaError_t encode_kv5_map(const CacheView &c, int box_rows, CUtensorMap *map);
+// An INT8 cache's codes as encode_kv5_map with whole rows a box (128-byte swizzle for rows of 128 bytes, 64-byte for
+// rows of 64) and box_kv (1 or 2) of K and V.
+cudaError_t encode_int8_map(const CacheView &c, int box_rows, int box_kv, CUtensorMap *map);
 cudaError_t encode_fp8_maps(const CacheView &c, int box_rows, CUtensorMap *codes, CUtensorMap *scales);
 // 2-D tensor map over `rows` rows of `cols` 16-bit elements (bf16 if bf16 != 0, else f16), rows
 // contiguous; boxes of box_cols x box_rows, 128-byte swizzle (box_cols * 2 = 128).
@@ -262,6 +266,7 @@ cudaError_t encode_rows_map(const void *ptr, int bf16, long long rows, int cols,
 cudaError_t launch_decode_gqa(const DecodeArgs &a, int grid, cudaStream_t s);
 // Tensor-core (tcgen05) decode for a unit of up to 128 query heads of one KV head.
 cudaError_t launch_decode_tc(const DecodeArgs &a, int grid, cudaStream_t s);
+cudaError_t launch_decode_int8(const DecodeArgs &a, int grid, cudaStream_t s);
 cudaError_t launch_decode_fp8(const DecodeArgs &a, int grid, cudaStream_t s);
 cudaError_t launch_decode(const DecodeArgs &a, int grid, cudaStream_t s);
 cudaError_t launch_combine(const CombineArgs &a, cudaStream_t s);
