@@ -12,16 +12,21 @@
 // FP32 scores. The V scales enter the weights, which go into the product relative to their tile's largest, as an f16
 // part and its remainder: the output's rounding is the only 16-bit one on the path, however small weights and scales are.
 //
-// Structure (persistent, two CTAs an SM, 6 warps each). A unit is (sequence, KV head's query group, split). Warp 4
-// streams the unit's tiles of 32 tokens into a ring: page slices of min(bs, 32) rows, each one 5-D TMA box of its K
-// rows and its V rows; a slice lies in one page, so its scales are two floats beside it. Tile j is warp j % 4's alone:
-// it waits for no other warp, and its two blocks of 16 tokens are two independent chains of ldmatrix, conversion
-// and mma. Warp 5 merges the four warps' rows and writes the output or the split's partial.
+// Structure (persistent, two CTAs an SM). A unit is (sequence, KV head's query group, split); tile j (32 tokens) of a unit
+// is warp j % W's. Every warp feeds itself: it has a ring of its own and sends for the tile that goes into a slot as
+// soon as it has read the slot's last one, so no warp waits for another one and there is no producer to fall behind
+// (with one, 0.131 ms on the 7B-like batch, 0.111 with three quarters of the arithmetic left out). A tile arrives in page
+// slices of min(bs, 32) rows, each one 5-D TMA box of its K rows and its V rows; a slice lies in one page, whose scales
+// come beside it by 4-byte asynchronous copies on the same mbarrier. The page ids of the tile after are loaded a tile
+// ahead. The two blocks of 16 tokens of a tile are two independent chains of ldmatrix, conversion and mma. The last
+// warp merges the others' rows and writes the output or the split's partial.
 //
 // Operand layouts. ldmatrix (.b16) hands lane (gid, tig) the codes of dims 4 tig .. 4 tig + 3 of a 16-dim chunk: the
 // k slots of the A fragment are the permutation {2tig, 2tig+1, 2tig+8, 2tig+9} -> {4tig .. 4tig+3}, and q's B fragment
 // is built alike. For P.V, ldmatrix.trans hands a lane (token 2tig: dims 2gid, 2gid+1; token 2tig+1: the same): the
 // permute that widens the codes also pairs them by dim, M slot gid holding dim 2gid and slot gid + 8 dim 2gid + 1.
+// Up to four heads take head slots 0-3 and, once more, 4-7: the first four carry the weights' f16 parts into the
+// product with V and the others the remainders, in one mma; with more heads the remainders are a second mma.
 #include <cuda.h>
 
 #include "decode_common.cuh"
@@ -34,25 +39,23 @@ namespace pkv {
 namespace {
 
 constexpr int kWarps = 4;  // consumer warps
-constexpr int kProducerWarp = kWarps;
-constexpr int kMergeWarp = kWarps + 1;
-constexpr int kThreads = (kWarps + 2) * 32;
-constexpr int kTile = 32;  // tokens a stage
-constexpr int kCtasPerSm = 2;
-constexpr float kRescale = 8.0f;  // lazy rescale threshold (log2 units)
+constexpr int kMergeWarp = kWarps;
+constexpr int kThreads = (kWarps + 1) * 32;
+constexpr int kTile = 32;  // tokens of a tile
+constexpr int kCtasPerSm = 3;
+constexpr float kRescale = 4.0f;  // lazy rescale threshold (log2 units)
+constexpr float kWeight = 2048.0f;  // weights, at most 2^kRescale, go into the product times this: below f16's 65504
 
 template <int D, int G>
 struct Int8Layout {
-    // ring slots: what two CTAs an SM leave room for beside their merge buffers and unit tables
-    static constexpr int kStages = D == 64 ? (G > 4 ? 20 : 22) : (G > 4 ? 10 : 11);
-    static constexpr int kMergeBufs = G > 2 ? 1 : 2;
+    // slots of a warp's ring: what two CTAs an SM leave room for beside their merge buffers and unit tables
+    static constexpr int kStages = D == 64 ? 4 : 2;
+    static constexpr int kMergeBufs = 1;
     static constexpr uint32_t kStageBytes = 2 * kTile * D;  // per slice: br K rows, br V rows of D bytes
-    static constexpr uint32_t kQBytes = G * D * 2;
-    static constexpr uint32_t kQOffset = kStages * kStageBytes;                          // [2]
-    static constexpr uint32_t kScaleOffset = kQOffset + 2 * kQBytes;                     // [kStages][4] (K, V) of a slice
-    static constexpr uint32_t kBarOffset = kScaleOffset + kStages * 32;
-    // full / empty per stage, q full / empty [2], merge full / empty, then the abort flag and the merge buffers' units
-    static constexpr uint32_t kMergeOffset = (kBarOffset + (2 * kStages + 4 + 2 * kMergeBufs) * 8 + 32 + 15) / 16 * 16;
+    static constexpr uint32_t kScaleOffset = kWarps * kStages * kStageBytes;             // [kWarps][kStages][4] (K, V)
+    static constexpr uint32_t kBarOffset = kScaleOffset + kWarps * kStages * 32;
+    // full per slot, merge full / empty, then the abort flag and the merge buffers' units
+    static constexpr uint32_t kMergeOffset = (kBarOffset + (kWarps * kStages + 2 * kMergeBufs) * 8 + 32 + 15) / 16 * 16;
     static constexpr uint32_t kMergeFloats = kWarps * G * kMergeRow<D>;
     static constexpr uint32_t kIntsOffset = kMergeOffset + kMergeBufs * kMergeFloats * 4;
     static size_t smem_bytes(int batch, int s_max) {
@@ -76,40 +79,47 @@ __device__ __forceinline__ uint32_t codes_f16(uint32_t x) {
     return r;
 }
 
+__device__ __forceinline__ float rcpf(float x) {
+    float y;
+    asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+    return y;
+}
+
+// Four bytes global -> shared, asynchronously; and an arrival on `bar` once this thread's copies so far have landed
+// (one of the arrivals that the barrier expects).
+__device__ __forceinline__ void cp_async4(void *dst, const void *src) {
+    asm volatile("cp.async.ca.shared.global [%0], [%1], 4;" ::"r"(smem_addr(dst)), "l"(src) : "memory");
+}
+__device__ __forceinline__ void cp_async_arrive(uint64_t *bar) {
+    asm volatile("cp.async.mbarrier.arrive.noinc.shared.b64 [%0];" ::"r"(smem_addr(bar)) : "memory");
+}
+
 template <int D, int G>
 __global__ void __launch_bounds__(kThreads, kCtasPerSm)
     decode_int8_kernel(const __grid_constant__ CUtensorMap tm, DecodeArgs a) {
     using L = Int8Layout<D, G>;
     constexpr int S = L::kStages, NB = L::kMergeBufs;
-    constexpr int kChunks = D / 16;  // 16-dim chunks: k-steps of q.K^T, m-tiles of O^T
+    constexpr int kChunks = D / 16;    // 16-dim chunks: k-steps of q.K^T, m-tiles of O^T
+    constexpr bool kPacked = G <= 4;   // weights and their remainders side by side in one mma
+    constexpr int kLanesFull = 4;      // lanes that copy scales: slices of a tile at most
     extern __shared__ uint8_t smem_raw[];
     uint8_t *smem = smem_raw + ((1024u - (smem_addr(smem_raw) & 1023u)) & 1023u);
-    uint64_t *full = reinterpret_cast<uint64_t *>(smem + L::kBarOffset);
-    uint64_t *empty = full + S;
-    uint64_t *qfull = empty + S;     // [2]
-    uint64_t *qempty = qfull + 2;    // [2]
-    uint64_t *mfull = qempty + 2;    // [NB] the warps' rows of a unit are in buffer i
-    uint64_t *mempty = mfull + NB;   // [NB] the merge warp has read buffer i
+    uint64_t *full = reinterpret_cast<uint64_t *>(smem + L::kBarOffset);  // [kWarps][S]
+    uint64_t *mfull = full + kWarps * S;  // [NB] the warps' rows of a unit are in buffer i
+    uint64_t *mempty = mfull + NB;        // [NB] the merge warp has read buffer i
     volatile int *abort_flag = reinterpret_cast<volatile int *>(mempty + NB);
     int *merge_unit = reinterpret_cast<int *>(mempty + NB) + 4;  // [NB] unit of each merge buffer, -1: end
-    float *scales = reinterpret_cast<float *>(smem + L::kScaleOffset);  // [S][4][2]
     float *merge = reinterpret_cast<float *>(smem + L::kMergeOffset);
     const UnitTable ut = unit_table(reinterpret_cast<int *>(smem + L::kIntsOffset), a.batch, a.s_max);
 
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
     const int hkv = a.cache.num_kv_heads, bs = a.cache.block_size;
     const int hu = hkv * a.head_groups;  // unit heads
-    const int br = bs < kTile ? bs : kTile;  // rows of a slice: splits and tiles start at multiples of 32 tokens
+    // rows of a slice (a power of two): splits and tiles start at multiples of 32 tokens
+    const int log2_br = min(a.cache.log2_block_size, 5), br = 1 << log2_br;
 
     if (tid == 0) {
-        for (int i = 0; i < S; ++i) {
-            mbar_init(&full[i], 2);  // the copies' bytes; the scales
-            mbar_init(&empty[i], 1);
-        }
-        for (int i = 0; i < 2; ++i) {
-            mbar_init(&qfull[i], 1);
-            mbar_init(&qempty[i], kWarps);
-        }
+        for (int i = 0; i < kWarps * S; ++i) mbar_init(&full[i], 1 + kLanesFull);  // the boxes' bytes; the scales
         for (int i = 0; i < NB; ++i) {
             mbar_init(&mfull[i], kWarps);
             mbar_init(&mempty[i], 1);
@@ -121,104 +131,6 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm)
     const int num_units = decode_scan_units<kThreads>(a, ut);
     const int chunk = ut.misc[0];  // the launch's split size
 
-    if (warp == kProducerWarp) {
-        // ===================================== producer warp =====================================
-        const uint64_t pol = l2_policy_evict_first();
-        const uint16_t *qg = static_cast<const uint16_t *>(a.q);
-        if (lane == 0) tc::prefetch_tensormap(&tm);
-        uint32_t it = 0;  // tiles issued
-        uint32_t qn = 0;  // units issued
-        bool ok = true;
-        UnitCursor c = {};
-        PageWindow win = {};
-        float k0 = 0.f, v0 = 0.f, k1 = 0.f, v1 = 0.f;  // scales of the window's pages (lane j: pages j and 32 + j)
-        auto load_scales = [&](const PageWindow &w, int head) {
-            const size_t at0 = (size_t)(unsigned)w.p0 * 2 * hkv + head, at1 = (size_t)(unsigned)w.p1 * 2 * hkv + head;
-            if (lane < w.count && (unsigned)w.p0 < (unsigned)a.cache.num_blocks) {
-                k0 = __ldg(a.cache.scales + at0);
-                v0 = __ldg(a.cache.scales + at0 + hkv);
-            } else if (lane < w.count) {  // (flagged and read from page 0)
-                k0 = __ldg(a.cache.scales + head);
-                v0 = __ldg(a.cache.scales + head + hkv);
-            }
-            if (lane + 32 < w.count && (unsigned)w.p1 < (unsigned)a.cache.num_blocks) {
-                k1 = __ldg(a.cache.scales + at1);
-                v1 = __ldg(a.cache.scales + at1 + hkv);
-            } else if (lane + 32 < w.count) {
-                k1 = __ldg(a.cache.scales + head);
-                v1 = __ldg(a.cache.scales + head + hkv);
-            }
-        };
-        if ((int)blockIdx.x < num_units) {
-            c = unit_of(blockIdx.x, ut, a.s_max, hu, chunk);
-            win = unit_pages(a, c, lane);
-            load_scales(win, c.kvh / a.head_groups);
-        }
-        for (int u = blockIdx.x; ok && u < num_units; u += gridDim.x) {
-            // the next unit's cursor and page ids, loading while this unit's copies go out
-            UnitCursor cn = c;
-            PageWindow wn = win;
-            if (u + (int)gridDim.x < num_units) {
-                cn = unit_of(u + gridDim.x, ut, a.s_max, hu, chunk);
-                wn = unit_pages(a, cn, lane);
-            }
-            const int kvr = c.kvh / a.head_groups;  // the KV head of this unit
-            const int *bt = a.block_tables + (size_t)c.b * a.max_blocks_per_seq;
-            const int unit_last_page = (c.t1 - 1) >> a.cache.log2_block_size;
-            // q into its slot
-            if (!(ok = mbar_wait(&qempty[qn & 1], ((qn >> 1) & 1u) ^ 1u, abort_flag, a.err))) break;
-            if (lane == 0) {
-                mbar_arrive_expect_tx(&qfull[qn & 1], L::kQBytes);
-                bulk_g2s(smem + L::kQOffset + (qn & 1) * L::kQBytes,
-                         qg + ((size_t)ut.qrow[c.b] * a.num_q_heads + (size_t)c.kvh * G) * D, L::kQBytes,
-                         &qfull[qn & 1], pol);
-            }
-            ++qn;
-            for (int ts = c.t0; ts < c.t1; ts += kTile, ++it) {
-                const int n = min(kTile, c.t1 - ts);
-                const int nslices = (n + br - 1) / br;  // <= 4
-                const int page0 = ts >> a.cache.log2_block_size;
-                const int page_last = (ts + n - 1) >> a.cache.log2_block_size;
-                if (page_last >= win.first + win.count) {  // units of more than 64 pages
-                    win = load_pages(bt, page0, unit_last_page - page0 + 1, lane);
-                    load_scales(win, kvr);
-                }
-                const int tok0 = ts + lane * br;  // this lane's slice
-                const int off = tok0 & (bs - 1);
-                const int lp = tok0 >> a.cache.log2_block_size;
-                int pb = window_page(win, lp);
-                const PageWindow wk = {win.first, win.count, __float_as_int(k0), __float_as_int(k1)};
-                const PageWindow wv = {win.first, win.count, __float_as_int(v0), __float_as_int(v1)};
-                const int stage = it % S;
-                if (lane < nslices && (pb < 0 || pb >= a.cache.num_blocks)) {
-                    set_error(a.err, kErrDeviceRange);
-                    pb = 0;
-                }
-                if (!(ok = mbar_wait(&empty[stage], ((it / S) & 1u) ^ 1u, abort_flag, a.err))) break;
-                if (lane == 0) mbar_arrive_expect_tx(&full[stage], (uint32_t)nslices * br * 2u * D);
-                __syncwarp();
-                if (lane < nslices)  // one box: the slice's K rows, then its V rows
-                    tc::tma_load_5d_hint(smem + (size_t)stage * L::kStageBytes + (size_t)lane * 2 * br * D, &tm, 0, off, kvr, 0,
-                                         pb, &full[stage], pol);
-                const float sk = __int_as_float(window_page(wk, lp)), sv = __int_as_float(window_page(wv, lp));
-                if (lane < nslices) *reinterpret_cast<float2 *>(scales + stage * 8 + lane * 2) = make_float2(sk, sv);
-                __syncwarp();
-                if (lane == 0) mbar_arrive(&full[stage]);
-            }
-            if (ok && u + (int)gridDim.x < num_units) load_scales(wn, cn.kvh / a.head_groups);
-            c = cn;
-            win = wn;
-        }
-        if (!ok) {
-            // let copies in flight land before the CTA exits (bounded)
-            volatile int no_abort = 0;
-            for (uint32_t i = it > (uint32_t)S ? it - S : 0u; i < it; ++i)
-                mbar_wait(&full[i % S], (i / S) & 1u, &no_abort, nullptr);
-            for (uint32_t i = qn > 2u ? qn - 2 : 0u; i < qn; ++i) mbar_wait(&qfull[i & 1], (i >> 1) & 1u, &no_abort, nullptr);
-        }
-        return;
-    }
-
     if (warp == kMergeWarp) {
         // ====================================== merge warp ======================================
         merge_warp_loop<D, G, kWarps, NB, true>(a, ut, merge, L::kMergeFloats, mfull, mempty, merge_unit, abort_flag, lane);
@@ -227,15 +139,72 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm)
     }
 
     // ===================================== consumer warps =====================================
+    uint8_t *ring = smem + (size_t)warp * S * L::kStageBytes;
+    float *scales = reinterpret_cast<float *>(smem + L::kScaleOffset) + warp * S * 8;  // [S][4][2]
+    full += warp * S;
+    // ---- what is sent for: the next tile, its unit and the page ids of its slices (lane j: slice j) ----
+    const uint64_t pol = l2_policy_evict_first();
+    int iu = blockIdx.x, its = 0, ipb = 0, ikv = 0;
+    uint32_t issued = 0;
+    UnitCursor ic = {};
+    auto seek = [&]() {  // from unit iu on, the first one with a tile of this warp; its page ids
+        for (; iu < num_units; iu += gridDim.x) {
+            ic = unit_of(iu, ut, a.s_max, hu, chunk);
+            its = ic.t0 + warp * kTile;
+            ikv = a.head_groups == 1 ? ic.kvh : ic.kvh / a.head_groups;  // the KV head of the unit
+            if (its < ic.t1) break;
+        }
+    };
+    auto page_ids = [&]() {
+        const int tok = its + lane * br;
+        ipb = 0;
+        if (iu < num_units && lane < kLanesFull && tok < ic.t1 && lane * br < kTile)
+            ipb = __ldg(a.block_tables + (size_t)ic.b * a.max_blocks_per_seq + (tok >> a.cache.log2_block_size));
+    };
+    auto send = [&](int slot) {
+        if (iu >= num_units) return;
+        const int n = min(kTile, ic.t1 - its);
+        const int nslices = (n + br - 1) >> log2_br;  // <= 4
+        if (lane == 0) mbar_arrive_expect_tx(&full[slot], (uint32_t)nslices * br * 2u * D);
+        __syncwarp();
+        if (lane < nslices) {
+            int pb = ipb;
+            if (pb < 0 || pb >= a.cache.num_blocks) {
+                set_error(a.err, kErrDeviceRange);
+                pb = 0;
+            }
+            tc::tma_load_5d_hint(ring + (size_t)slot * L::kStageBytes + (size_t)lane * 2 * br * D, &tm, 0,
+                                 (its + lane * br) & (bs - 1), ikv, 0, pb, &full[slot], pol);
+            const float *sc = a.cache.scales + (size_t)pb * 2 * hkv + ikv;
+            cp_async4(scales + slot * 8 + lane * 2, sc);
+            cp_async4(scales + slot * 8 + lane * 2 + 1, sc + hkv);
+        }
+        if (lane < kLanesFull) cp_async_arrive(&full[slot]);
+        ++issued;
+        its += kWarps * kTile;
+        if (its >= ic.t1) {
+            iu += gridDim.x;
+            seek();
+        }
+        page_ids();
+    };
+    seek();
+    page_ids();
+    if (lane == 0) tc::prefetch_tensormap(&tm);
+    for (int i = 0; i < S; ++i) send(i);
+
     const int gid = lane >> 2, tig = lane & 3;
     const int mi = lane >> 3;
     const float sl = a.scale * kLog2e;
     const bool bf16 = a.cache.dtype == 1;
+    const uint16_t *qg = static_cast<const uint16_t *>(a.q);
     uint32_t bq[kChunks][2];  // q as f16 B fragments, k slots permuted as the K codes
-    uint32_t base = 0;        // tiles of the units before this one
-    uint32_t qn = 0;
+    uint32_t taken = 0;       // tiles read
+    int slot = 0;
+    uint32_t phase = 0;
     int mbuf = 0;  // merge buffer of the next unit
     uint32_t mphase = 0;
+    bool ok = true;
     // rows of the warp's ldmatrix in the slice layout (slice j starts at row 2 j br): 16 tokens a block
     int trow[2];
 #pragma unroll
@@ -245,49 +214,45 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm)
     }
     for (int u = blockIdx.x; u < num_units; u += gridDim.x) {
         const UnitCursor c = unit_of(u, ut, a.s_max, hu, chunk);
-        const int ntiles = (c.t1 - c.t0 + kTile - 1) / kTile;
         float m[2] = {-INFINITY, -INFINITY}, l[2] = {0.f, 0.f};
-        float o[kChunks][4];
+        float2 o[kChunks][2];
 #pragma unroll
-        for (int mt = 0; mt < kChunks; ++mt) o[mt][0] = o[mt][1] = o[mt][2] = o[mt][3] = 0.f;
-        if (!mbar_wait(&qfull[qn & 1], (qn >> 1) & 1u, abort_flag, a.err)) return;
-        {
-            const uint16_t *sq = reinterpret_cast<const uint16_t *>(smem + L::kQOffset + (qn & 1) * L::kQBytes);
+        for (int mt = 0; mt < kChunks; ++mt) o[mt][0] = o[mt][1] = make_float2(0.f, 0.f);
+        const int first = c.t0 + warp * kTile;
+        if (first < c.t1) {
+            const int hq = kPacked ? gid & 3 : gid;  // head of this lane's column of the B fragment
+            const uint16_t *qr = qg + ((size_t)ut.qrow[c.b] * a.num_q_heads + (size_t)c.kvh * G + hq) * D + 4 * tig;
 #pragma unroll
             for (int kk = 0; kk < kChunks; ++kk) {
                 uint2 raw = make_uint2(0u, 0u);
-                if (gid < G) raw = *reinterpret_cast<const uint2 *>(sq + gid * D + kk * 16 + 4 * tig);
-                if (bf16) {
-                    raw = make_uint2(pack_pair<false>(__uint_as_float(raw.x << 16), __uint_as_float(raw.x & 0xffff0000u)),
-                                     pack_pair<false>(__uint_as_float(raw.y << 16), __uint_as_float(raw.y & 0xffff0000u)));
-                }
+                if (hq < G) raw = __ldg(reinterpret_cast<const uint2 *>(qr + kk * 16));
                 bq[kk][0] = raw.x;
                 bq[kk][1] = raw.y;
             }
-            __syncwarp();
-            if (lane == 0) mbar_arrive(&qempty[qn & 1]);
-            ++qn;
+            if (bf16) {
+#pragma unroll
+                for (int kk = 0; kk < kChunks; ++kk)
+#pragma unroll
+                    for (int i = 0; i < 2; ++i)
+                        bq[kk][i] = pack_pair<false>(__uint_as_float(bq[kk][i] << 16), __uint_as_float(bq[kk][i] & 0xffff0000u));
+            }
         }
-        for (int j = warp; j < ntiles; j += kWarps) {
-            const uint32_t it = base + j;
-            const int stage = it % S;
-            const int n = min(kTile, c.t1 - c.t0 - j * kTile);
-            if (!mbar_wait(&full[stage], (it / S) & 1u, abort_flag, a.err)) return;
-            const uint32_t aK = smem_addr(smem + (size_t)stage * L::kStageBytes), aV = aK + br * D;
+        for (int ts = first; ts < c.t1; ts += kWarps * kTile) {
+            const int n = min(kTile, c.t1 - ts);
+            if (!(ok = mbar_wait(&full[slot], phase, abort_flag, a.err))) break;
+            const uint32_t aK = smem_addr(ring + (size_t)slot * L::kStageBytes), aV = aK + br * D;
             // scales of the four groups of 8 tokens (a group lies in one page)
             float sk[4], sv[4];
 #pragma unroll
             for (int g = 0; g < 4; ++g) {
-                const float2 x = *reinterpret_cast<const float2 *>(scales + stage * 8 + (g * 8 / br) * 2);
+                const float2 x = *reinterpret_cast<const float2 *>(scales + slot * 8 + ((g * 8) >> log2_br) * 2);
                 sk[g] = x.x * sl;
                 sv[g] = x.y;
             }
             // ---- S^T = K q^T: two blocks of 16 tokens x 8 head slots ----
             float s[2][4];
 #pragma unroll
-            for (int bl = 0; bl < 2; ++bl) {
-                s[bl][0] = s[bl][1] = s[bl][2] = s[bl][3] = 0.f;
-            }
+            for (int bl = 0; bl < 2; ++bl) s[bl][0] = s[bl][1] = s[bl][2] = s[bl][3] = 0.f;
 #pragma unroll
             for (int cp = 0; cp < kChunks; cp += 2) {
                 uint32_t r[2][4];
@@ -304,67 +269,65 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm)
                     }
             }
             // token of s[bl][i]: bl * 16 + gid + 8 * (i >> 1); head slot 2 tig + (i & 1)
-            bool seen[4];
-#pragma unroll
-            for (int g = 0; g < 4; ++g) seen[g] = g * 8 + gid < n;
-            float mx[2] = {-INFINITY, -INFINITY};
 #pragma unroll
             for (int bl = 0; bl < 2; ++bl)
 #pragma unroll
-                for (int i = 0; i < 4; ++i) {
-                    const int g = bl * 2 + (i >> 1);
-                    s[bl][i] = seen[g] ? s[bl][i] * sk[g] : -INFINITY;
-                    mx[i & 1] = fmaxf(mx[i & 1], s[bl][i]);
+                for (int i = 0; i < 4; ++i) s[bl][i] *= sk[bl * 2 + (i >> 1)];
+            if (n < kTile) {  // behind the context's end (and maybe beyond the last slice): no weight, and no scale
+#pragma unroll
+                for (int g = 0; g < 4; ++g) {
+                    if (g * 8 >= n) sv[g] = 0.f;
+                    if (g * 8 + gid >= n) s[g >> 1][(g & 1) * 2] = s[g >> 1][(g & 1) * 2 + 1] = -INFINITY;
+                }
+            }
+            // The running max m of a head is a past maximum: it moves only when a score exceeds it by more than 2^4, so
+            // the lanes need one vote a tile and rarely each other's maxima.
+            float mx[2];
+#pragma unroll
+            for (int i = 0; i < 2; ++i) mx[i] = fmaxf(fmax3(s[0][i], s[0][i + 2], s[1][i]), s[1][i + 2]);
+            if (__any_sync(0xffffffffu, mx[0] > m[0] + kRescale || mx[1] > m[1] + kRescale)) {
+#pragma unroll
+                for (int ofs = 4; ofs < 32; ofs <<= 1) {
+                    mx[0] = fmaxf(mx[0], __shfl_xor_sync(0xffffffffu, mx[0], ofs));
+                    mx[1] = fmaxf(mx[1], __shfl_xor_sync(0xffffffffu, mx[1], ofs));
+                }
+                float al[2];
+#pragma unroll
+                for (int i = 0; i < 2; ++i) {
+                    const float mn = fmaxf(m[i], mx[i]);
+                    al[i] = mn > m[i] ? ex2f(m[i] - mn) : 1.f;  // 0 when m = -inf
+                    m[i] = mn;
+                    l[i] *= al[i];
                 }
 #pragma unroll
-            for (int ofs = 4; ofs < 32; ofs <<= 1) {
-                mx[0] = fmaxf(mx[0], __shfl_xor_sync(0xffffffffu, mx[0], ofs));
-                mx[1] = fmaxf(mx[1], __shfl_xor_sync(0xffffffffu, mx[1], ofs));
+                for (int mt = 0; mt < kChunks; ++mt)
+#pragma unroll
+                    for (int k = 0; k < 2; ++k) o[mt][k] = fmul2(o[mt][k], make_float2(al[0], al[1]));
             }
-            // The tile's weights are relative to its own maximum and its largest V scale: P' = 2^14 p / 2^mx * sv / w, as
-            // an f16 part and its remainder, holds weights down to 2^-38 of the tile's largest. The tile's product
-            // then enters O in FP32 times f = 2^(mx - m) w / 2^14; the running max m of a head moves only when a
-            // tile's exceeds it by more than 2^8.
-            float w = sv[0];
-#pragma unroll
-            for (int g = 1; g < 4; ++g) w = fmaxf(w, g * 8 < n ? sv[g] : 0.f);
-            const float rw = w >= 1.17549435e-38f ? 1.f / w : 0.f;  // (scales below 2^-126 count as 0)
-            float f[2];
-#pragma unroll
-            for (int i = 0; i < 2; ++i) {
-                if (mx[i] > m[i] + kRescale) {
-                    const float al = ex2f(m[i] - mx[i]);  // 0 when m = -inf
-                    l[i] *= al;
-#pragma unroll
-                    for (int mt = 0; mt < kChunks; ++mt) {
-                        o[mt][i] *= al;
-                        o[mt][i + 2] *= al;
-                    }
-                    m[i] = mx[i];
-                }
-                f[i] = ex2f(mx[i] - m[i]);
-            }
-            float lt[2] = {0.f, 0.f};
+            // The tile's weights enter the product relative to its largest V scale w and times 2^11: P' = 2^11 p sv / w (at
+            // most 2^15), as an f16 part and its remainder, holds weights down to 2^-35. The tile's product
+            // enters O in FP32 times w / 2^11.
+            const float w = fmaxf(fmax3(sv[0], sv[1], sv[2]), sv[3]);
+            const float rw = w >= 1.17549435e-38f ? kWeight * rcpf(w) : 0.f;  // (scales below 2^-126 count as 0)
             uint32_t ph[2][2], pe[2][2];
 #pragma unroll
             for (int bl = 0; bl < 2; ++bl)
 #pragma unroll
                 for (int hf = 0; hf < 2; ++hf) {
-                    const int g = bl * 2 + hf;
-                    const float p0 = seen[g] ? ex2f(s[bl][2 * hf] - mx[0]) : 0.f;
-                    const float p1 = seen[g] ? ex2f(s[bl][2 * hf + 1] - mx[1]) : 0.f;
-                    lt[0] += p0;
-                    lt[1] += p1;
-                    const float r = seen[g] ? sv[g] * rw * 16384.f : 0.f;
+                    const float p0 = ex2f(s[bl][2 * hf] - m[0]), p1 = ex2f(s[bl][2 * hf + 1] - m[1]);
+                    l[0] += p0;
+                    l[1] += p1;
+                    const float r = sv[bl * 2 + hf] * rw;
                     uint32_t hi, lo;
                     split_pair<false>(p0 * r, p1 * r, hi, lo);
-                    ph[bl][hf] = movmatrix_t(hi);
-                    pe[bl][hf] = movmatrix_t(lo);
+                    if (kPacked) {
+                        ph[bl][hf] = movmatrix_t(tig < 2 ? hi : lo);
+                    } else {
+                        ph[bl][hf] = movmatrix_t(hi);
+                        pe[bl][hf] = movmatrix_t(lo);
+                    }
                 }
-            l[0] = fmaf(lt[0], f[0], l[0]);
-            l[1] = fmaf(lt[1], f[1], l[1]);
-            f[0] *= w * (1.f / 16384.f);
-            f[1] *= w * (1.f / 16384.f);
+            const float2 f2 = make_float2(w * (1.f / kWeight), w * (1.f / kWeight));
             // ---- O^T += f V^T P'^T: D dims (permuted within each 16-dim chunk) x 8 slots ----
 #pragma unroll
             for (int cp = 0; cp < kChunks; cp += 2) {
@@ -381,25 +344,41 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm)
                         const uint32_t x = r[bl][2 * h] ^ 0x80808080u, y = r[bl][2 * h + 1] ^ 0x80808080u;
                         const uint32_t af[4] = {codes_f16<0x4240>(x), codes_f16<0x4341>(x), codes_f16<0x4240>(y),
                                                 codes_f16<0x4341>(y)};
-                        mma16816<false>(ot[h], af, pe[bl][0], pe[bl][1]);
+                        if (!kPacked) mma16816<false>(ot[h], af, pe[bl][0], pe[bl][1]);
                         mma16816<false>(ot[h], af, ph[bl][0], ph[bl][1]);
                     }
 #pragma unroll
-                for (int h = 0; h < 2; ++h)
-#pragma unroll
-                    for (int i = 0; i < 4; ++i) o[cp + h][i] = fmaf(ot[h][i], f[i & 1], o[cp + h][i]);
+                for (int h = 0; h < 2; ++h) {
+                    o[cp + h][0] = ffma2(make_float2(ot[h][0], ot[h][1]), f2, o[cp + h][0]);
+                    o[cp + h][1] = ffma2(make_float2(ot[h][2], ot[h][3]), f2, o[cp + h][1]);
+                }
             }
+            // the slot's next tile
             __syncwarp();
-            if (lane == 0) mbar_arrive(&empty[stage]);
+            ++taken;
+            send(slot);
+            if (++slot == S) {
+                slot = 0;
+                phase ^= 1u;
+            }
         }
-        base += ntiles;
+        if (!ok) break;
         // ---- l summed over the lanes of each head slot; rows to the merge warp ----
 #pragma unroll
         for (int ofs = 4; ofs < 32; ofs <<= 1) {
             l[0] += __shfl_xor_sync(0xffffffffu, l[0], ofs);
             l[1] += __shfl_xor_sync(0xffffffffu, l[1], ofs);
         }
-        if (!mbar_wait(&mempty[mbuf], mphase ^ 1u, abort_flag, a.err)) return;
+        if (kPacked) {  // the remainders' sums (slots 4-7: lanes 2 further on) to the heads'
+#pragma unroll
+            for (int mt = 0; mt < kChunks; ++mt)
+#pragma unroll
+                for (int k = 0; k < 2; ++k) {
+                    o[mt][k].x += __shfl_xor_sync(0xffffffffu, o[mt][k].x, 2);
+                    o[mt][k].y += __shfl_xor_sync(0xffffffffu, o[mt][k].y, 2);
+                }
+        }
+        if (!(ok = mbar_wait(&mempty[mbuf], mphase ^ 1u, abort_flag, a.err))) break;
         float *rows = merge + (size_t)mbuf * L::kMergeFloats;
 #pragma unroll
         for (int jj = 0; jj < 2; ++jj) {
@@ -408,7 +387,8 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm)
                 float *row = rows + ((size_t)warp * G + g) * kMergeRow<D>;
 #pragma unroll
                 for (int mt = 0; mt < kChunks; ++mt)  // M slot gid: dim 2gid of the chunk; gid + 8: dim 2gid + 1
-                    *reinterpret_cast<float2 *>(row + mt * 16 + 2 * gid) = make_float2(o[mt][jj], o[mt][jj + 2]);
+                    *reinterpret_cast<float2 *>(row + mt * 16 + 2 * gid) =
+                        jj ? make_float2(o[mt][0].y, o[mt][1].y) : make_float2(o[mt][0].x, o[mt][1].x);
                 if (gid == 0) {
                     // (every score NaN: the maximum passed over them; 0 lets the NaN sum through the merge)
                     row[D] = m[jj] == -INFINITY && l[jj] != l[jj] ? 0.f : m[jj];
@@ -423,6 +403,12 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm)
             mbuf = 0;
             mphase ^= 1u;
         }
+    }
+    if (!ok) {
+        // let copies in flight land before the CTA exits (bounded)
+        volatile int no_abort = 0;
+        for (; taken < issued; ++taken) mbar_wait(&full[taken % S], (taken / S) & 1u, &no_abort, nullptr);
+        return;
     }
     // end marker for the merge warp
     if (mbar_wait(&mempty[mbuf], mphase ^ 1u, abort_flag, a.err)) {
