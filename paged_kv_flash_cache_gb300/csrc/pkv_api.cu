@@ -480,7 +480,6 @@ pkv_status prefill_impl(const pkv_cache &cache, const void *q, int num_q_heads, 
     if (batch < 0 || max_blocks_per_seq <= 0 || num_q_heads <= 0 || total_q < 0 || max_q_len < 0)
         return PKV_ERR_INVALID_ARG;
     if (num_q_heads % cache.num_kv_heads != 0) return PKV_ERR_INVALID_ARG;
-    if (cache.format == PKV_KV_INT8_BLOCK) return PKV_ERR_UNSUPPORTED;
     if (batch == 0 || total_q == 0) return PKV_OK;
     if (!q || !cu_q_lens || !context_lens || !block_tables || !out) return PKV_ERR_INVALID_ARG;
     if (!aligned16(q) || !aligned16(out) || (lse && !aligned16(lse))) return PKV_ERR_INVALID_ARG;

@@ -271,6 +271,7 @@ cudaError_t launch_decode_fp8(const DecodeArgs &a, int grid, cudaStream_t s);
 cudaError_t launch_decode(const DecodeArgs &a, int grid, cudaStream_t s);
 cudaError_t launch_combine(const CombineArgs &a, cudaStream_t s);
 cudaError_t launch_prefill(const PrefillArgs &a, cudaStream_t s);
+cudaError_t launch_prefill_int8(const PrefillArgs &a, cudaStream_t s);
 // head_dim 256 (prefill_wide.cu): one 128-row query tile a CTA, 64-key tiles
 cudaError_t launch_prefill_wide(const PrefillArgs &a, cudaStream_t s);
 // q [total_q, Hq, D] as a 3-D tensor map (d, head, token), boxes of 64 columns x 1 head x box_rows

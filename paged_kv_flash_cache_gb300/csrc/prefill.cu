@@ -1007,6 +1007,7 @@ cudaError_t launch_t(const PrefillArgs &a, cudaStream_t stream) {
 
 cudaError_t launch_prefill(const PrefillArgs &a, cudaStream_t s) {
     if (a.max_q_len == 0) return cudaSuccess;
+    if (a.cache.int8) return launch_prefill_int8(a, s);
     if (a.cache.head_dim == 256) return a.cache.fp8 ? cudaErrorNotSupported : launch_prefill_wide(a, s);
     if (a.cache.head_dim != 64 && a.cache.head_dim != 128) return cudaErrorNotSupported;
     const bool bf16 = a.cache.dtype == 1;

@@ -1,0 +1,624 @@
+// prefill_int8.cu -- paged_attn_prefill over an INT8 cache (one scale per page, K or V, and KV head), head_dim 64 or
+// 128: a chunk of queries per sequence against its paged context, causal (bottom-right aligned) or not, on the
+// 5th-generation tensor cores.
+//
+// out = softmax(Q K^T * scale) V with K = sk c^k, V = sv c^v per page. The CTA first finds Wk and Wv, powers of two at or
+// above every scale of its pages; the converters then write (sk / Wk) c^k and (sv / Wv) c^v in f16 -- exact for powers of
+// two down to 2^-17 of the largest, else within 2^-25 of W or half a step of f16 --, and Wk goes into the softmax's
+// scale, Wv into the epilogue's 1 / l. So the softmax and the MMAs are those of a 16-bit cache, and a scale costs one
+// packed multiplication per pair of codes, in warps that have time for it.
+//
+// CTA = one query head x 256 query rows of one sequence, as two 128-row tiles A and B that share every K/V tile (512
+// threads, four warpgroups):
+//   warp 0     TMA producer: both Q tiles once; then for each 128-key tile the codes of K and of V, each into one slot of a
+//              4-slot ring: a lane looks up a page in the block table and issues its box;
+//   warp 1     TMEM owner and MMA issuer (one thread). TMEM columns: S_A [0,128), S_B [128,256), O_A [256,256+D),
+//              O_B [384,384+D); P_x over the first 64 columns of S_x. Per key tile j: O_A += P_A V_j, S_A = Q_A K_{j+1}^T,
+//              O_B += P_B V_j, S_B = Q_B K_{j+1}^T, so one tile's softmax overlaps the other tile's MMAs;
+//   WG 1, 2    softmax of tile A / tile B, one query row per thread; epilogue O / l -> out, lse;
+//   WG 3       converters: Q to f16 once (a bf16 one), then each slot's codes in place (head_dim 128: they land where the
+//              second half of the f16 tile goes; head_dim 64: from a buffer of their own), 32 rows a warp.
+// Conversion in a warpgroup of its own keeps it off the softmax, whose exponentials and hand-offs bound the kernel.
+#include <cuda.h>
+#include <cuda_runtime.h>
+
+#include "pkv_device.cuh"
+#include "pkv_internal.h"
+#include "prefill_common.cuh"
+#include "tcgen05.cuh"
+#include "warp_mma.cuh"
+
+namespace pkv {
+namespace {
+
+constexpr int kBM = 128;       // query rows per tile
+constexpr int kRows = 256;     // query rows per CTA (tiles A and B)
+constexpr int kBN = 128;       // keys per KV tile
+constexpr int kRing = 4;       // K/V ring slots
+constexpr int kThreads = 512;  // 4 warpgroups
+constexpr float kRescaleLog2 = 8.0f;  // rescale O only when the max grows by more than 2^8
+// Weights are 2^7 times themselves in the product with V (at most 2^15): f16 has no step below 2^-24, and many small
+// weights add up.
+constexpr float kWeightLog2 = 7.0f;
+constexpr uint32_t kColS = 0, kColO = 256;
+
+template <int D>
+struct Layout {
+    static constexpr int kHalves = D / 64;                    // 128-byte swizzle atoms along D
+    static constexpr uint32_t kTileHalf = 128 * 128;          // 128 rows x 128 bytes
+    static constexpr uint32_t kQBytes = kHalves * kTileHalf;  // one 128-row Q tile
+    static constexpr uint32_t kKVBytes = kHalves * kTileHalf; // one f16 K or V tile
+    static constexpr uint32_t kRingOff = 2 * kQBytes;
+    static constexpr bool kCodesApart = D == 64;
+    static constexpr uint32_t kCodeOff = kRingOff + kRing * kKVBytes;  // [kRing][128 x 64] (D = 64)
+    static constexpr uint32_t kBarOff = kCodeOff + (kCodesApart ? kRing * 128 * 64 : 0);
+    static constexpr uint32_t kSmemBytes = kBarOff + 512 + 1024;  // + alignment slack
+    __device__ static uint8_t *codes(uint8_t *smem, int slot) {
+        return kCodesApart ? smem + kCodeOff + slot * (128 * 64) : smem + kRingOff + slot * kKVBytes + kTileHalf;
+    }
+    static constexpr uint32_t kTmemCols = 512;
+};
+
+struct Params {
+    const int *cu_q_lens, *context_lens, *block_tables;
+    int batch, mb, num_q_heads, num_kv_heads, group, bs, log2_bs, num_blocks;
+    float scale_log2;
+    int causal;
+    int skip_single;      // mixed batch: leave sequences with one query row to the decode kernels
+    const float *scales;  // [NB, 2, Hkv]
+    void *out;
+    int out_dtype;
+    float *lse;
+    int *err;
+};
+
+// Smallest power of two >= x, for finite x >= 0 (0 for 0; at most 2^127).
+__device__ __forceinline__ float pow2_at_least(float x) {
+    uint32_t b = __float_as_uint(x);
+    if (b & 0x7fffffu) b = (b & 0x7f800000u) + 0x800000u;
+    return b >= 0x7f800000u ? 1.7014118e38f : __uint_as_float(b);
+}
+
+// Four codes (one word) times the f16 pair kk: 1024 + (c + 128), less 1152, is c exactly; one rounding in the product.
+__device__ __forceinline__ void codes4_f16(uint32_t w, uint32_t kk, uint32_t &lo, uint32_t &hi) {
+    const uint32_t x = w ^ 0x80808080u;
+    asm("{\n\t.reg .b32 a, b;\n\t"
+        "add.rn.f16x2 a, %2, %4;\n\tadd.rn.f16x2 b, %3, %4;\n\t"
+        "mul.rn.f16x2 %0, a, %5;\n\tmul.rn.f16x2 %1, b, %5;\n\t}"
+        : "=r"(lo), "=r"(hi)
+        : "r"(__byte_perm(x, 0x64646464u, 0x4140)), "r"(__byte_perm(x, 0x64646464u, 0x4342)), "r"(0xe480e480u), "r"(kk));
+}
+
+// Rows g .. g + 7 (g a multiple of 8) of a slot: codes to the f16 layout that TMA writes for a 16-bit cache (64-column
+// halves of 128-byte rows, 128-byte swizzle), times kk. A row is read entirely before any of it is written.
+template <int D>
+struct RowConverter;
+
+template <>
+struct RowConverter<128> {  // lane -> rows rr and rr + 4 (rr = lane / 8), 16-code chunk lane % 8; in place
+    uint32_t ld[2], sta[2], stb[2];
+    int hf;
+    __device__ __forceinline__ explicit RowConverter(int lane) {
+        const int c = lane & 7, rr = lane >> 3;
+        hf = c >> 2;
+        const int k0 = 2 * (c & 3);
+        // the lanes of the two halves store opposite chunks first: the 8 stores of a row in one instruction then
+        // fill all 32 banks once
+        const int ka = hf ? k0 + 1 : k0, kb = hf ? k0 : k0 + 1;
+#pragma unroll
+        for (int i = 0; i < 2; ++i) {
+            const int rw = rr + 4 * i;  // == row & 7
+            ld[i] = rw * 128u + ((c ^ rw) << 4);
+            sta[i] = hf * Layout<128>::kTileHalf + rw * 128u + ((ka ^ rw) << 4);
+            stb[i] = hf * Layout<128>::kTileHalf + rw * 128u + ((kb ^ rw) << 4);
+        }
+    }
+    __device__ __forceinline__ void pass(const uint8_t *codes, uint8_t *f16, int g, uint32_t kk) const {
+        const uint32_t grp = (uint32_t)g * 128u;
+        uint4 raw[2];
+#pragma unroll
+        for (int i = 0; i < 2; ++i) raw[i] = *reinterpret_cast<const uint4 *>(codes + grp + ld[i]);
+        __syncwarp();
+#pragma unroll
+        for (int i = 0; i < 2; ++i) {
+            uint4 v0, v1;
+            codes4_f16(raw[i].x, kk, v0.x, v0.y);
+            codes4_f16(raw[i].y, kk, v0.z, v0.w);
+            codes4_f16(raw[i].z, kk, v1.x, v1.y);
+            codes4_f16(raw[i].w, kk, v1.z, v1.w);
+            *reinterpret_cast<uint4 *>(f16 + grp + sta[i]) = hf ? v1 : v0;
+            *reinterpret_cast<uint4 *>(f16 + grp + stb[i]) = hf ? v0 : v1;
+        }
+    }
+};
+
+template <>
+struct RowConverter<64> {  // lane -> row lane / 4, 16-code chunk lane % 4 (64-byte rows, 64-byte swizzle)
+    uint32_t ld, sta, stb;
+    __device__ __forceinline__ explicit RowConverter(int lane) {
+        const int c = lane & 3, rr = lane >> 2;  // rr == row & 7
+        ld = rr * 64u + ((c ^ ((rr >> 1) & 3)) << 4);
+        sta = rr * 128u + (((2 * c) ^ rr) << 4);
+        stb = rr * 128u + (((2 * c + 1) ^ rr) << 4);
+    }
+    __device__ __forceinline__ void pass(const uint8_t *codes, uint8_t *f16, int g, uint32_t kk) const {
+        const uint4 raw = *reinterpret_cast<const uint4 *>(codes + (uint32_t)g * 64u + ld);
+        uint4 v0, v1;
+        codes4_f16(raw.x, kk, v0.x, v0.y);
+        codes4_f16(raw.y, kk, v0.z, v0.w);
+        codes4_f16(raw.z, kk, v1.x, v1.y);
+        codes4_f16(raw.w, kk, v1.z, v1.w);
+        const uint32_t grp = (uint32_t)g * 128u;
+        *reinterpret_cast<uint4 *>(f16 + grp + sta) = v0;
+        *reinterpret_cast<uint4 *>(f16 + grp + stb) = v1;
+    }
+};
+
+// BF16: type of q and the default output; the products run in f16.
+template <int D, bool BF16>
+__global__ void __launch_bounds__(kThreads, 1)
+    prefill_int8_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CUtensorMap tm_kv, Params p) {
+    using Lay = Layout<D>;
+    extern __shared__ uint8_t smem_raw[];
+    // 1024-byte alignment: the 128-byte swizzle pattern is a function of address bits 4-9.
+    uint8_t *smem = smem_raw + ((1024u - (smem_addr(smem_raw) & 1023u)) & 1023u);
+    uint8_t *sQ = smem;
+    uint8_t *sRing = smem + Lay::kRingOff;
+    uint64_t *bars = reinterpret_cast<uint64_t *>(smem + Lay::kBarOff);
+    uint64_t *kv_full = bars;       // [kRing] a slot's f16 tile is ready
+    uint64_t *kv_empty = bars + 4;  // [kRing] its MMAs are done
+    uint64_t *kv_code = bars + 8;   // [kRing] its codes have landed
+    uint64_t *s_full = bars + 12;   // [2] S_A / S_B computed
+    uint64_t *p_full = bars + 14;   // [2] P_A / P_B in TMEM (and O rescaled)
+    uint64_t *o_done = bars + 16;   // [2] P V accumulated into O_A / O_B
+    uint64_t *q_full = bars + 18;
+    uint64_t *q_ready = bars + 19;  // Q converted to f16 (or left as it is)
+    uint64_t *w_ready = bars + 20;  // Wk, Wv and the first pages that are not numbers
+    uint64_t *drain = bars + 21;    // every MMA issued has completed
+    uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(bars + 22);
+    volatile int *abort_flag = reinterpret_cast<volatile int *>(bars + 23);
+    uint32_t *sMax = reinterpret_cast<uint32_t *>(bars + 24);  // [2] bits of the largest finite K / V scale
+    int *sNan = reinterpret_cast<int *>(bars + 25);            // [2] first position of a page whose K / V scale is not finite
+
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    // grid (heads, batch, row blocks) with the row blocks last-first: CTAs start in linear order, so
+    // the row blocks that see the most keys (causal) start in the first wave and the short ones
+    // fill in behind them. A mixed batch: (heads, row blocks last-first, sequences by their rank
+    // among those with several query rows), so that no CTA without work precedes one with work.
+    const int h = blockIdx.x;
+    const int mt = p.skip_single ? (int)gridDim.y - 1 - (int)blockIdx.y : (int)gridDim.z - 1 - (int)blockIdx.z;
+    pdl_wait();  // lengths, tables, q and the chunk's own K/V may come from the previous kernel
+    const int b = p.skip_single ? nth_multi_row_sequence(p.cu_q_lens, p.batch, blockIdx.z) : (int)blockIdx.y;
+    if (b < 0) return;  // uniform: past the mixed batch's last chunk
+    const int q0 = __ldg(p.cu_q_lens + b);
+    const int q_len = __ldg(p.cu_q_lens + b + 1) - q0;
+    const int m_start = mt * kRows;
+    if (m_start >= q_len || (p.skip_single && q_len == 1)) return;  // uniform: nothing allocated yet
+    const int L = __ldg(p.context_lens + b);
+    if (L > p.mb * p.bs || q_len > L || L < 0) {
+        if (threadIdx.x == 0) set_error(p.err, kErrDeviceRange);
+        return;
+    }
+    const int rows = min(kRows, q_len - m_start);
+    const int qpos0 = L - q_len + m_start;           // absolute position of row 0
+    const int kv_end = p.causal ? qpos0 + rows : L;  // keys [0, kv_end) are needed
+    const int n_tiles = (kv_end + kBN - 1) / kBN;
+    const int g = h / p.group;
+    const int *bt = p.block_tables + (size_t)b * p.mb;
+
+    if (threadIdx.x == 0) {
+        for (int s = 0; s < kRing; ++s) {
+            mbar_init(&kv_full[s], 4);
+            mbar_init(&kv_empty[s], 1);
+            mbar_init(&kv_code[s], 1);
+        }
+        mbar_init(q_full, 1);
+        mbar_init(q_ready, 4);
+        mbar_init(w_ready, 4);
+        for (int x = 0; x < 2; ++x) {
+            mbar_init(&s_full[x], 1);
+            mbar_init(&p_full[x], 4);
+            mbar_init(&o_done[x], 1);
+        }
+        mbar_init(drain, 1);
+        *abort_flag = 0;
+        sMax[0] = sMax[1] = 0u;
+        sNan[0] = sNan[1] = 0x7fffffff;
+        fence_barrier_init();
+    }
+    if (warp == 1) {
+        tc::tmem_alloc(tmem_slot, Lay::kTmemCols);
+        tc::tmem_relinquish();
+    }
+    tc::fence_before_sync();
+    __syncthreads();
+    tc::fence_after_sync();
+    const uint32_t tmem = *tmem_slot;
+
+    if (warp < 4) {
+        tc::regs_dec<48>();
+        if (warp == 0) {
+            // ==================================== TMA producer ====================================
+            const int box_rows = p.bs < kBN ? p.bs : kBN;
+            uint32_t issued = 0;  // ring items issued (for the abort drain)
+            if (lane == 0) {
+                tc::prefetch_tensormap(&tm_q);
+                tc::prefetch_tensormap(&tm_kv);
+                mbar_arrive_expect_tx(q_full, 2 * Lay::kQBytes);
+#pragma unroll
+                for (int x = 0; x < 2; ++x)
+#pragma unroll
+                    for (int hf = 0; hf < Lay::kHalves; ++hf)
+                        tc::tma_load_3d(sQ + x * Lay::kQBytes + hf * Lay::kTileHalf, &tm_q, hf * 64, h,
+                                        q0 + m_start + x * kBM, q_full);
+            }
+            bool ok = true;
+            for (int j = 0; j < n_tiles && ok; ++j) {
+                const int kv_start = j * kBN;
+                const int n_valid = min(kBN, L - kv_start);
+                const int npages = p.bs < kBN ? (n_valid + p.bs - 1) >> p.log2_bs : 1;
+                const int off = p.bs < kBN ? 0 : (kv_start & (p.bs - 1));
+                int pb = 0;
+                if (lane < npages) {
+                    pb = __ldg(bt + (kv_start >> p.log2_bs) + lane);
+                    if (pb < 0 || pb >= p.num_blocks) {
+                        set_error(p.err, kErrDeviceRange);
+                        pb = 0;
+                    }
+                }
+                for (int kv = 0; kv < 2; ++kv) {
+                    const uint32_t u = 2u * j + kv, slot = u % kRing, ph = (u / kRing) & 1u;
+                    if (!mbar_wait(&kv_empty[slot], ph ^ 1u, abort_flag, p.err)) { ok = false; break; }
+                    if (lane == 0) mbar_arrive_expect_tx(&kv_code[slot], (uint32_t)npages * box_rows * D);
+                    __syncwarp();
+                    if (lane < npages)
+                        tc::tma_load_5d(Lay::codes(smem, slot) + (uint32_t)lane * box_rows * D, &tm_kv, 0, off, g, kv, pb,
+                                        &kv_code[slot]);
+                    ++issued;
+                }
+            }
+            if (!ok) {
+                // let copies in flight land before the CTA exits (bounded)
+                volatile int no_abort = 0;
+                mbar_wait(q_full, 0, &no_abort, nullptr);
+                for (uint32_t u = issued > (uint32_t)kRing ? issued - kRing : 0u; u < issued; ++u)
+                    mbar_wait(&kv_code[u % kRing], (u / kRing) & 1u, &no_abort, nullptr);
+            }
+        } else if (warp == 1) {
+            // ===================================== MMA issuer =====================================
+            if (lane == 0) {
+                const uint32_t id_qk = tc::idesc_f16(false, kBM, kBN, false);
+                const uint32_t id_pv = tc::idesc_f16(false, kBM, D, true);
+                const uint32_t aQ = smem_addr(sQ), aRing = smem_addr(sRing);
+                auto ring_wait = [&](uint32_t u) {
+                    return mbar_wait(&kv_full[u % kRing], (u / kRing) & 1u, abort_flag, p.err);
+                };
+                auto qk = [&](int x, uint32_t aK) {
+                    const uint32_t aQx = aQ + (uint32_t)x * Lay::kQBytes;
+#pragma unroll
+                    for (int kk = 0; kk < D / 16; ++kk) {
+                        const uint32_t o = (uint32_t)(kk >> 2) * Lay::kTileHalf + (uint32_t)(kk & 3) * 32u;
+                        tc::mma_f16_ss(tmem + kColS + 128u * x, tc::smem_desc(aQx + o, 16, 1024), tc::smem_desc(aK + o, 16, 1024),
+                                       id_qk, kk > 0 ? 1u : 0u);
+                    }
+                    tc::mma_commit(&s_full[x]);
+                };
+                auto pv = [&](int x, uint32_t aV, int j) {
+                    const uint32_t tP = tmem + kColS + 128u * x, tO = tmem + kColO + 128u * x;
+#pragma unroll
+                    for (int kk = 0; kk < kBN / 16; ++kk) {
+                        // V is [keys x D], D contiguous: MN-major B; 8-key groups 1024 B apart,
+                        // 64-column halves kTileHalf apart. P: 16 keys = 8 TMEM columns.
+                        tc::mma_f16_ts(tO, tP + 8u * kk, tc::smem_desc(aV + (uint32_t)kk * 2048u, Lay::kTileHalf, 1024),
+                                       id_pv, (j > 0 || kk > 0) ? 1u : 0u);
+                    }
+                    tc::mma_commit(&o_done[x]);
+                };
+                bool ok = mbar_wait(q_ready, 0, abort_flag, p.err) && ring_wait(0);
+                if (ok) {
+                    tc::fence_after_sync();
+                    qk(0, aRing);  // S_A = Q_A K_0^T
+                    qk(1, aRing);  // S_B = Q_B K_0^T
+                    tc::mma_commit(&kv_empty[0]);
+                }
+                // Ping-pong: tile A's P V_j then its next S, then tile B's. P_x sits in S_x's columns;
+                // the tensor pipe runs the MMAs of this thread in issue order, so S_x(j+1) is
+                // written only after P_x(j) V_j has read P_x(j).
+                for (int j = 0; ok && j < n_tiles; ++j) {
+                    const uint32_t uK = 2u * j, uV = uK + 1, uKn = uK + 2;
+                    const uint32_t aV = aRing + (uV % kRing) * Lay::kKVBytes;
+                    const uint32_t aKn = aRing + (uKn % kRing) * Lay::kKVBytes;
+                    const uint32_t ph = (uint32_t)j & 1u;
+                    const bool more = j + 1 < n_tiles;
+                    if (!(ok = ring_wait(uV) && mbar_wait(&p_full[0], ph, abort_flag, p.err))) break;
+                    tc::fence_after_sync();
+                    pv(0, aV, j);
+                    if (more) {
+                        if (!(ok = ring_wait(uKn))) break;
+                        qk(0, aKn);
+                    }
+                    if (!(ok = mbar_wait(&p_full[1], ph, abort_flag, p.err))) break;
+                    tc::fence_after_sync();
+                    pv(1, aV, j);
+                    tc::mma_commit(&kv_empty[uV % kRing]);
+                    if (more) {
+                        qk(1, aKn);
+                        tc::mma_commit(&kv_empty[uKn % kRing]);
+                    }
+                }
+                tc::mma_commit(drain);
+                volatile int no_abort = 0;
+                mbar_wait(drain, 0, &no_abort, p.err);
+            }
+            __syncwarp();
+        }
+    } else if (warp >= 12) {
+        tc::regs_dec<80>();
+        // ===================================== converters =====================================
+        const int cw = warp - 12;
+        // ---- Wk, Wv over the pages of keys [0, kv_end); a page id outside the pool: page 0, as the producer reads it ----
+        {
+            const int pages = (kv_end + p.bs - 1) >> p.log2_bs;
+            float mk = 0.f, mv = 0.f;
+            int nk = 0x7fffffff, nv = 0x7fffffff;
+            for (int i = cw * 32 + lane; i < pages; i += 128) {
+                int pb = __ldg(bt + i);
+                if (pb < 0 || pb >= p.num_blocks) pb = 0;
+                const float *sc = p.scales + (size_t)pb * 2 * p.num_kv_heads + g;
+                const float k = __ldg(sc), v = __ldg(sc + p.num_kv_heads);
+                if (k < INFINITY) mk = fmaxf(mk, k); else nk = min(nk, i << p.log2_bs);
+                if (v < INFINITY) mv = fmaxf(mv, v); else nv = min(nv, i << p.log2_bs);
+            }
+            mk = __uint_as_float(__reduce_max_sync(0xffffffffu, __float_as_uint(mk)));  // (bits of numbers >= 0 are in order)
+            mv = __uint_as_float(__reduce_max_sync(0xffffffffu, __float_as_uint(mv)));
+            nk = __reduce_min_sync(0xffffffffu, nk);
+            nv = __reduce_min_sync(0xffffffffu, nv);
+            if (lane == 0) {
+                atomicMax(&sMax[0], __float_as_uint(mk));
+                atomicMax(&sMax[1], __float_as_uint(mv));
+                atomicMin(&sNan[0], nk);
+                atomicMin(&sNan[1], nv);
+                __threadfence_block();
+                mbar_arrive(w_ready);
+            }
+            __syncwarp();
+        }
+        bool ok = true;
+        if (BF16) {
+            // q to f16 in place (exact for |q| within f16's range)
+            ok = mbar_wait(q_full, 0, abort_flag, p.err);
+            if (ok) {
+                uint4 *q4 = reinterpret_cast<uint4 *>(sQ);
+                for (int i = cw * 32 + lane; i < 2 * (int)Lay::kQBytes / 16; i += 128) {
+                    const uint4 v = q4[i];
+                    const uint32_t w[4] = {v.x, v.y, v.z, v.w};
+                    uint32_t o[4];
+#pragma unroll
+                    for (int k = 0; k < 4; ++k)
+                        o[k] = pack_pair<false>(__uint_as_float(w[k] << 16), __uint_as_float(w[k] & 0xffff0000u));
+                    q4[i] = make_uint4(o[0], o[1], o[2], o[3]);
+                }
+                tc::fence_proxy_async_smem();
+            }
+        } else {
+            ok = mbar_wait(q_full, 0, abort_flag, p.err);
+        }
+        __syncwarp();
+        if (ok && lane == 0) mbar_arrive(q_ready);
+        ok = ok && mbar_wait(w_ready, 0, abort_flag, p.err);
+        const float wk = pow2_at_least(__uint_as_float(sMax[0])), wv = pow2_at_least(__uint_as_float(sMax[1]));
+        const float ik = wk >= 1.17549435e-38f ? copysignf(1.f / wk, p.scale_log2) : 0.f, iv = wv >= 1.17549435e-38f ? 1.f / wv : 0.f;
+        // lane i: the scales of page i of the tile, loaded a tile ahead
+        auto scale_of = [&](int j, float &sk, float &sv) {
+            sk = sv = 0.f;
+            const int kv_start = j * kBN;
+            if (j >= n_tiles || kv_start + (lane << p.log2_bs) >= min(L, kv_start + kBN)) return;
+            int pb = __ldg(bt + (kv_start >> p.log2_bs) + lane);
+            if (pb < 0 || pb >= p.num_blocks) pb = 0;
+            const float *sc = p.scales + (size_t)pb * 2 * p.num_kv_heads + g;
+            sk = __ldg(sc);
+            sv = __ldg(sc + p.num_kv_heads);
+        };
+        float sk, sv;
+        scale_of(0, sk, sv);
+        const RowConverter<D> conv(lane);
+        for (int j = 0; ok && j < n_tiles; ++j) {
+            // f16 factors of the tile's pages; what is not finite counts as 0 here (its rows are made NaN at the end)
+            const float fk = sk < INFINITY ? sk * ik : 0.f, fv = sv < INFINITY ? sv * iv : 0.f;
+            const uint32_t kk = pack_pair<false>(fk, fk), kv2 = pack_pair<false>(fv, fv);
+            scale_of(j + 1, sk, sv);
+            for (int kv = 0; kv < 2; ++kv) {
+                const uint32_t u = 2u * j + kv, slot = u % kRing;
+                if (!(ok = mbar_wait(&kv_code[slot], (u / kRing) & 1u, abort_flag, p.err))) break;
+                const uint8_t *codes = Lay::codes(smem, slot);
+                uint8_t *f16 = sRing + slot * Lay::kKVBytes;
+#pragma unroll
+                for (int i = 0; i < 4; ++i) {
+                    const int row = cw * 32 + i * 8;
+                    conv.pass(codes, f16, row, __shfl_sync(0xffffffffu, kv ? kv2 : kk, (row >> p.log2_bs) & 31));
+                }
+                tc::fence_proxy_async_smem();
+                __syncwarp();
+                if (lane == 0) mbar_arrive(&kv_full[slot]);
+            }
+        }
+    } else {
+        tc::regs_inc<192>();
+        // ================================= softmax + epilogue =================================
+        const int x = (warp >> 2) - 1;                 // 0: tile A, 1: tile B
+        const int quarter = warp & 3;                  // TMEM lanes 32*quarter .. +31
+        const int r = quarter * 32 + lane;             // row within the tile
+        const int row = x * kBM + r;                   // row within the CTA block
+        const bool row_ok = row < rows;
+        const int qpos = qpos0 + row;
+        const uint32_t lane_base = (uint32_t)(quarter * 32) << 16;
+        const uint32_t tS = tmem + kColS + 128u * x + lane_base;   // S_x, and P_x over its first 64 columns
+        const uint32_t tO = tmem + kColO + 128u * x + lane_base;
+        float m_use = -INFINITY, l = 0.f;
+        bool ok = mbar_wait(w_ready, 0, abort_flag, p.err);
+        // (never 0, which times a masked score's -inf would be NaN; a negative scale has its sign in K)
+        const float wk = pow2_at_least(__uint_as_float(sMax[0]));
+        const float c = fmaxf(fabsf(p.scale_log2 * (wk > 0.f ? wk : 1.f)), 1.17549435e-38f);
+        for (int j = 0; ok && j < n_tiles; ++j) {
+            const int kv_start = j * kBN;
+            const uint32_t ph = (uint32_t)j & 1u;
+            if (!(ok = mbar_wait(&s_full[x], ph, abort_flag, p.err))) break;
+            tc::fence_after_sync();
+            float s[kBN];
+#pragma unroll
+            for (int cc = 0; cc < kBN / 32; ++cc)
+                tc::tmem_ld32(tS + cc * 32, *reinterpret_cast<float(*)[32]>(&s[cc * 32]));
+            tc::tmem_wait_ld();
+            // last key index this row may see in this tile (-1: none)
+            int lim = L - 1 - kv_start;
+            if (p.causal) lim = min(lim, qpos - kv_start);
+            if (!row_ok) lim = -1;
+            if (lim < kBN - 1) {
+#pragma unroll
+                for (int i = 0; i < kBN; ++i) s[i] = (i <= lim) ? s[i] : -INFINITY;
+            }
+            // row max as 8 independent chains (two warps per scheduler cannot hide a 64-deep chain)
+            float m8[8];
+#pragma unroll
+            for (int k = 0; k < 8; ++k) m8[k] = fmax3(s[k], s[k + 8], s[k + 16]);
+#pragma unroll
+            for (int i = 24; i < kBN; i += 16)
+#pragma unroll
+                for (int k = 0; k < 8; ++k) m8[k] = fmax3(m8[k], s[i + k], (i + 8 + k < kBN) ? s[i + 8 + k] : -INFINITY);
+            const float mx = fmaxf(fmax3(m8[0], m8[1], m8[2]), fmax3(fmax3(m8[3], m8[4], m8[5]), m8[6], m8[7]));
+            const float m_new = fmaxf(m_use, mx * c);
+            const bool grow = m_new > m_use + kRescaleLog2;   // false when m_new = -inf
+            const float alpha = grow ? ex2f(m_use - m_new) : 1.f;  // 0 when m_use = -inf
+            if (grow) {
+                m_use = m_new;
+                l *= alpha;
+            }
+            // masked entries are -inf; m_use is finite for a row with a visible key, and a row
+            // without one (padding row) uses 0 so that exp2(-inf) = 0 instead of a NaN
+            const float neg_m = kWeightLog2 - ((m_use == -INFINITY) ? 0.f : m_use);
+            uint32_t pk[kBN / 2];
+            float2 l4[4] = {make_float2(0.f, 0.f), make_float2(0.f, 0.f), make_float2(0.f, 0.f), make_float2(0.f, 0.f)};
+            const float2 c2 = make_float2(c, c), nm2 = make_float2(neg_m, neg_m);
+#pragma unroll
+            for (int q = 0; q < kBN / 2; ++q) {
+                const float2 xq = ffma2(make_float2(s[2 * q], s[2 * q + 1]), c2, nm2);
+                const float2 e = make_float2(ex2f(xq.x), ex2f(xq.y));
+                l4[q & 3] = fadd2(l4[q & 3], e);
+                pk[q] = pack_pair<false>(e.x, e.y);
+            }
+            const float2 l2 = fadd2(fadd2(l4[0], l4[1]), fadd2(l4[2], l4[3]));
+            l += l2.x + l2.y;
+            // P_x and O_x are touched only after P_x V_{j-1} is done
+            if (j > 0) {
+                if (!(ok = mbar_wait(&o_done[x], (uint32_t)(j - 1) & 1u, abort_flag, p.err))) break;
+                tc::fence_after_sync();
+                if (__any_sync(0xffffffffu, grow)) {
+#pragma unroll
+                    for (int cc = 0; cc < D / 32; ++cc) {
+                        float o[32];
+                        tc::tmem_ld32(tO + cc * 32, o);
+                        tc::tmem_wait_ld();
+#pragma unroll
+                        for (int i = 0; i < 32; ++i) o[i] *= alpha;
+                        tc::tmem_st32(tO + cc * 32, o);
+                    }
+                }
+            }
+#pragma unroll
+            for (int cc = 0; cc < kBN / 32; ++cc)
+                tc::tmem_st16(tS + cc * 16, *reinterpret_cast<uint32_t(*)[16]>(&pk[cc * 16]));
+            tc::tmem_wait_st();
+            tc::fence_before_sync();
+            __syncwarp();
+            if (lane == 0) mbar_arrive(&p_full[x]);
+        }
+        // ---- epilogue: O / l ----
+        if (ok && mbar_wait(&o_done[x], (uint32_t)(n_tiles - 1) & 1u, abort_flag, p.err)) {
+            tc::fence_after_sync();
+            // a row that sees a key of a page whose scale is not finite is NaN
+            const int last = p.causal ? qpos : L - 1;
+            const float nan = __uint_as_float(0x7fc00000u);
+            const bool nan_k = last >= sNan[0], nan_v = last >= sNan[1];
+            const float wv = pow2_at_least(__uint_as_float(sMax[1]));
+            const float inv = nan_k || nan_v ? nan : l > 0.f ? wv / l : 0.f;
+            const size_t row_g = (size_t)(q0 + m_start + row);
+            const size_t obase = (row_g * p.num_q_heads + h) * D;
+#pragma unroll
+            for (int cc = 0; cc < D / 32; ++cc) {
+                float o[32];
+                tc::tmem_ld32(tO + cc * 32, o);
+                tc::tmem_wait_ld();
+                if (row_ok) {
+#pragma unroll
+                    for (int i = 0; i < 4; ++i) {
+                        float v[8];
+#pragma unroll
+                        for (int k = 0; k < 8; ++k) v[k] = o[8 * i + k] * inv;
+                        store_out_vec<8>(p.out, obase + cc * 32 + 8 * i, v, p.out_dtype);
+                    }
+                }
+            }
+            if (row_ok && p.lse)
+                p.lse[row_g * p.num_q_heads + h] =
+                    nan_k ? nan : l > 0.f ? (m_use + (__log2f(l) - kWeightLog2)) * kLn2 : -INFINITY;
+        }
+    }
+    tc::fence_before_sync();
+    __syncthreads();
+    pdl_launch_dependents();
+    if (warp == 1) {
+        tc::fence_after_sync();
+        tc::tmem_dealloc(tmem, Lay::kTmemCols);
+    }
+}
+
+template <int D, bool BF16>
+cudaError_t launch_t(const PrefillArgs &a, cudaStream_t stream) {
+    using Lay = Layout<D>;
+    CUtensorMap tm_q, tm_kv;
+    cudaError_t e = encode_q_heads_map(a.q, BF16 ? 1 : 0, a.total_q, a.num_q_heads, D, kBM, &tm_q);
+    if (e != cudaSuccess) return e;
+    e = encode_int8_map(a.cache, a.cache.block_size < kBN ? a.cache.block_size : kBN, 1, &tm_kv);
+    if (e != cudaSuccess) return e;
+    Params p;
+    p.cu_q_lens = a.cu_q_lens;
+    p.context_lens = a.context_lens;
+    p.block_tables = a.block_tables;
+    p.batch = a.batch;
+    p.mb = a.max_blocks_per_seq;
+    p.num_q_heads = a.num_q_heads;
+    p.num_kv_heads = a.cache.num_kv_heads;
+    p.group = a.num_q_heads / a.cache.num_kv_heads;
+    p.bs = a.cache.block_size;
+    p.log2_bs = a.cache.log2_block_size;
+    p.num_blocks = a.cache.num_blocks;
+    p.scale_log2 = a.scale * kLog2e;
+    p.causal = a.causal;
+    p.skip_single = a.skip_single;
+    p.scales = a.cache.scales;
+    p.out = a.out;
+    p.out_dtype = a.out_dtype;
+    p.lse = a.lse;
+    p.err = a.err;
+    auto kern = prefill_int8_kernel<D, BF16>;
+    static DeviceFlags configured;
+    const int dev = device_info().device;
+    if (!configured.test(dev)) {
+        e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)Lay::kSmemBytes);
+        if (e != cudaSuccess) return e;
+        configured.set(dev);
+    }
+    const unsigned row_blocks = (unsigned)((a.max_q_len + kRows - 1) / kRows);
+    const dim3 grid = a.skip_single ? dim3(a.num_q_heads, row_blocks, a.batch) : dim3(a.num_q_heads, a.batch, row_blocks);
+    return launch_pdl(kern, grid, dim3(kThreads), Lay::kSmemBytes, stream, tm_q, tm_kv, p);
+}
+
+}  // namespace
+
+cudaError_t launch_prefill_int8(const PrefillArgs &a, cudaStream_t s) {
+    const bool bf16 = a.cache.dtype == 1;
+    if (a.cache.head_dim == 128) return bf16 ? launch_t<128, true>(a, s) : launch_t<128, false>(a, s);
+    return bf16 ? launch_t<64, true>(a, s) : launch_t<64, false>(a, s);
+}
+
+}  // namespace pkv

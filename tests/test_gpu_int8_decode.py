@@ -34,14 +34,19 @@ def tables_of(lens, bs, nb, mb, seed):
     return t
 
 
-def bounds(codes, scales, q, cu, lens, tables, scale, out, weight_eps, causal=True):
+def bounds(codes, scales, q, cu, lens, tables, scale, out, weight_eps, causal=True, weight_abs=2.0 ** -36):
     """Elementwise bounds (out, lse) of an FP32 result before its rounding.
 
     Scores: D exact products summed in FP32 (the tensor core's sums truncate: 2^-23 a step) and scaled: their error is
     at most e = (D + 4) 2^-23 scale sum |q||k|, and an element of q below f16's normal range is off by 2^-25, so
     e += D 2^-25 scale max|k|. A weight is then off by a factor within 2 e + 2^-20 (ex2: 2^-22, running maxima and
     the sums 2^-23 a step over the tiles of a warp: L / 128 steps, and the split's merge) + weight_eps (its rounding),
-    so the output by that times sum p |v| / sum p, and as much again for the sum it is divided by."""
+    so the output by that times sum p |v| / sum p, and as much again for the sum it is divided by.
+
+    f16 has no step below 2^-24, so a weight that goes into the product 2^k times itself (k = 11 in the decode, 7 in the
+    prefill), relative to a past maximum that is never above the row's, is off by 2^-25 2^-k = weight_abs of the row's largest
+    weight besides: over n keys of at most 127 steps of the context's largest V scale, by n weight_abs 127 max sv, over
+    sum p >= 1."""
     heads, d = codes.shape[2], codes.shape[4]
     group = q.shape[1] // heads
     err, err_lse = np.zeros(out.shape), np.zeros(out.shape[:2])
@@ -60,7 +65,9 @@ def bounds(codes, scales, q, cu, lens, tables, scale, out, weight_eps, causal=Tr
             p = np.exp(s - s.max(1, keepdims=True))
             e = ((d + 4) * 2.0 ** -23 * (np.abs(x) @ np.abs(k).T).max(1) + d * 2.0 ** -25 * np.abs(k).max()) * abs(scale)
             eps = 2 * e + 2.0 ** -20 + length / 128 * 2.0 ** -23 + weight_eps
-            err[r0:r0 + n, h] = 2 * eps[:, None] * (p @ np.abs(v)) / p.sum(1, keepdims=True)
+            pages = [int(i) for i in tables[b][:-(-length // codes.shape[3])]]
+            below = length * weight_abs * 127 * float(scales[pages, 1, h // group].max())
+            err[r0:r0 + n, h] = (2 * eps[:, None] * (p @ np.abs(v)) + below) / p.sum(1, keepdims=True)
             err_lse[r0:r0 + n, h] = eps + 2.0 ** -22 * (1 + np.abs(s.max(1)))
     return err, err_lse
 
