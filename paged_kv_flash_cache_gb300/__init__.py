@@ -24,6 +24,7 @@ v_new then stay float16 / bfloat16 (see pkv_kv_format in include/pkv.h).
 from __future__ import annotations
 
 import ctypes
+import functools
 import math
 import os
 import threading
@@ -235,12 +236,7 @@ def _cache_struct(cache, act_dtype, scales=None) -> _Cache:
         return _Cache(_dev(cache, "cache"), nb, hkv, bs, d, _dtype_code(act_dtype), KV_FP8_E4M3,
                       _dev(scales, "scales"))
     if cache.dtype is torch.int8:
-        if scales is None or scales.dtype != torch.float32 or tuple(scales.shape) != (nb, 2, hkv):
-            raise ValueError("an INT8 cache needs float32 scales [num_blocks, 2, num_kv_heads]")
-        if scales.get_device() != cache.get_device():
-            raise ValueError("scales on %s, the cache on another device" % scales.device)
-        return _Cache(_dev(cache, "cache"), nb, hkv, bs, d, _dtype_code(act_dtype), KV_INT8_BLOCK,
-                      _dev(scales, "scales"))
+        return _int8_cache(cache, scales, act_dtype)[0]
     if scales is not None:
         raise ValueError("scales are only for an FP8 or INT8 cache")
     if act_dtype != cache.dtype:
@@ -257,34 +253,91 @@ def _check(status: int, where: str):
 # entry points
 # ---------------------------------------------------------------------------------------------
 
-def _int8_args(cache, rows, rows_shape, batch, tables, lists):
-    """Checks of a call over an INT8 cache: the device of every tensor, the shape of the rows (name -> tensor) and of the
-    int32 lists (name -> (tensor, length))."""
+# Calls over an INT8 cache: every tensor on the cache's device, of the shape that the sizes give. (One line a check: a call of
+# a few microseconds on the GPU waits for them.)
+
+def _int8_cache(cache, scales, act_dtype):
+    """(C view of an INT8 cache, its device index, KV heads, block size, head_dim)."""
+    torch = _torch()
+    shape = cache.shape
+    if len(shape) != 5 or shape[1] != 2:
+        raise ValueError("cache must be [num_blocks, 2, num_kv_heads, block_size, head_dim]")
+    nb, _, hkv, bs, d = shape
+    if scales is None or scales.dtype is not torch.float32 or scales.shape != (nb, 2, hkv):
+        raise ValueError("an INT8 cache needs float32 scales [num_blocks, 2, num_kv_heads]")
     index = cache.get_device()
-    for name, t in rows.items():
-        if t.shape != rows_shape:
-            raise ValueError("%s must be %s" % (name, list(rows_shape)))
-    for name, (t, n) in lists.items():
-        if t.shape != (n,):
-            raise ValueError("%s must be [%d]" % (name, n))
-        rows = dict(rows, **{name: t})
-    for name, t in dict(rows, block_tables=tables).items():
-        if t.get_device() != index:
-            raise ValueError("%s is on %s, the cache on another device" % (name, t.device))
+    code = _DTYPES.get(act_dtype)
+    if code is None:
+        raise TypeError("unsupported dtype %s" % act_dtype)
+    return (_Cache(_dev(cache, "cache"), nb, hkv, bs, d, code, KV_INT8_BLOCK, _at(scales, torch.float32, index, "scales")),
+            index, hkv, bs, d)
 
 
-def _int8_out(cache, out, lse, shape, workspace=None):
-    """Checks of the tensors that an attention call over an INT8 cache writes."""
-    index = cache.get_device()
-    for name, t, want in (("out", out, shape), ("lse", lse, shape[:2]), ("workspace", workspace, None)):
-        if t is None:
-            continue
-        if t.get_device() != index:
-            raise ValueError("%s is on %s, the cache on another device" % (name, t.device))
-        if want is not None and tuple(t.shape) != tuple(want):
-            raise ValueError("%s must be %s" % (name, list(want)))
-    if lse is not None and lse.dtype != _torch().float32:
-        raise TypeError("lse must be float32")
+def _list(t, n, index, name):
+    """Pointer of an int32 list of n entries."""
+    if t.shape != (n,):
+        raise ValueError("%s must be [%d]" % (name, n))
+    return _at(t, _torch_module.int32, index, name)
+
+
+def _rows_at(t, shape, dtype, index, name):
+    """Pointer of a contiguous tensor of this shape."""
+    if t.shape != shape:
+        raise ValueError("%s must be %s" % (name, list(shape)))
+    return _at(t, dtype, index, name)
+
+
+@functools.lru_cache(maxsize=256)
+def _workspace_bytes(index, *sizes):
+    """decode_workspace_size with device `index` current (a function of the sizes and of the device's SMs)."""
+    return _on_device(index, load_library().pkv_decode_workspace_size, *sizes)
+
+
+def _int8_attention(name, cache, q, block_tables, context_lens, scale, workspace, out, out_dtype, lse, stream, scales,
+                    num_splits=None, cu_q_lens=None, max_q_len=0, causal=True, k_new=None, v_new=None):
+    """The attention calls over an INT8 cache: cu_q_lens None, one query row a sequence; num_splits None, a call without a
+    workspace."""
+    lib = load_library()
+    torch = _torch()
+    dtype = q.dtype
+    c, index, hkv, bs, d = _int8_cache(cache, scales, dtype)
+    total, hq, _ = q.shape
+    batch, mb = block_tables.shape
+    qp = _rows_at(q, (total if cu_q_lens is not None else batch, hq, d), dtype, index, "q")
+    bp = _at(block_tables, torch.int32, index, "block_tables")
+    cp = _list(context_lens, batch, index, "context_lens")
+    lp = None if lse is None else _rows_at(lse, (total, hq), torch.float32, index, "lse")
+    if out is None:
+        out = _new(q, (total, hq, d), out_dtype or dtype, stream)
+        op = out.data_ptr()
+    else:
+        op = _rows_at(out, (total, hq, d), out.dtype, index, "out")
+    oc = _dtype_code(out.dtype)
+    scale = (1.0 / math.sqrt(d)) if scale is None else float(scale)
+    wp, wb = None, 0
+    if num_splits is not None and name != "pkv_paged_attn_decode_noalloc":
+        if workspace is None:
+            wb = _workspace_bytes(index, batch, hq, hkv, d, bs, mb, num_splits)
+            if wb > 0:
+                workspace = _new(q, (wb,), torch.uint8, stream)
+                wp = workspace.data_ptr()
+        else:
+            wp, wb = _at(workspace, workspace.dtype, index, "workspace"), workspace.nbytes
+    st = _stream(stream, index)
+    if name == "pkv_paged_attn_decode":
+        args = (c, qp, hq, bp, cp, batch, mb, scale, num_splits, wp, wb, op, oc, lp, st)
+    elif name == "pkv_paged_attn_decode_step":
+        row = (batch, hkv, d)
+        args = (c, qp, hq, bp, cp, batch, mb, scale, num_splits, wp, wb, op, oc, lp, _rows_at(k_new, row, dtype, index, "k_new"),
+                _rows_at(v_new, row, dtype, index, "v_new"), st)
+    elif name == "pkv_paged_attn_decode_noalloc":
+        args = (c, qp, hq, bp, cp, batch, mb, scale, num_splits, op, oc, lp, st)
+    else:
+        up = _list(cu_q_lens, batch + 1, index, "cu_q_lens")
+        args = (c, qp, hq, up, cp, bp, batch, mb, total, int(max_q_len), scale, 1 if causal else 0)
+        args += (op, oc, lp, st) if name == "pkv_paged_attn_prefill" else (num_splits, wp, wb, op, oc, lp, st)
+    _check(_on_device(index, getattr(lib, name), *args), name)
+    return out
 
 
 def kv_cache_append(cache, k_new, v_new, cu_new_lens, ctx_before, block_tables, stream=None, scales=None) -> None:
@@ -294,11 +347,17 @@ def kv_cache_append(cache, k_new, v_new, cu_new_lens, ctx_before, block_tables, 
     lib = load_library()
     if k_new.dtype != v_new.dtype or k_new.shape != v_new.shape:
         raise TypeError("k_new / v_new must match each other")
-    c = _cache_struct(cache, k_new.dtype, scales)
     batch, mb = block_tables.shape
-    if c.format == KV_INT8_BLOCK:
-        _int8_args(cache, {"k_new": k_new, "v_new": v_new}, (k_new.shape[0], c.num_kv_heads, c.head_dim), batch, block_tables,
-                   {"cu_new_lens": (cu_new_lens, batch + 1), "ctx_before": (ctx_before, batch)})
+    if cache.dtype is _torch().int8:
+        dtype, total = k_new.dtype, k_new.shape[0]
+        c, index, hkv, _, d = _int8_cache(cache, scales, dtype)
+        _check(_on_device(index, lib.pkv_kv_cache_append, c, _rows_at(k_new, (total, hkv, d), dtype, index, "k_new"),
+                          _rows_at(v_new, (total, hkv, d), dtype, index, "v_new"),
+                          _list(cu_new_lens, batch + 1, index, "cu_new_lens"), _list(ctx_before, batch, index, "ctx_before"),
+                          _at(block_tables, _torch_module.int32, index, "block_tables"), batch, mb, total,
+                          _stream(stream, index)), "pkv_kv_cache_append")
+        return
+    c = _cache_struct(cache, k_new.dtype, scales)
     index = cache.get_device()
     _check(_on_device(index, lib.pkv_kv_cache_append, c, _dev(k_new, "k_new"), _dev(v_new, "v_new"),
                       _i32(cu_new_lens, "cu_new_lens"), _i32(ctx_before, "ctx_before"), _i32(block_tables, "block_tables"),
@@ -321,14 +380,13 @@ def paged_attn_decode(cache, q, block_tables, context_lens, scale: Optional[floa
                       workspace=None, out=None, out_dtype=None, lse=None, stream=None, scales=None):
     """One query per sequence ([B, Hq, D]) against its paged context. Returns `out`."""
     torch = _torch()
+    if cache.dtype is torch.int8:
+        return _int8_attention("pkv_paged_attn_decode", cache, q, block_tables, context_lens, scale, workspace, out, out_dtype,
+                               lse, stream, scales, int(num_splits))
     lib = load_library()
     c = _cache_struct(cache, q.dtype, scales)
     batch, hq, d = q.shape
     mb = block_tables.shape[1]
-    if c.format == KV_INT8_BLOCK:
-        _int8_args(cache, {"q": q}, (block_tables.shape[0], hq, c.head_dim), batch, block_tables,
-                   {"context_lens": (context_lens, batch)})
-        _int8_out(cache, out, lse, q.shape, workspace)
     index = cache.get_device()
     if out is None:
         out = _new(q, (batch, hq, d), out_dtype or q.dtype, stream)
@@ -351,6 +409,9 @@ def paged_attn_decode_step(cache, q, block_tables, context_lens, k_new, v_new, s
     """One decode step: paged_attn_decode over context_lens[b] cached tokens, and the step's new
     token (k_new / v_new [B, Hkv, D]) written at position context_lens[b]. Returns `out`."""
     torch = _torch()
+    if cache.dtype is torch.int8:
+        return _int8_attention("pkv_paged_attn_decode_step", cache, q, block_tables, context_lens, scale, workspace, out,
+                               out_dtype, lse, stream, scales, int(num_splits), k_new=k_new, v_new=v_new)
     lib = load_library()
     if k_new.dtype != q.dtype or v_new.dtype != q.dtype or k_new.shape != v_new.shape:
         raise TypeError("k_new / v_new must match each other and q's dtype")
@@ -359,11 +420,6 @@ def paged_attn_decode_step(cache, q, block_tables, context_lens, k_new, v_new, s
     if tuple(k_new.shape) != (batch, cache.shape[2], d):
         raise ValueError("k_new / v_new must be [batch, num_kv_heads, head_dim]")
     mb = block_tables.shape[1]
-    if c.format == KV_INT8_BLOCK:
-        _int8_args(cache, {"q": q}, (block_tables.shape[0], hq, c.head_dim), batch, block_tables,
-                   {"context_lens": (context_lens, batch)})
-        _int8_args(cache, {"k_new": k_new, "v_new": v_new}, k_new.shape, batch, block_tables, {})
-        _int8_out(cache, out, lse, q.shape, workspace)
     index = cache.get_device()
     if out is None:
         out = _new(q, (batch, hq, d), out_dtype or q.dtype, stream)
@@ -389,14 +445,13 @@ def paged_attn_decode_noalloc(cache, q, block_tables, context_lens, scale: Optio
     (PKV_ERR_WORKSPACE). Calls sharing a device must not overlap on the GPU. Returns `out`
     (allocated here with PyTorch only when the caller passes none)."""
     torch = _torch()
+    if cache.dtype is torch.int8:
+        return _int8_attention("pkv_paged_attn_decode_noalloc", cache, q, block_tables, context_lens, scale, None, out,
+                               out_dtype, lse, stream, scales, int(num_splits))
     lib = load_library()
     c = _cache_struct(cache, q.dtype, scales)
     batch, hq, d = q.shape
     mb = block_tables.shape[1]
-    if c.format == KV_INT8_BLOCK:
-        _int8_args(cache, {"q": q}, (block_tables.shape[0], hq, c.head_dim), batch, block_tables,
-                   {"context_lens": (context_lens, batch)})
-        _int8_out(cache, out, lse, q.shape)
     index = cache.get_device()
     if out is None:
         out = _new(q, (batch, hq, d), out_dtype or q.dtype, stream)
@@ -415,14 +470,13 @@ def paged_attn_prefill(cache, q, cu_q_lens, context_lens, block_tables, max_q_le
     (the chunk's own K/V already appended). Returns `out`. An FP8 cache (pass `scales`) needs
     head_dim 128; with head_dim 64 it raises PkvError (PKV_ERR_UNSUPPORTED)."""
     torch = _torch()
+    if cache.dtype is torch.int8:
+        return _int8_attention("pkv_paged_attn_prefill", cache, q, block_tables, context_lens, scale, None, out, out_dtype, lse,
+                               stream, scales, None, cu_q_lens, max_q_len, causal)
     lib = load_library()
     c = _cache_struct(cache, q.dtype, scales)
     total_q, hq, d = q.shape
     batch, mb = block_tables.shape
-    if c.format == KV_INT8_BLOCK:
-        _int8_args(cache, {"q": q}, (total_q, hq, c.head_dim), batch, block_tables,
-                   {"cu_q_lens": (cu_q_lens, batch + 1), "context_lens": (context_lens, batch)})
-        _int8_out(cache, out, lse, q.shape)
     index = cache.get_device()
     if out is None:
         out = _new(q, (total_q, hq, d), out_dtype or q.dtype, stream)
@@ -441,14 +495,13 @@ def paged_attn_mixed(cache, q, cu_q_lens, context_lens, block_tables, max_q_len:
     """One call over a batch mixing decode rows (q_len 1) and prefill chunks (q_len > 1):
     q [sum q_len, Hq, D], rows by cu_q_lens. Returns `out`."""
     torch = _torch()
+    if cache.dtype is torch.int8:
+        return _int8_attention("pkv_paged_attn_mixed", cache, q, block_tables, context_lens, scale, workspace, out, out_dtype,
+                               lse, stream, scales, int(num_splits), cu_q_lens, max_q_len, causal)
     lib = load_library()
     c = _cache_struct(cache, q.dtype, scales)
     total_q, hq, d = q.shape
     batch, mb = block_tables.shape
-    if c.format == KV_INT8_BLOCK:
-        _int8_args(cache, {"q": q}, (total_q, hq, c.head_dim), batch, block_tables,
-                   {"cu_q_lens": (cu_q_lens, batch + 1), "context_lens": (context_lens, batch)})
-        _int8_out(cache, out, lse, q.shape, workspace)
     index = cache.get_device()
     if out is None:
         out = _new(q, (total_q, hq, d), out_dtype or q.dtype, stream)

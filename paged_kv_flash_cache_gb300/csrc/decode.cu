@@ -635,11 +635,6 @@ __global__ void __launch_bounds__(256) combine_kernel(CombineArgs a) {
     for (int s = lane; s < S; s += 32) M = fmaxf(M, pl[s]);
 #pragma unroll
     for (int o = 16; o > 0; o >>= 1) M = fmaxf(M, __shfl_xor_sync(0xffffffffu, M, o));
-    if (a.nan_lse && M == -INFINITY) {  // (the maximum passes over NaN: they have to reach the sums)
-        bool nan = false;
-        for (int s = lane; s < S; s += 32) nan = nan || pl[s] != pl[s];
-        if (__any_sync(0xffffffffu, nan)) M = 0.f;
-    }
     float o_acc[kPer];
 #pragma unroll
     for (int j = 0; j < kPer; ++j) o_acc[j] = 0.f;
@@ -680,8 +675,7 @@ __global__ void __launch_bounds__(256) combine_kernel(CombineArgs a) {
 #pragma unroll
     for (int j = 0; j < kPer; ++j) o_acc[j] *= inv;
     store_out_vec<kPer>(a.out, out_row * D + lane * kPer, o_acc, a.out_dtype);
-    if (lane == 0 && a.lse)
-        a.lse[out_row] = wsum > 0.f ? M + logf(wsum) : a.nan_lse && wsum != wsum ? wsum : -INFINITY;
+    if (lane == 0 && a.lse) a.lse[out_row] = wsum > 0.f ? M + logf(wsum) : -INFINITY;
 }
 
 template <typename Tag, int D, int G, bool FP8>

@@ -167,9 +167,9 @@ __device__ __forceinline__ void append_step_rows(const DecodeArgs &a, int lane) 
 // (M + log2 sum w l) ln 2 -- writes the final output of a single-split context or the split's
 // partial, and frees the buffer on mempty[i]. NB buffers (1 or 2) take turns; unit id -1 ends the loop. Lane g
 // finds the weights of head g (all heads at once); then each head's output is D / 32 consecutive
-// dims per lane, read and written as vectors. NAN_LSE: a sum that is NaN gives a NaN lse (else -inf). Returns
-// false if a wait gave up (the error word is set).
-template <int D, int G, int W, int NB = 2, bool NAN_LSE = false>
+// dims per lane, read and written as vectors. Returns false if a wait gave up (the error word is
+// set).
+template <int D, int G, int W, int NB = 2>
 __device__ __forceinline__ bool merge_warp_loop(const DecodeArgs &a, const UnitTable &ut, const float *merge,
                                                 size_t buf_floats, uint64_t *mfull, uint64_t *mempty,
                                                 const int *merge_unit, volatile int *abort_flag, int lane) {
@@ -213,8 +213,7 @@ __device__ __forceinline__ bool merge_warp_loop(const DecodeArgs &a, const UnitT
             }
             const float lsum = tree_sum<W>(lt);
             inv_l = lsum > 0.f ? 1.f / lsum : 0.f;
-            float lse_v = lsum > 0.f ? (M + log2f(lsum)) * kLn2 : -INFINITY;
-            if (NAN_LSE && lsum != lsum) lse_v = lsum;
+            const float lse_v = lsum > 0.f ? (M + log2f(lsum)) * kLn2 : -INFINITY;
             if (splits == 1) {
                 if (a.lse) a.lse[orow0 + lane] = lse_v;
             } else {

@@ -12,14 +12,14 @@
 // FP32 scores. The V scales enter the weights, which go into the product relative to their tile's largest, as an f16
 // part and its remainder: the output's rounding is the only 16-bit one on the path, however small weights and scales are.
 //
-// Structure (persistent, two CTAs an SM). A unit is (sequence, KV head's query group, split); tile j (32 tokens) of a unit
+// Structure (persistent, three CTAs an SM of four warps). A unit is (sequence, KV head's query group, split); tile j (32 tokens) of a unit
 // is warp j % W's. Every warp feeds itself: it has a ring of its own and sends for the tile that goes into a slot as
 // soon as it has read the slot's last one, so no warp waits for another one and there is no producer to fall behind
 // (with one, 0.131 ms on the 7B-like batch, 0.111 with three quarters of the arithmetic left out). A tile arrives in page
 // slices of min(bs, 32) rows, each one 5-D TMA box of its K rows and its V rows; a slice lies in one page, whose scales
 // come beside it by 4-byte asynchronous copies on the same mbarrier. The page ids of the tile after are loaded a tile
-// ahead. The two blocks of 16 tokens of a tile are two independent chains of ldmatrix, conversion and mma. The last
-// warp merges the others' rows and writes the output or the split's partial.
+// ahead. The two blocks of 16 tokens of a tile are two independent chains of ldmatrix, conversion and mma. At the
+// end of a unit the warps merge their rows, a head each, and write the output or the split's partial.
 //
 // Operand layouts. ldmatrix (.b16) hands lane (gid, tig) the codes of dims 4 tig .. 4 tig + 3 of a 16-dim chunk: the
 // k slots of the A fragment are the permutation {2tig, 2tig+1, 2tig+8, 2tig+9} -> {4tig .. 4tig+3}, and q's B fragment
@@ -38,9 +38,8 @@
 namespace pkv {
 namespace {
 
-constexpr int kWarps = 4;  // consumer warps
-constexpr int kMergeWarp = kWarps;
-constexpr int kThreads = (kWarps + 1) * 32;
+constexpr int kWarps = 4;
+constexpr int kThreads = kWarps * 32;
 constexpr int kTile = 32;  // tokens of a tile
 constexpr int kCtasPerSm = 3;
 constexpr float kRescale = 4.0f;  // lazy rescale threshold (log2 units)
@@ -48,16 +47,16 @@ constexpr float kWeight = 2048.0f;  // weights, at most 2^kRescale, go into the 
 
 template <int D, int G>
 struct Int8Layout {
-    // slots of a warp's ring: what two CTAs an SM leave room for beside their merge buffers and unit tables
-    static constexpr int kStages = D == 64 ? 4 : 2;
-    static constexpr int kMergeBufs = 1;
+    // slots of a warp's ring: what three CTAs an SM (two for more than four heads) leave room for beside merge rows and
+    // unit tables
+    static constexpr int kStages = D == 64 ? (G > 4 ? 5 : 4) : (G > 4 ? 2 : 2);
     static constexpr uint32_t kStageBytes = 2 * kTile * D;  // per slice: br K rows, br V rows of D bytes
-    static constexpr uint32_t kScaleOffset = kWarps * kStages * kStageBytes;             // [kWarps][kStages][4] (K, V)
+    static constexpr uint32_t kScaleOffset = kWarps * kStages * kStageBytes;  // [kWarps][kStages][4] (K, V)
     static constexpr uint32_t kBarOffset = kScaleOffset + kWarps * kStages * 32;
-    // full per slot, merge full / empty, then the abort flag and the merge buffers' units
-    static constexpr uint32_t kMergeOffset = (kBarOffset + (kWarps * kStages + 2 * kMergeBufs) * 8 + 32 + 15) / 16 * 16;
+    // full per slot, rows written, rows read, then the abort flag
+    static constexpr uint32_t kMergeOffset = (kBarOffset + (kWarps * kStages + 2) * 8 + 16 + 15) / 16 * 16;
     static constexpr uint32_t kMergeFloats = kWarps * G * kMergeRow<D>;
-    static constexpr uint32_t kIntsOffset = kMergeOffset + kMergeBufs * kMergeFloats * 4;
+    static constexpr uint32_t kIntsOffset = kMergeOffset + kMergeFloats * 4;
     static size_t smem_bytes(int batch, int s_max) {
         return kIntsOffset + unit_table_ints(batch, s_max) * 4 + 1024;  // + 1024-byte alignment slack
     }
@@ -94,21 +93,64 @@ __device__ __forceinline__ void cp_async_arrive(uint64_t *bar) {
     asm volatile("cp.async.mbarrier.arrive.noinc.shared.b64 [%0];" ::"r"(smem_addr(bar)) : "memory");
 }
 
+// The unit tables. For small batches straight from their definitions, a thread an entry: first[s] = sum of min(splits, s)
+// over the sequences, ord by counting the sequences in front (2 us less a launch than decode_scan_units' scans, whose
+// latency a single request waits for).
+template <int kThreads>
+__device__ __forceinline__ int scan_units(const DecodeArgs &a, const UnitTable &t) {
+    const int S = a.s_max, cap = a.max_blocks_per_seq * a.cache.block_size;
+    if (a.auto_chunk || a.batch > kThreads || (long long)a.batch * (S / kThreads + 1) > 128)
+        return decode_scan_units<kThreads>(a, t);
+    const int tid = threadIdx.x;
+    int len = 0, k = 0;
+    if (tid < a.batch) {
+        len = __ldg(a.context_lens + tid);
+        int qrow = tid;
+        bool mine = true;
+        if (a.cu_q_lens) {  // mixed batch: only single-row sequences are decoded here
+            qrow = __ldg(a.cu_q_lens + tid);
+            mine = __ldg(a.cu_q_lens + tid + 1) - qrow == 1;
+        }
+        if (len < 0 || len > cap) {
+            set_error(a.err, kErrDeviceRange);
+            len = len < 0 ? 0 : cap;
+        }
+        if (!mine) len = 0;
+        k = (len + a.chunk - 1) / a.chunk;
+        t.lens[tid] = len;
+        t.qrow[tid] = qrow;
+        t.ord[tid] = k;
+    }
+    if (tid == 0) t.misc[0] = a.chunk;
+    __syncthreads();
+    int rank = 0;
+    if (tid < a.batch)
+        for (int j = 0; j < a.batch; ++j) rank += t.ord[j] > k || (t.ord[j] == k && j < tid) ? 1 : 0;
+    for (int s = tid; s <= S; s += kThreads) {
+        int f = 0;
+        for (int j = 0; j < a.batch; ++j) f += min(t.ord[j], s);
+        t.first[s] = f;
+    }
+    __syncthreads();
+    if (tid < a.batch) t.ord[rank] = tid;
+    __syncthreads();
+    return t.first[S] * a.cache.num_kv_heads * a.head_groups;
+}
+
 template <int D, int G>
 __global__ void __launch_bounds__(kThreads, kCtasPerSm)
     decode_int8_kernel(const __grid_constant__ CUtensorMap tm, DecodeArgs a) {
     using L = Int8Layout<D, G>;
-    constexpr int S = L::kStages, NB = L::kMergeBufs;
+    constexpr int S = L::kStages;
     constexpr int kChunks = D / 16;    // 16-dim chunks: k-steps of q.K^T, m-tiles of O^T
     constexpr bool kPacked = G <= 4;   // weights and their remainders side by side in one mma
     constexpr int kLanesFull = 4;      // lanes that copy scales: slices of a tile at most
     extern __shared__ uint8_t smem_raw[];
     uint8_t *smem = smem_raw + ((1024u - (smem_addr(smem_raw) & 1023u)) & 1023u);
     uint64_t *full = reinterpret_cast<uint64_t *>(smem + L::kBarOffset);  // [kWarps][S]
-    uint64_t *mfull = full + kWarps * S;  // [NB] the warps' rows of a unit are in buffer i
-    uint64_t *mempty = mfull + NB;        // [NB] the merge warp has read buffer i
-    volatile int *abort_flag = reinterpret_cast<volatile int *>(mempty + NB);
-    int *merge_unit = reinterpret_cast<int *>(mempty + NB) + 4;  // [NB] unit of each merge buffer, -1: end
+    uint64_t *written = full + kWarps * S;  // the warps' rows of a unit are in the merge buffer
+    uint64_t *read = written + 1;           // and have been merged
+    volatile int *abort_flag = reinterpret_cast<volatile int *>(read + 1);
     float *merge = reinterpret_cast<float *>(smem + L::kMergeOffset);
     const UnitTable ut = unit_table(reinterpret_cast<int *>(smem + L::kIntsOffset), a.batch, a.s_max);
 
@@ -120,25 +162,15 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm)
 
     if (tid == 0) {
         for (int i = 0; i < kWarps * S; ++i) mbar_init(&full[i], 1 + kLanesFull);  // the boxes' bytes; the scales
-        for (int i = 0; i < NB; ++i) {
-            mbar_init(&mfull[i], kWarps);
-            mbar_init(&mempty[i], 1);
-        }
+        mbar_init(written, kWarps);
+        mbar_init(read, kWarps);
         *abort_flag = 0;
         fence_barrier_init();
     }
     pdl_wait();  // lengths, tables, q and the cache may come from the previous kernel
-    const int num_units = decode_scan_units<kThreads>(a, ut);
+    const int num_units = scan_units<kThreads>(a, ut);
     const int chunk = ut.misc[0];  // the launch's split size
 
-    if (warp == kMergeWarp) {
-        // ====================================== merge warp ======================================
-        merge_warp_loop<D, G, kWarps, NB, true>(a, ut, merge, L::kMergeFloats, mfull, mempty, merge_unit, abort_flag, lane);
-        pdl_launch_dependents();
-        return;
-    }
-
-    // ===================================== consumer warps =====================================
     uint8_t *ring = smem + (size_t)warp * S * L::kStageBytes;
     float *scales = reinterpret_cast<float *>(smem + L::kScaleOffset) + warp * S * 8;  // [S][4][2]
     full += warp * S;
@@ -202,8 +234,7 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm)
     uint32_t taken = 0;       // tiles read
     int slot = 0;
     uint32_t phase = 0;
-    int mbuf = 0;  // merge buffer of the next unit
-    uint32_t mphase = 0;
+    uint32_t mphase = 0;  // of the merge buffer
     bool ok = true;
     // rows of the warp's ldmatrix in the slice layout (slice j starts at row 2 j br): 16 tokens a block
     int trow[2];
@@ -378,44 +409,172 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm)
                     o[mt][k].y += __shfl_xor_sync(0xffffffffu, o[mt][k].y, 2);
                 }
         }
-        if (!(ok = mbar_wait(&mempty[mbuf], mphase ^ 1u, abort_flag, a.err))) break;
-        float *rows = merge + (size_t)mbuf * L::kMergeFloats;
+        if (!(ok = mbar_wait(read, mphase ^ 1u, abort_flag, a.err))) break;
 #pragma unroll
         for (int jj = 0; jj < 2; ++jj) {
             const int g = 2 * tig + jj;
             if (g < G) {
-                float *row = rows + ((size_t)warp * G + g) * kMergeRow<D>;
+                float *row = merge + ((size_t)warp * G + g) * kMergeRow<D>;
 #pragma unroll
                 for (int mt = 0; mt < kChunks; ++mt)  // M slot gid: dim 2gid of the chunk; gid + 8: dim 2gid + 1
                     *reinterpret_cast<float2 *>(row + mt * 16 + 2 * gid) =
                         jj ? make_float2(o[mt][0].y, o[mt][1].y) : make_float2(o[mt][0].x, o[mt][1].x);
-                if (gid == 0) {
-                    // (every score NaN: the maximum passed over them; 0 lets the NaN sum through the merge)
-                    row[D] = m[jj] == -INFINITY && l[jj] != l[jj] ? 0.f : m[jj];
-                    row[D + 1] = l[jj];
-                }
+                // (every score NaN: the maximum passed over them; 0 lets the NaN sum through the merge)
+                if (gid == 0)
+                    *reinterpret_cast<float2 *>(row + D) =
+                        make_float2(m[jj] == -INFINITY && l[jj] != l[jj] ? 0.f : m[jj], l[jj]);
             }
         }
-        if (warp == 0 && lane == 0) merge_unit[mbuf] = u;
         __syncwarp();
-        if (lane == 0) mbar_arrive(&mfull[mbuf]);
-        if (++mbuf == NB) {
-            mbuf = 0;
-            mphase ^= 1u;
+        if (lane == 0) mbar_arrive(written);
+        if (!(ok = mbar_wait(written, mphase, abort_flag, a.err))) break;
+        // ---- the merge of head g by warp g % W: M = max m, weights 2^(m_w - M), out = sum w acc / sum w l ----
+        const int splits = (ut.lens[c.b] + chunk - 1) / chunk;
+        for (int g = warp; g < G; g += kWarps) {
+            const float *row = merge + (size_t)g * kMergeRow<D>;
+            float2 ml[kWarps];
+            float M = -INFINITY, sum = 0.f, acc[D / 32];
+#pragma unroll
+            for (int i = 0; i < kWarps; ++i) {
+                ml[i] = *reinterpret_cast<const float2 *>(row + (size_t)i * G * kMergeRow<D> + D);
+                M = fmaxf(M, ml[i].x);
+            }
+#pragma unroll
+            for (int v = 0; v < D / 32; ++v) acc[v] = 0.f;
+#pragma unroll
+            for (int i = 0; i < kWarps; ++i) {
+                const float wt = ml[i].x == -INFINITY ? 0.f : ex2f(ml[i].x - M);
+                sum = fmaf(wt, ml[i].y, sum);
+                const float *r = row + (size_t)i * G * kMergeRow<D> + lane * (D / 32);
+#pragma unroll
+                for (int v = 0; v < D / 32; ++v) acc[v] = fmaf(wt, r[v], acc[v]);
+            }
+            const float inv = 1.f / sum;  // (a unit has a token, so the sum is above 0, or NaN)
+#pragma unroll
+            for (int v = 0; v < D / 32; ++v) acc[v] *= inv;
+            const float lse = (M + __log2f(sum)) * kLn2;
+            const size_t head = (size_t)c.kvh * G + g;
+            if (splits == 1) {
+                const size_t row_o = (size_t)ut.qrow[c.b] * a.num_q_heads + head;
+                store_out_vec<D / 32>(a.out, row_o * D + lane * (D / 32), acc, a.out_dtype);
+                if (a.lse && lane == 0) a.lse[row_o] = lse;
+            } else {
+                const size_t row_p = ((size_t)c.b * a.num_q_heads + head) * a.s_max + c.split;
+                store_out_vec<D / 32>(a.part_o, row_p * D + lane * (D / 32), acc, 2);
+                if (lane == 0) a.part_lse[row_p] = lse;
+            }
         }
+        __syncwarp();
+        if (lane == 0) mbar_arrive(read);
+        mphase ^= 1u;
     }
     if (!ok) {
         // let copies in flight land before the CTA exits (bounded)
         volatile int no_abort = 0;
         for (; taken < issued; ++taken) mbar_wait(&full[taken % S], (taken / S) & 1u, &no_abort, nullptr);
-        return;
     }
-    // end marker for the merge warp
-    if (mbar_wait(&mempty[mbuf], mphase ^ 1u, abort_flag, a.err)) {
-        if (warp == 0 && lane == 0) merge_unit[mbuf] = -1;
-        __syncwarp();
-        if (lane == 0) mbar_arrive(&mfull[mbuf]);
+    pdl_launch_dependents();
+}
+
+// (volatile: issued where they stand, ahead of the arithmetic)
+__device__ __forceinline__ float ld_part(const float *p) {
+    float v;
+    asm volatile("ld.global.f32 %0, [%1];" : "=f"(v) : "l"(p));
+    return v;
+}
+__device__ __forceinline__ void ld_part_vec(const float *p, float (&v)[4]) {
+    asm volatile("ld.global.v4.f32 {%0,%1,%2,%3}, [%4];" : "=f"(v[0]), "=f"(v[1]), "=f"(v[2]), "=f"(v[3]) : "l"(p));
+}
+__device__ __forceinline__ void ld_part_vec(const float *p, float (&v)[2]) {
+    asm volatile("ld.global.v2.f32 {%0,%1}, [%2];" : "=f"(v[0]), "=f"(v[1]) : "l"(p));
+}
+
+// Log-sum-exp merge of the splits' partials: one CTA a row (sequence, query head), its warps a share of the splits each,
+// all of a warp's loads in flight at once (combine_kernel, a warp a row, takes 33 splits in five rounds of
+// loads: 3 us of a single request's 12).
+template <int D>
+__global__ void __launch_bounds__(128) merge_splits_kernel(CombineArgs a) {
+    constexpr int W = 4, V = D / 32, kBatch = 8;
+    __shared__ float part[W][D + 2];
+    const int row = blockIdx.x, warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const int b = row / a.rows_per_seq;
+    pdl_wait();  // lengths may come from the kernel before the split kernel, the partials come from it
+    const int len = max(__ldg(a.context_lens + b), 0);
+    const int S = min(len > 0 ? (len - 1) / a.chunk + 1 : 0, a.num_splits);
+    size_t out_row = row;
+    if (a.cu_q_lens) {  // mixed batch: rows of prefill chunks are not this kernel's
+        const int q0 = __ldg(a.cu_q_lens + b);
+        if (__ldg(a.cu_q_lens + b + 1) - q0 != 1) return;
+        out_row = (size_t)q0 * a.rows_per_seq + (row - b * a.rows_per_seq);
     }
+    if (S == 1) return;  // finished by the split kernel
+    const float *pl = a.part_lse + (size_t)row * a.num_splits;
+    const float *po = a.part_o + (size_t)row * a.num_splits * D + V * lane;
+    float M = -INFINITY, sum = 0.f, acc[V];
+#pragma unroll
+    for (int v = 0; v < V; ++v) acc[v] = 0.f;
+    for (int s0 = warp; s0 < S; s0 += W * kBatch) {
+        float x[kBatch][V], ls[kBatch];
+#pragma unroll
+        for (int i = 0; i < kBatch; ++i) {
+            const int s = s0 + i * W;
+            ls[i] = -INFINITY;
+            if (s < S) {
+                ls[i] = ld_part(pl + s);
+                ld_part_vec(po + (size_t)s * D, x[i]);
+            } else {
+#pragma unroll
+                for (int v = 0; v < V; ++v) x[i][v] = 0.f;
+            }
+        }
+        float m = M;
+#pragma unroll
+        for (int i = 0; i < kBatch; ++i) m = fmaxf(m, ls[i]);
+        // (every lse NaN so far: 0 lets them through)
+        const float mm = m == -INFINITY ? 0.f : m, al = M == -INFINITY ? 0.f : ex2f((M - mm) * kLog2e);
+        if (M != -INFINITY || sum != sum) {
+            sum *= M == -INFINITY ? 1.f : al;
+#pragma unroll
+            for (int v = 0; v < V; ++v) acc[v] *= M == -INFINITY ? 1.f : al;
+        }
+        M = m;
+#pragma unroll
+        for (int i = 0; i < kBatch; ++i) {
+            const float w = ls[i] == -INFINITY ? 0.f : ex2f((ls[i] - mm) * kLog2e);
+            sum += w;
+#pragma unroll
+            for (int v = 0; v < V; ++v) acc[v] = fmaf(w, x[i][v], acc[v]);
+        }
+    }
+#pragma unroll
+    for (int v = 0; v < V; ++v) part[warp][V * lane + v] = acc[v];
+    if (lane == 0) {
+        part[warp][D] = M;
+        part[warp][D + 1] = sum;
+    }
+    __syncthreads();
+    float top = -INFINITY, total = 0.f, wt[W];
+#pragma unroll
+    for (int i = 0; i < W; ++i) top = fmaxf(top, part[i][D]);
+    const float ref = top == -INFINITY ? 0.f : top;
+#pragma unroll
+    for (int i = 0; i < W; ++i) {
+        // (a warp without a maximum has a sum of 0, or one of NaN relative to 0)
+        wt[i] = part[i][D] == -INFINITY ? 1.f : ex2f((part[i][D] - ref) * kLog2e);
+        total = fmaf(wt[i], part[i][D + 1], total);
+    }
+    const float inv = S > 0 ? 1.f / total : 0.f;
+    if (threadIdx.x < D / 2) {
+        float o[2] = {0.f, 0.f};
+#pragma unroll
+        for (int i = 0; i < W; ++i)
+#pragma unroll
+            for (int v = 0; v < 2; ++v) o[v] = fmaf(wt[i], part[i][2 * threadIdx.x + v], o[v]);
+        o[0] *= inv;
+        o[1] *= inv;
+        store_out_vec<2>(a.out, out_row * D + 2 * threadIdx.x, o, a.out_dtype);
+    }
+    if (threadIdx.x == 0 && a.lse) a.lse[out_row] = S > 0 ? ref + logf(total) : -INFINITY;
     pdl_launch_dependents();
 }
 
@@ -432,11 +591,10 @@ cudaError_t launch_g(const DecodeArgs &a, int grid, cudaStream_t s) {
         if (e != cudaSuccess) return e;
         configured.set(dev);
     }
-    // two CTAs an SM when both fit in its shared memory (one CTA's maximum plus its 1 KB reserve, each less the
-    // reserve); a batch with large unit tables runs one
+    // as many CTAs an SM as fit in its shared memory (one CTA's maximum plus its 1 KB reserve, less a reserve each)
     const size_t smem = Int8Layout<D, G>::smem_bytes(a.batch, a.s_max);
-    const size_t cta_smem = ((size_t)device_info().max_smem + 1024) / kCtasPerSm - 1024;
-    const int ctas = smem <= cta_smem ? kCtasPerSm : 1;
+    int ctas = (int)(((size_t)device_info().max_smem + 1024) / (smem + 1024));
+    ctas = ctas > kCtasPerSm ? kCtasPerSm : ctas < 1 ? 1 : ctas;
     return launch_pdl(kern, dim3(grid * ctas), dim3(kThreads), smem, s, tm, a);
 }
 
@@ -456,6 +614,12 @@ cudaError_t launch_d(const DecodeArgs &a, int grid, cudaStream_t s) {
 }
 
 }  // namespace
+
+cudaError_t launch_merge_splits(const CombineArgs &a, cudaStream_t s) {
+    if (a.n_rows == 0) return cudaSuccess;
+    if (a.head_dim == 128) return launch_pdl(merge_splits_kernel<128>, dim3(a.n_rows), dim3(128), 0, s, a);
+    return launch_pdl(merge_splits_kernel<64>, dim3(a.n_rows), dim3(128), 0, s, a);
+}
 
 cudaError_t launch_decode_int8(const DecodeArgs &a, int grid, cudaStream_t s) {
     if (a.batch == 0) return cudaSuccess;

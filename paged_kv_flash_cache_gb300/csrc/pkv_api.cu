@@ -376,7 +376,6 @@ pkv_status decode_impl(const pkv_cache &cache, const void *q, int num_q_heads, c
         c.part_lse = d.part_lse;
         c.n_rows = nb * num_q_heads;
         c.num_splits = s_max;
-        c.nan_lse = int8 ? 1 : 0;
         c.head_dim = cache.head_dim;
         c.context_lens = d.context_lens;
         c.rows_per_seq = num_q_heads;
@@ -386,7 +385,7 @@ pkv_status decode_impl(const pkv_cache &cache, const void *q, int num_q_heads, c
         c.out = d.out;
         c.out_dtype = (int)out_dtype;
         c.lse = d.lse;
-        if (launch_combine(c, cs) != cudaSuccess) return PKV_ERR_CUDA;
+        if ((int8 ? launch_merge_splits(c, cs) : launch_combine(c, cs)) != cudaSuccess) return PKV_ERR_CUDA;
     }
     if (k_new && !fused_append) {
         AppendArgs ap;
@@ -451,7 +450,6 @@ pkv_status pkv_attn_combine(const float *partial_o, const float *partial_lse, in
     c.part_lse = partial_lse;
     c.n_rows = n_rows;
     c.num_splits = num_splits;
-    c.nan_lse = 0;
     c.head_dim = head_dim;
     c.context_lens = nullptr;
     c.cu_q_lens = nullptr;

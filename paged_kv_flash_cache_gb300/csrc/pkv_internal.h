@@ -161,7 +161,6 @@ struct TreeArgs {
 struct CombineArgs {
     const float *part_o, *part_lse;
     int n_rows, num_splits, head_dim;
-    int nan_lse;  // 1: a split's lse may be NaN, and then the row's is
     // When context_lens is set, row r = b * rows_per_seq + h uses ceil(len_b / chunk)
     // splits; rows with exactly one split were finished by the decode kernel.
     const int *context_lens;
@@ -266,6 +265,7 @@ cudaError_t encode_rows_map(const void *ptr, int bf16, long long rows, int cols,
 cudaError_t launch_decode_gqa(const DecodeArgs &a, int grid, cudaStream_t s);
 // Tensor-core (tcgen05) decode for a unit of up to 128 query heads of one KV head.
 cudaError_t launch_decode_tc(const DecodeArgs &a, int grid, cudaStream_t s);
+cudaError_t launch_merge_splits(const CombineArgs &a, cudaStream_t s);  // the INT8 decode's
 cudaError_t launch_decode_int8(const DecodeArgs &a, int grid, cudaStream_t s);
 cudaError_t launch_decode_fp8(const DecodeArgs &a, int grid, cudaStream_t s);
 cudaError_t launch_decode(const DecodeArgs &a, int grid, cudaStream_t s);
