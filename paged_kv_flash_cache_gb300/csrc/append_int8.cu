@@ -22,7 +22,7 @@
 namespace pkv {
 namespace {
 
-constexpr int kThreads = 256;
+constexpr int kThreads = 128;
 constexpr int kWarpsCta = kThreads / 32;
 constexpr int kVecs = 8;  // 16-byte vectors a lane holds: 4 KB of rows a warp
 
@@ -103,7 +103,7 @@ __device__ __forceinline__ int last_at_most(int batch, int lane, long long slot,
 
 // W warps a page of a head.
 template <int D, int W, typename Tag>
-__global__ void __launch_bounds__(kThreads) append_int8_kernel(AppendArgs a, long long tasks, int by_token) {
+__global__ void __launch_bounds__(kThreads, 6) append_int8_kernel(AppendArgs a, long long tasks, int by_token) {
     constexpr int kLanes = D / 8;               // lanes a row (16 bytes each)
     constexpr int kRowsLoad = 32 / kLanes;      // rows a load of the warp
     constexpr int kRowsWarp = kVecs * kRowsLoad;
@@ -132,15 +132,31 @@ __global__ void __launch_bounds__(kThreads) append_int8_kernel(AppendArgs a, lon
     } else {
         const int *cu = a.cu_new_lens;
         const int lb = a.log2_block_size;
-        b = by_token ? last_at_most(a.batch, lane, slot, [cu](int i) { return (long long)__ldg(cu + i); })
-                     : last_at_most(a.batch, lane, slot,
-                                    [cu, lb](int i) { return (long long)(__ldg(cu + i) >> lb) + 2ll * i; });
-        const int c0 = __ldg(cu + b), c1 = min(__ldg(cu + b + 1), a.num_new_tokens);
+        int c0, c1, ctx0;
+        if (a.batch <= 32) {  // everything in one round trip
+            const bool in = lane < a.batch;
+            c0 = in ? __ldg(cu + lane) : 0;
+            c1 = in ? __ldg(cu + lane + 1) : 0;
+            ctx0 = in ? __ldg(a.ctx_before + lane) : 0;
+            const long long base = by_token ? (long long)c0 : (long long)(c0 >> lb) + 2ll * lane;
+            b = __popc(__ballot_sync(0xffffffffu, in && (lane == 0 || base <= slot))) - 1;
+            c0 = __shfl_sync(0xffffffffu, c0, b);
+            c1 = __shfl_sync(0xffffffffu, c1, b);
+            ctx0 = __shfl_sync(0xffffffffu, ctx0, b);
+        } else {
+            b = by_token ? last_at_most(a.batch, lane, slot, [cu](int i) { return (long long)__ldg(cu + i); })
+                         : last_at_most(a.batch, lane, slot,
+                                        [cu, lb](int i) { return (long long)(__ldg(cu + i) >> lb) + 2ll * i; });
+            c0 = __ldg(cu + b);
+            c1 = __ldg(cu + b + 1);
+            ctx0 = __ldg(a.ctx_before + b);
+        }
+        c1 = min(c1, a.num_new_tokens);
         if (c0 < 0) {
             if (lane == 0) set_error(a.err, kErrDeviceRange);
             return;
         }
-        const long long ctx = __ldg(a.ctx_before + b);
+        const long long ctx = ctx0;
         end = ctx + (c1 - c0);
         if (by_token) {
             pos0 = ctx + (slot - c0);
@@ -274,8 +290,7 @@ cudaError_t launch_d(const AppendArgs &a, cudaStream_t s) {
     const int rows = by_token ? 1 : a.block_size, per_warp = kVecs * 256 / D;
     if (rows <= per_warp) return launch_w<D, 1, Tag>(a, slots, by_token, s);
     if (rows <= 2 * per_warp) return launch_w<D, 2, Tag>(a, slots, by_token, s);
-    if (rows <= 4 * per_warp) return launch_w<D, 4, Tag>(a, slots, by_token, s);
-    return launch_w<D, 8, Tag>(a, slots, by_token, s);
+    return launch_w<D, 4, Tag>(a, slots, by_token, s);
 }
 
 }  // namespace

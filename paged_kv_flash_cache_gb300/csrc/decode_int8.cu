@@ -166,6 +166,7 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm)
         mbar_init(read, kWarps);
         *abort_flag = 0;
         fence_barrier_init();
+        tc::prefetch_tensormap(&tm);
     }
     pdl_wait();  // lengths, tables, q and the cache may come from the previous kernel
     const int num_units = scan_units<kThreads>(a, ut);
@@ -222,7 +223,6 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm)
     };
     seek();
     page_ids();
-    if (lane == 0) tc::prefetch_tensormap(&tm);
     for (int i = 0; i < S; ++i) send(i);
 
     const int gid = lane >> 2, tig = lane & 3;
@@ -473,7 +473,7 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm)
         volatile int no_abort = 0;
         for (; taken < issued; ++taken) mbar_wait(&full[taken % S], (taken / S) & 1u, &no_abort, nullptr);
     }
-    pdl_launch_dependents();
+    pdl_launch_dependents();  // (at the start instead: one request 9.7 -> 9.4 us, but the mixed batch 37 -> 40)
 }
 
 // (volatile: issued where they stand, ahead of the arithmetic)
