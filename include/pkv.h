@@ -148,6 +148,10 @@ PKV_API pkv_status pkv_kv_cache_append(pkv_cache cache, const void *k_new, const
 PKV_API size_t pkv_decode_workspace_size(int batch, int num_q_heads, int num_kv_heads, int head_dim,
                                  int block_size, int max_blocks_per_seq, int num_splits);
 
+/* The same for an INT8 cache: never more, and 0 where the call needs none (few sequences, short tables). */
+PKV_API size_t pkv_decode_int8_workspace_size(int batch, int num_q_heads, int num_kv_heads, int head_dim,
+                                      int block_size, int max_blocks_per_seq, int num_splits);
+
 /* Tokens per split that pkv_paged_attn_decode uses for these sizes (a multiple of
  * 128, and at least capacity / 2048 so that a context has at most 2048 splits); a
  * context of L tokens is cut into ceil(L / chunk) splits.  With num_splits = 0 this is the

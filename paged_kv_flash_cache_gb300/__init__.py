@@ -48,7 +48,7 @@ F16, BF16, F32 = 0, 1, 2
 KV_NATIVE, KV_FP8_E4M3, KV_INT8_BLOCK = 0, 1, 2
 
 # Every symbol include/pkv.h declares.
-EXPORTS = ("pkv_kv_cache_append", "pkv_decode_workspace_size", "pkv_decode_split_tokens", "pkv_paged_attn_decode",
+EXPORTS = ("pkv_kv_cache_append", "pkv_decode_workspace_size", "pkv_decode_int8_workspace_size", "pkv_decode_split_tokens", "pkv_paged_attn_decode",
            "pkv_paged_attn_decode_step", "pkv_paged_attn_decode_noalloc", "pkv_paged_attn_prefill", "pkv_paged_attn_mixed", "pkv_attn_combine",
            "pkv_rope_append", "pkv_paged_attn_tree", "pkv_tree_workspace_size", "pkv_kv_cache_compact",
            "pkv_kv_cache_copy", "pkv_kv_cache_fork",
@@ -95,6 +95,8 @@ def load_library():
         lib.pkv_kv_cache_append.restype = I
         lib.pkv_decode_workspace_size.argtypes = [I, I, I, I, I, I, I]
         lib.pkv_decode_workspace_size.restype = Z
+        lib.pkv_decode_int8_workspace_size.argtypes = [I, I, I, I, I, I, I]
+        lib.pkv_decode_int8_workspace_size.restype = Z
         lib.pkv_decode_split_tokens.argtypes = [I, I, I, I, I, I, I]
         lib.pkv_decode_split_tokens.restype = I
         lib.pkv_paged_attn_decode.argtypes = [_Cache, P, I, P, P, I, I, F, I, P, Z, P, I, P, P]
@@ -288,9 +290,9 @@ def _rows_at(t, shape, dtype, index, name):
 
 
 @functools.lru_cache(maxsize=256)
-def _workspace_bytes(index, *sizes):
-    """decode_workspace_size with device `index` current (a function of the sizes and of the device's SMs)."""
-    return _on_device(index, load_library().pkv_decode_workspace_size, *sizes)
+def _int8_workspace(index, *sizes):
+    """The bytes of workspace with device `index` current (a function of the sizes and of the device's SMs)."""
+    return _on_device(index, load_library().pkv_decode_int8_workspace_size, *sizes)
 
 
 def _int8_attention(name, cache, q, block_tables, context_lens, scale, workspace, out, out_dtype, lse, stream, scales,
@@ -317,7 +319,7 @@ def _int8_attention(name, cache, q, block_tables, context_lens, scale, workspace
     wp, wb = None, 0
     if num_splits is not None and name != "pkv_paged_attn_decode_noalloc":
         if workspace is None:
-            wb = _workspace_bytes(index, batch, hq, hkv, d, bs, mb, num_splits)
+            wb = _int8_workspace(index, batch, hq, hkv, d, bs, mb, num_splits)
             if wb > 0:
                 workspace = _new(q, (wb,), torch.uint8, stream)
                 wp = workspace.data_ptr()

@@ -42,6 +42,7 @@ constexpr int kWarps = 4;
 constexpr int kThreads = kWarps * 32;
 constexpr int kTile = 32;  // tokens of a tile
 constexpr int kCtasPerSm = 3;
+constexpr int kClusterCtasPerSm = 2;  // clusters: CTAs an SM at most
 constexpr float kRescale = 4.0f;  // lazy rescale threshold (log2 units)
 constexpr float kWeight = 2048.0f;  // weights, at most 2^kRescale, go into the product times this: below f16's 65504
 
@@ -82,6 +83,11 @@ __device__ __forceinline__ float rcpf(float x) {
     float y;
     asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
     return y;
+}
+
+// A wait that gave up for one lane has for the warp: what follows needs its lanes together.
+__device__ __forceinline__ bool warp_wait(uint64_t *bar, uint32_t parity, volatile int *abort, int *err) {
+    return __all_sync(0xffffffffu, mbar_wait(bar, parity, abort, err));
 }
 
 // Four bytes global -> shared, asynchronously; and an arrival on `bar` once this thread's copies so far have landed
@@ -137,7 +143,36 @@ __device__ __forceinline__ int scan_units(const DecodeArgs &a, const UnitTable &
     return t.first[S] * a.cache.num_kv_heads * a.head_groups;
 }
 
-template <int D, int G>
+// ---- thread-block clusters: ranks, barrier, loads from another CTA's shared memory ----
+__device__ __forceinline__ uint32_t cluster_rank() {
+    uint32_t r;
+    asm("mov.u32 %0, %%cluster_ctarank;" : "=r"(r));
+    return r;
+}
+__device__ __forceinline__ uint32_t cluster_size() {
+    uint32_t r;
+    asm("mov.u32 %0, %%cluster_nctarank;" : "=r"(r));
+    return r;
+}
+__device__ __forceinline__ void cluster_barrier() {  // every thread of every CTA
+    __syncwarp();
+    asm volatile("barrier.cluster.arrive.release.aligned;\n\tbarrier.cluster.wait.acquire.aligned;" ::: "memory");
+}
+__device__ __forceinline__ uint32_t smem_of(const void *p, uint32_t rank) {
+    uint32_t a;
+    asm("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(a) : "r"(smem_addr(p)), "r"(rank));
+    return a;
+}
+__device__ __forceinline__ float2 ld_cluster2(uint32_t addr) {
+    float2 v;
+    asm volatile("ld.shared::cluster.v2.f32 {%0, %1}, [%2];" : "=f"(v.x), "=f"(v.y) : "r"(addr) : "memory");
+    return v;
+}
+
+// ONE: a cluster takes the whole context of one (sequence, KV head's query group), a run of keys a CTA, and merges it
+// over shared memory: no unit tables, partials or second launch. For launches that leave most CTAs with a unit or less
+// (decode_int8_cluster).
+template <int D, int G, bool ONE>
 __global__ void __launch_bounds__(kThreads, kCtasPerSm)
     decode_int8_kernel(const __grid_constant__ CUtensorMap tm, DecodeArgs a) {
     using L = Int8Layout<D, G>;
@@ -169,20 +204,46 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm)
         tc::prefetch_tensormap(&tm);
     }
     pdl_wait();  // lengths, tables, q and the cache may come from the previous kernel
-    const int num_units = scan_units<kThreads>(a, ut);
-    const int chunk = ut.misc[0];  // the launch's split size
+    UnitCursor one = {};
+    int num_units = 1, chunk = 0, first_unit = 0, one_row = 0;
+    bool one_mine = true;
+    if constexpr (ONE) {
+        const int n = cluster_size(), rank = cluster_rank(), id = blockIdx.x / n;
+        one.b = id / hu;
+        one.kvh = id - one.b * hu;
+        int len = __ldg(a.context_lens + one.b);
+        one_row = one.b;
+        if (a.cu_q_lens) {  // mixed batch: only single-row sequences are decoded here
+            one_row = __ldg(a.cu_q_lens + one.b);
+            one_mine = __ldg(a.cu_q_lens + one.b + 1) - one_row == 1;
+        }
+        const int cap = a.max_blocks_per_seq * bs;
+        if (len < 0 || len > cap) {
+            if (tid == 0) set_error(a.err, kErrDeviceRange);
+            len = len < 0 ? 0 : cap;
+        }
+        if (!one_mine) len = 0;
+        const int per = ((len + n - 1) / n + kTile - 1) / kTile * kTile;
+        one.t0 = min(rank * per, len);
+        one.t1 = min(one.t0 + per, len);
+        __syncthreads();  // (the barriers are initialised)
+    } else {
+        num_units = scan_units<kThreads>(a, ut);
+        chunk = ut.misc[0];  // the launch's split size
+        first_unit = blockIdx.x;
+    }
 
     uint8_t *ring = smem + (size_t)warp * S * L::kStageBytes;
     float *scales = reinterpret_cast<float *>(smem + L::kScaleOffset) + warp * S * 8;  // [S][4][2]
     full += warp * S;
     // ---- what is sent for: the next tile, its unit and the page ids of its slices (lane j: slice j) ----
     const uint64_t pol = l2_policy_evict_first();
-    int iu = blockIdx.x, its = 0, ipb = 0, ikv = 0;
+    int iu = first_unit, its = 0, ipb = 0, ikv = 0;
     uint32_t issued = 0;
     UnitCursor ic = {};
     auto seek = [&]() {  // from unit iu on, the first one with a tile of this warp; its page ids
         for (; iu < num_units; iu += gridDim.x) {
-            ic = unit_of(iu, ut, a.s_max, hu, chunk);
+            ic = ONE ? one : unit_of(iu, ut, a.s_max, hu, chunk);
             its = ic.t0 + warp * kTile;
             ikv = a.head_groups == 1 ? ic.kvh : ic.kvh / a.head_groups;  // the KV head of the unit
             if (its < ic.t1) break;
@@ -243,8 +304,8 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm)
         const int t = bl * 16 + (lane & 7) + 8 * (mi & 1);
         trow[bl] = t + (t & -br);
     }
-    for (int u = blockIdx.x; u < num_units; u += gridDim.x) {
-        const UnitCursor c = unit_of(u, ut, a.s_max, hu, chunk);
+    for (int u = first_unit; u < num_units; u += gridDim.x) {
+        const UnitCursor c = ONE ? one : unit_of(u, ut, a.s_max, hu, chunk);
         float m[2] = {-INFINITY, -INFINITY}, l[2] = {0.f, 0.f};
         float2 o[kChunks][2];
 #pragma unroll
@@ -252,7 +313,7 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm)
         const int first = c.t0 + warp * kTile;
         if (first < c.t1) {
             const int hq = kPacked ? gid & 3 : gid;  // head of this lane's column of the B fragment
-            const uint16_t *qr = qg + ((size_t)ut.qrow[c.b] * a.num_q_heads + (size_t)c.kvh * G + hq) * D + 4 * tig;
+            const uint16_t *qr = qg + ((size_t)(ONE ? one_row : ut.qrow[c.b]) * a.num_q_heads + (size_t)c.kvh * G + hq) * D + 4 * tig;
 #pragma unroll
             for (int kk = 0; kk < kChunks; ++kk) {
                 uint2 raw = make_uint2(0u, 0u);
@@ -270,7 +331,7 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm)
         }
         for (int ts = first; ts < c.t1; ts += kWarps * kTile) {
             const int n = min(kTile, c.t1 - ts);
-            if (!(ok = mbar_wait(&full[slot], phase, abort_flag, a.err))) break;
+            if (!(ok = warp_wait(&full[slot], phase, abort_flag, a.err))) break;
             const uint32_t aK = smem_addr(ring + (size_t)slot * L::kStageBytes), aV = aK + br * D;
             // scales of the four groups of 8 tokens (a group lies in one page)
             float sk[4], sv[4];
@@ -409,7 +470,7 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm)
                     o[mt][k].y += __shfl_xor_sync(0xffffffffu, o[mt][k].y, 2);
                 }
         }
-        if (!(ok = mbar_wait(read, mphase ^ 1u, abort_flag, a.err))) break;
+        if (!(ok = warp_wait(read, mphase ^ 1u, abort_flag, a.err))) break;
 #pragma unroll
         for (int jj = 0; jj < 2; ++jj) {
             const int g = 2 * tig + jj;
@@ -427,11 +488,11 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm)
         }
         __syncwarp();
         if (lane == 0) mbar_arrive(written);
-        if (!(ok = mbar_wait(written, mphase, abort_flag, a.err))) break;
+        if (!(ok = warp_wait(written, mphase, abort_flag, a.err))) break;
         // ---- the merge of head g by warp g % W: M = max m, weights 2^(m_w - M), out = sum w acc / sum w l ----
-        const int splits = (ut.lens[c.b] + chunk - 1) / chunk;
+        const int splits = ONE ? 1 : (ut.lens[c.b] + chunk - 1) / chunk;
         for (int g = warp; g < G; g += kWarps) {
-            const float *row = merge + (size_t)g * kMergeRow<D>;
+            float *row = merge + (size_t)g * kMergeRow<D>;
             float2 ml[kWarps];
             float M = -INFINITY, sum = 0.f, acc[D / 32];
 #pragma unroll
@@ -448,6 +509,13 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm)
                 const float *r = row + (size_t)i * G * kMergeRow<D> + lane * (D / 32);
 #pragma unroll
                 for (int v = 0; v < D / 32; ++v) acc[v] = fmaf(wt, r[v], acc[v]);
+            }
+            if constexpr (ONE) {  // the CTA's row, relative to M, over warp 0's
+                __syncwarp();
+#pragma unroll
+                for (int v = 0; v < D / 32; ++v) row[lane * (D / 32) + v] = acc[v];
+                if (lane == 0) *reinterpret_cast<float2 *>(row + D) = make_float2(M, sum);
+                continue;
             }
             const float inv = 1.f / sum;  // (a unit has a token, so the sum is above 0, or NaN)
 #pragma unroll
@@ -472,6 +540,51 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm)
         // let copies in flight land before the CTA exits (bounded)
         volatile int no_abort = 0;
         for (; taken < issued; ++taken) mbar_wait(&full[taken % S], (taken / S) & 1u, &no_abort, nullptr);
+    }
+    if constexpr (ONE) {
+        // ---- the cluster's rows: head g by warp g / n of CTA g % n; every CTA comes here, whatever its waits did ----
+        cluster_barrier();
+        const int n = cluster_size();
+        for (int g = warp * n + cluster_rank(); g < G; g += n * kWarps) {
+            const float *row = merge + (size_t)g * kMergeRow<D>;
+            const float2 ml = lane < n ? ld_cluster2(smem_of(row + D, lane)) : make_float2(-INFINITY, 0.f);
+            float M = ml.x;
+#pragma unroll
+            for (int i = 16; i > 0; i >>= 1) M = fmaxf(M, __shfl_xor_sync(0xffffffffu, M, i));
+            const float wt = ml.x == -INFINITY ? 0.f : ex2f(ml.x - M);
+            float sum = wt == 0.f ? 0.f : wt * ml.y;
+            float2 acc[D / 64];
+#pragma unroll
+            for (int v = 0; v < D / 64; ++v) acc[v] = make_float2(0.f, 0.f);
+            for (int i0 = 0; i0 < n; i0 += 4) {
+                float2 x[4][D / 64];
+#pragma unroll
+                for (int i = 0; i < 4; ++i)  // (n is 1, 2 or a multiple of 4)
+#pragma unroll
+                    for (int v = 0; v < D / 64; ++v)
+                        x[i][v] = ld_cluster2(smem_of(row + v * 64 + lane * 2, i0 + i < n ? i0 + i : i0));
+#pragma unroll
+                for (int i = 0; i < 4; ++i) {
+                    const float w = i0 + i < n ? __shfl_sync(0xffffffffu, wt, i0 + i) : 0.f;
+#pragma unroll
+                    for (int v = 0; v < D / 64; ++v) acc[v] = ffma2(make_float2(w, w), x[i][v], acc[v]);
+                }
+            }
+#pragma unroll
+            for (int i = 16; i > 0; i >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, i);
+            const bool empty = M == -INFINITY;  // an empty context
+            const float inv = empty ? 0.f : 1.f / sum;
+            const size_t row_o = (size_t)one_row * a.num_q_heads + (size_t)one.kvh * G + g;
+            if (ok && one_mine) {
+#pragma unroll
+                for (int v = 0; v < D / 64; ++v) {
+                    const float o2[2] = {acc[v].x * inv, acc[v].y * inv};
+                    store_out_vec<2>(a.out, row_o * D + v * 64 + lane * 2, o2, a.out_dtype);
+                }
+                if (a.lse && lane == 0) a.lse[row_o] = empty ? -INFINITY : (M + __log2f(sum)) * kLn2;
+            }
+        }
+        cluster_barrier();  // (no CTA leaves before its rows have been read)
     }
     pdl_launch_dependents();  // (at the start instead: one request 9.7 -> 9.4 us, but the mixed batch 37 -> 40)
 }
@@ -578,24 +691,47 @@ __global__ void __launch_bounds__(128) merge_splits_kernel(CombineArgs a) {
     pdl_launch_dependents();
 }
 
-template <int D, int G>
-cudaError_t launch_g(const DecodeArgs &a, int grid, cudaStream_t s) {
+template <int D, int G, bool ONE>
+cudaError_t launch_t(const DecodeArgs &a, int grid, cudaStream_t s) {
     CUtensorMap tm;
     cudaError_t e = encode_int8_map(a.cache, a.cache.block_size < kTile ? a.cache.block_size : kTile, 2, &tm);
     if (e != cudaSuccess) return e;
-    auto kern = decode_int8_kernel<D, G>;
+    auto kern = decode_int8_kernel<D, G, ONE>;
     static DeviceFlags configured;
     const int dev = device_info().device;
     if (!configured.test(dev)) {
         e = set_smem_attributes(kern, device_info().max_smem);
         if (e != cudaSuccess) return e;
+        if (ONE) e = cudaFuncSetAttribute(kern, cudaFuncAttributeNonPortableClusterSizeAllowed, 1);
+        if (e != cudaSuccess) return e;
         configured.set(dev);
+    }
+    if (ONE) {
+        cudaLaunchConfig_t cfg = {};
+        cfg.gridDim = dim3((unsigned)(a.batch * a.cache.num_kv_heads * a.head_groups * a.cluster));
+        cfg.blockDim = dim3(kThreads);
+        cfg.dynamicSmemBytes = Int8Layout<D, G>::smem_bytes(0, 0);
+        cfg.stream = s;
+        cudaLaunchAttribute attr[2];
+        attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+        attr[0].val.programmaticStreamSerializationAllowed = 1;
+        attr[1].id = cudaLaunchAttributeClusterDimension;
+        attr[1].val.clusterDim.x = (unsigned)a.cluster;
+        attr[1].val.clusterDim.y = attr[1].val.clusterDim.z = 1;
+        cfg.attrs = attr;
+        cfg.numAttrs = 2;
+        return cudaLaunchKernelEx(&cfg, kern, tm, a);
     }
     // as many CTAs an SM as fit in its shared memory (one CTA's maximum plus its 1 KB reserve, less a reserve each)
     const size_t smem = Int8Layout<D, G>::smem_bytes(a.batch, a.s_max);
     int ctas = (int)(((size_t)device_info().max_smem + 1024) / (smem + 1024));
     ctas = ctas > kCtasPerSm ? kCtasPerSm : ctas < 1 ? 1 : ctas;
     return launch_pdl(kern, dim3(grid * ctas), dim3(kThreads), smem, s, tm, a);
+}
+
+template <int D, int G>
+cudaError_t launch_g(const DecodeArgs &a, int grid, cudaStream_t s) {
+    return a.cluster > 0 ? launch_t<D, G, true>(a, grid, s) : launch_t<D, G, false>(a, grid, s);
 }
 
 template <int D>
@@ -614,6 +750,44 @@ cudaError_t launch_d(const DecodeArgs &a, int grid, cudaStream_t s) {
 }
 
 }  // namespace
+
+// CTAs of the cluster that takes a unit's whole context, 0: the split kernel and its merge. A cluster saves the unit tables,
+// the partials and the second launch, but has to leave SMs idle where the units times 16 are fewer. Measured against the
+// splits, 8 KV heads of 4 query heads: one sequence of 4096 tokens 7.8 us for 9.6, of 8192 10.5 for 11.5, of 16384
+// (not taken) 15.5 for 14.1; four of 4096 10.2 for 12.2, of 16384 26.1 for 29.2; 32 of 2048 25.5 for 28.4; 16 of 8192 47.6
+// for 47.2 (not taken: more units than CTAs at two an SM in clusters of one). Clusters of 16 only where they are alone on
+// their SMs: 16 units of 8192 tokens in 256 CTAs took 20.4 for 17.0.
+int decode_int8_cluster(int batch, int units_per_seq, long long capacity) {
+    const long long units = (long long)batch * units_per_seq;
+    for (int c = 16; c >= 1; c >>= 1)
+        if (units * c <= (long long)(c == 16 ? 1 : kClusterCtasPerSm) * device_info().num_sms)
+            return capacity <= (units * c <= device_info().num_sms ? 768ll : 4096ll) * c ? c : 0;
+    return 0;
+}
+
+// Tokens per split (a multiple of 128, 256 to 1024, and at most kDecodeMaxSplits splits): units are dealt round-robin
+// to the CTAs, so a launch takes about ceil(units / CTAs) times a unit's tokens and what a unit costs besides (150 tokens'
+// time), for contexts that fill the table but its last page. (4 sequences of 8192 tokens, 8 KV heads: 26 us with splits of
+// 128 tokens, 16 with 640.) With work for more rounds than four the contexts' own lengths matter more: 768 tokens, the best
+// for ragged batches (mixed serving batch 37 us; 384 tokens 40, 1024 43).
+int decode_int8_split(int batch, int units_per_seq, int block_size, long long capacity) {
+    const long long ctas = (long long)kCtasPerSm * device_info().num_sms;
+    const long long tokens = capacity > block_size ? capacity - block_size : capacity;
+    long long least = (capacity + kDecodeMaxSplits - 1) / kDecodeMaxSplits;
+    least = (least + 127) / 128 * 128;
+    if (least < 256) least = 256;
+    if (least <= 768 && (long long)batch * units_per_seq * ((tokens + 767) / 768) >= 4 * ctas) return 768;
+    long long best = least, best_cost = -1;
+    for (long long c = least; c <= (least > 1024 ? least : 1024); c += 128) {
+        const long long units = (long long)batch * units_per_seq * ((tokens + c - 1) / c);
+        const long long cost = (units + ctas - 1) / ctas * (c + 150);
+        if (best_cost < 0 || cost < best_cost) {
+            best_cost = cost;
+            best = c;
+        }
+    }
+    return (int)best;
+}
 
 cudaError_t launch_merge_splits(const CombineArgs &a, cudaStream_t s) {
     if (a.n_rows == 0) return cudaSuccess;

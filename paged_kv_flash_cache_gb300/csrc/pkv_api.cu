@@ -136,6 +136,26 @@ int split_tokens(int batch, int num_kv_heads, int block_size, int max_blocks_per
     return (int)(c < tile ? tile : c);
 }
 
+// Query heads of an INT8 decode's unit: the group or, above 8, its largest divisor up to 8.
+int int8_unit_heads(int group) {
+    int n = group;
+    for (int d = 8; n > 8; --d)
+        if (group % d == 0) n = d;
+    return n;
+}
+
+int int8_cluster(int batch, int num_q_heads, int num_kv_heads, long long capacity, int num_splits) {
+    if (num_splits > 0 || batch > decode_max_batch()) return 0;
+    return decode_int8_cluster(batch, num_q_heads / int8_unit_heads(num_q_heads / num_kv_heads), capacity);
+}
+
+// Tokens per split of a decode over an INT8 cache.
+int int8_split(int batch, int num_q_heads, int num_kv_heads, int block_size, int max_blocks_per_seq, int num_splits) {
+    if (num_splits > 0) return split_tokens(batch, num_kv_heads, block_size, max_blocks_per_seq, num_splits);
+    return decode_int8_split(batch, num_q_heads / int8_unit_heads(num_q_heads / num_kv_heads), block_size,
+                             (long long)max_blocks_per_seq * block_size);
+}
+
 }  // namespace
 
 const DeviceInfo &device_info() {
@@ -229,6 +249,18 @@ size_t pkv_decode_workspace_size(int batch, int num_q_heads, int num_kv_heads, i
     return partial_bytes(batch, num_q_heads, s_max, head_dim) + 16;
 }
 
+size_t pkv_decode_int8_workspace_size(int batch, int num_q_heads, int num_kv_heads, int head_dim, int block_size,
+                                      int max_blocks_per_seq, int num_splits) {
+    if (batch <= 0 || num_q_heads <= 0 || num_kv_heads <= 0 || num_q_heads % num_kv_heads != 0 || head_dim <= 0 ||
+        block_size <= 0 || max_blocks_per_seq <= 0)
+        return 0;
+    const long long cap = (long long)max_blocks_per_seq * block_size;
+    if (int8_cluster(batch, num_q_heads, num_kv_heads, cap, num_splits) > 0) return 0;
+    const int chunk = int8_split(batch, num_q_heads, num_kv_heads, block_size, max_blocks_per_seq, num_splits);
+    const long long s_max = (cap + chunk - 1) / chunk;
+    return s_max <= 1 ? 0 : partial_bytes(batch, num_q_heads, s_max, head_dim) + 16;
+}
+
 }  // extern "C"
 
 namespace pkv {
@@ -259,10 +291,12 @@ pkv_status decode_impl(const pkv_cache &cache, const void *q, int num_q_heads, c
     if (cap > (1ll << 30)) return PKV_ERR_UNSUPPORTED;
     DeviceSlot *s = slot();
     if (!s) return PKV_ERR_CUDA;
-    const int chunk = split_tokens(batch, cache.num_kv_heads, cache.block_size, max_blocks_per_seq, num_splits);
+    const int chunk = int8 ? int8_split(batch, num_q_heads, cache.num_kv_heads, cache.block_size, max_blocks_per_seq, num_splits)
+                           : split_tokens(batch, cache.num_kv_heads, cache.block_size, max_blocks_per_seq, num_splits);
     const int s_max = (int)((cap + chunk - 1) / chunk);
-    const size_t need = pkv_decode_workspace_size(batch, num_q_heads, cache.num_kv_heads, cache.head_dim,
-                                                  cache.block_size, max_blocks_per_seq, num_splits);
+    const int cluster = int8 ? int8_cluster(batch, num_q_heads, cache.num_kv_heads, cap, num_splits) : 0;
+    const size_t need = (int8 ? pkv_decode_int8_workspace_size : pkv_decode_workspace_size)(
+        batch, num_q_heads, cache.num_kv_heads, cache.head_dim, cache.block_size, max_blocks_per_seq, num_splits);
     if (need > 0 && (!workspace || workspace_bytes < need || !aligned16(workspace))) return PKV_ERR_WORKSPACE;
     DecodeArgs a;
     a.cache = view_of(cache);
@@ -280,6 +314,7 @@ pkv_status decode_impl(const pkv_cache &cache, const void *q, int num_q_heads, c
     a.q_rows = q_rows;
     a.s_max = s_max;
     a.stages = 0;  // set by the group kernel's launcher
+    a.cluster = cluster;
     // The kernel and the query heads of a unit (a KV head's group, or an equal share of it):
     //   FP8 cache: the FP8 kernels, at most 8 per unit;
     //   INT8 cache: mma.sync units of the group or, above 8 heads, of its largest divisor up to 8;
@@ -291,9 +326,7 @@ pkv_status decode_impl(const pkv_cache &cache, const void *q, int num_q_heads, c
     int per_unit;
     if (int8) {
         path = kInt8Tensor;
-        per_unit = group;
-        for (int d = 8; per_unit > 8; --d)
-            if (group % d == 0) per_unit = d;
+        per_unit = int8_unit_heads(group);
     } else if (fp8) {
         path = cache.head_dim == 128 ? kFp8Tensor : kCudaCores;
         per_unit = group < 8 ? group : 8;
@@ -370,6 +403,7 @@ pkv_status decode_impl(const pkv_cache &cache, const void *q, int num_q_heads, c
             default: le = launch_decode(d, grid, cs); break;
         }
         if (le != cudaSuccess) return PKV_ERR_CUDA;
+        if (cluster > 0) continue;  // (finished)
         // Rows that span several splits (and empty rows) are finished by the merge.
         CombineArgs c;
         c.part_o = d.part_o;

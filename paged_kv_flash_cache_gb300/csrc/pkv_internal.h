@@ -63,6 +63,7 @@ struct DecodeArgs {
     int out_dtype;
     float *lse;
     int *err;
+    int cluster;  // INT8 decode: CTAs of a cluster that takes a unit's whole context, or 0
     // Decode step on the kernels with a merge warp (a native cache on the CUDA-core and mma.sync
     // paths): the new token's K and V rows [batch, Hkv, D], which the merge warps write at
     // position context_lens[b] of each sequence before their first unit. nullptr: no append.
@@ -265,6 +266,8 @@ cudaError_t encode_rows_map(const void *ptr, int bf16, long long rows, int cols,
 cudaError_t launch_decode_gqa(const DecodeArgs &a, int grid, cudaStream_t s);
 // Tensor-core (tcgen05) decode for a unit of up to 128 query heads of one KV head.
 cudaError_t launch_decode_tc(const DecodeArgs &a, int grid, cudaStream_t s);
+int decode_int8_split(int batch, int units_per_seq, int block_size, long long capacity);
+int decode_int8_cluster(int batch, int units_per_seq, long long capacity);
 cudaError_t launch_merge_splits(const CombineArgs &a, cudaStream_t s);  // the INT8 decode's
 cudaError_t launch_decode_int8(const DecodeArgs &a, int grid, cudaStream_t s);
 cudaError_t launch_decode_fp8(const DecodeArgs &a, int grid, cudaStream_t s);

@@ -107,18 +107,27 @@ def run(lens, hq, heads, d, bs, dtype, seed, out_dtype=None, num_splits=0, sprea
     check(out, lse, ref, ref_lse, err, err_lse)
 
 
+@pytest.mark.parametrize("num_splits", [0, 1, 9])
 @pytest.mark.parametrize("d", [64, 128])
 @pytest.mark.parametrize("bs", [8, 16, 32, 64, 128, 512])
-def test_lengths(bs, d):
-    """Empty and one-token contexts, ones that end inside a page, a tile, a warp's share, a split."""
-    run([0, 1, bs - 1, bs, bs + 1, 31, 32, 33, 127, 129, 700, 1537], 4, 2, d, bs, "bf16", bs + d)
+def test_lengths(bs, d, num_splits):
+    """Empty and one-token contexts, ones that end inside a page, a tile, a warp's share, a split or a CTA's run."""
+    run([0, 1, bs - 1, bs, bs + 1, 31, 32, 33, 127, 129, 700, 1537], 4, 2, d, bs, "bf16", bs + d, num_splits=num_splits)
+
+
+@pytest.mark.parametrize("lens", [[5000], [1], [0], [17, 3000], [900, 0, 0, 33], [100] * 9, [2000] * 20, [600] * 40, [40] * 200])
+@pytest.mark.parametrize("hq,heads", [(4, 1), (8, 8), (7, 1), (16, 1)])
+def test_batches(lens, hq, heads):
+    """From one sequence to many: clusters of every size, and the splits."""
+    run(lens, hq, heads, 128, 16, "f16", len(lens) + hq)
 
 
 @pytest.mark.parametrize("hq,heads", [(1, 1), (4, 2), (6, 2), (4, 1), (10, 2), (6, 1), (21, 3), (8, 1), (9, 1), (13, 1), (32, 2),
                                       (24, 2), (34, 2), (32, 32)])
 @pytest.mark.parametrize("d", [64, 128])
-def test_groups(hq, heads, d):
-    run([300, 0, 45, 1000], hq, heads, d, 16, "f16", hq + d)
+@pytest.mark.parametrize("num_splits", [0, 3])
+def test_groups(hq, heads, d, num_splits):
+    run([300, 0, 45, 1000], hq, heads, d, 16, "f16", hq + d, num_splits=num_splits)
 
 
 @pytest.mark.parametrize("num_splits", [1, 2, 5, 40])
@@ -165,7 +174,7 @@ def test_what_is_not_a_number():
     scales[5], codes[4, :, :, 60:] = float("nan"), 127
     lens = torch.tensor([256, 256, 60, 200], dtype=torch.int32)
     q = torch.randn((4, 2, 64), generator=torch.Generator().manual_seed(1)).half()
-    for splits in (0, 1):
+    for splits in (0, 1, 2):
         lse = torch.empty((4, 2), device="cuda")
         out = pkv.paged_attn_decode(codes.cuda(), q.cuda(), tables.cuda(), lens.cuda(), lse=lse, num_splits=splits,
                                     scales=scales.cuda())
