@@ -761,7 +761,7 @@ int decode_int8_cluster(int batch, int units_per_seq, long long capacity) {
     const long long units = (long long)batch * units_per_seq;
     for (int c = 16; c >= 1; c >>= 1)
         if (units * c <= (long long)(c == 16 ? 1 : kClusterCtasPerSm) * device_info().num_sms)
-            return capacity <= (units * c <= device_info().num_sms ? 768ll : 4096ll) * c ? c : 0;
+            return capacity <= (units * c <= device_info().num_sms ? 640ll : 4096ll) * c ? c : 0;
     return 0;
 }
 

@@ -136,24 +136,36 @@ int split_tokens(int batch, int num_kv_heads, int block_size, int max_blocks_per
     return (int)(c < tile ? tile : c);
 }
 
-// Query heads of an INT8 decode's unit: the group or, above 8, its largest divisor up to 8.
-int int8_unit_heads(int group) {
+// How a decode over an INT8 cache runs: query heads of a unit, the cluster's CTAs (0: splits and a merge), tokens per split,
+// and whether the units are tcgen05's.
+//   few units and short tables: clusters (decode_int8_cluster), units of the group or, above 8 heads, of its largest
+//   divisor up to 8; more than 8 heads per KV head otherwise: tcgen05 units of the group or its largest divisor up to 128;
+//   else splits of mma.sync units.
+struct Int8Decode {
+    int unit_heads, cluster, chunk;
+    bool wide;
+};
+
+int largest_divisor(int group, int most) {
     int n = group;
-    for (int d = 8; n > 8; --d)
+    for (int d = most; n > most; --d)
         if (group % d == 0) n = d;
     return n;
 }
 
-int int8_cluster(int batch, int num_q_heads, int num_kv_heads, long long capacity, int num_splits) {
-    if (num_splits > 0 || batch > decode_max_batch()) return 0;
-    return decode_int8_cluster(batch, num_q_heads / int8_unit_heads(num_q_heads / num_kv_heads), capacity);
-}
-
-// Tokens per split of a decode over an INT8 cache.
-int int8_split(int batch, int num_q_heads, int num_kv_heads, int block_size, int max_blocks_per_seq, int num_splits) {
-    if (num_splits > 0) return split_tokens(batch, num_kv_heads, block_size, max_blocks_per_seq, num_splits);
-    return decode_int8_split(batch, num_q_heads / int8_unit_heads(num_q_heads / num_kv_heads), block_size,
-                             (long long)max_blocks_per_seq * block_size);
+Int8Decode int8_decode(int batch, int num_q_heads, int num_kv_heads, int block_size, int max_blocks_per_seq, int num_splits) {
+    const long long cap = (long long)max_blocks_per_seq * block_size;
+    const int group = num_q_heads / num_kv_heads;
+    Int8Decode d;
+    d.unit_heads = largest_divisor(group, 8);
+    d.cluster = num_splits > 0 || batch > decode_max_batch() ? 0 : decode_int8_cluster(batch, num_q_heads / d.unit_heads, cap);
+    d.wide = d.cluster == 0 && group > 8;
+    if (d.wide) d.unit_heads = largest_divisor(group, 128);
+    const int units = num_q_heads / d.unit_heads;
+    d.chunk = num_splits > 0 ? split_tokens(batch, num_kv_heads, block_size, max_blocks_per_seq, num_splits)
+              : d.wide       ? decode_int8_wide_split(batch, units, block_size, cap)
+                             : decode_int8_split(batch, units, block_size, cap);
+    return d;
 }
 
 }  // namespace
@@ -255,9 +267,9 @@ size_t pkv_decode_int8_workspace_size(int batch, int num_q_heads, int num_kv_hea
         block_size <= 0 || max_blocks_per_seq <= 0)
         return 0;
     const long long cap = (long long)max_blocks_per_seq * block_size;
-    if (int8_cluster(batch, num_q_heads, num_kv_heads, cap, num_splits) > 0) return 0;
-    const int chunk = int8_split(batch, num_q_heads, num_kv_heads, block_size, max_blocks_per_seq, num_splits);
-    const long long s_max = (cap + chunk - 1) / chunk;
+    const Int8Decode d = int8_decode(batch, num_q_heads, num_kv_heads, block_size, max_blocks_per_seq, num_splits);
+    if (d.cluster > 0) return 0;
+    const long long s_max = (cap + d.chunk - 1) / d.chunk;
     return s_max <= 1 ? 0 : partial_bytes(batch, num_q_heads, s_max, head_dim) + 16;
 }
 
@@ -291,10 +303,11 @@ pkv_status decode_impl(const pkv_cache &cache, const void *q, int num_q_heads, c
     if (cap > (1ll << 30)) return PKV_ERR_UNSUPPORTED;
     DeviceSlot *s = slot();
     if (!s) return PKV_ERR_CUDA;
-    const int chunk = int8 ? int8_split(batch, num_q_heads, cache.num_kv_heads, cache.block_size, max_blocks_per_seq, num_splits)
+    const Int8Decode how = int8 ? int8_decode(batch, num_q_heads, cache.num_kv_heads, cache.block_size, max_blocks_per_seq, num_splits)
+                                : Int8Decode{0, 0, 0, false};
+    const int chunk = int8 ? how.chunk
                            : split_tokens(batch, cache.num_kv_heads, cache.block_size, max_blocks_per_seq, num_splits);
     const int s_max = (int)((cap + chunk - 1) / chunk);
-    const int cluster = int8 ? int8_cluster(batch, num_q_heads, cache.num_kv_heads, cap, num_splits) : 0;
     const size_t need = (int8 ? pkv_decode_int8_workspace_size : pkv_decode_workspace_size)(
         batch, num_q_heads, cache.num_kv_heads, cache.head_dim, cache.block_size, max_blocks_per_seq, num_splits);
     if (need > 0 && (!workspace || workspace_bytes < need || !aligned16(workspace))) return PKV_ERR_WORKSPACE;
@@ -314,19 +327,19 @@ pkv_status decode_impl(const pkv_cache &cache, const void *q, int num_q_heads, c
     a.q_rows = q_rows;
     a.s_max = s_max;
     a.stages = 0;  // set by the group kernel's launcher
-    a.cluster = cluster;
+    a.cluster = how.cluster;
     // The kernel and the query heads of a unit (a KV head's group, or an equal share of it):
     //   FP8 cache: the FP8 kernels, at most 8 per unit;
-    //   INT8 cache: mma.sync units of the group or, above 8 heads, of its largest divisor up to 8;
+    //   INT8 cache: mma.sync or, above 8 heads, tcgen05 units (Int8Decode);
     //   native cache, 1 or 2 heads per KV head: CUDA cores (decode.cu), the group as one unit;
     //   4 or 8: mma.sync units of the whole group (decode_gqa.cu);
     //   any other group: tcgen05 units (decode_tc.cu) of the group, or, above 128 heads, of its
     //   largest divisor up to 128.
-    enum { kCudaCores, kMmaSync, kTcgen05, kFp8Tensor, kInt8Tensor } path;
+    enum { kCudaCores, kMmaSync, kTcgen05, kFp8Tensor, kInt8Tensor, kInt8Wide } path;
     int per_unit;
     if (int8) {
-        path = kInt8Tensor;
-        per_unit = int8_unit_heads(group);
+        path = how.wide ? kInt8Wide : kInt8Tensor;
+        per_unit = how.unit_heads;
     } else if (fp8) {
         path = cache.head_dim == 128 ? kFp8Tensor : kCudaCores;
         per_unit = group < 8 ? group : 8;
@@ -396,6 +409,7 @@ pkv_status decode_impl(const pkv_cache &cache, const void *q, int num_q_heads, c
         }
         cudaError_t le;
         switch (path) {
+            case kInt8Wide: le = launch_decode_int8_wide(d, cs); break;
             case kInt8Tensor: le = launch_decode_int8(d, grid, cs); break;
             case kFp8Tensor: le = launch_decode_fp8(d, grid, cs); break;
             case kMmaSync: le = launch_decode_gqa(d, grid, cs); break;
@@ -403,7 +417,7 @@ pkv_status decode_impl(const pkv_cache &cache, const void *q, int num_q_heads, c
             default: le = launch_decode(d, grid, cs); break;
         }
         if (le != cudaSuccess) return PKV_ERR_CUDA;
-        if (cluster > 0) continue;  // (finished)
+        if (how.cluster > 0) continue;  // (finished)
         // Rows that span several splits (and empty rows) are finished by the merge.
         CombineArgs c;
         c.part_o = d.part_o;

@@ -266,6 +266,9 @@ cudaError_t encode_rows_map(const void *ptr, int bf16, long long rows, int cols,
 cudaError_t launch_decode_gqa(const DecodeArgs &a, int grid, cudaStream_t s);
 // Tensor-core (tcgen05) decode for a unit of up to 128 query heads of one KV head.
 cudaError_t launch_decode_tc(const DecodeArgs &a, int grid, cudaStream_t s);
+// more than 8 query heads per KV head: tcgen05 units of up to 128 heads (decode_int8_wide.cu)
+int decode_int8_wide_split(int batch, int units_per_seq, int block_size, long long capacity);
+cudaError_t launch_decode_int8_wide(const DecodeArgs &a, cudaStream_t s);
 int decode_int8_split(int batch, int units_per_seq, int block_size, long long capacity);
 int decode_int8_cluster(int batch, int units_per_seq, long long capacity);
 cudaError_t launch_merge_splits(const CombineArgs &a, cudaStream_t s);  // the INT8 decode's

@@ -24,6 +24,7 @@
 #include <cuda.h>
 #include <cuda_runtime.h>
 
+#include "int8_tiles.cuh"
 #include "pkv_device.cuh"
 #include "pkv_internal.h"
 #include "prefill_common.cuh"
@@ -48,7 +49,6 @@ constexpr uint32_t kColS = 0, kColO = 256;
 template <int D>
 struct Layout {
     static constexpr int kHalves = D / 64;                    // 128-byte swizzle atoms along D
-    static constexpr uint32_t kTileHalf = 128 * 128;          // 128 rows x 128 bytes
     static constexpr uint32_t kQBytes = kHalves * kTileHalf;  // one 128-row Q tile
     static constexpr uint32_t kKVBytes = kHalves * kTileHalf; // one f16 K or V tile
     static constexpr uint32_t kCodeBytes = 128 * D;           // its codes
@@ -71,67 +71,6 @@ struct Params {
     float *lse;
     int *err;
 };
-
-// Smallest power of two >= x, for finite x >= 0 (0 for 0; at most 2^127).
-__device__ __forceinline__ float pow2_at_least(float x) {
-    uint32_t b = __float_as_uint(x);
-    if (b & 0x7fffffu) b = (b & 0x7f800000u) + 0x800000u;
-    return b >= 0x7f800000u ? 1.7014118e38f : __uint_as_float(b);
-}
-
-// Four codes (one word) times the f16 pair kk. 1024 + (c + 128) less 1152 is c exactly; kk a power of two: (1024 + c + 128)
-// kk - 1152 kk in one rounding, the exact product's (n = -1152 kk); else the product of c and kk, rounded.
-template <bool POW2>
-__device__ __forceinline__ void codes4_f16(uint32_t w, uint32_t kk, uint32_t n, uint32_t &lo, uint32_t &hi) {
-    const uint32_t x = w ^ 0x80808080u;
-    const uint32_t a = __byte_perm(x, 0x64646464u, 0x4140), b = __byte_perm(x, 0x64646464u, 0x4342);
-    if (POW2) {
-        asm("fma.rn.f16x2 %0, %1, %2, %3;" : "=r"(lo) : "r"(a), "r"(kk), "r"(n));
-        asm("fma.rn.f16x2 %0, %1, %2, %3;" : "=r"(hi) : "r"(b), "r"(kk), "r"(n));
-    } else {
-        asm("{\n\t.reg .b32 c;\n\tadd.rn.f16x2 c, %1, %2;\n\tmul.rn.f16x2 %0, c, %3;\n\t}" : "=r"(lo) : "r"(a), "r"(0xe480e480u), "r"(kk));
-        asm("{\n\t.reg .b32 c;\n\tadd.rn.f16x2 c, %1, %2;\n\tmul.rn.f16x2 %0, c, %3;\n\t}" : "=r"(hi) : "r"(b), "r"(0xe480e480u), "r"(kk));
-    }
-}
-
-// 32 rows r0 .. r0 + 31 of a tile by a warp: codes (rows of D bytes, 128-byte swizzle or, head_dim 64, 64-byte) to the f16
-// layout that TMA writes for a 16-bit cache (64-column halves of 128-byte rows, 128-byte swizzle), times the factor of
-// their page, which lane i holds for page i. Groups of 8 rows lie in one page.
-template <int D, bool POW2>
-__device__ __forceinline__ void convert_rows(const uint8_t *codes, uint8_t *f16, int r0, uint32_t kk, int log2_bs, int lane) {
-    constexpr int kLanes = D / 16;             // lanes a row: 16 codes each
-    constexpr int kRowsLoad = 32 / kLanes;     // rows a load of the warp: 4 (head_dim 128) or 8
-    constexpr int kLoads = 4;                  // loads in flight
-    const int c = lane % kLanes, rr = lane / kLanes;
-    // f16 chunks 2c and 2c + 1 (16 bytes each) of the row, in half c / 4; the lanes of the two halves store opposite chunks
-    // first: the stores of a row in one instruction then fill all 32 banks once
-    const int hf = c >> 2, k0 = 2 * (c & 3), ka = k0 + hf, kb = k0 + 1 - hf;
-#pragma unroll
-    for (int b0 = 0; b0 < 32; b0 += kLoads * kRowsLoad) {
-        uint4 raw[kLoads];
-#pragma unroll
-        for (int i = 0; i < kLoads; ++i) {
-            const int r = r0 + b0 + i * kRowsLoad + rr;
-            const int cc = D == 128 ? c ^ (r & 7) : c ^ ((r >> 1) & 3);
-            raw[i] = *reinterpret_cast<const uint4 *>(codes + r * D + (cc << 4));
-        }
-#pragma unroll
-        for (int i = 0; i < kLoads; ++i) {
-            const int g = r0 + b0 + i * kRowsLoad, r = g + rr;
-            const uint32_t f = __shfl_sync(0xffffffffu, kk, (g >> log2_bs) & 31);
-            uint32_t nf;
-            asm("mul.rn.f16x2 %0, %1, %2;" : "=r"(nf) : "r"(f), "r"(0xe480e480u));
-            uint4 v0, v1;
-            codes4_f16<POW2>(raw[i].x, f, nf, v0.x, v0.y);
-            codes4_f16<POW2>(raw[i].y, f, nf, v0.z, v0.w);
-            codes4_f16<POW2>(raw[i].z, f, nf, v1.x, v1.y);
-            codes4_f16<POW2>(raw[i].w, f, nf, v1.z, v1.w);
-            uint8_t *row = f16 + hf * Layout<D>::kTileHalf + r * 128;
-            *reinterpret_cast<uint4 *>(row + ((ka ^ (r & 7)) << 4)) = hf ? v1 : v0;
-            *reinterpret_cast<uint4 *>(row + ((kb ^ (r & 7)) << 4)) = hf ? v0 : v1;
-        }
-    }
-}
 
 // BF16: type of q and the default output; the products run in f16.
 template <int D, bool BF16>
@@ -232,7 +171,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                 for (int x = 0; x < 2; ++x)
 #pragma unroll
                     for (int hf = 0; hf < Lay::kHalves; ++hf)
-                        tc::tma_load_3d(sQ + x * Lay::kQBytes + hf * Lay::kTileHalf, &tm_q, hf * 64, h,
+                        tc::tma_load_3d(sQ + x * Lay::kQBytes + hf * kTileHalf, &tm_q, hf * 64, h,
                                         q0 + m_start + x * kBM, q_full);
             }
             bool ok = true;
@@ -280,7 +219,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                     const uint32_t aQx = aQ + (uint32_t)x * Lay::kQBytes;
 #pragma unroll
                     for (int kk = 0; kk < D / 16; ++kk) {
-                        const uint32_t o = (uint32_t)(kk >> 2) * Lay::kTileHalf + (uint32_t)(kk & 3) * 32u;
+                        const uint32_t o = (uint32_t)(kk >> 2) * kTileHalf + (uint32_t)(kk & 3) * 32u;
                         tc::mma_f16_ss(tmem + kColS + 128u * x, tc::smem_desc(aQx + o, 16, 1024), tc::smem_desc(aK + o, 16, 1024),
                                        id_qk, kk > 0 ? 1u : 0u);
                     }
@@ -292,7 +231,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                     for (int kk = 0; kk < kBN / 16; ++kk) {
                         // V is [keys x D], D contiguous: MN-major B; 8-key groups 1024 B apart,
                         // 64-column halves kTileHalf apart. P: 16 keys = 8 TMEM columns.
-                        tc::mma_f16_ts(tO, tP + 8u * kk, tc::smem_desc(aV + (uint32_t)kk * 2048u, Lay::kTileHalf, 1024),
+                        tc::mma_f16_ts(tO, tP + 8u * kk, tc::smem_desc(aV + (uint32_t)kk * 2048u, kTileHalf, 1024),
                                        id_pv, (j > 0 || kk > 0) ? 1u : 0u);
                     }
                     tc::mma_commit(&o_done[x]);
@@ -341,29 +280,8 @@ __global__ void __launch_bounds__(kThreads, 1)
         const int cw = warp - 12;
         // ---- Wk, Wv over the pages of keys [0, kv_end); a page id outside the pool: page 0, as the producer reads it ----
         {
-            const int pages = (kv_end + p.bs - 1) >> p.log2_bs;
-            float mk = 0.f, mv = 0.f;
-            int nk = 0x7fffffff, nv = 0x7fffffff;
-            for (int i = cw * 32 + lane; i < pages; i += 128) {
-                int pb = __ldg(bt + i);
-                if (pb < 0 || pb >= p.num_blocks) pb = 0;
-                const float *sc = p.scales + (size_t)pb * 2 * p.num_kv_heads + g;
-                const float k = __ldg(sc), v = __ldg(sc + p.num_kv_heads);
-                if (k < INFINITY) mk = fmaxf(mk, k); else nk = min(nk, i << p.log2_bs);
-                if (v < INFINITY) mv = fmaxf(mv, v); else nv = min(nv, i << p.log2_bs);
-            }
-            mk = __uint_as_float(__reduce_max_sync(0xffffffffu, __float_as_uint(mk)));  // (bits of numbers >= 0 are in order)
-            mv = __uint_as_float(__reduce_max_sync(0xffffffffu, __float_as_uint(mv)));
-            nk = __reduce_min_sync(0xffffffffu, nk);
-            nv = __reduce_min_sync(0xffffffffu, nv);
-            if (lane == 0) {
-                atomicMax(&sMax[0], __float_as_uint(mk));
-                atomicMax(&sMax[1], __float_as_uint(mv));
-                atomicMin(&sNan[0], nk);
-                atomicMin(&sNan[1], nv);
-                __threadfence_block();
-                mbar_arrive(w_ready);
-            }
+            page_scales(p.scales, bt, p.num_blocks, p.num_kv_heads, g, p.log2_bs, 0, kv_end, cw * 32 + lane, sMax, sNan);
+            if (lane == 0) mbar_arrive(w_ready);
             __syncwarp();
         }
         bool ok = true;
@@ -371,16 +289,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             // q to f16 in place (exact for |q| within f16's range)
             ok = mbar_wait(q_full, 0, abort_flag, p.err);
             if (ok) {
-                uint4 *q4 = reinterpret_cast<uint4 *>(sQ);
-                for (int i = cw * 32 + lane; i < 2 * (int)Lay::kQBytes / 16; i += 128) {
-                    const uint4 v = q4[i];
-                    const uint32_t w[4] = {v.x, v.y, v.z, v.w};
-                    uint32_t o[4];
-#pragma unroll
-                    for (int k = 0; k < 4; ++k)
-                        o[k] = pack_pair<false>(__uint_as_float(w[k] << 16), __uint_as_float(w[k] & 0xffff0000u));
-                    q4[i] = make_uint4(o[0], o[1], o[2], o[3]);
-                }
+                q_tiles_to_f16(sQ, 2 * (int)Lay::kQBytes / 16, cw * 32 + lane);
                 tc::fence_proxy_async_smem();
             }
         } else {

@@ -103,7 +103,10 @@ def run(lens, hq, heads, d, bs, dtype, seed, out_dtype=None, num_splits=0, sprea
     cu = np.arange(len(lens) + 1)
     args = (codes.numpy(), scales.numpy(), q.double().numpy(), cu, lens, tables.numpy(), scale)
     ref, ref_lse = int8_ref.attention(*args, causal=False)
-    err, err_lse = bounds(*args, ref, 2.0 ** -21, causal=False)
+    # more than 8 heads per KV head: the weights may be rounded once to f16 (half a step, 2^-11), times 2^7
+    wide = hq // heads > 8
+    err, err_lse = bounds(*args, ref, 2.0 ** -11 if wide else 2.0 ** -21, causal=False,
+                          weight_abs=2.0 ** -32 if wide else 2.0 ** -36)
     check(out, lse, ref, ref_lse, err, err_lse)
 
 
@@ -116,7 +119,7 @@ def test_lengths(bs, d, num_splits):
 
 
 @pytest.mark.parametrize("lens", [[5000], [1], [0], [17, 3000], [900, 0, 0, 33], [100] * 9, [2000] * 20, [600] * 40, [40] * 200])
-@pytest.mark.parametrize("hq,heads", [(4, 1), (8, 8), (7, 1), (16, 1)])
+@pytest.mark.parametrize("hq,heads", [(4, 1), (8, 8), (7, 1), (16, 1), (40, 1)])
 def test_batches(lens, hq, heads):
     """From one sequence to many: clusters of every size, and the splits."""
     run(lens, hq, heads, 128, 16, "f16", len(lens) + hq)
@@ -131,8 +134,28 @@ def test_groups(hq, heads, d, num_splits):
 
 
 @pytest.mark.parametrize("num_splits", [1, 2, 5, 40])
-def test_splits(num_splits):
-    run([3000, 17, 1, 0, 129], 8, 2, 128, 32, "bf16", num_splits, num_splits=num_splits)
+@pytest.mark.parametrize("hq", [8, 24])
+def test_splits(num_splits, hq):
+    run([3000, 17, 1, 0, 129], hq, 2, 128, 32, "bf16", num_splits, num_splits=num_splits)
+
+
+@pytest.mark.parametrize("d", [64, 128])
+@pytest.mark.parametrize("bs", [8, 16, 64, 128, 512])
+@pytest.mark.parametrize("hq", [12, 33, 128, 130])
+def test_many_heads(bs, d, hq):
+    """One KV head for many query heads: lengths around tiles, one tile, an odd and an even number of them."""
+    run([0, 1, bs, 127, 128, 129, 256, 257, 400, 1000, 1537], hq, 1, d, bs, "bf16" if bs == 16 else "f16", bs + hq, num_splits=2)
+
+
+def test_many_heads_float32_and_scales():
+    run([300, 900], 16, 1, 128, 16, "f16", 5, out_dtype=torch.float32, num_splits=1)
+    run([500, 64, 900], 20, 1, 128, 16, "bf16", 8, spread=6, scale=0.01, num_splits=1)
+    codes, scales = pool(60, 2, 8, 64, 9)
+    scales[::3, 1] = 0.0
+    run([200, 150], 24, 2, 64, 8, "bf16", 9, codes=codes, scales=scales, num_splits=1)
+    run([200, 150], 24, 2, 64, 8, "bf16", 9, codes=codes, scales=torch.zeros_like(scales), num_splits=1)
+    run([200, 150], 24, 2, 64, 8, "bf16", 9, scale=-0.2, num_splits=1)
+    run([200, 150], 24, 2, 64, 8, "bf16", 9, scale=0.0, num_splits=1)
 
 
 @pytest.mark.parametrize("dtype", ["f16", "bf16"])
@@ -173,9 +196,9 @@ def test_what_is_not_a_number():
     scales[0, 0], scales[3, 1] = float("nan"), float("nan")
     scales[5], codes[4, :, :, 60:] = float("nan"), 127
     lens = torch.tensor([256, 256, 60, 200], dtype=torch.int32)
-    q = torch.randn((4, 2, 64), generator=torch.Generator().manual_seed(1)).half()
-    for splits in (0, 1, 2):
-        lse = torch.empty((4, 2), device="cuda")
+    for splits, heads in ((0, 2), (1, 2), (2, 2), (1, 20), (2, 20)):
+        q = torch.randn((4, heads, 64), generator=torch.Generator().manual_seed(1)).half()
+        lse = torch.empty((4, heads), device="cuda")
         out = pkv.paged_attn_decode(codes.cuda(), q.cuda(), tables.cuda(), lens.cuda(), lse=lse, num_splits=splits,
                                     scales=scales.cuda())
         assert torch.isnan(out[:2]).all() and torch.isfinite(out[2:]).all()
