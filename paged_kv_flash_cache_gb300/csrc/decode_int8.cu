@@ -12,13 +12,13 @@
 // FP32 scores. The V scales enter the weights, which go into the product relative to their tile's largest, as an f16
 // part and its remainder: the output's rounding is the only 16-bit one on the path, however small weights and scales are.
 //
-// Structure (persistent, three CTAs an SM of four warps). A unit is (sequence, KV head's query group, split); tile j (32 tokens) of a unit
+// Structure (persistent, three CTAs an SM of four warps). A unit is (sequence, KV head's query group, split); tile j (8 KB of codes) of a unit
 // is warp j % W's. Every warp feeds itself: it has a ring of its own and sends for the tile that goes into a slot as
 // soon as it has read the slot's last one, so no warp waits for another one and there is no producer to fall behind
 // (with one, 0.131 ms on the 7B-like batch, 0.111 with three quarters of the arithmetic left out). A tile arrives in page
-// slices of min(bs, 32) rows, each one 5-D TMA box of its K rows and its V rows; a slice lies in one page, whose scales
+// slices of min(bs, tile) rows, each one 5-D TMA box of its K rows and its V rows; a slice lies in one page, whose scales
 // come beside it by 4-byte asynchronous copies on the same mbarrier. The page ids of the tile after are loaded a tile
-// ahead. The two blocks of 16 tokens of a tile are two independent chains of ldmatrix, conversion and mma. At the
+// ahead. The blocks of 16 tokens of a tile are independent chains of ldmatrix, conversion and mma. At the
 // end of a unit the warps merge their rows, a head each, and write the output or the split's partial.
 //
 // Operand layouts. ldmatrix (.b16) hands lane (gid, tig) the codes of dims 4 tig .. 4 tig + 3 of a 16-dim chunk: the
@@ -40,7 +40,10 @@ namespace {
 
 constexpr int kWarps = 4;
 constexpr int kThreads = kWarps * 32;
-constexpr int kTile = 32;  // tokens of a tile
+// Tokens of a tile: 8 KB of codes. (head_dim 64 with 32 tokens a tile: what a tile costs besides its codes bounded it, 64
+// sequences of 4096 tokens, 8 KV heads 61 us.)
+template <int D>
+constexpr int kTile = D == 64 ? 64 : 32;
 constexpr int kCtasPerSm = 3;
 constexpr int kClusterCtasPerSm = 2;  // clusters: CTAs an SM at most
 constexpr float kRescale = 4.0f;  // lazy rescale threshold (log2 units)
@@ -48,19 +51,22 @@ constexpr float kWeight = 2048.0f;  // weights, at most 2^kRescale, go into the 
 
 template <int D, int G>
 struct Int8Layout {
-    // slots of a warp's ring: what three CTAs an SM (two for more than four heads) leave room for beside merge rows and
-    // unit tables
-    static constexpr int kStages = D == 64 ? (G > 4 ? 5 : 4) : (G > 4 ? 2 : 2);
-    static constexpr uint32_t kStageBytes = 2 * kTile * D;  // per slice: br K rows, br V rows of D bytes
-    static constexpr uint32_t kScaleOffset = kWarps * kStages * kStageBytes;  // [kWarps][kStages][4] (K, V)
-    static constexpr uint32_t kBarOffset = kScaleOffset + kWarps * kStages * 32;
+    static constexpr int kStages = 2;  // slots of a warp's ring
+    static constexpr int kSlices = kTile<D> / 8;                  // page slices of a tile at most
+    static constexpr uint32_t kStageBytes = 2 * kTile<D> * D;     // per slice: br K rows, br V rows of D bytes
+    static constexpr uint32_t kScaleOffset = kWarps * kStages * kStageBytes;  // [kWarps][kStages][kSlices] (K, V)
+    static constexpr uint32_t kBarOffset = kScaleOffset + kWarps * kStages * kSlices * 8;
     // full per slot, rows written, rows read, then the abort flag
     static constexpr uint32_t kMergeOffset = (kBarOffset + (kWarps * kStages + 2) * 8 + 16 + 15) / 16 * 16;
-    static constexpr uint32_t kMergeFloats = kWarps * G * kMergeRow<D>;
+    // the warps' rows of up to four heads at a time (eight at once would leave room for two CTAs an SM only), and, in a
+    // cluster, the CTA's row of each head
+    static constexpr int kMergeHeads = G < 4 ? G : 4;
+    static constexpr uint32_t kMergeFloats = kWarps * kMergeHeads * kMergeRow<D>;
     static constexpr uint32_t kIntsOffset = kMergeOffset + kMergeFloats * 4;
     static size_t smem_bytes(int batch, int s_max) {
         return kIntsOffset + unit_table_ints(batch, s_max) * 4 + 1024;  // + 1024-byte alignment slack
     }
+    static size_t smem_bytes_one() { return kIntsOffset + G * kMergeRow<D> * 4 + 1024; }
 };
 
 // Shared-memory address of row t, 16-byte chunk c of rows of D bytes in the swizzled layout that TMA writes (128-byte
@@ -179,7 +185,9 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm)
     constexpr int S = L::kStages;
     constexpr int kChunks = D / 16;    // 16-dim chunks: k-steps of q.K^T, m-tiles of O^T
     constexpr bool kPacked = G <= 4;   // weights and their remainders side by side in one mma
-    constexpr int kLanesFull = 4;      // lanes that copy scales: slices of a tile at most
+    constexpr int T = kTile<D>, kBlocks = T / 16;
+    constexpr int kLanesFull = L::kSlices;  // lanes that copy scales
+    constexpr int kMH = L::kMergeHeads;
     extern __shared__ uint8_t smem_raw[];
     uint8_t *smem = smem_raw + ((1024u - (smem_addr(smem_raw) & 1023u)) & 1023u);
     uint64_t *full = reinterpret_cast<uint64_t *>(smem + L::kBarOffset);  // [kWarps][S]
@@ -187,13 +195,14 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm)
     uint64_t *read = written + 1;           // and have been merged
     volatile int *abort_flag = reinterpret_cast<volatile int *>(read + 1);
     float *merge = reinterpret_cast<float *>(smem + L::kMergeOffset);
+    float *cta_rows = reinterpret_cast<float *>(smem + L::kIntsOffset);  // ONE: in the tables' place
     const UnitTable ut = unit_table(reinterpret_cast<int *>(smem + L::kIntsOffset), a.batch, a.s_max);
 
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
     const int hkv = a.cache.num_kv_heads, bs = a.cache.block_size;
     const int hu = hkv * a.head_groups;  // unit heads
-    // rows of a slice (a power of two): splits and tiles start at multiples of 32 tokens
-    const int log2_br = min(a.cache.log2_block_size, 5), br = 1 << log2_br;
+    // rows of a slice (a power of two): splits and tiles start at multiples of the tile
+    const int log2_br = min(a.cache.log2_block_size, T == 64 ? 6 : 5), br = 1 << log2_br;
 
     if (tid == 0) {
         for (int i = 0; i < kWarps * S; ++i) mbar_init(&full[i], 1 + kLanesFull);  // the boxes' bytes; the scales
@@ -223,7 +232,7 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm)
             len = len < 0 ? 0 : cap;
         }
         if (!one_mine) len = 0;
-        const int per = ((len + n - 1) / n + kTile - 1) / kTile * kTile;
+        const int per = ((len + n - 1) / n + T - 1) / T * T;
         one.t0 = min(rank * per, len);
         one.t1 = min(one.t0 + per, len);
         __syncthreads();  // (the barriers are initialised)
@@ -234,7 +243,7 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm)
     }
 
     uint8_t *ring = smem + (size_t)warp * S * L::kStageBytes;
-    float *scales = reinterpret_cast<float *>(smem + L::kScaleOffset) + warp * S * 8;  // [S][4][2]
+    float *scales = reinterpret_cast<float *>(smem + L::kScaleOffset) + warp * S * L::kSlices * 2;
     full += warp * S;
     // ---- what is sent for: the next tile, its unit and the page ids of its slices (lane j: slice j) ----
     const uint64_t pol = l2_policy_evict_first();
@@ -244,7 +253,7 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm)
     auto seek = [&]() {  // from unit iu on, the first one with a tile of this warp; its page ids
         for (; iu < num_units; iu += gridDim.x) {
             ic = ONE ? one : unit_of(iu, ut, a.s_max, hu, chunk);
-            its = ic.t0 + warp * kTile;
+            its = ic.t0 + warp * T;
             ikv = a.head_groups == 1 ? ic.kvh : ic.kvh / a.head_groups;  // the KV head of the unit
             if (its < ic.t1) break;
         }
@@ -252,13 +261,13 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm)
     auto page_ids = [&]() {
         const int tok = its + lane * br;
         ipb = 0;
-        if (iu < num_units && lane < kLanesFull && tok < ic.t1 && lane * br < kTile)
+        if (iu < num_units && lane < kLanesFull && tok < ic.t1 && lane * br < T)
             ipb = __ldg(a.block_tables + (size_t)ic.b * a.max_blocks_per_seq + (tok >> a.cache.log2_block_size));
     };
     auto send = [&](int slot) {
         if (iu >= num_units) return;
-        const int n = min(kTile, ic.t1 - its);
-        const int nslices = (n + br - 1) >> log2_br;  // <= 4
+        const int n = min(T, ic.t1 - its);
+        const int nslices = (n + br - 1) >> log2_br;  // <= kSlices
         if (lane == 0) mbar_arrive_expect_tx(&full[slot], (uint32_t)nslices * br * 2u * D);
         __syncwarp();
         if (lane < nslices) {
@@ -270,12 +279,12 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm)
             tc::tma_load_5d_hint(ring + (size_t)slot * L::kStageBytes + (size_t)lane * 2 * br * D, &tm, 0,
                                  (its + lane * br) & (bs - 1), ikv, 0, pb, &full[slot], pol);
             const float *sc = a.cache.scales + (size_t)pb * 2 * hkv + ikv;
-            cp_async4(scales + slot * 8 + lane * 2, sc);
-            cp_async4(scales + slot * 8 + lane * 2 + 1, sc + hkv);
+            cp_async4(scales + slot * L::kSlices * 2 + lane * 2, sc);
+            cp_async4(scales + slot * L::kSlices * 2 + lane * 2 + 1, sc + hkv);
         }
         if (lane < kLanesFull) cp_async_arrive(&full[slot]);
         ++issued;
-        its += kWarps * kTile;
+        its += kWarps * T;
         if (its >= ic.t1) {
             iu += gridDim.x;
             seek();
@@ -298,9 +307,9 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm)
     uint32_t mphase = 0;  // of the merge buffer
     bool ok = true;
     // rows of the warp's ldmatrix in the slice layout (slice j starts at row 2 j br): 16 tokens a block
-    int trow[2];
+    int trow[kBlocks];
 #pragma unroll
-    for (int bl = 0; bl < 2; ++bl) {
+    for (int bl = 0; bl < kBlocks; ++bl) {
         const int t = bl * 16 + (lane & 7) + 8 * (mi & 1);
         trow[bl] = t + (t & -br);
     }
@@ -310,7 +319,7 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm)
         float2 o[kChunks][2];
 #pragma unroll
         for (int mt = 0; mt < kChunks; ++mt) o[mt][0] = o[mt][1] = make_float2(0.f, 0.f);
-        const int first = c.t0 + warp * kTile;
+        const int first = c.t0 + warp * T;
         if (first < c.t1) {
             const int hq = kPacked ? gid & 3 : gid;  // head of this lane's column of the B fragment
             const uint16_t *qr = qg + ((size_t)(ONE ? one_row : ut.qrow[c.b]) * a.num_q_heads + (size_t)c.kvh * G + hq) * D + 4 * tig;
@@ -329,54 +338,58 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm)
                         bq[kk][i] = pack_pair<false>(__uint_as_float(bq[kk][i] << 16), __uint_as_float(bq[kk][i] & 0xffff0000u));
             }
         }
-        for (int ts = first; ts < c.t1; ts += kWarps * kTile) {
-            const int n = min(kTile, c.t1 - ts);
+        for (int ts = first; ts < c.t1; ts += kWarps * T) {
+            const int n = min(T, c.t1 - ts);
             if (!(ok = warp_wait(&full[slot], phase, abort_flag, a.err))) break;
             const uint32_t aK = smem_addr(ring + (size_t)slot * L::kStageBytes), aV = aK + br * D;
-            // scales of the four groups of 8 tokens (a group lies in one page)
-            float sk[4], sv[4];
+            // scales of the groups of 8 tokens (a group lies in one page)
+            float sk[2 * kBlocks], sv[2 * kBlocks];
 #pragma unroll
-            for (int g = 0; g < 4; ++g) {
-                const float2 x = *reinterpret_cast<const float2 *>(scales + slot * 8 + ((g * 8) >> log2_br) * 2);
+            for (int g = 0; g < 2 * kBlocks; ++g) {
+                const float2 x = *reinterpret_cast<const float2 *>(scales + slot * L::kSlices * 2 + ((g * 8) >> log2_br) * 2);
                 sk[g] = x.x * sl;
                 sv[g] = x.y;
             }
-            // ---- S^T = K q^T: two blocks of 16 tokens x 8 head slots ----
-            float s[2][4];
+            // ---- S^T = K q^T: blocks of 16 tokens x 8 head slots ----
+            float s[kBlocks][4];
 #pragma unroll
-            for (int bl = 0; bl < 2; ++bl) s[bl][0] = s[bl][1] = s[bl][2] = s[bl][3] = 0.f;
+            for (int bl = 0; bl < kBlocks; ++bl) s[bl][0] = s[bl][1] = s[bl][2] = s[bl][3] = 0.f;
 #pragma unroll
-            for (int cp = 0; cp < kChunks; cp += 2) {
-                uint32_t r[2][4];
+            for (int cp = 0; cp < kChunks; cp += 2)
 #pragma unroll
-                for (int bl = 0; bl < 2; ++bl) ldsm_x4(swz<D>(aK, trow[bl], cp + (mi >> 1)), r[bl]);
+                for (int b0 = 0; b0 < kBlocks; b0 += 2) {
+                    uint32_t r[2][4];
 #pragma unroll
-                for (int h = 0; h < 2; ++h)
+                    for (int bl = 0; bl < 2; ++bl) ldsm_x4(swz<D>(aK, trow[b0 + bl], cp + (mi >> 1)), r[bl]);
 #pragma unroll
-                    for (int bl = 0; bl < 2; ++bl) {
-                        const uint32_t x = r[bl][2 * h] ^ 0x80808080u, y = r[bl][2 * h + 1] ^ 0x80808080u;
-                        const uint32_t af[4] = {codes_f16<0x4140>(x), codes_f16<0x4140>(y), codes_f16<0x4342>(x),
-                                                codes_f16<0x4342>(y)};
-                        mma16816<false>(s[bl], af, bq[cp + h][0], bq[cp + h][1]);
-                    }
-            }
+                    for (int h = 0; h < 2; ++h)
+#pragma unroll
+                        for (int bl = 0; bl < 2; ++bl) {
+                            const uint32_t x = r[bl][2 * h] ^ 0x80808080u, y = r[bl][2 * h + 1] ^ 0x80808080u;
+                            const uint32_t af[4] = {codes_f16<0x4140>(x), codes_f16<0x4140>(y), codes_f16<0x4342>(x),
+                                                    codes_f16<0x4342>(y)};
+                            mma16816<false>(s[b0 + bl], af, bq[cp + h][0], bq[cp + h][1]);
+                        }
+                }
             // token of s[bl][i]: bl * 16 + gid + 8 * (i >> 1); head slot 2 tig + (i & 1)
 #pragma unroll
-            for (int bl = 0; bl < 2; ++bl)
+            for (int bl = 0; bl < kBlocks; ++bl)
 #pragma unroll
                 for (int i = 0; i < 4; ++i) s[bl][i] *= sk[bl * 2 + (i >> 1)];
-            if (n < kTile) {  // behind the context's end (and maybe beyond the last slice): no weight, and no scale
+            if (n < T) {  // behind the context's end (and maybe beyond the last slice): no weight, and no scale
 #pragma unroll
-                for (int g = 0; g < 4; ++g) {
+                for (int g = 0; g < 2 * kBlocks; ++g) {
                     if (g * 8 >= n) sv[g] = 0.f;
                     if (g * 8 + gid >= n) s[g >> 1][(g & 1) * 2] = s[g >> 1][(g & 1) * 2 + 1] = -INFINITY;
                 }
             }
             // The running max m of a head is a past maximum: it moves only when a score exceeds it by more than 2^4, so
             // the lanes need one vote a tile and rarely each other's maxima.
-            float mx[2];
+            float mx[2] = {-INFINITY, -INFINITY};
 #pragma unroll
-            for (int i = 0; i < 2; ++i) mx[i] = fmaxf(fmax3(s[0][i], s[0][i + 2], s[1][i]), s[1][i + 2]);
+            for (int bl = 0; bl < kBlocks; ++bl)
+#pragma unroll
+                for (int i = 0; i < 2; ++i) mx[i] = fmax3(mx[i], s[bl][i], s[bl][i + 2]);
             if (__any_sync(0xffffffffu, mx[0] > m[0] + kRescale || mx[1] > m[1] + kRescale)) {
 #pragma unroll
                 for (int ofs = 4; ofs < 32; ofs <<= 1) {
@@ -399,11 +412,13 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm)
             // The tile's weights enter the product relative to its largest V scale w and times 2^11: P' = 2^11 p sv / w (at
             // most 2^15), as an f16 part and its remainder, holds weights down to 2^-35. The tile's product
             // enters O in FP32 times w / 2^11.
-            const float w = fmaxf(fmax3(sv[0], sv[1], sv[2]), sv[3]);
-            const float rw = w >= 1.17549435e-38f ? kWeight * rcpf(w) : 0.f;  // (scales below 2^-126 count as 0)
-            uint32_t ph[2][2], pe[2][2];
+            float w = sv[0];
 #pragma unroll
-            for (int bl = 0; bl < 2; ++bl)
+            for (int g = 1; g < 2 * kBlocks; ++g) w = fmaxf(w, sv[g]);
+            const float rw = w >= 1.17549435e-38f ? kWeight * rcpf(w) : 0.f;  // (scales below 2^-126 count as 0)
+            uint32_t ph[kBlocks][2], pe[kBlocks][2];
+#pragma unroll
+            for (int bl = 0; bl < kBlocks; ++bl)
 #pragma unroll
                 for (int hf = 0; hf < 2; ++hf) {
                     const float p0 = ex2f(s[bl][2 * hf] - m[0]), p1 = ex2f(s[bl][2 * hf + 1] - m[1]);
@@ -423,22 +438,25 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm)
             // ---- O^T += f V^T P'^T: D dims (permuted within each 16-dim chunk) x 8 slots ----
 #pragma unroll
             for (int cp = 0; cp < kChunks; cp += 2) {
-                uint32_t r[2][4];
-#pragma unroll
-                for (int bl = 0; bl < 2; ++bl) ldsm_x4_t(swz<D>(aV, trow[bl], cp + (mi >> 1)), r[bl]);
                 float ot[2][4];
 #pragma unroll
                 for (int h = 0; h < 2; ++h) ot[h][0] = ot[h][1] = ot[h][2] = ot[h][3] = 0.f;
 #pragma unroll
-                for (int bl = 0; bl < 2; ++bl)
+                for (int b0 = 0; b0 < kBlocks; b0 += 2) {
+                    uint32_t r[2][4];
 #pragma unroll
-                    for (int h = 0; h < 2; ++h) {
-                        const uint32_t x = r[bl][2 * h] ^ 0x80808080u, y = r[bl][2 * h + 1] ^ 0x80808080u;
-                        const uint32_t af[4] = {codes_f16<0x4240>(x), codes_f16<0x4341>(x), codes_f16<0x4240>(y),
-                                                codes_f16<0x4341>(y)};
-                        if (!kPacked) mma16816<false>(ot[h], af, pe[bl][0], pe[bl][1]);
-                        mma16816<false>(ot[h], af, ph[bl][0], ph[bl][1]);
-                    }
+                    for (int bl = 0; bl < 2; ++bl) ldsm_x4_t(swz<D>(aV, trow[b0 + bl], cp + (mi >> 1)), r[bl]);
+#pragma unroll
+                    for (int bl = 0; bl < 2; ++bl)
+#pragma unroll
+                        for (int h = 0; h < 2; ++h) {
+                            const uint32_t x = r[bl][2 * h] ^ 0x80808080u, y = r[bl][2 * h + 1] ^ 0x80808080u;
+                            const uint32_t af[4] = {codes_f16<0x4240>(x), codes_f16<0x4341>(x), codes_f16<0x4240>(y),
+                                                    codes_f16<0x4341>(y)};
+                            if (!kPacked) mma16816<false>(ot[h], af, pe[b0 + bl][0], pe[b0 + bl][1]);
+                            mma16816<false>(ot[h], af, ph[b0 + bl][0], ph[b0 + bl][1]);
+                        }
+                }
 #pragma unroll
                 for (int h = 0; h < 2; ++h) {
                     o[cp + h][0] = ffma2(make_float2(ot[h][0], ot[h][1]), f2, o[cp + h][0]);
@@ -470,71 +488,76 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm)
                     o[mt][k].y += __shfl_xor_sync(0xffffffffu, o[mt][k].y, 2);
                 }
         }
-        if (!(ok = warp_wait(read, mphase ^ 1u, abort_flag, a.err))) break;
-#pragma unroll
-        for (int jj = 0; jj < 2; ++jj) {
-            const int g = 2 * tig + jj;
-            if (g < G) {
-                float *row = merge + ((size_t)warp * G + g) * kMergeRow<D>;
-#pragma unroll
-                for (int mt = 0; mt < kChunks; ++mt)  // M slot gid: dim 2gid of the chunk; gid + 8: dim 2gid + 1
-                    *reinterpret_cast<float2 *>(row + mt * 16 + 2 * gid) =
-                        jj ? make_float2(o[mt][0].y, o[mt][1].y) : make_float2(o[mt][0].x, o[mt][1].x);
-                // (every score NaN: the maximum passed over them; 0 lets the NaN sum through the merge)
-                if (gid == 0)
-                    *reinterpret_cast<float2 *>(row + D) =
-                        make_float2(m[jj] == -INFINITY && l[jj] != l[jj] ? 0.f : m[jj], l[jj]);
-            }
-        }
-        __syncwarp();
-        if (lane == 0) mbar_arrive(written);
-        if (!(ok = warp_wait(written, mphase, abort_flag, a.err))) break;
-        // ---- the merge of head g by warp g % W: M = max m, weights 2^(m_w - M), out = sum w acc / sum w l ----
         const int splits = ONE ? 1 : (ut.lens[c.b] + chunk - 1) / chunk;
-        for (int g = warp; g < G; g += kWarps) {
-            float *row = merge + (size_t)g * kMergeRow<D>;
-            float2 ml[kWarps];
-            float M = -INFINITY, sum = 0.f, acc[D / 32];
 #pragma unroll
-            for (int i = 0; i < kWarps; ++i) {
-                ml[i] = *reinterpret_cast<const float2 *>(row + (size_t)i * G * kMergeRow<D> + D);
-                M = fmaxf(M, ml[i].x);
+        for (int g0 = 0; g0 < G && ok; g0 += kMH) {  // the heads g0 .. g0 + kMH - 1
+            if (!(ok = warp_wait(read, mphase ^ 1u, abort_flag, a.err))) break;
+#pragma unroll
+            for (int jj = 0; jj < 2; ++jj) {
+                const int g = 2 * tig + jj;
+                if (g >= g0 && g < g0 + kMH && g < G) {
+                    float *row = merge + ((size_t)warp * kMH + g - g0) * kMergeRow<D>;
+#pragma unroll
+                    for (int mt = 0; mt < kChunks; ++mt)  // M slot gid: dim 2gid of the chunk; gid + 8: dim 2gid + 1
+                        *reinterpret_cast<float2 *>(row + mt * 16 + 2 * gid) =
+                            jj ? make_float2(o[mt][0].y, o[mt][1].y) : make_float2(o[mt][0].x, o[mt][1].x);
+                    // (every score NaN: the maximum passed over them; 0 lets the NaN sum through the merge)
+                    if (gid == 0)
+                        *reinterpret_cast<float2 *>(row + D) =
+                            make_float2(m[jj] == -INFINITY && l[jj] != l[jj] ? 0.f : m[jj], l[jj]);
+                }
             }
+            __syncwarp();
+            if (lane == 0) mbar_arrive(written);
+            if (!(ok = warp_wait(written, mphase, abort_flag, a.err))) break;
+            // ---- the merge of head g0 + warp: M = max m, weights 2^(m_w - M), out = sum w acc / sum w l ----
+            const int g = g0 + warp;
+            if (warp < kMH && g < G) {
+                const float *row = merge + (size_t)warp * kMergeRow<D>;
+                float2 ml[kWarps];
+                float M = -INFINITY, sum = 0.f, acc[D / 32];
 #pragma unroll
-            for (int v = 0; v < D / 32; ++v) acc[v] = 0.f;
+                for (int i = 0; i < kWarps; ++i) {
+                    ml[i] = *reinterpret_cast<const float2 *>(row + (size_t)i * kMH * kMergeRow<D> + D);
+                    M = fmaxf(M, ml[i].x);
+                }
 #pragma unroll
-            for (int i = 0; i < kWarps; ++i) {
-                const float wt = ml[i].x == -INFINITY ? 0.f : ex2f(ml[i].x - M);
-                sum = fmaf(wt, ml[i].y, sum);
-                const float *r = row + (size_t)i * G * kMergeRow<D> + lane * (D / 32);
+                for (int v = 0; v < D / 32; ++v) acc[v] = 0.f;
 #pragma unroll
-                for (int v = 0; v < D / 32; ++v) acc[v] = fmaf(wt, r[v], acc[v]);
+                for (int i = 0; i < kWarps; ++i) {
+                    const float wt = ml[i].x == -INFINITY ? 0.f : ex2f(ml[i].x - M);
+                    sum = fmaf(wt, ml[i].y, sum);
+                    const float *r = row + (size_t)i * kMH * kMergeRow<D> + lane * (D / 32);
+#pragma unroll
+                    for (int v = 0; v < D / 32; ++v) acc[v] = fmaf(wt, r[v], acc[v]);
+                }
+                if constexpr (ONE) {  // the CTA's row, relative to M
+                    float *mine = cta_rows + (size_t)g * kMergeRow<D>;
+#pragma unroll
+                    for (int v = 0; v < D / 32; ++v) mine[lane * (D / 32) + v] = acc[v];
+                    if (lane == 0) *reinterpret_cast<float2 *>(mine + D) = make_float2(M, sum);
+                } else {
+                    const float inv = 1.f / sum;  // (a unit has a token, so the sum is above 0, or NaN)
+#pragma unroll
+                    for (int v = 0; v < D / 32; ++v) acc[v] *= inv;
+                    const float lse = (M + __log2f(sum)) * kLn2;
+                    const size_t head = (size_t)c.kvh * G + g;
+                    if (splits == 1) {
+                        const size_t row_o = (size_t)ut.qrow[c.b] * a.num_q_heads + head;
+                        store_out_vec<D / 32>(a.out, row_o * D + lane * (D / 32), acc, a.out_dtype);
+                        if (a.lse && lane == 0) a.lse[row_o] = lse;
+                    } else {
+                        const size_t row_p = ((size_t)c.b * a.num_q_heads + head) * a.s_max + c.split;
+                        store_out_vec<D / 32>(a.part_o, row_p * D + lane * (D / 32), acc, 2);
+                        if (lane == 0) a.part_lse[row_p] = lse;
+                    }
+                }
             }
-            if constexpr (ONE) {  // the CTA's row, relative to M, over warp 0's
-                __syncwarp();
-#pragma unroll
-                for (int v = 0; v < D / 32; ++v) row[lane * (D / 32) + v] = acc[v];
-                if (lane == 0) *reinterpret_cast<float2 *>(row + D) = make_float2(M, sum);
-                continue;
-            }
-            const float inv = 1.f / sum;  // (a unit has a token, so the sum is above 0, or NaN)
-#pragma unroll
-            for (int v = 0; v < D / 32; ++v) acc[v] *= inv;
-            const float lse = (M + __log2f(sum)) * kLn2;
-            const size_t head = (size_t)c.kvh * G + g;
-            if (splits == 1) {
-                const size_t row_o = (size_t)ut.qrow[c.b] * a.num_q_heads + head;
-                store_out_vec<D / 32>(a.out, row_o * D + lane * (D / 32), acc, a.out_dtype);
-                if (a.lse && lane == 0) a.lse[row_o] = lse;
-            } else {
-                const size_t row_p = ((size_t)c.b * a.num_q_heads + head) * a.s_max + c.split;
-                store_out_vec<D / 32>(a.part_o, row_p * D + lane * (D / 32), acc, 2);
-                if (lane == 0) a.part_lse[row_p] = lse;
-            }
+            __syncwarp();
+            if (lane == 0) mbar_arrive(read);
+            mphase ^= 1u;
         }
-        __syncwarp();
-        if (lane == 0) mbar_arrive(read);
-        mphase ^= 1u;
+        if (!ok) break;
     }
     if (!ok) {
         // let copies in flight land before the CTA exits (bounded)
@@ -546,7 +569,7 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm)
         cluster_barrier();
         const int n = cluster_size();
         for (int g = warp * n + cluster_rank(); g < G; g += n * kWarps) {
-            const float *row = merge + (size_t)g * kMergeRow<D>;
+            const float *row = cta_rows + (size_t)g * kMergeRow<D>;
             const float2 ml = lane < n ? ld_cluster2(smem_of(row + D, lane)) : make_float2(-INFINITY, 0.f);
             float M = ml.x;
 #pragma unroll
@@ -694,7 +717,7 @@ __global__ void __launch_bounds__(128) merge_splits_kernel(CombineArgs a) {
 template <int D, int G, bool ONE>
 cudaError_t launch_t(const DecodeArgs &a, int grid, cudaStream_t s) {
     CUtensorMap tm;
-    cudaError_t e = encode_int8_map(a.cache, a.cache.block_size < kTile ? a.cache.block_size : kTile, 2, &tm);
+    cudaError_t e = encode_int8_map(a.cache, a.cache.block_size < kTile<D> ? a.cache.block_size : kTile<D>, 2, &tm);
     if (e != cudaSuccess) return e;
     auto kern = decode_int8_kernel<D, G, ONE>;
     static DeviceFlags configured;
@@ -710,7 +733,7 @@ cudaError_t launch_t(const DecodeArgs &a, int grid, cudaStream_t s) {
         cudaLaunchConfig_t cfg = {};
         cfg.gridDim = dim3((unsigned)(a.batch * a.cache.num_kv_heads * a.head_groups * a.cluster));
         cfg.blockDim = dim3(kThreads);
-        cfg.dynamicSmemBytes = Int8Layout<D, G>::smem_bytes(0, 0);
+        cfg.dynamicSmemBytes = Int8Layout<D, G>::smem_bytes_one();
         cfg.stream = s;
         cudaLaunchAttribute attr[2];
         attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
