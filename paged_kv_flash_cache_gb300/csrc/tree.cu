@@ -747,7 +747,13 @@ __global__ void __launch_bounds__(TreeLayout<D, FP8>::kThreads, 1)
                 bool ok = true;
                 for (int j = 0; j < T; ++j, ++tiles) {
                     if (j > 0) step(j < ahead ? 1u : 2u);
-                    if (!(ok = mbar_wait(&kv_full[slot], par, abort_flag, a.err))) break;
+                    // The slot's last tile first: it may have been a V tile, which these warps wait for nowhere else, and
+                    // while that is on its way this tile's parity still shows the one before. (The tiles before the
+                    // last one have landed: the K tile that these warps took last went into a slot that the products
+                    // had read, and they read the tiles in the ring's order.)
+                    if (!(ok = mbar_wait(&kv_full[slot], par ^ 1u, abort_flag, a.err) &&
+                               mbar_wait(&kv_full[slot], par, abort_flag, a.err)))
+                        break;
                     float *const sc = reinterpret_cast<float *>(smem + L::kScaleOff) + slot * 128u;
                     convert_rows<D, BF16, false, 32>(sRing + slot * L::kTileBytes, smem + L::kCodeOff + slot * (kBN * 64u),
                                                      sc, first, s.len - (s.t0 + j) * kBN, 0, lane);
