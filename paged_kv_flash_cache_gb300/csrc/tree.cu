@@ -747,11 +747,11 @@ __global__ void __launch_bounds__(TreeLayout<D, FP8>::kThreads, 1)
                 bool ok = true;
                 for (int j = 0; j < T; ++j, ++tiles) {
                     if (j > 0) step(j < ahead ? 1u : 2u);
-                    // The slot's last tile first: it may have been a V tile, which these warps wait for nowhere else, and
-                    // while that is on its way this tile's parity still shows the one before. (The tiles before the
-                    // last one have landed: the K tile that these warps took last went into a slot that the products
-                    // had read, and they read the tiles in the ring's order.)
-                    if (!(ok = mbar_wait(&kv_full[slot], par ^ 1u, abort_flag, a.err) &&
+                    // First that the products have read the slot's last tile. That may have been a V tile, which these warps wait
+                    // for nowhere else: while it is on its way, kv_full's parity shows the tile before as it would show this one.
+                    // kv_empty's own is plain: the use before that one was read before the K tile that these warps took last was
+                    // loaded (it lies at most three items back), and this tile is not read before it is converted.
+                    if (!(ok = mbar_wait(&kv_empty[slot], par ^ 1u, abort_flag, a.err) &&
                                mbar_wait(&kv_full[slot], par, abort_flag, a.err)))
                         break;
                     float *const sc = reinterpret_cast<float *>(smem + L::kScaleOff) + slot * 128u;
