@@ -304,7 +304,8 @@ __global__ void __launch_bounds__(kThreads, 1)
         auto scale_of = [&](int j, float &sk, float &sv) {
             sk = sv = 0.f;
             const int kv_start = j * kBN;
-            if (j >= n_tiles || kv_start + (lane << p.log2_bs) >= min(L, kv_start + kBN)) return;
+            // (pages behind kv_end: no row's weight is above 0, and W does not know them: 0, lest a factor overflow f16)
+            if (j >= n_tiles || kv_start + (lane << p.log2_bs) >= min(kv_end, kv_start + kBN)) return;
             int pb = __ldg(bt + (kv_start >> p.log2_bs) + lane);
             if (pb < 0 || pb >= p.num_blocks) pb = 0;
             const float *sc = p.scales + (size_t)pb * 2 * p.num_kv_heads + g;

@@ -94,6 +94,18 @@ def test_scales_that_are_no_powers_of_two():
     assert np.abs(out.double().cpu().numpy() - ref).max() < 4e-3 * np.abs(ref).max()
 
 
+@pytest.mark.parametrize("kv", [0, 1])
+@pytest.mark.parametrize("bs", [8, 16])
+def test_larger_scales_behind_a_row_block(bs, kv):
+    """Pages in the last key tile of a causal row block that none of its rows sees, with scales 2^14 times those before."""
+    lens, d = [552], 128                                       # rows 0-255 see keys up to 295, in the tile of keys 256-383
+    codes, scales = pool(-(-552 // bs) + 2, 1, bs, d, 21, 1)
+    tables = tables_of(lens, bs, codes.shape[0], -(-552 // bs) + 1, 21)
+    for i in range(-(-552 // bs)):
+        scales[tables[0, i], kv] = 2.0 ** (4 if i * bs >= 304 else -10)
+    run(lens, [512], 2, 1, d, bs, "f16", 21, codes=codes, scales=scales, scale=0.01)
+
+
 def test_scale_zero_and_below():
     run([200], [150], 2, 1, 64, 16, "f16", 11, scale=0.0)
     run([200], [150], 2, 1, 64, 16, "f16", 11, scale=-0.125)
