@@ -93,9 +93,13 @@ typedef enum { PKV_F16 = 0, PKV_BF16 = 1, PKV_F32 = 2 } pkv_dtype;
  *                   by at most half a step of the scale it was written with, and by less than one step
  *                   of the page's last scale in all, however often that grew. Rows with a NaN or an
  *                   infinity make the scale NaN: the page reads as NaN until it starts again with its first row.
- *                   Attention takes any finite scale >= 0 (caches quantised elsewhere): exactly in FP32
- *                   in the decode, rounded to 11 bits relative to the context's largest in the prefill
- *                   (powers of two are exact in both). */
+ *                   Caches quantised elsewhere: scales of 0 and from 2^-126 to 2^126, powers of two or not
+ *                   (smaller ones count as 0; behind older rows under a scale that is no power of two, the
+ *                   code of an x / s within 2^-16 of a tie may be either neighbour). Attention: the
+ *                   scales act in FP32 in the decode of up to 8 query heads per KV head. Its tcgen05
+ *                   kernels (the prefill; the decode of more heads) round code * scale to f16, relative to
+ *                   the largest scale of the keys that the CTA meets: exact for powers of two down to 2^-17
+ *                   of that, else within half a step of f16 or 2^-25 of it; and the weights once to f16. */
 typedef enum { PKV_KV_NATIVE = 0, PKV_KV_FP8_E4M3 = 1, PKV_KV_INT8_BLOCK = 2 } pkv_kv_format;
 
 /* The paged KV cache [num_blocks, 2, num_kv_heads, block_size, head_dim] ([FAPA] s3).

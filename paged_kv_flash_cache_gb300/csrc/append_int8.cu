@@ -193,7 +193,8 @@ __global__ void __launch_bounds__(kThreads, 6) append_int8_kernel(AppendArgs a, 
         return;
     }
     const size_t page = ((size_t)pb * 2 + kv) * hkv + h;
-    const float s_old = off > 0 ? a.scales[page] : 0.f;
+    float s_old = off > 0 ? a.scales[page] : 0.f;
+    if (s_old < 1.17549435e-38f) s_old = 0.f;  // (written elsewhere: below 2^-126, whose reciprocal can overflow)
 
     // ---- the largest magnitude ----
     uint32_t m2 = 0u;

@@ -34,6 +34,7 @@ def append(codes, scales, k, v, cu, ctx, tables):
                 for h in range(heads):
                     y = x[rows, h]
                     old = float(scales[page, i, h]) if off else 0.0
+                    old = 0.0 if old < 2.0 ** -126 else old
                     if not np.all(np.isfinite(y)) or not math.isfinite(old):
                         scales[page, i, h] = np.nan
                         codes[page, i, h, off:off + count] = 0

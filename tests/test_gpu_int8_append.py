@@ -112,6 +112,17 @@ def test_ends_of_the_range(dtype):
         run(codes, scales, k[15:18].contiguous(), v[15:18].contiguous(), [0, 3], [9], torch.tensor([[1]], dtype=torch.int32))
 
 
+@pytest.mark.parametrize("old", [1e-45, 1e-40, 2.0 ** -127])
+def test_an_older_scale_below_the_range(old):
+    """It counts as 0: rows of zeros leave 0, others start the page's scale, older codes become 0."""
+    codes, scales = pool(3, 1, 16, 64, 4)
+    scales[1:] = old
+    k, v = torch.zeros((2, 3, 1, 64), dtype=torch.bfloat16)
+    k[1, 0, 3], v[2, 0, 5] = 1e-38, -2e-39
+    run(codes, scales, k, v, [0, 3], [9], torch.tensor([[1]], dtype=torch.int32))
+    run(codes, scales, v * 0, k * 0, [0, 3], [9], torch.tensor([[2]], dtype=torch.int32))
+
+
 def test_what_is_not_a_number():
     """A NaN or an infinity makes its page's scale NaN, stays so, and leaves with the page's next start."""
     codes, scales = pool(4, 2, 16, 64, 9)
