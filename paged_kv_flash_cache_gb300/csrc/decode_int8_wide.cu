@@ -254,25 +254,15 @@ __global__ void __launch_bounds__(kThreads, 1)
         ok = ok && mbar_wait(w_ready, 0, abort_flag, a.err);
         const float wk = pow2_at_least(__uint_as_float(sMax[0])), wv = pow2_at_least(__uint_as_float(sMax[1]));
         const float ik = wk >= 1.17549435e-38f ? copysignf(1.f / wk, a.scale) : 0.f, iv = wv >= 1.17549435e-38f ? 1.f / wv : 0.f;
-        // lane i: the scales of page i of the tile, loaded a tile ahead
-        auto scale_of = [&](int j, float &sk, float &sv) {
-            sk = sv = 0.f;
-            const int kv_start = t0 + j * kBN;
-            if (j >= n_tiles || kv_start + (lane << log2_bs) >= min(t1, kv_start + kBN)) return;
-            int pb = __ldg(bt + (kv_start >> log2_bs) + lane);
-            if (pb < 0 || pb >= a.cache.num_blocks) pb = 0;
-            const float *sc = a.cache.scales + (size_t)pb * 2 * hkv + kvr;
-            sk = __ldg(sc);
-            sv = __ldg(sc + hkv);
-        };
-        float sk, sv;
-        scale_of(0, sk, sv);
+        TileScales sc = {a.cache.scales, bt, a.cache.num_blocks, hkv, kvr, log2_bs, t0, t1, lane, 0, 0.f, 0.f};
+        sc.page(0);
+        sc.load(0);
         for (int j = 0; ok && j < n_tiles; ++j) {
             // f16 factors of the tile's pages; what is not finite counts as 0 here (the rows are made NaN at the end)
-            const float fk = sk < INFINITY ? sk * ik : 0.f, fv = sv < INFINITY ? sv * iv : 0.f;
+            const float fk = sc.k < INFINITY ? sc.k * ik : 0.f, fv = sc.v < INFINITY ? sc.v * iv : 0.f;
             const uint32_t kk = pack_pair<false>(fk, fk), kv2 = pack_pair<false>(fv, fv);
             const bool pow2 = __all_sync(0xffffffffu, ((__float_as_uint(fk) | __float_as_uint(fv)) & 0x7fffffu) == 0u);
-            scale_of(j + 1, sk, sv);
+            sc.load(j + 1);
             for (int kv = 0; kv < 2; ++kv) {
                 const uint32_t u = 2u * j + kv, slot = u % kRing, cs = u % kCodes;
                 if (!(ok = mbar_wait(&code_full[cs], (u / kCodes) & 1u, abort_flag, a.err))) break;

@@ -33,44 +33,76 @@ __device__ __forceinline__ void codes4_f16(uint32_t w, uint32_t kk, uint32_t n, 
     }
 }
 
-// 32 rows r0 .. r0 + 31 of a tile by a warp: codes (rows of D bytes, 128-byte swizzle or, head_dim 64, 64-byte) to the f16
-// layout that TMA writes for a 16-bit cache (64-column halves of 128-byte rows, 128-byte swizzle), times the factor of
-// their page, which lane i holds for page i. Groups of 8 rows lie in one page.
+// 32 rows r0 .. r0 + 31 (r0 a multiple of 32) of a tile by a warp: codes (rows of D bytes, 128-byte swizzle or, head_dim 64,
+// 64-byte) to the f16 layout that TMA writes for a 16-bit cache (64-column halves of 128-byte rows, 128-byte swizzle), times the
+// factor of their page, which lane i holds for page i. Groups of 8 rows lie in one page.
 template <int D, bool POW2>
 __device__ __forceinline__ void convert_rows(const uint8_t *codes, uint8_t *f16, int r0, uint32_t kk, int log2_bs, int lane) {
     constexpr int kLanes = D / 16;             // lanes a row: 16 codes each
     constexpr int kRowsLoad = 32 / kLanes;     // rows a load of the warp: 4 (head_dim 128) or 8
-    constexpr int kLoads = 4;                  // loads in flight
+    constexpr int kLoads = 32 / kRowsLoad;
+    constexpr int kAhead = 4;                  // loads in flight
     const int c = lane % kLanes, rr = lane / kLanes;
+    uint32_t f[4], n[4];  // of the groups of 8 rows
+#pragma unroll
+    for (int q = 0; q < 4; ++q) {
+        f[q] = __shfl_sync(0xffffffffu, kk, ((r0 + 8 * q) >> log2_bs) & 31);
+        asm("mul.rn.f16x2 %0, %1, %2;" : "=r"(n[q]) : "r"(f[q]), "r"(0xe480e480u));
+    }
     // f16 chunks 2c and 2c + 1 (16 bytes each) of the row, in half c / 4; the lanes of the two halves store opposite chunks
     // first: the stores of a row in one instruction then fill all 32 banks once
-    const int hf = c >> 2, k0 = 2 * (c & 3), ka = k0 + hf, kb = k0 + 1 - hf;
+    const int hf = c >> 2, ka = 2 * (c & 3) + hf, kb = ka ^ 1;
+    const uint8_t *src = codes + (r0 + rr) * D;
+    uint8_t *dst = f16 + hf * kTileHalf + (r0 + rr) * 128;
+    auto load = [&](int i) {
+        const int r = i * kRowsLoad + rr;  // (its low bits: the row's)
+        return *reinterpret_cast<const uint4 *>(src + i * kRowsLoad * D + ((D == 128 ? c ^ (r & 7) : c ^ ((r >> 1) & 3)) << 4));
+    };
+    uint4 raw[kAhead];
 #pragma unroll
-    for (int b0 = 0; b0 < 32; b0 += kLoads * kRowsLoad) {
-        uint4 raw[kLoads];
+    for (int i = 0; i < kAhead; ++i) raw[i] = load(i);
 #pragma unroll
-        for (int i = 0; i < kLoads; ++i) {
-            const int r = r0 + b0 + i * kRowsLoad + rr;
-            const int cc = D == 128 ? c ^ (r & 7) : c ^ ((r >> 1) & 3);
-            raw[i] = *reinterpret_cast<const uint4 *>(codes + r * D + (cc << 4));
-        }
-#pragma unroll
-        for (int i = 0; i < kLoads; ++i) {
-            const int g = r0 + b0 + i * kRowsLoad, r = g + rr;
-            const uint32_t f = __shfl_sync(0xffffffffu, kk, (g >> log2_bs) & 31);
-            uint32_t nf;
-            asm("mul.rn.f16x2 %0, %1, %2;" : "=r"(nf) : "r"(f), "r"(0xe480e480u));
-            uint4 v0, v1;
-            codes4_f16<POW2>(raw[i].x, f, nf, v0.x, v0.y);
-            codes4_f16<POW2>(raw[i].y, f, nf, v0.z, v0.w);
-            codes4_f16<POW2>(raw[i].z, f, nf, v1.x, v1.y);
-            codes4_f16<POW2>(raw[i].w, f, nf, v1.z, v1.w);
-            uint8_t *row = f16 + hf * kTileHalf + r * 128;
-            *reinterpret_cast<uint4 *>(row + ((ka ^ (r & 7)) << 4)) = hf ? v1 : v0;
-            *reinterpret_cast<uint4 *>(row + ((kb ^ (r & 7)) << 4)) = hf ? v0 : v1;
-        }
+    for (int i = 0; i < kLoads; ++i) {
+        const uint4 x = raw[i % kAhead];
+        if (i + kAhead < kLoads) raw[i % kAhead] = load(i + kAhead);
+        const int q = i * kRowsLoad / 8, s = (i * kRowsLoad + rr) & 7;
+        uint4 va, vb;
+        codes4_f16<POW2>(hf ? x.z : x.x, f[q], n[q], va.x, va.y);
+        codes4_f16<POW2>(hf ? x.w : x.y, f[q], n[q], va.z, va.w);
+        codes4_f16<POW2>(hf ? x.x : x.z, f[q], n[q], vb.x, vb.y);
+        codes4_f16<POW2>(hf ? x.y : x.w, f[q], n[q], vb.z, vb.w);
+        uint8_t *row = dst + i * kRowsLoad * 128;
+        *reinterpret_cast<uint4 *>(row + ((ka ^ s) << 4)) = va;
+        *reinterpret_cast<uint4 *>(row + ((kb ^ s) << 4)) = vb;
     }
 }
+
+// The scales of a tile's pages, lane i those of page i, on their way while the tile before is converted: the page ids are
+// loaded a tile further ahead, so that no load waits for another one.
+struct TileScales {
+    const float *scales;
+    const int *bt;  // the sequence's pages
+    int num_blocks, num_kv_heads, head, log2_bs, from, to, lane;  // keys [from, to), tiles of 128 keys
+    int pb;
+    float k, v;  // 0: no page there
+    __device__ __forceinline__ bool has(int j) const {
+        const int key = from + j * 128 + (lane << log2_bs);
+        return (lane << log2_bs) < 128 && key < to;
+    }
+    __device__ __forceinline__ void page(int j) {
+        pb = has(j) ? __ldg(bt + ((from + j * 128) >> log2_bs) + lane) : 0;
+    }
+    __device__ __forceinline__ void load(int j) {  // of tile j, whose page ids are here; then the ids of tile j + 1
+        k = v = 0.f;
+        if (has(j)) {
+            const int p = pb < 0 || pb >= num_blocks ? 0 : pb;
+            const float *sc = scales + (size_t)p * 2 * num_kv_heads + head;
+            k = __ldg(sc);
+            v = __ldg(sc + num_kv_heads);
+        }
+        page(j + 1);
+    }
+};
 
 // q tiles (n16 16-byte vectors) from bf16 to f16 in place by 128 threads, exactly for |q| within f16's range.
 __device__ __forceinline__ void q_tiles_to_f16(uint8_t *sq, int n16, int t) {

@@ -300,27 +300,17 @@ __global__ void __launch_bounds__(kThreads, 1)
         ok = ok && mbar_wait(w_ready, 0, abort_flag, p.err);
         const float wk = pow2_at_least(__uint_as_float(sMax[0])), wv = pow2_at_least(__uint_as_float(sMax[1]));
         const float ik = wk >= 1.17549435e-38f ? copysignf(1.f / wk, p.scale_log2) : 0.f, iv = wv >= 1.17549435e-38f ? 1.f / wv : 0.f;
-        // lane i: the scales of page i of the tile, loaded a tile ahead
-        auto scale_of = [&](int j, float &sk, float &sv) {
-            sk = sv = 0.f;
-            const int kv_start = j * kBN;
-            // (pages behind kv_end: no row's weight is above 0, and W does not know them: 0, lest a factor overflow f16)
-            if (j >= n_tiles || kv_start + (lane << p.log2_bs) >= min(kv_end, kv_start + kBN)) return;
-            int pb = __ldg(bt + (kv_start >> p.log2_bs) + lane);
-            if (pb < 0 || pb >= p.num_blocks) pb = 0;
-            const float *sc = p.scales + (size_t)pb * 2 * p.num_kv_heads + g;
-            sk = __ldg(sc);
-            sv = __ldg(sc + p.num_kv_heads);
-        };
-        float sk, sv;
-        scale_of(0, sk, sv);
+        // (pages behind kv_end: no row's weight is above 0, and W does not know them: 0, lest a factor overflow f16)
+        TileScales sc = {p.scales, bt, p.num_blocks, p.num_kv_heads, g, p.log2_bs, 0, kv_end, lane, 0, 0.f, 0.f};
+        sc.page(0);
+        sc.load(0);
         for (int j = 0; ok && j < n_tiles; ++j) {
             // f16 factors of the tile's pages; what is not finite counts as 0 here (its rows are made NaN at the end)
-            const float fk = sk < INFINITY ? sk * ik : 0.f, fv = sv < INFINITY ? sv * iv : 0.f;
+            const float fk = sc.k < INFINITY ? sc.k * ik : 0.f, fv = sc.v < INFINITY ? sc.v * iv : 0.f;
             const uint32_t kk = pack_pair<false>(fk, fk), kv2 = pack_pair<false>(fv, fv);
             // (every factor of the tile a power of two, as kv_cache_append makes them)
             const bool pow2 = __all_sync(0xffffffffu, ((__float_as_uint(fk) | __float_as_uint(fv)) & 0x7fffffu) == 0u);
-            scale_of(j + 1, sk, sv);
+            sc.load(j + 1);
             for (int kv = 0; kv < 2; ++kv) {
                 const uint32_t u = 2u * j + kv, slot = u % kRing, cs = u % kCodes;
                 if (!(ok = mbar_wait(&code_full[cs], (u / kCodes) & 1u, abort_flag, p.err))) break;
