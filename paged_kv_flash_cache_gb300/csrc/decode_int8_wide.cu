@@ -13,8 +13,12 @@
 //   WG 1, 2    softmax of lane A / B, one head a thread (warps without heads have nothing to do); then B's sums go to A
 //              through shared memory, and A writes the output or the split's partial;
 //   WG 3       converters, as in prefill_int8.cu: 4 f16 tiles, K and V of each lane.
-// Weights are rounded once to f16 in the product with V (half a step, 2^-12 of a weight, 2^7 times themselves so that
+// Weights are rounded once to f16 in the product with V (half a step, 2^-11 of a weight; 2^7 times themselves, so that
 // small ones count), sums are FP32.
+//
+// 64 sequences x 8192 tokens, 1 KV head (134 MB): 47.5 us with 32 query heads, 56 with 128 (a bf16 cache: 56 and 109). A tile
+// takes 2300 cycles, of which the tensor cores work 1040: the four converter warps bound it (1275 of a tile's cycles converting,
+// 420 waiting for a tile whose products are not done). K two tiles ahead of V in their order: 54 us.
 #include <cuda.h>
 #include <cuda_runtime.h>
 

@@ -19,8 +19,10 @@
 //   WG 3       converters: Q to f16 once (a bf16 one), then the code buffers to one of 3 f16 tiles each, 32 rows a warp.
 // Conversion in a warpgroup of its own keeps it off the softmax, and code buffers apart from the f16 tiles let four loads
 // run ahead of the conversions. The issuing thread is chosen by elect.sync and has 80 registers: whatever delays the next
-// MMA delays everything. 4 x 512 queries of 32 heads over 8192 keys: 228 us (1.17 PFLOP/s, 60% of the dense rate); 290 with
-// codes converted in place and 48 registers for the issuing warp. The 256 CTAs are 1.7 rounds of the 152 SMs.
+// MMA delays everything. 4 x 512 queries of 32 heads over 8192 keys: 226 us (1.18 PFLOP/s, 60% of the dense rate); 290 with
+// codes converted in place and 48 registers for the issuing warp. The 256 CTAs are 1.7 rounds of the 152 SMs; a pair of tiles
+// takes 3080 cycles, 2048 of them in the tensor cores: the issuing thread waits 1150 for the weights (softmax), 210 for
+// conversions. P handed over in two halves, the second's exponentials under the first's product: 238 us.
 #include <cuda.h>
 #include <cuda_runtime.h>
 
