@@ -34,6 +34,7 @@
 // product with V and the others the remainders, in one mma; with more heads the remainders are a second mma.
 #include <cuda.h>
 
+#include "cluster.cuh"
 #include "decode_common.cuh"
 #include "pkv_device.cuh"
 #include "pkv_internal.h"
@@ -152,32 +153,6 @@ __device__ __forceinline__ int scan_units(const DecodeArgs &a, const UnitTable &
     if (tid < a.batch) t.ord[rank] = tid;
     __syncthreads();
     return t.first[S] * a.cache.num_kv_heads * a.head_groups;
-}
-
-// ---- thread-block clusters: ranks, barrier, loads from another CTA's shared memory ----
-__device__ __forceinline__ uint32_t cluster_rank() {
-    uint32_t r;
-    asm("mov.u32 %0, %%cluster_ctarank;" : "=r"(r));
-    return r;
-}
-__device__ __forceinline__ uint32_t cluster_size() {
-    uint32_t r;
-    asm("mov.u32 %0, %%cluster_nctarank;" : "=r"(r));
-    return r;
-}
-__device__ __forceinline__ void cluster_barrier() {  // every thread of every CTA
-    __syncwarp();
-    asm volatile("barrier.cluster.arrive.release.aligned;\n\tbarrier.cluster.wait.acquire.aligned;" ::: "memory");
-}
-__device__ __forceinline__ uint32_t smem_of(const void *p, uint32_t rank) {
-    uint32_t a;
-    asm("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(a) : "r"(smem_addr(p)), "r"(rank));
-    return a;
-}
-__device__ __forceinline__ float2 ld_cluster2(uint32_t addr) {
-    float2 v;
-    asm volatile("ld.shared::cluster.v2.f32 {%0, %1}, [%2];" : "=f"(v.x), "=f"(v.y) : "r"(addr) : "memory");
-    return v;
 }
 
 // ONE: a cluster takes the whole context of one (sequence, KV head's query group), a run of keys a CTA, and merges it

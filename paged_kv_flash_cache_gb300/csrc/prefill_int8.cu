@@ -8,8 +8,10 @@
 // scale, Wv into the epilogue's 1 / l. So the softmax and the MMAs are those of a 16-bit cache, and a scale costs one
 // packed multiplication per pair of codes, in warps that have time for it.
 //
-// CTA = one query head x 256 query rows of one sequence, as two 128-row tiles A and B that share every K/V tile (512
-// threads, four warpgroups):
+// CTA = 256 query rows of one sequence, as two 128-row tiles A and B that share every K/V tile: 256 tokens of one query head,
+// or, for short chunks, of P heads of a KV head's group (a divisor of it; 128 / P tokens a tile, row = token x P + head), whose
+// keys are then fetched and converted once. Few blocks over long contexts: a cluster of 2 to 8 CTAs takes a block, a run of its keys
+// each, and joins the rows (max, sum, output) over shared memory. A CTA's warps (512 threads, four warpgroups):
 //   warp 0     TMA producer: both Q tiles once; then for each 128-key tile the codes of K and of V, each into one of 4
 //              code buffers: a lane looks up a page in the block table and issues its box;
 //   warp 1     TMEM owner and MMA issuer (one thread). TMEM columns: S_A [0,128), S_B [128,256), O_A [256,256+D),
@@ -19,13 +21,18 @@
 //   WG 3       converters: Q to f16 once (a bf16 one), then the code buffers to one of 3 f16 tiles each, 32 rows a warp.
 // Conversion in a warpgroup of its own keeps it off the softmax, and code buffers apart from the f16 tiles let four loads
 // run ahead of the conversions. The issuing thread is chosen by elect.sync and has 80 registers: whatever delays the next
-// MMA delays everything. 4 x 512 queries of 32 heads over 8192 keys: 226 us (1.18 PFLOP/s, 60% of the dense rate); 290 with
+// MMA delays everything. 4 x 512 queries of 32 heads over 8192 keys: 225 us (1.18 PFLOP/s, 60% of the dense rate); 290 with
 // codes converted in place and 48 registers for the issuing warp. The 256 CTAs are 1.7 rounds of the 152 SMs; a pair of tiles
 // takes 3080 cycles, 2048 of them in the tensor cores: the issuing thread waits 1150 for the weights (softmax), 210 for
 // conversions. P handed over in two halves, the second's exponentials under the first's product: 238 us.
+// Short chunks, one sequence of 32 / 8 heads: 16 queries over 16000 keys 35 us (272 with a CTA for each head and 256 rows),
+// 256 queries over 16000 keys 73 (207), 16 over 1000 10 (23); 256 queries of 16 heads over 1000 keys 18 (22).
 #include <cuda.h>
 #include <cuda_runtime.h>
 
+#include <mutex>
+
+#include "cluster.cuh"
 #include "int8_tiles.cuh"
 #include "pkv_device.cuh"
 #include "pkv_internal.h"
@@ -59,6 +66,10 @@ struct Layout {
     static constexpr uint32_t kBarOff = kCodeOff + kCodes * kCodeBytes;
     static constexpr uint32_t kSmemBytes = kBarOff + 512 + 1024;  // + alignment slack
     static constexpr uint32_t kTmemCols = 512;
+    // a cluster's CTA: its rows at the end, over everything before the barriers: O, max, sum, what is not a number (16-byte
+    // stores of 8 threads, a row each, fill all 32 banks)
+    static constexpr int kRowFloats = D + 4;
+    static_assert(kRows * kRowFloats * 4 <= kBarOff, "the rows fit over tiles and codes");
 };
 
 struct Params {
@@ -66,6 +77,8 @@ struct Params {
     int batch, mb, num_q_heads, num_kv_heads, group, bs, log2_bs, num_blocks;
     float scale_log2;
     int causal;
+    int pack, tile_tokens;  // heads of a row block, tokens of a tile of it
+    int cluster;          // CTAs that share a row block's keys
     int skip_single;      // mixed batch: leave sequences with one query row to the decode kernels
     const float *scales;  // [NB, 2, Hkv]
     void *out;
@@ -74,8 +87,9 @@ struct Params {
     int *err;
 };
 
-// BF16: type of q and the default output; the products run in f16.
-template <int D, bool BF16>
+// BF16: type of q and the default output; the products run in f16. SHORT: blocks of packed heads, of one tile only, or shared
+// by a cluster (the other kernel knows that there is none of it: 225 us for the chunks above, 240 with SHORT).
+template <int D, bool BF16, bool SHORT>
 __global__ void __launch_bounds__(kThreads, 1)
     prefill_int8_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CUtensorMap tm_kv, Params p) {
     using Lay = Layout<D>;
@@ -106,24 +120,30 @@ __global__ void __launch_bounds__(kThreads, 1)
     // the row blocks that see the most keys (causal) start in the first wave and the short ones
     // fill in behind them. A mixed batch: (heads, row blocks last-first, sequences by their rank
     // among those with several query rows), so that no CTA without work precedes one with work.
-    const int h = blockIdx.x;
+    const int n_cta = SHORT ? p.cluster : 1, pack = SHORT ? p.pack : 1, tile_tokens = SHORT ? p.tile_tokens : kBM;
+    const int rank = n_cta > 1 ? cluster_rank() : 0;
+    const int h = (int)blockIdx.x / n_cta * pack;  // the block's first head
     const int mt = p.skip_single ? (int)gridDim.y - 1 - (int)blockIdx.y : (int)gridDim.z - 1 - (int)blockIdx.z;
     pdl_wait();  // lengths, tables, q and the chunk's own K/V may come from the previous kernel
     const int b = p.skip_single ? nth_multi_row_sequence(p.cu_q_lens, p.batch, blockIdx.z) : (int)blockIdx.y;
     if (b < 0) return;  // uniform: past the mixed batch's last chunk
     const int q0 = __ldg(p.cu_q_lens + b);
     const int q_len = __ldg(p.cu_q_lens + b + 1) - q0;
-    const int m_start = mt * kRows;
+    const int m_start = mt * 2 * tile_tokens;
     if (m_start >= q_len || (p.skip_single && q_len == 1)) return;  // uniform: nothing allocated yet
     const int L = __ldg(p.context_lens + b);
     if (L > p.mb * p.bs || q_len > L || L < 0) {
         if (threadIdx.x == 0) set_error(p.err, kErrDeviceRange);
         return;
     }
-    const int rows = min(kRows, q_len - m_start);
-    const int qpos0 = L - q_len + m_start;           // absolute position of row 0
-    const int kv_end = p.causal ? qpos0 + rows : L;  // keys [0, kv_end) are needed
-    const int n_tiles = (kv_end + kBN - 1) / kBN;
+    const int tokens = min(2 * tile_tokens, q_len - m_start);
+    const bool two = !SHORT || tokens > tile_tokens;    // tile B has rows (or takes part without)
+    const int qpos0 = L - q_len + m_start;             // absolute position of row 0
+    const int all_end = p.causal ? qpos0 + tokens : L;  // keys [0, all_end) are needed,
+    const int per = ((all_end + kBN - 1) / kBN + n_cta - 1) / n_cta * kBN;
+    // [kv0, kv_end) by this CTA (maybe none)
+    const int kv0 = SHORT ? min(rank * per, all_end) : 0, kv_end = SHORT ? min(kv0 + per, all_end) : all_end;
+    const int n_tiles = (kv_end - kv0 + kBN - 1) / kBN;
     const int g = h / p.group;
     const int *bt = p.block_tables + (size_t)b * p.mb;
 
@@ -159,6 +179,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     tc::fence_after_sync();
     const uint32_t tmem = *tmem_slot;
 
+    // (a cluster's two barriers, at the end of each role: its registers differ)
     if (warp < 4) {
         tc::regs_dec<80>();
         if (warp == 0) {
@@ -168,17 +189,16 @@ __global__ void __launch_bounds__(kThreads, 1)
             if (lane == 0) {
                 tc::prefetch_tensormap(&tm_q);
                 tc::prefetch_tensormap(&tm_kv);
-                mbar_arrive_expect_tx(q_full, 2 * Lay::kQBytes);
-#pragma unroll
-                for (int x = 0; x < 2; ++x)
+                mbar_arrive_expect_tx(q_full, (uint32_t)((two ? 2 : 1) * tile_tokens * pack) * 128u * Lay::kHalves);
+                for (int x = 0; x < (two ? 2 : 1); ++x)
 #pragma unroll
                     for (int hf = 0; hf < Lay::kHalves; ++hf)
                         tc::tma_load_3d(sQ + x * Lay::kQBytes + hf * kTileHalf, &tm_q, hf * 64, h,
-                                        q0 + m_start + x * kBM, q_full);
+                                        q0 + m_start + x * tile_tokens, q_full);
             }
             bool ok = true;
             for (int j = 0; j < n_tiles && ok; ++j) {
-                const int kv_start = j * kBN;
+                const int kv_start = kv0 + j * kBN;
                 const int n_valid = min(kBN, L - kv_start);
                 const int npages = p.bs < kBN ? (n_valid + p.bs - 1) >> p.log2_bs : 1;
                 const int off = p.bs < kBN ? 0 : (kv_start & (p.bs - 1));
@@ -210,7 +230,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             }
         } else if (warp == 1) {
             // ===================================== MMA issuer =====================================
-            if (tc::elect_one()) {
+            if ((!SHORT || n_tiles > 0) && tc::elect_one()) {
                 const uint32_t id_qk = tc::idesc_f16(false, kBM, kBN, false);
                 const uint32_t id_pv = tc::idesc_f16(false, kBM, D, true);
                 const uint32_t aQ = smem_addr(sQ), aRing = smem_addr(sRing);
@@ -242,7 +262,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                 if (ok) {
                     tc::fence_after_sync();
                     qk(0, aRing);  // S_A = Q_A K_0^T
-                    qk(1, aRing);  // S_B = Q_B K_0^T
+                    if (two) qk(1, aRing);  // S_B = Q_B K_0^T
                     tc::mma_commit(&kv_empty[0]);
                 }
                 // Ping-pong: tile A's P V_j then its next S, then tile B's. P_x sits in S_x's columns;
@@ -261,12 +281,14 @@ __global__ void __launch_bounds__(kThreads, 1)
                         if (!(ok = ring_wait(uKn))) break;
                         qk(0, aKn);
                     }
-                    if (!(ok = mbar_wait(&p_full[1], ph, abort_flag, p.err))) break;
-                    tc::fence_after_sync();
-                    pv(1, aV, j);
+                    if (two) {
+                        if (!(ok = mbar_wait(&p_full[1], ph, abort_flag, p.err))) break;
+                        tc::fence_after_sync();
+                        pv(1, aV, j);
+                    }
                     tc::mma_commit(&kv_empty[uV % kRing]);
                     if (more) {
-                        qk(1, aKn);
+                        if (two) qk(1, aKn);
                         tc::mma_commit(&kv_empty[uKn % kRing]);
                     }
                 }
@@ -276,13 +298,17 @@ __global__ void __launch_bounds__(kThreads, 1)
             }
             __syncwarp();
         }
+        if (n_cta > 1) {
+            cluster_barrier();
+            cluster_barrier();
+        }
     } else if (warp >= 12) {
         tc::regs_dec<64>();
         // ===================================== converters =====================================
         const int cw = warp - 12;
         // ---- Wk, Wv over the pages of keys [0, kv_end); a page id outside the pool: page 0, as the producer reads it ----
         {
-            page_scales(p.scales, bt, p.num_blocks, p.num_kv_heads, g, p.log2_bs, 0, kv_end, cw * 32 + lane, sMax, sNan);
+            page_scales(p.scales, bt, p.num_blocks, p.num_kv_heads, g, p.log2_bs, kv0, kv_end, cw * 32 + lane, sMax, sNan);
             if (lane == 0) mbar_arrive(w_ready);
             __syncwarp();
         }
@@ -291,7 +317,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             // q to f16 in place (exact for |q| within f16's range)
             ok = mbar_wait(q_full, 0, abort_flag, p.err);
             if (ok) {
-                q_tiles_to_f16(sQ, 2 * (int)Lay::kQBytes / 16, cw * 32 + lane);
+                q_tiles_to_f16(sQ, (two ? 2 : 1) * (int)Lay::kQBytes / 16, cw * 32 + lane);
                 tc::fence_proxy_async_smem();
             }
         } else {
@@ -303,7 +329,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         const float wk = pow2_at_least(__uint_as_float(sMax[0])), wv = pow2_at_least(__uint_as_float(sMax[1]));
         const float ik = wk >= 1.17549435e-38f ? copysignf(1.f / wk, p.scale_log2) : 0.f, iv = wv >= 1.17549435e-38f ? 1.f / wv : 0.f;
         // (pages behind kv_end: no row's weight is above 0, and W does not know them: 0, lest a factor overflow f16)
-        TileScales sc = {p.scales, bt, p.num_blocks, p.num_kv_heads, g, p.log2_bs, 0, kv_end, lane, 0, 0.f, 0.f};
+        TileScales sc = {p.scales, bt, p.num_blocks, p.num_kv_heads, g, p.log2_bs, kv0, kv_end, lane, 0, 0.f, 0.f};
         sc.page(0);
         sc.load(0);
         for (int j = 0; ok && j < n_tiles; ++j) {
@@ -329,15 +355,21 @@ __global__ void __launch_bounds__(kThreads, 1)
                 }
             }
         }
+        if (n_cta > 1) {
+            cluster_barrier();
+            cluster_barrier();
+        }
     } else {
         tc::regs_inc<184>();
         // ================================= softmax + epilogue =================================
         const int x = (warp >> 2) - 1;                 // 0: tile A, 1: tile B
         const int quarter = warp & 3;                  // TMEM lanes 32*quarter .. +31
         const int r = quarter * 32 + lane;             // row within the tile
-        const int row = x * kBM + r;                   // row within the CTA block
-        const bool row_ok = row < rows;
-        const int qpos = qpos0 + row;
+        const int tile_rows = (x == 0 ? min(tokens, tile_tokens) : tokens - tile_tokens) * pack;
+        const bool row_ok = r < tile_rows;
+        const bool warp_ok = !SHORT || quarter * 32 < tile_rows;  // (uniform)
+        const int token = x * tile_tokens + r / pack;  // of the block
+        const int qpos = qpos0 + token;
         const uint32_t lane_base = (uint32_t)(quarter * 32) << 16;
         const uint32_t tS = tmem + kColS + 128u * x + lane_base;   // S_x, and P_x over its first 64 columns
         const uint32_t tO = tmem + kColO + 128u * x + lane_base;
@@ -346,20 +378,24 @@ __global__ void __launch_bounds__(kThreads, 1)
         // (never 0, which times a masked score's -inf would be NaN; a negative scale has its sign in K)
         const float wk = pow2_at_least(__uint_as_float(sMax[0]));
         const float c = fmaxf(fabsf(p.scale_log2 * (wk > 0.f ? wk : 1.f)), 1.17549435e-38f);
-        for (int j = 0; ok && j < n_tiles; ++j) {
-            const int kv_start = j * kBN;
+        for (int j = 0; ok && j < n_tiles && (x == 0 || two); ++j) {
+            const int kv_start = kv0 + j * kBN;
             const uint32_t ph = (uint32_t)j & 1u;
             if (!(ok = mbar_wait(&s_full[x], ph, abort_flag, p.err))) break;
             tc::fence_after_sync();
+            if (!warp_ok) {  // (a product's row touches no other row: what these hold does not matter)
+                tc::fence_before_sync();
+                if (lane == 0) mbar_arrive(&p_full[x]);
+                continue;
+            }
             float s[kBN];
 #pragma unroll
             for (int cc = 0; cc < kBN / 32; ++cc)
                 tc::tmem_ld32(tS + cc * 32, *reinterpret_cast<float(*)[32]>(&s[cc * 32]));
             tc::tmem_wait_ld();
-            // last key index this row may see in this tile (-1: none)
+            // last key index this row may see in this tile (below 0: none; a row behind the last one: as the last)
             int lim = L - 1 - kv_start;
             if (p.causal) lim = min(lim, qpos - kv_start);
-            if (!row_ok) lim = -1;
             if (lim < kBN - 1) {
 #pragma unroll
                 for (int i = 0; i < kBN; ++i) s[i] = (i <= lim) ? s[i] : -INFINITY;
@@ -419,17 +455,39 @@ __global__ void __launch_bounds__(kThreads, 1)
             __syncwarp();
             if (lane == 0) mbar_arrive(&p_full[x]);
         }
-        // ---- epilogue: O / l ----
-        if (ok && mbar_wait(&o_done[x], (uint32_t)(n_tiles - 1) & 1u, abort_flag, p.err)) {
+        // ---- epilogue: O / l; of a cluster's CTA: O, max and sum to its shared memory, once every product is done ----
+        const int last = p.causal ? qpos : L - 1;
+        const float nan = __uint_as_float(0x7fc00000u);
+        // a row that sees a key of a page whose scale is not finite is NaN
+        const bool nan_k = last >= sNan[0], nan_v = last >= sNan[1];
+        const float wv = pow2_at_least(__uint_as_float(sMax[1]));
+        if (n_cta > 1) {
+            float *out_row = reinterpret_cast<float *>(smem) + (size_t)(x * kBM + r) * Lay::kRowFloats;
+            if (ok && n_tiles > 0)
+                ok = mbar_wait(&o_done[0], (uint32_t)(n_tiles - 1) & 1u, abort_flag, p.err) &&
+                     (!two || mbar_wait(&o_done[1], (uint32_t)(n_tiles - 1) & 1u, abort_flag, p.err));
+            else if (ok)
+                ok = mbar_wait(q_ready, 0, abort_flag, p.err);  // (no keys: q is still on its way to where the rows go)
             tc::fence_after_sync();
-            // a row that sees a key of a page whose scale is not finite is NaN
-            const int last = p.causal ? qpos : L - 1;
-            const float nan = __uint_as_float(0x7fc00000u);
-            const bool nan_k = last >= sNan[0], nan_v = last >= sNan[1];
-            const float wv = pow2_at_least(__uint_as_float(sMax[1]));
+            if (ok && warp_ok) {
+                if (n_tiles > 0) {
+#pragma unroll
+                    for (int cc = 0; cc < D / 32; ++cc) {
+                        float o[32];
+                        tc::tmem_ld32(tO + cc * 32, o);
+                        tc::tmem_wait_ld();
+#pragma unroll
+                        for (int i = 0; i < 32; i += 4)
+                            *reinterpret_cast<float4 *>(out_row + cc * 32 + i) =
+                                make_float4(o[i] * wv, o[i + 1] * wv, o[i + 2] * wv, o[i + 3] * wv);
+                    }
+                }
+                *reinterpret_cast<float4 *>(out_row + D) = make_float4(m_use, l, nan_k ? 2.f : nan_v ? 1.f : 0.f, 0.f);
+            }
+        } else if (ok && warp_ok && mbar_wait(&o_done[x], (uint32_t)(n_tiles - 1) & 1u, abort_flag, p.err)) {
+            tc::fence_after_sync();
             const float inv = nan_k || nan_v ? nan : l > 0.f ? wv / l : 0.f;
-            const size_t row_g = (size_t)(q0 + m_start + row);
-            const size_t obase = (row_g * p.num_q_heads + h) * D;
+            const size_t orow = (size_t)(q0 + m_start + token) * p.num_q_heads + h + r % pack;
 #pragma unroll
             for (int cc = 0; cc < D / 32; ++cc) {
                 float o[32];
@@ -441,13 +499,78 @@ __global__ void __launch_bounds__(kThreads, 1)
                         float v[8];
 #pragma unroll
                         for (int k = 0; k < 8; ++k) v[k] = o[8 * i + k] * inv;
-                        store_out_vec<8>(p.out, obase + cc * 32 + 8 * i, v, p.out_dtype);
+                        store_out_vec<8>(p.out, orow * D + cc * 32 + 8 * i, v, p.out_dtype);
                     }
                 }
             }
             if (row_ok && p.lse)
-                p.lse[row_g * p.num_q_heads + h] =
-                    nan_k ? nan : l > 0.f ? (m_use + (__log2f(l) - kWeightLog2)) * kLn2 : -INFINITY;
+                p.lse[orow] = nan_k ? nan : l > 0.f ? (m_use + (__log2f(l) - kWeightLog2)) * kLn2 : -INFINITY;
+        }
+        if (n_cta > 1) {
+            // ---- the cluster's rows: row i by a softmax warp of CTA i % cluster; every CTA comes here, whatever its waits did ----
+            cluster_barrier();
+            if (!*abort_flag) {
+                // as many rows at a time as make 8 (row, CTA) pairs, whose loads are in flight together; lanes 8 r + i: the
+                // max and sum of the batch's row r in CTA i
+                const int batch = 8 / n_cta, step = 8 * n_cta;
+                const int rows = two ? kBM + (tokens - tile_tokens) * pack : tokens * pack;
+                auto has = [&](int row) { return row < rows && (row & (kBM - 1)) < tile_tokens * pack; };
+                for (int r0 = (warp - 4) * n_cta + rank; r0 < rows; r0 += batch * step) {
+                    const float *first = reinterpret_cast<const float *>(smem);
+                    const int lr = r0 + (lane >> 3) * step, li = lane & 7;
+                    float m = -INFINITY, l = 0.f, bad = 0.f;
+                    if ((lane >> 3) < batch && has(lr) && li < n_cta) {
+                        float x4[4];
+                        ld_cluster(smem_of(first + (size_t)lr * Lay::kRowFloats + D, li), x4);
+                        m = x4[0], l = x4[1], bad = x4[2];
+                    }
+                    float v[8][D / 32];
+#pragma unroll
+                    for (int k = 0, r = 0, i = 0; k < 8; ++k) {
+                        const int at_row = r0 + r * step;
+                        if (r < batch && has(at_row)) {
+                            ld_cluster(smem_of(first + (size_t)at_row * Lay::kRowFloats + lane * (D / 32), i), v[k]);
+                        }
+                        if (++i == n_cta) i = 0, ++r;
+                    }
+                    float M = m;
+#pragma unroll
+                    for (int i = 4; i > 0; i >>= 1) {
+                        M = fmaxf(M, __shfl_xor_sync(0xffffffffu, M, i));
+                        bad = fmaxf(bad, __shfl_xor_sync(0xffffffffu, bad, i));
+                    }
+                    const float w = m == -INFINITY ? 0.f : ex2f(m - M);
+                    float sum = w * l;
+#pragma unroll
+                    for (int i = 4; i > 0; i >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, i);
+                    float acc[D / 32];
+#pragma unroll
+                    for (int k = 0, r = 0, i = 0; k < 8; ++k) {
+                        const int at_row = r0 + r * step;
+                        const float wk = __shfl_sync(0xffffffffu, w, (8 * r + i) & 31);
+#pragma unroll
+                        for (int c = 0; c < D / 32; ++c) {
+                            if (i == 0) acc[c] = 0.f;
+                            if (wk != 0.f) acc[c] = fmaf(wk, v[k][c], acc[c]);  // (0: nothing there, or nothing of it left)
+                        }
+                        if (++i == n_cta) {
+                            const float s = __shfl_sync(0xffffffffu, sum, (8 * r) & 31), b8 = __shfl_sync(0xffffffffu, bad, (8 * r) & 31);
+                            const float top = __shfl_sync(0xffffffffu, M, (8 * r) & 31);
+                            if (r < batch && has(at_row)) {
+                                const float inv = b8 > 0.f ? nan : s > 0.f ? 1.f / s : s;
+                                const int tr = at_row & (kBM - 1), tok = (at_row / kBM) * tile_tokens + tr / pack;
+                                const size_t orow = (size_t)(q0 + m_start + tok) * p.num_q_heads + h + tr % pack;
+#pragma unroll
+                                for (int c = 0; c < D / 32; ++c) acc[c] *= inv;
+                                store_out_vec<D / 32>(p.out, orow * D + lane * (D / 32), acc, p.out_dtype);
+                                if (lane == 0 && p.lse) p.lse[orow] = b8 > 1.f ? nan : (top + (__log2f(s) - kWeightLog2)) * kLn2;
+                            }
+                            i = 0, ++r;
+                        }
+                    }
+                }
+            }
+            cluster_barrier();  // (no CTA leaves before its rows have been read)
         }
     }
     tc::fence_before_sync();
@@ -459,15 +582,103 @@ __global__ void __launch_bounds__(kThreads, 1)
     }
 }
 
+// Heads of a row block: the largest divisor of a group with which chunks of max_q_len tokens fit one block.
+int pack_heads(int group, int max_q_len) {
+    int n = 1;
+    for (int d = 2; d <= group && d <= kBM; ++d)
+        if (group % d == 0 && 2 * (kBM / d) >= max_q_len) n = d;
+    return n;
+}
+
+template <int D, bool BF16, bool SHORT>
+auto configured_kernel(cudaError_t &e) {
+    auto kern = prefill_int8_kernel<D, BF16, SHORT>;
+    static DeviceFlags configured;
+    const int dev = device_info().device;
+    e = cudaSuccess;
+    if (!configured.test(dev)) {
+        e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)Layout<D>::kSmemBytes);
+        if (e == cudaSuccess) configured.set(dev);
+    }
+    return kern;
+}
+
+// Clusters of 1 to 8 CTAs, an SM each, that the device runs at once (a cluster lies in one GPC, so that a few SMs stay out):
+// asked once a device.
+template <int D, bool BF16>
+cudaError_t clusters_at_once(int (&out)[9]) {
+    static int table[64][9];
+    static DeviceFlags known;
+    static std::mutex filling;
+    cudaError_t e;
+    auto kern = configured_kernel<D, BF16, true>(e);
+    if (e != cudaSuccess) return e;
+    const int dev = device_info().device;
+    if (!known.test(dev)) {
+        out[0] = 0;
+        out[1] = device_info().num_sms;
+        for (int n = 2; n <= 8; ++n) {
+            cudaLaunchConfig_t cfg = {};
+            cfg.gridDim = dim3((unsigned)n);
+            cfg.blockDim = dim3(kThreads);
+            cfg.dynamicSmemBytes = Layout<D>::kSmemBytes;
+            cudaLaunchAttribute attr;
+            attr.id = cudaLaunchAttributeClusterDimension;
+            attr.val.clusterDim.x = (unsigned)n;
+            attr.val.clusterDim.y = attr.val.clusterDim.z = 1;
+            cfg.attrs = &attr;
+            cfg.numAttrs = 1;
+            if ((e = cudaOccupancyMaxActiveClusters(&out[n], kern, &cfg)) != cudaSuccess) return e;
+        }
+        if (dev >= 0 && dev < 64) {
+            std::lock_guard<std::mutex> lock(filling);
+            for (int n = 0; n <= 8; ++n) table[dev][n] = out[n];
+            known.set(dev);
+        }
+        return cudaSuccess;
+    }
+    for (int n = 0; n <= 8; ++n) out[n] = table[dev][n];
+    return cudaSuccess;
+}
+
+// CTAs of a cluster that share a row block's keys, by the time that the launch takes for full tables: rounds of clusters, each a
+// share of the key tiles and what a CTA costs besides (kStart tiles' time; kJoin more for a cluster: 100 queries over 500 keys
+// take 14.8 us in clusters or not).
+int cluster_of(long long blocks, long long capacity, const int (&at_once)[9]) {
+    constexpr long long kStart = 5, kJoin = 4;
+    const long long tiles = (capacity + kBN - 1) / kBN;
+    int best = 1;
+    long long best_cost = -1;
+    for (int n = 1; n <= 8; ++n) {
+        if (at_once[n] <= 0) continue;
+        const long long cost = (blocks + at_once[n] - 1) / at_once[n] * ((tiles + n - 1) / n + kStart + (n > 1 ? kJoin : 0));
+        if (best_cost < 0 || cost < best_cost) {
+            best_cost = cost;
+            best = n;
+        }
+    }
+    return best;
+}
+
 template <int D, bool BF16>
 cudaError_t launch_t(const PrefillArgs &a, cudaStream_t stream) {
-    using Lay = Layout<D>;
+    Params p;
+    p.group = a.num_q_heads / a.cache.num_kv_heads;
+    p.pack = pack_heads(p.group, a.max_q_len);
+    p.tile_tokens = kBM / p.pack;
+    const int block = 2 * p.tile_tokens;  // tokens of a row block
+    const unsigned row_blocks = (unsigned)((a.max_q_len + block - 1) / block), heads = (unsigned)(a.num_q_heads / p.pack);
+    const long long by_grid = (long long)a.batch * row_blocks, by_rows = (long long)a.total_q / block + a.batch;
+    int at_once[9];
+    cudaError_t e = clusters_at_once<D, BF16>(at_once);
+    if (e != cudaSuccess) return e;
+    p.cluster = cluster_of(heads * (by_grid < by_rows ? by_grid : by_rows), (long long)a.max_blocks_per_seq * a.cache.block_size,
+                           at_once);
     CUtensorMap tm_q, tm_kv;
-    cudaError_t e = encode_q_heads_map(a.q, BF16 ? 1 : 0, a.total_q, a.num_q_heads, D, kBM, &tm_q);
+    e = encode_q_group_map(a.q, BF16 ? 1 : 0, a.total_q, a.num_q_heads, D, p.pack, p.tile_tokens, &tm_q);
     if (e != cudaSuccess) return e;
     e = encode_int8_map(a.cache, a.cache.block_size < kBN ? a.cache.block_size : kBN, 1, &tm_kv);
     if (e != cudaSuccess) return e;
-    Params p;
     p.cu_q_lens = a.cu_q_lens;
     p.context_lens = a.context_lens;
     p.block_tables = a.block_tables;
@@ -475,7 +686,6 @@ cudaError_t launch_t(const PrefillArgs &a, cudaStream_t stream) {
     p.mb = a.max_blocks_per_seq;
     p.num_q_heads = a.num_q_heads;
     p.num_kv_heads = a.cache.num_kv_heads;
-    p.group = a.num_q_heads / a.cache.num_kv_heads;
     p.bs = a.cache.block_size;
     p.log2_bs = a.cache.log2_block_size;
     p.num_blocks = a.cache.num_blocks;
@@ -487,17 +697,24 @@ cudaError_t launch_t(const PrefillArgs &a, cudaStream_t stream) {
     p.out_dtype = a.out_dtype;
     p.lse = a.lse;
     p.err = a.err;
-    auto kern = prefill_int8_kernel<D, BF16>;
-    static DeviceFlags configured;
-    const int dev = device_info().device;
-    if (!configured.test(dev)) {
-        e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)Lay::kSmemBytes);
-        if (e != cudaSuccess) return e;
-        configured.set(dev);
-    }
-    const unsigned row_blocks = (unsigned)((a.max_q_len + kRows - 1) / kRows);
-    const dim3 grid = a.skip_single ? dim3(a.num_q_heads, row_blocks, a.batch) : dim3(a.num_q_heads, a.batch, row_blocks);
-    return launch_pdl(kern, grid, dim3(kThreads), Lay::kSmemBytes, stream, tm_q, tm_kv, p);
+    const bool is_short = p.cluster > 1 || p.pack > 1 || a.max_q_len <= kBM;
+    auto kern = is_short ? configured_kernel<D, BF16, true>(e) : configured_kernel<D, BF16, false>(e);
+    if (e != cudaSuccess) return e;
+    const unsigned x = heads * (unsigned)p.cluster;
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = a.skip_single ? dim3(x, row_blocks, a.batch) : dim3(x, a.batch, row_blocks);
+    cfg.blockDim = dim3(kThreads);
+    cfg.dynamicSmemBytes = Layout<D>::kSmemBytes;
+    cfg.stream = stream;
+    cudaLaunchAttribute attr[2];
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    attr[1].id = cudaLaunchAttributeClusterDimension;
+    attr[1].val.clusterDim.x = (unsigned)p.cluster;
+    attr[1].val.clusterDim.y = attr[1].val.clusterDim.z = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = p.cluster > 1 ? 2 : 1;
+    return cudaLaunchKernelEx(&cfg, kern, tm_q, tm_kv, p);
 }
 
 }  // namespace

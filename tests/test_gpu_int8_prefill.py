@@ -153,6 +153,74 @@ def test_what_is_not_a_number():
         assert torch.isfinite(lse[:48]).all() and torch.isnan(lse[48:96]).all() == (kv == 0)
 
 
+@pytest.mark.parametrize("d", [64, 128])
+@pytest.mark.parametrize("hq,heads,new", [(2, 1, [1, 127, 128]), (8, 2, [64, 63]), (8, 2, [65, 3]), (6, 1, [50, 128]), (5, 1, [9]),
+                                          (16, 1, [16, 1, 5]), (40, 1, [31, 32]), (64, 1, [4, 3, 2]), (128, 1, [2, 1]),
+                                          (256, 1, [1, 1]), (24, 2, [20, 21]), (12, 4, [100])])
+def test_short_chunks(hq, heads, new, d):
+    """Rows of several heads in one block: every number of heads that a block takes, blocks of one tile and of two."""
+    run([n + 37 * i + 5 for i, n in enumerate(new)], new, hq, heads, d, 16, "bf16", hq + new[0])
+
+
+@pytest.mark.parametrize("causal", [True, False])
+@pytest.mark.parametrize("hq", [1, 2, 3, 5, 11, 17])
+@pytest.mark.parametrize("lens,new", [([3000], [200]), ([2100, 1, 300], [20, 1, 300]), ([1500, 1400], [130, 256])])
+def test_blocks_shared_by_several_ctas(lens, new, hq, causal):
+    """Few blocks over long contexts, from 2 to 8 CTAs a block; some of them without a key of theirs, or with masked ones only."""
+    run(lens, new, hq, hq, 64, 16, "f16", hq, causal=causal)
+
+
+@pytest.mark.parametrize("hq,heads,d,bs", [(8, 2, 128, 8), (4, 1, 128, 512), (32, 2, 64, 64), (16, 16, 128, 128)])
+def test_shared_blocks_of_short_chunks(hq, heads, d, bs):
+    run([4000, 700, 2500], [33, 5, 64], hq, heads, d, bs, "bf16", bs)
+    run([4000, 700, 2500], [33, 1, 64], hq, heads, d, bs, "bf16", bs, mixed=True)
+
+
+@pytest.mark.parametrize("kv", [0, 1])
+def test_not_a_number_in_a_shared_block(kv):
+    """Only the rows that see the page are NaN, whichever CTA had it; pages behind the last key do not count."""
+    d, bs, n, new = 128, 16, 3000, 250
+    codes, scales = pool(200, 1, bs, d, 5)
+    tables = torch.randperm(200, generator=torch.Generator().manual_seed(2))[:190].to(torch.int32)[None]
+    q = torch.randn((new, 4, d), generator=torch.Generator().manual_seed(3)).half()
+
+    def call(s):
+        lse = torch.empty((new, 4), device="cuda")
+        out = pkv.paged_attn_prefill(codes.cuda(), q.cuda(), torch.tensor([0, new], dtype=torch.int32).cuda(),
+                                     torch.tensor([n], dtype=torch.int32).cuda(), tables.cuda(), max_q_len=new, lse=lse,
+                                     scales=s.cuda())
+        assert pkv.get_device_error() == 0
+        return out, lse
+
+    want, want_lse = call(scales)
+    for page, value in ((181, float("nan")), (3, float("inf")), (188, float("nan"))):
+        s = scales.clone()
+        s[tables[0, page], kv] = value
+        out, lse = call(s)
+        first = min(new, max(0, page * bs - (n - new)))        # the first row that sees it
+        assert torch.equal(out[:first], want[:first]) and torch.isnan(out[first:]).all()
+        assert torch.equal(lse[:first], want_lse[:first])
+        assert torch.isnan(lse[first:]).all() if kv == 0 else torch.equal(lse[first:], want_lse[first:])
+
+
+def test_shared_blocks_again_and_again():
+    """The same bits from call to call, in a graph too."""
+    codes, scales = pool(130, 2, 16, 128, 6)
+    i = lambda v: torch.tensor(v, dtype=torch.int32).cuda()
+    tables = torch.randperm(130, generator=torch.Generator().manual_seed(2))[:128].to(torch.int32).reshape(1, 128).cuda()
+    q = torch.randn((300, 4, 128), generator=torch.Generator().manual_seed(3)).bfloat16().cuda()
+    call = lambda: pkv.paged_attn_prefill(codes, q, i_cu, i_len, tables, max_q_len=300, scales=scales)
+    codes, scales, i_cu, i_len = codes.cuda(), scales.cuda(), i([0, 300]), i([2040])
+    want = call()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        out = call()
+    for _ in range(20):
+        graph.replay()
+        assert torch.equal(out, want) and torch.equal(call(), want)
+    assert pkv.get_device_error() == 0
+
+
 def test_bad_arguments_are_flagged():
     codes, scales = pool(8, 1, 16, 64, 3)
     q = torch.randn((20, 1, 64)).half().cuda()
