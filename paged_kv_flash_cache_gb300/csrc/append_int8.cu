@@ -17,10 +17,10 @@
 // are the tokens and the first one of each page does the page. Rows stay in registers between the maximum and the
 // codes (16 rows of 128 a warp); a page of more rows than its warps hold reads the rest twice, the second time from L2.
 //
-// Measured, back to back: 4 x 2048 tokens of 8 heads x 128 in pages of 16 (50 MB) 10.9 us, 68% of the copy rate; 3 x 1367
-// tokens of 32 heads in pages of 64 (101 MB) 18.4 us, 81%; a token each of 64 sequences 2.7 us. A warp's one chain (lengths,
+// Measured, back to back: 4 x 2048 tokens of 8 heads x 128 in pages of 16 (50 MB) 10.5 us, 70% of the copy rate; 3 x 1367
+// tokens of 32 heads in pages of 64 (101 MB) 18.0 us, 82%; a token each of 64 sequences 2.7 us. A warp's one chain (lengths,
 // page id, scale; its rows; the maximum; the codes) and the launch's ramp bound it, not the arithmetic (a third of the issue
-// slots): with 16 vectors a lane the prompts take 15.7 us, with 4 13.6.
+// slots): with 16 vectors a lane the prompts take 15.7 us, with 4 13.6; six CTAs an SM instead of seven 10.9, eight 11.9.
 #include "pkv_device.cuh"
 #include "pkv_internal.h"
 
@@ -108,7 +108,7 @@ __device__ __forceinline__ int last_at_most(int batch, int lane, long long slot,
 
 // W warps a page of a head.
 template <int D, int W, typename Tag>
-__global__ void __launch_bounds__(kThreads, 6) append_int8_kernel(AppendArgs a, long long tasks, int by_token) {
+__global__ void __launch_bounds__(kThreads, 7) append_int8_kernel(AppendArgs a, long long tasks, int by_token) {
     constexpr int kLanes = D / 8;               // lanes a row (16 bytes each)
     constexpr int kRowsLoad = 32 / kLanes;      // rows a load of the warp
     constexpr int kRowsWarp = kVecs * kRowsLoad;
