@@ -99,7 +99,8 @@ typedef enum { PKV_F16 = 0, PKV_BF16 = 1, PKV_F32 = 2 } pkv_dtype;
  *                   scales act in FP32 in the decode of up to 8 query heads per KV head. Its tcgen05
  *                   kernels (the prefill; the decode of more heads) round code * scale to f16, relative to
  *                   the largest scale of the keys that the CTA meets: exact for powers of two down to 2^-17
- *                   of that, else within half a step of f16 or 2^-25 of it; and the weights once to f16. */
+ *                   of that, else within half a step of f16 or 2^-25 of it; and the weights once to f16.
+ *                   Sums are FP32: the magnitudes of a context's values, added up, have to be well within it. */
 typedef enum { PKV_KV_NATIVE = 0, PKV_KV_FP8_E4M3 = 1, PKV_KV_INT8_BLOCK = 2 } pkv_kv_format;
 
 /* The paged KV cache [num_blocks, 2, num_kv_heads, block_size, head_dim] ([FAPA] s3).

@@ -460,7 +460,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         const float nan = __uint_as_float(0x7fc00000u);
         // a row that sees a key of a page whose scale is not finite is NaN
         const bool nan_k = last >= sNan[0], nan_v = last >= sNan[1];
-        const float wv = pow2_at_least(__uint_as_float(sMax[1]));
+        const float wv = pow2_at_least(__uint_as_float(sMax[1])), over_l = l > 0.f ? wv / l : 0.f;
         if (n_cta > 1) {
             float *out_row = reinterpret_cast<float *>(smem) + (size_t)(x * kBM + r) * Lay::kRowFloats;
             if (ok && n_tiles > 0)
@@ -479,14 +479,14 @@ __global__ void __launch_bounds__(kThreads, 1)
 #pragma unroll
                         for (int i = 0; i < 32; i += 4)
                             *reinterpret_cast<float4 *>(out_row + cc * 32 + i) =
-                                make_float4(o[i] * wv, o[i + 1] * wv, o[i + 2] * wv, o[i + 3] * wv);
+                                make_float4(o[i] * over_l, o[i + 1] * over_l, o[i + 2] * over_l, o[i + 3] * over_l);
                     }
                 }
                 *reinterpret_cast<float4 *>(out_row + D) = make_float4(m_use, l, nan_k ? 2.f : nan_v ? 1.f : 0.f, 0.f);
             }
         } else if (ok && warp_ok && mbar_wait(&o_done[x], (uint32_t)(n_tiles - 1) & 1u, abort_flag, p.err)) {
             tc::fence_after_sync();
-            const float inv = nan_k || nan_v ? nan : l > 0.f ? wv / l : 0.f;
+            const float inv = nan_k || nan_v ? nan : over_l;
             const size_t orow = (size_t)(q0 + m_start + token) * p.num_q_heads + h + r % pack;
 #pragma unroll
             for (int cc = 0; cc < D / 32; ++cc) {
@@ -539,10 +539,10 @@ __global__ void __launch_bounds__(kThreads, 1)
                         M = fmaxf(M, __shfl_xor_sync(0xffffffffu, M, i));
                         bad = fmaxf(bad, __shfl_xor_sync(0xffffffffu, bad, i));
                     }
-                    const float w = m == -INFINITY ? 0.f : ex2f(m - M);
-                    float sum = w * l;
+                    float w = m == -INFINITY ? 0.f * l : ex2f(m - M) * l, sum = w;  // (0 times a NaN sum: NaN)
 #pragma unroll
                     for (int i = 4; i > 0; i >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, i);
+                    w = sum != 0.f ? w / sum : 0.f;  // shares of the row: nothing is above the largest value
                     float acc[D / 32];
 #pragma unroll
                     for (int k = 0, r = 0, i = 0; k < 8; ++k) {
@@ -557,11 +557,10 @@ __global__ void __launch_bounds__(kThreads, 1)
                             const float s = __shfl_sync(0xffffffffu, sum, (8 * r) & 31), b8 = __shfl_sync(0xffffffffu, bad, (8 * r) & 31);
                             const float top = __shfl_sync(0xffffffffu, M, (8 * r) & 31);
                             if (r < batch && has(at_row)) {
-                                const float inv = b8 > 0.f ? nan : s > 0.f ? 1.f / s : s;
                                 const int tr = at_row & (kBM - 1), tok = (at_row / kBM) * tile_tokens + tr / pack;
                                 const size_t orow = (size_t)(q0 + m_start + tok) * p.num_q_heads + h + tr % pack;
 #pragma unroll
-                                for (int c = 0; c < D / 32; ++c) acc[c] *= inv;
+                                for (int c = 0; c < D / 32; ++c) acc[c] = b8 > 0.f ? nan : acc[c];
                                 store_out_vec<D / 32>(p.out, orow * D + lane * (D / 32), acc, p.out_dtype);
                                 if (lane == 0 && p.lse) p.lse[orow] = b8 > 1.f ? nan : (top + (__log2f(s) - kWeightLog2)) * kLn2;
                             }

@@ -221,6 +221,15 @@ def test_shared_blocks_again_and_again():
     assert pkv.get_device_error() == 0
 
 
+@pytest.mark.parametrize("lens,new,hq", [([3000], [200], 2), ([300], [300], 40)])
+def test_largest_values(lens, new, hq):
+    """Values whose sum over the context is within FP32: blocks of one CTA and of several."""
+    d, bs = 64, 16
+    codes, scales = pool(200, 1, bs, d, 31)
+    codes[:, 1], scales[:, 1] = codes[:, 1].abs().clamp(min=100), 2.0 ** 107
+    run(lens, new, hq, 1, d, bs, "bf16", 31, codes=codes, scales=scales, scale=0.001)
+
+
 def test_bad_arguments_are_flagged():
     codes, scales = pool(8, 1, 16, 64, 3)
     q = torch.randn((20, 1, 64)).half().cuda()
