@@ -91,12 +91,6 @@ __device__ __forceinline__ uint32_t codes_f16(uint32_t x) {
     return r;
 }
 
-__device__ __forceinline__ float rcpf(float x) {
-    float y;
-    asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
-    return y;
-}
-
 // A wait that gave up for one lane has for the warp: what follows needs its lanes together.
 __device__ __forceinline__ bool warp_wait(uint64_t *bar, uint32_t parity, volatile int *abort, int *err) {
     return __all_sync(0xffffffffu, mbar_wait(bar, parity, abort, err));
@@ -389,13 +383,16 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm)
 #pragma unroll
                     for (int k = 0; k < 2; ++k) o[mt][k] = fmul2(o[mt][k], make_float2(al[0], al[1]));
             }
-            // The tile's weights enter the product relative to its largest V scale w and times 2^11: P' = 2^11 p sv / w (at
-            // most 2^15), as an f16 part and its remainder, holds weights down to 2^-35. The tile's product
-            // enters O in FP32 times w / 2^11.
+            // The tile's weights enter the product relative to W, the power of two at or above its largest V scale, and times
+            // 2^11: P' = 2^11 (p sv / W) (at most 2^15), as an f16 part and its remainder, holds weights down to 2^-35. The
+            // tile's product enters O in FP32 times W / 2^11. A power of two: 1 / W is one at both ends of the scales'
+            // range, W / 2^11 has no bits to lose below 2^-126, and neither rounds (2^11 / W would pass FP32's range for
+            // scales up to 2^-117).
             float w = sv[0];
 #pragma unroll
             for (int g = 1; g < 2 * kBlocks; ++g) w = fmaxf(w, sv[g]);
-            const float rw = w >= 1.17549435e-38f ? kWeight * rcpf(w) : 0.f;  // (scales below 2^-126 count as 0)
+            const uint32_t wb = (__float_as_uint(w) + 0x7fffffu) & 0xff800000u;
+            const float rw = w >= 1.17549435e-38f ? __uint_as_float(0x7f000000u - wb) : 0.f;  // (scales below 2^-126 count as 0)
             uint32_t ph[kBlocks][2], pe[kBlocks][2];
 #pragma unroll
             for (int bl = 0; bl < kBlocks; ++bl)
@@ -404,7 +401,7 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm)
                     const float p0 = ex2f(s[bl][2 * hf] - m[0]), p1 = ex2f(s[bl][2 * hf + 1] - m[1]);
                     l[0] += p0;
                     l[1] += p1;
-                    const float r = sv[bl * 2 + hf] * rw;
+                    const float r = sv[bl * 2 + hf] * rw * kWeight;
                     uint32_t hi, lo;
                     split_pair<false>(p0 * r, p1 * r, hi, lo);
                     if (kPacked) {
@@ -414,7 +411,8 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm)
                         pe[bl][hf] = movmatrix_t(lo);
                     }
                 }
-            const float2 f2 = make_float2(w * (1.f / kWeight), w * (1.f / kWeight));
+            const float f = __uint_as_float(wb) * (1.f / kWeight);
+            const float2 f2 = make_float2(f, f);
             // ---- O^T += f V^T P'^T: D dims (permuted within each 16-dim chunk) x 8 slots ----
 #pragma unroll
             for (int cp = 0; cp < kChunks; cp += 2) {
