@@ -399,7 +399,9 @@ __global__ void __launch_bounds__(kThreads, 1)
                 const float nan = __uint_as_float(0x7fc00000u);
                 const bool nan_k = sNan[0] != 0x7fffffff, nan_v = sNan[1] != 0x7fffffff;
                 const float wv = pow2_at_least(__uint_as_float(sMax[1]));
-                const float inv = nan_k || nan_v ? nan : wv / sum;  // (a split has a key, so the sum is above 0, or NaN)
+                // (a split has a key, so the sum is above 0, or NaN; O / sum first, then times Wv: Wv / sum has no normal
+                // number where the scales are near 2^-126)
+                const float inv = nan_k || nan_v ? nan : 1.f / sum;
                 const float lse = nan_k ? nan : (M + (__log2f(sum) - kWeightLog2)) * kLn2;
                 const int splits = (len - 1) / a.chunk + 1;
                 const size_t head = (size_t)head0 + r;
@@ -415,7 +417,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                         for (int q = 0; q < 4; ++q) {
                             float v[8];
 #pragma unroll
-                            for (int k = 0; k < 8; ++k) v[k] = (o[8 * q + k] * fa + rowB[cc * 32 + 8 * q + k] * fb) * inv;
+                            for (int k = 0; k < 8; ++k) v[k] = (o[8 * q + k] * fa + rowB[cc * 32 + 8 * q + k] * fb) * inv * wv;
                             if (splits == 1) store_out_vec<8>(a.out, row_o * D + cc * 32 + 8 * q, v, a.out_dtype);
                             else store_out_vec<8>(a.part_o, row_p * D + cc * 32 + 8 * q, v, 2);
                         }

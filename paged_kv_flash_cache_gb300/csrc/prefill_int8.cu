@@ -5,7 +5,7 @@
 // out = softmax(Q K^T * scale) V with K = sk c^k, V = sv c^v per page. The CTA first finds Wk and Wv, powers of two at or
 // above every scale of its pages; the converters then write (sk / Wk) c^k and (sv / Wv) c^v in f16 -- exact for powers of
 // two down to 2^-17 of the largest, else within 2^-25 of W or half a step of f16 --, and Wk goes into the softmax's
-// scale, Wv into the epilogue's 1 / l. So the softmax and the MMAs are those of a 16-bit cache, and a scale costs one
+// scale, Wv onto the epilogue's O / l. So the softmax and the MMAs are those of a 16-bit cache, and a scale costs one
 // packed multiplication per pair of codes, in warps that have time for it.
 //
 // CTA = 256 query rows of one sequence, as two 128-row tiles A and B that share every K/V tile: 256 tokens of one query head,
@@ -460,7 +460,8 @@ __global__ void __launch_bounds__(kThreads, 1)
         const float nan = __uint_as_float(0x7fc00000u);
         // a row that sees a key of a page whose scale is not finite is NaN
         const bool nan_k = last >= sNan[0], nan_v = last >= sNan[1];
-        const float wv = pow2_at_least(__uint_as_float(sMax[1])), over_l = l > 0.f ? wv / l : 0.f;
+        // (O / l first, then times Wv: Wv / l has no normal number where the scales are near 2^-126)
+        const float wv = pow2_at_least(__uint_as_float(sMax[1])), over_l = l > 0.f ? 1.f / l : 0.f;
         if (n_cta > 1) {
             float *out_row = reinterpret_cast<float *>(smem) + (size_t)(x * kBM + r) * Lay::kRowFloats;
             if (ok && n_tiles > 0)
@@ -479,7 +480,7 @@ __global__ void __launch_bounds__(kThreads, 1)
 #pragma unroll
                         for (int i = 0; i < 32; i += 4)
                             *reinterpret_cast<float4 *>(out_row + cc * 32 + i) =
-                                make_float4(o[i] * over_l, o[i + 1] * over_l, o[i + 2] * over_l, o[i + 3] * over_l);
+                                make_float4(o[i] * over_l * wv, o[i + 1] * over_l * wv, o[i + 2] * over_l * wv, o[i + 3] * over_l * wv);
                     }
                 }
                 *reinterpret_cast<float4 *>(out_row + D) = make_float4(m_use, l, nan_k ? 2.f : nan_v ? 1.f : 0.f, 0.f);
@@ -498,7 +499,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                     for (int i = 0; i < 4; ++i) {
                         float v[8];
 #pragma unroll
-                        for (int k = 0; k < 8; ++k) v[k] = o[8 * i + k] * inv;
+                        for (int k = 0; k < 8; ++k) v[k] = o[8 * i + k] * inv * wv;
                         store_out_vec<8>(p.out, orow * D + cc * 32 + 8 * i, v, p.out_dtype);
                     }
                 }
