@@ -553,7 +553,7 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm)
 #pragma unroll
             for (int i = 16; i > 0; i >>= 1) M = fmaxf(M, __shfl_xor_sync(0xffffffffu, M, i));
             const float wt = ml.x == -INFINITY ? 0.f : ex2f(ml.x - M);
-            float sum = wt == 0.f ? 0.f : wt * ml.y;
+            float sum = ml.x == -INFINITY ? 0.f : wt * ml.y;  // (a CTA without keys: 0; a NaN stays one at any weight)
             float2 acc[D / 64];
 #pragma unroll
             for (int v = 0; v < D / 64; ++v) acc[v] = make_float2(0.f, 0.f);
