@@ -461,7 +461,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         // a row that sees a key of a page whose scale is not finite is NaN
         const bool nan_k = last >= sNan[0], nan_v = last >= sNan[1];
         // (O / l first, then times Wv: Wv / l has no normal number where the scales are near 2^-126)
-        const float wv = pow2_at_least(__uint_as_float(sMax[1])), over_l = l > 0.f ? 1.f / l : 0.f;
+        const float wv = pow2_at_least(__uint_as_float(sMax[1])), over_l = l == 0.f ? 0.f : 1.f / l;  // (a NaN sum stays one)
         if (n_cta > 1) {
             float *out_row = reinterpret_cast<float *>(smem) + (size_t)(x * kBM + r) * Lay::kRowFloats;
             if (ok && n_tiles > 0)
@@ -505,7 +505,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                 }
             }
             if (row_ok && p.lse)
-                p.lse[orow] = nan_k ? nan : l > 0.f ? (m_use + (__log2f(l) - kWeightLog2)) * kLn2 : -INFINITY;
+                p.lse[orow] = nan_k ? nan : l == 0.f ? -INFINITY : (m_use + (__log2f(l) - kWeightLog2)) * kLn2;
         }
         if (n_cta > 1) {
             // ---- the cluster's rows: row i by a softmax warp of CTA i % cluster; every CTA comes here, whatever its waits did ----
