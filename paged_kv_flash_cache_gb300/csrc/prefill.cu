@@ -744,8 +744,8 @@ __global__ void __launch_bounds__(kThreads, 1)
         if (ok && mbar_wait(&o_done[x], (uint32_t)(n_tiles - 1) & 1u, abort_flag, p.err)) {
             tc::fence_after_sync();
             // O / l; over an FP8 cache O carries the factor W (0 only when every V scale is 0) and
-            // the converted codes' 2^-8
-            const float inv = l > 0.f ? (FP8 ? w_cur * kCodeFactorInv : 1.f) / l : 0.f;
+            // the converted codes' 2^-8; a NaN sum stays one
+            const float inv = l == 0.f ? 0.f : (FP8 ? w_cur * kCodeFactorInv : 1.f) / l;
             const size_t row_g = (size_t)(q0 + m_start + row);
             const size_t obase = (row_g * p.num_q_heads + h) * D;
 #pragma unroll
@@ -775,7 +775,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                     }
                 }
             }
-            if (row_ok && p.lse) p.lse[row_g * p.num_q_heads + h] = l > 0.f ? (m_use + __log2f(l)) * kLn2 : -INFINITY;
+            if (row_ok && p.lse) p.lse[row_g * p.num_q_heads + h] = l == 0.f ? -INFINITY : (m_use + __log2f(l)) * kLn2;
         }
     }
     tc::fence_before_sync();

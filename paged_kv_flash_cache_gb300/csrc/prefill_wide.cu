@@ -347,7 +347,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         const int jl = n_tiles - 1;
         if (ok && mbar_wait(&o_done[jl & 1], ((uint32_t)jl >> 1) & 1u, abort_flag, p.err)) {
             tc::fence_after_sync();
-            const float inv = l > 0.f ? 1.f / l : 0.f;
+            const float inv = l == 0.f ? 0.f : 1.f / l;  // (a NaN sum stays one)
             const size_t row_g = (size_t)(q0 + m_start + r);
             const size_t obase = (row_g * p.num_q_heads + h) * kD;
 #pragma unroll
@@ -363,7 +363,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                     }
                 }
             }
-            if (row_ok && p.lse) p.lse[row_g * p.num_q_heads + h] = l > 0.f ? (m_use + __log2f(l)) * kLn2 : -INFINITY;
+            if (row_ok && p.lse) p.lse[row_g * p.num_q_heads + h] = l == 0.f ? -INFINITY : (m_use + __log2f(l)) * kLn2;
         }
     }
     tc::fence_before_sync();
