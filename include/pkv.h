@@ -391,7 +391,8 @@ PKV_API pkv_status pkv_kv_cache_fork(pkv_cache cache, const int *block_tables, c
  *   partial_lse   FP32 [n_rows, num_splits]: natural-log lse of each split's
  *                 scaled scores; -inf marks an empty split (weight 0).
  *   out           [n_rows, head_dim] in out_dtype; lse FP32 [n_rows] or NULL.
- * A row whose splits are all empty gets output 0 and lse -inf. */
+ * A row whose splits are all empty gets output 0 and lse -inf; one with an lse of NaN is NaN, and
+ * so is its lse. */
 PKV_API pkv_status pkv_attn_combine(const float *partial_o, const float *partial_lse, int n_rows,
                             int num_splits, int head_dim, void *out, pkv_dtype out_dtype,
                             float *lse, void *stream);

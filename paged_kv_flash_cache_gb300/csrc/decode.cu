@@ -632,9 +632,10 @@ __global__ void __launch_bounds__(256) combine_kernel(CombineArgs a) {
     const float *pl = a.part_lse + (size_t)row * a.num_splits;
     const float *po = a.part_o + (size_t)row * a.num_splits * D + kPer * lane;
     float M = -INFINITY;
-    for (int s = lane; s < S; s += 32) M = fmaxf(M, pl[s]);
+    // (the maximum is NaN if one is: then so are all weights, the sum and the row)
+    for (int s = lane; s < S; s += 32) M = fmax_nan(M, pl[s]);
 #pragma unroll
-    for (int o = 16; o > 0; o >>= 1) M = fmaxf(M, __shfl_xor_sync(0xffffffffu, M, o));
+    for (int o = 16; o > 0; o >>= 1) M = fmax_nan(M, __shfl_xor_sync(0xffffffffu, M, o));
     float o_acc[kPer];
 #pragma unroll
     for (int j = 0; j < kPer; ++j) o_acc[j] = 0.f;
@@ -671,11 +672,11 @@ __global__ void __launch_bounds__(256) combine_kernel(CombineArgs a) {
 #pragma unroll
         for (int o = 16; o > 0; o >>= 1) wsum += __shfl_xor_sync(0xffffffffu, wsum, o);
     }
-    const float inv = wsum > 0.f ? 1.f / wsum : 0.f;
+    const float inv = wsum == 0.f ? 0.f : 1.f / wsum;
 #pragma unroll
     for (int j = 0; j < kPer; ++j) o_acc[j] *= inv;
     store_out_vec<kPer>(a.out, out_row * D + lane * kPer, o_acc, a.out_dtype);
-    if (lane == 0 && a.lse) a.lse[out_row] = wsum > 0.f ? M + logf(wsum) : -INFINITY;
+    if (lane == 0 && a.lse) a.lse[out_row] = wsum == 0.f ? -INFINITY : M + logf(wsum);
 }
 
 template <typename Tag, int D, int G, bool FP8>

@@ -212,8 +212,9 @@ __device__ __forceinline__ bool merge_warp_loop(const DecodeArgs &a, const UnitT
                 lt[w] = lw[w] * wl[w];
             }
             const float lsum = tree_sum<W>(lt);
-            inv_l = lsum > 0.f ? 1.f / lsum : 0.f;
-            const float lse_v = lsum > 0.f ? (M + log2f(lsum)) * kLn2 : -INFINITY;
+            // (a NaN sum stays one: with an lse of -inf a split's part would vanish in the merge, and the NaN with it)
+            inv_l = lsum == 0.f ? 0.f : 1.f / lsum;
+            const float lse_v = lsum == 0.f ? -INFINITY : (M + log2f(lsum)) * kLn2;
             if (splits == 1) {
                 if (a.lse) a.lse[orow0 + lane] = lse_v;
             } else {

@@ -363,8 +363,8 @@ __global__ void __launch_bounds__(kThreads, kCtas)
             const bool row_ok = r < gu;
             float lt = d.l;
             if constexpr (kM == 64) lt += __shfl_xor_sync(0xffffffffu, lt, 16);  // the row's two halves
-            const float inv = lt > 0.f ? 1.f / lt : 0.f;
-            const float lse_v = lt > 0.f ? (d.m + __log2f(lt)) * kLn2 : -INFINITY;
+            const float inv = lt == 0.f ? 0.f : 1.f / lt;  // (a NaN sum stays one)
+            const float lse_v = lt == 0.f ? -INFINITY : (d.m + __log2f(lt)) * kLn2;
             const size_t h = (size_t)d.c.kvh * gu + r;  // query head
             const size_t orow = (size_t)ut.qrow[d.c.b] * a.num_q_heads + h;
             const size_t prow = (size_t)d.c.b * a.num_q_heads + h;
