@@ -153,7 +153,8 @@ PKV_API pkv_status pkv_kv_cache_append(pkv_cache cache, const void *k_new, const
 PKV_API size_t pkv_decode_workspace_size(int batch, int num_q_heads, int num_kv_heads, int head_dim,
                                  int block_size, int max_blocks_per_seq, int num_splits);
 
-/* The same for an INT8 cache: never more, and 0 where the call needs none (few sequences, short tables). */
+/* The same for an INT8 cache: never more (a workspace of pkv_decode_workspace_size() bytes serves every format), and 0
+ * where the call needs none (few sequences, short tables). */
 PKV_API size_t pkv_decode_int8_workspace_size(int batch, int num_q_heads, int num_kv_heads, int head_dim,
                                       int block_size, int max_blocks_per_seq, int num_splits);
 
@@ -162,7 +163,9 @@ PKV_API size_t pkv_decode_int8_workspace_size(int batch, int num_q_heads, int nu
  * context of L tokens is cut into ceil(L / chunk) splits.  With num_splits = 0 this is the
  * smallest split: the split kernel, which sees the context lengths, may take 1.5, 2, 3 or
  * 4 times it (rounded up to a multiple of 128) where its model of the launch's time says
- * the work divides better over its CTAs; the workspace size holds for every choice. */
+ * the work divides better over its CTAs; the workspace size holds for every choice. Over an
+ * INT8 cache the call cuts contexts into these splits or fewer, or takes each with a cluster
+ * of CTAs and has none. */
 PKV_API int pkv_decode_split_tokens(int batch, int num_q_heads, int num_kv_heads, int head_dim,
                             int block_size, int max_blocks_per_seq, int num_splits);
 

@@ -368,6 +368,8 @@ def kv_cache_append(cache, k_new, v_new, cu_new_lens, ctx_before, block_tables, 
 
 def decode_workspace_size(batch, num_q_heads, num_kv_heads, head_dim, block_size, max_blocks_per_seq,
                           num_splits=0) -> int:
+    """Bytes of `workspace` that a decode or mixed call of these sizes needs at most, over a cache of any format (with the
+    device of the call current)."""
     return int(load_library().pkv_decode_workspace_size(batch, num_q_heads, num_kv_heads, head_dim, block_size,
                                                         max_blocks_per_seq, num_splits))
 

@@ -44,7 +44,7 @@ constexpr int kConsumerWarps = 8;
 constexpr int kProducerWarp = kConsumerWarps;
 constexpr int kMergeWarp = kConsumerWarps + 1;
 constexpr int kDecodeThreads = (kConsumerWarps + 2) * 32;
-constexpr int kMaxBatch = 2048;  // unit tables (lengths, order, split offsets) kept in shared memory
+constexpr int kMaxBatch = kDecodeMaxBatch;  // unit tables (lengths, order, split offsets) kept in shared memory
 constexpr float kRescaleLog2 = 8.0f;  // lazy rescale threshold (log2 units)
 
 __device__ __forceinline__ float ex2_approx(float x) {

@@ -50,8 +50,7 @@ constexpr int kThreads = kWarps * 32;
 // sequences of 4096 tokens, 8 KV heads 61 us.)
 template <int D>
 constexpr int kTile = D == 64 ? 64 : 32;
-constexpr int kCtasPerSm = 3;
-constexpr int kClusterCtasPerSm = 2;  // clusters: CTAs an SM at most
+constexpr int kCtasPerSm = kInt8CtasPerSm;
 constexpr float kRescale = 4.0f;  // lazy rescale threshold (log2 units)
 constexpr float kWeight = 2048.0f;  // weights, at most 2^kRescale, go into the product times this: below f16's 65504
 
@@ -751,44 +750,6 @@ cudaError_t launch_d(const DecodeArgs &a, int grid, cudaStream_t s) {
 }
 
 }  // namespace
-
-// CTAs of the cluster that takes a unit's whole context, 0: the split kernel and its merge. A cluster saves the unit tables,
-// the partials and the second launch, but has to leave SMs idle where the units times 16 are fewer. Measured against the
-// splits, 8 KV heads of 4 query heads: one sequence of 4096 tokens 7.8 us for 9.6, of 8192 10.5 for 11.5, of 16384
-// (not taken) 15.5 for 14.1; four of 4096 10.2 for 12.2, of 16384 26.1 for 29.2; 32 of 2048 25.5 for 28.4; 16 of 8192 47.6
-// for 47.2 (not taken: more units than CTAs at two an SM in clusters of one). Clusters of 16 only where they are alone on
-// their SMs: 16 units of 8192 tokens in 256 CTAs took 20.4 for 17.0.
-int decode_int8_cluster(int batch, int units_per_seq, long long capacity) {
-    const long long units = (long long)batch * units_per_seq;
-    for (int c = 16; c >= 1; c >>= 1)
-        if (units * c <= (long long)(c == 16 ? 1 : kClusterCtasPerSm) * device_info().num_sms)
-            return capacity <= (units * c <= device_info().num_sms ? 640ll : 4096ll) * c ? c : 0;
-    return 0;
-}
-
-// Tokens per split (a multiple of 128, 256 to 1024, and at most kDecodeMaxSplits splits): units are dealt round-robin
-// to the CTAs, so a launch takes about ceil(units / CTAs) times a unit's tokens and what a unit costs besides (150 tokens'
-// time), for contexts that fill the table but its last page. (4 sequences of 8192 tokens, 8 KV heads: 26 us with splits of
-// 128 tokens, 16 with 640.) With work for more rounds than four the contexts' own lengths matter more: 768 tokens, the best
-// for ragged batches (mixed serving batch 37 us; 384 tokens 40, 1024 43).
-int decode_int8_split(int batch, int units_per_seq, int block_size, long long capacity) {
-    const long long ctas = (long long)kCtasPerSm * device_info().num_sms;
-    const long long tokens = capacity > block_size ? capacity - block_size : capacity;
-    long long least = (capacity + kDecodeMaxSplits - 1) / kDecodeMaxSplits;
-    least = (least + 127) / 128 * 128;
-    if (least < 256) least = 256;
-    if (least <= 768 && (long long)batch * units_per_seq * ((tokens + 767) / 768) >= 4 * ctas) return 768;
-    long long best = least, best_cost = -1;
-    for (long long c = least; c <= (least > 1024 ? least : 1024); c += 128) {
-        const long long units = (long long)batch * units_per_seq * ((tokens + c - 1) / c);
-        const long long cost = (units + ctas - 1) / ctas * (c + 150);
-        if (best_cost < 0 || cost < best_cost) {
-            best_cost = cost;
-            best = c;
-        }
-    }
-    return (int)best;
-}
 
 cudaError_t launch_merge_splits(const CombineArgs &a, cudaStream_t s) {
     if (a.n_rows == 0) return cudaSuccess;

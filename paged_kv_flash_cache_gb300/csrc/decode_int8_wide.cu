@@ -462,26 +462,6 @@ cudaError_t launch_t(const DecodeArgs &a, cudaStream_t s) {
 
 }  // namespace
 
-// Tokens per split: a CTA an SM, so a launch takes about ceil(units / SMs) times a unit's tokens and what a CTA's start and
-// end cost (600 tokens' time), for contexts that fill the table but its last page; 768 tokens at least.
-int decode_int8_wide_split(int batch, int units_per_seq, int block_size, long long capacity) {
-    const long long ctas = device_info().num_sms;
-    const long long tokens = capacity > block_size ? capacity - block_size : capacity;
-    long long least = (capacity + kDecodeMaxSplits - 1) / kDecodeMaxSplits;
-    least = (least + 255) / 256 * 256;
-    if (least < 768) least = 768;
-    long long best = least, best_cost = -1;
-    for (long long c = least; c <= (least > 8192 ? least : 8192); c += 256) {
-        const long long units = (long long)batch * units_per_seq * ((tokens + c - 1) / c);
-        const long long cost = (units + ctas - 1) / ctas * (c + 600);
-        if (best_cost < 0 || cost < best_cost) {
-            best_cost = cost;
-            best = c;
-        }
-    }
-    return (int)best;
-}
-
 cudaError_t launch_decode_int8_wide(const DecodeArgs &a, cudaStream_t s) {
     if (a.batch == 0) return cudaSuccess;
     const bool bf16 = a.cache.dtype == 1;

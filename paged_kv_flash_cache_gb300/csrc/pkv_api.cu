@@ -71,8 +71,9 @@ DeviceSlot *slot() {
 }
 
 // Launch facts of a device that could not be queried: used only to size workspaces before any
-// device is usable (the smallest split chunk, so the size is never too small).
-const DeviceInfo kNoDevice = {-1, 1, 1, 48 * 1024};
+// device is usable. The more SMs, the smaller the splits: 160, more than a GB300 shows (152), so that
+// the size is never too small.
+const DeviceInfo kNoDevice = {-1, 160, 1, 48 * 1024};
 
 pkv_status check_cache(const pkv_cache &c) {
     if (!c.ptr || !aligned16(c.ptr)) return PKV_ERR_INVALID_ARG;
@@ -107,65 +108,13 @@ CacheView view_of(const pkv_cache &c) {
     return v;
 }
 
-// Tokens per decode split.  Automatic: enough (sequence, KV head, split) units for about
-// eight per CTA at full capacity, in [128, 512] tokens; explicit: capacity / num_splits
-// rounded up to kSplitAlign (128, the tensor-core decode's key tile).  Either way at least
-// capacity / kDecodeMaxSplits, rounded up, so that a full context has at most kDecodeMaxSplits
-// splits.
+// Tokens per split for the current device (decode_rules.h).
 int split_tokens(int batch, int num_kv_heads, int block_size, int max_blocks_per_seq, int num_splits) {
-    const long long cap = (long long)max_blocks_per_seq * block_size;
-    const long long tile = kSplitAlign;
-    long long c;
-    if (num_splits > 0) {
-        c = (cap + num_splits - 1) / num_splits;
-    } else {
-        const DeviceSlot *s = slot();
-        const DeviceInfo &d = s ? s->info : kNoDevice;
-        const long long ctas = (long long)d.num_sms * d.decode_ctas_per_sm;
-        const long long want = (long long)batch * num_kv_heads * cap / (ctas * 8 > 0 ? ctas * 8 : 1);
-        // the largest of these at or below want (at least 128): 768-token splits measured best on
-        // the streaming paths (7B-like, FP8 and mixed batches against 512, 640 and 1024)
-        static const int kSizes[] = {768, 512, 384, 256, 128};
-        int i = 0;
-        while (kSizes[i] > 128 && kSizes[i] > want) ++i;
-        c = kSizes[i];
-    }
-    const long long floor_c = (cap + kDecodeMaxSplits - 1) / kDecodeMaxSplits;
-    if (c < floor_c) c = floor_c;
-    c = (c + tile - 1) / tile * tile;
-    return (int)(c < tile ? tile : c);
-}
-
-// How a decode over an INT8 cache runs: query heads of a unit, the cluster's CTAs (0: splits and a merge), tokens per split,
-// and whether the units are tcgen05's.
-//   few units and short tables: clusters (decode_int8_cluster), units of the group or, above 8 heads, of its largest
-//   divisor up to 8; more than 8 heads per KV head otherwise: tcgen05 units of the group or its largest divisor up to 128;
-//   else splits of mma.sync units.
-struct Int8Decode {
-    int unit_heads, cluster, chunk;
-    bool wide;
-};
-
-int largest_divisor(int group, int most) {
-    int n = group;
-    for (int d = most; n > most; --d)
-        if (group % d == 0) n = d;
-    return n;
+    return decode_split_tokens(device_info().num_sms, batch, num_kv_heads, block_size, max_blocks_per_seq, num_splits);
 }
 
 Int8Decode int8_decode(int batch, int num_q_heads, int num_kv_heads, int block_size, int max_blocks_per_seq, int num_splits) {
-    const long long cap = (long long)max_blocks_per_seq * block_size;
-    const int group = num_q_heads / num_kv_heads;
-    Int8Decode d;
-    d.unit_heads = largest_divisor(group, 8);
-    d.cluster = num_splits > 0 || batch > decode_max_batch() ? 0 : decode_int8_cluster(batch, num_q_heads / d.unit_heads, cap);
-    d.wide = d.cluster == 0 && group > 8;
-    if (d.wide) d.unit_heads = largest_divisor(group, 128);
-    const int units = num_q_heads / d.unit_heads;
-    d.chunk = num_splits > 0 ? split_tokens(batch, num_kv_heads, block_size, max_blocks_per_seq, num_splits)
-              : d.wide       ? decode_int8_wide_split(batch, units, block_size, cap)
-                             : decode_int8_split(batch, units, block_size, cap);
-    return d;
+    return decode_int8_plan(device_info().num_sms, batch, num_q_heads, num_kv_heads, block_size, max_blocks_per_seq, num_splits);
 }
 
 }  // namespace
@@ -267,6 +216,8 @@ size_t pkv_decode_int8_workspace_size(int batch, int num_q_heads, int num_kv_hea
         block_size <= 0 || max_blocks_per_seq <= 0)
         return 0;
     const long long cap = (long long)max_blocks_per_seq * block_size;
+    if (!slot())  // no device yet, and no say on clusters
+        return pkv_decode_workspace_size(batch, num_q_heads, num_kv_heads, head_dim, block_size, max_blocks_per_seq, num_splits);
     const Int8Decode d = int8_decode(batch, num_q_heads, num_kv_heads, block_size, max_blocks_per_seq, num_splits);
     if (d.cluster > 0) return 0;
     const long long s_max = (cap + d.chunk - 1) / d.chunk;

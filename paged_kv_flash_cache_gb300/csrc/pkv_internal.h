@@ -9,6 +9,7 @@
 #include <stdint.h>
 
 #include "../../include/pkv.h"
+#include "decode_rules.h"
 
 namespace pkv {
 
@@ -242,8 +243,6 @@ struct DeviceFlags {
 int *device_error_word();  // the current device's sticky error word (device address)
 
 constexpr int kDecodeTile = 64;         // tokens per decode pipeline stage
-constexpr int kSplitAlign = 128;        // decode splits start at multiples of this many tokens
-constexpr int kDecodeMaxSplits = 2048;  // splits of one context (bounds the split size from below)
 constexpr int kUnitMisc = 8;           // ints of a decode CTA's unit table beyond its per-sequence and per-split parts
 
 cudaError_t launch_append(const AppendArgs &a, cudaStream_t s);
@@ -267,10 +266,7 @@ cudaError_t launch_decode_gqa(const DecodeArgs &a, int grid, cudaStream_t s);
 // Tensor-core (tcgen05) decode for a unit of up to 128 query heads of one KV head.
 cudaError_t launch_decode_tc(const DecodeArgs &a, int grid, cudaStream_t s);
 // more than 8 query heads per KV head: tcgen05 units of up to 128 heads (decode_int8_wide.cu)
-int decode_int8_wide_split(int batch, int units_per_seq, int block_size, long long capacity);
 cudaError_t launch_decode_int8_wide(const DecodeArgs &a, cudaStream_t s);
-int decode_int8_split(int batch, int units_per_seq, int block_size, long long capacity);
-int decode_int8_cluster(int batch, int units_per_seq, long long capacity);
 cudaError_t launch_merge_splits(const CombineArgs &a, cudaStream_t s);  // the INT8 decode's
 cudaError_t launch_decode_int8(const DecodeArgs &a, int grid, cudaStream_t s);
 cudaError_t launch_decode_fp8(const DecodeArgs &a, int grid, cudaStream_t s);
