@@ -410,7 +410,8 @@ PKV_API pkv_status pkv_attn_combine(const float *partial_o, const float *partial
  *     split partials live in a fixed array of PKV_DECODE_NOALLOC_SCRATCH_BYTES that
  *     the library keeps in device memory; every GPU that loads the library holds it
  *     until the process exits.
- *   - Sizes whose workspace (pkv_decode_workspace_size) exceeds that array are
+ *   - Sizes whose workspace (pkv_decode_workspace_size; over an INT8 cache
+ *     pkv_decode_int8_workspace_size, which is often less) exceeds that array are
  *     rejected with PKV_ERR_WORKSPACE before anything is launched.
  *   - The first call on each device (that device current) looks up the array's device
  *     address with cudaGetSymbolAddress; make that first call before any stream

@@ -65,8 +65,9 @@ extern "C" pkv_status pkv_paged_attn_decode_noalloc(pkv_cache cache, const void 
                                                     const int *block_tables, const int *context_lens, int batch,
                                                     int max_blocks_per_seq, float scale, int num_splits, void *out,
                                                     pkv_dtype out_dtype, float *lse, void *stream) {
-    const size_t need = pkv_decode_workspace_size(batch, num_q_heads, cache.num_kv_heads, cache.head_dim,
-                                                  cache.block_size, max_blocks_per_seq, num_splits);
+    const auto size = cache.format == PKV_KV_INT8_BLOCK ? pkv_decode_int8_workspace_size : pkv_decode_workspace_size;
+    const size_t need = size(batch, num_q_heads, cache.num_kv_heads, cache.head_dim, cache.block_size, max_blocks_per_seq,
+                             num_splits);
     if (need > (size_t)PKV_DECODE_NOALLOC_SCRATCH_BYTES) return PKV_ERR_WORKSPACE;
     void *scratch = nullptr;
     if (pkv::scratch_address(&scratch) != cudaSuccess || scratch == nullptr) return PKV_ERR_CUDA;
