@@ -34,6 +34,8 @@
 // product with V and the others the remainders, in one mma; with more heads the remainders are a second mma.
 #include <cuda.h>
 
+#include <atomic>
+
 #include "cluster.cuh"
 #include "decode_common.cuh"
 #include "pkv_device.cuh"
@@ -692,20 +694,65 @@ __global__ void __launch_bounds__(128) merge_splits_kernel(CombineArgs a) {
 }
 
 template <int D, int G, bool ONE>
+auto configured_kernel(cudaError_t &e) {
+    auto kern = decode_int8_kernel<D, G, ONE>;
+    static DeviceFlags configured;
+    const int dev = device_info().device;
+    e = cudaSuccess;
+    if (!configured.test(dev)) {
+        e = set_smem_attributes(kern, device_info().max_smem);
+        if (ONE && e == cudaSuccess) e = cudaFuncSetAttribute(kern, cudaFuncAttributeNonPortableClusterSizeAllowed, 1);
+        if (e == cudaSuccess) configured.set(dev);
+    }
+    return kern;
+}
+
+// Asked once a device: the cluster sizes that have a place on it (0 where the device does not say: then it is asked again).
+template <int D, int G>
+int cluster_sizes() {
+    static std::atomic<int> known[64];  // the sizes, and 32 once they are
+    const int dev = device_info().device;
+    if (dev < 0 || dev >= 64) return 0;
+    int sizes = known[dev].load(std::memory_order_relaxed);
+    if (sizes) return sizes & 31;
+    cudaError_t e;
+    auto kern = configured_kernel<D, G, true>(e);
+    for (int n = 1; n <= 16 && e == cudaSuccess; n *= 2) {
+        cudaLaunchConfig_t cfg = {};
+        cfg.gridDim = dim3((unsigned)n);
+        cfg.blockDim = dim3(kThreads);
+        cfg.dynamicSmemBytes = Int8Layout<D, G>::smem_bytes_one();
+        cudaLaunchAttribute attr;
+        attr.id = cudaLaunchAttributeClusterDimension;
+        attr.val.clusterDim.x = (unsigned)n;
+        attr.val.clusterDim.y = attr.val.clusterDim.z = 1;
+        cfg.attrs = &attr;
+        cfg.numAttrs = 1;
+        int clusters = 0;
+        e = cudaOccupancyMaxActiveClusters(&clusters, kern, &cfg);
+        // (a size that the device refuses outright is one without a place)
+        if (e == cudaErrorInvalidClusterSize) {
+            (void)cudaGetLastError();
+            e = cudaSuccess;
+            clusters = 0;
+        }
+        if (clusters > 0) sizes |= n;
+    }
+    if (e != cudaSuccess) {
+        (void)cudaGetLastError();
+        return 0;
+    }
+    known[dev].store(sizes | 32, std::memory_order_relaxed);
+    return sizes;
+}
+
+template <int D, int G, bool ONE>
 cudaError_t launch_t(const DecodeArgs &a, int grid, cudaStream_t s) {
     CUtensorMap tm;
     cudaError_t e = encode_int8_map(a.cache, a.cache.block_size < kTile<D> ? a.cache.block_size : kTile<D>, 2, &tm);
     if (e != cudaSuccess) return e;
-    auto kern = decode_int8_kernel<D, G, ONE>;
-    static DeviceFlags configured;
-    const int dev = device_info().device;
-    if (!configured.test(dev)) {
-        e = set_smem_attributes(kern, device_info().max_smem);
-        if (e != cudaSuccess) return e;
-        if (ONE) e = cudaFuncSetAttribute(kern, cudaFuncAttributeNonPortableClusterSizeAllowed, 1);
-        if (e != cudaSuccess) return e;
-        configured.set(dev);
-    }
+    auto kern = configured_kernel<D, G, ONE>(e);
+    if (e != cudaSuccess) return e;
     if (ONE) {
         cudaLaunchConfig_t cfg = {};
         cfg.gridDim = dim3((unsigned)(a.batch * a.cache.num_kv_heads * a.head_groups * a.cluster));
@@ -749,7 +796,26 @@ cudaError_t launch_d(const DecodeArgs &a, int grid, cudaStream_t s) {
     }
 }
 
+template <int D>
+int cluster_sizes_of(int heads) {
+    switch (heads) {
+        case 1: return cluster_sizes<D, 1>();
+        case 2: return cluster_sizes<D, 2>();
+        case 3: return cluster_sizes<D, 3>();
+        case 4: return cluster_sizes<D, 4>();
+        case 5: return cluster_sizes<D, 5>();
+        case 6: return cluster_sizes<D, 6>();
+        case 7: return cluster_sizes<D, 7>();
+        case 8: return cluster_sizes<D, 8>();
+        default: return 0;
+    }
+}
+
 }  // namespace
+
+int decode_int8_cluster_sizes(int head_dim, int heads) {
+    return head_dim == 128 ? cluster_sizes_of<128>(heads) : head_dim == 64 ? cluster_sizes_of<64>(heads) : 0;
+}
 
 cudaError_t launch_merge_splits(const CombineArgs &a, cudaStream_t s) {
     if (a.n_rows == 0) return cudaSuccess;

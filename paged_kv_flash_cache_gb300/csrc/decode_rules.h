@@ -46,10 +46,11 @@ inline int decode_split_tokens(int num_sms, int batch, int num_kv_heads, int blo
 // (not taken) 15.5 for 14.1; four of 4096 10.2 for 12.2, of 16384 26.1 for 29.2; 32 of 2048 25.5 for 28.4; 16 of 8192 47.6
 // for 47.2 (not taken: more units than CTAs at two an SM in clusters of one). Clusters of 16 only where they are alone on
 // their SMs: 16 units of 8192 tokens in 256 CTAs took 20.4 for 17.0. The lengths live on the device: capacity is the table's.
-inline int decode_int8_cluster(int num_sms, int batch, int units_per_seq, long long capacity) {
+// sizes: the cluster sizes that the device can place, ored (a cluster lies in one GPC, and sizes above 8 are no device's duty).
+inline int decode_int8_cluster(int num_sms, int sizes, int batch, int units_per_seq, long long capacity) {
     const long long units = (long long)batch * units_per_seq;
     for (int c = 16; c >= 1; c >>= 1)
-        if (units * c <= (long long)(c == 16 ? 1 : kInt8ClusterCtasPerSm) * num_sms)
+        if ((sizes & c) && units * c <= (long long)(c == 16 ? 1 : kInt8ClusterCtasPerSm) * num_sms)
             return capacity <= (units * c <= num_sms ? 640ll : 4096ll) * c ? c : 0;
     return 0;
 }
@@ -118,12 +119,14 @@ struct Int8Decode {
 };
 
 inline Int8Decode decode_int8_plan(int num_sms, int batch, int num_q_heads, int num_kv_heads, int block_size,
-                                   int max_blocks_per_seq, int num_splits) {
+                                   int max_blocks_per_seq, int num_splits, int cluster_sizes = 31) {
     const long long cap = (long long)max_blocks_per_seq * block_size;
     const int group = num_q_heads / num_kv_heads;
     Int8Decode d;
     d.unit_heads = largest_divisor(group, 8);
-    d.cluster = num_splits > 0 || batch > kDecodeMaxBatch ? 0 : decode_int8_cluster(num_sms, batch, num_q_heads / d.unit_heads, cap);
+    d.cluster = num_splits > 0 || batch > kDecodeMaxBatch
+                    ? 0
+                    : decode_int8_cluster(num_sms, cluster_sizes, batch, num_q_heads / d.unit_heads, cap);
     d.wide = d.cluster == 0 && group > 8;
     if (d.wide) d.unit_heads = largest_divisor(group, 128);
     const int units = num_q_heads / d.unit_heads;

@@ -113,8 +113,11 @@ int split_tokens(int batch, int num_kv_heads, int block_size, int max_blocks_per
     return decode_split_tokens(device_info().num_sms, batch, num_kv_heads, block_size, max_blocks_per_seq, num_splits);
 }
 
-Int8Decode int8_decode(int batch, int num_q_heads, int num_kv_heads, int block_size, int max_blocks_per_seq, int num_splits) {
-    return decode_int8_plan(device_info().num_sms, batch, num_q_heads, num_kv_heads, block_size, max_blocks_per_seq, num_splits);
+Int8Decode int8_decode(int batch, int num_q_heads, int num_kv_heads, int head_dim, int block_size, int max_blocks_per_seq,
+                       int num_splits) {
+    const int sizes = decode_int8_cluster_sizes(head_dim, largest_divisor(num_q_heads / num_kv_heads, 8));
+    return decode_int8_plan(device_info().num_sms, batch, num_q_heads, num_kv_heads, block_size, max_blocks_per_seq, num_splits,
+                            sizes);
 }
 
 }  // namespace
@@ -218,7 +221,7 @@ size_t pkv_decode_int8_workspace_size(int batch, int num_q_heads, int num_kv_hea
     const long long cap = (long long)max_blocks_per_seq * block_size;
     if (!slot())  // no device yet, and no say on clusters
         return pkv_decode_workspace_size(batch, num_q_heads, num_kv_heads, head_dim, block_size, max_blocks_per_seq, num_splits);
-    const Int8Decode d = int8_decode(batch, num_q_heads, num_kv_heads, block_size, max_blocks_per_seq, num_splits);
+    const Int8Decode d = int8_decode(batch, num_q_heads, num_kv_heads, head_dim, block_size, max_blocks_per_seq, num_splits);
     if (d.cluster > 0) return 0;
     const long long s_max = (cap + d.chunk - 1) / d.chunk;
     return s_max <= 1 ? 0 : partial_bytes(batch, num_q_heads, s_max, head_dim) + 16;
@@ -254,7 +257,8 @@ pkv_status decode_impl(const pkv_cache &cache, const void *q, int num_q_heads, c
     if (cap > (1ll << 30)) return PKV_ERR_UNSUPPORTED;
     DeviceSlot *s = slot();
     if (!s) return PKV_ERR_CUDA;
-    const Int8Decode how = int8 ? int8_decode(batch, num_q_heads, cache.num_kv_heads, cache.block_size, max_blocks_per_seq, num_splits)
+    const Int8Decode how = int8 ? int8_decode(batch, num_q_heads, cache.num_kv_heads, cache.head_dim, cache.block_size,
+                                              max_blocks_per_seq, num_splits)
                                 : Int8Decode{0, 0, 0, false};
     const int chunk = int8 ? how.chunk
                            : split_tokens(batch, cache.num_kv_heads, cache.block_size, max_blocks_per_seq, num_splits);

@@ -269,6 +269,8 @@ cudaError_t launch_decode_tc(const DecodeArgs &a, int grid, cudaStream_t s);
 cudaError_t launch_decode_int8_wide(const DecodeArgs &a, cudaStream_t s);
 cudaError_t launch_merge_splits(const CombineArgs &a, cudaStream_t s);  // the INT8 decode's
 cudaError_t launch_decode_int8(const DecodeArgs &a, int grid, cudaStream_t s);
+// Cluster sizes (1, 2, 4, 8, 16, ored) that the current device can place for units of `heads` query heads (at most 8).
+int decode_int8_cluster_sizes(int head_dim, int heads);
 cudaError_t launch_decode_fp8(const DecodeArgs &a, int grid, cudaStream_t s);
 cudaError_t launch_decode(const DecodeArgs &a, int grid, cudaStream_t s);
 cudaError_t launch_combine(const CombineArgs &a, cudaStream_t s);
