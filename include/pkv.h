@@ -95,11 +95,15 @@ typedef enum { PKV_F16 = 0, PKV_BF16 = 1, PKV_F32 = 2 } pkv_dtype;
  *                   infinity make the scale NaN: the page reads as NaN until it starts again with its first row.
  *                   Caches quantised elsewhere: scales of 0 and from 2^-126 to 2^126, powers of two or not
  *                   (smaller ones count as 0; behind older rows under a scale that is no power of two, the
- *                   code of an x / s within 2^-16 of a tie may be either neighbour). Attention: the
- *                   scales act in FP32 in the decode of up to 8 query heads per KV head. Its tcgen05
- *                   kernels (the prefill; the decode of more heads) round code * scale to f16, relative to
- *                   the largest scale of the keys that the CTA meets: exact for powers of two down to 2^-17
- *                   of that, else within half a step of f16 or 2^-25 of it; and the weights once to f16.
+ *                   code of an x / s within 2^-16 of a tie may be either neighbour). Attention: in the
+ *                   decode of up to 8 query heads per KV head (and of more where a few sequences with short
+ *                   tables are taken by clusters) K's scales act in FP32 and V's with the weights: a weight
+ *                   times its scale is held to 2^-22 of itself, or, where that is more, to 2^-35 of the row's
+ *                   largest weight times the largest scale of its 32 keys (head_dim 64: 64). The tcgen05 kernels (the prefill; the decode
+ *                   of more heads) take code * scale in f16, relative to the least power of two W at or above
+ *                   every scale of the keys that the CTA meets: exact for powers of two down to 2^-24 of W,
+ *                   below which they count as 0; others are off by two half steps of f16 (2^-10) and 2^-24 of
+ *                   W times the code at most; and the weights once to f16.
  *                   Sums are FP32: the magnitudes of a context's values, added up, have to be well within it. */
 typedef enum { PKV_KV_NATIVE = 0, PKV_KV_FP8_E4M3 = 1, PKV_KV_INT8_BLOCK = 2 } pkv_kv_format;
 
@@ -380,7 +384,7 @@ PKV_API pkv_status pkv_kv_cache_copy(pkv_cache dst, pkv_cache src, const int *sr
  * A child's table names its parent's full pages, which both then share. Where the parent's last page is partly
  * filled, its rows are copied to new_pages[c], which takes its place; with -1 the child's table names the parent's
  * page itself (right for one child of a parent that ends). Where it is full, new_pages[c] (if not -1) becomes the
- * page of the child's next token. The entries behind are -1; out_lens[c] = context_lens[p].
+ * page of the child's next token (a parent that fills its whole table has no entry for it: the page is not used). The entries behind are -1; out_lens[c] = context_lens[p].
  * A parent outside [0, num_parents) or with a length out of range is flagged, and its child is empty; a new page
  * outside the pool is flagged, and the child's entry is -1. Reference counts are the host's. */
 PKV_API pkv_status pkv_kv_cache_fork(pkv_cache cache, const int *block_tables, const int *context_lens, const int *parents,

@@ -18,7 +18,8 @@
 // codes (16 rows of 128 a warp); a page of more rows than its warps hold reads the rest twice, the second time from L2.
 //
 // Measured, back to back: 4 x 2048 tokens of 8 heads x 128 in pages of 16 (50 MB) 10.5 us, 70% of the copy rate; 3 x 1367
-// tokens of 32 heads in pages of 64 (101 MB) 18.0 us, 82%; a token each of 64 sequences 2.7 us. A warp's one chain (lengths,
+// tokens of 32 heads in pages of 64 (101 MB) 18.0 us, 82%; a token each of 64 sequences 2.7 us. 72 registers a thread, so that
+// seven CTAs fit; f16 with one warp a page spills 40 bytes for it (the prompts again and again into L2: 7.5 us, bf16 7.2). A warp's one chain (lengths,
 // page id, scale; its rows; the maximum; the codes) and the launch's ramp bound it, not the arithmetic (a third of the issue
 // slots): with 16 vectors a lane the prompts take 15.7 us, with 4 13.6; six CTAs an SM instead of seven 10.9, eight 11.9.
 #include "pkv_device.cuh"

@@ -9,8 +9,9 @@
 // codes a clock, each of which has to become a 16-bit operand. 16 tokens x 8 head slots x 16 dims are one mma.sync
 // m16n8k16 in f16. A code becomes f16 by two instructions a pair: c + 128 placed as the low byte of a half of exponent
 // 1024 (a byte permute, after one exclusive-or for four codes), then 1152 subtracted: exact. The K scale multiplies the
-// FP32 scores. The V scales enter the weights, which go into the product relative to their tile's largest, as an f16
-// part and its remainder: the output's rounding is the only 16-bit one on the path, however small weights and scales are.
+// FP32 scores. The V scales enter the weights, which go into the product relative to the power of two at or above their
+// tile's largest, as an f16 part and its remainder: the output's rounding is the only 16-bit one on the path
+// (weights times scales below 2^-35 of the row's largest weight and the tile's largest scale are lost).
 //
 // Structure (persistent, three CTAs an SM of four warps). A unit is (sequence, KV head's query group, split); tile j (8 KB of
 // codes) of a unit is warp j % W's. Every warp feeds itself: it has a ring of its own and sends for the tile that goes into a slot as

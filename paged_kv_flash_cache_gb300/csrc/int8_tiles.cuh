@@ -1,7 +1,7 @@
 // int8_tiles.cuh -- INT8 codes to f16 tiles for the tcgen05 kernels over an INT8 cache (prefill_int8.cu,
 // decode_int8_wide.cu): K = sk c and V = sv c enter the products as (s / W) c in f16, W a power of two at or above
-// every scale that the CTA meets -- exact for powers of two down to 2^-17 of the largest, else within 2^-25 of W or
-// half a step of f16 --, and W goes into the softmax's scale or the output's.
+// every scale that the CTA meets, and W goes into the softmax's scale or the output's. Exact for powers of two down to
+// 2^-24 of W (f16's smallest step), below which they count as 0; else within two half steps of f16 and 2^-24 W times the code.
 #pragma once
 
 #include "pkv_device.cuh"

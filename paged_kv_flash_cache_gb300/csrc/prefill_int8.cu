@@ -4,7 +4,7 @@
 //
 // out = softmax(Q K^T * scale) V with K = sk c^k, V = sv c^v per page. The CTA first finds Wk and Wv, powers of two at or
 // above every scale of its pages; the converters then write (sk / Wk) c^k and (sv / Wv) c^v in f16 -- exact for powers of
-// two down to 2^-17 of the largest, else within 2^-25 of W or half a step of f16 --, and Wk goes into the softmax's
+// two down to 2^-24 of W, else within two half steps of f16 and 2^-24 W times the code --, and Wk goes into the softmax's
 // scale, Wv onto the epilogue's O / l. So the softmax and the MMAs are those of a 16-bit cache, and a scale costs one
 // packed multiplication per pair of codes, in warps that have time for it.
 //
