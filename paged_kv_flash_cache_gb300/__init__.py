@@ -210,8 +210,9 @@ def _new(like, shape, dtype, stream):
     torch = _torch()
     if stream is None:
         return torch.empty(shape, dtype=dtype, device=like.device)  # (new_empty: 3 us more between two launches)
-    if not hasattr(stream, "cuda_stream"):
-        stream = torch.cuda.ExternalStream(int(stream), device=like.device)
+    if not isinstance(stream, torch.cuda.Stream):
+        handle = _stream(stream)  # (1, CUDA's name of the legacy default stream, is no stream's number in PyTorch: 0 is the same)
+        stream = torch.cuda.ExternalStream(0 if handle == 1 else handle, device=like.device)
     with torch.cuda.stream(stream):
         return torch.empty(shape, dtype=dtype, device=like.device)
 
